@@ -8,6 +8,7 @@ unloadable library raises immediately - there is no fallback path.
 from __future__ import annotations
 
 import ctypes as C
+import dataclasses
 import pathlib
 import re
 from typing import Dict, List, Optional
@@ -53,6 +54,15 @@ class dflash_weights(C.Structure):
         ("layers", dflash_layer_weights * MAX_LAYERS)]
 
 
+class dflash_cache_config(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in (
+        "n_layer", "n_head", "n_head_kv", "head_dim", "page_size", "n_pages", "max_seq",
+        "max_pages", "dtype", "rope_layout", "rotary_dim", "rope_scaling",
+        "rope_orig_positions")] + [(n, C.c_float) for n in (
+            "rope_factor", "rope_beta_fast", "rope_beta_slow", "rope_mscale", "attn_scale")] + [
+        ("rope_theta", C.c_double)]
+
+
 class DFlashError(RuntimeError):
     pass
 
@@ -61,7 +71,7 @@ def _load() -> C.CDLL:
     if not LIB_PATH.exists():
         raise DFlashError(f"{LIB_PATH} is missing: build it with block_diffusion_drafter_fc_gb300.build")
     lib = C.CDLL(str(LIB_PATH))
-    vp, i32, szp = C.c_void_p, C.c_int32, C.POINTER(C.c_size_t)
+    vp, i32, i64, szp = C.c_void_p, C.c_int32, C.c_int64, C.POINTER(C.c_size_t)
     sig = {
         "dflash_workspace_size": (C.c_int, [C.POINTER(dflash_config), szp, szp]),
         "dflash_create": (C.c_int, [C.POINTER(dflash_config), C.POINTER(dflash_weights), vp, vp,
@@ -90,6 +100,23 @@ def _load() -> C.CDLL:
         "dflash_profile_read": (C.c_int, [vp, C.POINTER(C.c_double), C.POINTER(C.c_int32)]),
         "dflash_status_string": (C.c_char_p, [C.c_int]),
         "dflash_last_error": (C.c_char_p, [vp]),
+        "dflash_cache_workspace_size": (C.c_int, [C.POINTER(dflash_cache_config), szp, szp, szp]),
+        "dflash_cache_create": (C.c_int, [C.POINTER(dflash_cache_config), vp, vp, vp,
+                                          C.POINTER(vp)]),
+        "dflash_cache_destroy": (None, [vp]),
+        "dflash_rope": (C.c_int, [vp, i32, i32, vp, i64, vp, vp, i64, i32, vp]),
+        "dflash_cache_append": (C.c_int, [vp, i32, i32, vp, vp, i32, vp, vp, i64, vp, i64, vp, i64,
+                                          vp, i64, vp]),
+        "dflash_tree_mask": (C.c_int, [vp, i32, vp, i32, vp, vp, i32, vp, vp]),
+        "dflash_tree_attend": (C.c_int, [vp, i32, i32, vp, vp, i32, i32, vp, i32, vp, i64, vp, i64,
+                                         vp, vp]),
+        "dflash_tree_accept": (C.c_int, [vp, i32, vp, i32, vp, vp, vp, vp, i32, vp, vp, vp]),
+        "dflash_cache_commit": (C.c_int, [vp, i32, vp, vp, i32, vp, vp]),
+        "dflash_cache_reserve": (C.c_int, [vp, i32, vp, vp, vp]),
+        "dflash_cache_fork": (C.c_int, [vp, i32, vp, vp, vp]),
+        "dflash_cache_trim": (C.c_int, [vp, i32, vp, vp, vp]),
+        "dflash_cache_read_status": (C.c_int, [vp, C.POINTER(C.c_uint32), vp]),
+        "dflash_cache_last_error": (C.c_char_p, [vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -318,3 +345,230 @@ class DeviceWeight:
 
     def __init__(self, data: torch.Tensor, scale: Optional[torch.Tensor]):
         self.data, self.scale = data, scale
+
+
+# ---------------------------------------------------------------------------
+# the target model's side: paged cache, tree attention, rotary positions
+
+MAX_TREE = 1024       # most nodes of a tree with a mask
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+@dataclasses.dataclass(frozen=True)
+class CacheConfig:
+    """Geometry of a PagedCache (include/dflash.h, dflash_cache_config).  dtype: "f32" |
+    "bf16"; rotary_dim None: the whole head."""
+
+    n_layer: int
+    n_head: int
+    n_head_kv: int
+    head_dim: int
+    page_size: int
+    n_pages: int
+    max_seq: int
+    max_pages: int
+    dtype: str = "bf16"
+    rope_layout: str = "half"       # half | interleaved
+    rotary_dim: Optional[int] = None
+    rope_theta: float = 1e6
+    rope_scaling: str = "none"      # none | linear | ntk | yarn
+    rope_factor: float = 1.0
+    rope_orig_positions: int = 0
+    rope_beta_fast: float = 32.0
+    rope_beta_slow: float = 1.0
+    rope_mscale: float = 0.0
+    attn_scale: float = 0.0
+
+
+def make_cache_config(cfg) -> dflash_cache_config:
+    """dflash_cache_config from any object with CacheConfig's attributes."""
+    c = dflash_cache_config()
+    for n in ("n_layer", "n_head", "n_head_kv", "head_dim", "page_size", "n_pages", "max_seq",
+              "max_pages", "rope_orig_positions", "rope_factor", "rope_beta_fast",
+              "rope_beta_slow", "rope_mscale", "attn_scale", "rope_theta"):
+        setattr(c, n, getattr(cfg, n))
+    c.dtype = DTYPE[cfg.dtype]
+    c.rope_layout, c.rope_scaling = ROPE_LAYOUT[cfg.rope_layout], ROPE_SCALING[cfg.rope_scaling]
+    c.rotary_dim = cfg.head_dim if cfg.rotary_dim is None else cfg.rotary_dim
+    return c
+
+
+def cache_workspace_size(c: dflash_cache_config):
+    """(page bytes, state bytes, scratch bytes) of a cache handle."""
+    a, b, s = C.c_size_t(), C.c_size_t(), C.c_size_t()
+    _check(LIB.dflash_cache_workspace_size(C.byref(c), C.byref(a), C.byref(b), C.byref(s)),
+           what="cache_workspace_size")
+    return a.value, b.value, s.value
+
+
+class PagedCache:
+    """A libdflash cache handle.  Pages, state and scratch are torch areas owned by
+    this object; `pages` [n_pages][n_layer][2][n_head_kv][page_size][head_dim], `table`
+    [max_seq][max_pages], `length` [max_seq] and `refs` [n_pages] are views of them.
+
+    Tensors of rows are [T][heads][head_dim] with any row stride of a multiple of 16
+    bytes (a slice of a fused projection's rows will do); row_start is int32 [n_seq + 1],
+    seqs int32 [n_seq] or None for sequences 0.., all on the device."""
+
+    def __init__(self, cfg, device: str = "cuda"):
+        self.cfg = cfg
+        self.c = make_cache_config(cfg)
+        pb, stb, scb = cache_workspace_size(self.c)
+        self.page_mem = torch.empty(pb + 256, dtype=torch.uint8, device=device)
+        self.state_mem = torch.empty(stb + 256, dtype=torch.uint8, device=device)
+        self.scratch = torch.empty(scb + 256, dtype=torch.uint8, device=device)
+        h = C.c_void_p()
+        _check(LIB.dflash_cache_create(C.byref(self.c), Drafter._aligned(self.page_mem),
+                                       Drafter._aligned(self.state_mem),
+                                       Drafter._aligned(self.scratch), C.byref(h)),
+               what="cache_create")
+        self.h = h.value
+        self.dtype = torch.bfloat16 if cfg.dtype == "bf16" else torch.float32
+
+        def view(mem, off, shape, dt):
+            n = dt.itemsize
+            for d in shape:
+                n *= d
+            off += Drafter._aligned(mem) - mem.data_ptr()
+            return mem[off:off + n].view(dt).view(shape)
+
+        up = lambda x: (x + 255) // 256 * 256  # noqa: E731
+        self.pages = view(self.page_mem, 0, (cfg.n_pages, cfg.n_layer, 2, cfg.n_head_kv,
+                                             cfg.page_size, cfg.head_dim), self.dtype)
+        self.table = view(self.state_mem, 0, (cfg.max_seq, cfg.max_pages), torch.int32)
+        off = up(4 * cfg.max_seq * cfg.max_pages)
+        self.length = view(self.state_mem, off, (cfg.max_seq,), torch.int32)
+        self.refs = view(self.state_mem, off + up(4 * cfg.max_seq), (cfg.n_pages,), torch.int32)
+
+    def close(self):
+        if getattr(self, "h", None):
+            LIB.dflash_cache_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _ok(self, rc: int, what: str) -> None:
+        if rc != 0:
+            extra = LIB.dflash_cache_last_error(self.h).decode() if self.h else ""
+            msg = LIB.dflash_status_string(rc).decode() + (f" ({extra})" if extra else "")
+            raise DFlashError(f"{what}: {msg} [{rc}]")
+
+    def _rows(self, t: torch.Tensor, what: str, heads: Optional[int] = None) -> int:
+        """Row stride of a [T][heads][head_dim] operand."""
+        if t.dtype != self.dtype or t.dim() != 3 or t.shape[2] != self.cfg.head_dim or (
+                heads is not None and t.shape[1] != heads):
+            raise DFlashError(f"{what}: {tuple(t.shape)} {t.dtype} is not [T][{heads or 'heads'}]"
+                              f"[{self.cfg.head_dim}] {self.dtype}")
+        if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+            raise DFlashError(f"{what}: a row's heads have to be contiguous")
+        return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+
+    @staticmethod
+    def _ints(what: str, *ts) -> None:
+        for t, n in ts:
+            if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n):
+                raise DFlashError(f"{what}: index arrays are contiguous int32 of the call's size")
+
+    # ---- C-ABI calls (same names)
+    def dflash_rope(self, x, pos, out, backward: bool = False, stream=None):
+        xs, os_ = self._rows(x, "rope"), self._rows(out, "rope", x.shape[1])
+        if out.shape[0] != x.shape[0]:
+            raise DFlashError("rope: x and out have different rows")
+        self._ints("rope", (pos, x.shape[0]))
+        self._ok(LIB.dflash_rope(self.h, x.shape[0], x.shape[1], x.data_ptr(), xs, pos.data_ptr(),
+                                 out.data_ptr(), os_, int(backward), _stream(stream)), "rope")
+
+    def dflash_cache_append(self, layer: int, row_start, k, v, depth=None, q=None, q_out=None,
+                            seqs=None, stream=None):
+        cfg, T, n = self.cfg, k.shape[0], row_start.shape[0] - 1
+        ks, vs = self._rows(k, "append", cfg.n_head_kv), self._rows(v, "append", cfg.n_head_kv)
+        qs = qos = 0
+        if (q is None) != (q_out is None):
+            raise DFlashError("append: q and q_out go together")
+        if q is not None:
+            qs, qos = self._rows(q, "append", cfg.n_head), self._rows(q_out, "append", cfg.n_head)
+        if v.shape[0] != T or (q is not None and (q.shape[0] != T or q_out.shape[0] != T)):
+            raise DFlashError("append: operands have different rows")
+        self._ints("append", (row_start, 1), (depth, T), (seqs, n))
+        self._ok(LIB.dflash_cache_append(
+            self.h, layer, n, _ptr(seqs), row_start.data_ptr(), T, _ptr(depth), _ptr(q), qs,
+            _ptr(q_out), qos, k.data_ptr(), ks, v.data_ptr(), vs, _stream(stream)), "append")
+
+    def dflash_tree_mask(self, row_start, parents, mask, depth=None, stream=None):
+        n, T = row_start.shape[0] - 1, parents.shape[0]
+        self._ints("tree_mask", (row_start, 1), (parents, T), (mask, T), (depth, T))
+        if mask.dim() != 2 or mask.shape[0] != T:
+            raise DFlashError("tree_mask: mask is int32 [T][words]")
+        self._ok(LIB.dflash_tree_mask(self.h, n, row_start.data_ptr(), T, parents.data_ptr(),
+                                      mask.data_ptr(), mask.shape[1], _ptr(depth), _stream(stream)),
+                 "tree_mask")
+
+    def dflash_tree_attend(self, layer: int, row_start, max_tree: int, q, out, mask=None, lse=None,
+                           seqs=None, stream=None):
+        cfg, T, n = self.cfg, q.shape[0], row_start.shape[0] - 1
+        qs, os_ = self._rows(q, "tree_attend", cfg.n_head), self._rows(out, "tree_attend", cfg.n_head)
+        self._ints("tree_attend", (row_start, 1), (seqs, n))
+        words = 0
+        if mask is not None:
+            if mask.dim() != 2 or mask.shape[0] != T:
+                raise DFlashError("tree_attend: mask is int32 [T][words]")
+            self._ints("tree_attend", (mask, 0))
+            words = mask.shape[1]
+        if out.shape[0] != T or (lse is not None and (
+                lse.dtype != torch.float32 or not lse.is_contiguous() or lse.numel() != T * cfg.n_head)):
+            raise DFlashError("tree_attend: out has q's rows, lse is contiguous f32 [T][n_head]")
+        self._ok(LIB.dflash_tree_attend(
+            self.h, layer, n, _ptr(seqs), row_start.data_ptr(), T, max_tree, _ptr(mask), words,
+            q.data_ptr(), qs, out.data_ptr(), os_, _ptr(lse), _stream(stream)), "tree_attend")
+
+    def dflash_tree_accept(self, row_start, parents, tokens, targets, path, n_path, id_last,
+                           stream=None):
+        n, T = row_start.shape[0] - 1, parents.shape[0]
+        self._ints("tree_accept", (row_start, 1), (parents, T), (tokens, T), (targets, T),
+                   (path, 0), (n_path, n), (id_last, n))
+        if path.dim() != 2 or path.shape[0] != n:
+            raise DFlashError("tree_accept: path is int32 [n_seq][max_path]")
+        self._ok(LIB.dflash_tree_accept(
+            self.h, n, row_start.data_ptr(), T, parents.data_ptr(), tokens.data_ptr(),
+            targets.data_ptr(), path.data_ptr(), path.shape[1], n_path.data_ptr(),
+            id_last.data_ptr(), _stream(stream)), "tree_accept")
+
+    def dflash_cache_commit(self, path, n_path, seqs=None, stream=None):
+        """path int32 [n_seq][max_path], or None: the first n_path nodes stay in place."""
+        n = n_path.shape[0]
+        if path is not None and (path.dim() != 2 or path.shape[0] != n):
+            raise DFlashError("commit: path is int32 [n_seq][max_path]")
+        self._ints("commit", (path, 0), (n_path, n), (seqs, n))
+        self._ok(LIB.dflash_cache_commit(self.h, n, _ptr(seqs), _ptr(path),
+                                         0 if path is None else path.shape[1], n_path.data_ptr(),
+                                         _stream(stream)), "commit")
+
+    def dflash_cache_reserve(self, count, seqs=None, stream=None):
+        n = count.shape[0]
+        self._ints("reserve", (count, n), (seqs, n))
+        self._ok(LIB.dflash_cache_reserve(self.h, n, _ptr(seqs), count.data_ptr(), _stream(stream)),
+                 "reserve")
+
+    def dflash_cache_fork(self, src, dst, stream=None):
+        n = src.shape[0]
+        self._ints("fork", (src, n), (dst, n))
+        self._ok(LIB.dflash_cache_fork(self.h, n, src.data_ptr(), dst.data_ptr(), _stream(stream)),
+                 "fork")
+
+    def dflash_cache_trim(self, new_len, seqs=None, stream=None):
+        n = new_len.shape[0]
+        self._ints("trim", (new_len, n), (seqs, n))
+        self._ok(LIB.dflash_cache_trim(self.h, n, _ptr(seqs), new_len.data_ptr(), _stream(stream)),
+                 "trim")
+
+    def dflash_cache_read_status(self, stream=None) -> int:
+        v = C.c_uint32()
+        rc = LIB.dflash_cache_read_status(self.h, C.byref(v), _stream(stream))
+        if rc not in (0, -7):
+            self._ok(rc, "cache_read_status")
+        return v.value

@@ -83,6 +83,13 @@ typedef enum {
 #define DFLASH_DEV_BAD_TOKEN 0x1u     /* an id_last outside [0, n_vocab): clamped */
 #define DFLASH_DEV_BAD_POSITION 0x2u  /* a negative inject position or n_past: row skipped */
 #define DFLASH_DEV_TIMEOUT 0x4u       /* a pipeline wait gave up after ~2 s: outputs invalid */
+/* Bits of a cache handle's status word (dflash_cache_read_status; with BAD_POSITION
+ * and TIMEOUT above). */
+#define DFLASH_DEV_BAD_ROWS 0x8u      /* row_start, a row count or a length out of range: sequence skipped */
+#define DFLASH_DEV_BAD_PAGE 0x10u     /* a page that is missing, out of range or (for a write) shared */
+#define DFLASH_DEV_BAD_TREE 0x20u     /* a parent that is not an earlier node, or a path that is not ascending */
+#define DFLASH_DEV_BAD_SEQ 0x40u      /* a sequence out of range, listed twice, or not empty where it has to be */
+#define DFLASH_DEV_NO_PAGES 0x80u     /* dflash_cache_reserve found too few pages: nothing was changed */
 
 /*
  * Drafter geometry and storage formats.
@@ -457,6 +464,267 @@ DFLASH_API const char* dflash_status_string(int status);
 
 /* Text of the last CUDA error recorded in the handle ("" if none). */
 DFLASH_API const char* dflash_last_error(const dflash_handle* h);
+
+/* ------------------------------------------------------------------------- *
+ * The target model's side: rotary positions, attention of a tree of drafted
+ * tokens over a paged cache, acceptance along the tree, and the cache's pages.
+ *
+ * The drafter's block (or a tree made of several drafts) is verified by the
+ * target model in one forward (dflash_engine.py, DFlashSpeculativeVerifier;
+ * dflash_head.rs names the engine's paged K/V cache and its block tables).
+ * One turn of a layer stack over a batch of trees:
+ *
+ *   dflash_cache_reserve    room for the trees behind each sequence
+ *   dflash_tree_mask        parents -> ancestor masks and depths (once a turn)
+ *   per layer: dflash_cache_append   rotate q and k, put k and v into the pages
+ *              dflash_tree_attend    every node over its sequence and ancestors
+ *   dflash_tree_accept      the path the target agrees with, and its next token
+ *   dflash_cache_commit     the path's keys and values moved together
+ *
+ * and dflash_cache_fork / dflash_cache_trim share and release pages.  None of
+ * these calls (dflash_cache_create, _destroy and _read_status apart) allocates,
+ * synchronises or reads device data on the host, so all can be captured in a
+ * CUDA graph; lengths and the page table live on the device.
+ *
+ * Rows.  A call works on T rows of n_seq sequences: rows row_start[s] ..
+ * row_start[s+1] - 1 (device int32 [n_seq + 1], ascending, within 0..T) are
+ * nodes 0.. of entry s.  Entry s is sequence seqs[s] of the cache (device int32
+ * [n_seq]; NULL: sequence s).  Node i of a sequence of length n occupies slot
+ * n + i.  Rows outside every range are neither read nor written.  An entry
+ * whose range is not within 0..T, or whose sequence is out of range, is skipped
+ * and sets a status bit, as does every other fault that only the device can
+ * see; no such fault makes a kernel read or write outside the handle's memory
+ * and the buffers of the call.  Where a call changes the cache (append, commit,
+ * trim, reserve), only the first entry of a sequence that is listed twice is
+ * used (BAD_SEQ).
+ *
+ * The calls of one handle share its scratch area and change its state: they
+ * must not overlap on the GPU (one stream, or streams ordered by events; the
+ * same holds for two graphs captured from one handle).  Different handles are
+ * independent.  A call uses the device its pages lie on, whichever is current.
+ * ------------------------------------------------------------------------- */
+
+/* Most nodes of a tree that has a mask, and most entries of one call. */
+#define DFLASH_MAX_TREE 1024
+#define DFLASH_MAX_CALL_SEQ 1024
+
+typedef enum {
+  DFLASH_ROPE_HALF = 0,         /* pair j: dims j and rotary_dim / 2 + j of a head */
+  DFLASH_ROPE_INTERLEAVED = 1   /* pair j: dims 2j and 2j + 1 */
+} dflash_rope_layout;
+
+/* Angle of pair j at position p is p f_j with, for r = rotary_dim and F =
+ * rope_factor:
+ *   NONE    f_j = theta^(-2j/r)
+ *   LINEAR  f_j = theta^(-2j/r) / F
+ *   NTK     f_j = (theta F^(r/(r-2)))^(-2j/r)                         (r > 2)
+ *   YARN    f_j = theta^(-2j/r) (w_j / F + 1 - w_j), w_j a ramp from 0 to 1
+ *           between pairs lo and hi: w_j = clamp((j - lo) / max(hi - lo, 1e-3)),
+ *           lo = max(floor(d(beta_fast)), 0), hi = min(ceil(d(beta_slow)), r - 1),
+ *           d(b) = r ln(orig_positions / (2 pi b)) / (2 ln theta).
+ * Rotated values are multiplied by rope_mscale (0: 0.1 ln F + 1 for YARN with
+ * F > 1, else 1). */
+typedef enum {
+  DFLASH_ROPE_NONE = 0,
+  DFLASH_ROPE_LINEAR = 1,
+  DFLASH_ROPE_NTK = 2,
+  DFLASH_ROPE_YARN = 3
+} dflash_rope_scaling;
+
+/*
+ * Geometry of a cache handle.
+ *   head_dim in {32, 64, 128}; n_head % n_head_kv == 0; page_size a power of two
+ *   in 16..256; max_seq <= 4096 sequences, each of at most max_pages pages
+ *   (max_pages * page_size < 2^31); n_pages * n_layer * 2 * n_head_kv < 2^31;
+ *   dtype F32 or BF16: pages, queries, keys, values and outputs;
+ *   rotary_dim: rotated dims of each head, a multiple of 8 in 0..head_dim;
+ *   rope_theta > 1, rope_factor >= 1 (both read only with rotary_dim > 0);
+ *   attn_scale >= 0: factor of the scores (0: 1 / sqrt(head_dim)).
+ */
+typedef struct {
+  int32_t n_layer;
+  int32_t n_head;
+  int32_t n_head_kv;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t n_pages;
+  int32_t max_seq;
+  int32_t max_pages;
+  int32_t dtype;
+  int32_t rope_layout;
+  int32_t rotary_dim;
+  int32_t rope_scaling;
+  int32_t rope_orig_positions;
+  float rope_factor;
+  float rope_beta_fast;
+  float rope_beta_slow;
+  float rope_mscale;
+  float attn_scale;
+  double rope_theta;
+} dflash_cache_config;
+
+typedef struct dflash_cache dflash_cache;
+
+/*
+ * Sizes of the three caller-owned device areas of a cache handle (256-byte
+ * aligned):
+ *   page_bytes: pages[n_pages][n_layer][k, v][n_head_kv][page_size][head_dim] in
+ *     dtype (slot p of a sequence: row p % page_size of its page p / page_size);
+ *   state_bytes: int32 table[max_seq][max_pages] (-1: no page), then int32
+ *     length[max_seq], then int32 refs[n_pages] (sequences that hold the page;
+ *     0: free), each starting at a multiple of 256 bytes.  A caller may read and
+ *     set them between calls;
+ *   scratch_bytes: the library's own.
+ */
+DFLASH_API int dflash_cache_workspace_size(const dflash_cache_config* cfg, size_t* page_bytes,
+                                           size_t* state_bytes, size_t* scratch_bytes);
+
+/* Build a cache handle over those areas: every sequence empty, every page free
+ * (the pages' contents are left as they are).  Synchronous. */
+DFLASH_API int dflash_cache_create(const dflash_cache_config* cfg, void* page_mem, void* state_mem,
+                                   void* scratch_mem, dflash_cache** out);
+
+/* Free the handle's host state (not the borrowed memory). */
+DFLASH_API void dflash_cache_destroy(dflash_cache* c);
+
+/*
+ * Rotary positions of n_heads heads per row, or their gradient:
+ *   out[t][h] = R(pos[t]) x[t][h], or R(pos[t])^T x[t][h] when backward != 0
+ * (with out = R x, dx = R^T dout), dims from rotary_dim on copied.
+ *   x, out: device [T][n_heads][head_dim] in dtype with row strides x_stride and
+ *   out_stride in elements (a head's dims and a row's heads are contiguous), both
+ *   16-byte aligned with strides that are multiples of 16 bytes; out may be x.
+ *   pos: device int32 [T].  A negative position sets DFLASH_DEV_BAD_POSITION and
+ *   its row is not written.
+ */
+DFLASH_API int dflash_rope(dflash_cache* c, int32_t T, int32_t n_heads, const void* x, int64_t x_stride,
+                           const int32_t* pos, void* out, int64_t out_stride, int32_t backward,
+                           void* stream);
+
+/*
+ * Put T rows' keys and values of one layer into the pages, keys rotated, and
+ * rotate their queries: row i of entry s has position n + depth (depth NULL: n +
+ * i), n the sequence's length, and goes to slot n + i.  Lengths do not change
+ * (dflash_cache_commit adds the rows that stay).
+ *   k, v: device [T][n_head_kv][head_dim]; q, q_out: device [T][n_head][head_dim],
+ *   or both NULL; q_out may be q.  Strides and alignment as for dflash_rope.
+ *   depth: device int32 [T] (dflash_tree_mask) or NULL.
+ * A slot without a page, or whose page other sequences hold too
+ * (dflash_cache_reserve makes it private), sets DFLASH_DEV_BAD_PAGE and its key
+ * and value are not written; a negative position is skipped with
+ * DFLASH_DEV_BAD_POSITION.
+ */
+DFLASH_API int dflash_cache_append(dflash_cache* c, int32_t layer, int32_t n_seq, const int32_t* seqs,
+                                   const int32_t* row_start, int32_t T, const int32_t* depth,
+                                   const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                                   const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                   void* stream);
+
+/*
+ * Ancestor masks of trees given by parents: bit j of mask[t] is set when node j
+ * is row t's node or one of its ancestors; depth[t] counts the proper ancestors.
+ *   parents: device int32 [T], the parent's node index within the row's own tree
+ *   (an earlier node), or -1 for a root: a chain of B tokens has parents i - 1;
+ *   mask: device uint32 [T][mask_words], mask_words in 1..32 (bits from the
+ *   entry's node count on are zero); depth: device int32 [T] or NULL.
+ * A parent that is neither -1 nor an earlier node counts as -1 and sets
+ * DFLASH_DEV_BAD_TREE; an entry of more than 32 mask_words nodes is skipped with
+ * DFLASH_DEV_BAD_ROWS.
+ */
+DFLASH_API int dflash_tree_mask(dflash_cache* c, int32_t n_seq, const int32_t* row_start, int32_t T,
+                                const int32_t* parents, uint32_t* mask, int32_t mask_words,
+                                int32_t* depth, void* stream);
+
+/*
+ * Attention of T rows over their sequences' pages: node i of an entry of length
+ * n attends to slots 0 .. n-1 and to those slots n + j, j < the entry's node
+ * count, whose bit j of mask is set (mask NULL: j <= i, a causal chain of any
+ * length, e.g. a prompt):
+ *   out[t][h] = sum_p w_p V[p], w = softmax over the attended slots of
+ *   attn_scale q[t][h] . K[p], head h reading key/value head h / (n_head / n_head_kv);
+ *   lse[t][h] = ln of the sum of exp of the scores.
+ * A row that attends to nothing gets out 0 and lse -inf.  What slots past the
+ * last node hold does not matter; an infinite or NaN value of a node may reach
+ * every row of its entry, whether the row attends to it or not.
+ *   max_tree: an upper bound of the entries' node counts (<= 32 mask_words with a
+ *   mask); an entry of more is skipped with DFLASH_DEV_BAD_ROWS.
+ *   q, out: device [T][n_head][head_dim], strides and alignment as for
+ *   dflash_rope (out must not overlap q); lse: device f32 [T][n_head] or NULL.
+ * A missing page sets DFLASH_DEV_BAD_PAGE; the entry's outputs are then
+ * unspecified.
+ */
+DFLASH_API int dflash_tree_attend(dflash_cache* c, int32_t layer, int32_t n_seq, const int32_t* seqs,
+                                  const int32_t* row_start, int32_t T, int32_t max_tree,
+                                  const uint32_t* mask, int32_t mask_words, const void* q,
+                                  int64_t q_stride, void* out, int64_t out_stride, float* lse,
+                                  void* stream);
+
+/*
+ * Greedy acceptance along trees (the tree form of dflash_accept): node 0 is the
+ * anchor, always accepted; after an accepted node i follows its child of lowest
+ * index whose token equals targets[row of i], until there is none or the path
+ * holds max_path nodes.
+ *   parents (as for dflash_tree_mask; a bad one is never reached), tokens (the
+ *   nodes' drafted tokens), targets (the target model's greedy token after each
+ *   node): device int32 [T];
+ *   path: device int32 [n_seq][max_path], the accepted nodes, ascending, -1 behind
+ *   them; n_path: device int32 [n_seq], their number (0 for an entry without
+ *   rows); id_last: device int32 [n_seq], the target's token after the last
+ *   accepted node (unchanged for an entry without rows).
+ */
+DFLASH_API int dflash_tree_accept(dflash_cache* c, int32_t n_seq, const int32_t* row_start, int32_t T,
+                                  const int32_t* parents, const int32_t* tokens, const int32_t* targets,
+                                  int32_t* path, int32_t max_path, int32_t* n_path, int32_t* id_last,
+                                  void* stream);
+
+/*
+ * Keep an accepted path: in every layer the keys and values of slots n +
+ * path[s][j] move to slots n + j, j < n_path[s] (all read before they are
+ * overwritten), and the sequence's length becomes n + n_path[s].
+ *   path: device int32 [n_seq][max_path], strictly ascending node indices (entry j
+ *   at least j), or NULL: nodes 0 .. n_path[s] - 1 stay where they are (a prompt
+ *   or a chain).  An entry with a path that is not so, or with slots that have no
+ *   private page, is skipped (BAD_TREE, BAD_PAGE).
+ */
+DFLASH_API int dflash_cache_commit(dflash_cache* c, int32_t n_seq, const int32_t* seqs,
+                                   const int32_t* path, int32_t max_path, const int32_t* n_path,
+                                   void* stream);
+
+/*
+ * Make slots n .. n + count[s] - 1 of every entry ready to write: missing pages
+ * are given out, and a part-filled last page that other sequences hold too is
+ * replaced by a private copy of its slots below n (the last of its holders keeps
+ * it).  Free pages are given out in ascending order to the entries in their
+ * order.  If there are too few, or an entry would pass max_pages, nothing is
+ * changed and DFLASH_DEV_NO_PAGES is set.  A negative count counts as 0
+ * (BAD_ROWS).
+ */
+DFLASH_API int dflash_cache_reserve(dflash_cache* c, int32_t n_seq, const int32_t* seqs,
+                                    const int32_t* count, void* stream);
+
+/*
+ * Fork: sequence dst[i] becomes a copy of sequence src[i] that shares its pages
+ * (nothing is copied until dflash_cache_reserve).  src, dst: device int32 [n].
+ * An entry whose dst is not empty (dflash_cache_trim to 0), is listed twice or is
+ * a source of the same call is skipped (BAD_SEQ).
+ */
+DFLASH_API int dflash_cache_fork(dflash_cache* c, int32_t n, const int32_t* src, const int32_t* dst,
+                                 void* stream);
+
+/*
+ * Cut every entry's sequence to at most new_len[s] tokens and release its pages
+ * behind slot new_len[s] - 1, reserved ones too; 0 frees the sequence.  A page is
+ * free once no sequence holds it.  A negative new_len is skipped (BAD_ROWS).
+ */
+DFLASH_API int dflash_cache_trim(dflash_cache* c, int32_t n_seq, const int32_t* seqs,
+                                 const int32_t* new_len, void* stream);
+
+/* Read and clear the handle's device status word after waiting for `stream`.
+ * Synchronous.  Returns DFLASH_ERR_DEVICE when a bit was set. */
+DFLASH_API int dflash_cache_read_status(dflash_cache* c, uint32_t* status, void* stream);
+
+/* Text of the last CUDA error recorded in the handle ("" if none). */
+DFLASH_API const char* dflash_cache_last_error(const dflash_cache* c);
 
 #ifdef __cplusplus
 }
