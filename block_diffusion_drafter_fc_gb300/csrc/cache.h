@@ -107,6 +107,27 @@ struct AttendParams {
   float* lse;
   float scale;
 };
-cudaError_t launch_attend(const AttendParams& p, cudaStream_t st);
+// What a handle keeps for attention: tensor maps of the pages, scratch for the
+// partial rows of tiles that several blocks share, and a description per block
+// of the cut tile that begins in it.
+struct Cut {
+  int lo, row0, kvh, rows;   // first row of the entry; the tile's first row, kv head, rows
+  int last, slot;            // its last block (below the block itself: no such tile), the first part's slot
+};
+constexpr int kAttendSms = 160;        // most SMs a launch uses: 1 (tcgen05) or 2 (streaming) blocks each
+struct AttendWork {
+  const CUtensorMap* tm;   // boxes of attend_chunk slots
+  float* part_o;      // [attend_part_rows][hd]
+  float2* part_ml;    // [attend_part_rows]
+  Cut* cuts;          // [2 kAttendSms]
+  int sms;
+};
+bool attend_on_umma(int el, int hd);   // tcgen05 kernel, else the streaming kernel
+size_t attend_part_rows(int el, int hd);
+int attend_chunk(int el, int hd);
+cudaError_t configure_attend();
+cudaError_t configure_attend_umma();
+cudaError_t launch_attend_umma(const AttendParams& p, const AttendWork& w, cudaStream_t st);
+cudaError_t launch_attend(const AttendParams& p, const AttendWork& w, cudaStream_t st);
 
 }  // namespace dflash

@@ -3,6 +3,7 @@
 // and tree_attention.cu.
 #include "../../include/dflash.h"
 #include "cache.h"
+#include "internal.h"
 
 #include <algorithm>
 #include <cmath>
@@ -28,7 +29,7 @@ size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 struct Layout {
   size_t page_bytes;
   size_t table, length, refs, state_bytes;
-  size_t status, turns, tickets, free_list, copies, scratch_bytes;
+  size_t status, turns, tickets, free_list, copies, part_o, part_ml, cuts, scratch_bytes;
 };
 
 int el_of(const dflash_cache_config& c) { return c.dtype == DFLASH_DTYPE_BF16 ? 2 : 4; }
@@ -52,6 +53,10 @@ Layout layout(const dflash_cache_config& c) {
   L.tickets = take(sizeof(int) * kCallSeq);
   L.free_list = take(sizeof(int32_t) * (size_t)c.n_pages);
   L.copies = take(sizeof(int4) * kCallSeq);
+  const size_t parts = attend_part_rows(el_of(c), c.head_dim);
+  L.part_o = take(sizeof(float) * parts * c.head_dim);
+  L.part_ml = take(sizeof(float2) * parts);
+  L.cuts = take(sizeof(Cut) * 2 * kAttendSms);
   L.scratch_bytes = off;
   return L;
 }
@@ -128,6 +133,8 @@ struct dflash_cache {
   Layout L;
   CacheView v;
   RopeView rope;
+  CUtensorMap tm;
+  AttendWork work;
   char* scratch;
   int device;
   char err[512];
@@ -165,6 +172,24 @@ struct OnDevice {
 
 bool bad_area(const void* p, size_t align) {
   return !p || (reinterpret_cast<uintptr_t>(p) & (align - 1));
+}
+
+// The pages as a 3-D tensor [rows of (page, layer, k|v, head)][page_size][hd], in
+// boxes of up to `rows` slots of one row and 128 bytes (a whole head of 64) of
+// each: 64- and 128-byte rows swizzled, rows past the tensor read as zero.
+bool page_map(CUtensorMap* m, const CacheView& v, int rows) {
+  const EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  const uint32_t row_bytes = v.hd * v.el, box_bytes = row_bytes < 128 ? row_bytes : 128;
+  const cuuint64_t dims[3] = {(cuuint64_t)v.hd, (cuuint64_t)v.ps,
+                              (cuuint64_t)v.n_pages * v.n_layer * 2 * v.n_head_kv};
+  const cuuint64_t strides[2] = {row_bytes, (cuuint64_t)row_bytes * v.ps};
+  const cuuint32_t box[3] = {box_bytes / v.el, (cuuint32_t)(v.ps < rows ? v.ps : rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, v.el == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, v.pages, dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A [T][heads][head_dim] operand: 16-byte aligned, rows at least a row apart.
@@ -249,6 +274,12 @@ int dflash_cache_create(const dflash_cache_config* cfg, void* page_mem, void* st
     if (e == cudaSuccess)
       e = cudaMemcpy(c->S<void>(c->L.turns), turns, sizeof(turns), cudaMemcpyHostToDevice);
     if (e == cudaSuccess) e = configure_tree();
+    if (e == cudaSuccess) e = configure_attend();
+    int sms = 0;
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c->device);
+    if (e == cudaSuccess && !page_map(&c->tm, w, attend_chunk(w.el, w.hd))) e = cudaErrorNotSupported;
+    c->work = {&c->tm, c->S<float>(c->L.part_o), c->S<float2>(c->L.part_ml),
+               c->S<Cut>(c->L.cuts), std::min(sms, kAttendSms)};
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
   }
   if (e != cudaSuccess) {
@@ -357,7 +388,7 @@ int dflash_tree_attend(dflash_cache* c, int32_t layer, int32_t n_seq, const int3
   p.out_ld = out_stride * p.c.el;
   p.lse = lse;
   p.scale = c->cfg.attn_scale != 0.f ? c->cfg.attn_scale : (float)(1.0 / std::sqrt((double)c->cfg.head_dim));
-  DC_CHECK(c, launch_attend(p, static_cast<cudaStream_t>(stream)));
+  DC_CHECK(c, launch_attend(p, c->work, static_cast<cudaStream_t>(stream)));
   return DFLASH_OK;
 }
 

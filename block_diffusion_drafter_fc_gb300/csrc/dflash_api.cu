@@ -14,6 +14,19 @@
 
 using namespace dflash;
 
+EncodeTiledFn dflash::encode_tiled_fn() {
+  static EncodeTiledFn fn = nullptr;
+  if (!fn) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  }
+  return fn;
+}
+
 namespace {
 
 constexpr int kPlanSMs = 152;        // GB300: 2 dies x 76 SMs
@@ -339,25 +352,7 @@ inline void clear_stale_error() { (void)cudaGetLastError(); }
     if (e_ != cudaSuccess) return cuda_fail(h, e_, #call);  \
   } while (0)
 
-// cuTensorMapEncodeTiled through the runtime's driver entry point (the library
-// does not link libcuda).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  }
-  return fn;
-}
+EncodeTiledFn encode_fn() { return encode_tiled_fn(); }
 
 // 2-D map of a row-major [rows][cols] matrix with boxes of box_cols x box_rows
 // elements; out-of-range rows / columns read as zero.

@@ -1,0 +1,610 @@
+// Tree attention on the 5th-generation tensor cores (tcgen05), bf16 with heads
+// of 64 and 128.
+//
+// Why not mma.sync: it runs bf16 at 256 products a clock and SM here (ncu on
+// the streaming kernel: 32 cycles per m16n8k16 and scheduler, tensor pipe 86%
+// busy at 66% of the copy bandwidth with 16-row tiles), a sixteenth of
+// tcgen05.mma; the matrix work of a 16-row tile alone (two products, the
+// weights split) exceeded the time to read its pages.  tcgen05.mma on a padded
+// 128-row tile takes 8 clocks a slot (QK^T and PV, 128 dims), the read of a
+// slot at an SM's share of the copy bandwidth 22.
+//
+// One persistent block per SM walks its range of the call's units (a unit: 128
+// slots of one tile of one kv head's query rows; tree_common.cuh), with two
+// streams of scores in flight so that one stream's softmax runs under the other
+// stream's products:
+//   tile of more than 128 rows (pair): stream i holds rows 128 i .. + 127, both
+//     use every chunk;
+//   tile of at most 128 rows (split): stream i takes every second chunk, with
+//     its own maximum, sum and accumulator, joined at the tile's end.  With at
+//     most 64 (32) rows, the rows are there 2 (4) times, in different lanes of
+//     the tile, and each copy of a row exponentiates its own half (quarter) of
+//     the chunk's slots, its weights for the others zero: the products cost the
+//     same, the exponentials of a chunk spread over all four warps.
+// Roles:
+//   warps 0..3, 4..7  softmax of stream 0 and 1, a thread per row: S from tensor
+//                     memory (tcgen05.ld), running maximum m and sum l, weights
+//                     e^(s - m) back as bf16 over S (the A operand of PV).  The
+//                     accumulator is rescaled only when the maximum grew by
+//                     more than 2^8 (weights stay below 2^8, their sum is fp32);
+//   warp 8 (a lane)   K and V chunks by TMA into a ring of stages, page by page,
+//                     across tiles;
+//   warp 9 (a lane)   tcgen05.mma: S_i = Q_i K^T (both in shared memory), O_i +=
+//                     P_i V (P in tensor memory, V as it lies: MN-major).
+// Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (head_dim each).
+// The weights are rounded to bf16 for the product with V (their sum is not):
+// each is off by at most 2^-8 of itself, independently, which adds as much
+// again as the rounding of the result; splitting them as in the streaming
+// kernel would cost half of PV more.
+// Every mbarrier wait gives up after ~2 s with DFLASH_DEV_TIMEOUT and the block
+// runs to its end without further waits; tensor memory is always released.
+#include "tree_common.cuh"
+
+namespace dflash {
+
+using namespace tree;
+
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kChunk = 128, kTile = 256;
+constexpr int kMinUnits = 1;   // a block's least share of a call's units
+constexpr int kProducer = 8, kIssuer = 9;
+
+template <int HD>
+struct Lay {
+  static constexpr int kHalf = 128 * 128;               // 128 rows x 64 dims, 128-byte swizzle
+  static constexpr int kHalves = HD / 64;
+  static constexpr int kMat = kHalf * kHalves;          // a Q tile, a K or V chunk
+  static constexpr int kOffRing = 2 * kMat;             // Q tiles first
+  static constexpr int kStagesMost = HD == 128 ? 5 : 10;
+  static constexpr int kDch = HD / 4;                   // dims of one pass of the tile's join
+  static constexpr int kCols = 512;
+};
+
+DF_DEVICE uint64_t desc_k(uint32_t a) {   // K-major, 128-byte swizzle, 8-row groups of 1024 bytes
+  return ((uint64_t)(a >> 4) & 0x3FFFull) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+// MN-major, 128-byte swizzle: 64 dims per 128-byte row, the next 64 dims kHalf
+// bytes on, the next 8 slots 1024 bytes on.
+DF_DEVICE uint64_t desc_mn(uint32_t a, uint32_t next64) {
+  return ((uint64_t)(a >> 4) & 0x3FFFull) | ((uint64_t)(next64 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// kind::f16: bf16 A and B, fp32 D, A K-major, B K-major or MN-major.
+constexpr uint32_t idesc(int N, bool mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+DF_DEVICE void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+DF_DEVICE void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+DF_DEVICE void commit(uint64_t* b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   su32(b))
+               : "memory");
+}
+DF_DEVICE void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+DF_DEVICE void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+DF_DEVICE void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 32 columns of the warp's lanes <-> 32 registers
+DF_DEVICE void tmem_ld32(uint32_t a, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(a));
+}
+DF_DEVICE void tmem_st32(uint32_t a, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
+      "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
+      "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]) : "memory");
+}
+DF_DEVICE void tmem_st16(uint32_t a, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16};" ::"r"(a),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]) : "memory");
+}
+DF_DEVICE void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+DF_DEVICE void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+DF_DEVICE void sync_rows() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+struct UmmaParams {
+  CUtensorMap tm;     // pages as [rows of (page, layer, k|v, head)][page_size][hd], boxes of 64 dims
+  AttendParams a;
+  float* part_o;      // [2 blocks][kTile][hd]
+  float2* part_ml;    // [2 blocks][kTile]
+  Cut* cuts;          // [blocks]
+  int stages, box_rows;
+};
+
+// Bit j: the row sees slot `slot` + j.
+DF_DEVICE uint32_t visible(const AttendParams& p, const Entry& x, int node, int slot) {
+  const int a = slot - x.len;                    // node index of bit 0
+  if (a <= -32) return ~0u;
+  const int valid = x.n - a;                     // bits below it are slots of the entry
+  uint32_t v;
+  if (!p.mask) {
+    const int c = node - a + 1;
+    v = c >= 32 ? ~0u : c <= 0 ? 0u : (1u << c) - 1u;
+  } else {
+    const uint32_t* w = p.mask + (size_t)(x.lo + node) * p.words;
+    if (a < 0) {
+      v = (__ldg(w) << -a) | ((1u << -a) - 1u);
+    } else {
+      const int k = a >> 5;
+      const uint32_t lo = k < p.words ? __ldg(w + k) : 0u, hi = k + 1 < p.words ? __ldg(w + k + 1) : 0u;
+      v = __funnelshift_r(lo, hi, a & 31);
+    }
+  }
+  if (valid < 32) v &= valid <= 0 ? 0u : (1u << valid) - 1u;
+  return v;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_constant__ UmmaParams p) {
+  using Lt = Lay<HD>;
+  constexpr int kMat = Lt::kMat, kHalf = Lt::kHalf, kHalves = Lt::kHalves;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int S = p.stages;
+  uint8_t* ring = sm + Lt::kOffRing;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + S * kMat);
+  uint64_t* empty = full + S;
+  uint64_t* q_full = empty + S;      // the tile's Q is in shared memory, the last tile's O is read
+  uint64_t* s_full = q_full + 1;     // [2] S_i computed (and every product before it done)
+  uint64_t* p_full = s_full + 2;     // [2] P_i stored
+  uint64_t* o_full = p_full + 2;     // the tile's products are done
+  long long* s_warp = reinterpret_cast<long long*>(o_full + 1);   // [10]
+  long long* s_end = s_warp + 10;
+  Entry* s_e = reinterpret_cast<Entry*>(s_end + p.a.rows.n_seq);
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+
+  const CacheView& c = p.a.c;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.x;
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      bar_init(&full[i], 1);
+      bar_init(&empty[i], 1);
+    }
+    bar_init(q_full, 8);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&s_full[i], 1);
+      bar_init(&p_full[i], 4);
+    }
+    bar_init(o_full, 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  plan_entries(p.a, kTile, kChunk, s_e, s_end, s_warp, kThreads, b == 0);
+  __syncthreads();
+  const long long U = s_end[p.a.rows.n_seq - 1];
+  // fewer blocks than launched where their shares would get too small
+  const int Gr = (int)min((long long)gridDim.x, max(1LL, U / kMinUnits));
+  Cut cut = {0, 0, 0, 0, -1, 0};
+  if (b >= Gr || U == 0) {
+    if (tid == 0) p.cuts[b] = cut;
+    return;
+  }
+  if (warp == kIssuer) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&s_tmem)),
+                 "n"(Lt::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = s_tmem;
+  const long long ub0 = range_begin(U, Gr, b), ub1 = range_begin(U, Gr, b + 1);
+  long long u = ub0;
+  int s = find_entry(s_end, p.a.rows.n_seq, ub0);
+  const int grp = c.n_head / c.n_head_kv;
+  Segment g;
+  int it = 0;   // ring position of the segment's first K chunk
+
+  if (warp == kProducer) {
+    // ---------------------------------------------------------------- copies
+    const int none = c.n_pages * c.n_layer * 2 * c.n_head_kv;   // past the tensor: reads as zero
+    while (next_segment(p.a, kTile, kChunk, s_e, s_end, u, ub1, s, g)) {
+      const Entry x = s_e[g.s];
+      const int32_t* table = c.table + (size_t)x.q * c.max_pages;
+      const int last = (x.len + x.n - 1) >> c.ps_log2;
+      int base = -64, row = none;             // lane i holds the tensor row of page base + i
+      for (int ch = g.c0; ch < g.c1; ++ch) {
+        if (((ch * kChunk + kChunk - 1) >> c.ps_log2) > base + 31) {
+          base = (ch * kChunk) >> c.ps_log2;
+          row = none;
+          if (base + lane <= last) {
+            const int t = table[base + lane];
+            if (t >= 0 && t < c.n_pages)
+              row = (t * c.n_layer + p.a.layer) * 2 * c.n_head_kv + g.kvh;
+            else
+              set_status(c.status, DEV_BAD_PAGE);
+          }
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++it) {
+          const int st = it % S;
+          if (lane == 0) {
+            bar_wait(&empty[st], (uint32_t)((it / S) & 1) ^ 1, &s_abort, c.status);
+            bar_expect(&full[st], kMat);
+          }
+          __syncwarp();
+          uint8_t* dst = ring + st * kMat;
+          for (int i = 0; i < kChunk; i += p.box_rows) {
+            const int slot = ch * kChunk + i;
+            const int r = __shfl_sync(0xffffffffu, row, ((slot >> c.ps_log2) - base) & 31);
+            if (lane == 0)
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h)
+                tma3d(dst + h * kHalf + i * 128, &p.tm, h * 64, slot & (c.ps - 1),
+                      r == none ? none : r + kv * c.n_head_kv, &full[st]);
+          }
+        }
+      }
+    }
+    // no copy may still be landing when the block ends
+    if (lane == 0)
+      for (int j = max(0, it - S); j < it; ++j) {
+        const long long t0 = clock64();
+        while (!bar_try(&full[j % S], (uint32_t)((j / S) & 1)) && clock64() - t0 < kWait) {
+        }
+      }
+  } else if (warp == kIssuer) {
+    // -------------------------------------------------------------- products
+    if (lane == 0) {
+      int seg = 0, n_p[2] = {0, 0};
+      while (next_segment(p.a, kTile, kChunk, s_e, s_end, u, ub1, s, g)) {
+        const Entry x = s_e[g.s];
+        const bool pair = (long long)x.n * grp - g.row0 > 128;
+        const int nc = g.c1 - g.c0, steps = pair ? 2 * nc : nc;
+        bar_wait(q_full, seg & 1, &s_abort, c.status);
+        ++seg;
+        auto scores = [&](int k) {
+          const int i = k & 1, r = it + 2 * (pair ? k >> 1 : k), st = r % S;
+          bar_wait(&full[st], (uint32_t)((r / S) & 1), &s_abort, c.status);
+          fence_after();
+          const uint64_t qa = desc_k(su32(sm + (pair ? i : 0) * kMat)), kb = desc_k(su32(ring + st * kMat));
+#pragma unroll
+          for (int e = 0; e < HD / 16; ++e) {
+            const uint32_t off = ((e >> 2) * kHalf + (e & 3) * 32) >> 4;
+            mma_ss(tmem + i * 128, qa + off, kb + off, idesc(128, false), e > 0);
+          }
+          commit(&s_full[i]);
+          if (!pair || i) commit(&empty[st]);
+        };
+        scores(0);
+        if (steps > 1) scores(1);
+        for (int k = 0; k < steps; ++k) {
+          const int i = k & 1, r = it + 2 * (pair ? k >> 1 : k) + 1, st = r % S;
+          bar_wait(&p_full[i], n_p[i] & 1, &s_abort, c.status);
+          ++n_p[i];
+          bar_wait(&full[st], (uint32_t)((r / S) & 1), &s_abort, c.status);
+          fence_after();
+          const uint64_t vb = desc_mn(su32(ring + st * kMat), kHalf);
+#pragma unroll
+          for (int e = 0; e < kChunk / 16; ++e)   // 16 slots: 2 groups of 1024 bytes
+            mma_ts(tmem + 256 + i * HD, tmem + i * 128 + 8 * e, vb + ((e * 2048) >> 4), idesc(HD, true),
+                   k > 1 || e > 0);
+          if (!pair || i) commit(&empty[st]);
+          if (k + 2 < steps) scores(k + 2);
+        }
+        commit(o_full);
+        it += 2 * nc;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------ rows
+    const int i = warp >> 2, pos = tid & 127;     // stream, lane of the tile
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // the warp's tensor-memory lanes: 32 (warp % 4) << 16
+    const uint32_t tS = tmem + i * 128 + lanes, tO = tmem + 256 + i * HD + lanes;
+    const float scale = p.a.scale * kLog2e;
+    int seg = 0, n_s = 0;
+    while (next_segment(p.a, kTile, kChunk, s_e, s_end, u, ub1, s, g)) {
+      const Entry x = s_e[g.s];
+      const int left = (int)min((long long)x.n * grp - g.row0, (long long)kTile), end = x.len + x.n;
+      const bool pair = left > 128;
+      const int rep = left > 64 ? 1 : left > 32 ? 2 : 4, per = 128 / rep;   // copies of a row, rows
+      const int nc = g.c1 - g.c0, steps = pair ? 2 * nc : nc;
+      // Q: lane q of tile t is row 128 t + q (pair) or row q % per
+      for (int e = tid; e < (pair ? 2 : 1) * 128 * (HD / 8); e += 256) {
+        const int q = e / (HD / 8), pc = e - q * (HD / 8), r = pair ? q : q & (per - 1);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < left) {
+          const int node = (g.row0 + r) / grp, h = g.kvh * grp + (g.row0 + r) - node * grp;
+          v = *reinterpret_cast<const uint4*>(p.a.q + (size_t)(x.lo + node) * p.a.q_ld + (size_t)h * HD * 2 + pc * 16);
+        }
+        *reinterpret_cast<uint4*>(sm + (q >> 7) * kMat + (pc >> 3) * kHalf + (q & 127) * 128 +
+                                  (((pc & 7) ^ (q & 7)) << 4)) = v;
+      }
+      fence_async();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(q_full);
+
+      const int row = pair ? i * 128 + pos : pos & (per - 1);
+      const int copy = pair ? 0 : pos / per, col0 = copy * per, batches = per / 32;
+      // per / 32: the copy's share of a chunk's slots, in batches of 32
+      const bool real = row < left;
+      const int node = real ? (g.row0 + row) / grp : 0;
+      const bool idle = !__any_sync(0xffffffffu, real);   // S and so P are zero, or of no row
+      float m = -CUDART_INF_F, l = 0.f;
+      for (int k = i; k < steps; k += 2, ++n_s) {
+        const int j = pair ? k >> 1 : k, slot0 = (g.c0 + j) * kChunk;
+        bar_wait(&s_full[i], n_s & 1, &s_abort, c.status);
+        fence_after();
+        if (!idle) {
+          const bool part = slot0 + kChunk > x.len;   // nodes or slots past the last among them
+          float top = -CUDART_INF_F;
+          for (int t = 0; t < batches; ++t) {
+            uint32_t v[32];
+            __syncwarp();
+            tmem_ld32(tS + col0 + 32 * t, v);
+            const uint32_t see = part ? visible(p.a, x, node, slot0 + col0 + 32 * t) : ~0u;
+            wait_ld();
+            if (part) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (see & (1u << e)) top = fmaxf(top, __uint_as_float(v[e]));
+            } else {
+              float t4[4] = {top, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+              for (int e = 0; e < 32; ++e) t4[e & 3] = fmaxf(t4[e & 3], __uint_as_float(v[e]));
+              top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+            }
+          }
+          top *= scale;
+          // a larger maximum: the accumulator's products so far are done
+          // (s_full follows them)
+          float fade = 1.f;
+          if (top > m + 8.f) {
+            fade = ex2(m - top);   // 0 when nothing was attended yet
+            l *= fade;
+            m = top;
+          }
+          if (k > 1 && __any_sync(0xffffffffu, fade != 1.f)) {
+#pragma unroll 1
+            for (int t = 0; t < HD / 32; ++t) {
+              uint32_t v[32];
+              __syncwarp();
+              tmem_ld32(tO + 32 * t, v);
+              wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * fade);
+              tmem_st32(tO + 32 * t, v);
+            }
+          }
+          const float use = m == -CUDART_INF_F ? 0.f : m;
+          float s4[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int t = 0; t < batches; ++t) {
+            uint32_t v[32], w[16];
+            __syncwarp();
+            tmem_ld32(tS + col0 + 32 * t, v);
+            const uint32_t see = part ? visible(p.a, x, node, slot0 + col0 + 32 * t) : ~0u;
+            wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float a0 = ex2(fmaf(__uint_as_float(v[e]), scale, -use));
+              float a1 = ex2(fmaf(__uint_as_float(v[e + 1]), scale, -use));
+              if (part) {
+                a0 = see & (1u << e) ? a0 : 0.f;
+                a1 = see & (2u << e) ? a1 : 0.f;
+              }
+              s4[e & 2] += a0;
+              s4[(e & 2) + 1] += a1;
+              w[e / 2] = pack_bf16x2(a0, a1);
+            }
+            tmem_st16(tS + col0 / 2 + 16 * t, w);
+          }
+          l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+          if (rep > 1) {   // the other copies' slots
+            const uint32_t z[16] = {};
+            for (int t = 0; t < 4; ++t)
+              if (t * 32 < col0 || t * 32 >= col0 + per) tmem_st16(tS + 16 * t, z);
+          }
+          wait_st();
+        }
+        if (slot0 + kChunk > end && (!pair || i == 0)) {
+          // slots past the last node may hold anything: 0 x NaN is NaN
+          const int r = it + 2 * j + 1, st = r % S;
+          bar_wait(&full[st], (uint32_t)((r / S) & 1), &s_abort, c.status);
+          const int first = max(0, end - slot0);
+          for (int e = first * (HD / 8) + pos; e < kChunk * (HD / 8); e += 128) {
+            const int q = e / (HD / 8), pc = e - q * (HD / 8);
+            *reinterpret_cast<uint4*>(ring + st * kMat + (pc >> 3) * kHalf + q * 128 + (((pc & 7) ^ (q & 7)) << 4)) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_async();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&p_full[i]);
+      }
+      it += 2 * nc;
+
+      // ---- the tile's end
+      bar_wait(o_full, seg & 1, &s_abort, c.status);
+      ++seg;
+      fence_after();
+      const bool whole = g.c0 == 0 && g.c1 == g.nch;
+      // partial rows: slot 0 of the block if its range starts in the tile, else 1
+      const int slot = 2 * b + (ub0 >= g.u0 ? 0 : 1);
+      auto out_row = [&](int r, char*& dst, float*& lse) {
+        const int nd = (g.row0 + r) / grp, h = g.kvh * grp + (g.row0 + r) - nd * grp;
+        dst = p.a.out + (size_t)(x.lo + nd) * p.a.out_ld + (size_t)h * HD * 2;
+        lse = p.a.lse ? p.a.lse + (size_t)(x.lo + nd) * c.n_head + h : nullptr;
+      };
+      if (pair) {
+        // a thread's own row
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        char* dst = nullptr;
+        float* lse = nullptr;
+        float* po = p.part_o + ((size_t)slot * kTile + row) * HD;
+        if (real) {
+          out_row(row, dst, lse);
+          if (whole && lse) *lse = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
+          if (!whole) p.part_ml[(size_t)slot * kTile + row] = make_float2(m, l);
+        }
+#pragma unroll 1
+        for (int t = 0; t < HD / 32; ++t) {
+          uint32_t v[32];
+          __syncwarp();
+          tmem_ld32(tO + 32 * t, v);
+          wait_ld();
+          if (!real) continue;
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int f = 0; f < 4; ++f)
+                w[f] = pack_bf16x2(__uint_as_float(v[e + 2 * f]) * inv, __uint_as_float(v[e + 2 * f + 1]) * inv);
+              *reinterpret_cast<uint4*>(dst + (32 * t + e) * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(po + 32 * t + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          }
+        }
+        sync_rows();   // Q may be overwritten: every product of the tile is done
+      } else {
+        // 256 partial rows (stream, copy, row) joined through the Q area, kDch
+        // dims at a time
+        constexpr int D = Lt::kDch, P4 = D / 4;
+        float* buf = reinterpret_cast<float*>(sm);
+        float2* ml = reinterpret_cast<float2*>(sm + 256 * D * 4);
+        const bool none = i >= steps;             // a stream without a chunk
+        ml[tid] = make_float2(none ? -CUDART_INF_F : m, none ? 0.f : l);
+        auto piece = [&](int r, int q) { return buf + r * D + ((q ^ (P4 == 8 ? r & 7 : (r >> 1) & 3)) << 2); };
+#pragma unroll 1
+        for (int t = 0; t < 4; ++t) {
+          uint32_t v[32];
+          __syncwarp();
+          tmem_ld32(tO + (D * t & ~31), v);
+          wait_ld();
+          const bool up = D == 16 && (t & 1);   // the upper half of the loaded columns
+#pragma unroll
+          for (int q = 0; q < P4; ++q) {
+            float4 f;
+            f.x = __uint_as_float(up ? v[(4 * q + 16) & 31] : v[4 * q]);
+            f.y = __uint_as_float(up ? v[(4 * q + 17) & 31] : v[4 * q + 1]);
+            f.z = __uint_as_float(up ? v[(4 * q + 18) & 31] : v[4 * q + 2]);
+            f.w = __uint_as_float(up ? v[(4 * q + 19) & 31] : v[4 * q + 3]);
+            if (none) f = make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<float4*>(piece(tid, q)) = f;
+          }
+          sync_rows();
+          for (int e = tid; e < per * P4; e += 256) {
+            const int r = e / P4, q = e - r * P4;
+            if (r >= left) continue;
+            float top = -CUDART_INF_F;
+            for (int y = 0; y < 2 * rep; ++y) top = fmaxf(top, ml[y * per + r].x);
+            const float use = top == -CUDART_INF_F ? 0.f : top;
+            float sum = 0.f;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int y = 0; y < 2 * rep; ++y) {
+              const float2 w2 = ml[y * per + r];
+              const float w = ex2(w2.x - use);
+              const float4 f = *reinterpret_cast<const float4*>(piece(y * per + r, q));
+              sum += w * w2.y;
+              a.x += w * f.x;
+              a.y += w * f.y;
+              a.z += w * f.z;
+              a.w += w * f.w;
+            }
+            const int dim = D * t + 4 * q;
+            if (whole) {
+              const float inv = sum > 0.f ? 1.f / sum : 0.f;
+              char* dst;
+              float* lse;
+              out_row(r, dst, lse);
+              *reinterpret_cast<uint2*>(dst + dim * 2) =
+                  make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+              if (lse && dim == 0) *lse = sum > 0.f ? (top + log2f(sum)) * kLn2 : -CUDART_INF_F;
+            } else {
+              *reinterpret_cast<float4*>(p.part_o + ((size_t)slot * kTile + r) * HD + dim) = a;
+              if (dim == 0) p.part_ml[(size_t)slot * kTile + r] = make_float2(top, sum);
+            }
+          }
+          sync_rows();
+        }
+      }
+      // the block with a cut tile's first chunk describes it to the join
+      if (tid == 0 && g.c0 == 0 && !whole) cut = {x.lo, g.row0, g.kvh, left, block_of(U, Gr, g.u0 + g.nch - 1), slot};
+    }
+    if (tid == 0) p.cuts[b] = cut;
+  }
+
+  fence_before();
+  __syncthreads();
+  if (warp == kIssuer) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(Lt::kCols) : "memory");
+  }
+}
+
+template <int HD>
+size_t fixed_smem(int n_seq) {   // without the ring
+  return 1024 + Lay<HD>::kOffRing + 6 * 8 + 10 * 8 + (size_t)n_seq * (sizeof(long long) + sizeof(Entry));
+}
+constexpr size_t kSmemMost = 227 * 1024 - 256;
+
+template <int HD>
+cudaError_t umma_as(const AttendParams& a, const AttendWork& w, cudaStream_t st) {
+  using Lt = Lay<HD>;
+  UmmaParams p;
+  p.tm = *w.tm;
+  p.a = a;
+  p.part_o = w.part_o;
+  p.part_ml = w.part_ml;
+  p.cuts = w.cuts;
+  p.box_rows = a.c.ps < kChunk ? a.c.ps : kChunk;
+  const size_t fixed = fixed_smem<HD>(a.rows.n_seq);
+  p.stages = (int)((kSmemMost - fixed) / (Lt::kMat + 16));
+  if (p.stages > Lt::kStagesMost) p.stages = Lt::kStagesMost;
+  const size_t smem = fixed + (size_t)p.stages * (Lt::kMat + 16);
+  attend_umma_kernel<HD><<<w.sms, kThreads, smem, st>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_join<2, HD>(a, w, kTile, w.sms, st);
+}
+
+}  // namespace
+
+cudaError_t configure_attend_umma() {
+  const cudaError_t e = cudaFuncSetAttribute(attend_umma_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)kSmemMost);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(attend_umma_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost);
+}
+
+cudaError_t launch_attend_umma(const AttendParams& a, const AttendWork& w, cudaStream_t st) {
+  return a.c.hd == 64 ? umma_as<64>(a, w, st) : umma_as<128>(a, w, st);
+}
+
+}  // namespace dflash
