@@ -126,11 +126,16 @@ struct Copies {
           set_status(c.status, DEV_BAD_PAGE);
       }
     }
+    int stop = 0;
     if (lane == 0) {
       bar_wait(&empty[st], (uint32_t)((it / S) & 1) ^ 1, abort, c.status);
-      bar_expect(&full[st], G::kHalf);
+      stop = *abort;
+      if (!stop) bar_expect(&full[st], G::kHalf);
     }
-    __syncwarp();
+    if (__shfl_sync(0xffffffffu, stop, 0)) {
+      more = false;
+      return;
+    }
     uint8_t* dst = sm + st * G::kHalf;
     for (int i = 0; i < G::CS; i += p.box_rows) {
       const int slot = ch * G::CS + i;
@@ -297,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
         }
       }
       __syncwarp();
-      if (lane == 0) bar_arrive(&empty[it % S]);
+      if (lane == 0 && !s_abort) bar_arrive(&empty[it % S]);
       ++it;
       // ---- what a row does not attend to
       if (slot0 + G::WS > x.len) {
@@ -418,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
       }
       if (ragged) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) bar_arrive(&empty[st]);
+      if (lane == 0 && !s_abort) bar_arrive(&empty[st]);
       ++it;
     }
 

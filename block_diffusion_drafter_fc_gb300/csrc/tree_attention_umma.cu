@@ -29,15 +29,20 @@
 //                     more than 2^8 (weights stay below 2^8, their sum is fp32);
 //   warp 8 (a lane)   K and V chunks by TMA into a ring of stages, page by page,
 //                     across tiles;
-//   warp 9 (a lane)   tcgen05.mma: S_i = Q_i K^T (both in shared memory), O_i +=
-//                     P_i V (P in tensor memory, V as it lies: MN-major).
+//   warps 9, 10       (a lane each) tcgen05.mma of stream 0 and 1: S_i = Q_i K^T
+//                     (both in shared memory), O_i += P_i V (P in tensor memory,
+//                     V as it lies: MN-major).  Issuing waits for the pipe (60
+//                     clocks a product of 16), so one thread's barrier waits and
+//                     address arithmetic would leave it idle: one issuer per
+//                     stream took attend steps from 1900 to ... clocks.
 // Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (head_dim each).
 // The weights are rounded to bf16 for the product with V (their sum is not):
 // each is off by at most 2^-8 of itself, independently, which adds as much
 // again as the rounding of the result; splitting them as in the streaming
 // kernel would cost half of PV more.
-// Every mbarrier wait gives up after ~2 s with DFLASH_DEV_TIMEOUT and the block
-// runs to its end without further waits; tensor memory is always released.
+// Every mbarrier wait gives up after ~2 s with DFLASH_DEV_TIMEOUT; the block then
+// issues nothing more, runs to its end without further waits or arrivals, and
+// releases its tensor memory.
 #include "tree_common.cuh"
 
 namespace dflash {
@@ -46,7 +51,7 @@ using namespace tree;
 
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;   // warp 11 only gives its registers away
 constexpr int kChunk = 128, kTile = 256;
 constexpr int kMinUnits = 1;   // a block's least share of a call's units
 constexpr int kProducer = 8, kIssuer = 9;
@@ -58,7 +63,6 @@ struct Lay {
   static constexpr int kMat = kHalf * kHalves;          // a Q tile, a K or V chunk
   static constexpr int kOffRing = 2 * kMat;             // Q tiles first
   static constexpr int kStagesMost = HD == 128 ? 5 : 10;
-  static constexpr int kDch = HD / 4;                   // dims of one pass of the tile's join
   static constexpr int kCols = 512;
 };
 
@@ -130,6 +134,27 @@ DF_DEVICE void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "me
 DF_DEVICE void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 DF_DEVICE void sync_rows() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
+DF_DEVICE void publish(int* at, int v) {
+  asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(su32(at)), "r"(v) : "memory");
+}
+// Wait for copy number `pos` in its stage's barrier.  The stages of a split tile
+// alternate between the streams, and copies land in any order, so a stream may
+// come to a stage whose last use, the other stream's, has not landed yet: the
+// barrier is then two phases behind, which its parity cannot tell from done.  A
+// copy that has been issued has no such predecessor.
+DF_DEVICE void copy_wait(int* issued, int pos, uint64_t* b, uint32_t par, volatile int* abort, unsigned* status) {
+  int n;
+  const long long t0 = clock64();
+  do {
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(n) : "r"(su32(issued)) : "memory");
+    if (n <= pos && clock64() - t0 > kWait) {
+      *abort = 1;
+      set_status(status, DEV_TIMEOUT);
+    }
+  } while (n <= pos && !*abort);
+  bar_wait(b, par, abort, status);
+}
+
 struct UmmaParams {
   CUtensorMap tm;     // pages as [rows of (page, layer, k|v, head)][page_size][hd], boxes of 64 dims
   AttendParams a;
@@ -162,6 +187,102 @@ DF_DEVICE uint32_t visible(const AttendParams& p, const Entry& x, int node, int 
   return v;
 }
 
+// Two fp32 operations at a time.
+DF_DEVICE uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+DF_DEVICE void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+DF_DEVICE uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+DF_DEVICE uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// One row's share of a chunk: slots slot0 + col0 .. + 32 NB - 1 of the chunk at
+// slot0.  Scores from tensor memory, weights back over them (zeros for the rest
+// of the chunk's slots), m and l updated, the accumulator rescaled where the
+// maximum grew (`later`: it holds something; its products are done, the scores'
+// barrier follows them).
+template <int NB, int HD>
+DF_DEVICE void softmax_step(const AttendParams& p, const Entry& x, int node, int slot0, int col0, bool part,
+                            uint32_t tS, uint32_t tO, float scale, bool later, float& m, float& l) {
+  uint32_t v[NB][32];
+  __syncwarp();
+#pragma unroll
+  for (int t = 0; t < NB; ++t) tmem_ld32(tS + col0 + 32 * t, v[t]);
+  if (part) {
+    uint32_t see[NB];
+#pragma unroll
+    for (int t = 0; t < NB; ++t) see[t] = visible(p, x, node, slot0 + col0 + 32 * t);
+    wait_ld();
+#pragma unroll
+    for (int t = 0; t < NB; ++t)
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (!(see[t] & (1u << e))) v[t][e] = 0xff800000u;   // -inf
+  } else {
+    wait_ld();
+  }
+  float t4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+  for (int t = 0; t < NB; ++t)
+#pragma unroll
+    for (int e = 0; e < 32; e += 2)
+      t4[(e >> 1) & 3] = fmaxf(fmaxf(t4[(e >> 1) & 3], __uint_as_float(v[t][e])), __uint_as_float(v[t][e + 1]));
+  const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * scale;
+  float fade = 1.f;
+  if (top > m + 8.f) {
+    fade = ex2(m - top);   // 0 when nothing was attended yet
+    l *= fade;
+    m = top;
+  }
+  const float use = m == -CUDART_INF_F ? 0.f : m;
+  const uint64_t sc2 = pack2(scale, scale), mn2 = pack2(-use, -use);
+  uint64_t s2[2] = {0, 0};
+#pragma unroll
+  for (int t = 0; t < NB; ++t) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      float a0, a1;
+      unpack2(fma2(pack2(__uint_as_float(v[t][e]), __uint_as_float(v[t][e + 1])), sc2, mn2), a0, a1);
+      a0 = ex2(a0);
+      a1 = ex2(a1);
+      s2[(e >> 1) & 1] = add2(s2[(e >> 1) & 1], pack2(a0, a1));
+      w[e / 2] = pack_bf16x2(a0, a1);
+    }
+    tmem_st16(tS + col0 / 2 + 16 * t, w);
+  }
+  float a0, a1;
+  unpack2(add2(s2[0], s2[1]), a0, a1);
+  l += a0 + a1;
+  if (NB < 4) {   // the other copies' slots
+    const uint32_t z[16] = {};
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      if (t * 32 < col0 || t * 32 >= col0 + 32 * NB) tmem_st16(tS + 16 * t, z);
+  }
+  if (later && __any_sync(0xffffffffu, fade != 1.f)) {
+#pragma unroll 1
+    for (int t = 0; t < HD / 32; ++t) {
+      uint32_t o[32];
+      tmem_ld32(tO + 32 * t, o);
+      wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
+      tmem_st32(tO + 32 * t, o);
+    }
+  }
+  wait_st();
+}
+
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_constant__ UmmaParams p) {
   using Lt = Lay<HD>;
@@ -176,10 +297,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
   uint64_t* s_full = q_full + 1;     // [2] S_i computed (and every product before it done)
   uint64_t* p_full = s_full + 2;     // [2] P_i stored
   uint64_t* o_full = p_full + 2;     // the tile's products are done
-  long long* s_warp = reinterpret_cast<long long*>(o_full + 1);   // [10]
-  long long* s_end = s_warp + 10;
+  long long* s_warp = reinterpret_cast<long long*>(o_full + 1);   // [12]
+  long long* s_end = s_warp + 12;
   Entry* s_e = reinterpret_cast<Entry*>(s_end + p.a.rows.n_seq);
   __shared__ uint32_t s_tmem;
+  __shared__ int s_issued;           // copies issued so far
   __shared__ volatile int s_abort;
 
   const CacheView& c = p.a.c;
@@ -187,15 +309,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
       bar_init(&full[i], 1);
-      bar_init(&empty[i], 1);
+      bar_init(&empty[i], 2);
     }
     bar_init(q_full, 8);
     for (int i = 0; i < 2; ++i) {
       bar_init(&s_full[i], 1);
       bar_init(&p_full[i], 4);
     }
-    bar_init(o_full, 1);
+    bar_init(o_full, 2);
     s_abort = 0;
+    s_issued = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   plan_entries(p.a, kTile, kChunk, s_e, s_end, s_warp, kThreads, b == 0);
@@ -223,102 +346,144 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
   int s = find_entry(s_end, p.a.rows.n_seq, ub0);
   const int grp = c.n_head / c.n_head_kv;
   Segment g;
-  int it = 0;   // ring position of the segment's first K chunk
+  int it = 0;   // chunks copied before the segment, K and V
 
-  if (warp == kProducer) {
-    // ---------------------------------------------------------------- copies
-    const int none = c.n_pages * c.n_layer * 2 * c.n_head_kv;   // past the tensor: reads as zero
-    while (next_segment(p.a, kTile, kChunk, s_e, s_end, u, ub1, s, g)) {
-      const Entry x = s_e[g.s];
-      const int32_t* table = c.table + (size_t)x.q * c.max_pages;
-      const int last = (x.len + x.n - 1) >> c.ps_log2;
-      int base = -64, row = none;             // lane i holds the tensor row of page base + i
-      for (int ch = g.c0; ch < g.c1; ++ch) {
-        if (((ch * kChunk + kChunk - 1) >> c.ps_log2) > base + 31) {
-          base = (ch * kChunk) >> c.ps_log2;
-          row = none;
-          if (base + lane <= last) {
-            const int t = table[base + lane];
-            if (t >= 0 && t < c.n_pages)
-              row = (t * c.n_layer + p.a.layer) * 2 * c.n_head_kv + g.kvh;
-            else
-              set_status(c.status, DEV_BAD_PAGE);
-          }
-        }
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++it) {
-          const int st = it % S;
-          if (lane == 0) {
-            bar_wait(&empty[st], (uint32_t)((it / S) & 1) ^ 1, &s_abort, c.status);
-            bar_expect(&full[st], kMat);
-          }
-          __syncwarp();
-          uint8_t* dst = ring + st * kMat;
-          for (int i = 0; i < kChunk; i += p.box_rows) {
-            const int slot = ch * kChunk + i;
-            const int r = __shfl_sync(0xffffffffu, row, ((slot >> c.ps_log2) - base) & 31);
-            if (lane == 0)
-#pragma unroll
-              for (int h = 0; h < kHalves; ++h)
-                tma3d(dst + h * kHalf + i * 128, &p.tm, h * 64, slot & (c.ps - 1),
-                      r == none ? none : r + kv * c.n_head_kv, &full[st]);
-          }
-        }
-      }
-    }
-    // no copy may still be landing when the block ends
-    if (lane == 0)
-      for (int j = max(0, it - S); j < it; ++j) {
-        const long long t0 = clock64();
-        while (!bar_try(&full[j % S], (uint32_t)((j / S) & 1)) && clock64() - t0 < kWait) {
-        }
-      }
-  } else if (warp == kIssuer) {
-    // -------------------------------------------------------------- products
-    if (lane == 0) {
-      int seg = 0, n_p[2] = {0, 0};
-      while (next_segment(p.a, kTile, kChunk, s_e, s_end, u, ub1, s, g)) {
+  // registers: the launch's 384 x 168 split into 256 x 208 (softmax: a row's
+  // scores of a chunk are held in registers) and 128 x 88
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == kProducer) {
+      // ---------------------------------------------------------------- copies
+      const int none = c.n_pages * c.n_layer * 2 * c.n_head_kv;   // past the tensor: reads as zero
+      int st = 0, ph = 1, n = 0, stop = 0;   // ring position, parity of its empty barrier, copies issued
+      while (!stop && next_segment(p.a, kTile, kChunk, s_e, s_end, u, ub1, s, g)) {
         const Entry x = s_e[g.s];
-        const bool pair = (long long)x.n * grp - g.row0 > 128;
-        const int nc = g.c1 - g.c0, steps = pair ? 2 * nc : nc;
-        bar_wait(q_full, seg & 1, &s_abort, c.status);
-        ++seg;
-        auto scores = [&](int k) {
-          const int i = k & 1, r = it + 2 * (pair ? k >> 1 : k), st = r % S;
-          bar_wait(&full[st], (uint32_t)((r / S) & 1), &s_abort, c.status);
-          fence_after();
-          const uint64_t qa = desc_k(su32(sm + (pair ? i : 0) * kMat)), kb = desc_k(su32(ring + st * kMat));
-#pragma unroll
-          for (int e = 0; e < HD / 16; ++e) {
-            const uint32_t off = ((e >> 2) * kHalf + (e & 3) * 32) >> 4;
-            mma_ss(tmem + i * 128, qa + off, kb + off, idesc(128, false), e > 0);
+        const int32_t* table = c.table + (size_t)x.q * c.max_pages;
+        const int last = (x.len + x.n - 1) >> c.ps_log2;
+        int base = -64, row = none;             // lane i holds the tensor row of page base + i
+        for (int ch = g.c0; ch < g.c1 && !stop; ++ch) {
+          if (((ch * kChunk + kChunk - 1) >> c.ps_log2) > base + 31) {
+            base = (ch * kChunk) >> c.ps_log2;
+            row = none;
+            if (base + lane <= last) {
+              const int t = table[base + lane];
+              if (t >= 0 && t < c.n_pages)
+                row = (t * c.n_layer + p.a.layer) * 2 * c.n_head_kv + g.kvh;
+              else
+                set_status(c.status, DEV_BAD_PAGE);
+            }
           }
-          commit(&s_full[i]);
-          if (!pair || i) commit(&empty[st]);
-        };
-        scores(0);
-        if (steps > 1) scores(1);
-        for (int k = 0; k < steps; ++k) {
-          const int i = k & 1, r = it + 2 * (pair ? k >> 1 : k) + 1, st = r % S;
-          bar_wait(&p_full[i], n_p[i] & 1, &s_abort, c.status);
-          ++n_p[i];
-          bar_wait(&full[st], (uint32_t)((r / S) & 1), &s_abort, c.status);
-          fence_after();
-          const uint64_t vb = desc_mn(su32(ring + st * kMat), kHalf);
 #pragma unroll
-          for (int e = 0; e < kChunk / 16; ++e)   // 16 slots: 2 groups of 1024 bytes
-            mma_ts(tmem + 256 + i * HD, tmem + i * 128 + 8 * e, vb + ((e * 2048) >> 4), idesc(HD, true),
-                   k > 1 || e > 0);
-          if (!pair || i) commit(&empty[st]);
-          if (k + 2 < steps) scores(k + 2);
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            if (lane == 0) {
+              bar_wait(&empty[st], ph, &s_abort, c.status);
+              stop = s_abort;
+              if (!stop) {
+                bar_expect(&full[st], kMat);
+                publish(&s_issued, n + 1);
+              }
+            }
+            stop = __shfl_sync(0xffffffffu, stop, 0);
+            if (stop) break;
+            uint8_t* dst = ring + st * kMat;
+            for (int i = 0; i < kChunk; i += p.box_rows) {
+              const int slot = ch * kChunk + i;
+              const int r = __shfl_sync(0xffffffffu, row, ((slot >> c.ps_log2) - base) & 31);
+              if (lane == 0)
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h)
+                  tma3d(dst + h * kHalf + i * 128, &p.tm, h * 64, slot & (c.ps - 1),
+                        r == none ? none : r + kv * c.n_head_kv, &full[st]);
+            }
+            if (++st == S) {
+              st = 0;
+              ph ^= 1;
+            }
+          }
         }
-        commit(o_full);
-        it += 2 * nc;
       }
+      // no copy may still be landing when the block ends
+      if (lane == 0)
+        for (int j = max(0, n - S); j < n; ++j) {
+          const long long t0 = clock64();
+          while (!bar_try(&full[j % S], (uint32_t)((j / S) & 1)) && clock64() - t0 < kWait) {
+          }
+        }
+    } else if (warp < kIssuer + 2) {
+      // -------------------------------------------------------------- products
+      if (lane == 0) {
+        const int i = warp - kIssuer;
+        int base = 0, bph = 0, par = 0, n_p = 0;   // ring position of the segment's first K chunk, parities
+        const uint64_t q0 = desc_k(su32(sm)), k0 = desc_k(su32(ring)), v0 = desc_mn(su32(ring), kHalf);
+        const uint32_t dS = tmem + i * 128, dO = tmem + 256 + i * HD;
+        while (!s_abort && next_segment(p.a, kTile, kChunk, s_e, s_end, u, ub1, s, g)) {
+          const Entry x = s_e[g.s];
+          const bool pair = (long long)x.n * grp - g.row0 > 128;
+          const int nc = g.c1 - g.c0, mine = pair ? nc : (nc + 1 - i) >> 1;
+          const uint64_t qa = q0 + (pair ? i * (kMat >> 4) : 0);
+          int st = base, ph = bph, no = it;   // the K chunk's stage, parity, number; its V chunk is the next
+          it += 2 * nc;
+          auto step = [&](int& pos, int& parity, int by) {
+            pos += by;
+            if (pos >= S) {
+              pos -= S;
+              parity ^= 1;
+            }
+          };
+          // a stage is free once both streams have read it (one, of a split tile)
+          auto release = [&](int pos) {
+            if (!pair) bar_arrive(&empty[pos]);
+            commit(&empty[pos]);
+          };
+          auto scores = [&]() {
+            copy_wait(&s_issued, no, &full[st], ph, &s_abort, c.status);
+            if (s_abort) return;
+            fence_after();
+            const uint64_t kb = k0 + (uint64_t)(st * (kMat >> 4));
+#pragma unroll
+            for (int e = 0; e < HD / 16; ++e) {
+              const uint32_t off = ((e >> 2) * kHalf + (e & 3) * 32) >> 4;
+              mma_ss(dS, qa + off, kb + off, idesc(128, false), e > 0);
+            }
+            commit(&s_full[i]);
+            release(st);
+          };
+          if (!pair && i) {
+            step(st, ph, 2);
+            no += 2;
+          }
+          bar_wait(q_full, par, &s_abort, c.status);
+          par ^= 1;
+          if (mine > 0 && !s_abort) scores();
+          for (int k = 0; k < mine && !s_abort; ++k) {
+            int vs = st, vph = ph;
+            step(vs, vph, 1);
+            step(st, ph, pair ? 2 : 4);
+            copy_wait(&s_issued, no + 1, &full[vs], vph, &s_abort, c.status);
+            no += pair ? 2 : 4;
+            bar_wait(&p_full[i], n_p, &s_abort, c.status);
+            if (s_abort) break;
+            n_p ^= 1;
+            fence_after();
+            const uint64_t vb = v0 + (uint64_t)(vs * (kMat >> 4));
+#pragma unroll
+            for (int e = 0; e < kChunk / 16; ++e)   // 16 slots: 2 groups of 1024 bytes
+              mma_ts(dO, dS + 8 * e, vb + ((e * 2048) >> 4), idesc(HD, true), k > 0 || e > 0);
+            release(vs);
+            if (k + 1 < mine && !s_abort) scores();
+          }
+          if (s_abort) break;
+          commit(o_full);
+          const int to = base + 2 * nc;
+          bph ^= (to / S) & 1;
+          base = to % S;
+        }
+      }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
     // ------------------------------------------------------------------ rows
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int i = warp >> 2, pos = tid & 127;     // stream, lane of the tile
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // the warp's tensor-memory lanes: 32 (warp % 4) << 16
     const uint32_t tS = tmem + i * 128 + lanes, tO = tmem + 256 + i * HD + lanes;
@@ -331,24 +496,33 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       const int rep = left > 64 ? 1 : left > 32 ? 2 : 4, per = 128 / rep;   // copies of a row, rows
       const int nc = g.c1 - g.c0, steps = pair ? 2 * nc : nc;
       // Q: lane q of tile t is row 128 t + q (pair) or row q % per
-      for (int e = tid; e < (pair ? 2 : 1) * 128 * (HD / 8); e += 256) {
-        const int q = e / (HD / 8), pc = e - q * (HD / 8), r = pair ? q : q & (per - 1);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < left) {
-          const int node = (g.row0 + r) / grp, h = g.kvh * grp + (g.row0 + r) - node * grp;
-          v = *reinterpret_cast<const uint4*>(p.a.q + (size_t)(x.lo + node) * p.a.q_ld + (size_t)h * HD * 2 + pc * 16);
+      // (a thread's piece of a row is fixed: 256 threads cover whole rows)
+      constexpr int kPc = HD / 8, kRows = 256 / kPc, kLoads = 128 / kRows;
+      const int pc = tid & (kPc - 1), q0 = tid / kPc;
+      for (int tile = 0; tile < (pair ? 2 : 1); ++tile) {
+        uint4 v[kLoads];
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e) {
+          const int q = q0 + e * kRows, r = pair ? tile * 128 + q : q & (per - 1);
+          v[e] = make_uint4(0, 0, 0, 0);
+          if (r < left) {
+            const int node = (g.row0 + r) / grp, h = g.kvh * grp + (g.row0 + r) - node * grp;
+            v[e] = *reinterpret_cast<const uint4*>(p.a.q + (size_t)(x.lo + node) * p.a.q_ld + (size_t)h * HD * 2 + pc * 16);
+          }
         }
-        *reinterpret_cast<uint4*>(sm + (q >> 7) * kMat + (pc >> 3) * kHalf + (q & 127) * 128 +
-                                  (((pc & 7) ^ (q & 7)) << 4)) = v;
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e) {
+          const int q = q0 + e * kRows;
+          *reinterpret_cast<uint4*>(sm + tile * kMat + (pc >> 3) * kHalf + q * 128 + (((pc & 7) ^ (q & 7)) << 4)) = v[e];
+        }
       }
       fence_async();
       fence_before();
       __syncwarp();
-      if (lane == 0) bar_arrive(q_full);
+      if (lane == 0 && !s_abort) bar_arrive(q_full);
 
       const int row = pair ? i * 128 + pos : pos & (per - 1);
-      const int copy = pair ? 0 : pos / per, col0 = copy * per, batches = per / 32;
-      // per / 32: the copy's share of a chunk's slots, in batches of 32
+      const int col0 = pair ? 0 : pos / per * per;   // the copy's share of a chunk's slots: col0 .. col0 + per - 1
       const bool real = row < left;
       const int node = real ? (g.row0 + row) / grp : 0;
       const bool idle = !__any_sync(0xffffffffu, real);   // S and so P are zero, or of no row
@@ -359,79 +533,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         fence_after();
         if (!idle) {
           const bool part = slot0 + kChunk > x.len;   // nodes or slots past the last among them
-          float top = -CUDART_INF_F;
-          for (int t = 0; t < batches; ++t) {
-            uint32_t v[32];
-            __syncwarp();
-            tmem_ld32(tS + col0 + 32 * t, v);
-            const uint32_t see = part ? visible(p.a, x, node, slot0 + col0 + 32 * t) : ~0u;
-            wait_ld();
-            if (part) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (see & (1u << e)) top = fmaxf(top, __uint_as_float(v[e]));
-            } else {
-              float t4[4] = {top, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
-              for (int e = 0; e < 32; ++e) t4[e & 3] = fmaxf(t4[e & 3], __uint_as_float(v[e]));
-              top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-            }
-          }
-          top *= scale;
-          // a larger maximum: the accumulator's products so far are done
-          // (s_full follows them)
-          float fade = 1.f;
-          if (top > m + 8.f) {
-            fade = ex2(m - top);   // 0 when nothing was attended yet
-            l *= fade;
-            m = top;
-          }
-          if (k > 1 && __any_sync(0xffffffffu, fade != 1.f)) {
-#pragma unroll 1
-            for (int t = 0; t < HD / 32; ++t) {
-              uint32_t v[32];
-              __syncwarp();
-              tmem_ld32(tO + 32 * t, v);
-              wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * fade);
-              tmem_st32(tO + 32 * t, v);
-            }
-          }
-          const float use = m == -CUDART_INF_F ? 0.f : m;
-          float s4[4] = {0.f, 0.f, 0.f, 0.f};
-          for (int t = 0; t < batches; ++t) {
-            uint32_t v[32], w[16];
-            __syncwarp();
-            tmem_ld32(tS + col0 + 32 * t, v);
-            const uint32_t see = part ? visible(p.a, x, node, slot0 + col0 + 32 * t) : ~0u;
-            wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float a0 = ex2(fmaf(__uint_as_float(v[e]), scale, -use));
-              float a1 = ex2(fmaf(__uint_as_float(v[e + 1]), scale, -use));
-              if (part) {
-                a0 = see & (1u << e) ? a0 : 0.f;
-                a1 = see & (2u << e) ? a1 : 0.f;
-              }
-              s4[e & 2] += a0;
-              s4[(e & 2) + 1] += a1;
-              w[e / 2] = pack_bf16x2(a0, a1);
-            }
-            tmem_st16(tS + col0 / 2 + 16 * t, w);
-          }
-          l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-          if (rep > 1) {   // the other copies' slots
-            const uint32_t z[16] = {};
-            for (int t = 0; t < 4; ++t)
-              if (t * 32 < col0 || t * 32 >= col0 + per) tmem_st16(tS + 16 * t, z);
-          }
-          wait_st();
+          if (rep == 1)
+            softmax_step<4, HD>(p.a, x, node, slot0, 0, part, tS, tO, scale, k > 1, m, l);
+          else if (rep == 2)
+            softmax_step<2, HD>(p.a, x, node, slot0, col0, part, tS, tO, scale, k > 1, m, l);
+          else
+            softmax_step<1, HD>(p.a, x, node, slot0, col0, part, tS, tO, scale, k > 1, m, l);
         }
-        if (slot0 + kChunk > end && (!pair || i == 0)) {
-          // slots past the last node may hold anything: 0 x NaN is NaN
+        if (slot0 + kChunk > end) {
+          // slots past the last node may hold anything: 0 x NaN is NaN (of a pair,
+          // each stream clears them before its own product)
           const int r = it + 2 * j + 1, st = r % S;
-          bar_wait(&full[st], (uint32_t)((r / S) & 1), &s_abort, c.status);
+          copy_wait(&s_issued, r, &full[st], (uint32_t)((r / S) & 1), &s_abort, c.status);
           const int first = max(0, end - slot0);
           for (int e = first * (HD / 8) + pos; e < kChunk * (HD / 8); e += 128) {
             const int q = e / (HD / 8), pc = e - q * (HD / 8);
@@ -442,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         }
         fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(&p_full[i]);
+        if (lane == 0 && !s_abort) bar_arrive(&p_full[i]);
       }
       it += 2 * nc;
 
@@ -493,62 +606,74 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         }
         sync_rows();   // Q may be overwritten: every product of the tile is done
       } else {
-        // 256 partial rows (stream, copy, row) joined through the Q area, kDch
-        // dims at a time
-        constexpr int D = Lt::kDch, P4 = D / 4;
+        // the 2 rep copies (stream, share of the slots) of a row joined through the
+        // Q area, as many of the dims at a time as it holds
+        const int copies = 2 * rep, lines = copies * left;
+        const int D = lines * HD * 4 <= 2 * kMat ? HD : HD / 2;
         float* buf = reinterpret_cast<float*>(sm);
-        float2* ml = reinterpret_cast<float2*>(sm + 256 * D * 4);
-        const bool none = i >= steps;             // a stream without a chunk
+        float2* ml = reinterpret_cast<float2*>(sm);            // [copies][per], before the buffer's first use
+        const bool none = i >= steps;                          // a stream without a chunk
+        const int cp = i * rep + pos / per;                    // the thread's copy of its row
         ml[tid] = make_float2(none ? -CUDART_INF_F : m, none ? 0.f : l);
-        auto piece = [&](int r, int q) { return buf + r * D + ((q ^ (P4 == 8 ? r & 7 : (r >> 1) & 3)) << 2); };
-#pragma unroll 1
-        for (int t = 0; t < 4; ++t) {
-          uint32_t v[32];
-          __syncwarp();
-          tmem_ld32(tO + (D * t & ~31), v);
-          wait_ld();
-          const bool up = D == 16 && (t & 1);   // the upper half of the loaded columns
-#pragma unroll
-          for (int q = 0; q < P4; ++q) {
-            float4 f;
-            f.x = __uint_as_float(up ? v[(4 * q + 16) & 31] : v[4 * q]);
-            f.y = __uint_as_float(up ? v[(4 * q + 17) & 31] : v[4 * q + 1]);
-            f.z = __uint_as_float(up ? v[(4 * q + 18) & 31] : v[4 * q + 2]);
-            f.w = __uint_as_float(up ? v[(4 * q + 19) & 31] : v[4 * q + 3]);
-            if (none) f = make_float4(0.f, 0.f, 0.f, 0.f);
-            *reinterpret_cast<float4*>(piece(tid, q)) = f;
+        sync_rows();
+        float top = -CUDART_INF_F, sum = 0.f;
+        for (int y = 0; y < copies; ++y) top = fmaxf(top, ml[y * per + row].x);
+        const float use = top == -CUDART_INF_F ? 0.f : top;
+        for (int y = 0; y < copies; ++y) sum += ex2(ml[y * per + row].x - use) * ml[y * per + row].y;
+        // the row's result is a weighted sum of its copies
+        const float wgt = none ? 0.f : ex2(m - use) * (!whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f);
+        if (cp == 0 && real) {
+          if (!whole) {
+            p.part_ml[(size_t)slot * kTile + row] = make_float2(top, sum);
+          } else {
+            char* dst;
+            float* lse;
+            out_row(row, dst, lse);
+            if (lse) *lse = sum > 0.f ? (top + log2f(sum)) * kLn2 : -CUDART_INF_F;
           }
-          sync_rows();
-          for (int e = tid; e < per * P4; e += 256) {
-            const int r = e / P4, q = e - r * P4;
-            if (r >= left) continue;
-            float top = -CUDART_INF_F;
-            for (int y = 0; y < 2 * rep; ++y) top = fmaxf(top, ml[y * per + r].x);
-            const float use = top == -CUDART_INF_F ? 0.f : top;
-            float sum = 0.f;
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int y = 0; y < 2 * rep; ++y) {
-              const float2 w2 = ml[y * per + r];
-              const float w = ex2(w2.x - use);
-              const float4 f = *reinterpret_cast<const float4*>(piece(y * per + r, q));
-              sum += w * w2.y;
-              a.x += w * f.x;
-              a.y += w * f.y;
-              a.z += w * f.z;
-              a.w += w * f.w;
+        }
+        const int line = cp * left + row;
+        sync_rows();
+#pragma unroll 1
+        for (int d0 = 0; d0 < HD; d0 += D) {
+          if (!idle)
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+              uint32_t v[32];
+              __syncwarp();
+              tmem_ld32(tO + d0 + d, v);
+              wait_ld();
+              if (real)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                  float4 f;
+                  f.x = none ? 0.f : __uint_as_float(v[4 * q]) * wgt;
+                  f.y = none ? 0.f : __uint_as_float(v[4 * q + 1]) * wgt;
+                  f.z = none ? 0.f : __uint_as_float(v[4 * q + 2]) * wgt;
+                  f.w = none ? 0.f : __uint_as_float(v[4 * q + 3]) * wgt;
+                  *reinterpret_cast<float4*>(buf + line * D + d + ((q ^ (line & 7)) << 2)) = f;
+                }
             }
-            const int dim = D * t + 4 * q;
+          sync_rows();
+          for (int e = tid; e < left * (D / 4); e += 256) {
+            const int r = e / (D / 4), q = e - r * (D / 4);
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int y = 0; y < copies; ++y) {
+              const int ln = y * left + r;
+              const float4 f = *reinterpret_cast<const float4*>(buf + ln * D + (q & ~7) * 4 + (((q & 7) ^ (ln & 7)) << 2));
+              a.x += f.x;
+              a.y += f.y;
+              a.z += f.z;
+              a.w += f.w;
+            }
+            const int dim = d0 + 4 * q;
             if (whole) {
-              const float inv = sum > 0.f ? 1.f / sum : 0.f;
               char* dst;
               float* lse;
               out_row(r, dst, lse);
-              *reinterpret_cast<uint2*>(dst + dim * 2) =
-                  make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-              if (lse && dim == 0) *lse = sum > 0.f ? (top + log2f(sum)) * kLn2 : -CUDART_INF_F;
+              *reinterpret_cast<uint2*>(dst + dim * 2) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
             } else {
               *reinterpret_cast<float4*>(p.part_o + ((size_t)slot * kTile + r) * HD + dim) = a;
-              if (dim == 0) p.part_ml[(size_t)slot * kTile + r] = make_float2(top, sum);
             }
           }
           sync_rows();
@@ -570,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
 
 template <int HD>
 size_t fixed_smem(int n_seq) {   // without the ring
-  return 1024 + Lay<HD>::kOffRing + 6 * 8 + 10 * 8 + (size_t)n_seq * (sizeof(long long) + sizeof(Entry));
+  return 1024 + Lay<HD>::kOffRing + 6 * 8 + 12 * 8 + (size_t)n_seq * (sizeof(long long) + sizeof(Entry));
 }
 constexpr size_t kSmemMost = 227 * 1024 - 256;
 

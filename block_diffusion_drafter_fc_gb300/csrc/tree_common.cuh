@@ -59,6 +59,12 @@ DF_DEVICE float ex2(float x) {
   return y;
 }
 
+// Quotient of nonnegative numbers; the 64-bit division (some hundred clocks,
+// which every block of a small call would wait for) only where it is needed.
+DF_DEVICE long long quotient(long long a, long long b) {
+  return ((unsigned long long)(a | b) >> 32) ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
+
 // An entry of the call.  Its rows (a row: one query head of a kv head's group,
 // of one node) form tiles, its slots chunks; a unit of work is one chunk of one
 // tile of one kv head.
@@ -79,8 +85,8 @@ struct Blocks {
 
   DF_DEVICE Blocks(const AttendParams& p, int tile, int chunk_, const Entry& x) : step(0), first(0), chunk(chunk_) {
     const int g = p.c.n_head / p.c.n_head_kv;
-    count = (int)(((long long)x.n * g + tile - 1) / tile);
-    nch = (int)(((long long)x.len + x.n + chunk - 1) / chunk);
+    count = (int)quotient((long long)x.n * g + tile - 1, tile);
+    nch = (int)quotient((long long)x.len + x.n + chunk - 1, chunk);
     const int per = tile / g;
     if (!p.mask && tile % g == 0 && count > 1 && (per % chunk == 0 || chunk % per == 0)) {
       step = per;
@@ -93,12 +99,12 @@ struct Blocks {
     const int full = min(i, count - 1);   // the last block ends with the entry
     long long sum;
     if (step >= chunk) {
-      sum = (long long)full * (first / chunk) + (long long)(step / chunk) * full * (full - 1) / 2;
+      sum = (long long)full * quotient(first, chunk) + (long long)(step / chunk) * full * (full - 1) / 2;
     } else {
       // sum of floor((first + j step) / chunk) = sum of a + floor((r + j) / q)
-      const int q = chunk / step, a = (int)(first / chunk), r = (int)(first - (long long)a * chunk) / step;
+      const int q = chunk / step, a = (int)quotient(first, chunk), r = (int)(first - (long long)a * chunk) / step;
       auto tri = [&](long long x) {
-        const long long t = x / q;
+        const long long t = quotient(x, q);
         return q * (t * (t - 1) / 2) + t * (x - q * t);
       };
       sum = (long long)full * a + tri(r + full) - tri(r);
@@ -186,11 +192,11 @@ DF_DEVICE bool next_segment(const AttendParams& p, int tile, int chunk, const En
   const Blocks b(p, tile, chunk, e[s]);
   const long long first = s ? end[s - 1] : 0, per = b.before(b.count), local = u - first;
   g.s = s;
-  g.kvh = (int)(local / per);
+  g.kvh = (int)quotient(local, per);
   const long long in = local - g.kvh * per;
   int i = 0;
   if (!b.step) {
-    i = (int)(in / b.nch);
+    i = (int)quotient(in, b.nch);
   } else {
     int hi = b.count - 1;   // the last block that begins at or before `in`
     while (i < hi) {
@@ -219,8 +225,8 @@ DF_DEVICE int find_entry(const long long* end, int n, long long u) {
 }
 
 // Range of block b of G over U units, and the block that holds unit u.
-DF_DEVICE long long range_begin(long long U, int G, int b) { return U * b / G; }
-DF_DEVICE int block_of(long long U, int G, long long u) { return (int)(((u + 1) * G - 1) / U); }
+DF_DEVICE long long range_begin(long long U, int G, int b) { return quotient(U * b, G); }
+DF_DEVICE int block_of(long long U, int G, long long u) { return (int)quotient((u + 1) * G - 1, U); }
 
 // ------------------------------------------------------------------ join
 
