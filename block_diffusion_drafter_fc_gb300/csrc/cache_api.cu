@@ -373,6 +373,7 @@ int dflash_tree_attend(dflash_cache* c, int32_t layer, int32_t n_seq, const int3
     return DFLASH_ERR_INVALID_ARG;
   if (n_seq == 0 || T == 0) return DFLASH_OK;
   const int hq = c->cfg.n_head;
+  if ((int64_t)T * (hq / c->cfg.n_head_kv) > 0x7fffffff - 1024) return DFLASH_ERR_TOO_MANY_ROWS;
   if (bad_rows(c, q, q_stride, hq) || bad_rows(c, out, out_stride, hq)) return DFLASH_ERR_INVALID_ARG;
   OnDevice on(c->device);
   AttendParams p;

@@ -37,7 +37,8 @@ namespace {
 
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * kConsumers;
-constexpr int kMinUnits = 2;   // a block's least share of a call's units
+constexpr int kExtra = 2;      // units that a tile costs besides its chunks
+constexpr int kMinUnits = 3;   // a block's least share of a call's units
 
 template <int EL, int HD>
 struct Geo {
@@ -104,7 +105,7 @@ struct Copies {
   Segment g;
 
   DF_DEVICE void open(const StreamParams& p, const Entry* e, const long long* end, long long u1, int tile) {
-    more = next_segment(p.a, tile, G::CS, e, end, u, u1, s, g);
+    more = next_segment(p.a, tile, G::CS, kExtra, e, end, u, u1, s, g);
     ch = g.c0;
     base = -64;
   }
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  plan_entries(p.a, TR, G::CS, s_e, s_end, s_warp, kThreads, blockIdx.x == 0);
+  plan_entries(p.a, TR, G::CS, kExtra, s_e, s_end, s_warp, kThreads, blockIdx.x == 0);
   __syncthreads();
   const long long U = s_end[p.a.rows.n_seq - 1];
   // fewer blocks than launched where their shares would get too small
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
   long long u = ub0;
   int s = s_first, it = 0;
   Segment g;
-  while (next_segment(p.a, TR, G::CS, s_e, s_end, u, ub1, s, g)) {
+  while (next_segment(p.a, TR, G::CS, kExtra, s_e, s_end, u, ub1, s, g)) {
     const Entry x = s_e[g.s];
     const int rows = min(TR, x.n * grp - g.row0), end = x.len + x.n;
     // Q: row r is head kvh grp + (row0 + r) % grp of node (row0 + r) / grp

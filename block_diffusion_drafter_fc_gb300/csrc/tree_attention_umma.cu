@@ -51,17 +51,20 @@ using namespace tree;
 
 namespace {
 
-constexpr int kThreads = 384;   // warp 11 only gives its registers away
+constexpr int kThreads = 384;
 constexpr int kChunk = 128, kTile = 256;
-constexpr int kMinUnits = 1;   // a block's least share of a call's units
-constexpr int kProducer = 8, kIssuer = 9;
+constexpr int kExtra = 2;      // units that a tile costs besides its chunks
+constexpr int kMinUnits = 2;   // a block's least share of a call's units
+constexpr int kProducer = 8, kIssuer = 9, kLoader = 11;
 
 template <int HD>
 struct Lay {
   static constexpr int kHalf = 128 * 128;               // 128 rows x 64 dims, 128-byte swizzle
   static constexpr int kHalves = HD / 64;
   static constexpr int kMat = kHalf * kHalves;          // a Q tile, a K or V chunk
-  static constexpr int kOffRing = 2 * kMat;             // Q tiles first
+  // the tile's join takes 32 KB: the Q area of its tile, or its own
+  static constexpr int kScratch = kMat < 32768 ? 32768 : 0;
+  static constexpr int kOffRing = 2 * kMat + kScratch;  // Q tiles first
   static constexpr int kStagesMost = HD == 128 ? 5 : 10;
   static constexpr int kCols = 512;
 };
@@ -153,6 +156,12 @@ DF_DEVICE void copy_wait(int* issued, int pos, uint64_t* b, uint32_t par, volati
     }
   } while (n <= pos && !*abort);
   bar_wait(b, par, abort, status);
+}
+
+DF_DEVICE bool copy_there(int* issued, int pos, uint64_t* b, uint32_t par) {
+  int n;
+  asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(n) : "r"(su32(issued)) : "memory");
+  return n > pos && bar_try(b, par);
 }
 
 struct UmmaParams {
@@ -293,11 +302,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
   uint8_t* ring = sm + Lt::kOffRing;
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + S * kMat);
   uint64_t* empty = full + S;
-  uint64_t* q_full = empty + S;      // the tile's Q is in shared memory, the last tile's O is read
-  uint64_t* s_full = q_full + 1;     // [2] S_i computed (and every product before it done)
+  uint64_t* q_full = empty + S;      // [2] the Q of an even (odd) tile is in shared memory
+  uint64_t* q_free = q_full + 2;     // [2] Q area i is free
+  uint64_t* s_full = q_free + 2;     // [2] S_i computed (and the stream's products before it done)
   uint64_t* p_full = s_full + 2;     // [2] P_i stored
   uint64_t* o_full = p_full + 2;     // the tile's products are done
-  long long* s_warp = reinterpret_cast<long long*>(o_full + 1);   // [12]
+  uint64_t* o_free = o_full + 1;     // the tile's O has been read
+  uint64_t* turn = o_free + 1;       // [2] issuer i may issue
+  long long* s_warp = reinterpret_cast<long long*>(turn + 2);   // [12]
   long long* s_end = s_warp + 12;
   Entry* s_e = reinterpret_cast<Entry*>(s_end + p.a.rows.n_seq);
   __shared__ uint32_t s_tmem;
@@ -311,8 +323,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       bar_init(&full[i], 1);
       bar_init(&empty[i], 2);
     }
-    bar_init(q_full, 8);
+    bar_init(o_free, 8);
     for (int i = 0; i < 2; ++i) {
+      bar_init(&q_full[i], 1);
+      bar_init(&q_free[i], 8);
+      bar_init(&turn[i], 1);
       bar_init(&s_full[i], 1);
       bar_init(&p_full[i], 4);
     }
@@ -321,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
     s_issued = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  plan_entries(p.a, kTile, kChunk, s_e, s_end, s_warp, kThreads, b == 0);
+  plan_entries(p.a, kTile, kChunk, kExtra, s_e, s_end, s_warp, kThreads, b == 0);
   __syncthreads();
   const long long U = s_end[p.a.rows.n_seq - 1];
   // fewer blocks than launched where their shares would get too small
@@ -356,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       // ---------------------------------------------------------------- copies
       const int none = c.n_pages * c.n_layer * 2 * c.n_head_kv;   // past the tensor: reads as zero
       int st = 0, ph = 1, n = 0, stop = 0;   // ring position, parity of its empty barrier, copies issued
-      while (!stop && next_segment(p.a, kTile, kChunk, s_e, s_end, u, ub1, s, g)) {
+      while (!stop && next_segment(p.a, kTile, kChunk, kExtra, s_e, s_end, u, ub1, s, g)) {
         const Entry x = s_e[g.s];
         const int32_t* table = c.table + (size_t)x.q * c.max_pages;
         const int last = (x.len + x.n - 1) >> c.ps_log2;
@@ -413,14 +428,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       // -------------------------------------------------------------- products
       if (lane == 0) {
         const int i = warp - kIssuer;
-        int base = 0, bph = 0, par = 0, n_p = 0;   // ring position of the segment's first K chunk, parities
+        // ring position of the segment's first K chunk, parities
+        int base = 0, bph = 0, n_p = 0, n_t = i ^ 1, seg = 0, qb = 0;
         const uint64_t q0 = desc_k(su32(sm)), k0 = desc_k(su32(ring)), v0 = desc_mn(su32(ring), kHalf);
         const uint32_t dS = tmem + i * 128, dO = tmem + 256 + i * HD;
-        while (!s_abort && next_segment(p.a, kTile, kChunk, s_e, s_end, u, ub1, s, g)) {
+        while (!s_abort && next_segment(p.a, kTile, kChunk, kExtra, s_e, s_end, u, ub1, s, g)) {
           const Entry x = s_e[g.s];
           const bool pair = (long long)x.n * grp - g.row0 > 128;
-          const int nc = g.c1 - g.c0, mine = pair ? nc : (nc + 1 - i) >> 1;
-          const uint64_t qa = q0 + (pair ? i * (kMat >> 4) : 0);
+          const int nc = g.c1 - g.c0, rounds = pair ? nc : (nc + 1) >> 1, mine = pair ? nc : (nc + 1 - i) >> 1;
+          const uint64_t qa = q0 + (uint64_t)((pair ? i : qb) * (kMat >> 4));
+          if (!pair) qb ^= 1;
           int st = base, ph = bph, no = it;   // the K chunk's stage, parity, number; its V chunk is the next
           it += 2 * nc;
           auto step = [&](int& pos, int& parity, int by) {
@@ -436,9 +453,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
             commit(&empty[pos]);
           };
           auto scores = [&]() {
-            copy_wait(&s_issued, no, &full[st], ph, &s_abort, c.status);
-            if (s_abort) return;
-            fence_after();
             const uint64_t kb = k0 + (uint64_t)(st * (kMat >> 4));
 #pragma unroll
             for (int e = 0; e < HD / 16; ++e) {
@@ -446,31 +460,64 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
               mma_ss(dS, qa + off, kb + off, idesc(128, false), e > 0);
             }
             commit(&s_full[i]);
-            release(st);
+          };
+          auto take = [&]() {
+            bar_wait(&turn[i], n_t, &s_abort, c.status);
+            n_t ^= 1;
+          };
+          auto pass = [&]() {
+            if (!s_abort) bar_arrive(&turn[i ^ 1]);
           };
           if (!pair && i) {
             step(st, ph, 2);
             no += 2;
           }
-          bar_wait(q_full, par, &s_abort, c.status);
-          par ^= 1;
-          if (mine > 0 && !s_abort) scores();
-          for (int k = 0; k < mine && !s_abort; ++k) {
-            int vs = st, vph = ph;
+          bar_wait(&q_full[seg & 1], (seg >> 1) & 1, &s_abort, c.status);
+          if (mine > 0) copy_wait(&s_issued, no, &full[st], ph, &s_abort, c.status);
+          take();
+          if (mine > 0 && !s_abort) {
+            fence_after();
+            scores();
+          }
+          pass();
+          if (mine > 0 && !s_abort) release(st);
+          // the last tile's accumulators have been read
+          if (seg > 0) bar_wait(o_free, (seg & 1) ^ 1, &s_abort, c.status);
+          ++seg;
+          for (int k = 0; k < rounds && !s_abort; ++k) {
+            if (k >= mine) {
+              take();
+              pass();
+              continue;
+            }
+            int vs = st, vph = ph, ks = st, kph = ph;
             step(vs, vph, 1);
-            step(st, ph, pair ? 2 : 4);
+            step(ks, kph, pair ? 2 : 4);
             copy_wait(&s_issued, no + 1, &full[vs], vph, &s_abort, c.status);
             no += pair ? 2 : 4;
             bar_wait(&p_full[i], n_p, &s_abort, c.status);
-            if (s_abort) break;
             n_p ^= 1;
+            // with the next K chunk there, its scores follow PV in the same turn
+            const bool more = k + 1 < mine, ready = more && copy_there(&s_issued, no, &full[ks], kph);
+            take();
+            if (s_abort) break;
             fence_after();
             const uint64_t vb = v0 + (uint64_t)(vs * (kMat >> 4));
 #pragma unroll
             for (int e = 0; e < kChunk / 16; ++e)   // 16 slots: 2 groups of 1024 bytes
               mma_ts(dO, dS + 8 * e, vb + ((e * 2048) >> 4), idesc(HD, true), k > 0 || e > 0);
+            st = ks;
+            ph = kph;
+            if (ready) scores();
+            pass();
             release(vs);
-            if (k + 1 < mine && !s_abort) scores();
+            if (more && !ready) {
+              copy_wait(&s_issued, no, &full[st], ph, &s_abort, c.status);
+              if (s_abort) break;
+              fence_after();
+              scores();
+            }
+            if (more) release(st);
           }
           if (s_abort) break;
           commit(o_full);
@@ -480,6 +527,38 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         }
       }
       __syncwarp();
+    } else {
+      // --------------------------------------------------------------- queries
+      // lane q of tile t is row 128 t + q of a pair, row q % per of a split tile
+      constexpr int kPc = HD / 8;
+      int free_par[2] = {1, 1}, qb = 0, seg = 0;
+      while (!s_abort && next_segment(p.a, kTile, kChunk, kExtra, s_e, s_end, u, ub1, s, g)) {
+        const Entry x = s_e[g.s];
+        const int left = (int)min((long long)x.n * grp - g.row0, (long long)kTile);
+        const bool pair = left > 128;
+        const int per = left > 64 ? 128 : left > 32 ? 64 : 32;
+        for (int t = 0; t < (pair ? 2 : 1); ++t) {
+          const int area = pair ? t : qb;
+          bar_wait(&q_free[area], free_par[area], &s_abort, c.status);
+          free_par[area] ^= 1;
+          for (int e = lane; e < 128 * kPc; e += 32) {
+            const int q = e / kPc, pc = e & (kPc - 1), r = pair ? t * 128 + q : q & (per - 1);
+            const int node = min(g.row0 + r, x.n * grp - 1) / grp, h = g.kvh * grp + (g.row0 + r) % grp;
+            const char* src = p.a.q + (size_t)(x.lo + node) * p.a.q_ld + (size_t)h * HD * 2 + pc * 16;
+            const uint32_t dst = su32(sm + area * kMat + (pc >> 3) * kHalf + q * 128 + (((pc & 7) ^ (q & 7)) << 4));
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(r < left ? 16 : 0)
+                         : "memory");
+          }
+        }
+        if (!pair) qb ^= 1;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async();
+        __syncwarp();
+        if (lane == 0 && !s_abort) bar_arrive(&q_full[seg & 1]);
+        ++seg;
+        __syncwarp();
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
     // ------------------------------------------------------------------ rows
@@ -488,39 +567,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // the warp's tensor-memory lanes: 32 (warp % 4) << 16
     const uint32_t tS = tmem + i * 128 + lanes, tO = tmem + 256 + i * HD + lanes;
     const float scale = p.a.scale * kLog2e;
-    int seg = 0, n_s = 0;
-    while (next_segment(p.a, kTile, kChunk, s_e, s_end, u, ub1, s, g)) {
+    int seg = 0, n_s = 0, qb = 0;
+    while (next_segment(p.a, kTile, kChunk, kExtra, s_e, s_end, u, ub1, s, g)) {
       const Entry x = s_e[g.s];
       const int left = (int)min((long long)x.n * grp - g.row0, (long long)kTile), end = x.len + x.n;
       const bool pair = left > 128;
       const int rep = left > 64 ? 1 : left > 32 ? 2 : 4, per = 128 / rep;   // copies of a row, rows
       const int nc = g.c1 - g.c0, steps = pair ? 2 * nc : nc;
-      // Q: lane q of tile t is row 128 t + q (pair) or row q % per
-      // (a thread's piece of a row is fixed: 256 threads cover whole rows)
-      constexpr int kPc = HD / 8, kRows = 256 / kPc, kLoads = 128 / kRows;
-      const int pc = tid & (kPc - 1), q0 = tid / kPc;
-      for (int tile = 0; tile < (pair ? 2 : 1); ++tile) {
-        uint4 v[kLoads];
-#pragma unroll
-        for (int e = 0; e < kLoads; ++e) {
-          const int q = q0 + e * kRows, r = pair ? tile * 128 + q : q & (per - 1);
-          v[e] = make_uint4(0, 0, 0, 0);
-          if (r < left) {
-            const int node = (g.row0 + r) / grp, h = g.kvh * grp + (g.row0 + r) - node * grp;
-            v[e] = *reinterpret_cast<const uint4*>(p.a.q + (size_t)(x.lo + node) * p.a.q_ld + (size_t)h * HD * 2 + pc * 16);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < kLoads; ++e) {
-          const int q = q0 + e * kRows;
-          *reinterpret_cast<uint4*>(sm + tile * kMat + (pc >> 3) * kHalf + q * 128 + (((pc & 7) ^ (q & 7)) << 4)) = v[e];
-        }
-      }
-      fence_async();
-      fence_before();
-      __syncwarp();
-      if (lane == 0 && !s_abort) bar_arrive(q_full);
-
       const int row = pair ? i * 128 + pos : pos & (per - 1);
       const int col0 = pair ? 0 : pos / per * per;   // the copy's share of a chunk's slots: col0 .. col0 + per - 1
       const bool real = row < left;
@@ -604,14 +657,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
               *reinterpret_cast<uint4*>(po + 32 * t + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
           }
         }
-        sync_rows();   // Q may be overwritten: every product of the tile is done
       } else {
         // the 2 rep copies (stream, share of the slots) of a row joined through the
-        // Q area, as many of the dims at a time as it holds
+        // tile's Q area, as many of the dims at a time as it holds
         const int copies = 2 * rep, lines = copies * left;
-        const int D = lines * HD * 4 <= 2 * kMat ? HD : HD / 2;
-        float* buf = reinterpret_cast<float*>(sm);
-        float2* ml = reinterpret_cast<float2*>(sm);            // [copies][per], before the buffer's first use
+        const int D = lines * HD <= 8192 ? HD : lines * HD <= 16384 ? HD / 2 : 32;
+        float* buf = reinterpret_cast<float*>(sm + (Lt::kScratch ? 2 : qb) * kMat);
+        float2* ml = reinterpret_cast<float2*>(buf);           // [copies][per], before the buffer's first use
         const bool none = i >= steps;                          // a stream without a chunk
         const int cp = i * rep + pos / per;                    // the thread's copy of its row
         ml[tid] = make_float2(none ? -CUDART_INF_F : m, none ? 0.f : l);
@@ -679,6 +731,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
           sync_rows();
         }
       }
+      // O has been read; the Q areas of the tile are free
+      fence_before();
+      __syncwarp();
+      if (lane == 0 && !s_abort) {
+        bar_arrive(o_free);
+        if (pair || qb == 0) bar_arrive(&q_free[0]);
+        if (pair || qb == 1) bar_arrive(&q_free[1]);
+      }
+      if (!pair) qb ^= 1;
       // the block with a cut tile's first chunk describes it to the join
       if (tid == 0 && g.c0 == 0 && !whole) cut = {x.lo, g.row0, g.kvh, left, block_of(U, Gr, g.u0 + g.nch - 1), slot};
     }
@@ -695,9 +756,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
 
 template <int HD>
 size_t fixed_smem(int n_seq) {   // without the ring
-  return 1024 + Lay<HD>::kOffRing + 6 * 8 + 12 * 8 + (size_t)n_seq * (sizeof(long long) + sizeof(Entry));
+  return 1024 + Lay<HD>::kOffRing + 12 * 8 + 12 * 8 + (size_t)n_seq * (sizeof(long long) + sizeof(Entry));
 }
-constexpr size_t kSmemMost = 227 * 1024 - 256;
+constexpr size_t kSmemMost = 227 * 1024 - 64;
 
 template <int HD>
 cudaError_t umma_as(const AttendParams& a, const AttendWork& w, cudaStream_t st) {

@@ -77,13 +77,19 @@ struct Entry {
 // chunk) chunks, e_i = tile (i + 1) / group nodes, summed in closed form (the
 // tile holds whole nodes and one of tile / group and chunk divides the other);
 // else every block has all chunks.
+//
+// A tile costs `extra` units besides its chunks (starting and ending it): units 0
+// .. extra - 1 of a tile stand for no chunk.  Without them, a range of many short
+// tiles took twice the time of a range within a long one.
 struct Blocks {
   int count, nch;          // row blocks; chunks of the last (longest) one
+  int extra;
   int step;                // chain: nodes per block (0: not trimmed)
   long long first;         // slots of block 0, + chunk - 1
   int chunk;
 
-  DF_DEVICE Blocks(const AttendParams& p, int tile, int chunk_, const Entry& x) : step(0), first(0), chunk(chunk_) {
+  DF_DEVICE Blocks(const AttendParams& p, int tile, int chunk_, int extra_, const Entry& x)
+      : extra(extra_), step(0), first(0), chunk(chunk_) {
     const int g = p.c.n_head / p.c.n_head_kv;
     count = (int)quotient((long long)x.n * g + tile - 1, tile);
     nch = (int)quotient((long long)x.len + x.n + chunk - 1, chunk);
@@ -93,9 +99,9 @@ struct Blocks {
       first = (long long)x.len + per + chunk - 1;
     }
   }
-  // chunks of blocks 0 .. i - 1, i <= count
+  // units of blocks 0 .. i - 1, i <= count
   DF_DEVICE long long before(int i) const {
-    if (!step) return (long long)i * nch;
+    if (!step) return (long long)i * (nch + extra);
     const int full = min(i, count - 1);   // the last block ends with the entry
     long long sum;
     if (step >= chunk) {
@@ -109,16 +115,16 @@ struct Blocks {
       };
       sum = (long long)full * a + tri(r + full) - tri(r);
     }
-    return sum + (i == count ? nch : 0);
+    return sum + (i == count ? nch : 0) + (long long)i * extra;
   }
-  DF_DEVICE int chunks(int i) const { return (int)(before(i + 1) - before(i)); }
+  DF_DEVICE int chunks(int i) const { return (int)(before(i + 1) - before(i)) - extra; }
 };
 
 // The call's work as one list of units, the entries' one after another: fills
 // e[] and end[] (end[s]: units of entries 0..s; a skipped entry has none) with
 // all `threads` threads of the block (a multiple of 32).  One block reports
 // faults.  s_warp: a word per warp in shared memory.
-DF_DEVICE void plan_entries(const AttendParams& p, int tile, int chunk, Entry* e, long long* end,
+DF_DEVICE void plan_entries(const AttendParams& p, int tile, int chunk, int extra, Entry* e, long long* end,
                             long long* s_warp, int threads, bool report) {
   const CacheView& c = p.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -144,7 +150,7 @@ DF_DEVICE void plan_entries(const AttendParams& p, int tile, int chunk, Entry* e
       }
       e[s] = x;
       if (x.n > 0) {
-        const Blocks b(p, tile, chunk, x);
+        const Blocks b(p, tile, chunk, extra, x);
         units = c.n_head_kv * b.before(b.count);
       }
     }
@@ -181,37 +187,40 @@ struct DimVec<4> { using T = float4; };
 struct Segment {
   int s, kvh, row0;       // entry, kv head, first row of the tile
   int c0, c1, nch;        // chunks [c0, c1) of the tile's nch
-  long long u0;           // the tile's first unit
+  long long u0;           // the unit of the tile's first chunk
 };
 
 // The segments of units [u, u1): call repeatedly; s carries the entry.
-DF_DEVICE bool next_segment(const AttendParams& p, int tile, int chunk, const Entry* e, const long long* end,
-                            long long& u, long long u1, int& s, Segment& g) {
-  if (u >= u1) return false;
-  while (end[s] <= u) ++s;
-  const Blocks b(p, tile, chunk, e[s]);
-  const long long first = s ? end[s - 1] : 0, per = b.before(b.count), local = u - first;
-  g.s = s;
-  g.kvh = (int)quotient(local, per);
-  const long long in = local - g.kvh * per;
-  int i = 0;
-  if (!b.step) {
-    i = (int)quotient(in, b.nch);
-  } else {
-    int hi = b.count - 1;   // the last block that begins at or before `in`
-    while (i < hi) {
-      const int mid = (i + hi + 1) >> 1;
-      if (b.before(mid) <= in) i = mid; else hi = mid - 1;
+DF_DEVICE bool next_segment(const AttendParams& p, int tile, int chunk, int extra, const Entry* e,
+                            const long long* end, long long& u, long long u1, int& s, Segment& g) {
+  while (u < u1) {
+    while (end[s] <= u) ++s;
+    const Blocks b(p, tile, chunk, extra, e[s]);
+    const long long first = s ? end[s - 1] : 0, per = b.before(b.count), local = u - first;
+    g.s = s;
+    g.kvh = (int)quotient(local, per);
+    const long long in = local - g.kvh * per;
+    int i = 0;
+    if (!b.step) {
+      i = (int)quotient(in, b.nch + extra);
+    } else {
+      int hi = b.count - 1;   // the last block that begins at or before `in`
+      while (i < hi) {
+        const int mid = (i + hi + 1) >> 1;
+        if (b.before(mid) <= in) i = mid; else hi = mid - 1;
+      }
     }
+    const long long start = b.before(i);
+    g.row0 = i * tile;
+    g.nch = b.chunks(i);
+    const long long from = in - start, to = min((long long)g.nch + extra, from + (u1 - u));
+    g.c0 = max((int)from - extra, 0);
+    g.c1 = max((int)to - extra, 0);
+    g.u0 = first + g.kvh * per + start + extra;
+    u += to - from;
+    if (g.c1 > g.c0) return true;   // else the range ends within the tile's extra units
   }
-  const long long start = b.before(i);
-  g.row0 = i * tile;
-  g.nch = b.chunks(i);
-  g.c0 = (int)(in - start);
-  g.c1 = (int)min((long long)g.nch, g.c0 + (u1 - u));
-  g.u0 = first + g.kvh * per + start;
-  u += g.c1 - g.c0;
-  return true;
+  return false;
 }
 
 // First entry whose units end behind u.
