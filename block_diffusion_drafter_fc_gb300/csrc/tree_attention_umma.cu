@@ -23,10 +23,8 @@
 //     same, the exponentials of a chunk spread over all four warps.
 // Roles:
 //   warps 0..3, 4..7  softmax of stream 0 and 1, a thread per row: S from tensor
-//                     memory (tcgen05.ld), running maximum m and sum l, weights
-//                     e^(s - m) back as bf16 over S (the A operand of PV).  The
-//                     accumulator is rescaled only when the maximum grew by
-//                     more than 2^8 (weights stay below 2^8, their sum is fp32);
+//                     memory (tcgen05.ld), reference m and sum l, weights
+//                     e^(s - m) back as bf16 over S (the A operand of PV);
 //   warp 8 (a lane)   K and V chunks by TMA into a ring of stages, page by page,
 //                     across tiles;
 //   warps 9, 10       (a lane each) tcgen05.mma of stream 0 and 1: S_i = Q_i K^T
@@ -34,7 +32,9 @@
 //                     V as it lies: MN-major).  Issuing waits for the pipe (60
 //                     clocks a product of 16), so one thread's barrier waits and
 //                     address arithmetic would leave it idle: one issuer per
-//                     stream took attend steps from 1900 to ... clocks.
+//                     stream, and their products (PV of a chunk, scores of the
+//                     next) in strict turns, so that one stream's softmax runs
+//                     under the other's products.
 // Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (head_dim each).
 // The weights are rounded to bf16 for the product with V (their sum is not):
 // each is off by at most 2^-8 of itself, independently, which adds as much
@@ -133,7 +133,16 @@ DF_DEVICE void tmem_st16(uint32_t a, const uint32_t (&v)[16]) {
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
       "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]) : "memory");
 }
-DF_DEVICE void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Loads done; the loaded registers are operands, so that nothing that reads them can
+// be moved ahead of it
+DF_DEVICE void wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :: "memory");
+}
 DF_DEVICE void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 DF_DEVICE void sync_rows() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -145,23 +154,25 @@ DF_DEVICE void publish(int* at, int v) {
 // come to a stage whose last use, the other stream's, has not landed yet: the
 // barrier is then two phases behind, which its parity cannot tell from done.  A
 // copy that has been issued has no such predecessor.
-DF_DEVICE void copy_wait(int* issued, int pos, uint64_t* b, uint32_t par, volatile int* abort, unsigned* status) {
+DF_DEVICE int copies_issued(int* at) {
   int n;
-  const long long t0 = clock64();
-  do {
-    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(n) : "r"(su32(issued)) : "memory");
-    if (n <= pos && clock64() - t0 > kWait) {
-      *abort = 1;
-      set_status(status, DEV_TIMEOUT);
-    }
-  } while (n <= pos && !*abort);
-  bar_wait(b, par, abort, status);
+  asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(n) : "r"(su32(at)) : "memory");
+  return n;
 }
-
+DF_DEVICE bool copy_wait(int* issued, int pos, uint64_t* b, uint32_t par, volatile int* abort, unsigned* status) {
+  if (copies_issued(issued) <= pos) {
+    const long long t0 = clock64();
+    while (copies_issued(issued) <= pos && !*abort)
+      if (clock64() - t0 > kWait) {
+        *abort = 1;
+        set_status(status, DEV_TIMEOUT);
+      }
+    if (*abort) return false;
+  }
+  return bar_wait(b, par, abort, status);
+}
 DF_DEVICE bool copy_there(int* issued, int pos, uint64_t* b, uint32_t par) {
-  int n;
-  asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(n) : "r"(su32(issued)) : "memory");
-  return n > pos && bar_try(b, par);
+  return copies_issued(issued) > pos && bar_try(b, par);
 }
 
 struct UmmaParams {
@@ -214,83 +225,120 @@ DF_DEVICE uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// Scores that the row does not see become -inf.
+DF_DEVICE void hide(uint32_t (&v)[32], uint32_t see) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!(see & (1u << e))) v[e] = 0xff800000u;
+}
+
 // One row's share of a chunk: slots slot0 + col0 .. + 32 NB - 1 of the chunk at
-// slot0.  Scores from tensor memory, weights back over them (zeros for the rest
-// of the chunk's slots), m and l updated, the accumulator rescaled where the
-// maximum grew (`later`: it holds something; its products are done, the scores'
-// barrier follows them).
-template <int NB, int HD>
-DF_DEVICE void softmax_step(const AttendParams& p, const Entry& x, int node, int slot0, int col0, bool part,
-                            uint32_t tS, uint32_t tO, float scale, bool later, float& m, float& l) {
-  uint32_t v[NB][32];
-  __syncwarp();
+// slot0; scores from tensor memory, weights 2^(s - m) back over them (zeros for
+// the rest of the chunk's slots), l updated.
+//
+// m need not be the maximum: any reference that keeps the weights within fp32
+// gives the same quotient, as weights, sums and products are all floating point
+// (bf16 has fp32's exponents).  m starts at 0, and moves to the largest score
+// (with the accumulator rescaled; its products are done, the scores' barrier
+// follows them) only when a chunk's weights sum to more than 2^60 or all weights
+// so far to less than 2^-60.  So the maximum - 64 three-way comparisons and a
+// pass over the scores before the first exponential - is not on the path of a
+// chunk: it took prompts of 2047 rows over 8192 slots from 348 to 326 us.
+// MASKED: the row may not see every slot.  `later`: the accumulator holds
+// something.
+template <int NB, int HD, bool MASKED>
+DF_DEVICE void softmax_step(const AttendParams& p, const Entry& x, int node, int slot0, int col0, uint32_t tS,
+                            uint32_t tO, float scale, bool later, float& m, float& l) {
+  uint32_t w[NB][16];
+  float sum;
+  for (bool again = false;; again = true) {
+    const uint64_t sc2 = pack2(scale, scale), mn2 = pack2(-m, -m);
+    uint64_t s2[2] = {0, 0};
+    // (all loads at once: one takes some 250 clocks under the products, and a wait
+    // is for every load before it)
+    uint32_t v[NB][32];
+    __syncwarp();
 #pragma unroll
-  for (int t = 0; t < NB; ++t) tmem_ld32(tS + col0 + 32 * t, v[t]);
-  if (part) {
-    uint32_t see[NB];
+    for (int t = 0; t < NB; ++t) tmem_ld32(tS + col0 + 32 * t, v[t]);
+    if constexpr (MASKED) {
+      uint32_t see[NB];
 #pragma unroll
-    for (int t = 0; t < NB; ++t) see[t] = visible(p, x, node, slot0 + col0 + 32 * t);
-    wait_ld();
+      for (int t = 0; t < NB; ++t) see[t] = visible(p, x, node, slot0 + col0 + 32 * t);
 #pragma unroll
-    for (int t = 0; t < NB; ++t)
+      for (int t = 0; t < NB; ++t) wait_ld(v[t]);
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (!(see[t] & (1u << e))) v[t][e] = 0xff800000u;   // -inf
-  } else {
-    wait_ld();
-  }
-  float t4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+      for (int t = 0; t < NB; ++t) hide(v[t], see[t]);
+    } else {
 #pragma unroll
-  for (int t = 0; t < NB; ++t)
-#pragma unroll
-    for (int e = 0; e < 32; e += 2)
-      t4[(e >> 1) & 3] = fmaxf(fmaxf(t4[(e >> 1) & 3], __uint_as_float(v[t][e])), __uint_as_float(v[t][e + 1]));
-  const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * scale;
-  float fade = 1.f;
-  if (top > m + 8.f) {
-    fade = ex2(m - top);   // 0 when nothing was attended yet
-    l *= fade;
-    m = top;
-  }
-  const float use = m == -CUDART_INF_F ? 0.f : m;
-  const uint64_t sc2 = pack2(scale, scale), mn2 = pack2(-use, -use);
-  uint64_t s2[2] = {0, 0};
-#pragma unroll
-  for (int t = 0; t < NB; ++t) {
-    uint32_t w[16];
-#pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      float a0, a1;
-      unpack2(fma2(pack2(__uint_as_float(v[t][e]), __uint_as_float(v[t][e + 1])), sc2, mn2), a0, a1);
-      a0 = ex2(a0);
-      a1 = ex2(a1);
-      s2[(e >> 1) & 1] = add2(s2[(e >> 1) & 1], pack2(a0, a1));
-      w[e / 2] = pack_bf16x2(a0, a1);
+      for (int t = 0; t < NB; ++t) wait_ld(v[t]);
     }
-    tmem_st16(tS + col0 / 2 + 16 * t, w);
+#pragma unroll
+    for (int t = 0; t < NB; ++t) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        float a0, a1;
+        unpack2(fma2(pack2(__uint_as_float(v[t][e]), __uint_as_float(v[t][e + 1])), sc2, mn2), a0, a1);
+        a0 = ex2(a0);
+        a1 = ex2(a1);
+        s2[(e >> 1) & 1] = add2(s2[(e >> 1) & 1], pack2(a0, a1));
+        w[t][e / 2] = pack_bf16x2(a0, a1);
+      }
+    }
+    float a0, a1;
+    unpack2(add2(s2[0], s2[1]), a0, a1);
+    sum = a0 + a1;
+    const bool bad = !(sum < 0x1p60f) || !(l + sum > 0x1p-60f);
+    if (again || !__any_sync(0xffffffffu, bad)) break;
+    // ---- a new reference: the larger of the chunk's maximum and the sum so far
+    float top = l > 0.f ? m + log2f(l) : -CUDART_INF_F;
+#pragma unroll 1
+    for (int t = 0; t < NB; ++t) {
+      uint32_t o[32];
+      __syncwarp();
+      tmem_ld32(tS + col0 + 32 * t, o);
+      const uint32_t see = MASKED ? visible(p, x, node, slot0 + col0 + 32 * t) : ~0u;
+      wait_ld(o);
+      hide(o, see);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(o[e]) * scale);
+    }
+    if (!bad || top == -CUDART_INF_F) top = m;   // nothing attended yet: any reference will do
+    const float fade = ex2(m - top);
+    m = top;
+    l *= fade;
+    if (later && __any_sync(0xffffffffu, fade != 1.f)) {
+#pragma unroll 1
+      for (int t = 0; t < HD / 32; ++t) {
+        uint32_t o[32];
+        __syncwarp();
+        tmem_ld32(tO + 32 * t, o);
+        wait_ld(o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
+        tmem_st32(tO + 32 * t, o);
+      }
+    }
   }
-  float a0, a1;
-  unpack2(add2(s2[0], s2[1]), a0, a1);
-  l += a0 + a1;
+  l += sum;
+#pragma unroll
+  for (int t = 0; t < NB; ++t) tmem_st16(tS + col0 / 2 + 16 * t, w[t]);
   if (NB < 4) {   // the other copies' slots
     const uint32_t z[16] = {};
 #pragma unroll
     for (int t = 0; t < 4; ++t)
       if (t * 32 < col0 || t * 32 >= col0 + 32 * NB) tmem_st16(tS + 16 * t, z);
   }
-  if (later && __any_sync(0xffffffffu, fade != 1.f)) {
-#pragma unroll 1
-    for (int t = 0; t < HD / 32; ++t) {
-      uint32_t o[32];
-      tmem_ld32(tO + 32 * t, o);
-      wait_ld();
-#pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
-      tmem_st32(tO + 32 * t, o);
-    }
-  }
   wait_st();
 }
+
+template <int N>
+struct Int { static constexpr int value = N; };
+
+// A segment as a softmax warp keeps it.
+struct RowSeg {
+  Entry x;
+  int kvh, row0, left, whole, slot;
+};
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_constant__ UmmaParams p) {
@@ -305,13 +353,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
   uint64_t* q_full = empty + S;      // [2] the Q of an even (odd) tile is in shared memory
   uint64_t* q_free = q_full + 2;     // [2] Q area i is free
   uint64_t* s_full = q_free + 2;     // [2] S_i computed (and the stream's products before it done)
-  uint64_t* p_full = s_full + 2;     // [2] P_i stored
+  uint64_t* p_full = s_full + 2;     // [2] P_i stored, and it is stream i's turn
   uint64_t* o_full = p_full + 2;     // the tile's products are done
   uint64_t* o_free = o_full + 1;     // the tile's O has been read
-  uint64_t* turn = o_free + 1;       // [2] issuer i may issue
-  long long* s_warp = reinterpret_cast<long long*>(turn + 2);   // [12]
+  long long* s_warp = reinterpret_cast<long long*>(o_free + 1);   // [12]
   long long* s_end = s_warp + 12;
   Entry* s_e = reinterpret_cast<Entry*>(s_end + p.a.rows.n_seq);
+  __shared__ RowSeg s_seg[8];
   __shared__ uint32_t s_tmem;
   __shared__ int s_issued;           // copies issued so far
   __shared__ volatile int s_abort;
@@ -327,9 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
     for (int i = 0; i < 2; ++i) {
       bar_init(&q_full[i], 1);
       bar_init(&q_free[i], 8);
-      bar_init(&turn[i], 1);
       bar_init(&s_full[i], 1);
-      bar_init(&p_full[i], 4);
+      bar_init(&p_full[i], 5);
     }
     bar_init(o_full, 2);
     s_abort = 0;
@@ -341,11 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
   const long long U = s_end[p.a.rows.n_seq - 1];
   // fewer blocks than launched where their shares would get too small
   const int Gr = (int)min((long long)gridDim.x, max(1LL, U / kMinUnits));
-  Cut cut = {0, 0, 0, 0, -1, 0};
-  if (b >= Gr || U == 0) {
-    if (tid == 0) p.cuts[b] = cut;
-    return;
-  }
+  if (tid == 0) p.cuts[b] = {0, 0, 0, 0, -1, 0};
+  if (b >= Gr || U == 0) return;
   if (warp == kIssuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&s_tmem)),
                  "n"(Lt::kCols)
@@ -391,8 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++n) {
             if (lane == 0) {
-              bar_wait(&empty[st], ph, &s_abort, c.status);
-              stop = s_abort;
+              stop = !bar_wait(&empty[st], ph, &s_abort, c.status);
               if (!stop) {
                 bar_expect(&full[st], kMat);
                 publish(&s_issued, n + 1);
@@ -429,13 +472,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       if (lane == 0) {
         const int i = warp - kIssuer;
         // ring position of the segment's first K chunk, parities
-        int base = 0, bph = 0, n_p = 0, n_t = i ^ 1, seg = 0, qb = 0;
+        int base = 0, bph = 0, n_p = 0, seg = 0, qb = 0;
+        bool live = true;
         const uint64_t q0 = desc_k(su32(sm)), k0 = desc_k(su32(ring)), v0 = desc_mn(su32(ring), kHalf);
         const uint32_t dS = tmem + i * 128, dO = tmem + 256 + i * HD;
-        while (!s_abort && next_segment(p.a, kTile, kChunk, kExtra, s_e, s_end, u, ub1, s, g)) {
-          const Entry x = s_e[g.s];
-          const bool pair = (long long)x.n * grp - g.row0 > 128;
-          const int nc = g.c1 - g.c0, rounds = pair ? nc : (nc + 1) >> 1, mine = pair ? nc : (nc + 1 - i) >> 1;
+        while (live && next_segment(p.a, kTile, kChunk, kExtra, s_e, s_end, u, ub1, s, g)) {
+          const bool pair = (long long)s_e[g.s].n * grp - g.row0 > 128;
+          const int nc = g.c1 - g.c0, mine = pair ? nc : (nc + 1 - i) >> 1, other = pair ? nc : (nc + i) >> 1;
           const uint64_t qa = q0 + (uint64_t)((pair ? i : qb) * (kMat >> 4));
           if (!pair) qb ^= 1;
           int st = base, ph = bph, no = it;   // the K chunk's stage, parity, number; its V chunk is the next
@@ -461,46 +504,33 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
             }
             commit(&s_full[i]);
           };
-          auto take = [&]() {
-            bar_wait(&turn[i], n_t, &s_abort, c.status);
-            n_t ^= 1;
-          };
-          auto pass = [&]() {
-            if (!s_abort) bar_arrive(&turn[i ^ 1]);
-          };
           if (!pair && i) {
             step(st, ph, 2);
             no += 2;
           }
-          bar_wait(&q_full[seg & 1], (seg >> 1) & 1, &s_abort, c.status);
-          if (mine > 0) copy_wait(&s_issued, no, &full[st], ph, &s_abort, c.status);
-          take();
-          if (mine > 0 && !s_abort) {
+          live = bar_wait(&q_full[seg & 1], (seg >> 1) & 1, &s_abort, c.status);
+          if (mine > 0 && live) {
+            live = copy_wait(&s_issued, no, &full[st], ph, &s_abort, c.status);
+            if (!live) break;
             fence_after();
             scores();
+            release(st);
+            if (i == 0) bar_arrive(&p_full[0]);   // its first turn
           }
-          pass();
-          if (mine > 0 && !s_abort) release(st);
           // the last tile's accumulators have been read
-          if (seg > 0) bar_wait(o_free, (seg & 1) ^ 1, &s_abort, c.status);
+          if (seg > 0) live = live && bar_wait(o_free, (seg & 1) ^ 1, &s_abort, c.status);
           ++seg;
-          for (int k = 0; k < rounds && !s_abort; ++k) {
-            if (k >= mine) {
-              take();
-              pass();
-              continue;
-            }
+          for (int k = 0; k < mine && live; ++k) {
             int vs = st, vph = ph, ks = st, kph = ph;
             step(vs, vph, 1);
             step(ks, kph, pair ? 2 : 4);
-            copy_wait(&s_issued, no + 1, &full[vs], vph, &s_abort, c.status);
+            live = copy_wait(&s_issued, no + 1, &full[vs], vph, &s_abort, c.status);
             no += pair ? 2 : 4;
-            bar_wait(&p_full[i], n_p, &s_abort, c.status);
-            n_p ^= 1;
             // with the next K chunk there, its scores follow PV in the same turn
             const bool more = k + 1 < mine, ready = more && copy_there(&s_issued, no, &full[ks], kph);
-            take();
-            if (s_abort) break;
+            live = live && bar_wait(&p_full[i], n_p, &s_abort, c.status);
+            if (!live) break;
+            n_p ^= 1;
             fence_after();
             const uint64_t vb = v0 + (uint64_t)(vs * (kMat >> 4));
 #pragma unroll
@@ -509,17 +539,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
             st = ks;
             ph = kph;
             if (ready) scores();
-            pass();
+            // the other stream's turn: round k after stream 0's, k + 1 after stream 1's
+            if (k + i < other) bar_arrive(&p_full[i ^ 1]);
             release(vs);
             if (more && !ready) {
-              copy_wait(&s_issued, no, &full[st], ph, &s_abort, c.status);
-              if (s_abort) break;
+              live = copy_wait(&s_issued, no, &full[st], ph, &s_abort, c.status);
+              if (!live) break;
               fence_after();
               scores();
             }
             if (more) release(st);
           }
-          if (s_abort) break;
+          if (!live) break;
           commit(o_full);
           const int to = base + 2 * nc;
           bph ^= (to / S) & 1;
@@ -532,14 +563,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       // lane q of tile t is row 128 t + q of a pair, row q % per of a split tile
       constexpr int kPc = HD / 8;
       int free_par[2] = {1, 1}, qb = 0, seg = 0;
-      while (!s_abort && next_segment(p.a, kTile, kChunk, kExtra, s_e, s_end, u, ub1, s, g)) {
+      bool live = true;
+      while (live && next_segment(p.a, kTile, kChunk, kExtra, s_e, s_end, u, ub1, s, g)) {
         const Entry x = s_e[g.s];
         const int left = (int)min((long long)x.n * grp - g.row0, (long long)kTile);
         const bool pair = left > 128;
         const int per = left > 64 ? 128 : left > 32 ? 64 : 32;
         for (int t = 0; t < (pair ? 2 : 1); ++t) {
           const int area = pair ? t : qb;
-          bar_wait(&q_free[area], free_par[area], &s_abort, c.status);
+          live = live && bar_wait(&q_free[area], free_par[area], &s_abort, c.status);
           free_par[area] ^= 1;
           for (int e = lane; e < 128 * kPc; e += 32) {
             const int q = e / kPc, pc = e & (kPc - 1), r = pair ? t * 128 + q : q & (per - 1);
@@ -554,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         asm volatile("cp.async.wait_all;" ::: "memory");
         fence_async();
         __syncwarp();
-        if (lane == 0 && !s_abort) bar_arrive(&q_full[seg & 1]);
+        if (lane == 0 && live) bar_arrive(&q_full[seg & 1]);
         ++seg;
         __syncwarp();
       }
@@ -568,36 +600,59 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
     const uint32_t tS = tmem + i * 128 + lanes, tO = tmem + 256 + i * HD + lanes;
     const float scale = p.a.scale * kLog2e;
     int seg = 0, n_s = 0, qb = 0;
+    bool live = true;   // after a wait that gave up: no more arrivals
     while (next_segment(p.a, kTile, kChunk, kExtra, s_e, s_end, u, ub1, s, g)) {
-      const Entry x = s_e[g.s];
-      const int left = (int)min((long long)x.n * grp - g.row0, (long long)kTile), end = x.len + x.n;
+      // the segment waits in shared memory: its registers are the weights'
+      const int left = (int)min((long long)s_e[g.s].n * grp - g.row0, (long long)kTile);
+      if (lane == 0) {
+        RowSeg& w = s_seg[warp];
+        w.x = s_e[g.s];
+        w.kvh = g.kvh;
+        w.row0 = g.row0;
+        w.whole = g.c0 == 0 && g.c1 == g.nch;
+        // partial rows: slot 0 of the block if its range starts in the tile, else 1
+        w.slot = 2 * b + (ub0 >= g.u0 ? 0 : 1);
+        w.left = left;
+        // the block with a cut tile's first chunk describes it to the join
+        if (tid == 0 && g.c0 == 0 && !w.whole)
+          p.cuts[b] = {w.x.lo, g.row0, g.kvh, left, block_of(U, Gr, g.u0 + g.nch - 1), w.slot};
+      }
+      __syncwarp();
       const bool pair = left > 128;
       const int rep = left > 64 ? 1 : left > 32 ? 2 : 4, per = 128 / rep;   // copies of a row, rows
       const int nc = g.c1 - g.c0, steps = pair ? 2 * nc : nc;
       const int row = pair ? i * 128 + pos : pos & (per - 1);
       const int col0 = pair ? 0 : pos / per * per;   // the copy's share of a chunk's slots: col0 .. col0 + per - 1
       const bool real = row < left;
-      const int node = real ? (g.row0 + row) / grp : 0;
+      const int node = real ? (g.row0 + row) / grp : 0, s_len = s_seg[warp].x.len, end = s_len + s_seg[warp].x.n;
+      const int ch0 = g.c0;
       const bool idle = !__any_sync(0xffffffffu, real);   // S and so P are zero, or of no row
-      float m = -CUDART_INF_F, l = 0.f;
+      float m = 0.f, l = 0.f;
+      auto step = [&](auto nb, int slot0, bool part, bool later) {
+        constexpr int NB = decltype(nb)::value;
+        if (part)
+          softmax_step<NB, HD, true>(p.a, s_seg[warp].x, node, slot0, col0, tS, tO, scale, later, m, l);
+        else
+          softmax_step<NB, HD, false>(p.a, s_seg[warp].x, node, slot0, col0, tS, tO, scale, later, m, l);
+      };
       for (int k = i; k < steps; k += 2, ++n_s) {
-        const int j = pair ? k >> 1 : k, slot0 = (g.c0 + j) * kChunk;
-        bar_wait(&s_full[i], n_s & 1, &s_abort, c.status);
+        const int j = pair ? k >> 1 : k, slot0 = (ch0 + j) * kChunk;
+        live = live && bar_wait(&s_full[i], n_s & 1, &s_abort, c.status);
         fence_after();
         if (!idle) {
-          const bool part = slot0 + kChunk > x.len;   // nodes or slots past the last among them
+          const bool part = slot0 + kChunk > s_len;   // nodes or slots past the last among them
           if (rep == 1)
-            softmax_step<4, HD>(p.a, x, node, slot0, 0, part, tS, tO, scale, k > 1, m, l);
+            step(Int<4>(), slot0, part, k > 1);
           else if (rep == 2)
-            softmax_step<2, HD>(p.a, x, node, slot0, col0, part, tS, tO, scale, k > 1, m, l);
+            step(Int<2>(), slot0, part, k > 1);
           else
-            softmax_step<1, HD>(p.a, x, node, slot0, col0, part, tS, tO, scale, k > 1, m, l);
+            step(Int<1>(), slot0, part, k > 1);
         }
         if (slot0 + kChunk > end) {
           // slots past the last node may hold anything: 0 x NaN is NaN (of a pair,
           // each stream clears them before its own product)
           const int r = it + 2 * j + 1, st = r % S;
-          copy_wait(&s_issued, r, &full[st], (uint32_t)((r / S) & 1), &s_abort, c.status);
+          live = live && copy_wait(&s_issued, r, &full[st], (uint32_t)((r / S) & 1), &s_abort, c.status);
           const int first = max(0, end - slot0);
           for (int e = first * (HD / 8) + pos; e < kChunk * (HD / 8); e += 128) {
             const int q = e / (HD / 8), pc = e - q * (HD / 8);
@@ -608,21 +663,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         }
         fence_before();
         __syncwarp();
-        if (lane == 0 && !s_abort) bar_arrive(&p_full[i]);
+        if (lane == 0 && live) bar_arrive(&p_full[i]);
       }
       it += 2 * nc;
 
       // ---- the tile's end
-      bar_wait(o_full, seg & 1, &s_abort, c.status);
+      live = live && bar_wait(o_full, seg & 1, &s_abort, c.status);
       ++seg;
       fence_after();
-      const bool whole = g.c0 == 0 && g.c1 == g.nch;
-      // partial rows: slot 0 of the block if its range starts in the tile, else 1
-      const int slot = 2 * b + (ub0 >= g.u0 ? 0 : 1);
+      if (l == 0.f) m = -CUDART_INF_F;   // nothing attended: no reference to others
+      const RowSeg w = s_seg[warp];
+      const bool whole = w.whole;
+      const int slot = w.slot;
       auto out_row = [&](int r, char*& dst, float*& lse) {
-        const int nd = (g.row0 + r) / grp, h = g.kvh * grp + (g.row0 + r) - nd * grp;
-        dst = p.a.out + (size_t)(x.lo + nd) * p.a.out_ld + (size_t)h * HD * 2;
-        lse = p.a.lse ? p.a.lse + (size_t)(x.lo + nd) * c.n_head + h : nullptr;
+        const int nd = (w.row0 + r) / grp, h = w.kvh * grp + (w.row0 + r) - nd * grp;
+        dst = p.a.out + (size_t)(w.x.lo + nd) * p.a.out_ld + (size_t)h * HD * 2;
+        lse = p.a.lse ? p.a.lse + (size_t)(w.x.lo + nd) * c.n_head + h : nullptr;
       };
       if (pair) {
         // a thread's own row
@@ -640,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
           uint32_t v[32];
           __syncwarp();
           tmem_ld32(tO + 32 * t, v);
-          wait_ld();
+          wait_ld(v);
           if (!real) continue;
           if (whole) {
 #pragma unroll
@@ -694,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
               uint32_t v[32];
               __syncwarp();
               tmem_ld32(tO + d0 + d, v);
-              wait_ld();
+              wait_ld(v);
               if (real)
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
@@ -734,16 +790,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       // O has been read; the Q areas of the tile are free
       fence_before();
       __syncwarp();
-      if (lane == 0 && !s_abort) {
+      if (lane == 0 && live) {
         bar_arrive(o_free);
         if (pair || qb == 0) bar_arrive(&q_free[0]);
         if (pair || qb == 1) bar_arrive(&q_free[1]);
       }
       if (!pair) qb ^= 1;
-      // the block with a cut tile's first chunk describes it to the join
-      if (tid == 0 && g.c0 == 0 && !whole) cut = {x.lo, g.row0, g.kvh, left, block_of(U, Gr, g.u0 + g.nch - 1), slot};
     }
-    if (tid == 0) p.cuts[b] = cut;
   }
 
   fence_before();
@@ -756,9 +809,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
 
 template <int HD>
 size_t fixed_smem(int n_seq) {   // without the ring
-  return 1024 + Lay<HD>::kOffRing + 12 * 8 + 12 * 8 + (size_t)n_seq * (sizeof(long long) + sizeof(Entry));
+  return 1024 + Lay<HD>::kOffRing + 10 * 8 + 12 * 8 + (size_t)n_seq * (sizeof(long long) + sizeof(Entry));
 }
-constexpr size_t kSmemMost = 227 * 1024 - 64;
+constexpr size_t kSmemMost = 227 * 1024 - 512;   // static shared memory aside
 
 template <int HD>
 cudaError_t umma_as(const AttendParams& a, const AttendWork& w, cudaStream_t st) {

@@ -33,18 +33,21 @@ DF_DEVICE bool bar_try(uint64_t* b, uint32_t par) {
       : "memory");
   return ok != 0;
 }
-// Bounded wait; after one that gave up the block runs to its end without waiting.
-DF_DEVICE void bar_wait(uint64_t* b, uint32_t par, volatile int* abort, unsigned* status) {
-  if (bar_try(b, par) || *abort) return;
+// Bounded wait: false when it, or one of another thread, gave up; the block then
+// runs to its end without waiting.
+DF_DEVICE bool bar_wait(uint64_t* b, uint32_t par, volatile int* abort, unsigned* status) {
+  if (bar_try(b, par)) return true;
+  if (*abort) return false;
   const long long t0 = clock64();
   while (!bar_try(b, par)) {
-    if (*abort) return;
+    if (*abort) return false;
     if (clock64() - t0 > kWait) {
       *abort = 1;
       set_status(status, DEV_TIMEOUT);
-      return;
+      return false;
     }
   }
+  return true;
 }
 DF_DEVICE void tma3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* b) {
   asm volatile(
