@@ -37,7 +37,6 @@ namespace {
 
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * kConsumers;
-constexpr int kExtra = 2;      // units that a tile costs besides its chunks
 constexpr int kMinUnits = 3;   // a block's least share of a call's units
 
 template <int EL, int HD>
@@ -84,6 +83,12 @@ DF_DEVICE void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
 }
 
+// every chunk one unit, a tile two besides
+template <int EL>
+DF_DEVICE Cutting cutting(int tile) {
+  return {tile, Geo<EL, 64>::CS, 0, 1, 1, 2};
+}
+
 struct StreamParams {
   CUtensorMap tm;     // pages as [rows of (page, layer, k|v, head)][page_size][hd]
   AttendParams a;
@@ -105,7 +110,7 @@ struct Copies {
   Segment g;
 
   DF_DEVICE void open(const StreamParams& p, const Entry* e, const long long* end, long long u1, int tile) {
-    more = next_segment(p.a, tile, G::CS, kExtra, e, end, u, u1, s, g);
+    more = next_segment(p.a, cutting<EL>(tile), e, end, u, u1, s, g);
     ch = g.c0;
     base = -64;
   }
@@ -191,11 +196,11 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  plan_entries(p.a, TR, G::CS, kExtra, s_e, s_end, s_warp, kThreads, blockIdx.x == 0);
+  plan_entries(p.a, cutting<EL>(TR), s_e, s_end, s_warp, kThreads, blockIdx.x == 0);
   __syncthreads();
   const long long U = s_end[p.a.rows.n_seq - 1];
   // fewer blocks than launched where their shares would get too small
-  const int Gr = (int)min((long long)gridDim.x, max(1LL, U / kMinUnits)), b = blockIdx.x;
+  const int Gr = blocks_used(U, gridDim.x, kMinUnits), b = blockIdx.x;
   Cut d = {0, 0, 0, 0, -1, 0};
   if (b >= Gr || U == 0) {
     if (tid == 0) p.cuts[b] = d;
@@ -219,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
   long long u = ub0;
   int s = s_first, it = 0;
   Segment g;
-  while (next_segment(p.a, TR, G::CS, kExtra, s_e, s_end, u, ub1, s, g)) {
+  while (next_segment(p.a, cutting<EL>(TR), s_e, s_end, u, ub1, s, g)) {
     const Entry x = s_e[g.s];
     const int rows = min(TR, x.n * grp - g.row0), end = x.len + x.n;
     // Q: row r is head kvh grp + (row0 + r) % grp of node (row0 + r) / grp
@@ -516,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
       d.row0 = g.row0;
       d.kvh = g.kvh;
       d.rows = rows;
-      d.last = block_of(U, Gr, g.u0 + g.nch - 1);
+      d.last = block_of(U, Gr, g.u0 + (long long)(g.nch - 1) * g.w);
       d.slot = slot;
     }
   }

@@ -53,18 +53,19 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kChunk = 128, kTile = 256;
-constexpr int kExtra = 2;      // units that a tile costs besides its chunks
-constexpr int kMinUnits = 2;   // a block's least share of a call's units
-constexpr int kProducer = 8, kIssuer = 9, kLoader = 11;
+// a chunk of a pair costs 3 units, of a split tile 2, a tile 8 besides
+constexpr int kWide = 128;
+DF_DEVICE Cutting cutting() { return {kTile, kChunk, kWide, 3, 2, 8}; }
+constexpr int kMinUnits = 4;   // a block's least share of a call's units
+constexpr int kScratch = 32768;   // 32 rows x 32 dims of every softmax warp
+constexpr int kProducer = 8, kIssuer = 9;
 
 template <int HD>
 struct Lay {
   static constexpr int kHalf = 128 * 128;               // 128 rows x 64 dims, 128-byte swizzle
   static constexpr int kHalves = HD / 64;
   static constexpr int kMat = kHalf * kHalves;          // a Q tile, a K or V chunk
-  // the tile's join takes 32 KB: the Q area of its tile, or its own
-  static constexpr int kScratch = kMat < 32768 ? 32768 : 0;
-  static constexpr int kOffRing = 2 * kMat + kScratch;  // Q tiles first
+  static constexpr int kOffScratch = 2 * kMat;          // Q tiles first
   static constexpr int kStagesMost = HD == 128 ? 5 : 10;
   static constexpr int kCols = 512;
 };
@@ -182,6 +183,9 @@ struct UmmaParams {
   float2* part_ml;    // [2 blocks][kTile]
   Cut* cuts;          // [blocks]
   int stages, box_rows;
+  // shared memory of its own for a tile's end (else the tile's Q area): the next
+  // tile's Q can then be loaded under it, at the cost of a ring stage
+  int scratch;
 };
 
 // Bit j: the row sees slot `slot` + j.
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int S = p.stages;
-  uint8_t* ring = sm + Lt::kOffRing;
+  uint8_t* ring = sm + Lt::kOffScratch + p.scratch;
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + S * kMat);
   uint64_t* empty = full + S;
   uint64_t* q_full = empty + S;      // [2] the Q of an even (odd) tile is in shared memory
@@ -383,11 +387,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
     s_issued = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  plan_entries(p.a, kTile, kChunk, kExtra, s_e, s_end, s_warp, kThreads, b == 0);
+  plan_entries(p.a, cutting(), s_e, s_end, s_warp, kThreads, b == 0);
   __syncthreads();
   const long long U = s_end[p.a.rows.n_seq - 1];
   // fewer blocks than launched where their shares would get too small
-  const int Gr = (int)min((long long)gridDim.x, max(1LL, U / kMinUnits));
+  const int Gr = blocks_used(U, gridDim.x, kMinUnits);
   if (tid == 0) p.cuts[b] = {0, 0, 0, 0, -1, 0};
   if (b >= Gr || U == 0) return;
   if (warp == kIssuer) {
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       // ---------------------------------------------------------------- copies
       const int none = c.n_pages * c.n_layer * 2 * c.n_head_kv;   // past the tensor: reads as zero
       int st = 0, ph = 1, n = 0, stop = 0;   // ring position, parity of its empty barrier, copies issued
-      while (!stop && next_segment(p.a, kTile, kChunk, kExtra, s_e, s_end, u, ub1, s, g)) {
+      while (!stop && next_segment(p.a, cutting(), s_e, s_end, u, ub1, s, g)) {
         const Entry x = s_e[g.s];
         const int32_t* table = c.table + (size_t)x.q * c.max_pages;
         const int last = (x.len + x.n - 1) >> c.ps_log2;
@@ -476,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         bool live = true;
         const uint64_t q0 = desc_k(su32(sm)), k0 = desc_k(su32(ring)), v0 = desc_mn(su32(ring), kHalf);
         const uint32_t dS = tmem + i * 128, dO = tmem + 256 + i * HD;
-        while (live && next_segment(p.a, kTile, kChunk, kExtra, s_e, s_end, u, ub1, s, g)) {
+        while (live && next_segment(p.a, cutting(), s_e, s_end, u, ub1, s, g)) {
           const bool pair = (long long)s_e[g.s].n * grp - g.row0 > 128;
           const int nc = g.c1 - g.c0, mine = pair ? nc : (nc + 1 - i) >> 1, other = pair ? nc : (nc + i) >> 1;
           const uint64_t qa = q0 + (uint64_t)((pair ? i : qb) * (kMat >> 4));
@@ -564,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       constexpr int kPc = HD / 8;
       int free_par[2] = {1, 1}, qb = 0, seg = 0;
       bool live = true;
-      while (live && next_segment(p.a, kTile, kChunk, kExtra, s_e, s_end, u, ub1, s, g)) {
+      while (live && next_segment(p.a, cutting(), s_e, s_end, u, ub1, s, g)) {
         const Entry x = s_e[g.s];
         const int left = (int)min((long long)x.n * grp - g.row0, (long long)kTile);
         const bool pair = left > 128;
@@ -601,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
     const float scale = p.a.scale * kLog2e;
     int seg = 0, n_s = 0, qb = 0;
     bool live = true;   // after a wait that gave up: no more arrivals
-    while (next_segment(p.a, kTile, kChunk, kExtra, s_e, s_end, u, ub1, s, g)) {
+    while (next_segment(p.a, cutting(), s_e, s_end, u, ub1, s, g)) {
       // the segment waits in shared memory: its registers are the weights'
       const int left = (int)min((long long)s_e[g.s].n * grp - g.row0, (long long)kTile);
       if (lane == 0) {
@@ -615,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         w.left = left;
         // the block with a cut tile's first chunk describes it to the join
         if (tid == 0 && g.c0 == 0 && !w.whole)
-          p.cuts[b] = {w.x.lo, g.row0, g.kvh, left, block_of(U, Gr, g.u0 + g.nch - 1), w.slot};
+          p.cuts[b] = {w.x.lo, g.row0, g.kvh, left, block_of(U, Gr, g.u0 + (long long)(g.nch - 1) * g.w), w.slot};
       }
       __syncwarp();
       const bool pair = left > 128;
@@ -628,6 +632,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       const int ch0 = g.c0;
       const bool idle = !__any_sync(0xffffffffu, real);   // S and so P are zero, or of no row
       float m = 0.f, l = 0.f;
+      // the stream is done with the tile's Q (a pair: its own area, which takes 8
+      // arrivals too).  A stream without a chunk says so at the tile's end, when its
+      // issuer has seen that Q was there.
+      auto free_q = [&]() {
+        if (lane == 0 && live) bar_arrive_n(&q_free[pair ? i : qb], pair ? 2 : 1);
+      };
       auto step = [&](auto nb, int slot0, bool part, bool later) {
         constexpr int NB = decltype(nb)::value;
         if (part)
@@ -638,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       for (int k = i; k < steps; k += 2, ++n_s) {
         const int j = pair ? k >> 1 : k, slot0 = (ch0 + j) * kChunk;
         live = live && bar_wait(&s_full[i], n_s & 1, &s_abort, c.status);
+        if (p.scratch && k + 2 >= steps) free_q();   // the stream's last scores
         fence_after();
         if (!idle) {
           const bool part = slot0 + kChunk > s_len;   // nodes or slots past the last among them
@@ -681,44 +692,54 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         lse = p.a.lse ? p.a.lse + (size_t)(w.x.lo + nd) * c.n_head + h : nullptr;
       };
       if (pair) {
-        // a thread's own row
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        char* dst = nullptr;
-        float* lse = nullptr;
-        float* po = p.part_o + ((size_t)slot * kTile + row) * HD;
+        // 32 rows x 32 dims of a warp at a time through its own shared memory, so
+        // that rows are written as whole sectors by neighbouring lanes (16-byte
+        // pieces of a thread's own row took 10000 clocks a tile)
+        const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : 0.f;
+        char* dst = reinterpret_cast<char*>(p.part_o + ((size_t)slot * kTile + row) * HD);
         if (real) {
-          out_row(row, dst, lse);
-          if (whole && lse) *lse = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
-          if (!whole) p.part_ml[(size_t)slot * kTile + row] = make_float2(m, l);
-        }
-#pragma unroll 1
-        for (int t = 0; t < HD / 32; ++t) {
-          uint32_t v[32];
-          __syncwarp();
-          tmem_ld32(tO + 32 * t, v);
-          wait_ld(v);
-          if (!real) continue;
           if (whole) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int f = 0; f < 4; ++f)
-                w[f] = pack_bf16x2(__uint_as_float(v[e + 2 * f]) * inv, __uint_as_float(v[e + 2 * f + 1]) * inv);
-              *reinterpret_cast<uint4*>(dst + (32 * t + e) * 2) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            float* lse;
+            out_row(row, dst, lse);
+            if (lse) *lse = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
           } else {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(po + 32 * t + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+            p.part_ml[(size_t)slot * kTile + row] = make_float2(m, l);
           }
         }
+        float* buf = reinterpret_cast<float*>(sm + Lt::kOffScratch) + warp * 1024;
+        const int last = left - (row - lane);   // rows of the warp that exist
+        if (!idle)
+#pragma unroll 1
+          for (int t = 0; t < HD / 32; ++t) {
+            uint32_t v[32];
+            __syncwarp();
+            tmem_ld32(tO + 32 * t, v);
+            wait_ld(v);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<float4*>(buf + lane * 32 + ((q ^ (lane & 7)) << 2)) =
+                  make_float4(__uint_as_float(v[4 * q]) * inv, __uint_as_float(v[4 * q + 1]) * inv,
+                              __uint_as_float(v[4 * q + 2]) * inv, __uint_as_float(v[4 * q + 3]) * inv);
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int r = 4 * e + (lane >> 3), q = lane & 7;
+              const float4 f = *reinterpret_cast<const float4*>(buf + r * 32 + ((q ^ (r & 7)) << 2));
+              char* d = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, (unsigned long long)dst, r));
+              if (r >= last) continue;
+              if (whole)
+                *reinterpret_cast<uint2*>(d + (32 * t + 4 * q) * 2) =
+                    make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+              else
+                *reinterpret_cast<float4*>(d + (32 * t + 4 * q) * 4) = f;
+            }
+          }
       } else {
         // the 2 rep copies (stream, share of the slots) of a row joined through the
         // tile's Q area, as many of the dims at a time as it holds
         const int copies = 2 * rep, lines = copies * left;
         const int D = lines * HD <= 8192 ? HD : lines * HD <= 16384 ? HD / 2 : 32;
-        float* buf = reinterpret_cast<float*>(sm + (Lt::kScratch ? 2 : qb) * kMat);
+        float* buf = reinterpret_cast<float*>(sm + (p.scratch ? Lt::kOffScratch : qb * kMat));
         float2* ml = reinterpret_cast<float2*>(buf);           // [copies][per], before the buffer's first use
         const bool none = i >= steps;                          // a stream without a chunk
         const int cp = i * rep + pos / per;                    // the thread's copy of its row
@@ -787,14 +808,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
           sync_rows();
         }
       }
-      // O has been read; the Q areas of the tile are free
+      // O has been read (and the tile's Q area, if it was the end's memory, is free)
       fence_before();
       __syncwarp();
       if (lane == 0 && live) {
         bar_arrive(o_free);
-        if (pair || qb == 0) bar_arrive(&q_free[0]);
-        if (pair || qb == 1) bar_arrive(&q_free[1]);
       }
+      if (!p.scratch || i >= steps) free_q();
       if (!pair) qb ^= 1;
     }
   }
@@ -809,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
 
 template <int HD>
 size_t fixed_smem(int n_seq) {   // without the ring
-  return 1024 + Lay<HD>::kOffRing + 10 * 8 + 12 * 8 + (size_t)n_seq * (sizeof(long long) + sizeof(Entry));
+  return 1024 + Lay<HD>::kOffScratch + 10 * 8 + 12 * 8 + (size_t)n_seq * (sizeof(long long) + sizeof(Entry));
 }
 constexpr size_t kSmemMost = 227 * 1024 - 512;   // static shared memory aside
 
@@ -823,7 +843,11 @@ cudaError_t umma_as(const AttendParams& a, const AttendWork& w, cudaStream_t st)
   p.part_ml = w.part_ml;
   p.cuts = w.cuts;
   p.box_rows = a.c.ps < kChunk ? a.c.ps : kChunk;
-  const size_t fixed = fixed_smem<HD>(a.rows.n_seq);
+  // pairs fill both Q areas; split tiles of 128 dims alternate between them and
+  // are bound by memory, where the stage counts for more
+  const bool pairs = (long long)a.max_tree * (a.c.n_head / a.c.n_head_kv) > kWide;
+  p.scratch = pairs || HD == 64 ? kScratch : 0;
+  const size_t fixed = fixed_smem<HD>(a.rows.n_seq) + p.scratch;
   p.stages = (int)((kSmemMost - fixed) / (Lt::kMat + 16));
   if (p.stages > Lt::kStagesMost) p.stages = Lt::kStagesMost;
   const size_t smem = fixed + (size_t)p.stages * (Lt::kMat + 16);

@@ -23,6 +23,9 @@ DF_DEVICE void bar_expect(uint64_t* b, uint32_t bytes) {
 DF_DEVICE void bar_arrive(uint64_t* b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
 }
+DF_DEVICE void bar_arrive_n(uint64_t* b, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(n) : "memory");
+}
 DF_DEVICE bool bar_try(uint64_t* b, uint32_t par) {
   uint32_t ok;
   asm volatile(
@@ -69,65 +72,73 @@ DF_DEVICE long long quotient(long long a, long long b) {
 }
 
 // An entry of the call.  Its rows (a row: one query head of a kv head's group,
-// of one node) form tiles, its slots chunks; a unit of work is one chunk of one
-// tile of one kv head.
+// of one node) form tiles, its slots chunks; the work is the chunks of every
+// tile of every kv head.
 struct Entry {
   int lo, n, len, q;
 };
 
-// The row blocks of one kv head of an entry and their chunks.  Without a mask a
+// How a kernel cuts a call's rows and slots, and what the pieces cost: a chunk
+// of a tile of more than `wide` rows `heavy` units, of others `light`, and every
+// tile `extra` units for its start and end.  Without the weights a range of many
+// short tiles took twice the time of a range within a long one.
+struct Cutting {
+  int tile, chunk, wide, heavy, light, extra;
+};
+
+// The row blocks of one kv head of an entry and their cost.  Without a mask a
 // tile sees no slot behind its last node: block i then has ceil((len + e_i) /
 // chunk) chunks, e_i = tile (i + 1) / group nodes, summed in closed form (the
 // tile holds whole nodes and one of tile / group and chunk divides the other);
 // else every block has all chunks.
-//
-// A tile costs `extra` units besides its chunks (starting and ending it): units 0
-// .. extra - 1 of a tile stand for no chunk.  Without them, a range of many short
-// tiles took twice the time of a range within a long one.
 struct Blocks {
+  Cutting c;
   int count, nch;          // row blocks; chunks of the last (longest) one
-  int extra;
   int step;                // chain: nodes per block (0: not trimmed)
+  int last;                // units of a chunk of the last block (the others are full)
   long long first;         // slots of block 0, + chunk - 1
-  int chunk;
 
-  DF_DEVICE Blocks(const AttendParams& p, int tile, int chunk_, int extra_, const Entry& x)
-      : extra(extra_), step(0), first(0), chunk(chunk_) {
+  DF_DEVICE Blocks(const AttendParams& p, const Cutting& cut, const Entry& x) : c(cut), step(0), first(0) {
     const int g = p.c.n_head / p.c.n_head_kv;
-    count = (int)quotient((long long)x.n * g + tile - 1, tile);
-    nch = (int)quotient((long long)x.len + x.n + chunk - 1, chunk);
-    const int per = tile / g;
-    if (!p.mask && tile % g == 0 && count > 1 && (per % chunk == 0 || chunk % per == 0)) {
+    const long long rows = (long long)x.n * g;
+    count = (int)quotient(rows + c.tile - 1, c.tile);
+    nch = (int)quotient((long long)x.len + x.n + c.chunk - 1, c.chunk);
+    last = rows - (long long)(count - 1) * c.tile > c.wide ? c.heavy : c.light;
+    const int per = c.tile / g;
+    if (!p.mask && c.tile % g == 0 && count > 1 && (per % c.chunk == 0 || c.chunk % per == 0)) {
       step = per;
-      first = (long long)x.len + per + chunk - 1;
+      first = (long long)x.len + per + c.chunk - 1;
     }
+  }
+  DF_DEVICE int units(int i) const { return i == count - 1 ? last : c.heavy; }   // of a chunk of block i
+  // chunks of blocks 0 .. i - 1, i <= count - 1
+  DF_DEVICE long long chunks_before(int i) const {
+    if (!step) return (long long)i * nch;
+    if (step >= c.chunk)
+      return (long long)i * quotient(first, c.chunk) + (long long)(step / c.chunk) * i * (i - 1) / 2;
+    // sum of floor((first + j step) / chunk) = sum of a + floor((r + j) / q)
+    const int q = c.chunk / step, a = (int)quotient(first, c.chunk), r = (int)(first - (long long)a * c.chunk) / step;
+    auto tri = [&](long long x) {
+      const long long t = quotient(x, q);
+      return q * (t * (t - 1) / 2) + t * (x - q * t);
+    };
+    return (long long)i * a + tri(r + i) - tri(r);
   }
   // units of blocks 0 .. i - 1, i <= count
   DF_DEVICE long long before(int i) const {
-    if (!step) return (long long)i * (nch + extra);
-    const int full = min(i, count - 1);   // the last block ends with the entry
-    long long sum;
-    if (step >= chunk) {
-      sum = (long long)full * quotient(first, chunk) + (long long)(step / chunk) * full * (full - 1) / 2;
-    } else {
-      // sum of floor((first + j step) / chunk) = sum of a + floor((r + j) / q)
-      const int q = chunk / step, a = (int)quotient(first, chunk), r = (int)(first - (long long)a * chunk) / step;
-      auto tri = [&](long long x) {
-        const long long t = quotient(x, q);
-        return q * (t * (t - 1) / 2) + t * (x - q * t);
-      };
-      sum = (long long)full * a + tri(r + full) - tri(r);
-    }
-    return sum + (i == count ? nch : 0) + (long long)i * extra;
+    return chunks_before(min(i, count - 1)) * c.heavy + (i == count ? (long long)nch * last : 0) +
+           (long long)i * c.extra;
   }
-  DF_DEVICE int chunks(int i) const { return (int)(before(i + 1) - before(i)) - extra; }
+  DF_DEVICE int chunks(int i) const {
+    return i == count - 1 ? nch : (int)(chunks_before(i + 1) - chunks_before(i));
+  }
 };
 
 // The call's work as one list of units, the entries' one after another: fills
 // e[] and end[] (end[s]: units of entries 0..s; a skipped entry has none) with
 // all `threads` threads of the block (a multiple of 32).  One block reports
 // faults.  s_warp: a word per warp in shared memory.
-DF_DEVICE void plan_entries(const AttendParams& p, int tile, int chunk, int extra, Entry* e, long long* end,
+DF_DEVICE void plan_entries(const AttendParams& p, const Cutting& cut, Entry* e, long long* end,
                             long long* s_warp, int threads, bool report) {
   const CacheView& c = p.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -153,7 +164,7 @@ DF_DEVICE void plan_entries(const AttendParams& p, int tile, int chunk, int extr
       }
       e[s] = x;
       if (x.n > 0) {
-        const Blocks b(p, tile, chunk, extra, x);
+        const Blocks b(p, cut, x);
         units = c.n_head_kv * b.before(b.count);
       }
     }
@@ -190,23 +201,22 @@ struct DimVec<4> { using T = float4; };
 struct Segment {
   int s, kvh, row0;       // entry, kv head, first row of the tile
   int c0, c1, nch;        // chunks [c0, c1) of the tile's nch
-  long long u0;           // the unit of the tile's first chunk
+  int w;                  // units of a chunk
+  long long u0;           // the first unit of the tile's first chunk
 };
 
 // The segments of units [u, u1): call repeatedly; s carries the entry.
-DF_DEVICE bool next_segment(const AttendParams& p, int tile, int chunk, int extra, const Entry* e,
+DF_DEVICE bool next_segment(const AttendParams& p, const Cutting& cut, const Entry* e,
                             const long long* end, long long& u, long long u1, int& s, Segment& g) {
   while (u < u1) {
     while (end[s] <= u) ++s;
-    const Blocks b(p, tile, chunk, extra, e[s]);
+    const Blocks b(p, cut, e[s]);
     const long long first = s ? end[s - 1] : 0, per = b.before(b.count), local = u - first;
     g.s = s;
     g.kvh = (int)quotient(local, per);
     const long long in = local - g.kvh * per;
     int i = 0;
-    if (!b.step) {
-      i = (int)quotient(in, b.nch + extra);
-    } else {
+    if (b.count > 1) {
       int hi = b.count - 1;   // the last block that begins at or before `in`
       while (i < hi) {
         const int mid = (i + hi + 1) >> 1;
@@ -214,14 +224,17 @@ DF_DEVICE bool next_segment(const AttendParams& p, int tile, int chunk, int extr
       }
     }
     const long long start = b.before(i);
-    g.row0 = i * tile;
+    g.row0 = i * cut.tile;
     g.nch = b.chunks(i);
-    const long long from = in - start, to = min((long long)g.nch + extra, from + (u1 - u));
-    g.c0 = max((int)from - extra, 0);
-    g.c1 = max((int)to - extra, 0);
-    g.u0 = first + g.kvh * per + start + extra;
+    const int w = b.units(i);
+    const long long from = in - start, to = min((long long)g.nch * w + cut.extra, from + (u1 - u));
+    // a chunk belongs to the range that holds its first unit
+    g.c0 = (int)quotient(max(from - cut.extra, 0LL) + w - 1, w);
+    g.c1 = (int)quotient(max(to - cut.extra, 0LL) + w - 1, w);
+    g.u0 = first + g.kvh * per + start + cut.extra;
+    g.w = w;
     u += to - from;
-    if (g.c1 > g.c0) return true;   // else the range ends within the tile's extra units
+    if (g.c1 > g.c0) return true;   // else the range holds no chunk of the tile
   }
   return false;
 }
@@ -234,6 +247,12 @@ DF_DEVICE int find_entry(const long long* end, int n, long long u) {
     if (end[m] > u) b = m; else a = m + 1;
   }
   return a;
+}
+
+// Blocks of a launch that take part: every range holds a chunk of each tile it
+// lies in when it is as long as the dearest chunk.
+DF_DEVICE int blocks_used(long long U, int launched, int least) {
+  return (int)min((long long)launched, max(1LL, quotient(U, least)));
 }
 
 // Range of block b of G over U units, and the block that holds unit u.
