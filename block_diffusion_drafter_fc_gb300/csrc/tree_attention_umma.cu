@@ -25,6 +25,7 @@
 //   warps 0..3, 4..7  softmax of stream 0 and 1, a thread per row: S from tensor
 //                     memory (tcgen05.ld), reference m and sum l, weights
 //                     e^(s - m) back as bf16 over S (the A operand of PV);
+//   warp 11           plans the block's segments for all, and loads their Q;
 //   warp 8 (a lane)   K and V chunks by TMA into a ring of stages, page by page,
 //                     across tiles;
 //   warps 9, 10       (a lane each) tcgen05.mma of stream 0 and 1: S_i = Q_i K^T
@@ -155,15 +156,15 @@ DF_DEVICE void publish(int* at, int v) {
 // come to a stage whose last use, the other stream's, has not landed yet: the
 // barrier is then two phases behind, which its parity cannot tell from done.  A
 // copy that has been issued has no such predecessor.
-DF_DEVICE int copies_issued(int* at) {
+DF_DEVICE int load_acquire(int* at) {
   int n;
   asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(n) : "r"(su32(at)) : "memory");
   return n;
 }
 DF_DEVICE bool copy_wait(int* issued, int pos, uint64_t* b, uint32_t par, volatile int* abort, unsigned* status) {
-  if (copies_issued(issued) <= pos) {
+  if (load_acquire(issued) <= pos) {
     const long long t0 = clock64();
-    while (copies_issued(issued) <= pos && !*abort)
+    while (load_acquire(issued) <= pos && !*abort)
       if (clock64() - t0 > kWait) {
         *abort = 1;
         set_status(status, DEV_TIMEOUT);
@@ -172,8 +173,10 @@ DF_DEVICE bool copy_wait(int* issued, int pos, uint64_t* b, uint32_t par, volati
   }
   return bar_wait(b, par, abort, status);
 }
+// y / d of y < 2^32 / d, magic = ceil(2^32 / d) (0: d = 1)
+DF_DEVICE int small_quotient(int y, uint32_t magic) { return magic ? (int)__umulhi((uint32_t)y, magic) : y; }
 DF_DEVICE bool copy_there(int* issued, int pos, uint64_t* b, uint32_t par) {
-  return copies_issued(issued) > pos && bar_try(b, par);
+  return load_acquire(issued) > pos && bar_try(b, par);
 }
 
 struct UmmaParams {
@@ -186,6 +189,7 @@ struct UmmaParams {
   // shared memory of its own for a tile's end (else the tile's Q area): the next
   // tile's Q can then be loaded under it, at the cost of a ring stage
   int scratch;
+  uint32_t grp_magic;   // ceil(2^32 / query heads per kv head): quotients of small numbers
 };
 
 // Bit j: the row sees slot `slot` + j.
@@ -338,11 +342,30 @@ DF_DEVICE void softmax_step(const AttendParams& p, const Entry& x, int node, int
 template <int N>
 struct Int { static constexpr int value = N; };
 
-// A segment as a softmax warp keeps it.
-struct RowSeg {
+// A segment (a run of a tile's chunks), planned by one warp for all: the
+// arithmetic that finds it, and its instructions, are paid for once.
+struct SegDesc {
   Entry x;
-  int kvh, row0, left, whole, slot;
+  int kvh, row0, left;   // kv head, first row, rows of the tile
+  int node0, h0;         // node and query head of row 0
+  int c0, nc;            // first chunk, chunks
+  int whole, slot;       // the whole tile; else the slot of its partial rows
 };
+constexpr int kSegs = 8;
+
+// Segment `seg` has been planned; false: there is none.
+DF_DEVICE bool seg_wait(int* planned, int* total, int seg, volatile int* abort, unsigned* status) {
+  const long long t0 = clock64();
+  while (true) {
+    if (load_acquire(planned) > seg) return true;
+    if (load_acquire(total) <= seg || *abort) return false;
+    if (clock64() - t0 > kWait) {
+      *abort = 1;
+      set_status(status, DEV_TIMEOUT);
+      return false;
+    }
+  }
+}
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_constant__ UmmaParams p) {
@@ -354,18 +377,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
   uint8_t* ring = sm + Lt::kOffScratch + p.scratch;
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + S * kMat);
   uint64_t* empty = full + S;
-  uint64_t* q_full = empty + S;      // [2] the Q of an even (odd) tile is in shared memory
+  uint64_t* q_full = empty + S;      // [2] the Q of an even (odd) segment is in shared memory
   uint64_t* q_free = q_full + 2;     // [2] Q area i is free
   uint64_t* s_full = q_free + 2;     // [2] S_i computed (and the stream's products before it done)
   uint64_t* p_full = s_full + 2;     // [2] P_i stored, and it is stream i's turn
-  uint64_t* o_full = p_full + 2;     // the tile's products are done
-  uint64_t* o_free = o_full + 1;     // the tile's O has been read
+  uint64_t* o_full = p_full + 2;     // the segment's products are done
+  uint64_t* o_free = o_full + 1;     // the segment's O has been read
   long long* s_warp = reinterpret_cast<long long*>(o_free + 1);   // [12]
   long long* s_end = s_warp + 12;
   Entry* s_e = reinterpret_cast<Entry*>(s_end + p.a.rows.n_seq);
-  __shared__ RowSeg s_seg[8];
+  __shared__ SegDesc s_seg[kSegs];
   __shared__ uint32_t s_tmem;
   __shared__ int s_issued;           // copies issued so far
+  __shared__ int s_planned, s_total; // segments planned so far; all of them, once known
   __shared__ volatile int s_abort;
 
   const CacheView& c = p.a.c;
@@ -375,7 +399,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       bar_init(&full[i], 1);
       bar_init(&empty[i], 2);
     }
-    bar_init(o_free, 8);
     for (int i = 0; i < 2; ++i) {
       bar_init(&q_full[i], 1);
       bar_init(&q_free[i], 8);
@@ -383,33 +406,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       bar_init(&p_full[i], 5);
     }
     bar_init(o_full, 2);
+    bar_init(o_free, 8);
     s_abort = 0;
     s_issued = 0;
+    s_planned = 0;
+    s_total = 0x7fffffff;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  plan_entries(p.a, cutting(), s_e, s_end, s_warp, kThreads, b == 0);
-  __syncthreads();
-  const long long U = s_end[p.a.rows.n_seq - 1];
-  // fewer blocks than launched where their shares would get too small
-  const int Gr = blocks_used(U, gridDim.x, kMinUnits);
-  if (tid == 0) p.cuts[b] = {0, 0, 0, 0, -1, 0};
-  if (b >= Gr || U == 0) return;
   if (warp == kIssuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&s_tmem)),
                  "n"(Lt::kCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  pdl_wait();
+  plan_entries(p.a, cutting(), s_e, s_end, s_warp, kThreads, b == 0);
+  if (tid == 0) p.cuts[b] = {0, 0, 0, 0, -1, 0};
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = s_tmem;
-  const long long ub0 = range_begin(U, Gr, b), ub1 = range_begin(U, Gr, b + 1);
-  long long u = ub0;
-  int s = find_entry(s_end, p.a.rows.n_seq, ub0);
-  const int grp = c.n_head / c.n_head_kv;
-  Segment g;
-  int it = 0;   // chunks copied before the segment, K and V
 
   // registers: the launch's 384 x 168 split into 256 x 208 (softmax: a row's
   // scores of a chunk are held in registers) and 128 x 88
@@ -419,24 +435,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       // ---------------------------------------------------------------- copies
       const int none = c.n_pages * c.n_layer * 2 * c.n_head_kv;   // past the tensor: reads as zero
       int st = 0, ph = 1, n = 0, stop = 0;   // ring position, parity of its empty barrier, copies issued
-      while (!stop && next_segment(p.a, cutting(), s_e, s_end, u, ub1, s, g)) {
-        const Entry x = s_e[g.s];
+      for (int seg = 0; !stop && seg_wait(&s_planned, &s_total, seg, &s_abort, c.status); ++seg) {
+        const SegDesc& d = s_seg[seg % kSegs];
+        const Entry x = d.x;
         const int32_t* table = c.table + (size_t)x.q * c.max_pages;
-        const int last = (x.len + x.n - 1) >> c.ps_log2;
+        const int last = (x.len + x.n - 1) >> c.ps_log2, head = p.a.layer * 2 * c.n_head_kv + d.kvh;
+        const int c0 = d.c0, c1 = c0 + d.nc;
         int base = -64, row = none;             // lane i holds the tensor row of page base + i
-        for (int ch = g.c0; ch < g.c1 && !stop; ++ch) {
+        for (int ch = c0; ch < c1 && !stop; ++ch) {
           if (((ch * kChunk + kChunk - 1) >> c.ps_log2) > base + 31) {
             base = (ch * kChunk) >> c.ps_log2;
             row = none;
             if (base + lane <= last) {
               const int t = table[base + lane];
               if (t >= 0 && t < c.n_pages)
-                row = (t * c.n_layer + p.a.layer) * 2 * c.n_head_kv + g.kvh;
+                row = t * c.n_layer * 2 * c.n_head_kv + head;
               else
                 set_status(c.status, DEV_BAD_PAGE);
             }
           }
-#pragma unroll
+#pragma unroll 1
           for (int kv = 0; kv < 2; ++kv, ++n) {
             if (lane == 0) {
               stop = !bar_wait(&empty[st], ph, &s_abort, c.status);
@@ -475,14 +493,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       // -------------------------------------------------------------- products
       if (lane == 0) {
         const int i = warp - kIssuer;
-        // ring position of the segment's first K chunk, parities
-        int base = 0, bph = 0, n_p = 0, seg = 0, qb = 0;
+        // ring position of the segment's first K chunk, parities, copies before it
+        int base = 0, bph = 0, n_p = 0, qb = 0, it = 0;
         bool live = true;
         const uint64_t q0 = desc_k(su32(sm)), k0 = desc_k(su32(ring)), v0 = desc_mn(su32(ring), kHalf);
         const uint32_t dS = tmem + i * 128, dO = tmem + 256 + i * HD;
-        while (live && next_segment(p.a, cutting(), s_e, s_end, u, ub1, s, g)) {
-          const bool pair = (long long)s_e[g.s].n * grp - g.row0 > 128;
-          const int nc = g.c1 - g.c0, mine = pair ? nc : (nc + 1 - i) >> 1, other = pair ? nc : (nc + i) >> 1;
+        for (int seg = 0; live && seg_wait(&s_planned, &s_total, seg, &s_abort, c.status); ++seg) {
+          const SegDesc& d = s_seg[seg % kSegs];
+          const bool pair = d.left > 128;
+          const int nc = d.nc, mine = pair ? nc : (nc + 1 - i) >> 1, other = pair ? nc : (nc + i) >> 1;
           const uint64_t qa = q0 + (uint64_t)((pair ? i : qb) * (kMat >> 4));
           if (!pair) qb ^= 1;
           int st = base, ph = bph, no = it;   // the K chunk's stage, parity, number; its V chunk is the next
@@ -523,7 +542,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
           }
           // the last tile's accumulators have been read
           if (seg > 0) live = live && bar_wait(o_free, (seg & 1) ^ 1, &s_abort, c.status);
-          ++seg;
           for (int k = 0; k < mine && live; ++k) {
             int vs = st, vph = ph, ks = st, kph = ph;
             step(vs, vph, 1);
@@ -563,27 +581,74 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       }
       __syncwarp();
     } else {
-      // --------------------------------------------------------------- queries
-      // lane q of tile t is row 128 t + q of a pair, row q % per of a split tile
-      constexpr int kPc = HD / 8;
-      int free_par[2] = {1, 1}, qb = 0, seg = 0;
-      bool live = true;
-      while (live && next_segment(p.a, cutting(), s_e, s_end, u, ub1, s, g)) {
-        const Entry x = s_e[g.s];
-        const int left = (int)min((long long)x.n * grp - g.row0, (long long)kTile);
+      // ----------------------------------------------------- segments, queries
+      const long long U = s_end[p.a.rows.n_seq - 1];
+      // fewer blocks than launched where their shares would get too small
+      const int Gr = blocks_used(U, gridDim.x, kMinUnits), grp = c.n_head / c.n_head_kv;
+      const long long ub0 = U > 0 && b < Gr ? range_begin(U, Gr, b) : 0;
+      const long long ub1 = U > 0 && b < Gr ? range_begin(U, Gr, b + 1) : 0;
+      long long u = ub0;
+      int s = ub1 > ub0 ? find_entry(s_end, p.a.rows.n_seq, ub0) : 0, planned = 0;
+      bool more = true, live = true;
+      int free_par[2] = {1, 1}, qb = 0;
+      for (int seg = 0; live; ++seg) {
+        // three segments ahead, for the copies (a description's last reader is done
+        // when the Q of the fifth segment after it has been loaded)
+        while (more && planned < seg + 3) {
+          Segment g;
+          more = next_segment(p.a, cutting(), s_e, s_end, u, ub1, s, g);
+          if (!more) {
+            if (lane == 0) publish(&s_total, planned);
+            break;
+          }
+          const Entry x = s_e[g.s];
+          SegDesc& d = s_seg[planned % kSegs];
+          const int left = (int)min((long long)x.n * grp - g.row0, (long long)kTile);
+          if (lane == 0) {
+            d.x = x;
+            d.kvh = g.kvh;
+            d.row0 = g.row0;
+            d.left = left;
+            d.node0 = g.row0 / grp;
+            d.h0 = g.row0 - d.node0 * grp;
+            d.c0 = g.c0;
+            d.nc = g.c1 - g.c0;
+            d.whole = g.c0 == 0 && g.c1 == g.nch;
+            // partial rows: slot 0 of the block if its range starts in the tile, else 1
+            d.slot = 2 * b + (ub0 >= g.u0 ? 0 : 1);
+            // the block with a cut tile's first chunk describes it to the join
+            if (g.c0 == 0 && !d.whole)
+              p.cuts[b] = {x.lo, g.row0, g.kvh, left, block_of(U, Gr, g.u0 + (long long)(g.nch - 1) * g.w), d.slot};
+            publish(&s_planned, planned + 1);
+          }
+          __syncwarp();
+          ++planned;
+        }
+        if (seg >= planned) break;
+        // Q: lane q of tile t is row 128 t + q of a pair, row q % per of a split tile
+        const SegDesc& d = s_seg[seg % kSegs];
+        const int left = d.left;
         const bool pair = left > 128;
         const int per = left > 64 ? 128 : left > 32 ? 64 : 32;
+        constexpr int kPc = HD / 8, kStep = 32 / kPc;   // 16-byte pieces of a row, rows of a warp's copy
+        const int pc = lane & (kPc - 1);
+        const char* q_row = p.a.q + (size_t)d.x.lo * p.a.q_ld + (size_t)d.kvh * grp * HD * 2 + pc * 16;
         for (int t = 0; t < (pair ? 2 : 1); ++t) {
           const int area = pair ? t : qb;
           live = live && bar_wait(&q_free[area], free_par[area], &s_abort, c.status);
           free_par[area] ^= 1;
-          for (int e = lane; e < 128 * kPc; e += 32) {
-            const int q = e / kPc, pc = e & (kPc - 1), r = pair ? t * 128 + q : q & (per - 1);
-            const int node = min(g.row0 + r, x.n * grp - 1) / grp, h = g.kvh * grp + (g.row0 + r) % grp;
-            const char* src = p.a.q + (size_t)(x.lo + node) * p.a.q_ld + (size_t)h * HD * 2 + pc * 16;
-            const uint32_t dst = su32(sm + area * kMat + (pc >> 3) * kHalf + q * 128 + (((pc & 7) ^ (q & 7)) << 4));
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(r < left ? 16 : 0)
-                         : "memory");
+          uint8_t* dst0 = sm + area * kMat + (pc >> 3) * kHalf;
+#pragma unroll 2
+          for (int q = lane / kPc; q < per; q += kStep) {
+            const int r = pair ? t * 128 + q : q;
+            const bool real = r < left;
+            const int y = d.h0 + (real ? r : 0), nd = small_quotient(y, p.grp_magic), h = y - nd * grp;
+            const char* src = q_row + (size_t)(d.node0 + nd) * p.a.q_ld + h * HD * 2;
+            for (int z = q; z < 128; z += per)   // the row's copies
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                               su32(dst0 + z * 128 + (((pc & 7) ^ (z & 7)) << 4))),
+                           "l"(src), "r"(real ? 16 : 0)
+                           : "memory");
           }
         }
         if (!pair) qb ^= 1;
@@ -591,10 +656,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         fence_async();
         __syncwarp();
         if (lane == 0 && live) bar_arrive(&q_full[seg & 1]);
-        ++seg;
         __syncwarp();
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
     // ------------------------------------------------------------------ rows
@@ -603,33 +666,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // the warp's tensor-memory lanes: 32 (warp % 4) << 16
     const uint32_t tS = tmem + i * 128 + lanes, tO = tmem + 256 + i * HD + lanes;
     const float scale = p.a.scale * kLog2e;
-    int seg = 0, n_s = 0, qb = 0;
+    int n_s = 0, qb = 0, it = 0;
     bool live = true;   // after a wait that gave up: no more arrivals
-    while (next_segment(p.a, cutting(), s_e, s_end, u, ub1, s, g)) {
-      // the segment waits in shared memory: its registers are the weights'
-      const int left = (int)min((long long)s_e[g.s].n * grp - g.row0, (long long)kTile);
-      if (lane == 0) {
-        RowSeg& w = s_seg[warp];
-        w.x = s_e[g.s];
-        w.kvh = g.kvh;
-        w.row0 = g.row0;
-        w.whole = g.c0 == 0 && g.c1 == g.nch;
-        // partial rows: slot 0 of the block if its range starts in the tile, else 1
-        w.slot = 2 * b + (ub0 >= g.u0 ? 0 : 1);
-        w.left = left;
-        // the block with a cut tile's first chunk describes it to the join
-        if (tid == 0 && g.c0 == 0 && !w.whole)
-          p.cuts[b] = {w.x.lo, g.row0, g.kvh, left, block_of(U, Gr, g.u0 + (long long)(g.nch - 1) * g.w), w.slot};
-      }
-      __syncwarp();
+    for (int seg = 0;; ++seg) {
+      int there = 0;
+      if (lane == 0) there = seg_wait(&s_planned, &s_total, seg, &s_abort, c.status);
+      if (!__shfl_sync(0xffffffffu, there, 0)) break;
+      const SegDesc& d = s_seg[seg % kSegs];
+      const int left = d.left, nc = d.nc, ch0 = d.c0, s_len = d.x.len, end = s_len + d.x.n;
       const bool pair = left > 128;
       const int rep = left > 64 ? 1 : left > 32 ? 2 : 4, per = 128 / rep;   // copies of a row, rows
-      const int nc = g.c1 - g.c0, steps = pair ? 2 * nc : nc;
+      const int steps = pair ? 2 * nc : nc;
       const int row = pair ? i * 128 + pos : pos & (per - 1);
       const int col0 = pair ? 0 : pos / per * per;   // the copy's share of a chunk's slots: col0 .. col0 + per - 1
       const bool real = row < left;
-      const int node = real ? (g.row0 + row) / grp : 0, s_len = s_seg[warp].x.len, end = s_len + s_seg[warp].x.n;
-      const int ch0 = g.c0;
+      const int node = real ? d.node0 + small_quotient(d.h0 + row, p.grp_magic) : 0;
       const bool idle = !__any_sync(0xffffffffu, real);   // S and so P are zero, or of no row
       float m = 0.f, l = 0.f;
       // the stream is done with the tile's Q (a pair: its own area, which takes 8
@@ -641,9 +692,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       auto step = [&](auto nb, int slot0, bool part, bool later) {
         constexpr int NB = decltype(nb)::value;
         if (part)
-          softmax_step<NB, HD, true>(p.a, s_seg[warp].x, node, slot0, col0, tS, tO, scale, later, m, l);
+          softmax_step<NB, HD, true>(p.a, d.x, node, slot0, col0, tS, tO, scale, later, m, l);
         else
-          softmax_step<NB, HD, false>(p.a, s_seg[warp].x, node, slot0, col0, tS, tO, scale, later, m, l);
+          softmax_step<NB, HD, false>(p.a, d.x, node, slot0, col0, tS, tO, scale, later, m, l);
       };
       for (int k = i; k < steps; k += 2, ++n_s) {
         const int j = pair ? k >> 1 : k, slot0 = (ch0 + j) * kChunk;
@@ -680,16 +731,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
 
       // ---- the tile's end
       live = live && bar_wait(o_full, seg & 1, &s_abort, c.status);
-      ++seg;
       fence_after();
       if (l == 0.f) m = -CUDART_INF_F;   // nothing attended: no reference to others
-      const RowSeg w = s_seg[warp];
-      const bool whole = w.whole;
-      const int slot = w.slot;
+      const bool whole = d.whole;
+      const int slot = d.slot;
       auto out_row = [&](int r, char*& dst, float*& lse) {
-        const int nd = (w.row0 + r) / grp, h = w.kvh * grp + (w.row0 + r) - nd * grp;
-        dst = p.a.out + (size_t)(w.x.lo + nd) * p.a.out_ld + (size_t)h * HD * 2;
-        lse = p.a.lse ? p.a.lse + (size_t)(w.x.lo + nd) * c.n_head + h : nullptr;
+        const int y = d.h0 + r, nd = small_quotient(y, p.grp_magic), h = d.kvh * (c.n_head / c.n_head_kv) + y -
+                                                                       nd * (c.n_head / c.n_head_kv);
+        dst = p.a.out + (size_t)(d.x.lo + d.node0 + nd) * p.a.out_ld + (size_t)h * HD * 2;
+        lse = p.a.lse ? p.a.lse + (size_t)(d.x.lo + d.node0 + nd) * c.n_head + h : nullptr;
       };
       if (pair) {
         // 32 rows x 32 dims of a warp at a time through its own shared memory, so
@@ -738,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         // the 2 rep copies (stream, share of the slots) of a row joined through the
         // tile's Q area, as many of the dims at a time as it holds
         const int copies = 2 * rep, lines = copies * left;
-        const int D = lines * HD <= 8192 ? HD : lines * HD <= 16384 ? HD / 2 : 32;
+        const int D = lines * HD <= 8192 ? HD : lines * HD <= 16384 ? HD / 2 : 32, ql = __ffs(D) - 3;   // D / 4 = 2^ql
         float* buf = reinterpret_cast<float*>(sm + (p.scratch ? Lt::kOffScratch : qb * kMat));
         float2* ml = reinterpret_cast<float2*>(buf);           // [copies][per], before the buffer's first use
         const bool none = i >= steps;                          // a stream without a chunk
@@ -784,8 +834,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
                 }
             }
           sync_rows();
-          for (int e = tid; e < left * (D / 4); e += 256) {
-            const int r = e / (D / 4), q = e - r * (D / 4);
+          for (int e = tid; e < left << ql; e += 256) {
+            const int r = e >> ql, q = e - (r << ql);
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int y = 0; y < copies; ++y) {
               const int ln = y * left + r;
@@ -811,9 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       // O has been read (and the tile's Q area, if it was the end's memory, is free)
       fence_before();
       __syncwarp();
-      if (lane == 0 && live) {
-        bar_arrive(o_free);
-      }
+      if (lane == 0 && live) bar_arrive(o_free);
       if (!p.scratch || i >= steps) free_q();
       if (!pair) qb ^= 1;
     }
@@ -846,13 +894,14 @@ cudaError_t umma_as(const AttendParams& a, const AttendWork& w, cudaStream_t st)
   // pairs fill both Q areas; split tiles of 128 dims alternate between them and
   // are bound by memory, where the stage counts for more
   const bool pairs = (long long)a.max_tree * (a.c.n_head / a.c.n_head_kv) > kWide;
+  const uint32_t grp = a.c.n_head / a.c.n_head_kv;
+  p.grp_magic = grp > 1 ? (uint32_t)((0x100000000ull + grp - 1) / grp) : 0;
   p.scratch = pairs || HD == 64 ? kScratch : 0;
   const size_t fixed = fixed_smem<HD>(a.rows.n_seq) + p.scratch;
   p.stages = (int)((kSmemMost - fixed) / (Lt::kMat + 16));
   if (p.stages > Lt::kStagesMost) p.stages = Lt::kStagesMost;
   const size_t smem = fixed + (size_t)p.stages * (Lt::kMat + 16);
-  attend_umma_kernel<HD><<<w.sms, kThreads, smem, st>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_dependent(attend_umma_kernel<HD>, dim3(w.sms), kThreads, smem, st, p);
   if (e != cudaSuccess) return e;
   return launch_join<2, HD>(a, w, kTile, w.sms, st);
 }

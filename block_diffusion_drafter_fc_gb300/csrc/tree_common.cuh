@@ -259,6 +259,23 @@ DF_DEVICE int blocks_used(long long U, int launched, int least) {
 DF_DEVICE long long range_begin(long long U, int G, int b) { return quotient(U * b, G); }
 DF_DEVICE int block_of(long long U, int G, long long u) { return (int)quotient((u + 1) * G - 1, U); }
 
+// A launch that may start while the kernel before it ends (it waits for it with
+// griddepcontrol.wait before it touches global memory).
+template <typename K, typename... A>
+cudaError_t launch_dependent(K* kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ------------------------------------------------------------------ join
 
 // Rows of tiles cut by ranges: grid (blocks of the attention launch, up to 16
@@ -326,17 +343,8 @@ template <int EL, int HD>
 cudaError_t launch_join(const AttendParams& p, const AttendWork& w, int tile, int blocks, cudaStream_t st) {
   const long long rows = (long long)p.max_tree * (p.c.n_head / p.c.n_head_kv);
   const int most = rows < tile ? (int)rows : tile;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, most < 64 ? (most + 3) / 4 : 16);
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_join_kernel<EL, HD>, p, (const Cut*)w.cuts, (const float*)w.part_o,
-                            (const float2*)w.part_ml, tile);
+  return launch_dependent(attend_join_kernel<EL, HD>, dim3(blocks, most < 64 ? (most + 3) / 4 : 16), 128, 0, st, p,
+                          (const Cut*)w.cuts, (const float*)w.part_o, (const float2*)w.part_ml, tile);
 }
 
 }  // namespace tree
