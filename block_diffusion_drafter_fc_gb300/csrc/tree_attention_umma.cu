@@ -44,6 +44,7 @@
 // Every mbarrier wait gives up after ~2 s with DFLASH_DEV_TIMEOUT; the block then
 // issues nothing more, runs to its end without further waits or arrivals, and
 // releases its tensor memory.
+#include "internal.h"
 #include "tree_common.cuh"
 
 namespace dflash {
@@ -181,6 +182,8 @@ DF_DEVICE bool copy_there(int* issued, int pos, uint64_t* b, uint32_t par) {
 
 struct UmmaParams {
   CUtensorMap tm;     // pages as [rows of (page, layer, k|v, head)][page_size][hd], boxes of 64 dims
+  CUtensorMap tm_q;   // queries as [T][n_head][hd], boxes of 64 dims x a group's heads x nodes: 32 rows
+  int q_boxes;        // ... where groups divide 32 heads; else rows are copied piece by piece
   AttendParams a;
   float* part_o;      // [2 blocks][kTile][hd]
   float2* part_ml;    // [2 blocks][kTile]
@@ -213,6 +216,15 @@ DF_DEVICE uint32_t visible(const AttendParams& p, const Entry& x, int node, int 
   }
   if (valid < 32) v &= valid <= 0 ? 0u : (1u << valid) - 1u;
   return v;
+}
+
+// The mask words of the 128 slots from `slot` on, into L1 ahead of their use.
+DF_DEVICE void prefetch_mask(const AttendParams& p, const Entry& x, int node, int slot) {
+  const int k = max(slot - x.len, 0) >> 5;
+  if (k >= p.words) return;
+  const uint32_t* w = p.mask + (size_t)(x.lo + node) * p.words;
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(w + k));
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(w + min(k + 4, p.words - 1)));
 }
 
 // Two fp32 operations at a time.
@@ -630,34 +642,56 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         const int left = d.left;
         const bool pair = left > 128;
         const int per = left > 64 ? 128 : left > 32 ? 64 : 32;
-        constexpr int kPc = HD / 8, kStep = 32 / kPc;   // 16-byte pieces of a row, rows of a warp's copy
-        const int pc = lane & (kPc - 1);
-        const char* q_row = p.a.q + (size_t)d.x.lo * p.a.q_ld + (size_t)d.kvh * grp * HD * 2 + pc * 16;
-        for (int t = 0; t < (pair ? 2 : 1); ++t) {
-          const int area = pair ? t : qb;
+        for (int y = 0; y < (pair ? 2 : 1); ++y) {
+          const int area = pair ? y : qb;
           live = live && bar_wait(&q_free[area], free_par[area], &s_abort, c.status);
           free_par[area] ^= 1;
-          uint8_t* dst0 = sm + area * kMat + (pc >> 3) * kHalf;
-#pragma unroll 2
-          for (int q = lane / kPc; q < per; q += kStep) {
-            const int r = pair ? t * 128 + q : q;
-            const bool real = r < left;
-            const int y = d.h0 + (real ? r : 0), nd = small_quotient(y, p.grp_magic), h = y - nd * grp;
-            const char* src = q_row + (size_t)(d.node0 + nd) * p.a.q_ld + h * HD * 2;
-            for (int z = q; z < 128; z += per)   // the row's copies
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                               su32(dst0 + z * 128 + (((pc & 7) ^ (z & 7)) << 4))),
-                           "l"(src), "r"(real ? 16 : 0)
-                           : "memory");
+        }
+        if (!live) break;
+        if (p.q_boxes) {
+          // (groups of 32 rows that do not exist stay as they are: their lanes count
+          // for nothing)
+          const int groups = (pair ? (left + 31) >> 5 : (min(left, per) + 31) >> 5 << (per == 32 ? 2 : per == 64 ? 1 : 0));
+          if (lane == 0) {
+            bar_expect(&q_full[seg & 1], groups * 4096 * kHalves);
+            for (int z = 0; z < (pair ? 8 : 4); ++z) {
+              const int r = pair ? 32 * z : 32 * z & (per - 1);
+              if (r >= left) continue;
+              uint8_t* dst = sm + (pair ? z >> 2 : qb) * kMat + (z & 3) * 4096;
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h)
+                tma3d(dst + h * kHalf, &p.tm_q, h * 64, d.kvh * grp, d.x.lo + d.node0 + small_quotient(r, p.grp_magic),
+                      &q_full[seg & 1]);
+            }
           }
+        } else {
+          constexpr int kPc = HD / 8, kStep = 32 / kPc;   // 16-byte pieces of a row, rows of a warp's copy
+          const int pc = lane & (kPc - 1);
+          const char* q_row = p.a.q + (size_t)d.x.lo * p.a.q_ld + (size_t)d.kvh * grp * HD * 2 + pc * 16;
+          for (int y = 0; y < (pair ? 2 : 1); ++y) {
+            uint8_t* dst0 = sm + (pair ? y : qb) * kMat + (pc >> 3) * kHalf;
+#pragma unroll 2
+            for (int q = lane / kPc; q < per; q += kStep) {
+              const int r = pair ? y * 128 + q : q;
+              const bool real = r < left;
+              const int x = d.h0 + (real ? r : 0), nd = small_quotient(x, p.grp_magic), h = x - nd * grp;
+              const char* src = q_row + (size_t)(d.node0 + nd) * p.a.q_ld + h * HD * 2;
+              for (int z = q; z < 128; z += per)   // the row's copies
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 su32(dst0 + z * 128 + (((pc & 7) ^ (z & 7)) << 4))),
+                             "l"(src), "r"(real ? 16 : 0)
+                             : "memory");
+            }
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_async();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&q_full[seg & 1]);
         }
         if (!pair) qb ^= 1;
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_async();
-        __syncwarp();
-        if (lane == 0 && live) bar_arrive(&q_full[seg & 1]);
         __syncwarp();
       }
+      // (a Q that was loaded is a segment's that runs: no copy is in flight at the end)
     }
   } else {
     // ------------------------------------------------------------------ rows
@@ -698,11 +732,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       };
       for (int k = i; k < steps; k += 2, ++n_s) {
         const int j = pair ? k >> 1 : k, slot0 = (ch0 + j) * kChunk;
+        const bool part = slot0 + kChunk > s_len;   // nodes or slots past the last among them
+        if (part && real && p.a.mask) prefetch_mask(p.a, d.x, node, slot0 + col0);
         live = live && bar_wait(&s_full[i], n_s & 1, &s_abort, c.status);
         if (p.scratch && k + 2 >= steps) free_q();   // the stream's last scores
         fence_after();
         if (!idle) {
-          const bool part = slot0 + kChunk > s_len;   // nodes or slots past the last among them
           if (rep == 1)
             step(Int<4>(), slot0, part, k > 1);
           else if (rep == 2)
@@ -741,127 +776,133 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         dst = p.a.out + (size_t)(d.x.lo + d.node0 + nd) * p.a.out_ld + (size_t)h * HD * 2;
         lse = p.a.lse ? p.a.lse + (size_t)(d.x.lo + d.node0 + nd) * c.n_head + h : nullptr;
       };
-      if (pair) {
-        // 32 rows x 32 dims of a warp at a time through its own shared memory, so
-        // that rows are written as whole sectors by neighbouring lanes (16-byte
-        // pieces of a thread's own row took 10000 clocks a tile)
-        const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : 0.f;
-        char* dst = reinterpret_cast<char*>(p.part_o + ((size_t)slot * kTile + row) * HD);
-        if (real) {
-          if (whole) {
-            float* lse;
-            out_row(row, dst, lse);
-            if (lse) *lse = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
-          } else {
-            p.part_ml[(size_t)slot * kTile + row] = make_float2(m, l);
-          }
+      // Row weights of the accumulators.  A split tile's row lies in both streams'
+      // accumulators (the same tensor-memory lane, other columns) and, with copies,
+      // in 2 or 4 lanes of each; stream i's warps write half i of its dims.
+      float* area = reinterpret_cast<float*>(sm + (p.scratch ? Lt::kOffScratch : qb * kMat));   // 32 KB
+      float top = m, sum = l, wa = 1.f, wb = 0.f;
+      if (!pair) {
+        float2* ml = reinterpret_cast<float2*>(area);   // [stream][lane of the tile]
+        ml[tid] = i < steps ? make_float2(m, l) : make_float2(-CUDART_INF_F, 0.f);
+        sync_rows();
+        top = -CUDART_INF_F;
+        sum = 0.f;
+        for (int y = row; y < 256; y += per) top = fmaxf(top, ml[y].x);
+        const float use = top == -CUDART_INF_F ? 0.f : top;
+        for (int y = row; y < 256; y += per) sum += ex2(ml[y].x - use) * ml[y].y;
+        wa = ex2(ml[pos].x - use);
+        wb = ex2(ml[128 + pos].x - use);
+        sync_rows();   // the area is the accumulators' from here on
+      }
+      if (whole) {
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        wa *= inv;
+        wb *= inv;
+      }
+      char* dst = reinterpret_cast<char*>(p.part_o + ((size_t)slot * kTile + row) * HD);
+      if (real) {
+        float* lse;
+        if (whole) out_row(row, dst, lse);
+        if (pair || (i == 0 && pos < per)) {
+          if (!whole)
+            p.part_ml[(size_t)slot * kTile + row] = make_float2(top, sum);
+          else if (lse)
+            *lse = sum > 0.f ? (top + log2f(sum)) * kLn2 : -CUDART_INF_F;
         }
-        float* buf = reinterpret_cast<float*>(sm + Lt::kOffScratch) + warp * 1024;
-        const int last = left - (row - lane);   // rows of the warp that exist
+      }
+      // 32 weighted columns of this thread's row: column d of stream 0's (a pair: of
+      // the own) accumulator, and of stream 1's
+      const uint32_t tA = pair ? tO : tmem + 256 + lanes;
+      auto columns = [&](int d, float (&f)[32]) {
+        uint32_t v[32];
+        __syncwarp();
+        tmem_ld32(tA + d, v);
+        wait_ld(v);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]) * wa;
+        if (!pair && steps > 1) {   // (an accumulator that was never written may hold anything)
+          tmem_ld32(tA + HD + d, v);
+          wait_ld(v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) f[e] += __uint_as_float(v[e]) * wb;
+        }
+      };
+      if (rep == 1) {
+        // 32 rows x 32 dims of a warp at a time through its 4 KB of the area, so that
+        // rows are written as whole sectors by neighbouring lanes (16-byte pieces of a
+        // thread's own row took 10000 clocks a tile)
+        float* buf = area + warp * 1024;
+        const int last = left - (row - lane), d1 = pair ? HD : HD / 2;   // rows of the warp that exist; its dims
         if (!idle)
 #pragma unroll 1
-          for (int t = 0; t < HD / 32; ++t) {
-            uint32_t v[32];
-            __syncwarp();
-            tmem_ld32(tO + 32 * t, v);
-            wait_ld(v);
+          for (int d0 = 0; d0 < d1; d0 += 32) {
+            const int dim = (pair ? 0 : i * (HD / 2)) + d0;
+            float f[32];
+            columns(dim, f);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
               *reinterpret_cast<float4*>(buf + lane * 32 + ((q ^ (lane & 7)) << 2)) =
-                  make_float4(__uint_as_float(v[4 * q]) * inv, __uint_as_float(v[4 * q + 1]) * inv,
-                              __uint_as_float(v[4 * q + 2]) * inv, __uint_as_float(v[4 * q + 3]) * inv);
+                  make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
             __syncwarp();
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const int r = 4 * e + (lane >> 3), q = lane & 7;
-              const float4 f = *reinterpret_cast<const float4*>(buf + r * 32 + ((q ^ (r & 7)) << 2));
-              char* d = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, (unsigned long long)dst, r));
+              const float4 x = *reinterpret_cast<const float4*>(buf + r * 32 + ((q ^ (r & 7)) << 2));
+              char* to = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, (unsigned long long)dst, r));
               if (r >= last) continue;
               if (whole)
-                *reinterpret_cast<uint2*>(d + (32 * t + 4 * q) * 2) =
-                    make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+                *reinterpret_cast<uint2*>(to + (dim + 4 * q) * 2) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
               else
-                *reinterpret_cast<float4*>(d + (32 * t + 4 * q) * 4) = f;
+                *reinterpret_cast<float4*>(to + (dim + 4 * q) * 4) = x;
             }
           }
       } else {
-        // the 2 rep copies (stream, share of the slots) of a row joined through the
-        // tile's Q area, as many of the dims at a time as it holds
-        const int copies = 2 * rep, lines = copies * left;
-        const int D = lines * HD <= 8192 ? HD : lines * HD <= 16384 ? HD / 2 : 32, ql = __ffs(D) - 3;   // D / 4 = 2^ql
-        float* buf = reinterpret_cast<float*>(sm + (p.scratch ? Lt::kOffScratch : qb * kMat));
-        float2* ml = reinterpret_cast<float2*>(buf);           // [copies][per], before the buffer's first use
-        const bool none = i >= steps;                          // a stream without a chunk
-        const int cp = i * rep + pos / per;                    // the thread's copy of its row
-        ml[tid] = make_float2(none ? -CUDART_INF_F : m, none ? 0.f : l);
-        sync_rows();
-        float top = -CUDART_INF_F, sum = 0.f;
-        for (int y = 0; y < copies; ++y) top = fmaxf(top, ml[y * per + row].x);
-        const float use = top == -CUDART_INF_F ? 0.f : top;
-        for (int y = 0; y < copies; ++y) sum += ex2(ml[y * per + row].x - use) * ml[y * per + row].y;
-        // the row's result is a weighted sum of its copies
-        const float wgt = none ? 0.f : ex2(m - use) * (!whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f);
-        if (cp == 0 && real) {
-          if (!whole) {
-            p.part_ml[(size_t)slot * kTile + row] = make_float2(top, sum);
-          } else {
-            char* dst;
-            float* lse;
-            out_row(row, dst, lse);
-            if (lse) *lse = sum > 0.f ? (top + log2f(sum)) * kLn2 : -CUDART_INF_F;
-          }
-        }
-        const int line = cp * left + row;
-        sync_rows();
+        // the copies of a row summed through the area, in one or two passes over the dims
+        const int lines = rep * left, line = pos / per * left + row;
+        const int D = lines * HD <= 8192 ? HD : HD / 2, ql = __ffs(D) - 3;   // D / 4 = 2^ql
 #pragma unroll 1
-        for (int d0 = 0; d0 < HD; d0 += D) {
+        for (int p0 = 0; p0 < HD; p0 += D) {
           if (!idle)
 #pragma unroll 1
-            for (int d = 0; d < D; d += 32) {
-              uint32_t v[32];
-              __syncwarp();
-              tmem_ld32(tO + d0 + d, v);
-              wait_ld(v);
+            for (int d0 = i * (D / 2); d0 < (i + 1) * (D / 2); d0 += 32) {
+              float f[32];
+              columns(p0 + d0, f);
               if (real)
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                  float4 f;
-                  f.x = none ? 0.f : __uint_as_float(v[4 * q]) * wgt;
-                  f.y = none ? 0.f : __uint_as_float(v[4 * q + 1]) * wgt;
-                  f.z = none ? 0.f : __uint_as_float(v[4 * q + 2]) * wgt;
-                  f.w = none ? 0.f : __uint_as_float(v[4 * q + 3]) * wgt;
-                  *reinterpret_cast<float4*>(buf + line * D + d + ((q ^ (line & 7)) << 2)) = f;
-                }
+                for (int q = 0; q < 8; ++q)
+                  *reinterpret_cast<float4*>(area + line * D + d0 + ((q ^ (line & 7)) << 2)) =
+                      make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
             }
           sync_rows();
           for (int e = tid; e < left << ql; e += 256) {
             const int r = e >> ql, q = e - (r << ql);
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int y = 0; y < copies; ++y) {
-              const int ln = y * left + r;
-              const float4 f = *reinterpret_cast<const float4*>(buf + ln * D + (q & ~7) * 4 + (((q & 7) ^ (ln & 7)) << 2));
-              a.x += f.x;
-              a.y += f.y;
-              a.z += f.z;
-              a.w += f.w;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int y = r; y < lines; y += left) {
+              const float4 f = *reinterpret_cast<const float4*>(area + y * D + (q & ~7) * 4 + (((q & 7) ^ (y & 7)) << 2));
+              x.x += f.x;
+              x.y += f.y;
+              x.z += f.z;
+              x.w += f.w;
             }
-            const int dim = d0 + 4 * q;
+            const int dim = p0 + 4 * q;
             if (whole) {
-              char* dst;
+              char* to;
               float* lse;
-              out_row(r, dst, lse);
-              *reinterpret_cast<uint2*>(dst + dim * 2) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+              out_row(r, to, lse);
+              *reinterpret_cast<uint2*>(to + dim * 2) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
             } else {
-              *reinterpret_cast<float4*>(p.part_o + ((size_t)slot * kTile + r) * HD + dim) = a;
+              *reinterpret_cast<float4*>(p.part_o + ((size_t)slot * kTile + r) * HD + dim) = x;
             }
           }
-          sync_rows();
+          if (D < HD) sync_rows();
         }
       }
       // O has been read (and the tile's Q area, if it was the end's memory, is free)
       fence_before();
       __syncwarp();
       if (lane == 0 && live) bar_arrive(o_free);
+      if (!p.scratch) fence_async();   // the next Q comes by TMA
+      __syncwarp();
       if (!p.scratch || i >= steps) free_q();
       if (!pair) qb ^= 1;
     }
@@ -881,12 +922,27 @@ size_t fixed_smem(int n_seq) {   // without the ring
 }
 constexpr size_t kSmemMost = 227 * 1024 - 512;   // static shared memory aside
 
+// The call's queries as a 3-D tensor (made per call: it names the caller's buffer).
+bool q_map(CUtensorMap* m, const AttendParams& a, uint32_t grp) {
+  const EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)a.c.hd, (cuuint64_t)a.c.n_head, (cuuint64_t)a.rows.T};
+  const cuuint64_t strides[2] = {(cuuint64_t)a.c.hd * 2, (cuuint64_t)a.q_ld};
+  const cuuint32_t box[3] = {64, grp, 32 / grp}, estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<char*>(a.q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int HD>
 cudaError_t umma_as(const AttendParams& a, const AttendWork& w, cudaStream_t st) {
   using Lt = Lay<HD>;
   UmmaParams p;
   p.tm = *w.tm;
   p.a = a;
+  const uint32_t grp = a.c.n_head / a.c.n_head_kv;
+  p.q_boxes = 32 % grp == 0;
+  if (p.q_boxes && !q_map(&p.tm_q, a, grp)) return cudaErrorInvalidValue;
   p.part_o = w.part_o;
   p.part_ml = w.part_ml;
   p.cuts = w.cuts;
@@ -894,7 +950,6 @@ cudaError_t umma_as(const AttendParams& a, const AttendWork& w, cudaStream_t st)
   // pairs fill both Q areas; split tiles of 128 dims alternate between them and
   // are bound by memory, where the stage counts for more
   const bool pairs = (long long)a.max_tree * (a.c.n_head / a.c.n_head_kv) > kWide;
-  const uint32_t grp = a.c.n_head / a.c.n_head_kv;
   p.grp_magic = grp > 1 ? (uint32_t)((0x100000000ull + grp - 1) / grp) : 0;
   p.scratch = pairs || HD == 64 ? kScratch : 0;
   const size_t fixed = fixed_smem<HD>(a.rows.n_seq) + p.scratch;

@@ -116,11 +116,13 @@ struct Blocks {
     if (!step) return (long long)i * nch;
     if (step >= c.chunk)
       return (long long)i * quotient(first, c.chunk) + (long long)(step / c.chunk) * i * (i - 1) / 2;
-    // sum of floor((first + j step) / chunk) = sum of a + floor((r + j) / q)
-    const int q = c.chunk / step, a = (int)quotient(first, c.chunk), r = (int)(first - (long long)a * c.chunk) / step;
+    // sum of floor((first + j step) / chunk) = sum of a + floor((r + j) / 2^lq)
+    // (step is a power of two: it divides the tile)
+    const int ls = __ffs(step) - 1, lq = __ffs(c.chunk) - 1 - ls;
+    const int a = (int)quotient(first, c.chunk), r = (int)(first - (long long)a * c.chunk) >> ls;
     auto tri = [&](long long x) {
-      const long long t = quotient(x, q);
-      return q * (t * (t - 1) / 2) + t * (x - q * t);
+      const long long t = x >> lq;
+      return (t * (t - 1) / 2 << lq) + t * (x - (t << lq));
     };
     return (long long)i * a + tri(r + i) - tri(r);
   }
