@@ -9,18 +9,18 @@
 // 128-row tile takes 8 clocks a slot (QK^T and PV, 128 dims), the read of a
 // slot at an SM's share of the copy bandwidth 22.
 //
-// One persistent block per SM walks its range of the call's units (a unit: 128
-// slots of one tile of one kv head's query rows; tree_common.cuh), with two
-// streams of scores in flight so that one stream's softmax runs under the other
-// stream's products:
+// One persistent block per SM walks its range of the call's work (128-slot
+// chunks of the tiles of every kv head's query rows; tree_common.cuh) with two
+// streams of scores, each of two halves of 64 slots that take turns, so that
+// the products of one half run under the softmax of the other:
 //   tile of more than 128 rows (pair): stream i holds rows 128 i .. + 127, both
 //     use every chunk;
 //   tile of at most 128 rows (split): stream i takes every second chunk, with
-//     its own maximum, sum and accumulator, joined at the tile's end.  With at
-//     most 64 (32) rows, the rows are there 2 (4) times, in different lanes of
-//     the tile, and each copy of a row exponentiates its own half (quarter) of
-//     the chunk's slots, its weights for the others zero: the products cost the
-//     same, the exponentials of a chunk spread over all four warps.
+//     its own reference, sum and accumulator, joined at the tile's end.  With at
+//     most 64 rows, the rows are there twice, in different lanes of the tile, and
+//     each copy of a row exponentiates its own half of the slots, its weights for
+//     the others zero: the products cost the same, the exponentials spread over
+//     all four warps.
 // Roles:
 //   warps 0..3, 4..7  softmax of stream 0 and 1, a thread per row: S from tensor
 //                     memory (tcgen05.ld), reference m and sum l, weights
@@ -30,13 +30,14 @@
 //                     across tiles;
 //   warps 9, 10       (a lane each) tcgen05.mma of stream 0 and 1: S_i = Q_i K^T
 //                     (both in shared memory), O_i += P_i V (P in tensor memory,
-//                     V as it lies: MN-major).  Issuing waits for the pipe (60
-//                     clocks a product of 16), so one thread's barrier waits and
-//                     address arithmetic would leave it idle: one issuer per
-//                     stream, and their products (PV of a chunk, scores of the
-//                     next) in strict turns, so that one stream's softmax runs
-//                     under the other's products.
-// Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (head_dim each).
+//                     V as it lies: MN-major).  Issuing waits for the pipe (a
+//                     product of 16 dims or slots takes some 60 clocks), so an
+//                     issuer per stream: one's barriers are under the other's
+//                     products.
+// Tensor memory: S_0, S_1 (two halves of 64 columns each), O_0, O_1 (head_dim
+// each).  With whole chunks (128 columns, one buffer per stream) a stream's
+// scores, softmax and PV followed one another, and two streams left the tensor
+// pipe idle half of the time: 288 us instead of 271 for 2047 rows over 8192 slots.
 // The weights are rounded to bf16 for the product with V (their sum is not):
 // each is off by at most 2^-8 of itself, independently, which adds as much
 // again as the rounding of the result; splitting them as in the streaming
@@ -252,23 +253,22 @@ DF_DEVICE void hide(uint32_t (&v)[32], uint32_t see) {
     if (!(see & (1u << e))) v[e] = 0xff800000u;
 }
 
-// One row's share of a chunk: slots slot0 + col0 .. + 32 NB - 1 of the chunk at
+// One row's share of half a chunk: slots slot0 + col0 .. + 32 NB - 1 of the 64 at
 // slot0; scores from tensor memory, weights 2^(s - m) back over them (zeros for
-// the rest of the chunk's slots), l updated.
+// the rest of the 64), l updated.
 //
 // m need not be the maximum: any reference that keeps the weights within fp32
 // gives the same quotient, as weights, sums and products are all floating point
 // (bf16 has fp32's exponents).  m starts at 0, and moves to the largest score
-// (with the accumulator rescaled; its products are done, the scores' barrier
-// follows them) only when a chunk's weights sum to more than 2^60 or all weights
-// so far to less than 2^-60.  So the maximum - 64 three-way comparisons and a
-// pass over the scores before the first exponential - is not on the path of a
-// chunk: it took prompts of 2047 rows over 8192 slots from 348 to 326 us.
-// MASKED: the row may not see every slot.  `later`: the accumulator holds
-// something.
-template <int NB, int HD, bool MASKED>
+// (with the accumulator rescaled once its products are done: settle()) only when
+// 64 slots' weights sum to more than 2^60 or all weights so far to less than
+// 2^-60.  So the maximum - a pass over the scores before the first exponential -
+// is not on the path: it took prompts of 2047 rows over 8192 slots from 348 to
+// 326 us.  MASKED: the row may not see every slot.  `later`: the accumulator
+// holds something.
+template <int NB, int HD, bool MASKED, typename F>
 DF_DEVICE void softmax_step(const AttendParams& p, const Entry& x, int node, int slot0, int col0, uint32_t tS,
-                            uint32_t tO, float scale, bool later, float& m, float& l) {
+                            uint32_t tO, float scale, bool later, F settle, float& m, float& l) {
   uint32_t w[NB][16];
   float sum;
   for (bool again = false;; again = true) {
@@ -323,10 +323,11 @@ DF_DEVICE void softmax_step(const AttendParams& p, const Entry& x, int node, int
       for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(o[e]) * scale);
     }
     if (!bad || top == -CUDART_INF_F) top = m;   // nothing attended yet: any reference will do
-    const float fade = ex2(m - top);
+    const float fade = l > 0.f ? ex2(m - top) : 1.f;   // (an empty sum has no scale; m may fall by any amount)
     m = top;
     l *= fade;
     if (later && __any_sync(0xffffffffu, fade != 1.f)) {
+      settle();
 #pragma unroll 1
       for (int t = 0; t < HD / 32; ++t) {
         uint32_t o[32];
@@ -342,11 +343,9 @@ DF_DEVICE void softmax_step(const AttendParams& p, const Entry& x, int node, int
   l += sum;
 #pragma unroll
   for (int t = 0; t < NB; ++t) tmem_st16(tS + col0 / 2 + 16 * t, w[t]);
-  if (NB < 4) {   // the other copies' slots
+  if (NB == 1) {   // the other copy's slots
     const uint32_t z[16] = {};
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      if (t * 32 < col0 || t * 32 >= col0 + 32 * NB) tmem_st16(tS + 16 * t, z);
+    tmem_st16(tS + 16 - col0 / 2, z);
   }
   wait_st();
 }
@@ -391,9 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
   uint64_t* empty = full + S;
   uint64_t* q_full = empty + S;      // [2] the Q of an even (odd) segment is in shared memory
   uint64_t* q_free = q_full + 2;     // [2] Q area i is free
-  uint64_t* s_full = q_free + 2;     // [2] S_i computed (and the stream's products before it done)
-  uint64_t* p_full = s_full + 2;     // [2] P_i stored, and it is stream i's turn
-  uint64_t* o_full = p_full + 2;     // the segment's products are done
+  uint64_t* s_full = q_free + 2;     // [2][2] half h of S_i computed (and the stream's products before it done)
+  uint64_t* p_full = s_full + 4;     // [2][2] half h of P_i stored
+  uint64_t* pv_half = p_full + 4;    // [2] the first half of PV of a chunk of stream i is done
+  uint64_t* o_full = pv_half + 2;    // the segment's products are done
   uint64_t* o_free = o_full + 1;     // the segment's O has been read
   long long* s_warp = reinterpret_cast<long long*>(o_free + 1);   // [12]
   long long* s_end = s_warp + 12;
@@ -414,8 +414,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
     for (int i = 0; i < 2; ++i) {
       bar_init(&q_full[i], 1);
       bar_init(&q_free[i], 8);
-      bar_init(&s_full[i], 1);
-      bar_init(&p_full[i], 5);
+      bar_init(&pv_half[i], 1);
+      for (int h = 0; h < 2; ++h) {
+        bar_init(&s_full[2 * i + h], 1);
+        bar_init(&p_full[2 * i + h], 4);
+      }
     }
     bar_init(o_full, 2);
     bar_init(o_free, 8);
@@ -439,10 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
   fence_after();
   const uint32_t tmem = s_tmem;
 
-  // registers: the launch's 384 x 168 split into 256 x 208 (softmax: a row's
-  // scores of a chunk are held in registers) and 128 x 88
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kProducer) {
       // ---------------------------------------------------------------- copies
       const int none = c.n_pages * c.n_layer * 2 * c.n_head_kv;   // past the tensor: reads as zero
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         for (int seg = 0; live && seg_wait(&s_planned, &s_total, seg, &s_abort, c.status); ++seg) {
           const SegDesc& d = s_seg[seg % kSegs];
           const bool pair = d.left > 128;
-          const int nc = d.nc, mine = pair ? nc : (nc + 1 - i) >> 1, other = pair ? nc : (nc + i) >> 1;
+          const int nc = d.nc, mine = pair ? nc : (nc + 1 - i) >> 1;
           const uint64_t qa = q0 + (uint64_t)((pair ? i : qb) * (kMat >> 4));
           if (!pair) qb ^= 1;
           int st = base, ph = bph, no = it;   // the K chunk's stage, parity, number; its V chunk is the next
@@ -530,14 +530,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
             if (!pair) bar_arrive(&empty[pos]);
             commit(&empty[pos]);
           };
-          auto scores = [&]() {
-            const uint64_t kb = k0 + (uint64_t)(st * (kMat >> 4));
+          auto scores = [&](int h) {   // of the chunk's 64 slots h
+            const uint64_t kb = k0 + (uint64_t)(st * (kMat >> 4) + h * 512);
 #pragma unroll
             for (int e = 0; e < HD / 16; ++e) {
               const uint32_t off = ((e >> 2) * kHalf + (e & 3) * 32) >> 4;
-              mma_ss(dS, qa + off, kb + off, idesc(128, false), e > 0);
+              mma_ss(dS + 64 * h, qa + off, kb + off, idesc(64, false), e > 0);
             }
-            commit(&s_full[i]);
+            commit(&s_full[2 * i + h]);
           };
           if (!pair && i) {
             step(st, ph, 2);
@@ -548,39 +548,41 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
             live = copy_wait(&s_issued, no, &full[st], ph, &s_abort, c.status);
             if (!live) break;
             fence_after();
-            scores();
+            scores(0);
+            scores(1);
             release(st);
-            if (i == 0) bar_arrive(&p_full[0]);   // its first turn
           }
           // the last tile's accumulators have been read
           if (seg > 0) live = live && bar_wait(o_free, (seg & 1) ^ 1, &s_abort, c.status);
           for (int k = 0; k < mine && live; ++k) {
-            int vs = st, vph = ph, ks = st, kph = ph;
+            int vs = st, vph = ph;
             step(vs, vph, 1);
-            step(ks, kph, pair ? 2 : 4);
+            step(st, ph, pair ? 2 : 4);
             live = copy_wait(&s_issued, no + 1, &full[vs], vph, &s_abort, c.status);
             no += pair ? 2 : 4;
-            // with the next K chunk there, its scores follow PV in the same turn
-            const bool more = k + 1 < mine, ready = more && copy_there(&s_issued, no, &full[ks], kph);
-            live = live && bar_wait(&p_full[i], n_p, &s_abort, c.status);
-            if (!live) break;
-            n_p ^= 1;
-            fence_after();
+            // with the next K chunk there, its scores follow each half of PV
+            const bool more = k + 1 < mine, ready = more && copy_there(&s_issued, no, &full[st], ph);
             const uint64_t vb = v0 + (uint64_t)(vs * (kMat >> 4));
 #pragma unroll
-            for (int e = 0; e < kChunk / 16; ++e)   // 16 slots: 2 groups of 1024 bytes
-              mma_ts(dO, dS + 8 * e, vb + ((e * 2048) >> 4), idesc(HD, true), k > 0 || e > 0);
-            st = ks;
-            ph = kph;
-            if (ready) scores();
-            // the other stream's turn: round k after stream 0's, k + 1 after stream 1's
-            if (k + i < other) bar_arrive(&p_full[i ^ 1]);
+            for (int h = 0; h < 2; ++h) {
+              live = live && bar_wait(&p_full[2 * i + h], n_p, &s_abort, c.status);
+              if (!live) break;
+              fence_after();
+#pragma unroll
+              for (int e = 0; e < 4; ++e)   // 16 slots: 2 groups of 1024 bytes
+                mma_ts(dO, dS + 64 * h + 8 * e, vb + ((h * 8192 + e * 2048) >> 4), idesc(HD, true), k + h + e > 0);
+              if (ready) scores(h);
+              if (h == 0) commit(&pv_half[i]);
+            }
+            if (!live) break;
+            n_p ^= 1;
             release(vs);
             if (more && !ready) {
               live = copy_wait(&s_issued, no, &full[st], ph, &s_abort, c.status);
               if (!live) break;
               fence_after();
-              scores();
+              scores(0);
+              scores(1);
             }
             if (more) release(st);
           }
@@ -604,9 +606,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       bool more = true, live = true;
       int free_par[2] = {1, 1}, qb = 0;
       for (int seg = 0; live; ++seg) {
-        // three segments ahead, for the copies (a description's last reader is done
+        // (from the second on) three segments ahead, for the copies (a description's last reader is done
         // when the Q of the fifth segment after it has been loaded)
-        while (more && planned < seg + 3) {
+        while (more && planned < (seg ? seg + 3 : 1)) {
           Segment g;
           more = next_segment(p.a, cutting(), s_e, s_end, u, ub1, s, g);
           if (!more) {
@@ -641,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         const SegDesc& d = s_seg[seg % kSegs];
         const int left = d.left;
         const bool pair = left > 128;
-        const int per = left > 64 ? 128 : left > 32 ? 64 : 32;
+        const int per = left > 64 ? 128 : 64;
         for (int y = 0; y < (pair ? 2 : 1); ++y) {
           const int area = pair ? y : qb;
           live = live && bar_wait(&q_free[area], free_par[area], &s_abort, c.status);
@@ -651,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         if (p.q_boxes) {
           // (groups of 32 rows that do not exist stay as they are: their lanes count
           // for nothing)
-          const int groups = (pair ? (left + 31) >> 5 : (min(left, per) + 31) >> 5 << (per == 32 ? 2 : per == 64 ? 1 : 0));
+          const int groups = (pair ? (left + 31) >> 5 : (left + 31) >> 5 << (per == 64));
           if (lane == 0) {
             bar_expect(&q_full[seg & 1], groups * 4096 * kHalves);
             for (int z = 0; z < (pair ? 8 : 4); ++z) {
@@ -695,12 +697,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
     }
   } else {
     // ------------------------------------------------------------------ rows
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int i = warp >> 2, pos = tid & 127;     // stream, lane of the tile
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // the warp's tensor-memory lanes: 32 (warp % 4) << 16
     const uint32_t tS = tmem + i * 128 + lanes, tO = tmem + 256 + i * HD + lanes;
     const float scale = p.a.scale * kLog2e;
-    int n_s = 0, qb = 0, it = 0;
+    int n_s = 0, qb = 0, it = 0;   // the stream's chunks so far, Q area, copies so far
     bool live = true;   // after a wait that gave up: no more arrivals
     for (int seg = 0;; ++seg) {
       int there = 0;
@@ -709,10 +710,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       const SegDesc& d = s_seg[seg % kSegs];
       const int left = d.left, nc = d.nc, ch0 = d.c0, s_len = d.x.len, end = s_len + d.x.n;
       const bool pair = left > 128;
-      const int rep = left > 64 ? 1 : left > 32 ? 2 : 4, per = 128 / rep;   // copies of a row, rows
+      const int rep = left > 64 ? 1 : 2, per = 128 / rep;   // copies of a row, rows
       const int steps = pair ? 2 * nc : nc;
       const int row = pair ? i * 128 + pos : pos & (per - 1);
-      const int col0 = pair ? 0 : pos / per * per;   // the copy's share of a chunk's slots: col0 .. col0 + per - 1
+      const int col0 = rep == 2 ? pos >> 6 << 5 : 0;   // the copy's share of 64 slots: col0 .. col0 + 64 / rep - 1
       const bool real = row < left;
       const int node = real ? d.node0 + small_quotient(d.h0 + row, p.grp_magic) : 0;
       const bool idle = !__any_sync(0xffffffffu, real);   // S and so P are zero, or of no row
@@ -723,31 +724,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       auto free_q = [&]() {
         if (lane == 0 && live) bar_arrive_n(&q_free[pair ? i : qb], pair ? 2 : 1);
       };
-      auto step = [&](auto nb, int slot0, bool part, bool later) {
+      auto step = [&](auto nb, int h, int slot0, bool part, bool later) {
         constexpr int NB = decltype(nb)::value;
+        // the stream's products so far are done: those before a chunk precede the
+        // scores of its second half
+        auto settle = [&]() {
+          live = live && bar_wait(h ? &pv_half[i] : &s_full[2 * i + 1], n_s & 1, &s_abort, c.status);
+          fence_after();
+        };
         if (part)
-          softmax_step<NB, HD, true>(p.a, d.x, node, slot0, col0, tS, tO, scale, later, m, l);
+          softmax_step<NB, HD, true>(p.a, d.x, node, slot0, col0, tS + 64 * h, tO, scale, later, settle, m, l);
         else
-          softmax_step<NB, HD, false>(p.a, d.x, node, slot0, col0, tS, tO, scale, later, m, l);
+          softmax_step<NB, HD, false>(p.a, d.x, node, slot0, col0, tS + 64 * h, tO, scale, later, settle, m, l);
       };
       for (int k = i; k < steps; k += 2, ++n_s) {
         const int j = pair ? k >> 1 : k, slot0 = (ch0 + j) * kChunk;
-        const bool part = slot0 + kChunk > s_len;   // nodes or slots past the last among them
-        if (part && real && p.a.mask) prefetch_mask(p.a, d.x, node, slot0 + col0);
-        live = live && bar_wait(&s_full[i], n_s & 1, &s_abort, c.status);
-        if (p.scratch && k + 2 >= steps) free_q();   // the stream's last scores
-        fence_after();
-        if (!idle) {
-          if (rep == 1)
-            step(Int<4>(), slot0, part, k > 1);
-          else if (rep == 2)
-            step(Int<2>(), slot0, part, k > 1);
-          else
-            step(Int<1>(), slot0, part, k > 1);
-        }
+        const bool masked = slot0 + kChunk > s_len;   // nodes or slots past the last among them
+        if (masked && real && p.a.mask) prefetch_mask(p.a, d.x, node, slot0);
         if (slot0 + kChunk > end) {
           // slots past the last node may hold anything: 0 x NaN is NaN (of a pair,
-          // each stream clears them before its own product)
+          // each stream clears them before its own products)
           const int r = it + 2 * j + 1, st = r % S;
           live = live && copy_wait(&s_issued, r, &full[st], (uint32_t)((r / S) & 1), &s_abort, c.status);
           const int first = max(0, end - slot0);
@@ -758,9 +754,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
           }
           fence_async();
         }
-        fence_before();
-        __syncwarp();
-        if (lane == 0 && live) bar_arrive(&p_full[i]);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          live = live && bar_wait(&s_full[2 * i + h], n_s & 1, &s_abort, c.status);
+          if (p.scratch && h && k + 2 >= steps) free_q();   // the stream's last scores
+          fence_after();
+          if (!idle) {
+            const int slot = slot0 + 64 * h;
+            if (rep == 1)
+              step(Int<2>(), h, slot, slot + 64 > s_len, k > 1 || h);
+            else
+              step(Int<1>(), h, slot, slot + 64 > s_len, k > 1 || h);
+          }
+          fence_before();
+          __syncwarp();
+          if (lane == 0 && live) bar_arrive(&p_full[2 * i + h]);
+        }
       }
       it += 2 * nc;
 
@@ -918,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
 
 template <int HD>
 size_t fixed_smem(int n_seq) {   // without the ring
-  return 1024 + Lay<HD>::kOffScratch + 10 * 8 + 12 * 8 + (size_t)n_seq * (sizeof(long long) + sizeof(Entry));
+  return 1024 + Lay<HD>::kOffScratch + 16 * 8 + 12 * 8 + (size_t)n_seq * (sizeof(long long) + sizeof(Entry));
 }
 constexpr size_t kSmemMost = 227 * 1024 - 512;   // static shared memory aside
 

@@ -537,7 +537,7 @@ def test_append_faults_write_nothing_else():
 # ------------------------------------------------------------------ attention
 
 def attend_case(c, rng, g, seqs, lens, counts, mask_kind, dtype, max_tree=None, tail=2, with_lse=True, layer=0,
-                q_scale=1.0, poison=True):
+                q_scale=1.0, poison=True, ramp=0.0):
     cfg = c.cfg
     ps, hd, hq = cfg.page_size, cfg.head_dim, cfg.n_head
     scattered(c, rng, seqs, lens, counts, fill=float("nan") if poison else None)
@@ -561,6 +561,9 @@ def attend_case(c, rng, g, seqs, lens, counts, mask_kind, dtype, max_tree=None, 
             mask[r:r + cnt] = R.words_of(m, words)
         sets.append(m)
         data = normal(g, (2, n + cnt, cfg.n_head_kv, hd), dtype)
+        if ramp:      # keys that grow (ramp > 0) or shrink along the sequence
+            p = torch.arange(n + cnt, dtype=torch.float32)
+            data[0] = (data[0].float() * (1 + abs(ramp) * (p if ramp > 0 else n + cnt - p))[:, None, None]).to(DT[dtype])
         kv.append(np64(data))
         for i in range(-(-(n + cnt) // ps)):
             part = data[:, i * ps:(i + 1) * ps].transpose(1, 2).cuda()
@@ -632,6 +635,20 @@ def test_attend_large_scores(dtype):
     attend_case(c, rng, g, [0, 1], [300, 40], [20, 3], "tree", dtype, q_scale=16.0)
     c = make(n_head=2, n_head_kv=1, head_dim=64, page_size=16, n_pages=100, max_seq=2, max_pages=60, dtype=dtype, attn_scale=2.0 ** -20)
     attend_case(c, rng, g, [0, 1], [300, 40], [20, 3], "tree", dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("ramp", [0.1, -0.1])
+def test_attend_scores_that_grow_along_the_sequence(dtype, hd, ramp):
+    """The largest score moves by hundreds from chunk to chunk, up or down: the weights'
+    reference has to follow, with what was summed before it."""
+    rng = np.random.default_rng(hd)
+    g = torch.Generator().manual_seed(hd)
+    c = make(n_head=8, n_head_kv=2, head_dim=hd, page_size=64, n_pages=100, max_seq=4, max_pages=60, dtype=dtype)
+    attend_case(c, rng, g, [0, 1, 2], [1500, 40, 700], [20, 3, 70], "tree", dtype, ramp=ramp)
+    attend_case(c, rng, g, [3], [0], [300], "chain", dtype, ramp=ramp)
+    attend_case(c, rng, g, [1, 0], [900, 2000], [1, 9], "tree", dtype, ramp=ramp)
 
 
 def test_attend_faults():
