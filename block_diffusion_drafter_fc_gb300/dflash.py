@@ -424,6 +424,7 @@ class PagedCache:
                                        Drafter._aligned(self.scratch), C.byref(h)),
                what="cache_create")
         self.h = h.value
+        self.device_index = self.page_mem.device.index
         self.dtype = torch.bfloat16 if cfg.dtype == "bf16" else torch.float32
 
         def view(mem, off, shape, dt):
@@ -458,117 +459,133 @@ class PagedCache:
             msg = LIB.dflash_status_string(rc).decode() + (f" ({extra})" if extra else "")
             raise DFlashError(f"{what}: {msg} [{rc}]")
 
-    def _rows(self, t: torch.Tensor, what: str, heads: Optional[int] = None) -> int:
-        """Row stride of a [T][heads][head_dim] operand."""
-        if t.dtype != self.dtype or t.dim() != 3 or t.shape[2] != self.cfg.head_dim or (
-                heads is not None and t.shape[1] != heads):
-            raise DFlashError(f"{what}: {tuple(t.shape)} {t.dtype} is not [T][{heads or 'heads'}]"
-                              f"[{self.cfg.head_dim}] {self.dtype}")
-        if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+    def _rows(self, t: torch.Tensor, what: str, heads: Optional[int] = None):
+        """(rows, row stride) of a [T][heads][head_dim] operand."""
+        shape, stride = t.shape, t.stride()
+        hd = self.cfg.head_dim
+        if t.dtype is not self.dtype or len(shape) != 3 or shape[2] != hd or (
+                heads is not None and shape[1] != heads):
+            raise DFlashError(f"{what}: {tuple(shape)} {t.dtype} is not [T][{heads or 'heads'}]"
+                              f"[{hd}] {self.dtype}")
+        if shape[0] and (stride[2] != 1 or (stride[1] != hd and shape[1] > 1)):
             raise DFlashError(f"{what}: a row's heads have to be contiguous")
-        return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+        return shape[0], stride[0] if shape[0] > 1 else shape[1] * hd
 
     @staticmethod
-    def _ints(what: str, *ts) -> None:
-        for t, n in ts:
-            if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n):
-                raise DFlashError(f"{what}: index arrays are contiguous int32 of the call's size")
+    def _int(what: str, t, n: int) -> int:
+        """Address of a contiguous int32 tensor of at least n values (None: null)."""
+        if t is None:
+            return 0
+        if t.dtype is not torch.int32 or not t.is_contiguous() or t.numel() < n:
+            raise DFlashError(f"{what}: index arrays are contiguous int32 of the call's size")
+        return t.data_ptr()
+
+    def _on(self, stream) -> int:
+        """The stream's handle (None: torch's current one of the cache's device)."""
+        if stream is not None:
+            return stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.device_index)
 
     # ---- C-ABI calls (same names)
     def dflash_rope(self, x, pos, out, backward: bool = False, stream=None):
-        xs, os_ = self._rows(x, "rope"), self._rows(out, "rope", x.shape[1])
-        if out.shape[0] != x.shape[0]:
+        T, xs = self._rows(x, "rope")
+        n = x.shape[1]
+        rows, os_ = self._rows(out, "rope", n)
+        if rows != T:
             raise DFlashError("rope: x and out have different rows")
-        self._ints("rope", (pos, x.shape[0]))
-        self._ok(LIB.dflash_rope(self.h, x.shape[0], x.shape[1], x.data_ptr(), xs, pos.data_ptr(),
-                                 out.data_ptr(), os_, int(backward), _stream(stream)), "rope")
+        self._ok(LIB.dflash_rope(self.h, T, n, x.data_ptr(), xs, self._int("rope", pos, T), out.data_ptr(), os_,
+                                 backward, self._on(stream)), "rope")
 
     def dflash_cache_append(self, layer: int, row_start, k, v, depth=None, q=None, q_out=None,
                             seqs=None, stream=None):
-        cfg, T, n = self.cfg, k.shape[0], row_start.shape[0] - 1
-        ks, vs = self._rows(k, "append", cfg.n_head_kv), self._rows(v, "append", cfg.n_head_kv)
-        qs = qos = 0
+        cfg, n = self.cfg, row_start.shape[0] - 1
+        T, ks = self._rows(k, "append", cfg.n_head_kv)
+        rows, vs = self._rows(v, "append", cfg.n_head_kv)
+        qs = qos = qp = qop = 0
         if (q is None) != (q_out is None):
             raise DFlashError("append: q and q_out go together")
+        same = rows == T
         if q is not None:
-            qs, qos = self._rows(q, "append", cfg.n_head), self._rows(q_out, "append", cfg.n_head)
-        if v.shape[0] != T or (q is not None and (q.shape[0] != T or q_out.shape[0] != T)):
+            rows, qs = self._rows(q, "append", cfg.n_head)
+            rows_out, qos = self._rows(q_out, "append", cfg.n_head)
+            same = same and rows == T and rows_out == T
+            qp, qop = q.data_ptr(), q_out.data_ptr()
+        if not same:
             raise DFlashError("append: operands have different rows")
-        self._ints("append", (row_start, 1), (depth, T), (seqs, n))
         self._ok(LIB.dflash_cache_append(
-            self.h, layer, n, _ptr(seqs), row_start.data_ptr(), T, _ptr(depth), _ptr(q), qs,
-            _ptr(q_out), qos, k.data_ptr(), ks, v.data_ptr(), vs, _stream(stream)), "append")
+            self.h, layer, n, self._int("append", seqs, n), self._int("append", row_start, 1), T,
+            self._int("append", depth, T), qp, qs, qop, qos, k.data_ptr(), ks, v.data_ptr(), vs,
+            self._on(stream)), "append")
 
     def dflash_tree_mask(self, row_start, parents, mask, depth=None, stream=None):
-        n, T = row_start.shape[0] - 1, parents.shape[0]
-        self._ints("tree_mask", (row_start, 1), (parents, T), (mask, T), (depth, T))
-        if mask.dim() != 2 or mask.shape[0] != T:
+        T, shape = parents.shape[0], mask.shape
+        if len(shape) != 2 or shape[0] != T:
             raise DFlashError("tree_mask: mask is int32 [T][words]")
-        self._ok(LIB.dflash_tree_mask(self.h, n, row_start.data_ptr(), T, parents.data_ptr(),
-                                      mask.data_ptr(), mask.shape[1], _ptr(depth), _stream(stream)),
-                 "tree_mask")
+        i = self._int
+        self._ok(LIB.dflash_tree_mask(
+            self.h, row_start.shape[0] - 1, i("tree_mask", row_start, 1), T, i("tree_mask", parents, T),
+            i("tree_mask", mask, T), shape[1], i("tree_mask", depth, T), self._on(stream)), "tree_mask")
 
     def dflash_tree_attend(self, layer: int, row_start, max_tree: int, q, out, mask=None, lse=None,
                            seqs=None, stream=None):
-        cfg, T, n = self.cfg, q.shape[0], row_start.shape[0] - 1
-        qs, os_ = self._rows(q, "tree_attend", cfg.n_head), self._rows(out, "tree_attend", cfg.n_head)
-        self._ints("tree_attend", (row_start, 1), (seqs, n))
-        words = 0
+        hq, n = self.cfg.n_head, row_start.shape[0] - 1
+        T, qs = self._rows(q, "tree_attend", hq)
+        rows, os_ = self._rows(out, "tree_attend", hq)
+        words = lp = 0
         if mask is not None:
             if mask.dim() != 2 or mask.shape[0] != T:
                 raise DFlashError("tree_attend: mask is int32 [T][words]")
-            self._ints("tree_attend", (mask, 0))
             words = mask.shape[1]
-        if out.shape[0] != T or (lse is not None and (
-                lse.dtype != torch.float32 or not lse.is_contiguous() or lse.numel() != T * cfg.n_head)):
-            raise DFlashError("tree_attend: out has q's rows, lse is contiguous f32 [T][n_head]")
+        if rows != T:
+            raise DFlashError("tree_attend: q and out have different rows")
+        if lse is not None:
+            if lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() != T * hq:
+                raise DFlashError("tree_attend: lse is contiguous f32 [T][n_head]")
+            lp = lse.data_ptr()
+        i = self._int
         self._ok(LIB.dflash_tree_attend(
-            self.h, layer, n, _ptr(seqs), row_start.data_ptr(), T, max_tree, _ptr(mask), words,
-            q.data_ptr(), qs, out.data_ptr(), os_, _ptr(lse), _stream(stream)), "tree_attend")
+            self.h, layer, n, i("tree_attend", seqs, n), i("tree_attend", row_start, 1), T, max_tree,
+            i("tree_attend", mask, 0), words, q.data_ptr(), qs, out.data_ptr(), os_, lp, self._on(stream)),
+            "tree_attend")
 
     def dflash_tree_accept(self, row_start, parents, tokens, targets, path, n_path, id_last,
                            stream=None):
-        n, T = row_start.shape[0] - 1, parents.shape[0]
-        self._ints("tree_accept", (row_start, 1), (parents, T), (tokens, T), (targets, T),
-                   (path, 0), (n_path, n), (id_last, n))
-        if path.dim() != 2 or path.shape[0] != n:
+        n, T, shape, i = row_start.shape[0] - 1, parents.shape[0], path.shape, self._int
+        if len(shape) != 2 or shape[0] != n:
             raise DFlashError("tree_accept: path is int32 [n_seq][max_path]")
         self._ok(LIB.dflash_tree_accept(
-            self.h, n, row_start.data_ptr(), T, parents.data_ptr(), tokens.data_ptr(),
-            targets.data_ptr(), path.data_ptr(), path.shape[1], n_path.data_ptr(),
-            id_last.data_ptr(), _stream(stream)), "tree_accept")
+            self.h, n, i("tree_accept", row_start, 1), T, i("tree_accept", parents, T),
+            i("tree_accept", tokens, T), i("tree_accept", targets, T), i("tree_accept", path, 0), shape[1],
+            i("tree_accept", n_path, n), i("tree_accept", id_last, n), self._on(stream)), "tree_accept")
 
     def dflash_cache_commit(self, path, n_path, seqs=None, stream=None):
         """path int32 [n_seq][max_path], or None: the first n_path nodes stay in place."""
-        n = n_path.shape[0]
-        if path is not None and (path.dim() != 2 or path.shape[0] != n):
-            raise DFlashError("commit: path is int32 [n_seq][max_path]")
-        self._ints("commit", (path, 0), (n_path, n), (seqs, n))
-        self._ok(LIB.dflash_cache_commit(self.h, n, _ptr(seqs), _ptr(path),
-                                         0 if path is None else path.shape[1], n_path.data_ptr(),
-                                         _stream(stream)), "commit")
+        n, i, most = n_path.shape[0], self._int, 0
+        if path is not None:
+            if path.dim() != 2 or path.shape[0] != n:
+                raise DFlashError("commit: path is int32 [n_seq][max_path]")
+            most = path.shape[1]
+        self._ok(LIB.dflash_cache_commit(self.h, n, i("commit", seqs, n), i("commit", path, 0), most,
+                                         i("commit", n_path, n), self._on(stream)), "commit")
 
     def dflash_cache_reserve(self, count, seqs=None, stream=None):
-        n = count.shape[0]
-        self._ints("reserve", (count, n), (seqs, n))
-        self._ok(LIB.dflash_cache_reserve(self.h, n, _ptr(seqs), count.data_ptr(), _stream(stream)),
-                 "reserve")
+        n, i = count.shape[0], self._int
+        self._ok(LIB.dflash_cache_reserve(self.h, n, i("reserve", seqs, n), i("reserve", count, n),
+                                          self._on(stream)), "reserve")
 
     def dflash_cache_fork(self, src, dst, stream=None):
-        n = src.shape[0]
-        self._ints("fork", (src, n), (dst, n))
-        self._ok(LIB.dflash_cache_fork(self.h, n, src.data_ptr(), dst.data_ptr(), _stream(stream)),
+        n, i = src.shape[0], self._int
+        self._ok(LIB.dflash_cache_fork(self.h, n, i("fork", src, n), i("fork", dst, n), self._on(stream)),
                  "fork")
 
     def dflash_cache_trim(self, new_len, seqs=None, stream=None):
-        n = new_len.shape[0]
-        self._ints("trim", (new_len, n), (seqs, n))
-        self._ok(LIB.dflash_cache_trim(self.h, n, _ptr(seqs), new_len.data_ptr(), _stream(stream)),
-                 "trim")
+        n, i = new_len.shape[0], self._int
+        self._ok(LIB.dflash_cache_trim(self.h, n, i("trim", seqs, n), i("trim", new_len, n),
+                                       self._on(stream)), "trim")
 
     def dflash_cache_read_status(self, stream=None) -> int:
         v = C.c_uint32()
-        rc = LIB.dflash_cache_read_status(self.h, C.byref(v), _stream(stream))
+        rc = LIB.dflash_cache_read_status(self.h, C.byref(v), self._on(stream))
         if rc not in (0, -7):
             self._ok(rc, "cache_read_status")
         return v.value
