@@ -22,6 +22,8 @@ namespace {
 // pointer read in this round skips.
 __global__ void tree_mask_kernel(RowView rows, const int32_t* parents, uint32_t* mask, int words,
                                  int32_t* depth, unsigned* status) {
+  pdl_trigger();
+  pdl_wait();
   extern __shared__ uint32_t sm[];
   const int s = blockIdx.x;
   int lo, n;
@@ -84,6 +86,8 @@ __global__ void tree_mask_kernel(RowView rows, const int32_t* parents, uint32_t*
 __global__ void tree_accept_kernel(RowView rows, const int32_t* parents, const int32_t* tokens,
                                    const int32_t* targets, int32_t* path, int max_path, int32_t* n_path,
                                    int32_t* id_last, unsigned* status) {
+  pdl_trigger();
+  pdl_wait();
   extern __shared__ int next[];   // [kTreeMax], longer trees walk in pieces below
   __shared__ int s_len, s_cur;
   const int s = blockIdx.x;
@@ -144,6 +148,8 @@ constexpr int kBatch = 8;   // tokens in flight per thread
 // one.
 __global__ void __launch_bounds__(256) commit_kernel(CacheView c, RowView rows, const int32_t* path,
                                                      int max_path, const int32_t* n_path, int* tickets) {
+  pdl_trigger();
+  pdl_wait();
   extern __shared__ long long s_off[];   // [max_path] from, [max_path] to
   const int s = blockIdx.y;
   const int q = entry_sequence(rows, s, c.max_seq);
@@ -256,6 +262,8 @@ DF_DEVICE int block_scan(int v, int* s_warp, int& total) {
 // changed before the totals are known.
 __global__ void __launch_bounds__(kPlan) reserve_plan_kernel(CacheView c, RowView rows, const int32_t* count,
                                                              int32_t* free_list, int4* copies) {
+  pdl_trigger();
+  pdl_wait();
   __shared__ int s_warp[32];
   __shared__ int s_owner[4096];
   __shared__ int s_first[kCallSeq], s_end[kCallSeq], s_seq[kCallSeq], s_old[kCallSeq];
@@ -380,6 +388,7 @@ __global__ void __launch_bounds__(kPlan) reserve_plan_kernel(CacheView c, RowVie
 // grid (blocks, entries): the slots an entry keeps of its part-filled page, for
 // every (layer, k|v, head) a contiguous run.
 __global__ void __launch_bounds__(256) reserve_copy_kernel(CacheView c, const int4* copies) {
+  pdl_trigger();
   pdl_wait();
   const int4 w = copies[blockIdx.y];
   if (w.z <= 0) return;
@@ -411,6 +420,8 @@ __global__ void __launch_bounds__(256) reserve_copy_kernel(CacheView c, const in
 
 // One block per entry.
 __global__ void __launch_bounds__(256) fork_kernel(CacheView c, int n, const int32_t* src, const int32_t* dst) {
+  pdl_trigger();
+  pdl_wait();
   const int i = blockIdx.x, a = src[i], b = dst[i];
   int bad = a < 0 || a >= c.max_seq || b < 0 || b >= c.max_seq;
   for (int j = threadIdx.x; j < n; j += blockDim.x) bad |= src[j] == b || (j < i && dst[j] == b);
@@ -437,6 +448,8 @@ __global__ void __launch_bounds__(256) fork_kernel(CacheView c, int n, const int
 
 // grid (blocks, entries): table entries from the first page that is not kept.
 __global__ void __launch_bounds__(256) trim_kernel(CacheView c, RowView rows, const int32_t* new_len) {
+  pdl_trigger();
+  pdl_wait();
   const int s = blockIdx.y;
   const int q = entry_sequence(rows, s, c.max_seq);
   const bool dup = listed_before(rows, s, q);
@@ -471,16 +484,15 @@ cudaError_t configure_tree() {
 
 cudaError_t launch_tree_mask(const RowView& rows, const int32_t* parents, uint32_t* mask, int words,
                              int32_t* depth, unsigned* status, cudaStream_t st) {
-  tree_mask_kernel<<<rows.n_seq, 128, mask_smem(words), st>>>(rows, parents, mask, words, depth, status);
-  return cudaGetLastError();
+  return launch_dependent(tree_mask_kernel, dim3(rows.n_seq), 128, mask_smem(words), st, rows, parents, mask, words,
+                          depth, status);
 }
 
 cudaError_t launch_tree_accept(const RowView& rows, const int32_t* parents, const int32_t* tokens,
                                const int32_t* targets, int32_t* path, int max_path, int32_t* n_path,
                                int32_t* id_last, unsigned* status, cudaStream_t st) {
-  tree_accept_kernel<<<rows.n_seq, 128, sizeof(int) * kTreeMax, st>>>(rows, parents, tokens, targets, path,
-                                                                      max_path, n_path, id_last, status);
-  return cudaGetLastError();
+  return launch_dependent(tree_accept_kernel, dim3(rows.n_seq), 128, sizeof(int) * kTreeMax, st, rows, parents, tokens,
+                          targets, path, max_path, n_path, id_last, status);
 }
 
 cudaError_t launch_commit(const CacheView& c, const RowView& rows, const int32_t* path, int max_path,
@@ -492,31 +504,27 @@ cudaError_t launch_commit(const CacheView& c, const RowView& rows, const int32_t
     const long long want = (cols + 255) / 256;
     gx = (int)(want < most ? want : most);
   }
-  commit_kernel<<<dim3(gx, rows.n_seq), 256, path ? sizeof(long long) * 2 * max_path : 0, st>>>(
-      c, rows, path, max_path, n_path, tickets);
-  return cudaGetLastError();
+  return launch_dependent(commit_kernel, dim3(gx, rows.n_seq), 256, path ? sizeof(long long) * 2 * max_path : 0, st, c,
+                          rows, path, max_path, n_path, tickets);
 }
 
 cudaError_t launch_reserve(const CacheView& c, const RowView& rows, const int32_t* count,
                            int32_t* free_list, int4* copies, cudaStream_t st) {
-  reserve_plan_kernel<<<1, kPlan, 0, st>>>(c, rows, count, free_list, copies);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_dependent(reserve_plan_kernel, dim3(1), kPlan, 0, st, c, rows, count, free_list, copies);
   if (e != cudaSuccess) return e;
   const long long vecs = (long long)c.n_layer * 2 * c.n_head_kv * c.ps * c.hd * c.el / 16;
   const long long most = (4LL * 152 * 8 + rows.n_seq - 1) / rows.n_seq, want = (vecs + 1023) / 1024;
-  reserve_copy_kernel<<<dim3((int)(want < most ? want : most), rows.n_seq), 256, 0, st>>>(c, copies);
-  return cudaGetLastError();
+  return launch_dependent(reserve_copy_kernel, dim3((int)(want < most ? want : most), rows.n_seq), 256, 0, st, c,
+                          (const int4*)copies);
 }
 
 cudaError_t launch_fork(const CacheView& c, int n, const int32_t* src, const int32_t* dst, cudaStream_t st) {
-  fork_kernel<<<n, 256, 0, st>>>(c, n, src, dst);
-  return cudaGetLastError();
+  return launch_dependent(fork_kernel, dim3(n), 256, 0, st, c, n, src, dst);
 }
 
 cudaError_t launch_trim(const CacheView& c, const RowView& rows, const int32_t* new_len, cudaStream_t st) {
   const int gx = (c.max_pages + 1023) / 1024;   // four entries a thread
-  trim_kernel<<<dim3(gx < 64 ? gx : 64, rows.n_seq), 256, 0, st>>>(c, rows, new_len);
-  return cudaGetLastError();
+  return launch_dependent(trim_kernel, dim3(gx < 64 ? gx : 64, rows.n_seq), 256, 0, st, c, rows, new_len);
 }
 
 }  // namespace dflash

@@ -36,4 +36,29 @@ DF_DEVICE bool listed_before(const RowView& r, int s, int q) {
   return __syncthreads_or(dup) != 0;
 }
 
+// y / d of y < 2^32 / d, magic = ceil(2^32 / d) (0: d = 1)
+DF_DEVICE int small_quotient(int y, uint32_t magic) { return magic ? (int)__umulhi((uint32_t)y, magic) : y; }
+inline uint32_t quotient_magic(uint32_t d) {
+  return d > 1 ? (uint32_t)((0x100000000ull + d - 1) / d) : 0;
+}
+
+// A launch that may start while the kernel before it ends: every kernel here lets
+// the next one be scheduled at once and waits for the one before it with
+// griddepcontrol.wait before it touches global memory (a turn's small calls then
+// cost no launch gaps).
+template <typename K, typename... A>
+cudaError_t launch_dependent(K* kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace dflash

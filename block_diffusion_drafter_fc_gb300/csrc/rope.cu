@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxRows = 32;   // rows of one block
+constexpr int kAppendRows = 16;
 
 template <int VB>
 struct Vec;
@@ -120,6 +121,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p, int rows_p
   constexpr int E = VB / EL;
   extern __shared__ float2 cs[];   // [rows][rd / 2]
   __shared__ int s_pos[kMaxRows];
+  pdl_trigger();
+  pdl_wait();
   const int ipr = p.hd / (2 * E), items = p.n_heads * ipr, half = p.r.rd / 2;
   const Span sp = block_span(p.T, rows_per_block, items, U * kThreads);
   const int width = sp.it1 - sp.it0, total = sp.n_rows * width;
@@ -161,35 +164,42 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p, int rows_p
 }
 
 // Rows of q heads, then k heads, then v heads.  One warp per row finds the
-// row's entry (the number of range starts at or below it: ranges ascend) and
-// the page of its slot, while the block's loads are in flight.
+// row's entry (the number of range starts at or below it: ranges ascend) and the
+// page of its slot: five dependent loads, which a block makes for all of its rows
+// at once while its first values are in flight.  Then the block streams its
+// items, U a thread, the next U in flight while the last are turned and written.
 template <int EL, int VB, int U>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p, int rows_per_block) {
+__global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p, int rows_per_block, uint32_t width_magic) {
   using V = typename Vec<VB>::T;
   constexpr int E = VB / EL;
   extern __shared__ float2 cs[];
   __shared__ int s_pos[kMaxRows];       // -1: the row does nothing
   __shared__ long long s_dst[kMaxRows]; // its slot's row of (layer, k, head 0), -1: not written
+  pdl_trigger();
+  pdl_wait();
   const CacheView& c = p.c;
-  const int ipr = c.hd / (2 * E), half = p.r.rd / 2;
+  const int ipr = c.hd / (2 * E), li = __ffs(ipr) - 1, half = p.r.rd / 2;   // (ipr is a power of two)
   const int hq = p.q ? c.n_head : 0, heads = hq + 2 * c.n_head_kv, items = heads * ipr;
   const Span sp = block_span(p.rows.T, rows_per_block, items, U * kThreads);
   const int width = sp.it1 - sp.it0, total = sp.n_rows * width;
-  V v0[U], v1[U];
+  V v[2][U][2];
+  auto load = [&](int g0, V (&x)[U][2]) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int g = threadIdx.x + u * kThreads;
-    if (g >= total) continue;
-    const int r = g / width, it = sp.it0 + g - r * width, h = it / ipr;
-    int o0, o1;
-    item_offsets<E>(p.r, it - h * ipr, o0, o1);
-    const size_t t = sp.row0 + r;
-    const char* src = h < hq ? p.q + t * p.q_ld + (size_t)h * c.hd * EL
-                      : h < hq + c.n_head_kv ? p.k + t * p.k_ld + (size_t)(h - hq) * c.hd * EL
-                                             : p.v + t * p.v_ld + (size_t)(h - hq - c.n_head_kv) * c.hd * EL;
-    v0[u] = *reinterpret_cast<const V*>(src + o0 * EL);
-    v1[u] = *reinterpret_cast<const V*>(src + o1 * EL);
-  }
+    for (int u = 0; u < U; ++u) {
+      const int g = g0 + threadIdx.x + u * kThreads;
+      if (g >= total) continue;
+      const int r = small_quotient(g, width_magic), it = sp.it0 + g - r * width, h = it >> li;
+      int o0, o1;
+      item_offsets<E>(p.r, it - (h << li), o0, o1);
+      const size_t t = sp.row0 + r;
+      const char* src = h < hq ? p.q + t * p.q_ld + (size_t)h * c.hd * EL
+                        : h < hq + c.n_head_kv ? p.k + t * p.k_ld + (size_t)(h - hq) * c.hd * EL
+                                               : p.v + t * p.v_ld + (size_t)(h - hq - c.n_head_kv) * c.hd * EL;
+      x[u][0] = *reinterpret_cast<const V*>(src + o0 * EL);
+      x[u][1] = *reinterpret_cast<const V*>(src + o1 * EL);
+    }
+  };
+  load(0, v[0]);
   const int lane = threadIdx.x & 31;
   const bool first = blockIdx.y == 0 && lane == 0;   // one report per row
   for (int r = threadIdx.x >> 5; r < sp.n_rows; r += kThreads / 32) {
@@ -245,24 +255,34 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p, int ro
   }
   __syncthreads();
   const size_t head_bytes = (size_t)c.ps * c.hd * EL;   // one (page, layer, k|v, head)
+  auto store = [&](int g0, V (&x)[U][2]) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int g = threadIdx.x + u * kThreads;
-    if (g >= total) continue;
-    const int r = g / width, it = sp.it0 + g - r * width, h = it / ipr, i = it - h * ipr;
-    if (s_pos[r] < 0) continue;
-    int o0, o1;
-    const bool rot = item_offsets<E>(p.r, i, o0, o1);
-    if (rot && h < hq + c.n_head_kv) turn<EL, VB>(v0[u], v1[u], cs + r * half + i * E, p.r.interleaved);
-    char* dst;
-    if (h < hq) {
-      dst = p.q_out + (size_t)(sp.row0 + r) * p.q_out_ld + (size_t)h * c.hd * EL;
-    } else {
-      if (s_dst[r] < 0) continue;
-      dst = c.pages + s_dst[r] + (h - hq) * head_bytes;   // v follows the k heads
+    for (int u = 0; u < U; ++u) {
+      const int g = g0 + threadIdx.x + u * kThreads;
+      if (g >= total) continue;
+      const int r = small_quotient(g, width_magic), it = sp.it0 + g - r * width, h = it >> li, i = it - (h << li);
+      if (s_pos[r] < 0) continue;
+      int o0, o1;
+      const bool rot = item_offsets<E>(p.r, i, o0, o1);
+      if (rot && h < hq + c.n_head_kv) turn<EL, VB>(x[u][0], x[u][1], cs + r * half + i * E, p.r.interleaved);
+      char* dst;
+      if (h < hq) {
+        dst = p.q_out + (size_t)(sp.row0 + r) * p.q_out_ld + (size_t)h * c.hd * EL;
+      } else {
+        if (s_dst[r] < 0) continue;
+        dst = c.pages + s_dst[r] + (h - hq) * head_bytes;   // v follows the k heads
+      }
+      *reinterpret_cast<V*>(dst + o0 * EL) = x[u][0];
+      *reinterpret_cast<V*>(dst + o1 * EL) = x[u][1];
     }
-    *reinterpret_cast<V*>(dst + o0 * EL) = v0[u];
-    *reinterpret_cast<V*>(dst + o1 * EL) = v1[u];
+  };
+  constexpr int kStep = U * kThreads;
+  for (int g0 = 0; g0 < total; g0 += 2 * kStep) {
+    if (g0 + kStep < total) load(g0 + kStep, v[1]);
+    store(g0, v[0]);
+    if (g0 + kStep >= total) break;
+    if (g0 + 2 * kStep < total) load(g0 + 2 * kStep, v[0]);
+    store(g0 + kStep, v[1]);
   }
 }
 
@@ -288,23 +308,25 @@ template <int EL, int VB>
 cudaError_t rope_as(const RopeParams& p, cudaStream_t st) {
   const Shape s = shape_of(p.T, p.n_heads * (p.hd / (2 * (VB / EL))), p.r.rd);
   const dim3 grid(s.gx, s.gy);
-  if (s.u == 4)
-    rope_kernel<EL, VB, 4><<<grid, kThreads, s.smem, st>>>(p, s.rows);
-  else
-    rope_kernel<EL, VB, 1><<<grid, kThreads, s.smem, st>>>(p, s.rows);
-  return cudaGetLastError();
+  return s.u == 4 ? launch_dependent(rope_kernel<EL, VB, 4>, grid, kThreads, s.smem, st, p, s.rows)
+                  : launch_dependent(rope_kernel<EL, VB, 1>, grid, kThreads, s.smem, st, p, s.rows);
 }
 
 template <int EL, int VB>
 cudaError_t append_as(const AppendParams& p, cudaStream_t st) {
-  const int heads = (p.q ? p.c.n_head : 0) + 2 * p.c.n_head_kv;
-  const Shape s = shape_of(p.rows.T, heads * (p.c.hd / (2 * (VB / EL))), p.r.rd);
-  const dim3 grid(s.gx, s.gy);
-  if (s.u == 4)
-    append_kernel<EL, VB, 4><<<grid, kThreads, s.smem, st>>>(p, s.rows);
-  else
-    append_kernel<EL, VB, 1><<<grid, kThreads, s.smem, st>>>(p, s.rows);
-  return cudaGetLastError();
+  const int heads = (p.q ? p.c.n_head : 0) + 2 * p.c.n_head_kv, items = heads * (p.c.hd / (2 * (VB / EL)));
+  Shape s = shape_of(p.rows.T, items, p.r.rd);
+  if (s.u == 1) {
+    // (a block of part of a row has one row: a divisor beyond its items)
+    return launch_dependent(append_kernel<EL, VB, 1>, dim3(s.gx, s.gy), kThreads, s.smem, st, p, s.rows,
+                            quotient_magic(s.rows > 1 ? items : 1 << 30));
+  }
+  // large calls: 16 rows a block, whatever their items (8192 rows of 48 heads:
+  // 47 us with one pass of 4 items a thread, whose page look-ups nothing covered)
+  s.rows = kAppendRows;
+  s.smem = sizeof(float2) * s.rows * (p.r.rd / 2);
+  return launch_dependent(append_kernel<EL, VB, 2>, dim3((p.rows.T + s.rows - 1) / s.rows), kThreads, s.smem, st, p,
+                          s.rows, quotient_magic(items));
 }
 
 }  // namespace

@@ -196,6 +196,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  pdl_trigger();
+  pdl_wait();
   plan_entries(p.a, cutting<EL>(TR), s_e, s_end, s_warp, kThreads, blockIdx.x == 0);
   __syncthreads();
   const long long U = s_end[p.a.rows.n_seq - 1];
@@ -551,8 +553,7 @@ cudaError_t stream_as(const AttendParams& a, const AttendWork& w, cudaStream_t s
   p.stages = (int)((kSmemTwo - fixed) / (G::kHalf + 16));
   if (p.stages > kStagesMost) p.stages = kStagesMost;
   const size_t smem = fixed + (size_t)p.stages * (G::kHalf + 16);
-  attend_stream_kernel<EL, HD, MT><<<2 * w.sms, kThreads, smem, st>>>(p);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_dependent(attend_stream_kernel<EL, HD, MT>, dim3(2 * w.sms), kThreads, smem, st, p);
   if (e != cudaSuccess) return e;
   return launch_join<EL, HD>(a, w, 16 * MT, 2 * w.sms, st);
 }

@@ -175,8 +175,6 @@ DF_DEVICE bool copy_wait(int* issued, int pos, uint64_t* b, uint32_t par, volati
   }
   return bar_wait(b, par, abort, status);
 }
-// y / d of y < 2^32 / d, magic = ceil(2^32 / d) (0: d = 1)
-DF_DEVICE int small_quotient(int y, uint32_t magic) { return magic ? (int)__umulhi((uint32_t)y, magic) : y; }
 DF_DEVICE bool copy_there(int* issued, int pos, uint64_t* b, uint32_t par) {
   return load_acquire(issued) > pos && bar_try(b, par);
 }
@@ -434,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  pdl_trigger();
   pdl_wait();
   plan_entries(p.a, cutting(), s_e, s_end, s_warp, kThreads, b == 0);
   if (tid == 0) p.cuts[b] = {0, 0, 0, 0, -1, 0};
@@ -959,7 +958,7 @@ cudaError_t umma_as(const AttendParams& a, const AttendWork& w, cudaStream_t st)
   // pairs fill both Q areas; split tiles of 128 dims alternate between them and
   // are bound by memory, where the stage counts for more
   const bool pairs = (long long)a.max_tree * (a.c.n_head / a.c.n_head_kv) > kWide;
-  p.grp_magic = grp > 1 ? (uint32_t)((0x100000000ull + grp - 1) / grp) : 0;
+  p.grp_magic = quotient_magic(grp);
   p.scratch = pairs || HD == 64 ? kScratch : 0;
   const size_t fixed = fixed_smem<HD>(a.rows.n_seq) + p.scratch;
   p.stages = (int)((kSmemMost - fixed) / (Lt::kMat + 16));

@@ -261,23 +261,6 @@ DF_DEVICE int blocks_used(long long U, int launched, int least) {
 DF_DEVICE long long range_begin(long long U, int G, int b) { return quotient(U * b, G); }
 DF_DEVICE int block_of(long long U, int G, long long u) { return (int)quotient((u + 1) * G - 1, U); }
 
-// A launch that may start while the kernel before it ends (it waits for it with
-// griddepcontrol.wait before it touches global memory).
-template <typename K, typename... A>
-cudaError_t launch_dependent(K* kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // ------------------------------------------------------------------ join
 
 // Rows of tiles cut by ranges: grid (blocks of the attention launch, up to 16
@@ -289,6 +272,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(AttendParams p, const 
                                                           const float2* part_ml, int tile) {
   constexpr int VL = HD / 32;
   using V = typename DimVec<VL>::T;
+  pdl_trigger();
   pdl_wait();
   const int b0 = blockIdx.x, lane = threadIdx.x & 31;
   const Cut d = cuts[b0];
