@@ -321,9 +321,12 @@ cudaError_t append_as(const AppendParams& p, cudaStream_t st) {
     return launch_dependent(append_kernel<EL, VB, 1>, dim3(s.gx, s.gy), kThreads, s.smem, st, p, s.rows,
                             quotient_magic(s.rows > 1 ? items : 1 << 30));
   }
-  // large calls: 16 rows a block, whatever their items (8192 rows of 48 heads:
-  // 47 us with one pass of 4 items a thread, whose page look-ups nothing covered)
-  s.rows = kAppendRows;
+  // large calls: one or more full waves of blocks (four per SM by their registers)
+  // of at most 16 rows each.  8192 rows of 48 heads: 39 us in blocks of 14 rows, 41
+  // of 16, 50 of 27, 51 of 11; 47 us with one pass of 4 items a thread, whose page
+  // look-ups nothing covered.
+  const int wave = 4 * 152, waves = (p.rows.T + wave * kAppendRows - 1) / (wave * kAppendRows);
+  s.rows = (p.rows.T + wave * waves - 1) / (wave * waves);
   s.smem = sizeof(float2) * s.rows * (p.r.rd / 2);
   return launch_dependent(append_kernel<EL, VB, 2>, dim3((p.rows.T + s.rows - 1) / s.rows), kThreads, s.smem, st, p,
                           s.rows, quotient_magic(items));
