@@ -22,7 +22,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden", f"-I{ROOT / 'include'}", f"-I{CSRC}"]
 SOURCES = ["dflash_api.cu", "attention.cu", "gemm.cu", "gemm_tma.cu", "gemm_umma.cu", "gemm_fp4.cu", "kernels.cu", "noalloc.cu",
-           "cache_api.cu", "cache.cu", "rope.cu", "tree_attention.cu", "tree_attention_umma.cu"]
+           "cache_api.cu", "cache.cu", "rope.cu", "tree_attention.cu", "tree_attention_umma.cu",
+           "tree_attention_f32.cu"]
 
 
 def nvcc() -> str:

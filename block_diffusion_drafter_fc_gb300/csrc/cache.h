@@ -127,6 +127,8 @@ size_t attend_part_rows(int el, int hd);
 int attend_chunk(int el, int hd);
 cudaError_t configure_attend();
 cudaError_t configure_attend_umma();
+cudaError_t configure_attend_f32();
+cudaError_t launch_attend_f32(const AttendParams& p, const AttendWork& w, cudaStream_t st);
 cudaError_t launch_attend_umma(const AttendParams& p, const AttendWork& w, cudaStream_t st);
 cudaError_t launch_attend(const AttendParams& p, const AttendWork& w, cudaStream_t st);
 

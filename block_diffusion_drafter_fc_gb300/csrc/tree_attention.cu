@@ -8,26 +8,24 @@
 // changes them to m' = max(m, s), l' = l e^(m-m') + e^(s-m'), and the weighted
 // sum of values likewise.  Parts of a row's slots join the same way.
 //
-// Streaming kernel, for calls with few rows per kv head (decoding, small trees)
-// and for f32 storage: the bound is the read of the pages.  The call's work is
-// one list of units (a tile of 16 or 32 rows of one kv head's query group x a
-// chunk of slots), cut into equal ranges, one per resident block, so that one
-// long sequence is spread over the whole GPU and many short ones are balanced;
-// a tile cut by ranges leaves partial rows in scratch, which a second, dependent
-// launch joins in block order (a warp per row: joining in the tile's last block
-// took 40 of 78 us for a 16-node chain over 2048 slots).  K and V chunks come through a ring of shared-memory
-// stages (TMA, one box per page and 128 bytes of a row), across tiles; four
-// warps each take a quarter of a chunk's slots for all rows of the tile, with
-// their own m, l and sums (no exchange until the tile ends), on mma.sync.  Warp
-// 0 also refills the stage of the chunk before the current one: a fifth, copying
-// warp would leave the others 168 registers instead of 255 (two blocks per SM),
-// and the 32-row tiles spill at that.
+// Streaming kernel, here for bf16 heads of 32 (tree_attention_umma.cu has the
+// larger bf16 heads, tree_attention_f32.cu f32).  The call's work is one list of
+// units (a tile of 16 or 32 rows of one kv head's query group x a chunk of slots),
+// cut into equal ranges, one per resident block, so that one long sequence is
+// spread over the whole GPU and many short ones are balanced; a tile cut by ranges
+// leaves partial rows in scratch, which a second, dependent launch joins in block
+// order (a warp per row: joining in the tile's last block took 40 of 78 us for a
+// 16-node chain over 2048 slots).  K and V chunks come through a ring of
+// shared-memory stages (TMA, one box per page and 128 bytes of a row), across
+// tiles; four warps each take a quarter of a chunk's slots for all rows of the
+// tile, with their own m, l and sums (no exchange until the tile ends), on
+// mma.sync.  Warp 0 also refills the stage of the chunk before the current one.
+// A chunk of 64 slots of 32 dims is too short a product to feed tcgen05 for, and
+// the bound is the latency of its steps.
 //
-// bf16: products of bf16 operands are exact in fp32; the weights are split
-// into bf16 hi + lo (2^-17), which costs one more mma per tile and is free
-// here.  f32: every operand is split into tf32 hi + lo and three products are
-// kept (2^-21 of a product's size).
-#include "tree_common.cuh"
+// Products of bf16 operands are exact in fp32; the weights are split into bf16
+// hi + lo (2^-17), which costs one more mma per tile and is free here.
+#include "tree_stream.cuh"
 
 namespace dflash {
 
@@ -35,149 +33,26 @@ using namespace tree;
 
 namespace {
 
-constexpr int kConsumers = 4;
-constexpr int kThreads = 32 * kConsumers;
-constexpr int kMinUnits = 3;   // a block's least share of a call's units
-
-template <int EL, int HD>
-struct Geo {
-  static constexpr int CS = EL == 2 ? 64 : 32;            // slots of a chunk
-  static constexpr int WS = CS / kConsumers;              // slots of a warp
-  static constexpr int kRowB = HD * EL;                   // bytes of a row
-  static constexpr int kBoxB = kRowB < 128 ? kRowB : 128; // bytes of a row within a box
-  static constexpr int kBoxes = kRowB / kBoxB;
-  static constexpr int kHalf = CS * kRowB;                // bytes of a K or V chunk
-};
-
-// Offset of 16-byte piece `c` of row r in a block of `rows` rows as the copies
-// lay it out: boxes of 128-byte (64-byte) rows, swizzled.
-template <int RowB>
-DF_DEVICE int swz(int rows, int r, int c) {
-  if constexpr (RowB >= 128)
-    return (c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-  else
-    return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-}
-
 DF_DEVICE void ldsm4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
-}
-DF_DEVICE void ldsm2(uint32_t (&r)[2], uint32_t a) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
 }
 DF_DEVICE void ldsm4t(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
-DF_DEVICE void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 "
-      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// x = hi + lo with both in tf32 (11 significant bits each)
-DF_DEVICE void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
-}
-
-// every chunk one unit, a tile two besides
-template <int EL>
-DF_DEVICE Cutting cutting(int tile) {
-  return {tile, Geo<EL, 64>::CS, 0, 1, 1, 2};
-}
-
-struct StreamParams {
-  CUtensorMap tm;     // pages as [rows of (page, layer, k|v, head)][page_size][hd]
-  AttendParams a;
-  float* part_o;      // [2 blocks][rows of a tile][hd]
-  float2* part_ml;    // [2 blocks][rows of a tile] (maximum in powers of two, sum)
-  Cut* cuts;          // [blocks]
-  int stages, box_rows;
-};
-
-// The copies of a block's chunks, run ahead of their use by one warp: K, then V
-// of every chunk of every segment.
-template <int EL, int HD>
-struct Copies {
-  using G = Geo<EL, HD>;
-  long long u;
-  int s, it = 0, ch = 0, kv = 0;
-  int base = 0, row = 0;    // lane i holds the tensor row of page base + i
-  bool more = false;
-  Segment g;
-
-  DF_DEVICE void open(const StreamParams& p, const Entry* e, const long long* end, long long u1, int tile) {
-    more = next_segment(p.a, cutting<EL>(tile), e, end, u, u1, s, g);
-    ch = g.c0;
-    base = -64;
-  }
-  DF_DEVICE void issue(const StreamParams& p, uint8_t* sm, uint64_t* full, uint64_t* empty, const Entry* e,
-                       const long long* end, long long u1, int tile, volatile int* abort) {
-    if (!more) return;
-    const CacheView& c = p.a.c;
-    const int lane = threadIdx.x & 31, S = p.stages, st = it % S;
-    const int none = c.n_pages * c.n_layer * 2 * c.n_head_kv;   // past the tensor: reads as zero
-    if (kv == 0 && ((ch * G::CS + G::CS - 1) >> c.ps_log2) > base + 31) {
-      const Entry x = e[g.s];
-      base = (ch * G::CS) >> c.ps_log2;
-      row = none;
-      if (base + lane <= (x.len + x.n - 1) >> c.ps_log2) {
-        const int t = c.table[(size_t)x.q * c.max_pages + base + lane];
-        if (t >= 0 && t < c.n_pages)
-          row = (t * c.n_layer + p.a.layer) * 2 * c.n_head_kv + g.kvh;
-        else
-          set_status(c.status, DEV_BAD_PAGE);
-      }
-    }
-    int stop = 0;
-    if (lane == 0) {
-      bar_wait(&empty[st], (uint32_t)((it / S) & 1) ^ 1, abort, c.status);
-      stop = *abort;
-      if (!stop) bar_expect(&full[st], G::kHalf);
-    }
-    if (__shfl_sync(0xffffffffu, stop, 0)) {
-      more = false;
-      return;
-    }
-    uint8_t* dst = sm + st * G::kHalf;
-    for (int i = 0; i < G::CS; i += p.box_rows) {
-      const int slot = ch * G::CS + i;
-      const int r = __shfl_sync(0xffffffffu, row, ((slot >> c.ps_log2) - base) & 31);
-      if (lane == 0)
-#pragma unroll
-        for (int x4 = 0; x4 < G::kBoxes; ++x4)
-          tma3d(dst + x4 * G::CS * G::kBoxB + i * G::kBoxB, &p.tm, x4 * (G::kBoxB / EL), slot & (c.ps - 1),
-                r == none ? none : r + kv * c.n_head_kv, &full[st]);
-    }
-    ++it;
-    if (kv ^= 1) return;
-    if (++ch == g.c1) open(p, e, end, u1, tile);
-  }
-  // no copy may still be landing when the block ends
-  DF_DEVICE void drain(int S, uint64_t* full) {
-    if ((threadIdx.x & 31) == 0)
-      for (int j = max(0, it - S); j < it; ++j) {
-        const long long t0 = clock64();
-        while (!bar_try(&full[j % S], (uint32_t)((j / S) & 1)) && clock64() - t0 < kWait) {
-        }
-      }
-  }
-};
-
-template <int EL, int HD, int MT>
+template <int HD, int MT>
 __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid_constant__ StreamParams p) {
+  constexpr int EL = 2;
   using G = Geo<EL, HD>;
   constexpr int TR = 16 * MT;                 // rows of a tile
   constexpr int NV = HD / 8;                  // 8-wide column blocks of the output
-  constexpr int kQ = TR * G::kRowB;           // bytes of Q (f32: hi, then lo)
+  constexpr int kQ = TR * G::kRowB;           // bytes of Q
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int S = p.stages;
   uint8_t* s_q = sm + S * G::kHalf;
-  float* s_o = reinterpret_cast<float*>(s_q + (EL == 4 ? 2 : 1) * kQ);    // two 16 x HD tiles
+  float* s_o = reinterpret_cast<float*>(s_q + kQ);    // two 16 x HD tiles
   float2* s_ml = reinterpret_cast<float2*>(s_o + 2 * 16 * HD);            // [2][16]
   uint64_t* full = reinterpret_cast<uint64_t*>(s_ml + 32);
   uint64_t* empty = full + S;
@@ -239,17 +114,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
         v = *reinterpret_cast<const uint4*>(p.a.q + (size_t)(x.lo + node) * p.a.q_ld + (size_t)h * G::kRowB + pc * 16);
       }
       uint8_t* d = s_q + swz<G::kRowB>(TR, r, pc);
-      if constexpr (EL == 2) {
-        *reinterpret_cast<uint4*>(d) = v;
-      } else {
-        uint4 hi, lo;
-        split_tf32(__uint_as_float(v.x), hi.x, lo.x);
-        split_tf32(__uint_as_float(v.y), hi.y, lo.y);
-        split_tf32(__uint_as_float(v.z), hi.z, lo.z);
-        split_tf32(__uint_as_float(v.w), hi.w, lo.w);
-        *reinterpret_cast<uint4*>(d) = hi;
-        *reinterpret_cast<uint4*>(d + kQ) = lo;
-      }
+      *reinterpret_cast<uint4*>(d) = v;
     }
     __syncthreads();
     float o[MT][NV][4], m[MT][2], l[MT][2];
@@ -277,36 +142,16 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
       if (warp == 0 && it > 0) cp.issue(p, sm, full, empty, s_e, s_end, ub1, TR, &s_abort);
       bar_wait(&full[it % S], (uint32_t)((it / S) & 1), &s_abort, c.status);
       const uint32_t kbase = su32(kb), qbase = su32(s_q);
-      if constexpr (EL == 2) {
+      #pragma unroll
+      for (int k = 0; k < HD / 16; ++k) {
+        uint32_t kf[4];   // (slots 0-7, k 0-7), (slots 0-7, k 8-15), (slots 8-15, ..)
+        ldsm4(kf, kbase + swz<G::kRowB>(G::CS, warp * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
 #pragma unroll
-        for (int k = 0; k < HD / 16; ++k) {
-          uint32_t kf[4];   // (slots 0-7, k 0-7), (slots 0-7, k 8-15), (slots 8-15, ..)
-          ldsm4(kf, kbase + swz<G::kRowB>(G::CS, warp * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            uint32_t qf[4];
-            ldsm4(qf, qbase + swz<G::kRowB>(TR, t * 16 + (lane & 15), 2 * k + (lane >> 4)));
-            mma_bf16_16816(sc[t][0], qf, kf[0], kf[1]);
-            mma_bf16_16816(sc[t][1], qf, kf[2], kf[3]);
-          }
-        }
-      } else {
-#pragma unroll 4
-        for (int k = 0; k < HD / 8; ++k) {
-          uint32_t kf[2], kh[2], kl[2];
-          ldsm2(kf, kbase + swz<G::kRowB>(G::CS, warp * 8 + (lane & 7), 2 * k + ((lane >> 3) & 1)));
-          split_tf32(__uint_as_float(kf[0]), kh[0], kl[0]);
-          split_tf32(__uint_as_float(kf[1]), kh[1], kl[1]);
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            uint32_t qh[4], ql[4];
-            const uint32_t qa = qbase + swz<G::kRowB>(TR, t * 16 + (lane & 15), 2 * k + (lane >> 4));
-            ldsm4(qh, qa);
-            ldsm4(ql, qa + kQ);
-            mma_tf32(sc[t][0], ql, kh[0], kh[1]);
-            mma_tf32(sc[t][0], qh, kl[0], kl[1]);
-            mma_tf32(sc[t][0], qh, kh[0], kh[1]);
-          }
+        for (int t = 0; t < MT; ++t) {
+          uint32_t qf[4];
+          ldsm4(qf, qbase + swz<G::kRowB>(TR, t * 16 + (lane & 15), 2 * k + (lane >> 4)));
+          mma_bf16_16816(sc[t][0], qf, kf[0], kf[1]);
+          mma_bf16_16816(sc[t][1], qf, kf[2], kf[3]);
         }
       }
       __syncwarp();
@@ -379,54 +224,24 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
         }
         __syncwarp();
       }
-      if constexpr (EL == 2) {
-        uint32_t ph[MT][4], pl[MT][4];   // weights as the A operand: the score fragment's layout
+      uint32_t ph[MT][4], pl[MT][4];   // weights as the A operand: the score fragment's layout
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        split_bf16x2(sc[t][0][0], sc[t][0][1], ph[t][0], pl[t][0]);
+        split_bf16x2(sc[t][0][2], sc[t][0][3], ph[t][1], pl[t][1]);
+        split_bf16x2(sc[t][1][0], sc[t][1][1], ph[t][2], pl[t][2]);
+        split_bf16x2(sc[t][1][2], sc[t][1][3], ph[t][3], pl[t][3]);
+      }
+#pragma unroll
+      for (int j = 0; j < NV; j += 2) {
+        uint32_t vf[4];   // (slots 0-7, dims j), (slots 8-15, dims j), (.., dims j + 1)
+        ldsm4t(vf, vbase + swz<G::kRowB>(G::CS, warp * 16 + (lane & 15), j + (lane >> 4)));
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-          split_bf16x2(sc[t][0][0], sc[t][0][1], ph[t][0], pl[t][0]);
-          split_bf16x2(sc[t][0][2], sc[t][0][3], ph[t][1], pl[t][1]);
-          split_bf16x2(sc[t][1][0], sc[t][1][1], ph[t][2], pl[t][2]);
-          split_bf16x2(sc[t][1][2], sc[t][1][3], ph[t][3], pl[t][3]);
-        }
-#pragma unroll
-        for (int j = 0; j < NV; j += 2) {
-          uint32_t vf[4];   // (slots 0-7, dims j), (slots 8-15, dims j), (.., dims j + 1)
-          ldsm4t(vf, vbase + swz<G::kRowB>(G::CS, warp * 16 + (lane & 15), j + (lane >> 4)));
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            mma_bf16_16816(o[t][j], pl[t], vf[0], vf[1]);
-            mma_bf16_16816(o[t][j], ph[t], vf[0], vf[1]);
-            mma_bf16_16816(o[t][j + 1], pl[t], vf[2], vf[3]);
-            mma_bf16_16816(o[t][j + 1], ph[t], vf[2], vf[3]);
-          }
-        }
-      } else {
-        // k index t of the product is slot 2t, t + 4 is slot 2t + 1: the score
-        // fragment is the A operand as it stands
-        uint32_t ph[MT][4], pl[MT][4];
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          split_tf32(sc[t][0][0], ph[t][0], pl[t][0]);
-          split_tf32(sc[t][0][2], ph[t][1], pl[t][1]);
-          split_tf32(sc[t][0][1], ph[t][2], pl[t][2]);
-          split_tf32(sc[t][0][3], ph[t][3], pl[t][3]);
-        }
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          uint32_t vh[2], vl[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int d = j * 8 + gr;
-            const float v = *reinterpret_cast<const float*>(
-                vb + swz<G::kRowB>(G::CS, warp * 8 + 2 * qd + k, d >> 2) + (d & 3) * 4);
-            split_tf32(v, vh[k], vl[k]);
-          }
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            mma_tf32(o[t][j], pl[t], vh[0], vh[1]);
-            mma_tf32(o[t][j], ph[t], vl[0], vl[1]);
-            mma_tf32(o[t][j], ph[t], vh[0], vh[1]);
-          }
+          mma_bf16_16816(o[t][j], pl[t], vf[0], vf[1]);
+          mma_bf16_16816(o[t][j], ph[t], vf[0], vf[1]);
+          mma_bf16_16816(o[t][j + 1], pl[t], vf[2], vf[3]);
+          mma_bf16_16816(o[t][j + 1], ph[t], vf[2], vf[3]);
         }
       }
       if (ragged) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -503,10 +318,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
               const float a = o[t][j][hf * 2] * inv, bb = o[t][j][hf * 2 + 1] * inv;
-              if constexpr (EL == 2)
-                *reinterpret_cast<uint32_t*>(dst + (j * 8 + qd * 2) * 2) = pack_bf16x2(a, bb);
-              else
-                *reinterpret_cast<float2*>(dst + (j * 8 + qd * 2) * 4) = make_float2(a, bb);
+              *reinterpret_cast<uint32_t*>(dst + (j * 8 + qd * 2) * 2) = pack_bf16x2(a, bb);
             }
           } else {
             float* po = p.part_o + ((size_t)slot * TR + r) * HD;
@@ -531,43 +343,24 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
   if (tid == 0) p.cuts[b] = d;
 }
 
-template <int EL, int HD, int MT>
+template <int HD, int MT>
 size_t fixed_smem(int n_seq) {
-  return 1024 + (EL == 4 ? 2 : 1) * 16 * MT * HD * EL + 2 * 16 * HD * 4 + 32 * 8 + 8 * 8 +
+  return 1024 + 16 * MT * HD * 2 + 2 * 16 * HD * 4 + 32 * 8 + 8 * 8 +
          (size_t)n_seq * (sizeof(long long) + sizeof(Entry));
 }
-constexpr size_t kSmemTwo = 114 * 1024 - 512;   // dynamic shared memory of a block, two blocks per SM
-constexpr int kStagesMost = 12;
 
-template <int EL, int HD, int MT>
+template <int HD, int MT>
 cudaError_t stream_as(const AttendParams& a, const AttendWork& w, cudaStream_t st) {
-  using G = Geo<EL, HD>;
-  StreamParams p;
-  p.tm = *w.tm;
-  p.a = a;
-  p.part_o = w.part_o;
-  p.part_ml = w.part_ml;
-  p.cuts = w.cuts;
-  p.box_rows = a.c.ps < G::CS ? a.c.ps : G::CS;
-  const size_t fixed = fixed_smem<EL, HD, MT>(a.rows.n_seq);
-  p.stages = (int)((kSmemTwo - fixed) / (G::kHalf + 16));
-  if (p.stages > kStagesMost) p.stages = kStagesMost;
-  const size_t smem = fixed + (size_t)p.stages * (G::kHalf + 16);
-  const cudaError_t e = launch_dependent(attend_stream_kernel<EL, HD, MT>, dim3(2 * w.sms), kThreads, smem, st, p);
+  size_t smem;
+  const StreamParams p = stream_params<2, HD>(a, w, fixed_smem<HD, MT>(a.rows.n_seq), kSmemTwo, smem);
+  const cudaError_t e = launch_dependent(attend_stream_kernel<HD, MT>, dim3(2 * w.sms), kThreads, smem, st, p);
   if (e != cudaSuccess) return e;
-  return launch_join<EL, HD>(a, w, 16 * MT, 2 * w.sms, st);
+  return launch_join<2, HD>(a, w, 16 * MT, 2 * w.sms, st);
 }
 
-template <int EL, int HD>
-cudaError_t stream_hd(const AttendParams& a, const AttendWork& w, cudaStream_t st) {
-  const long long rows = (long long)a.max_tree * (a.c.n_head / a.c.n_head_kv);
-  return rows <= 16 ? stream_as<EL, HD, 1>(a, w, st) : stream_as<EL, HD, 2>(a, w, st);
-}
-
-template <int EL, int HD, int MT>
+template <int HD, int MT>
 cudaError_t raise_smem() {
-  return cudaFuncSetAttribute(attend_stream_kernel<EL, HD, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)kSmemTwo);
+  return cudaFuncSetAttribute(attend_stream_kernel<HD, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemTwo);
 }
 
 }  // namespace
@@ -581,23 +374,18 @@ size_t attend_part_rows(int el, int hd) { return 2 * (size_t)kAttendSms * (atten
 
 cudaError_t configure_attend() {
   cudaError_t e = configure_attend_umma();
-  auto both = [&](cudaError_t x) { if (e == cudaSuccess) e = x; };
-  both(raise_smem<2, 32, 1>());
-  both(raise_smem<2, 32, 2>());
-  both(raise_smem<4, 32, 1>());
-  both(raise_smem<4, 32, 2>());
-  both(raise_smem<4, 64, 1>());
-  both(raise_smem<4, 64, 2>());
-  both(raise_smem<4, 128, 1>());
-  both(raise_smem<4, 128, 2>());
+  if (e == cudaSuccess) e = configure_attend_f32();
+  if (e == cudaSuccess) e = raise_smem<32, 1>();
+  if (e == cudaSuccess) e = raise_smem<32, 2>();
   return e;
 }
 
 cudaError_t launch_attend(const AttendParams& a, const AttendWork& w, cudaStream_t st) {
+  if (a.c.el == 4) return launch_attend_f32(a, w, st);
   if (attend_on_umma(a.c.el, a.c.hd)) return launch_attend_umma(a, w, st);
-  if (a.c.el == 2) return stream_hd<2, 32>(a, w, st);
-  return a.c.hd == 32 ? stream_hd<4, 32>(a, w, st) : a.c.hd == 64 ? stream_hd<4, 64>(a, w, st)
-                                                                : stream_hd<4, 128>(a, w, st);
+  // 32-row tiles once a call has entries of more than 16 rows per kv head
+  const long long rows = (long long)a.max_tree * (a.c.n_head / a.c.n_head_kv);
+  return rows <= 16 ? stream_as<32, 1>(a, w, st) : stream_as<32, 2>(a, w, st);
 }
 
 }  // namespace dflash
