@@ -194,7 +194,8 @@ struct UmmaParams {
   uint32_t grp_magic;   // ceil(2^32 / query heads per kv head): quotients of small numbers
 };
 
-// Bit j: the row sees slot `slot` + j.
+// Bit j: the row sees slot `slot` + j.  (Plain loads: a dependent launch may start
+// before the kernel that writes the mask has ended, which the read-only path excludes.)
 DF_DEVICE uint32_t visible(const AttendParams& p, const Entry& x, int node, int slot) {
   const int a = slot - x.len;                    // node index of bit 0
   if (a <= -32) return ~0u;
@@ -206,10 +207,10 @@ DF_DEVICE uint32_t visible(const AttendParams& p, const Entry& x, int node, int 
   } else {
     const uint32_t* w = p.mask + (size_t)(x.lo + node) * p.words;
     if (a < 0) {
-      v = (__ldg(w) << -a) | ((1u << -a) - 1u);
+      v = (*w << -a) | ((1u << -a) - 1u);
     } else {
       const int k = a >> 5;
-      const uint32_t lo = k < p.words ? __ldg(w + k) : 0u, hi = k + 1 < p.words ? __ldg(w + k + 1) : 0u;
+      const uint32_t lo = k < p.words ? w[k] : 0u, hi = k + 1 < p.words ? w[k + 1] : 0u;
       v = __funnelshift_r(lo, hi, a & 31);
     }
   }
