@@ -853,16 +853,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
               *reinterpret_cast<float4*>(buf + lane * 32 + ((q ^ (lane & 7)) << 2)) =
                   make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
             __syncwarp();
+            // (loads first, then stores: a branch between them made it 125 clocks a row of four)
+            const int q = lane & 7;
+            float4 x[8];
+            unsigned long long to[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const int r = 4 * e + (lane >> 3), q = lane & 7;
-              const float4 x = *reinterpret_cast<const float4*>(buf + r * 32 + ((q ^ (r & 7)) << 2));
-              char* to = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, (unsigned long long)dst, r));
-              if (r >= last) continue;
-              if (whole)
-                *reinterpret_cast<uint2*>(to + (dim + 4 * q) * 2) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-              else
-                *reinterpret_cast<float4*>(to + (dim + 4 * q) * 4) = x;
+              const int r = 4 * e + (lane >> 3);
+              x[e] = *reinterpret_cast<const float4*>(buf + r * 32 + ((q ^ (r & 7)) << 2));
+              to[e] = __shfl_sync(0xffffffffu, (unsigned long long)dst, r);
+            }
+            if (whole) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (4 * e + (lane >> 3) < last)
+                  *reinterpret_cast<uint2*>(to[e] + (dim + 4 * q) * 2) =
+                      make_uint2(pack_bf16x2(x[e].x, x[e].y), pack_bf16x2(x[e].z, x[e].w));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (4 * e + (lane >> 3) < last) *reinterpret_cast<float4*>(to[e] + (dim + 4 * q) * 4) = x[e];
             }
           }
       } else {
@@ -883,24 +893,35 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
                       make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
             }
           sync_rows();
-          for (int e = tid; e < left << ql; e += 256) {
-            const int r = e >> ql, q = e - (r << ql);
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int y = r; y < lines; y += left) {
-              const float4 f = *reinterpret_cast<const float4*>(area + y * D + (q & ~7) * 4 + (((q & 7) ^ (y & 7)) << 2));
-              x.x += f.x;
-              x.y += f.y;
-              x.z += f.z;
-              x.w += f.w;
-            }
-            const int dim = p0 + 4 * q;
-            if (whole) {
-              char* to;
-              float* lse;
-              out_row(r, to, lse);
-              *reinterpret_cast<uint2*>(to + dim * 2) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-            } else {
-              *reinterpret_cast<float4*>(p.part_o + ((size_t)slot * kTile + r) * HD + dim) = x;
+          for (int e0 = tid; e0 < left << ql; e0 += 1024) {   // four at a time
+            float4 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int y = 0; y < rep; ++y)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int e = e0 + 256 * k, r = e >> ql, q = e - (r << ql), at = y * left + r;
+                if (r >= left) continue;
+                const float4 f =
+                    *reinterpret_cast<const float4*>(area + at * D + (q & ~7) * 4 + (((q & 7) ^ (at & 7)) << 2));
+                x[k].x += f.x;
+                x[k].y += f.y;
+                x[k].z += f.z;
+                x[k].w += f.w;
+              }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int e = e0 + 256 * k, r = e >> ql, dim = p0 + 4 * (e - (r << ql));
+              if (r >= left) continue;
+              if (whole) {
+                char* to;
+                float* lse;
+                out_row(r, to, lse);
+                *reinterpret_cast<uint2*>(to + dim * 2) =
+                    make_uint2(pack_bf16x2(x[k].x, x[k].y), pack_bf16x2(x[k].z, x[k].w));
+              } else {
+                *reinterpret_cast<float4*>(p.part_o + ((size_t)slot * kTile + r) * HD + dim) = x[k];
+              }
             }
           }
           if (D < HD) sync_rows();
