@@ -19,7 +19,8 @@ namespace {
 // up_{up_i}; after round r M_i covers 2^r levels, so a chain of n nodes takes
 // log2 n rounds instead of n dependent steps.  Within a round a set may already
 // hold another node's update: still only ancestors, and at least the levels the
-// pointer read in this round skips.
+// pointer read in this round skips.  Bound: latency, the rounds' barriers: masks
+// and walk of 256 trees of 1..128 nodes take 6.4 us in a graph, of one of 26 4.4.
 __global__ void tree_mask_kernel(RowView rows, const int32_t* parents, uint32_t* mask, int words,
                                  int32_t* depth, unsigned* status) {
   pdl_trigger();
@@ -145,7 +146,8 @@ constexpr int kBatch = 8;   // tokens in flight per thread
 // tokens of a column before it writes any of them, ascending, so a slot is read
 // before it is overwritten (path[j] >= j, ascending; no other thread touches the
 // column).  The last block of an entry to have read its length writes the new
-// one.
+// one.  Bound: memory: 92 MB (32 sequences, 32 layers, 12 slots) in 18 us from HBM =
+// 5.1 TB/s, 14.6 us in a loop that finds them in L2.
 __global__ void __launch_bounds__(256) commit_kernel(CacheView c, RowView rows, const int32_t* path,
                                                      int max_path, const int32_t* n_path, int* tickets) {
   pdl_trigger();
@@ -259,7 +261,8 @@ DF_DEVICE int block_scan(int v, int* s_warp, int& total) {
 // order, and the entries of it that need a page are ranked by scans of the
 // list; rank r gets the r-th free page.  Three passes over the list and one
 // over refs (until enough free pages are found), each kPlan wide: nothing is
-// changed before the totals are known.
+// changed before the totals are known.  Bound: latency, 9 us for 24 entries,
+// cold; more blocks would have to agree on the pages' order.
 __global__ void __launch_bounds__(kPlan) reserve_plan_kernel(CacheView c, RowView rows, const int32_t* count,
                                                              int32_t* free_list, int4* copies) {
   pdl_trigger();
@@ -386,7 +389,7 @@ __global__ void __launch_bounds__(kPlan) reserve_plan_kernel(CacheView c, RowVie
 }
 
 // grid (blocks, entries): the slots an entry keeps of its part-filled page, for
-// every (layer, k|v, head) a contiguous run.
+// every (layer, k|v, head) a contiguous run; 74 MB in 13 us (5.7 TB/s).
 __global__ void __launch_bounds__(256) reserve_copy_kernel(CacheView c, const int4* copies) {
   pdl_trigger();
   pdl_wait();
