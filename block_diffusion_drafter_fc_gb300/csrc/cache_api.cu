@@ -259,10 +259,18 @@ int dflash_cache_create(const dflash_cache_config* cfg, void* page_mem, void* st
   c->rope = {c->S<unsigned long long>(c->L.turns), cfg->rotary_dim, cfg->rope_layout == DFLASH_ROPE_INTERLEAVED,
              rope_mscale(*cfg)};
   (void)cudaGetLastError();
-  cudaPointerAttributes at;
-  cudaError_t e = cudaPointerGetAttributes(&at, page_mem);
-  c->device = e == cudaSuccess && at.type == cudaMemoryTypeDevice ? at.device : -1;
-  if (e == cudaSuccess && c->device < 0) e = cudaErrorInvalidDevicePointer;
+  // all three areas are memory of one device, which is the handle's
+  cudaError_t e = cudaSuccess;
+  c->device = -1;
+  for (const void* area : {static_cast<const void*>(page_mem), static_cast<const void*>(state_mem),
+                           static_cast<const void*>(scratch_mem)}) {
+    cudaPointerAttributes at;
+    if (e == cudaSuccess) e = cudaPointerGetAttributes(&at, area);
+    if (e != cudaSuccess) break;
+    if (at.type != cudaMemoryTypeDevice || (c->device >= 0 && at.device != c->device))
+      e = cudaErrorInvalidDevicePointer;
+    c->device = at.device;
+  }
   if (e == cudaSuccess) {
     OnDevice on(c->device);
     unsigned long long turns[64] = {};

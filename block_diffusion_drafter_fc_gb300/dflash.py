@@ -409,7 +409,9 @@ class PagedCache:
 
     Tensors of rows are [T][heads][head_dim] with any row stride of a multiple of 16
     bytes (a slice of a fused projection's rows will do); row_start is int32 [n_seq + 1],
-    seqs int32 [n_seq] or None for sequences 0.., all on the device."""
+    seqs int32 [n_seq] or None for sequences 0.., all on the cache's device."""
+
+    device_index = -1     # before the handle: the host's
 
     def __init__(self, cfg, device: str = "cuda"):
         self.cfg = cfg
@@ -469,15 +471,18 @@ class PagedCache:
                               f"[{hd}] {self.dtype}")
         if shape[0] and (stride[2] != 1 or (stride[1] != hd and shape[1] > 1)):
             raise DFlashError(f"{what}: a row's heads have to be contiguous")
+        if t.get_device() != self.device_index:
+            raise DFlashError(f"{what}: a tensor on {t.device}, not on the cache's device")
         return shape[0], stride[0] if shape[0] > 1 else shape[1] * hd
 
-    @staticmethod
-    def _int(what: str, t, n: int) -> int:
+    def _int(self, what: str, t, n: int) -> int:
         """Address of a contiguous int32 tensor of at least n values (None: null)."""
         if t is None:
             return 0
         if t.dtype is not torch.int32 or not t.is_contiguous() or t.numel() < n:
             raise DFlashError(f"{what}: index arrays are contiguous int32 of the call's size")
+        if t.get_device() != self.device_index:
+            raise DFlashError(f"{what}: an index array on {t.device}, not on the cache's device")
         return t.data_ptr()
 
     def _on(self, stream) -> int:
@@ -539,8 +544,9 @@ class PagedCache:
         if rows != T:
             raise DFlashError("tree_attend: q and out have different rows")
         if lse is not None:
-            if lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() != T * hq:
-                raise DFlashError("tree_attend: lse is contiguous f32 [T][n_head]")
+            if (lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() != T * hq
+                    or lse.get_device() != self.device_index):
+                raise DFlashError("tree_attend: lse is contiguous f32 [T][n_head] on the cache's device")
             lp = lse.data_ptr()
         i = self._int
         self._ok(LIB.dflash_tree_attend(

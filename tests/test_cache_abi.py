@@ -119,3 +119,21 @@ def test_binding_refuses_wrong_tensors():
         c.dflash_cache_trim(torch.zeros(3, dtype=torch.int32), seqs=torch.zeros(2, dtype=torch.int32))
     with pytest.raises(D.DFlashError, match="invalid argument"):
         c.dflash_rope(x, pos, x, stream=types.SimpleNamespace(cuda_stream=0))   # no handle
+
+
+def test_binding_refuses_tensors_of_another_device():
+    c = _binding()
+    c.device_index = 0
+    x = torch.zeros(3, 8, 64, dtype=torch.bfloat16)
+    kv = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    i = torch.zeros(3, dtype=torch.int32)
+    start = torch.tensor([0, 3], dtype=torch.int32)
+    calls = [lambda: c.dflash_rope(x, i, x), lambda: c.dflash_cache_append(0, start, kv, kv),
+             lambda: c.dflash_tree_mask(start, i, torch.zeros(3, 1, dtype=torch.int32)),
+             lambda: c.dflash_tree_attend(0, start, 3, x, torch.empty_like(x)),
+             lambda: c.dflash_tree_accept(start, i, i, i, i.view(1, 3), i[:1], i[:1]),
+             lambda: c.dflash_cache_commit(i[None], i[:1]), lambda: c.dflash_cache_reserve(i),
+             lambda: c.dflash_cache_fork(i, i), lambda: c.dflash_cache_trim(i)]
+    for call in calls:
+        with pytest.raises(D.DFlashError, match="device"):
+            call()

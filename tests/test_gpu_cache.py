@@ -627,6 +627,30 @@ def test_attend_long_and_many(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attend_most_entries(dtype):
+    """As many entries as a call may have, one of them with tall tiles."""
+    rng = np.random.default_rng(10)
+    g = torch.Generator().manual_seed(10)
+    n = 1024
+    c = make(n_head=4, n_head_kv=1, head_dim=128, page_size=16, n_pages=2200, max_seq=n, max_pages=8, dtype=dtype)
+    counts = rng.integers(0, 4, n)
+    lens = rng.integers(0, 26, n)
+    counts[700], lens[700] = 70, 20
+    attend_case(c, rng, g, rng.permutation(n).tolist(), lens.tolist(), counts.tolist(), "tree", dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hd,hq,hkv", [(128, 5, 1), (64, 40, 1), (128, 14, 2), (64, 300, 1), (32, 300, 1)], ids=str)
+def test_attend_group_sizes(dtype, hd, hq, hkv):
+    """Groups of query heads that no tile holds a whole number of, or that are larger than a tile."""
+    rng = np.random.default_rng(hq)
+    g = torch.Generator().manual_seed(hq)
+    c = make(n_head=hq, n_head_kv=hkv, head_dim=hd, page_size=32, n_pages=60, max_seq=4, max_pages=16, dtype=dtype)
+    attend_case(c, rng, g, [2, 0, 3], [200, 0, 31], [33, 60, 1], "tree", dtype)
+    attend_case(c, rng, g, [1], [129], [52], "chain", dtype, with_lse=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attend_large_scores(dtype):
     """Scores far outside exp's range, of both signs, and scales of their own."""
     rng = np.random.default_rng(2)
@@ -893,3 +917,18 @@ def test_offsets_past_32_bits():
     now = np64(c.pages[n_pages - 1, 0, 1, :, 250:253]).transpose(1, 0, 2)
     np.testing.assert_array_equal(now, np64(rows[[0, 7, 11], 16:]))
     assert c.dflash_cache_read_status() == 0
+
+
+def test_areas_on_the_host_are_refused():
+    import ctypes as C
+    D = _D()
+    cfg = D.make_cache_config(D.CacheConfig(n_layer=1, n_head=2, n_head_kv=1, head_dim=64, page_size=16, n_pages=4,
+                                            max_seq=2, max_pages=4))
+    sizes = D.cache_workspace_size(cfg)
+    good = [torch.empty(n + 256, dtype=torch.uint8, device="cuda") for n in sizes]
+    for bad in range(3):
+        areas = list(good)
+        areas[bad] = torch.empty(sizes[bad] + 256, dtype=torch.uint8)
+        h = C.c_void_p()
+        rc = D.LIB.dflash_cache_create(C.byref(cfg), *(D.Drafter._aligned(a) for a in areas), C.byref(h))
+        assert rc != 0 and not h.value
