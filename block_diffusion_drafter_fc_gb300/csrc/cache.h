@@ -106,6 +106,8 @@ struct AttendParams {
   int64_t q_ld, out_ld;   // bytes
   float* lse;
   float scale;
+  int grp;    // query heads per kv head
+  int step;   // nodes of a tile where a chain's tiles are cut short (set by the kernels' launchers; 0: never)
 };
 // What a handle keeps for attention: tensor maps of the pages, scratch for the
 // partial rows of tiles that several blocks share, and a description per block

@@ -396,6 +396,8 @@ int dflash_tree_attend(dflash_cache* c, int32_t layer, int32_t n_seq, const int3
   p.q_ld = q_stride * p.c.el;
   p.out_ld = out_stride * p.c.el;
   p.lse = lse;
+  p.grp = hq / c->cfg.n_head_kv;
+  p.step = 0;
   p.scale = c->cfg.attn_scale != 0.f ? c->cfg.attn_scale : (float)(1.0 / std::sqrt((double)c->cfg.head_dim));
   DC_CHECK(c, launch_attend(p, c->work, static_cast<cudaStream_t>(stream)));
   return DFLASH_OK;

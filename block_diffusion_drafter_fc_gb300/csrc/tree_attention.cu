@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
   }
   const long long ub0 = range_begin(U, Gr, b), ub1 = range_begin(U, Gr, b + 1);
   const int s_first = find_entry(s_end, p.a.rows.n_seq, ub0);
-  const int grp = c.n_head / c.n_head_kv;
+  const int grp = p.a.grp;
 
   Copies<EL, HD> cp;
   cp.u = ub0;
@@ -352,7 +352,7 @@ size_t fixed_smem(int n_seq) {
 template <int HD, int MT>
 cudaError_t stream_as(const AttendParams& a, const AttendWork& w, cudaStream_t st) {
   size_t smem;
-  const StreamParams p = stream_params<2, HD>(a, w, fixed_smem<HD, MT>(a.rows.n_seq), kSmemTwo, smem);
+  const StreamParams p = stream_params<2, HD>(a, w, 16 * MT, fixed_smem<HD, MT>(a.rows.n_seq), smem);
   const cudaError_t e = launch_dependent(attend_stream_kernel<HD, MT>, dim3(2 * w.sms), kThreads, smem, st, p);
   if (e != cudaSuccess) return e;
   return launch_join<2, HD>(a, w, 16 * MT, 2 * w.sms, st);
@@ -384,7 +384,7 @@ cudaError_t launch_attend(const AttendParams& a, const AttendWork& w, cudaStream
   if (a.c.el == 4) return launch_attend_f32(a, w, st);
   if (attend_on_umma(a.c.el, a.c.hd)) return launch_attend_umma(a, w, st);
   // 32-row tiles once a call has entries of more than 16 rows per kv head
-  const long long rows = (long long)a.max_tree * (a.c.n_head / a.c.n_head_kv);
+  const long long rows = (long long)a.max_tree * a.grp;
   return rows <= 16 ? stream_as<32, 1>(a, w, st) : stream_as<32, 2>(a, w, st);
 }
 

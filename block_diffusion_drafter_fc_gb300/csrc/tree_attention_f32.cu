@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kAll, kPerSm) attend_f32_kernel(const __grid_c
   }
   const long long ub0 = range_begin(U, Gr, b), ub1 = range_begin(U, Gr, b + 1);
   const int s_first = find_entry(s_end, p.a.rows.n_seq, ub0);
-  const int grp = c.n_head / c.n_head_kv;
+  const int grp = p.a.grp;
   if (warp == kConsumers) {
     Copies<4, HD> cp;
     cp.u = ub0;
@@ -350,7 +350,7 @@ size_t fixed_smem(int n_seq) {
 template <int HD>
 cudaError_t f32_as(const AttendParams& a, const AttendWork& w, cudaStream_t st) {
   size_t smem;
-  const StreamParams p = stream_params<4, HD>(a, w, fixed_smem<HD>(a.rows.n_seq), kSmemTwo, smem);
+  const StreamParams p = stream_params<4, HD>(a, w, TR, fixed_smem<HD>(a.rows.n_seq), smem);
   const cudaError_t e = launch_dependent(attend_f32_kernel<HD>, dim3(kPerSm * w.sms), kAll, smem, st, p);
   if (e != cudaSuccess) return e;
   return launch_join<4, HD>(a, w, TR, kPerSm * w.sms, st);

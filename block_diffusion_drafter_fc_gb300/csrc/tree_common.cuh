@@ -84,7 +84,13 @@ struct Entry {
 // short tiles took twice the time of a range within a long one.
 struct Cutting {
   int tile, chunk, wide, heavy, light, extra;
+  // chunks of w units that begin before unit x (divisions by constants, not by w)
+  DF_DEVICE int chunks(long long x, int w) const;
 };
+
+DF_DEVICE int Cutting::chunks(long long x, int w) const {
+  return (int)(w == light ? quotient(x + light - 1, light) : quotient(x + heavy - 1, heavy));
+}
 
 // The row blocks of one kv head of an entry and their cost.  Without a mask a
 // tile sees no slot behind its last node: block i then has ceil((len + e_i) /
@@ -99,15 +105,13 @@ struct Blocks {
   long long first;         // slots of block 0, + chunk - 1
 
   DF_DEVICE Blocks(const AttendParams& p, const Cutting& cut, const Entry& x) : c(cut), step(0), first(0) {
-    const int g = p.c.n_head / p.c.n_head_kv;
-    const long long rows = (long long)x.n * g;
+    const long long rows = (long long)x.n * p.grp;
     count = (int)quotient(rows + c.tile - 1, c.tile);
     nch = (int)quotient((long long)x.len + x.n + c.chunk - 1, c.chunk);
     last = rows - (long long)(count - 1) * c.tile > c.wide ? c.heavy : c.light;
-    const int per = c.tile / g;
-    if (!p.mask && c.tile % g == 0 && count > 1 && (per % c.chunk == 0 || c.chunk % per == 0)) {
-      step = per;
-      first = (long long)x.len + per + c.chunk - 1;
+    if (p.step && count > 1) {
+      step = p.step;
+      first = (long long)x.len + step + c.chunk - 1;
     }
   }
   DF_DEVICE int units(int i) const { return i == count - 1 ? last : c.heavy; }   // of a chunk of block i
@@ -136,13 +140,59 @@ struct Blocks {
   }
 };
 
+// Nodes of a tile, where Blocks may trim (see there).
+inline int trim_step(const AttendParams& a, int tile, int chunk) {
+  if (a.mask || tile % a.grp) return 0;
+  const int per = tile / a.grp;
+  return per % chunk == 0 || chunk % per == 0 ? per : 0;
+}
+
+// Entry s and its units (0: skipped; bad: why).
+DF_DEVICE long long plan_entry(const AttendParams& p, const Cutting& cut, int s, Entry& x, unsigned& bad) {
+  const CacheView& c = p.c;
+  const int lo = p.rows.row_start[s], hi = p.rows.row_start[s + 1];   // (loads of one round trip)
+  x.q = entry_sequence(p.rows, s, c.max_seq);
+  x.len = x.q >= 0 ? c.length[x.q] : 0;
+  x.lo = lo;
+  x.n = hi - lo;
+  bad = 0;
+  if (lo < 0 || lo > hi || hi > p.rows.T || x.n > p.max_tree)
+    bad = DEV_BAD_ROWS;
+  else if (x.n > 0 && x.q < 0)
+    bad = DEV_BAD_SEQ;
+  else if (x.n > 0 && (x.len < 0 || (long long)x.len + x.n > (long long)c.max_pages * c.ps))
+    bad = DEV_BAD_ROWS;
+  if (bad) x.n = 0;
+  if (x.n <= 0) return 0;
+  const Blocks b(p, cut, x);
+  return c.n_head_kv * b.before(b.count);
+}
+
+// plan_entries by one warp, of at most 32 entries: the block's other warps need not wait.
+DF_DEVICE void plan_few(const AttendParams& p, const Cutting& cut, Entry* e, long long* end, bool report) {
+  const int s = threadIdx.x & 31;
+  Entry x;
+  unsigned bad = 0;
+  long long v = s < p.rows.n_seq ? plan_entry(p, cut, s, x, bad) : 0;
+  if (bad && report) set_status(p.c.status, bad);
+#pragma unroll 1
+  for (int o = 1; o < p.rows.n_seq; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, v, o);
+    if (s >= o) v += y;
+  }
+  if (s < p.rows.n_seq) {
+    e[s] = x;
+    end[s] = v;
+  }
+  __syncwarp();
+}
+
 // The call's work as one list of units, the entries' one after another: fills
 // e[] and end[] (end[s]: units of entries 0..s; a skipped entry has none) with
 // all `threads` threads of the block (a multiple of 32).  One block reports
 // faults.  s_warp: a word per warp in shared memory.
 DF_DEVICE void plan_entries(const AttendParams& p, const Cutting& cut, Entry* e, long long* end,
                             long long* s_warp, int threads, bool report) {
-  const CacheView& c = p.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long before = 0;
   for (int s0 = 0; s0 < p.rows.n_seq; s0 += threads) {
@@ -150,25 +200,10 @@ DF_DEVICE void plan_entries(const AttendParams& p, const Cutting& cut, Entry* e,
     long long units = 0;
     if (s < p.rows.n_seq) {
       Entry x;
-      unsigned bad = 0;
-      if (!entry_rows(p.rows, s, x.lo, x.n) || x.n > p.max_tree) bad = DEV_BAD_ROWS;
-      x.q = entry_sequence(p.rows, s, c.max_seq);
-      x.len = x.q >= 0 ? c.length[x.q] : 0;
-      if (!bad && x.n > 0) {
-        if (x.q < 0)
-          bad = DEV_BAD_SEQ;
-        else if (x.len < 0 || (long long)x.len + x.n > (long long)c.max_pages * c.ps)
-          bad = DEV_BAD_ROWS;
-      }
-      if (bad) {
-        x.n = 0;
-        if (report) set_status(c.status, bad);
-      }
+      unsigned bad;
+      units = plan_entry(p, cut, s, x, bad);
+      if (bad && report) set_status(p.c.status, bad);
       e[s] = x;
-      if (x.n > 0) {
-        const Blocks b(p, cut, x);
-        units = c.n_head_kv * b.before(b.count);
-      }
     }
     long long v = units;
 #pragma unroll
@@ -231,8 +266,8 @@ DF_DEVICE bool next_segment(const AttendParams& p, const Cutting& cut, const Ent
     const int w = b.units(i);
     const long long from = in - start, to = min((long long)g.nch * w + cut.extra, from + (u1 - u));
     // a chunk belongs to the range that holds its first unit
-    g.c0 = (int)quotient(max(from - cut.extra, 0LL) + w - 1, w);
-    g.c1 = (int)quotient(max(to - cut.extra, 0LL) + w - 1, w);
+    g.c0 = cut.chunks(max(from - cut.extra, 0LL), w);
+    g.c1 = cut.chunks(max(to - cut.extra, 0LL), w);
     g.u0 = first + g.kvh * per + start + cut.extra;
     g.w = w;
     u += to - from;
@@ -307,7 +342,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(AttendParams p, const 
       }
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int grp = p.c.n_head / p.c.n_head_kv, node = (d.row0 + r) / grp;
+    const int grp = p.grp, node = (d.row0 + r) / grp;
     const int h = d.kvh * grp + (d.row0 + r) - node * grp;
     char* dst = p.out + (size_t)(d.lo + node) * p.out_ld + (size_t)(h * HD + lane * VL) * EL;
 #pragma unroll
@@ -327,7 +362,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(AttendParams p, const 
 
 template <int EL, int HD>
 cudaError_t launch_join(const AttendParams& p, const AttendWork& w, int tile, int blocks, cudaStream_t st) {
-  const long long rows = (long long)p.max_tree * (p.c.n_head / p.c.n_head_kv);
+  const long long rows = (long long)p.max_tree * p.grp;
   const int most = rows < tile ? (int)rows : tile;
   return launch_dependent(attend_join_kernel<EL, HD>, dim3(blocks, most < 64 ? (most + 3) / 4 : 16), 128, 0, st, p,
                           (const Cut*)w.cuts, (const float*)w.part_o, (const float2*)w.part_ml, tile);

@@ -119,19 +119,20 @@ struct Copies {
 constexpr size_t kSmemTwo = 114 * 1024 - 512;
 constexpr int kStagesMost = 12;
 
-// Parameters of a streaming launch whose blocks need `fixed` of their
-// `most` bytes of shared memory besides the ring.
+// Parameters of a streaming launch whose blocks have tiles of `tile`
+// rows and need `fixed` bytes of shared memory besides the ring.
 template <int EL, int HD>
-StreamParams stream_params(const AttendParams& a, const AttendWork& w, size_t fixed, size_t most, size_t& smem) {
+StreamParams stream_params(const AttendParams& a, const AttendWork& w, int tile, size_t fixed, size_t& smem) {
   using G = Geo<EL, HD>;
   StreamParams p;
   p.tm = *w.tm;
   p.a = a;
+  p.a.step = trim_step(a, tile, G::CS);
   p.part_o = w.part_o;
   p.part_ml = w.part_ml;
   p.cuts = w.cuts;
   p.box_rows = a.c.ps < G::CS ? a.c.ps : G::CS;
-  p.stages = (int)((most - fixed) / (G::kHalf + 16));
+  p.stages = (int)((kSmemTwo - fixed) / (G::kHalf + 16));
   if (p.stages > kStagesMost) p.stages = kStagesMost;
   smem = fixed + (size_t)p.stages * (G::kHalf + 16);
   return p;
