@@ -37,7 +37,9 @@
 // Tensor memory: S_0, S_1 (two halves of 64 columns each), O_0, O_1 (head_dim
 // each).  With whole chunks (128 columns, one buffer per stream) a stream's
 // scores, softmax and PV followed one another, and two streams left the tensor
-// pipe idle half of the time: 288 us instead of 271 for 2047 rows over 8192 slots.
+// pipe idle half of the time: 288 us instead of 271 for 2047 rows over 8192 slots
+// (266 by now).  The price: scores of 64 slots cost as much as of 128, as both read
+// Q, 3072 clocks of products a chunk of a pair, which is what a chunk takes.
 // The weights are rounded to bf16 for the product with V (their sum is not):
 // each is off by at most 2^-8 of itself, independently, which adds as much
 // again as the rounding of the result; splitting them as in the streaming
