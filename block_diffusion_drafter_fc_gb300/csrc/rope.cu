@@ -299,7 +299,7 @@ Shape shape_of(int T, int items, int rd) {
   const int span = s.u * kThreads;
   s.rows = items >= span ? 1 : span / items;
   if (s.rows > kMaxRows) s.rows = kMaxRows;
-  s.gx = (T + s.rows - 1) / s.rows;
+  s.gx = (int)(((long long)T + s.rows - 1) / s.rows);
   s.gy = s.rows > 1 ? 1 : (items + span - 1) / span;
   s.smem = sizeof(float2) * s.rows * (rd / 2);
   return s;
@@ -326,11 +326,13 @@ cudaError_t append_as(const AppendParams& p, cudaStream_t st) {
   // of at most 16 rows each.  8192 rows of 48 heads: 39 us in blocks of 14 rows, 41
   // of 16, 50 of 27, 51 of 11; 47 us with one pass of 4 items a thread, whose page
   // look-ups nothing covered.
-  const int wave = 4 * 152, waves = (p.rows.T + wave * kAppendRows - 1) / (wave * kAppendRows);
-  s.rows = (p.rows.T + wave * waves - 1) / (wave * waves);
+  const long long T = p.rows.T, wave = 4 * 152, waves = (T + wave * kAppendRows - 1) / (wave * kAppendRows);
+  s.rows = (int)((T + wave * waves - 1) / (wave * waves));
+  // (thousands of heads: as many rows as the quotient by `items` is exact for)
+  while (s.rows > 1 && !quotient_exact((long long)s.rows * items, items)) --s.rows;
   s.smem = sizeof(float2) * s.rows * (p.r.rd / 2);
-  return launch_dependent(append_kernel<EL, VB, 2>, dim3((p.rows.T + s.rows - 1) / s.rows), kThreads, s.smem, st, p,
-                          s.rows, quotient_magic(items));
+  return launch_dependent(append_kernel<EL, VB, 2>, dim3((unsigned)((T + s.rows - 1) / s.rows)), kThreads, s.smem, st,
+                          p, s.rows, quotient_magic(s.rows > 1 ? items : 1 << 30));
 }
 
 }  // namespace

@@ -503,6 +503,29 @@ def test_append(dtype, hd, ps, rot, kw, with_q):
         assert c.dflash_cache_read_status() == 0
 
 
+def test_append_thousands_of_heads():
+    """Rows of so many items that a block's numbers leave the range of its quotients."""
+    hq, hkv, hd, ps, T = 4096, 512, 128, 16, 1300
+    c = make(n_layer=1, n_head=hq, n_head_kv=hkv, head_dim=hd, page_size=ps, n_pages=90, max_seq=2, max_pages=90)
+    rng = np.random.default_rng(1)
+    scattered(c, rng, [1], [0], [T])
+    g = torch.Generator(device="cuda").manual_seed(1)
+    qkv = torch.randn(T, hq + 2 * hkv, hd, generator=g, device="cuda", dtype=torch.bfloat16)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    q_out = torch.full((T, hq, hd), 3.0, dtype=torch.bfloat16, device="cuda")
+    c.dflash_cache_append(0, starts([T]), k, v, q=q, q_out=q_out, seqs=ints([1]))
+    at = torch.arange(T, device="cuda")
+    page = c.table[1].long()[at // ps]
+    assert torch.equal(c.pages[page, 0, 1, :, at % ps], v)
+    rd, f, m = rope_setup(hd, "half", None, {})
+    rows = [0, 1, 2, 3, 617, 618, T - 1]
+    keys = c.pages[page, 0, 0, :, at % ps]
+    for src, got in ((k, keys), (q, q_out)):
+        want, size = R.rope(np64(src[rows]), np.asarray(rows), "half", rd, f, m)
+        check(np64(got[rows]), want, rope_tol(size, want, "bf16"), "rows")
+    assert c.dflash_cache_read_status() == 0
+
+
 def test_append_faults_write_nothing_else():
     rng = np.random.default_rng(0)
     c = make(n_layer=1, n_head=2, n_head_kv=1, head_dim=32, page_size=16, n_pages=12, max_seq=4, max_pages=3)
