@@ -89,7 +89,8 @@ int validate(const dflash_cache_config* c) {
   if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
     return DFLASH_ERR_UNSUPPORTED;
   if (c->rotary_dim > c->head_dim || c->rotary_dim % 8) return DFLASH_ERR_UNSUPPORTED;
-  if (c->max_seq > kMaxSeq || (long long)c->max_pages * c->page_size > 0x7fffffffLL)
+  // (a tile of slots may reach past the last one: slot numbers stay below 2^31 there too)
+  if (c->max_seq > kMaxSeq || (long long)c->max_pages * c->page_size > (1LL << 31) - 1024)
     return DFLASH_ERR_UNSUPPORTED;
   if (c->n_head > 4096 || c->n_layer > 4096) return DFLASH_ERR_UNSUPPORTED;
   if ((long long)c->n_layer * 2 * c->n_head_kv * c->n_pages > 0x7fffffffLL) return DFLASH_ERR_UNSUPPORTED;

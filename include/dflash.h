@@ -535,7 +535,7 @@ typedef enum {
  * Geometry of a cache handle.
  *   head_dim in {32, 64, 128}; n_head % n_head_kv == 0; page_size a power of two
  *   in 16..256; max_seq <= 4096 sequences, each of at most max_pages pages
- *   (max_pages * page_size < 2^31); n_pages * n_layer * 2 * n_head_kv < 2^31;
+ *   (max_pages * page_size <= 2^31 - 1024); n_pages * n_layer * 2 * n_head_kv < 2^31;
  *   dtype F32 or BF16: pages, queries, keys, values and outputs;
  *   rotary_dim: rotated dims of each head, a multiple of 8 in 0..head_dim;
  *   rope_theta > 1, rope_factor >= 1 (both read only with rotary_dim > 0);

@@ -137,3 +137,9 @@ def test_binding_refuses_tensors_of_another_device():
     for call in calls:
         with pytest.raises(D.DFlashError, match="device"):
             call()
+
+
+def test_most_slots_of_a_sequence():
+    """Slot numbers of a whole tile of slots stay below 2^31."""
+    assert _size(max_pages=(1 << 27) - 64) == 0        # pages of 16 slots
+    assert _size(max_pages=(1 << 27) - 63) == -2
