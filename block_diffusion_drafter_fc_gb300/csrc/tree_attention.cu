@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
   while (next_segment(p.a, cutting<EL>(TR), s_e, s_end, u, ub1, s, g)) {
     const Entry x = s_e[g.s];
     const int rows = min(TR, x.n * grp - g.row0), end = x.len + x.n;
+    const int all = x.len + (p.a.mask ? 0 : g.row0 / grp + 1);   // slots that all rows see
     // Q: row r is head kvh grp + (row0 + r) % grp of node (row0 + r) / grp
     __syncthreads();   // the previous tile's Q and sums have been read
     for (int i = tid; i < TR * (G::kRowB / 16); i += 32 * kConsumers) {
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
       if (lane == 0 && !s_abort) bar_arrive(&empty[it % S]);
       ++it;
       // ---- what a row does not attend to
-      if (slot0 + G::WS > x.len) {
+      if (slot0 + G::WS > all) {
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll

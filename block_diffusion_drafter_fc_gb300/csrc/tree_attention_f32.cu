@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(kAll, kPerSm) attend_f32_kernel(const __grid_c
   while (next_segment(p.a, cutting<4>(TR), s_e, s_end, u, ub1, s, g)) {
     const Entry x = s_e[g.s];
     const int rows = min(TR, x.n * grp - g.row0), end = x.len + x.n;
+    const int all = x.len + (p.a.mask ? 0 : g.row0 / grp + 1);   // slots that all rows see
     sync_tile<kThreads>();   // the previous tile's sums have been read
     for (int i = tid; i < TR * (G::kRowB / 16); i += kThreads) {
       const int r = i / (G::kRowB / 16), pc = i - r * (G::kRowB / 16);
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(kAll, kPerSm) attend_f32_kernel(const __grid_c
       if (lane == 0 && !s_abort) bar_arrive(&empty[st]);
       step();
       // ---- what a row does not attend to; running maximum, weights
-      const bool masked = slot0 + G::WS > x.len;
+      const bool masked = slot0 + G::WS > all;
       float sc[NS], top = -CUDART_INF_F;
 #pragma unroll
       for (int i = 0; i < NS; ++i) {

@@ -11,8 +11,8 @@
 //
 // One persistent block per SM walks its range of the call's work (128-slot
 // chunks of the tiles of every kv head's query rows; tree_common.cuh) with two
-// streams of scores, each of two halves of 64 slots that take turns, so that
-// the products of one half run under the softmax of the other:
+// streams of scores, so that the products of one run under the softmax of the
+// other:
 //   tile of more than 128 rows (pair): stream i holds rows 128 i .. + 127, both
 //     use every chunk;
 //   tile of at most 128 rows (split): stream i takes every second chunk, with
@@ -34,12 +34,14 @@
 //                     product of 16 dims or slots takes some 60 clocks), so an
 //                     issuer per stream: one's barriers are under the other's
 //                     products.
-// Tensor memory: S_0, S_1 (two halves of 64 columns each), O_0, O_1 (head_dim
-// each).  With whole chunks (128 columns, one buffer per stream) a stream's
-// scores, softmax and PV followed one another, and two streams left the tensor
-// pipe idle half of the time: 288 us instead of 271 for 2047 rows over 8192 slots
-// (266 by now).  The price: scores of 64 slots cost as much as of 128, as both read
-// Q, 3072 clocks of products a chunk of a pair, which is what a chunk takes.
+// Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (head_dim each): all of it.
+// A stream's scores, softmax and PV follow one another; the softmax is done by
+// halves of 64 slots, PV of the first under the softmax of the second, and the last
+// PV and the next scores are issued together.  The streams of a pair do that in
+// turn: otherwise their products interleave in the pipe, and both wait for all of
+// them (2047 rows over 8192 slots: 235 us in turn, 262 without).  Scores by halves
+// too, with a buffer for each, kept both in work all the time, but 64 columns of
+// scores cost as much as 128 (both read Q): 261 us.
 // The weights are rounded to bf16 for the product with V (their sum is not):
 // each is off by at most 2^-8 of itself, independently, which adds as much
 // again as the rounding of the result; splitting them as in the streaming
@@ -353,6 +355,61 @@ DF_DEVICE void softmax_step(const AttendParams& p, const Entry& x, int node, int
   wait_st();
 }
 
+// Weights of 32 scores, relative to m (mn2: -m twice); their sums on s2.
+DF_DEVICE void weights(const uint32_t (&v)[32], uint64_t sc2, uint64_t mn2, uint64_t (&s2)[2], uint32_t (&w)[16]) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    float a0, a1;
+    unpack2(fma2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, mn2), a0, a1);
+    a0 = ex2(a0);
+    a1 = ex2(a1);
+    s2[(e >> 1) & 1] = add2(s2[(e >> 1) & 1], pack2(a0, a1));
+    w[e / 2] = pack_bf16x2(a0, a1);
+  }
+}
+
+// A chunk whose 128 slots the rows all see, each load under the weights before it.
+// Halves of P are stored and told of (told(h)) as they are done; returns the first
+// half that is not, because m has to move.
+template <typename F>
+DF_DEVICE int softmax_chunk(uint32_t tS, float scale, F told, float m, float& l) {
+  const uint64_t sc2 = pack2(scale, scale), mn2 = pack2(-m, -m);
+  uint32_t v[2][32], n[32], w[2][16];
+  __syncwarp();
+  tmem_ld32(tS, v[0]);
+  wait_ld(v[0]);
+  tmem_ld32(tS + 32, v[1]);
+  uint64_t s2[2] = {0, 0};
+  weights(v[0], sc2, mn2, s2, w[0]);
+  wait_ld(v[1]);
+  tmem_ld32(tS + 64, n);
+  weights(v[1], sc2, mn2, s2, w[1]);
+  wait_ld(n);
+  float a0, a1;
+  unpack2(add2(s2[0], s2[1]), a0, a1);
+  float sum = a0 + a1;
+  if (__any_sync(0xffffffffu, !(sum < 0x1p60f) || !(l + sum > 0x1p-60f))) return 0;
+  l += sum;
+  tmem_st16(tS, w[0]);
+  tmem_st16(tS + 16, w[1]);
+  wait_st();
+  told(0);
+  tmem_ld32(tS + 96, v[0]);
+  s2[0] = s2[1] = 0;
+  weights(n, sc2, mn2, s2, w[0]);
+  wait_ld(v[0]);
+  weights(v[0], sc2, mn2, s2, w[1]);
+  unpack2(add2(s2[0], s2[1]), a0, a1);
+  sum = a0 + a1;
+  if (__any_sync(0xffffffffu, !(sum < 0x1p60f) || !(l + sum > 0x1p-60f))) return 1;
+  l += sum;
+  tmem_st16(tS + 64, w[0]);
+  tmem_st16(tS + 80, w[1]);
+  wait_st();
+  told(1);
+  return 2;
+}
+
 template <int N>
 struct Int { static constexpr int value = N; };
 
@@ -367,13 +424,16 @@ struct SegDesc {
 };
 constexpr int kSegs = 8;
 
-// Segment `seg` has been planned; false: there is none.
+// Segment `seg` has been planned; false: there is none.  All warps get the same
+// answer, also after a wait that gave up (they meet in barriers at a tile's end):
+// the planning warp, whose own waits are bounded, tells the number of segments in
+// any case.
 DF_DEVICE bool seg_wait(int* planned, int* total, int seg, volatile int* abort, unsigned* status) {
   const long long t0 = clock64();
   while (true) {
     if (load_acquire(planned) > seg) return true;
-    if (load_acquire(total) <= seg || *abort) return false;
-    if (clock64() - t0 > kWait) {
+    if (load_acquire(total) <= seg) return load_acquire(planned) > seg;
+    if (clock64() - t0 > 4 * kWait) {
       *abort = 1;
       set_status(status, DEV_TIMEOUT);
       return false;
@@ -393,10 +453,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
   uint64_t* empty = full + S;
   uint64_t* q_full = empty + S;      // [2] the Q of an even (odd) segment is in shared memory
   uint64_t* q_free = q_full + 2;     // [2] Q area i is free
-  uint64_t* s_full = q_free + 2;     // [2][2] half h of S_i computed (and the stream's products before it done)
-  uint64_t* p_full = s_full + 4;     // [2][2] half h of P_i stored
+  uint64_t* s_full = q_free + 2;     // [2] S_i computed (and the stream's products before it done)
+  uint64_t* p_full = s_full + 2;     // [2][2] half h of P_i stored
   uint64_t* pv_half = p_full + 4;    // [2] the first half of PV of a chunk of stream i is done
-  uint64_t* o_full = pv_half + 2;    // the segment's products are done
+  uint64_t* turn = pv_half + 2;      // [2] stream i may issue (of a pair)
+  uint64_t* o_full = turn + 2;       // the segment's products are done
   uint64_t* o_free = o_full + 1;     // the segment's O has been read
   long long* s_warp = reinterpret_cast<long long*>(o_free + 1);   // [12]
   long long* s_end = s_warp + 12;
@@ -418,10 +479,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       bar_init(&q_full[i], 1);
       bar_init(&q_free[i], 8);
       bar_init(&pv_half[i], 1);
-      for (int h = 0; h < 2; ++h) {
-        bar_init(&s_full[2 * i + h], 1);
-        bar_init(&p_full[2 * i + h], 4);
-      }
+      bar_init(&turn[i], 1);
+      bar_init(&s_full[i], 1);
+      bar_init(&p_full[2 * i], 4);
+      bar_init(&p_full[2 * i + 1], 4);
     }
     bar_init(o_full, 2);
     bar_init(o_free, 8);
@@ -521,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       if (lane == 0) {
         const int i = warp - kIssuer;
         // ring position of the segment's first K chunk, parities, copies before it
-        int base = 0, bph = 0, n_p = 0, qb = 0, it = 0;
+        int base = 0, bph = 0, n_p = 0, qb = 0, it = 0, n_t = i ^ 1;
         bool live = true;
         const uint64_t q0 = desc_k(su32(sm)), k0 = desc_k(su32(ring)), v0 = desc_mn(su32(ring), kHalf);
         const uint32_t dS = tmem + i * 128, dO = tmem + 256 + i * HD;
@@ -545,14 +606,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
             if (!pair) bar_arrive(&empty[pos]);
             commit(&empty[pos]);
           };
-          auto scores = [&](int h) {   // of the chunk's 64 slots h
-            const uint64_t kb = k0 + (uint64_t)(st * (kMat >> 4) + h * 512);
+          auto scores = [&]() {
+            const uint64_t kb = k0 + (uint64_t)(st * (kMat >> 4));
 #pragma unroll
             for (int e = 0; e < HD / 16; ++e) {
               const uint32_t off = ((e >> 2) * kHalf + (e & 3) * 32) >> 4;
-              mma_ss(dS + 64 * h, qa + off, kb + off, idesc(64, false), e > 0);
+              mma_ss(dS, qa + off, kb + off, idesc(128, false), e > 0);
             }
-            commit(&s_full[2 * i + h]);
+            commit(&s_full[i]);
+          };
+          // The streams of a pair issue in turn: the pipe serves two issuers by halves,
+          // and both streams' softmax would then wait for all products of both.
+          auto my_turn = [&]() {
+            if (!pair) return true;
+            const bool ok = bar_wait(&turn[i], n_t, &s_abort, c.status);
+            n_t ^= 1;
+            return ok;
+          };
+          auto pass = [&]() {
+            if (pair) bar_arrive(&turn[i ^ 1]);
           };
           if (!pair && i) {
             step(st, ph, 2);
@@ -560,12 +632,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
           }
           live = bar_wait(&q_full[seg & 1], (seg >> 1) & 1, &s_abort, c.status);
           if (mine > 0 && live) {
-            live = copy_wait(&s_issued, no, &full[st], ph, &s_abort, c.status);
+            live = copy_wait(&s_issued, no, &full[st], ph, &s_abort, c.status) && my_turn();
             if (!live) break;
             fence_after();
-            scores(0);
-            scores(1);
+            scores();
             release(st);
+            pass();
           }
           // the last tile's accumulators have been read
           if (seg > 0) live = live && bar_wait(o_free, (seg & 1) ^ 1, &s_abort, c.status);
@@ -575,31 +647,30 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
             step(st, ph, pair ? 2 : 4);
             live = copy_wait(&s_issued, no + 1, &full[vs], vph, &s_abort, c.status);
             no += pair ? 2 : 4;
-            // with the next K chunk there, its scores follow each half of PV
+            // with the next K chunk there, its scores follow PV at once
             const bool more = k + 1 < mine, ready = more && copy_there(&s_issued, no, &full[st], ph);
             const uint64_t vb = v0 + (uint64_t)(vs * (kMat >> 4));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              live = live && bar_wait(&p_full[2 * i + h], n_p, &s_abort, c.status);
+              live = live && bar_wait(&p_full[2 * i + h], n_p, &s_abort, c.status) && (!h || my_turn());
               if (!live) break;
               fence_after();
 #pragma unroll
               for (int e = 0; e < 4; ++e)   // 16 slots: 2 groups of 1024 bytes
                 mma_ts(dO, dS + 64 * h + 8 * e, vb + ((h * 8192 + e * 2048) >> 4), idesc(HD, true), k + h + e > 0);
-              if (ready) scores(h);
               if (h == 0) commit(&pv_half[i]);
             }
             if (!live) break;
             n_p ^= 1;
             release(vs);
-            if (more && !ready) {
-              live = copy_wait(&s_issued, no, &full[st], ph, &s_abort, c.status);
+            if (more) {
+              if (!ready) live = copy_wait(&s_issued, no, &full[st], ph, &s_abort, c.status);
               if (!live) break;
               fence_after();
-              scores(0);
-              scores(1);
+              scores();
+              release(st);
             }
-            if (more) release(st);
+            pass();
           }
           if (!live) break;
           commit(o_full);
@@ -711,6 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         if (!pair) qb ^= 1;
         __syncwarp();
       }
+      if (lane == 0) publish(&s_total, planned);   // (known already, unless a wait gave up)
       // (a Q that was loaded is a segment's that runs: no copy is in flight at the end)
     }
   } else {
@@ -727,7 +799,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       if (lane == 0) there = seg_wait(&s_planned, &s_total, seg, &s_abort, c.status);
       if (!__shfl_sync(0xffffffffu, there, 0)) break;
       const SegDesc& d = s_seg[seg % kSegs];
-      const int left = d.left, nc = d.nc, ch0 = d.c0, s_len = d.x.len, end = s_len + d.x.n;
+      const int left = d.left, nc = d.nc, ch0 = d.c0, end = d.x.len + d.x.n;
+      // the slots that all rows see (of a chain those of its nodes up to the tile's first)
+      const int all = d.x.len + (p.a.mask ? 0 : d.node0 + 1);
       const bool pair = left > 128;
       const int rep = left > 64 ? 1 : 2, per = 128 / rep;   // copies of a row, rows
       const int steps = pair ? 2 * nc : nc;
@@ -745,10 +819,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       };
       auto step = [&](auto nb, int h, int slot0, bool part, bool later) {
         constexpr int NB = decltype(nb)::value;
-        // the stream's products so far are done: those before a chunk precede the
-        // scores of its second half
+        // the stream's products so far are done (those of chunks before this one
+        // preceded its scores)
         auto settle = [&]() {
-          live = live && bar_wait(h ? &pv_half[i] : &s_full[2 * i + 1], n_s & 1, &s_abort, c.status);
+          if (h) live = live && bar_wait(&pv_half[i], n_s & 1, &s_abort, c.status);
           fence_after();
         };
         if (part)
@@ -758,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       };
       for (int k = i; k < steps; k += 2, ++n_s) {
         const int j = pair ? k >> 1 : k, slot0 = (ch0 + j) * kChunk;
-        const bool masked = slot0 + kChunk > s_len;   // nodes or slots past the last among them
+        const bool masked = slot0 + kChunk > all;
         if (masked && real && p.a.mask) prefetch_mask(p.a, d.x, node, slot0);
         if (slot0 + kChunk > end) {
           // slots past the last node may hold anything: 0 x NaN is NaN (of a pair,
@@ -773,21 +847,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
           }
           fence_async();
         }
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          live = live && bar_wait(&s_full[2 * i + h], n_s & 1, &s_abort, c.status);
-          if (p.scratch && h && k + 2 >= steps) free_q();   // the stream's last scores
-          fence_after();
-          if (!idle) {
-            const int slot = slot0 + 64 * h;
-            if (rep == 1)
-              step(Int<2>(), h, slot, slot + 64 > s_len, k > 1 || h);
-            else
-              step(Int<1>(), h, slot, slot + 64 > s_len, k > 1 || h);
-          }
+        live = live && bar_wait(&s_full[i], n_s & 1, &s_abort, c.status);
+        if (p.scratch && k + 2 >= steps) free_q();   // the stream's last scores
+        fence_after();
+        auto told = [&](int h) {
           fence_before();
           __syncwarp();
           if (lane == 0 && live) bar_arrive(&p_full[2 * i + h]);
+        };
+        int h = 0;
+        if (!idle && rep == 1 && !masked) h = softmax_chunk(tS, scale, told, m, l);
+#pragma unroll 1
+        for (; h < 2; ++h) {
+          if (!idle) {
+            const int slot = slot0 + 64 * h;
+            if (rep == 1)
+              step(Int<2>(), h, slot, slot + 64 > all, k > 1 || h);
+            else
+              step(Int<1>(), h, slot, slot + 64 > all, k > 1 || h);
+          }
+          told(h);
         }
       }
       it += 2 * nc;
