@@ -351,6 +351,7 @@ class DeviceWeight:
 # the target model's side: paged cache, tree attention, rotary positions
 
 MAX_TREE = 1024       # most nodes of a tree with a mask
+_INT32, _raw_stream = torch.int32, getattr(torch._C, "_cuda_getCurrentRawStream", None)
 ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -479,17 +480,18 @@ class PagedCache:
         """Address of a contiguous int32 tensor of at least n values (None: null)."""
         if t is None:
             return 0
-        if t.dtype is not torch.int32 or not t.is_contiguous() or t.numel() < n:
-            raise DFlashError(f"{what}: index arrays are contiguous int32 of the call's size")
+        if (t.dtype is _INT32 and t.get_device() == self.device_index and t.numel() >= n
+                and t.is_contiguous()):
+            return t.data_ptr()
         if t.get_device() != self.device_index:
             raise DFlashError(f"{what}: an index array on {t.device}, not on the cache's device")
-        return t.data_ptr()
+        raise DFlashError(f"{what}: index arrays are contiguous int32 of the call's size")
 
     def _on(self, stream) -> int:
         """The stream's handle (None: torch's current one of the cache's device)."""
         if stream is not None:
             return stream.cuda_stream
-        return torch._C._cuda_getCurrentRawStream(self.device_index)
+        return _raw_stream(self.device_index)
 
     # ---- C-ABI calls (same names)
     def dflash_rope(self, x, pos, out, backward: bool = False, stream=None):
