@@ -3,6 +3,7 @@
 
 #include "cache.h"
 #include "common.cuh"
+#include "launch_shapes.h"
 
 namespace dflash {
 
@@ -36,13 +37,8 @@ DF_DEVICE bool listed_before(const RowView& r, int s, int q) {
   return __syncthreads_or(dup) != 0;
 }
 
-// y / d of y <= 2^32 / d, magic = ceil(2^32 / d) (0: d = 1): the magic is off by less
-// than one from 2^32 / d, the product by less than y
+// y / d (launch_shapes.h: quotient_magic, and where it is exact)
 DF_DEVICE int small_quotient(int y, uint32_t magic) { return magic ? (int)__umulhi((uint32_t)y, magic) : y; }
-inline bool quotient_exact(long long y, long long d) { return y * d <= 1ll << 32; }
-inline uint32_t quotient_magic(uint32_t d) {
-  return d > 1 ? (uint32_t)((0x100000000ull + d - 1) / d) : 0;
-}
 
 // A launch that may start while the kernel before it ends: every kernel here lets
 // the next one be scheduled at once and waits for the one before it with

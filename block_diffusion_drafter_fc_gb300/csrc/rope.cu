@@ -19,11 +19,9 @@
 
 namespace dflash {
 
-namespace {
+using namespace rope;
 
-constexpr int kThreads = 256;
-constexpr int kMaxRows = 32;   // rows of one block
-constexpr int kAppendRows = 16;
+namespace {
 
 template <int VB>
 struct Vec;
@@ -103,21 +101,8 @@ DF_DEVICE float2 angle(const RopeView& r, int pos, int j, bool backward) {
   return make_float2(c * r.mscale, backward ? -s : s);
 }
 
-// What a block works on: rows [row0, row0 + n_rows) and items [it0, it1) of each.
-struct Span {
-  int row0, n_rows, it0, it1;
-};
-DF_DEVICE Span block_span(int T, int rows_per_block, int items, int span) {
-  Span s;
-  s.row0 = blockIdx.x * rows_per_block;
-  s.n_rows = min(rows_per_block, T - s.row0);
-  s.it0 = blockIdx.y * span;
-  s.it1 = rows_per_block > 1 ? items : min(items, s.it0 + span);
-  return s;
-}
-
 template <int EL, int VB, int U>
-__global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p, int rows_per_block) {
+__global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p, int rows_per_block, int span) {
   using V = typename Vec<VB>::T;
   constexpr int E = VB / EL;
   extern __shared__ float2 cs[];   // [rows][rd / 2]
@@ -125,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p, int rows_p
   pdl_trigger();
   pdl_wait();
   const int ipr = p.hd / (2 * E), items = p.n_heads * ipr, half = p.r.rd / 2;
-  const Span sp = block_span(p.T, rows_per_block, items, U * kThreads);
+  const Span sp = block_span(p.T, rows_per_block, items, span, blockIdx.x, blockIdx.y);
   const int width = sp.it1 - sp.it0, total = sp.n_rows * width;
   if (threadIdx.x < sp.n_rows) {
     const int q = p.pos[sp.row0 + threadIdx.x];
@@ -170,7 +155,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p, int rows_p
 // at once while its first values are in flight.  Then the block streams its
 // items, U a thread, the next U in flight while the last are turned and written.
 template <int EL, int VB, int U>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p, int rows_per_block, uint32_t width_magic) {
+__global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p, int rows_per_block, int span,
+                                                          uint32_t width_magic) {
   using V = typename Vec<VB>::T;
   constexpr int E = VB / EL;
   extern __shared__ float2 cs[];
@@ -181,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p, int ro
   const CacheView& c = p.c;
   const int ipr = c.hd / (2 * E), li = __ffs(ipr) - 1, half = p.r.rd / 2;   // (ipr is a power of two)
   const int hq = p.q ? c.n_head : 0, heads = hq + 2 * c.n_head_kv, items = heads * ipr;
-  const Span sp = block_span(p.rows.T, rows_per_block, items, U * kThreads);
+  const Span sp = block_span(p.rows.T, rows_per_block, items, span, blockIdx.x, blockIdx.y);
   const int width = sp.it1 - sp.it0, total = sp.n_rows * width;
   V v[2][U][2];
   auto load = [&](int g0, V (&x)[U][2]) {
@@ -287,52 +273,22 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p, int ro
   }
 }
 
-// Rows and items of a block: 4 items a thread once that still gives every SM
-// a few blocks, else 1 (a small call is latency: as many blocks as there are).
-struct Shape {
-  int u, rows, gx, gy;
-  size_t smem;
-};
-Shape shape_of(int T, int items, int rd) {
-  Shape s;
-  s.u = (long long)T * items >= 152LL * 2 * 4 * kThreads ? 4 : 1;
-  const int span = s.u * kThreads;
-  s.rows = items >= span ? 1 : span / items;
-  if (s.rows > kMaxRows) s.rows = kMaxRows;
-  s.gx = (int)(((long long)T + s.rows - 1) / s.rows);
-  s.gy = s.rows > 1 ? 1 : (items + span - 1) / span;
-  s.smem = sizeof(float2) * s.rows * (rd / 2);
-  return s;
-}
-
 template <int EL, int VB>
 cudaError_t rope_as(const RopeParams& p, cudaStream_t st) {
   const Shape s = shape_of(p.T, p.n_heads * (p.hd / (2 * (VB / EL))), p.r.rd);
   const dim3 grid(s.gx, s.gy);
-  return s.u == 4 ? launch_dependent(rope_kernel<EL, VB, 4>, grid, kThreads, s.smem, st, p, s.rows)
-                  : launch_dependent(rope_kernel<EL, VB, 1>, grid, kThreads, s.smem, st, p, s.rows);
+  return s.u == 4 ? launch_dependent(rope_kernel<EL, VB, 4>, grid, kThreads, s.smem, st, p, s.rows, s.span)
+                  : launch_dependent(rope_kernel<EL, VB, 1>, grid, kThreads, s.smem, st, p, s.rows, s.span);
 }
 
 template <int EL, int VB>
 cudaError_t append_as(const AppendParams& p, cudaStream_t st) {
   const int heads = (p.q ? p.c.n_head : 0) + 2 * p.c.n_head_kv, items = heads * (p.c.hd / (2 * (VB / EL)));
-  Shape s = shape_of(p.rows.T, items, p.r.rd);
-  if (s.u == 1) {
-    // (a block of part of a row has one row: a divisor beyond its items)
-    return launch_dependent(append_kernel<EL, VB, 1>, dim3(s.gx, s.gy), kThreads, s.smem, st, p, s.rows,
-                            quotient_magic(s.rows > 1 ? items : 1 << 30));
-  }
-  // large calls: one or more full waves of blocks (four per SM by their registers)
-  // of at most 16 rows each.  8192 rows of 48 heads: 39 us in blocks of 14 rows, 41
-  // of 16, 50 of 27, 51 of 11; 47 us with one pass of 4 items a thread, whose page
-  // look-ups nothing covered.
-  const long long T = p.rows.T, wave = 4 * 152, waves = (T + wave * kAppendRows - 1) / (wave * kAppendRows);
-  s.rows = (int)((T + wave * waves - 1) / (wave * waves));
-  // (thousands of heads: as many rows as the quotient by `items` is exact for)
-  while (s.rows > 1 && !quotient_exact((long long)s.rows * items, items)) --s.rows;
-  s.smem = sizeof(float2) * s.rows * (p.r.rd / 2);
-  return launch_dependent(append_kernel<EL, VB, 2>, dim3((unsigned)((T + s.rows - 1) / s.rows)), kThreads, s.smem, st,
-                          p, s.rows, quotient_magic(s.rows > 1 ? items : 1 << 30));
+  const Shape s = append_shape(p.rows.T, items, p.r.rd);
+  const dim3 grid(s.gx, s.gy);
+  const uint32_t magic = append_magic(s, items);
+  return s.u == 1 ? launch_dependent(append_kernel<EL, VB, 1>, grid, kThreads, s.smem, st, p, s.rows, s.span, magic)
+                  : launch_dependent(append_kernel<EL, VB, 2>, grid, kThreads, s.smem, st, p, s.rows, s.span, magic);
 }
 
 }  // namespace

@@ -526,6 +526,41 @@ def test_append_thousands_of_heads():
     assert c.dflash_cache_read_status() == 0
 
 
+@pytest.mark.parametrize("dtype,hq,hkv,hd,rot,T", [
+    # rows of more items than a block of one row takes in one step
+    ("bf16", 64, 8, 128, None, 487), ("bf16", 64, 8, 128, None, 512), ("bf16", 64, 8, 128, None, 608),
+    ("bf16", 64, 8, 128, None, 609), ("f32", 32, 8, 128, None, 406), ("f32", 32, 8, 128, None, 512),
+    ("f32", 32, 8, 128, None, 608), ("bf16", 32, 8, 128, -8, 450), ("bf16", 4096, 1024, 128, None, 40),
+    # either side of where a thread takes more items, a block more rows, the grid another wave
+    ("bf16", 32, 8, 128, None, 810), ("bf16", 32, 8, 128, None, 811), ("bf16", 32, 8, 128, None, 1217),
+    ("f32", 32, 8, 128, None, 405), ("bf16", 4, 2, 64, None, 9728), ("bf16", 4, 2, 64, None, 9729),
+    ("f32", 4, 2, 32, 0.5, 9729)], ids=str)
+def test_append_every_item_of_every_row(dtype, hq, hkv, hd, rot, T):
+    """Nothing of a row is left out, whatever the shape of the launch."""
+    ps = 64
+    rd, f, m = rope_setup(hd, "half", rot, {})
+    n_pages = -(-T // ps) + 1
+    c = make(n_layer=1, n_head=hq, n_head_kv=hkv, head_dim=hd, page_size=ps, n_pages=n_pages, max_seq=2, max_pages=n_pages,
+             dtype=dtype, rotary_dim=rd)
+    c.pages.fill_(float("nan"))
+    g = torch.Generator(device="cuda").manual_seed(T)
+    qkv = torch.randn(T, hq + 2 * hkv, hd, generator=g, device="cuda").to(DT[dtype])
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    q_out = torch.full((T, hq, hd), float("nan"), dtype=DT[dtype], device="cuda")
+    c.dflash_cache_reserve(ints([T]), seqs=ints([1]))
+    c.dflash_cache_append(0, starts([T]), k, v, q=q, q_out=q_out, seqs=ints([1]))
+    at = torch.arange(T, device="cuda")
+    page = c.table[1].long()[at // ps]
+    assert torch.equal(c.pages[page, 0, 1, :, at % ps], v)
+    keys = c.pages[page, 0, 0, :, at % ps]
+    assert not torch.isnan(keys).any() and not torch.isnan(q_out).any()
+    rows = sorted({*range(0, T, max(1, T // 60)), T - 1})
+    for src, got in ((k, keys), (q, q_out)):
+        want, size = R.rope(np64(src[rows]), np.asarray(rows), "half", rd, f, m)
+        check(np64(got[rows]), want, rope_tol(size, want, dtype), "rows")
+    assert c.dflash_cache_read_status() == 0
+
+
 def test_append_faults_write_nothing_else():
     rng = np.random.default_rng(0)
     c = make(n_layer=1, n_head=2, n_head_kv=1, head_dim=32, page_size=16, n_pages=12, max_seq=4, max_pages=3)
