@@ -17,6 +17,7 @@ static int cover(const rope::Shape& s, int T, int items, int rd, bool append) {
   if (s.smem < (size_t)8 * s.rows * (rd / 2) || s.smem > 48 * 1024) return 2;
   const rope::Span last = rope::block_span(T, s.rows, items, s.span, s.gx - 1, 0);
   if (last.n_rows < 1 || last.n_rows > s.rows || last.row0 + last.n_rows != T) return 3;
+  if (append && s.u > 1 && (s.gy != 1 || s.span != items)) return 8;   // what its kernel goes by
   int at = 0;
   for (int y = 0; y < s.gy; ++y) {
     const rope::Span b = rope::block_span(T, s.rows, items, s.span, 0, y);
