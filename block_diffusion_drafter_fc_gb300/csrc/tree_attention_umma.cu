@@ -594,13 +594,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
           if (!pair) qb ^= 1;
           int st = base, ph = bph, no = it;   // the K chunk's stage, parity, number; its V chunk is the next
           it += 2 * nc;
-          auto step = [&](int& pos, int& parity, int by) {
-            pos += by;
-            if (pos >= S) {
-              pos -= S;
-              parity ^= 1;
-            }
-          };
           // a stage is free once both streams have read it (one, of a split tile)
           auto release = [&](int pos) {
             if (!pair) bar_arrive(&empty[pos]);
@@ -627,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
             if (pair) bar_arrive(&turn[i ^ 1]);
           };
           if (!pair && i) {
-            step(st, ph, 2);
+            ring_step(st, ph, 2, S);
             no += 2;
           }
           live = bar_wait(&q_full[seg & 1], (seg >> 1) & 1, &s_abort, c.status);
@@ -643,8 +636,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
           if (seg > 0) live = live && bar_wait(o_free, (seg & 1) ^ 1, &s_abort, c.status);
           for (int k = 0; k < mine && live; ++k) {
             int vs = st, vph = ph;
-            step(vs, vph, 1);
-            step(st, ph, pair ? 2 : 4);
+            ring_step(vs, vph, 1, S);
+            ring_step(st, ph, 2, S);
+            if (!pair) ring_step(st, ph, 2, S);
             live = copy_wait(&s_issued, no + 1, &full[vs], vph, &s_abort, c.status);
             no += pair ? 2 : 4;
             // with the next K chunk there, its scores follow PV at once
@@ -1044,10 +1038,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
 }
 
 template <int HD>
-size_t fixed_smem(int n_seq) {   // without the ring
+constexpr size_t fixed_smem(int n_seq) {   // without the ring
   return 1024 + Lay<HD>::kOffScratch + 16 * 8 + 12 * 8 + (size_t)n_seq * (sizeof(long long) + sizeof(Entry));
 }
 constexpr size_t kSmemMost = 227 * 1024 - 512;   // static shared memory aside
+// stages of the ring (128 dims: 5, beside the scratch 4, there with 53 entries and more 3)
+template <int HD>
+constexpr int ring_stages(int n_seq, int scratch) {
+  const size_t n = (kSmemMost - fixed_smem<HD>(n_seq) - scratch) / (Lay<HD>::kMat + 16);
+  return n > Lay<HD>::kStagesMost ? Lay<HD>::kStagesMost : (int)n;
+}
+// (a stream's chunk and the next one's keys)
+static_assert(ring_stages<128>(kCallSeq, kScratch) >= 3 && ring_stages<64>(kCallSeq, kScratch) >= 3, "ring too short");
 
 // The call's queries as a 3-D tensor (made per call: it names the caller's buffer).
 bool q_map(CUtensorMap* m, const AttendParams& a, uint32_t grp) {
@@ -1080,10 +1082,8 @@ cudaError_t umma_as(const AttendParams& a, const AttendWork& w, cudaStream_t st)
   const bool pairs = (long long)a.max_tree * a.grp > kWide;
   p.grp_magic = quotient_magic(grp);
   p.scratch = pairs || HD == 64 ? kScratch : 0;
-  const size_t fixed = fixed_smem<HD>(a.rows.n_seq) + p.scratch;
-  p.stages = (int)((kSmemMost - fixed) / (Lt::kMat + 16));
-  if (p.stages > Lt::kStagesMost) p.stages = Lt::kStagesMost;
-  const size_t smem = fixed + (size_t)p.stages * (Lt::kMat + 16);
+  p.stages = ring_stages<HD>(a.rows.n_seq, p.scratch);
+  const size_t smem = fixed_smem<HD>(a.rows.n_seq) + p.scratch + (size_t)p.stages * (Lt::kMat + 16);
   const cudaError_t e = launch_dependent(attend_umma_kernel<HD>, dim3(w.sms), kThreads, smem, st, p);
   if (e != cudaSuccess) return e;
   return launch_join<2, HD>(a, w, kTile, w.sms, st);

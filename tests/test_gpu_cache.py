@@ -697,6 +697,24 @@ def test_attend_most_entries(dtype):
     attend_case(c, rng, g, rng.permutation(n).tolist(), lens.tolist(), counts.tolist(), "tree", dtype)
 
 
+@pytest.mark.parametrize("hd,n", [(128, 52), (128, 53), (128, 1024), (64, 60)])
+@pytest.mark.parametrize("mask_kind", ["tree", "chain"])
+def test_attend_many_entries_of_many_chunks(hd, n, mask_kind):
+    """Entry lists that leave the kernel few ring stages (3 with heads of 128 and 53 entries),
+    tiles of more and of fewer than 128 rows, many chunks each."""
+    rng = np.random.default_rng(n + hd)
+    g = torch.Generator().manual_seed(n + hd)
+    long = min(n, 60)
+    counts, lens = rng.integers(0, 3, n), rng.integers(0, 40, n)
+    at = rng.permutation(n)[:long]
+    lens[at] = rng.integers(1500, 2700, long)
+    counts[at] = rng.choice([1, 7, 20, 33, 40, 64], long)
+    counts[at[0]], lens[at[0]] = 64, 6000
+    counts[at[1]], lens[at[1]] = 5, 9000
+    c = make(n_head=4, n_head_kv=1, head_dim=hd, page_size=64, n_pages=5000, max_seq=1024, max_pages=200)
+    attend_case(c, rng, g, rng.permutation(1024)[:n].tolist(), lens.tolist(), counts.tolist(), mask_kind, "bf16")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("hd,hq,hkv", [(128, 5, 1), (64, 40, 1), (128, 14, 2), (64, 300, 1), (32, 300, 1)], ids=str)
 def test_attend_group_sizes(dtype, hd, hq, hkv):

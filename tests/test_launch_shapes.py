@@ -1,6 +1,7 @@
 """Launch arithmetic (csrc/launch_shapes.h, plain C++) over every size, without a GPU."""
 import ctypes as C
 import pathlib
+import random
 import subprocess
 
 import pytest
@@ -43,6 +44,17 @@ extern "C" int rope_cover(int T, int items, int rd) { return cover(rope::shape_o
 extern "C" int append_cover(int T, int items, int rd) {
   return cover(rope::append_shape(T, items, rd), T, items, rd, true);
 }
+// 0: positions and parities along a ring equal those of the copy's number
+extern "C" int ring_walk(int S, int start, int steps, const int* by) {
+  int pos = start % S, parity = start / S & 1;
+  long long n = start;
+  for (int i = 0; i < steps; ++i) {
+    ring_step(pos, parity, by[i], S);
+    n += by[i];
+    if (pos != n % S || parity != (int)(n / S & 1)) return i + 1;
+  }
+  return 0;
+}
 extern "C" int append_rows(int T, int items) { return rope::append_shape(T, items, 128).rows; }
 """
 
@@ -71,3 +83,14 @@ def test_every_item_of_every_row_has_a_block(lib):
 def test_large_appends_of_one_row_a_block(lib, T, items):
     """More items than a block takes in one step (512), and a block per row."""
     assert lib.append_rows(T, items) == 1 and lib.append_cover(T, items, 128) == 0
+
+
+def test_ring_positions(lib):
+    """Steps of 1 and 2 copies, as the streams of an attention tile take them (4 as two of 2),
+    from rings of 2 stages on."""
+    rng = random.Random(0)
+    for S in range(2, 13):
+        for start in range(3 * S):
+            by = [rng.choice((1, 2)) for _ in range(200)]
+            for steps in (by, [2] * 200, [1] * 200):
+                assert lib.ring_walk(S, start, 200, (C.c_int * 200)(*steps)) == 0, (S, start)
