@@ -190,8 +190,10 @@ __global__ void __launch_bounds__(256) commit_kernel(CacheView c, RowView rows, 
   if (!bad && !path && n > 0) {
     const int k1 = (int)(((long long)len + n - 1) >> c.ps_log2);
     int gone = 0;
-    for (int k = (len >> c.ps_log2) + threadIdx.x; k <= k1; k += blockDim.x)
-      gone |= (unsigned)c.table[(size_t)q * c.max_pages + k] >= (unsigned)c.n_pages;
+    for (int k = (len >> c.ps_log2) + threadIdx.x; k <= k1; k += blockDim.x) {
+      const int page = c.table[(size_t)q * c.max_pages + k];
+      gone |= page < 0 || page >= c.n_pages || c.refs[page] > 1;   // (a shared one was not written for this sequence)
+    }
     if (__syncthreads_or(gone)) bad = DEV_BAD_PAGE;
   }
   // every thread of the block has the length

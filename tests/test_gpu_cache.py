@@ -433,6 +433,24 @@ def test_commit_refusals():
     assert c.dflash_cache_read_status() == 0x10 and torch.equal(c.table, refuse_table) and torch.equal(c.pages, before)
 
 
+def test_commit_without_a_path_refuses_shared_pages():
+    """Slots of a page that others hold too were never written by this sequence."""
+    c = make(max_seq=4, max_pages=4, page_size=16, n_pages=10)
+    c.dflash_cache_reserve(ints([40]))
+    c.dflash_cache_commit(None, ints([20]))
+    c.dflash_cache_fork(ints([0]), ints([2]))
+    for q in (0, 2):
+        c.dflash_cache_commit(None, ints([1]), seqs=ints([q]))
+        assert c.dflash_cache_read_status() == 0x10
+    c.dflash_cache_commit(None, ints([0]), seqs=ints([2]))        # nothing to keep
+    assert c.dflash_cache_read_status() == 0
+    assert c.length.cpu().tolist() == [20, 0, 20, 0]
+    c.dflash_cache_reserve(ints([5, 5]), seqs=ints([2, 0]))
+    c.dflash_cache_commit(None, ints([5, 3]), seqs=ints([2, 0]))
+    assert c.dflash_cache_read_status() == 0
+    assert c.length.cpu().tolist() == [23, 0, 25, 0]
+
+
 # ------------------------------------------------------------------ append
 
 def scattered(c, rng, seqs, lens, counts, fill=None):
