@@ -266,11 +266,12 @@ DF_DEVICE void hide(uint32_t (&v)[32], uint32_t see) {
 // gives the same quotient, as weights, sums and products are all floating point
 // (bf16 has fp32's exponents).  m starts at 0, and moves to the largest score
 // (with the accumulator rescaled once its products are done: settle()) only when
-// 64 slots' weights sum to more than 2^60 or all weights so far to less than
-// 2^-60.  So the maximum - a pass over the scores before the first exponential -
-// is not on the path: it took prompts of 2047 rows over 8192 slots from 348 to
-// 326 us.  MASKED: the row may not see every slot.  `later`: the accumulator
-// holds something.
+// all weights so far sum to more than 2^60 or to less than 2^-60.  (An accumulator
+// is then below 2^60 times the largest value, four of them from each of 160 blocks
+// below 2^70 times: values up to 2^56 stay finite.)  So the maximum - a pass over
+// the scores before the first exponential - is not on the path: it took prompts of
+// 2047 rows over 8192 slots from 348 to 326 us.  MASKED: the row may not see every
+// slot.  `later`: the accumulator holds something.
 template <int NB, int HD, bool MASKED, typename F>
 DF_DEVICE void softmax_step(const AttendParams& p, const Entry& x, int node, int slot0, int col0, uint32_t tS,
                             uint32_t tO, float scale, bool later, F settle, float& m, float& l) {
@@ -312,7 +313,7 @@ DF_DEVICE void softmax_step(const AttendParams& p, const Entry& x, int node, int
     float a0, a1;
     unpack2(add2(s2[0], s2[1]), a0, a1);
     sum = a0 + a1;
-    const bool bad = !(sum < 0x1p60f) || !(l + sum > 0x1p-60f);
+    const bool bad = !(l + sum < 0x1p60f) || !(l + sum > 0x1p-60f);
     if (again || !__any_sync(0xffffffffu, bad)) break;
     // ---- a new reference: the larger of the chunk's maximum and the sum so far
     float top = l > 0.f ? m + log2f(l) : -CUDART_INF_F;
@@ -388,7 +389,7 @@ DF_DEVICE int softmax_chunk(uint32_t tS, float scale, F told, float m, float& l)
   float a0, a1;
   unpack2(add2(s2[0], s2[1]), a0, a1);
   float sum = a0 + a1;
-  if (__any_sync(0xffffffffu, !(sum < 0x1p60f) || !(l + sum > 0x1p-60f))) return 0;
+  if (__any_sync(0xffffffffu, !(l + sum < 0x1p60f) || !(l + sum > 0x1p-60f))) return 0;
   l += sum;
   tmem_st16(tS, w[0]);
   tmem_st16(tS + 16, w[1]);
@@ -401,7 +402,7 @@ DF_DEVICE int softmax_chunk(uint32_t tS, float scale, F told, float m, float& l)
   weights(v[0], sc2, mn2, s2, w[1]);
   unpack2(add2(s2[0], s2[1]), a0, a1);
   sum = a0 + a1;
-  if (__any_sync(0xffffffffu, !(sum < 0x1p60f) || !(l + sum > 0x1p-60f))) return 1;
+  if (__any_sync(0xffffffffu, !(l + sum < 0x1p60f) || !(l + sum > 0x1p-60f))) return 1;
   l += sum;
   tmem_st16(tS + 64, w[0]);
   tmem_st16(tS + 80, w[1]);

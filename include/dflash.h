@@ -646,6 +646,8 @@ DFLASH_API int dflash_tree_mask(dflash_cache* c, int32_t n_seq, const int32_t* r
  * A row that attends to nothing gets out 0 and lse -inf.  What slots past the
  * last node hold does not matter; an infinite or NaN value of a node may reach
  * every row of its entry, whether the row attends to it or not.
+ * Weighted values are summed in fp32 relative to a reference that need not be the
+ * largest score: values of magnitude up to 2^56 give finite results.
  *   max_tree: an upper bound of the entries' node counts (<= 32 mask_words with a
  *   mask); an entry of more is skipped with DFLASH_DEV_BAD_ROWS.
  *   q, out: device [T][n_head][head_dim], strides and alignment as for

@@ -769,6 +769,41 @@ def test_attend_scores_that_grow_along_the_sequence(dtype, hd, ramp):
     attend_case(c, rng, g, [1, 0], [900, 2000], [1, 9], "tree", dtype, ramp=ramp)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hd", [32, 64, 128])
+@pytest.mark.parametrize("top,rows", [(56, 1), (56, 70), (64, 70)])
+def test_attend_large_values(dtype, hd, top, rows):
+    """Values of one sign, up to 2^56 (and, in tiles of few parts, 2^64), under scores that are
+    all far above zero, as far as a reference may lag: 64 weights come to 2^59.4.  A sum that
+    went on from there would reach 2^65 with the 66 halves of a chunk that a stream has here,
+    and with values of 2^64 leave fp32; one that stays below 2^60 is at most 2^124, two streams
+    and four parts of a tile 2^127."""
+    g = torch.Generator().manual_seed(hd)
+    hkv, n = 160, 8400
+    c = make(n_head=hkv, n_head_kv=hkv, head_dim=hd, page_size=256, n_pages=36, max_seq=1, max_pages=36, dtype=dtype,
+             attn_scale=1.0)
+    scattered(c, np.random.default_rng(hd), [0], [n], [rows], fill=float("nan"))
+    slots = n + rows
+    key = torch.zeros(slots, hd)
+    key[:, 0] = 1.0
+    data = torch.stack([key, (1 + torch.rand(slots, hd, generator=g)) * 2.0 ** (top - 1)]).to(DT[dtype])
+    table = c.table.cpu().tolist()
+    for i in range(-(-slots // 256)):
+        part = data[:, None, i * 256:(i + 1) * 256].cuda()
+        c.pages[table[0][i], 0, :, :, :part.shape[2]] = part
+    q = torch.zeros(rows, hkv, hd, dtype=DT[dtype])
+    q[..., 0] = 37.0                                      # 53.4 in powers of two
+    out, lse = torch.empty_like(q, device="cuda"), torch.empty(rows, hkv, device="cuda")
+    c.dflash_tree_attend(0, starts([rows]), rows, q.cuda(), out, lse=lse)
+    sees = np.concatenate([np.ones((rows, n), bool), np.tril(np.ones((rows, rows), bool))], 1)
+    kv = np64(data[:, :, None])
+    o, ls, size, big = R.attend(np64(q[:, :1]), kv[0], kv[1], sees, 1.0)
+    tol, tol_l = R.attend_bounds(o, size, big, slots, hd, dtype)
+    check(np64(out), np.broadcast_to(o, out.shape), np.broadcast_to(tol, out.shape))
+    check(np64(lse), np.broadcast_to(ls, lse.shape), np.broadcast_to(tol_l, lse.shape), "lse")
+    assert c.dflash_cache_read_status() == 0
+
+
 def test_attend_faults():
     D = _D()
     rng = np.random.default_rng(1)
