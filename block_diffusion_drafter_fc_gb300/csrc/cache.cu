@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kPlan) reserve_plan_kernel(CacheView c, RowVie
       len = c.length[q];
       if (cnt < 0 || len < 0 || len > c.max_pages * c.ps) bad = DEV_BAD_ROWS;
     }
-    if (bad) cnt = 0;
+    if (bad) len = cnt = 0;   // (such an entry asks for nothing, and refuses nothing to the others)
   }
   const int first = len >> c.ps_log2;
   const long long last = cnt > 0 ? ((long long)len + cnt - 1) >> c.ps_log2 : first - 1;

@@ -352,6 +352,23 @@ def test_reserve_refusals():
         c.dflash_cache_trim(ints([0] * 1025), seqs=ints([0] * 1025))
 
 
+def test_reserve_skips_a_length_out_of_range():
+    """One sequence with a length that is none does not keep the others from their pages."""
+    c = make(max_seq=4, max_pages=3, page_size=16, n_pages=9)
+    for bad in (49, 64, 2 ** 31 - 1, -1, -100):
+        c.length[1] = bad
+        c.dflash_cache_reserve(ints([20, 5, 1]), seqs=ints([0, 1, 2]))
+        assert c.dflash_cache_read_status() == 0x8
+        assert c.table.cpu().tolist() == [[0, 1, -1], [-1] * 3, [2, -1, -1], [-1] * 3]
+        assert c.refs.cpu().tolist() == [1, 1, 1] + [0] * 6
+        c.dflash_cache_trim(ints([0, 0]), seqs=ints([0, 2]))
+    c.length[1] = 48                                      # full: no room, and none asked for
+    c.dflash_cache_reserve(ints([20, 0, 1]), seqs=ints([0, 1, 2]))
+    assert c.dflash_cache_read_status() == 0
+    c.dflash_cache_reserve(ints([1]), seqs=ints([1]))
+    assert c.dflash_cache_read_status() == 0x80
+
+
 def test_fork_and_trim_refusals():
     c = make(max_seq=5, max_pages=4, page_size=16, n_pages=20)
     c.dflash_cache_reserve(ints([20, 30]))
