@@ -276,7 +276,10 @@ int dflash_cache_create(const dflash_cache_config* cfg, void* page_mem, void* st
     OnDevice on(c->device);
     unsigned long long turns[64] = {};
     if (cfg->rotary_dim > 0) rope_turns(*cfg, turns);
-    e = cudaMemset(c->scratch, 0, c->L.scratch_bytes);
+    // (the areas may be memory that work in flight on some stream still writes: an
+    // allocator hands a freed block out again in its own stream's order)
+    e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = cudaMemset(c->scratch, 0, c->L.scratch_bytes);
     if (e == cudaSuccess) e = cudaMemset(w.table, 0xff, sizeof(int32_t) * (size_t)w.max_seq * w.max_pages);
     if (e == cudaSuccess) e = cudaMemset(w.length, 0, sizeof(int32_t) * w.max_seq);
     if (e == cudaSuccess) e = cudaMemset(w.refs, 0, sizeof(int32_t) * w.n_pages);

@@ -580,7 +580,8 @@ DFLASH_API int dflash_cache_workspace_size(const dflash_cache_config* cfg, size_
                                            size_t* state_bytes, size_t* scratch_bytes);
 
 /* Build a cache handle over those areas: every sequence empty, every page free
- * (the pages' contents are left as they are).  Synchronous. */
+ * (the pages' contents are left as they are).  Synchronous, after all work that the
+ * device has so far: the areas may be memory that some of it still uses. */
 DFLASH_API int dflash_cache_create(const dflash_cache_config* cfg, void* page_mem, void* state_mem,
                                    void* scratch_mem, dflash_cache** out);
 

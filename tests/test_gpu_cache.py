@@ -1037,6 +1037,26 @@ def test_other_streams_and_two_handles():
             assert torch.equal(o, alone[k])
 
 
+def test_create_waits_for_what_its_memory_was_used_for():
+    """A cache made on a stream of its own gets blocks that this stream freed, and that work
+    in flight on it still writes: its state is that of an empty cache all the same."""
+    D = _D()
+    kw = dict(n_layer=1, n_head=4, n_head_kv=2, head_dim=64, page_size=16, n_pages=3000, max_seq=500, max_pages=1500)
+    sizes = D.cache_workspace_size(D.make_cache_config(D.CacheConfig(**kw)))
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        old = [torch.empty(n + 256, dtype=torch.uint8, device="cuda") for n in sizes]
+        at = {t.data_ptr() for t in old}
+        torch.cuda._sleep(200_000_000)
+        for t in old:
+            t.fill_(1)
+        del old, t
+        c = make(**kw)
+    assert c.state_mem.data_ptr() in at and c.scratch.data_ptr() in at
+    assert (c.table == -1).all() and not c.length.any() and not c.refs.any()
+    assert c.dflash_cache_read_status() == 0
+
+
 def test_offsets_past_32_bits():
     """Pages beyond 4 GB: append, attend and commit at the end of a large pool."""
     hd, ps = 128, 256
