@@ -410,9 +410,14 @@ class PagedCache:
 
     Tensors of rows are [T][heads][head_dim] with any row stride of a multiple of 16
     bytes (a slice of a fused projection's rows will do); row_start is int32 [n_seq + 1],
-    seqs int32 [n_seq] or None for sequences 0.., all on the cache's device."""
+    seqs int32 [n_seq] or None for sequences 0.., all on the cache's device.
+
+    A call runs on `stream`, or torch's current one.  The cache's own memory may be dropped
+    with work in flight on any of them; a caller's tensors are the caller's to keep."""
 
     device_index = -1     # before the handle: the host's
+    _areas = ()
+    _streams = frozenset()   # those of the calls so far
 
     def __init__(self, cfg, device: str = "cuda"):
         self.cfg = cfg
@@ -428,6 +433,7 @@ class PagedCache:
                what="cache_create")
         self.h = h.value
         self.device_index = self.page_mem.device.index
+        self._areas = (self.page_mem, self.state_mem, self.scratch)
         self.dtype = torch.bfloat16 if cfg.dtype == "bf16" else torch.float32
 
         def view(mem, off, shape, dt):
@@ -489,9 +495,13 @@ class PagedCache:
 
     def _on(self, stream) -> int:
         """The stream's handle (None: torch's current one of the cache's device)."""
-        if stream is not None:
-            return stream.cuda_stream
-        return _raw_stream(self.device_index)
+        h = _raw_stream(self.device_index) if stream is None else stream.cuda_stream
+        if h not in self._streams:
+            # freed areas are handed out again only once this stream is done with them
+            self._streams |= {h}
+            for area in self._areas:
+                area.record_stream(torch.cuda.ExternalStream(h, device=area.device))
+        return h
 
     # ---- C-ABI calls (same names)
     def dflash_rope(self, x, pos, out, backward: bool = False, stream=None):

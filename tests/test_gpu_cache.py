@@ -1057,6 +1057,29 @@ def test_create_waits_for_what_its_memory_was_used_for():
     assert c.dflash_cache_read_status() == 0
 
 
+@pytest.mark.parametrize("explicit", [True, False])
+def test_dropped_with_work_in_flight(explicit):
+    """A cache that goes while a call on another stream than its own waits to run: its memory
+    is not handed out before that call is done."""
+    n = 64
+    c = make(n_layer=1, n_head=4, n_head_kv=2, head_dim=64, page_size=256, n_pages=200, max_seq=2, max_pages=100)
+    c.dflash_cache_reserve(ints([n]))
+    start, kv = starts([n]), torch.ones(n, 2, 64, dtype=torch.bfloat16, device="cuda")
+    size = c.page_mem.numel()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+        if not explicit:
+            c.dflash_cache_append(0, start, kv, kv)
+    if explicit:
+        c.dflash_cache_append(0, start, kv, kv, stream=side)
+    del c
+    new = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    assert not any(t.any() for t in new)
+
+
 def test_offsets_past_32_bits():
     """Pages beyond 4 GB: append, attend and commit at the end of a large pool."""
     hd, ps = 128, 256
