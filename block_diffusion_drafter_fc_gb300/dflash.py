@@ -550,7 +550,7 @@ class PagedCache:
         rows, os_ = self._rows(out, "tree_attend", hq)
         words = lp = 0
         if mask is not None:
-            if mask.dim() != 2 or mask.shape[0] != T:
+            if mask.dim() != 2 or mask.shape[0] != T or T and not mask.shape[1]:   # (no words: a null address, a chain)
                 raise DFlashError("tree_attend: mask is int32 [T][words]")
             words = mask.shape[1]
         if rows != T:
@@ -580,7 +580,7 @@ class PagedCache:
         """path int32 [n_seq][max_path], or None: the first n_path nodes stay in place."""
         n, i, most = n_path.shape[0], self._int, 0
         if path is not None:
-            if path.dim() != 2 or path.shape[0] != n:
+            if path.dim() != 2 or path.shape[0] != n or n and not path.shape[1]:   # (a null address: no path)
                 raise DFlashError("commit: path is int32 [n_seq][max_path]")
             most = path.shape[1]
         self._ok(LIB.dflash_cache_commit(self.h, n, i("commit", seqs, n), i("commit", path, 0), most,

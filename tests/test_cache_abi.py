@@ -121,6 +121,17 @@ def test_binding_refuses_wrong_tensors():
         c.dflash_rope(x, pos, x, stream=types.SimpleNamespace(cuda_stream=0))   # no handle
 
 
+def test_binding_refuses_masks_and_paths_without_columns():
+    """An empty tensor has no address, which to the library means a chain, or no path at all."""
+    c = _binding()
+    x = torch.zeros(3, 8, 64, dtype=torch.bfloat16)
+    start = torch.tensor([0, 3], dtype=torch.int32)
+    with pytest.raises(D.DFlashError, match="words"):
+        c.dflash_tree_attend(0, start, 3, x, torch.empty_like(x), mask=torch.zeros(3, 0, dtype=torch.int32))
+    with pytest.raises(D.DFlashError, match="max_path"):
+        c.dflash_cache_commit(torch.zeros(2, 0, dtype=torch.int32), torch.zeros(2, dtype=torch.int32))
+
+
 def test_binding_refuses_tensors_of_another_device():
     c = _binding()
     c.device_index = 0
