@@ -115,8 +115,10 @@ struct Copies {
   }
 };
 
-// Dynamic shared memory of a block, two blocks per SM.
-constexpr size_t kSmemTwo = 114 * 1024 - 512;
+// Dynamic shared memory of a block, two blocks per SM: of its 228 KB each block takes 1 KB
+// more than it asks for, and up to 128 bytes of static memory.  (512 bytes more fit one
+// block only: a call of 215..236 entries with f32 heads of 128 took half as long again.)
+constexpr size_t kSmemTwo = 113 * 1024 - 128;
 constexpr int kStagesMost = 12;
 
 // Parameters of a streaming launch whose blocks have tiles of `tile`

@@ -821,6 +821,34 @@ def test_attend_large_values(dtype, hd, top, rows):
     assert c.dflash_cache_read_status() == 0
 
 
+def test_attend_f32_keeps_two_blocks_per_sm():
+    """The same work in calls of more and more entries (all but one without rows): where the
+    entries' descriptions left room for one block per SM only, a call took half as long again."""
+    c = make(n_head=16, n_head_kv=8, head_dim=128, page_size=64, n_pages=1100, max_seq=4, max_pages=1024, dtype="f32")
+    c.pages.normal_()
+    c.table[0] = torch.arange(1024, device="cuda")
+    c.length[0] = 60000
+    q = torch.randn(8, 16, 128, device="cuda")
+    out = torch.empty_like(q)
+
+    def time(n):
+        start, seqs = starts([8] + [0] * (n - 1)), ints([0] * n)
+        ts = []
+        for _ in range(12):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            c.dflash_tree_attend(0, start, 8, q, out, seqs=seqs)
+            b.record()
+            b.synchronize()
+            ts.append(a.elapsed_time(b))
+        return sorted(ts)[4]
+
+    few = time(150)
+    for n in range(200, 260, 5):
+        assert time(n) < 1.4 * few, n
+    assert c.dflash_cache_read_status() == 0
+
+
 def test_attend_faults():
     D = _D()
     rng = np.random.default_rng(1)
