@@ -6,7 +6,7 @@
 // memory: exact products, fp32 sums, pairs of them by fma.rn.f32x2.  Why not
 // mma.sync with operands split into tf32 hi + lo and three products: m16n8k8
 // keeps a scheduler busy for 32 clocks, so that leaves 43 products a clock and SM
-// of the fp32 units' 128 (238 us against 142 for four trees of 9..33 nodes over
+// of the fp32 units' 128 (238 us against 145 for four trees of 9..33 nodes over
 // 1000..4100 slots, 32 / 8 heads of 128).
 //
 // Tiles have 16 rows whatever a tree's size: a tile of 48 rows (12 warps, one

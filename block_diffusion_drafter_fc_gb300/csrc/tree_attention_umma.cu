@@ -39,7 +39,7 @@
 // halves of 64 slots, PV of the first under the softmax of the second, and the last
 // PV and the next scores are issued together.  The streams of a pair do that in
 // turn: otherwise their products interleave in the pipe, and both wait for all of
-// them (2047 rows over 8192 slots: 235 us in turn, 262 without).  Scores by halves
+// them (2047 rows over 8192 slots took 235 us in turn, 262 without; 243 now).  Scores by halves
 // too, with a buffer for each, kept both in work all the time, but 64 columns of
 // scores cost as much as 128 (both read Q): 261 us.
 // The weights are rounded to bf16 for the product with V (their sum is not):

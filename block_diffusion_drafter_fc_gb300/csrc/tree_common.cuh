@@ -299,8 +299,8 @@ DF_DEVICE int block_of(long long U, int G, long long u) { return (int)quotient((
 // ------------------------------------------------------------------ join
 
 // Rows of tiles cut by ranges: grid (blocks of the attention launch, up to 16
-// groups of four rows: 32 trees of 17..64 nodes take 91.6 us in all, 93.8 with 8
-// groups, 91.1 with 32, 93.0 with 64), a warp per row.  Part i of a tile that begins in block b0 is slot
+// groups of four rows: 32 trees of 17..64 nodes took 91.6 us in all (88 now), 93.8 with
+// 8 groups, 91.1 with 32, 93.0 with 64), a warp per row.  Part i of a tile that begins in block b0 is slot
 // 2 i of the partial rows (b0 itself: the slot its description names).  Weights
 // e^(m_i - max) are applied and summed in block order.
 template <int EL, int HD>

@@ -490,10 +490,10 @@ DFLASH_API const char* dflash_last_error(const dflash_handle* h);
  * row_start[s+1] - 1 (device int32 [n_seq + 1], ascending, within 0..T) are
  * nodes 0.. of entry s.  Entry s is sequence seqs[s] of the cache (device int32
  * [n_seq]; NULL: sequence s).  Node i of a sequence of length n occupies slot
- * n + i.  Rows outside every range are neither read nor written.  An entry
- * whose range is not within 0..T, or whose sequence is out of range, is skipped
- * and sets a status bit, as does every other fault that only the device can
- * see; no such fault makes a kernel read or write outside the handle's memory
+ * n + i.  Rows outside every range are not written, and what they hold (of q, k
+ * and v, which a call may load whole) does not matter.  An entry whose range is
+ * not within 0..T, or whose sequence is out of range, is skipped and sets a status
+ * bit, as does every other fault that only the device can see; no such fault makes a kernel read or write outside the handle's memory
  * and the buffers of the call.  Where a call changes the cache (append, commit,
  * trim, reserve), only the first entry of a sequence that is listed twice is
  * used (BAD_SEQ).
@@ -648,7 +648,10 @@ DFLASH_API int dflash_tree_mask(dflash_cache* c, int32_t n_seq, const int32_t* r
  * last node hold does not matter; an infinite or NaN value of a node may reach
  * every row of its entry, whether the row attends to it or not.
  * Weighted values are summed in fp32 relative to a reference that need not be the
- * largest score: values of magnitude up to 2^56 give finite results.
+ * largest score: values of magnitude up to 2^56 give finite results.  Scores, weights
+ * and their sum are fp32; for the product with V bf16 heads of 64 and 128 round each
+ * weight to bf16 once more (up to 2^-8 of it, independently of one another), bf16 heads
+ * of 32 keep 16 bits of it, f32 all.
  *   max_tree: an upper bound of the entries' node counts (<= 32 mask_words with a
  *   mask); an entry of more is skipped with DFLASH_DEV_BAD_ROWS.
  *   q, out: device [T][n_head][head_dim], strides and alignment as for
