@@ -497,6 +497,8 @@ class PagedCache:
         """The stream's handle (None: torch's current one of the cache's device)."""
         h = _raw_stream(self.device_index) if stream is None else stream.cuda_stream
         if h not in self._streams:
+            if h and getattr(stream, "device_index", self.device_index) != self.device_index:
+                raise DFlashError(f"a stream of device {stream.device_index}, not of the cache's")
             # freed areas are handed out again only once this stream is done with them
             self._streams |= {h}
             for area in self._areas:

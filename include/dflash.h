@@ -493,10 +493,10 @@ DFLASH_API const char* dflash_last_error(const dflash_handle* h);
  * n + i.  Rows outside every range are not written, and what they hold (of q, k
  * and v, which a call may load whole) does not matter.  An entry whose range is
  * not within 0..T, or whose sequence is out of range, is skipped and sets a status
- * bit, as does every other fault that only the device can see; no such fault makes a kernel read or write outside the handle's memory
- * and the buffers of the call.  Where a call changes the cache (append, commit,
- * trim, reserve), only the first entry of a sequence that is listed twice is
- * used (BAD_SEQ).
+ * bit, as does every other fault that only the device can see; no such fault makes
+ * a kernel read or write outside the handle's memory and the buffers of the call.
+ * Where a call changes the cache (append, commit, trim, reserve), only the first
+ * entry of a sequence that is listed twice is used (BAD_SEQ).
  *
  * The calls of one handle share its scratch area and change its state: they
  * must not overlap on the GPU (one stream, or streams ordered by events; the

@@ -121,6 +121,13 @@ def test_binding_refuses_wrong_tensors():
         c.dflash_rope(x, pos, x, stream=types.SimpleNamespace(cuda_stream=0))   # no handle
 
 
+def test_binding_refuses_streams_of_another_device():
+    c = _binding()
+    x, i = torch.zeros(3, 8, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(D.DFlashError, match="device 1"):
+        c.dflash_rope(x, i, x, stream=types.SimpleNamespace(cuda_stream=16, device_index=1))
+
+
 def test_binding_refuses_masks_and_paths_without_columns():
     """An empty tensor has no address, which to the library means a chain, or no path at all."""
     c = _binding()
