@@ -690,7 +690,8 @@ DFLASH_API int dflash_tree_accept(dflash_cache* c, int32_t n_seq, const int32_t*
  *   path: device int32 [n_seq][max_path], strictly ascending node indices (entry j
  *   at least j), or NULL: nodes 0 .. n_path[s] - 1 stay where they are (a prompt
  *   or a chain).  An entry with a path that is not so, or with slots that have no
- *   private page, is skipped (BAD_TREE, BAD_PAGE).
+ *   private page (a fork after the reserve shares the part-filled one), is skipped
+ *   (BAD_TREE, BAD_PAGE).
  */
 DFLASH_API int dflash_cache_commit(dflash_cache* c, int32_t n_seq, const int32_t* seqs,
                                    const int32_t* path, int32_t max_path, const int32_t* n_path,
