@@ -74,8 +74,34 @@ struct AppendParams {
   const char *q, *k, *v;   // q null: keys and values alone
   char* q_out;
   int64_t q_ld, q_out_ld, k_ld, v_ld;   // bytes
+  // norms of every head's queries and keys: weights [hd] (k_norm null: none), 1 / hd, epsilon
+  const char *q_norm, *k_norm;
+  float per_dim, eps;
 };
 cudaError_t launch_append(const AppendParams& p, cudaStream_t st);
+
+// Norm and rotation of T rows' query heads (part 0) and key heads (part 1), or the
+// gradient.  A part without heads has none.
+struct NormRopePart {
+  int heads;
+  const char *x, *w;        // heads [T][heads][hd], weights [hd]
+  const char* dy;           // gradient: of the result
+  char* out;                // the result, or the gradient of x
+  int64_t x_ld, dy_ld, out_ld;   // bytes
+  float* dw;                // gradient: of the weights [hd]
+};
+struct NormRopeParams {
+  RopeView r;
+  int T, hd, el;
+  const int32_t* pos;
+  float per_dim, eps;
+  NormRopePart part[2];
+  float* sums;              // gradient: [kNormBlocks][2][hd]
+  unsigned* status;
+};
+constexpr int kNormBlocks = 608;   // most blocks of a gradient's launch: 4 on each of 152 SMs
+cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t st);
+cudaError_t launch_norm_rope_grad(const NormRopeParams& p, cudaStream_t st);
 
 cudaError_t launch_tree_mask(const RowView& rows, const int32_t* parents, uint32_t* mask, int words,
                              int32_t* depth, unsigned* status, cudaStream_t st);

@@ -29,7 +29,7 @@ size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 struct Layout {
   size_t page_bytes;
   size_t table, length, refs, state_bytes;
-  size_t status, turns, tickets, free_list, copies, part_o, part_ml, cuts, scratch_bytes;
+  size_t status, turns, tickets, free_list, copies, part_o, part_ml, cuts, norm_sums, scratch_bytes;
 };
 
 int el_of(const dflash_cache_config& c) { return c.dtype == DFLASH_DTYPE_BF16 ? 2 : 4; }
@@ -57,6 +57,7 @@ Layout layout(const dflash_cache_config& c) {
   L.part_o = take(sizeof(float) * parts * c.head_dim);
   L.part_ml = take(sizeof(float2) * parts);
   L.cuts = take(sizeof(Cut) * 2 * kAttendSms);
+  L.norm_sums = take(sizeof(float) * kNormBlocks * 2 * c.head_dim);
   L.scratch_bytes = off;
   return L;
 }
@@ -330,10 +331,10 @@ int dflash_rope(dflash_cache* c, int32_t T, int32_t n_heads, const void* x, int6
   return DFLASH_OK;
 }
 
-int dflash_cache_append(dflash_cache* c, int32_t layer, int32_t n_seq, const int32_t* seqs,
-                        const int32_t* row_start, int32_t T, const int32_t* depth, const void* q,
-                        int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
-                        int64_t k_stride, const void* v, int64_t v_stride, void* stream) {
+static int append(dflash_cache* c, int32_t layer, int32_t n_seq, const int32_t* seqs, const int32_t* row_start,
+                  int32_t T, const int32_t* depth, const void* q, int64_t q_stride, void* q_out,
+                  int64_t q_out_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                  const void* q_norm, const void* k_norm, float eps, void* stream) {
   const int rc = check_call(c, n_seq, row_start, T);
   if (rc != DFLASH_OK) return rc;
   if (layer < 0 || layer >= c->cfg.n_layer || !q != !q_out) return DFLASH_ERR_INVALID_ARG;
@@ -356,7 +357,96 @@ int dflash_cache_append(dflash_cache* c, int32_t layer, int32_t n_seq, const int
   p.q_out_ld = q_out_stride * p.c.el;
   p.k_ld = k_stride * p.c.el;
   p.v_ld = v_stride * p.c.el;
+  p.q_norm = static_cast<const char*>(q_norm);
+  p.k_norm = static_cast<const char*>(k_norm);
+  p.per_dim = 1.f / c->v.hd;
+  p.eps = eps;
   DC_CHECK(c, launch_append(p, static_cast<cudaStream_t>(stream)));
+  return DFLASH_OK;
+}
+
+int dflash_cache_append(dflash_cache* c, int32_t layer, int32_t n_seq, const int32_t* seqs,
+                        const int32_t* row_start, int32_t T, const int32_t* depth, const void* q,
+                        int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
+                        int64_t k_stride, const void* v, int64_t v_stride, void* stream) {
+  return append(c, layer, n_seq, seqs, row_start, T, depth, q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride,
+                nullptr, nullptr, 0.f, stream);
+}
+
+int dflash_norm_append(dflash_cache* c, int32_t layer, int32_t n_seq, const int32_t* seqs, const int32_t* row_start,
+                       int32_t T, const int32_t* depth, float eps, const void* q, int64_t q_stride, const void* q_norm,
+                       void* q_out, int64_t q_out_stride, const void* k, int64_t k_stride, const void* k_norm,
+                       const void* v, int64_t v_stride, void* stream) {
+  if (!(eps > 0.f) || !std::isfinite(eps) || !q != !q_norm || bad_area(k_norm, 16) || (q_norm && bad_area(q_norm, 16)))
+    return DFLASH_ERR_INVALID_ARG;
+  return append(c, layer, n_seq, seqs, row_start, T, depth, q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride,
+                q_norm, k_norm, eps, stream);
+}
+
+// One part of a norm and rotation: 0 = absent, 1 = there, negative = refused.
+static int norm_part(const dflash_cache* c, NormRopePart& p, int heads, const void* x, int64_t x_stride, const void* w,
+                     const void* dy, int64_t dy_stride, void* out, int64_t out_stride, float* dw, bool grad) {
+  p = {};
+  if (!x && !w && !out && !dy && !dw) return 0;
+  if (bad_rows(c, x, x_stride, heads) || bad_rows(c, out, out_stride, heads) || bad_area(w, 16)) return DFLASH_ERR_INVALID_ARG;
+  if (grad && (bad_rows(c, dy, dy_stride, heads) || bad_area(dw, 4))) return DFLASH_ERR_INVALID_ARG;
+  const int64_t el = el_of(c->cfg);
+  p = {heads, static_cast<const char*>(x), static_cast<const char*>(w), static_cast<const char*>(dy),
+       static_cast<char*>(out), x_stride * el, dy_stride * el, out_stride * el, dw};
+  return 1;
+}
+
+static int norm_rope(dflash_cache* c, int T, const int32_t* pos, float eps, NormRopeParams& p) {
+  if (!(eps > 0.f) || !std::isfinite(eps) || !pos) return DFLASH_ERR_INVALID_ARG;
+  p.r = c->rope;
+  p.T = T;
+  p.hd = c->v.hd;
+  p.el = c->v.el;
+  p.pos = pos;
+  p.per_dim = 1.f / c->v.hd;
+  p.eps = eps;
+  p.sums = c->S<float>(c->L.norm_sums);
+  p.status = c->v.status;
+  return DFLASH_OK;
+}
+
+int dflash_norm_rope(dflash_cache* c, int32_t T, const int32_t* pos, float eps, const void* q, int64_t q_stride,
+                     const void* q_norm, void* q_out, int64_t q_out_stride, const void* k, int64_t k_stride,
+                     const void* k_norm, void* k_out, int64_t k_out_stride, void* stream) {
+  if (!c || T < 0) return DFLASH_ERR_INVALID_ARG;
+  if (T == 0) return DFLASH_OK;
+  NormRopeParams p;
+  const int a = norm_part(c, p.part[0], c->cfg.n_head, q, q_stride, q_norm, nullptr, 0, q_out, q_out_stride, nullptr, false);
+  const int b = norm_part(c, p.part[1], c->cfg.n_head_kv, k, k_stride, k_norm, nullptr, 0, k_out, k_out_stride, nullptr, false);
+  if (a < 0 || b < 0 || !(a | b)) return DFLASH_ERR_INVALID_ARG;
+  const int rc = norm_rope(c, T, pos, eps, p);
+  if (rc != DFLASH_OK) return rc;
+  OnDevice on(c->device);
+  DC_CHECK(c, launch_norm_rope(p, static_cast<cudaStream_t>(stream)));
+  return DFLASH_OK;
+}
+
+int dflash_norm_rope_grad(dflash_cache* c, int32_t T, const int32_t* pos, float eps, const void* q, int64_t q_stride,
+                          const void* q_norm, const void* dq_out, int64_t dq_out_stride, void* dq, int64_t dq_stride,
+                          float* dq_norm, const void* k, int64_t k_stride, const void* k_norm, const void* dk_out,
+                          int64_t dk_out_stride, void* dk, int64_t dk_stride, float* dk_norm, void* stream) {
+  if (!c || T < 0) return DFLASH_ERR_INVALID_ARG;
+  NormRopeParams p;
+  const int hq = c->cfg.n_head, hkv = c->cfg.n_head_kv;
+  if (T == 0) {   // sums over no rows
+    if (!dq_norm && !dk_norm) return DFLASH_OK;
+    OnDevice on(c->device);
+    for (float* dw : {dq_norm, dk_norm})
+      if (dw) DC_CHECK(c, cudaMemsetAsync(dw, 0, sizeof(float) * c->v.hd, static_cast<cudaStream_t>(stream)));
+    return DFLASH_OK;
+  }
+  const int a = norm_part(c, p.part[0], hq, q, q_stride, q_norm, dq_out, dq_out_stride, dq, dq_stride, dq_norm, true);
+  const int b = norm_part(c, p.part[1], hkv, k, k_stride, k_norm, dk_out, dk_out_stride, dk, dk_stride, dk_norm, true);
+  if (a < 0 || b < 0 || !(a | b)) return DFLASH_ERR_INVALID_ARG;
+  const int rc = norm_rope(c, T, pos, eps, p);
+  if (rc != DFLASH_OK) return rc;
+  OnDevice on(c->device);
+  DC_CHECK(c, launch_norm_rope_grad(p, static_cast<cudaStream_t>(stream)));
   return DFLASH_OK;
 }
 

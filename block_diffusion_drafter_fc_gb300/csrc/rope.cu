@@ -15,91 +15,13 @@
 // the (cos, sin) table of its rows in shared memory - shared by the rows' heads
 // - while they are in flight.  16381 rows x 20 heads of 128 f32: 52.5 us, 0.94 of the
 // copy rate; append of 8192 rows of 32 + 8 + 8 bf16 heads: 38.8 us, 0.77.
-#include "cache.cuh"
+#include "rope.cuh"
 
 namespace dflash {
 
 using namespace rope;
 
 namespace {
-
-template <int VB>
-struct Vec;
-template <>
-struct Vec<16> { using T = uint4; };
-template <>
-struct Vec<8> { using T = uint2; };
-
-template <int EL, int VB>
-DF_DEVICE void unpack(const typename Vec<VB>::T& v, float* f) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
-#pragma unroll
-  for (int i = 0; i < VB / 4; ++i) {
-    if constexpr (EL == 4) {
-      f[i] = __uint_as_float(w[i]);
-    } else {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-}
-
-template <int EL, int VB>
-DF_DEVICE typename Vec<VB>::T pack(const float* f) {
-  typename Vec<VB>::T v;
-  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-  for (int i = 0; i < VB / 4; ++i)
-    w[i] = EL == 4 ? __float_as_uint(f[i]) : pack_bf16x2(f[2 * i], f[2 * i + 1]);
-  return v;
-}
-
-// Turn the pairs of one item in place; cs: the item's (cos, sin), one per pair.
-template <int EL, int VB>
-DF_DEVICE void turn(typename Vec<VB>::T& v0, typename Vec<VB>::T& v1, const float2* cs, bool interleaved) {
-  constexpr int E = VB / EL;
-  float f[2 * E];
-  unpack<EL, VB>(v0, f);
-  unpack<EL, VB>(v1, f + E);
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float2 t = cs[e];
-    if (interleaved) {
-      const float a = f[2 * e], b = f[2 * e + 1];
-      f[2 * e] = a * t.x - b * t.y;
-      f[2 * e + 1] = b * t.x + a * t.y;
-    } else {
-      const float a = f[e], b = f[E + e];
-      f[e] = a * t.x - b * t.y;
-      f[E + e] = b * t.x + a * t.y;
-    }
-  }
-  v0 = pack<EL, VB>(f);
-  v1 = pack<EL, VB>(f + E);
-}
-
-// Element offsets of item i's two vectors within a head; true for a rotated item.
-template <int E>
-DF_DEVICE bool item_offsets(const RopeView& r, int i, int& o0, int& o1) {
-  const int n_rot = r.rd / (2 * E);
-  const bool rot = i < n_rot;
-  if (!rot || r.interleaved) {
-    o0 = i * 2 * E;
-    o1 = o0 + E;
-  } else {
-    o0 = i * E;
-    o1 = r.rd / 2 + o0;
-  }
-  return rot;
-}
-
-DF_DEVICE float2 angle(const RopeView& r, int pos, int j, bool backward) {
-  const long long t = (long long)((unsigned long long)(unsigned)pos * r.turns[j]);
-  float s, c;
-  sincospif((float)t * 0x1p-63f, &s, &c);
-  s *= r.mscale;
-  return make_float2(c * r.mscale, backward ? -s : s);
-}
 
 template <int EL, int VB, int U>
 __global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p, int rows_per_block, int span) {
@@ -154,7 +76,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p, int rows_p
 // page of its slot: five dependent loads, which a block makes for all of its rows
 // at once while its first values are in flight.  Then the block streams its
 // items, U a thread, the next U in flight while the last are turned and written.
-template <int EL, int VB, int U>
+// NORM: every q and k head is divided by its root mean square and multiplied by the
+// weights before it is turned, in registers: its lanes hold it whole.  8192 rows of 32 + 8 +
+// 8 heads: 56 us (without norms 39).
+template <int EL, int VB, int U, bool NORM>
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p, int rows_per_block, int span,
                                                           uint32_t width_magic) {
   using V = typename Vec<VB>::T;
@@ -189,6 +114,18 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p, int ro
     }
   };
   load(0, v[0]);
+  // (a thread's items are all at the same place of their heads: kThreads and a row's items
+  // are multiples of a head's)
+  V wq[2], wk[2];
+  if constexpr (NORM) {
+    int o0, o1;
+    item_offsets<E>(p.r, (sp.it0 + (int)threadIdx.x) & (ipr - 1), o0, o1);
+    const char* nq = hq ? p.q_norm : p.k_norm;
+    wq[0] = *reinterpret_cast<const V*>(nq + o0 * EL);
+    wq[1] = *reinterpret_cast<const V*>(nq + o1 * EL);
+    wk[0] = *reinterpret_cast<const V*>(p.k_norm + o0 * EL);
+    wk[1] = *reinterpret_cast<const V*>(p.k_norm + o1 * EL);
+  }
   const int lane = threadIdx.x & 31;
   const bool first = blockIdx.y == 0 && lane == 0;   // one report per row
   for (int r = threadIdx.x >> 5; r < sp.n_rows; r += kThreads / 32) {
@@ -248,12 +185,31 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p, int ro
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int g = g0 + threadIdx.x + u * kThreads;
+      float f[2 * E];
+      if constexpr (NORM) {   // (with all lanes: a head's may be the last ones of a warp)
+        unpack<EL, VB>(x[u][0], f);
+        unpack<EL, VB>(x[u][1], f + E);
+        norm_head<E>(f, ipr, p.per_dim, p.eps);
+      }
       if (g >= total) continue;
       const int r = small_quotient(g, width_magic), it = sp.it0 + g - r * width, h = it >> li, i = it - (h << li);
       if (s_pos[r] < 0) continue;
       int o0, o1;
       const bool rot = item_offsets<E>(p.r, i, o0, o1);
-      if (rot && h < hq + c.n_head_kv) turn<EL, VB>(x[u][0], x[u][1], cs + r * half + i * E, p.r.interleaved);
+      if constexpr (NORM) {
+        if (h < hq + c.n_head_kv) {
+          float w[2 * E];
+          unpack<EL, VB>(h < hq ? wq[0] : wk[0], w);
+          unpack<EL, VB>(h < hq ? wq[1] : wk[1], w + E);
+#pragma unroll
+          for (int e = 0; e < 2 * E; ++e) f[e] *= w[e];
+          if (rot) turn<E>(f, cs + r * half + i * E, p.r.interleaved);
+          x[u][0] = pack<EL, VB>(f);
+          x[u][1] = pack<EL, VB>(f + E);
+        }
+      } else if (rot && h < hq + c.n_head_kv) {
+        turn<EL, VB>(x[u][0], x[u][1], cs + r * half + i * E, p.r.interleaved);
+      }
       char* dst;
       if (h < hq) {
         dst = p.q_out + (size_t)(sp.row0 + r) * p.q_out_ld + (size_t)h * c.hd * EL;
@@ -283,14 +239,14 @@ cudaError_t rope_as(const RopeParams& p, cudaStream_t st) {
                   : launch_dependent(rope_kernel<EL, VB, 1>, grid, kThreads, s.smem, st, p, s.rows, s.span);
 }
 
-template <int EL, int VB>
+template <int EL, int VB, bool NORM>
 cudaError_t append_as(const AppendParams& p, cudaStream_t st) {
   const int heads = (p.q ? p.c.n_head : 0) + 2 * p.c.n_head_kv, items = heads * (p.c.hd / (2 * (VB / EL)));
   const Shape s = append_shape(p.rows.T, items, p.r.rd);
   const dim3 grid(s.gx, s.gy);
   const uint32_t magic = append_magic(s, items);
-  return s.u == 1 ? launch_dependent(append_kernel<EL, VB, 1>, grid, kThreads, s.smem, st, p, s.rows, s.span, magic)
-                  : launch_dependent(append_kernel<EL, VB, 2>, grid, kThreads, s.smem, st, p, s.rows, s.span, magic);
+  return s.u == 1 ? launch_dependent(append_kernel<EL, VB, 1, NORM>, grid, kThreads, s.smem, st, p, s.rows, s.span, magic)
+                  : launch_dependent(append_kernel<EL, VB, 2, NORM>, grid, kThreads, s.smem, st, p, s.rows, s.span, magic);
 }
 
 }  // namespace
@@ -303,9 +259,14 @@ cudaError_t launch_rope(const RopeParams& p, cudaStream_t st) {
   return p.r.rd % 16 == 0 ? rope_as<2, 16>(p, st) : rope_as<2, 8>(p, st);
 }
 
+template <bool NORM>
+static cudaError_t append_by_type(const AppendParams& p, cudaStream_t st) {
+  if (p.c.el == 4) return append_as<4, 16, NORM>(p, st);
+  return p.r.rd % 16 == 0 ? append_as<2, 16, NORM>(p, st) : append_as<2, 8, NORM>(p, st);
+}
+
 cudaError_t launch_append(const AppendParams& p, cudaStream_t st) {
-  if (p.c.el == 4) return append_as<4, 16>(p, st);
-  return p.r.rd % 16 == 0 ? append_as<2, 16>(p, st) : append_as<2, 8>(p, st);
+  return p.k_norm ? append_by_type<true>(p, st) : append_by_type<false>(p, st);
 }
 
 }  // namespace dflash

@@ -71,7 +71,7 @@ def _load() -> C.CDLL:
     if not LIB_PATH.exists():
         raise DFlashError(f"{LIB_PATH} is missing: build it with block_diffusion_drafter_fc_gb300.build")
     lib = C.CDLL(str(LIB_PATH))
-    vp, i32, i64, szp = C.c_void_p, C.c_int32, C.c_int64, C.POINTER(C.c_size_t)
+    vp, i32, i64, f32, szp = C.c_void_p, C.c_int32, C.c_int64, C.c_float, C.POINTER(C.c_size_t)
     sig = {
         "dflash_workspace_size": (C.c_int, [C.POINTER(dflash_config), szp, szp]),
         "dflash_create": (C.c_int, [C.POINTER(dflash_config), C.POINTER(dflash_weights), vp, vp,
@@ -107,6 +107,11 @@ def _load() -> C.CDLL:
         "dflash_rope": (C.c_int, [vp, i32, i32, vp, i64, vp, vp, i64, i32, vp]),
         "dflash_cache_append": (C.c_int, [vp, i32, i32, vp, vp, i32, vp, vp, i64, vp, i64, vp, i64,
                                           vp, i64, vp]),
+        "dflash_norm_append": (C.c_int, [vp, i32, i32, vp, vp, i32, vp, f32, vp, i64, vp, vp, i64, vp, i64,
+                                         vp, vp, i64, vp]),
+        "dflash_norm_rope": (C.c_int, [vp, i32, vp, f32, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp]),
+        "dflash_norm_rope_grad": (C.c_int, [vp, i32, vp, f32, vp, i64, vp, vp, i64, vp, i64, vp,
+                                            vp, i64, vp, vp, i64, vp, i64, vp, vp]),
         "dflash_tree_mask": (C.c_int, [vp, i32, vp, i32, vp, vp, i32, vp, vp]),
         "dflash_tree_attend": (C.c_int, [vp, i32, i32, vp, vp, i32, i32, vp, i32, vp, i64, vp, i64,
                                          vp, vp]),
@@ -535,6 +540,78 @@ class PagedCache:
             self.h, layer, n, self._int("append", seqs, n), self._int("append", row_start, 1), T,
             self._int("append", depth, T), qp, qs, qop, qos, k.data_ptr(), ks, v.data_ptr(), vs,
             self._on(stream)), "append")
+
+    def _norm(self, what: str, w) -> int:
+        """Address of a head's norm weights."""
+        if w.get_device() != self.device_index:
+            raise DFlashError(f"{what}: norm weights on {w.device}, not on the cache's device")
+        if w.dtype is not self.dtype or w.shape != (self.cfg.head_dim,) or not w.is_contiguous():
+            raise DFlashError(f"{what}: norm weights are contiguous [{self.cfg.head_dim}] {self.dtype}")
+        return w.data_ptr()
+
+    def dflash_norm_append(self, layer: int, row_start, k, v, k_norm, depth=None, q=None, q_out=None,
+                           q_norm=None, eps: float = 1e-6, seqs=None, stream=None):
+        cfg, n = self.cfg, row_start.shape[0] - 1
+        T, ks = self._rows(k, "norm_append", cfg.n_head_kv)
+        rows, vs = self._rows(v, "norm_append", cfg.n_head_kv)
+        qs = qos = qp = qop = qn = 0
+        if (q is None) != (q_out is None) or (q is None) != (q_norm is None):
+            raise DFlashError("norm_append: q, q_norm and q_out go together")
+        same = rows == T
+        if q is not None:
+            rows, qs = self._rows(q, "norm_append", cfg.n_head)
+            rows_out, qos = self._rows(q_out, "norm_append", cfg.n_head)
+            same = same and rows == T and rows_out == T
+            qp, qop, qn = q.data_ptr(), q_out.data_ptr(), self._norm("norm_append", q_norm)
+        if not same:
+            raise DFlashError("norm_append: operands have different rows")
+        i = self._int
+        self._ok(LIB.dflash_norm_append(
+            self.h, layer, n, i("norm_append", seqs, n), i("norm_append", row_start, 1), T, i("norm_append", depth, T),
+            eps, qp, qs, qn, qop, qos, k.data_ptr(), ks, self._norm("norm_append", k_norm), v.data_ptr(), vs,
+            self._on(stream)), "norm_append")
+
+    def _parts(self, what: str, T: int, heads: int, tensors, w, dw=None):
+        """Addresses and strides of a part's row tensors, weights after the first; all None: absent."""
+        if all(t is None for t in (*tensors, w)) and dw is None:
+            return None
+        if any(t is None for t in (*tensors, w)):
+            raise DFlashError(f"{what}: a part's tensors go together")
+        got = []
+        for t in tensors:
+            rows, stride = self._rows(t, what, heads)
+            if rows != T:
+                raise DFlashError(f"{what}: operands have different rows")
+            got += [t.data_ptr(), stride]
+        return got[:2] + [self._norm(what, w)] + got[2:]
+
+    def dflash_norm_rope(self, pos, q=None, q_norm=None, q_out=None, k=None, k_norm=None, k_out=None,
+                         eps: float = 1e-6, stream=None):
+        if q is None and k is None:
+            raise DFlashError("norm_rope: neither q nor k")
+        T = (k if q is None else q).shape[0]
+        a = self._parts("norm_rope", T, self.cfg.n_head, (q, q_out), q_norm) or [0] * 5
+        b = self._parts("norm_rope", T, self.cfg.n_head_kv, (k, k_out), k_norm) or [0] * 5
+        self._ok(LIB.dflash_norm_rope(self.h, T, self._int("norm_rope", pos, T), eps, *a, *b, self._on(stream)),
+                 "norm_rope")
+
+    def _sum(self, what: str, t) -> int:
+        if (t is None or t.dtype is not torch.float32 or t.shape != (self.cfg.head_dim,) or not t.is_contiguous()
+                or t.get_device() != self.device_index):
+            raise DFlashError(f"{what}: gradients of norm weights are contiguous f32 [head_dim] on the cache's device")
+        return t.data_ptr()
+
+    def dflash_norm_rope_grad(self, pos, q=None, q_norm=None, dq_out=None, dq=None, dq_norm=None, k=None,
+                              k_norm=None, dk_out=None, dk=None, dk_norm=None, eps: float = 1e-6, stream=None):
+        if q is None and k is None:
+            raise DFlashError("norm_rope_grad: neither q nor k")
+        T = (k if q is None else q).shape[0]
+        a = self._parts("norm_rope_grad", T, self.cfg.n_head, (q, dq_out, dq), q_norm, dq_norm)
+        b = self._parts("norm_rope_grad", T, self.cfg.n_head_kv, (k, dk_out, dk), k_norm, dk_norm)
+        a = a + [self._sum("norm_rope_grad", dq_norm)] if a else [0] * 8
+        b = b + [self._sum("norm_rope_grad", dk_norm)] if b else [0] * 8
+        self._ok(LIB.dflash_norm_rope_grad(self.h, T, self._int("norm_rope_grad", pos, T), eps, *a, *b,
+                                           self._on(stream)), "norm_rope_grad")
 
     def dflash_tree_mask(self, row_start, parents, mask, depth=None, stream=None):
         T, shape = parents.shape[0], mask.shape

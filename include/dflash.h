@@ -622,6 +622,51 @@ DFLASH_API int dflash_cache_append(dflash_cache* c, int32_t layer, int32_t n_seq
                                    void* stream);
 
 /*
+ * dflash_cache_append of a target whose query and key heads are normalised first:
+ * every head x of q and k becomes w * x / sqrt(mean(x^2) + eps) before it is turned
+ * (one rounding, of the result).
+ *   q_norm (with q; else NULL), k_norm: device [head_dim] in dtype, 16-byte aligned;
+ *   eps > 0; values of magnitude up to 2^60.
+ */
+DFLASH_API int dflash_norm_append(dflash_cache* c, int32_t layer, int32_t n_seq, const int32_t* seqs,
+                                  const int32_t* row_start, int32_t T, const int32_t* depth, float eps,
+                                  const void* q, int64_t q_stride, const void* q_norm, void* q_out,
+                                  int64_t q_out_stride, const void* k, int64_t k_stride, const void* k_norm,
+                                  const void* v, int64_t v_stride, void* stream);
+
+/*
+ * Norm and rotation of T rows' query and key heads in one pass:
+ *   out[t][h] = R(pos[t]) (w * x[t][h] / sqrt(mean(x[t][h]^2) + eps)),
+ * n_head heads of q with weights q_norm, n_head_kv heads of k with k_norm; q or k may be
+ * absent (all of its pointers NULL).
+ *   q, q_out: device [T][n_head][head_dim]; k, k_out: device [T][n_head_kv][head_dim],
+ *   strides and alignment as for dflash_rope; q_out may be q, k_out k.
+ *   pos, eps and weights as for dflash_rope and dflash_norm_append.
+ * A negative position sets DFLASH_DEV_BAD_POSITION and its row is not written.
+ */
+DFLASH_API int dflash_norm_rope(dflash_cache* c, int32_t T, const int32_t* pos, float eps, const void* q,
+                                int64_t q_stride, const void* q_norm, void* q_out, int64_t q_out_stride,
+                                const void* k, int64_t k_stride, const void* k_norm, void* k_out,
+                                int64_t k_out_stride, void* stream);
+
+/*
+ * The gradient of dflash_norm_rope: with g = R(pos)^T dout and n = x / sqrt(mean(x^2) + eps),
+ *   dx = (g * w - n mean(g * w * n)) / sqrt(mean(x^2) + eps)   (in dtype),
+ *   dw = sum over rows and heads of g * n                      (f32, overwritten).
+ *   q, k: dflash_norm_rope's inputs; dq_out, dk_out: gradients of its results;
+ *   dq, dk: as q_out, k_out there (each may be its own input or dout);
+ *   dq_norm, dk_norm: device f32 [head_dim].
+ * A row of a negative position (DFLASH_DEV_BAD_POSITION) is not written and not counted.
+ * Sums are taken in an order that depends on T alone.
+ */
+DFLASH_API int dflash_norm_rope_grad(dflash_cache* c, int32_t T, const int32_t* pos, float eps, const void* q,
+                                     int64_t q_stride, const void* q_norm, const void* dq_out,
+                                     int64_t dq_out_stride, void* dq, int64_t dq_stride, float* dq_norm,
+                                     const void* k, int64_t k_stride, const void* k_norm, const void* dk_out,
+                                     int64_t dk_out_stride, void* dk, int64_t dk_stride, float* dk_norm,
+                                     void* stream);
+
+/*
  * Ancestor masks of trees given by parents: bit j of mask[t] is set when node j
  * is row t's node or one of its ancestors; depth[t] counts the proper ancestors.
  *   parents: device int32 [T], the parent's node index within the row's own tree
