@@ -134,6 +134,13 @@ struct AttendParams {
   float scale;
   int grp;    // query heads per kv head
   int step;   // nodes of a tile where a chain's tiles are cut short (set by the kernels' launchers; 0: never)
+  // Shared prefixes (n_group 0: none): entries group_start[g] .. group_start[g + 1] - 1 share
+  // slots; plan[s]: slots of entry s that its group attends to for it, plan[n_seq + g]: of
+  // group g.  Rows' parts [group, entry][T][n_head] are left for the combination.
+  int n_group;
+  const int32_t *group_start, *plan;
+  float* row_o;      // [2][T][n_head][hd]
+  float2* row_ml;    // [2][T][n_head]: reference in powers of two, sum
 };
 // What a handle keeps for attention: tensor maps of the pages, scratch for the
 // partial rows of tiles that several blocks share, and a description per block
@@ -141,6 +148,7 @@ struct AttendParams {
 struct Cut {
   int lo, row0, kvh, rows;   // first row of the entry; the tile's first row, kv head, rows
   int last, slot;            // its last block (below the block itself: no such tile), the first part's slot
+  int pass;                  // the part of its rows (shared prefixes): 0 a group's, 1 an entry's
 };
 constexpr int kAttendSms = 160;        // most SMs a launch uses: 1 (tcgen05) or 2 (streaming) blocks each
 struct AttendWork {
@@ -150,6 +158,9 @@ struct AttendWork {
   Cut* cuts;          // [2 kAttendSms]
   int sms;
 };
+// plan: [n_seq + n_group] (AttendParams)
+cudaError_t launch_prefix_plan(const CacheView& c, const RowView& rows, int n_group, const int32_t* group_start,
+                               int32_t* plan, cudaStream_t st);
 bool attend_on_umma(int el, int hd);   // tcgen05 kernel, else the streaming kernel
 size_t attend_part_rows(int el, int hd);
 int attend_chunk(int el, int hd);

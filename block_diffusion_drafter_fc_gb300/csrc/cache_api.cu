@@ -464,10 +464,16 @@ int dflash_tree_mask(dflash_cache* c, int32_t n_seq, const int32_t* row_start, i
   return DFLASH_OK;
 }
 
-int dflash_tree_attend(dflash_cache* c, int32_t layer, int32_t n_seq, const int32_t* seqs,
-                       const int32_t* row_start, int32_t T, int32_t max_tree, const uint32_t* mask,
-                       int32_t mask_words, const void* q, int64_t q_stride, void* out, int64_t out_stride,
-                       float* lse, void* stream) {
+// Bytes of a call's parts of sums, before those of its references.
+static size_t prefix_ml(const dflash_cache* c, int T) {
+  return up(sizeof(float) * 2 * (size_t)T * c->cfg.n_head * c->cfg.head_dim);
+}
+
+// n_group 0: no shared prefixes.
+static int attend(dflash_cache* c, int32_t layer, int32_t n_seq, const int32_t* seqs, const int32_t* row_start,
+                  int32_t T, int32_t max_tree, const uint32_t* mask, int32_t mask_words, int32_t n_group,
+                  const int32_t* group_start, const int32_t* plan, void* work, const void* q, int64_t q_stride,
+                  void* out, int64_t out_stride, float* lse, void* stream) {
   const int rc = check_call(c, n_seq, row_start, T);
   if (rc != DFLASH_OK) return rc;
   if (layer < 0 || layer >= c->cfg.n_layer || max_tree < 1) return DFLASH_ERR_INVALID_ARG;
@@ -492,9 +498,56 @@ int dflash_tree_attend(dflash_cache* c, int32_t layer, int32_t n_seq, const int3
   p.lse = lse;
   p.grp = hq / c->cfg.n_head_kv;
   p.step = 0;
+  p.n_group = n_group;
+  p.group_start = group_start;
+  p.plan = plan;
+  p.row_o = static_cast<float*>(work);
+  p.row_ml = n_group ? reinterpret_cast<float2*>(static_cast<char*>(work) + prefix_ml(c, T)) : nullptr;
   p.scale = c->cfg.attn_scale != 0.f ? c->cfg.attn_scale : (float)(1.0 / std::sqrt((double)c->cfg.head_dim));
   DC_CHECK(c, launch_attend(p, c->work, static_cast<cudaStream_t>(stream)));
   return DFLASH_OK;
+}
+
+int dflash_tree_attend(dflash_cache* c, int32_t layer, int32_t n_seq, const int32_t* seqs,
+                       const int32_t* row_start, int32_t T, int32_t max_tree, const uint32_t* mask,
+                       int32_t mask_words, const void* q, int64_t q_stride, void* out, int64_t out_stride,
+                       float* lse, void* stream) {
+  return attend(c, layer, n_seq, seqs, row_start, T, max_tree, mask, mask_words, 0, nullptr, nullptr, nullptr, q, q_stride,
+                out, out_stride, lse, stream);
+}
+
+static int check_groups(const dflash_cache* c, int n_seq, int n_group, const int32_t* group_start, const int32_t* plan) {
+  if (!c || n_group < 1 || !group_start || !plan) return DFLASH_ERR_INVALID_ARG;
+  if (n_seq < 0 || (int64_t)n_seq + n_group > kCallSeq) return DFLASH_ERR_SEQ_RANGE;
+  return DFLASH_OK;
+}
+
+int dflash_prefix_plan(dflash_cache* c, int32_t n_seq, const int32_t* seqs, int32_t n_group,
+                       const int32_t* group_start, int32_t* plan, void* stream) {
+  const int rc = check_groups(c, n_seq, n_group, group_start, plan);
+  if (rc != DFLASH_OK) return rc;
+  OnDevice on(c->device);
+  DC_CHECK(c, launch_prefix_plan(c->v, {n_seq, seqs, nullptr, 0}, n_group, group_start, plan,
+                                 static_cast<cudaStream_t>(stream)));
+  return DFLASH_OK;
+}
+
+int dflash_prefix_workspace_size(const dflash_cache* c, int32_t T, size_t* bytes) {
+  if (!c || T < 0 || !bytes) return DFLASH_ERR_INVALID_ARG;
+  *bytes = prefix_ml(c, T) + up(sizeof(float2) * 2 * (size_t)T * c->cfg.n_head);
+  return DFLASH_OK;
+}
+
+int dflash_prefix_attend(dflash_cache* c, int32_t layer, int32_t n_seq, const int32_t* seqs,
+                         const int32_t* row_start, int32_t T, int32_t max_tree, const uint32_t* mask,
+                         int32_t mask_words, int32_t n_group, const int32_t* group_start, const int32_t* plan,
+                         void* work, const void* q, int64_t q_stride, void* out, int64_t out_stride, float* lse,
+                         void* stream) {
+  const int rc = check_groups(c, n_seq, n_group, group_start, plan);
+  if (rc != DFLASH_OK) return rc;
+  if (n_seq > 0 && T > 0 && bad_area(work, kAlign)) return DFLASH_ERR_INVALID_ARG;
+  return attend(c, layer, n_seq, seqs, row_start, T, max_tree, mask, mask_words, n_group, group_start, plan, work, q,
+                q_stride, out, out_stride, lse, stream);
 }
 
 int dflash_tree_accept(dflash_cache* c, int32_t n_seq, const int32_t* row_start, int32_t T,

@@ -1,0 +1,76 @@
+// Shared prefixes of a call's entries (the attention over them: tree_common.cuh).
+//
+// Sequences that were forked from one another hold the same pages for as long as their
+// beginnings are full pages, so a group's common slots are found in the page table: no
+// promise of the caller's is needed, and a wrong group only shares less.
+#include "cache.cuh"
+
+namespace dflash {
+
+namespace {
+
+constexpr int kPlanThreads = 256;
+
+// A block per group.  The group shares the full pages, below the least length, in which no
+// member's row of the table differs from the first's.  Bound: latency, five dependent loads.
+__global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(CacheView c, RowView rows, int n_group,
+                                                                   const int32_t* group_start, int32_t* plan) {
+  __shared__ int s_pages;
+  pdl_trigger();
+  pdl_wait();
+  const int g = blockIdx.x, tid = threadIdx.x, n = rows.n_seq;
+  // group ranges that are none: nothing is shared
+  int bad = 0;
+  for (int i = tid; i < n_group; i += kPlanThreads) {
+    const int a = group_start[i], b = group_start[i + 1];
+    bad |= a < 0 || a > b || b > n;
+  }
+  if (tid == 0) s_pages = 0x7fffffff;
+  if (__syncthreads_or(bad)) {
+    if (g == 0) {
+      for (int i = tid; i < n + n_group; i += kPlanThreads) plan[i] = 0;
+      if (tid == 0) set_status(c.status, DEV_BAD_ROWS);
+    }
+    return;
+  }
+  const int e0 = group_start[g], e1 = group_start[g + 1], members = e1 - e0;
+  // entries of no group
+  if (g == 0)
+    for (int i = tid; i < e0; i += kPlanThreads) plan[i] = 0;
+  if (g == n_group - 1)
+    for (int i = e1 + tid; i < n; i += kPlanThreads) plan[i] = 0;
+  int pages = 0x7fffffff;
+  for (int i = tid; i < members; i += kPlanThreads) {
+    const int q = entry_sequence(rows, e0 + i, c.max_seq), len = q >= 0 ? c.length[q] : -1;
+    pages = min(pages, len < 0 ? 0 : min(len >> c.ps_log2, c.max_pages));
+  }
+  atomicMin(&s_pages, pages);
+  __syncthreads();
+  pages = members > 1 ? s_pages : 0;
+  __syncthreads();
+  if (pages > 0) {
+    const int32_t* first = c.table + (size_t)entry_sequence(rows, e0, c.max_seq) * c.max_pages;
+    // (members of a warp's own: its lanes follow the member's row of the table)
+    int same = pages;
+    for (int i = 1 + (tid >> 5); i < members; i += kPlanThreads / 32) {
+      const int32_t* mine = c.table + (size_t)entry_sequence(rows, e0 + i, c.max_seq) * c.max_pages;
+      for (int p = tid & 31; p < same; p += 32)
+        if (mine[p] != first[p]) same = p;
+    }
+    if (same < pages) atomicMin(&s_pages, same);
+    __syncthreads();
+    pages = s_pages;
+  }
+  const int shared = pages << c.ps_log2;
+  for (int i = tid; i < members; i += kPlanThreads) plan[e0 + i] = shared;
+  if (tid == 0) plan[n + g] = shared;
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_plan(const CacheView& c, const RowView& rows, int n_group, const int32_t* group_start,
+                               int32_t* plan, cudaStream_t st) {
+  return launch_dependent(prefix_plan_kernel, dim3(n_group), kPlanThreads, 0, st, c, rows, n_group, group_start, plan);
+}
+
+}  // namespace dflash

@@ -41,7 +41,7 @@ DF_DEVICE void ldsm4t(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
-template <int HD, int MT>
+template <int HD, int MT, typename E>
 __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid_constant__ StreamParams p) {
   constexpr int EL = 2;
   using G = Geo<EL, HD>;
@@ -58,7 +58,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
   uint64_t* empty = full + S;
   long long* s_warp = reinterpret_cast<long long*>(empty + S);            // [8]
   long long* s_end = s_warp + 8;
-  Entry* s_e = reinterpret_cast<Entry*>(s_end + p.a.rows.n_seq);
+  const int entries = E::count(p.a);
+  E* s_e = reinterpret_cast<E*>(s_end + entries);
   __shared__ volatile int s_abort;
 
   const CacheView& c = p.a.c;
@@ -75,19 +76,19 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
   pdl_wait();
   plan_entries(p.a, cutting<EL>(TR), s_e, s_end, s_warp, kThreads, blockIdx.x == 0);
   __syncthreads();
-  const long long U = s_end[p.a.rows.n_seq - 1];
+  const long long U = s_end[entries - 1];
   // fewer blocks than launched where their shares would get too small
   const int Gr = blocks_used(U, gridDim.x, kMinUnits), b = blockIdx.x;
-  Cut d = {0, 0, 0, 0, -1, 0};
+  Cut d = {0, 0, 0, 0, -1, 0, 0};
   if (b >= Gr || U == 0) {
     if (tid == 0) p.cuts[b] = d;
     return;
   }
   const long long ub0 = range_begin(U, Gr, b), ub1 = range_begin(U, Gr, b + 1);
-  const int s_first = find_entry(s_end, p.a.rows.n_seq, ub0);
+  const int s_first = find_entry(s_end, entries, ub0);
   const int grp = p.a.grp;
 
-  Copies<EL, HD> cp;
+  Copies<EL, HD, E> cp;
   cp.u = ub0;
   cp.s = s_first;
   if (warp == 0) {
@@ -102,9 +103,9 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
   int s = s_first, it = 0;
   Segment g;
   while (next_segment(p.a, cutting<EL>(TR), s_e, s_end, u, ub1, s, g)) {
-    const Entry x = s_e[g.s];
-    const int rows = min(TR, x.n * grp - g.row0), end = x.len + x.n;
-    const int all = x.len + (p.a.mask ? 0 : g.row0 / grp + 1);   // slots that all rows see
+    const E x = s_e[g.s];
+    const int rows = min(TR, x.n * grp - g.row0), end = x.len + x.nodes();
+    const int all = x.len + (p.a.mask || !x.nodes() ? 0 : g.row0 / grp + 1);   // slots that all rows see
     // Q: row r is head kvh grp + (row0 + r) % grp of node (row0 + r) / grp
     __syncthreads();   // the previous tile's Q and sums have been read
     for (int i = tid; i < TR * (G::kRowB / 16); i += 32 * kConsumers) {
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
     }
     constexpr int NS = G::WS / 8;             // 8-slot blocks of the warp's slots
     for (int ch = g.c0; ch < g.c1; ++ch) {
-      const int slot0 = ch * G::CS + warp * G::WS;
+      const int slot0 = x.base() + ch * G::CS + warp * G::WS;
       // ---- scores
       float sc[MT][NS][4];
 #pragma unroll
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
         for (int hf = 0; hf < 2; ++hf) {
           const int r = t * 16 + hf * 8 + gr;
           if (r >= rows) continue;
-          if (whole) {
+          if (!E::kParts && whole) {
             const float inv = l[t][hf] > 0.f ? 1.f / l[t][hf] : 0.f;
             char* dst;
             float* lse;
@@ -322,8 +323,11 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
               *reinterpret_cast<uint32_t*>(dst + (j * 8 + qd * 2) * 2) = pack_bf16x2(a, bb);
             }
           } else {
-            float* po = p.part_o + ((size_t)slot * TR + r) * HD;
-            if (qd == 0) p.part_ml[(size_t)slot * TR + r] = make_float2(m[t][hf], l[t][hf]);
+            const int node = (g.row0 + r) / grp;
+            const size_t at = E::kParts && whole ? part_row(p.a, x.pass(), x.lo + node, g.kvh * grp + g.row0 + r - node * grp)
+                                                 : (size_t)slot * TR + r;
+            float* po = (E::kParts && whole ? p.a.row_o : p.part_o) + at * HD;
+            if (qd == 0) (E::kParts && whole ? p.a.row_ml : p.part_ml)[at] = make_float2(m[t][hf], l[t][hf]);
 #pragma unroll
             for (int j = 0; j < NV; ++j)
               *reinterpret_cast<float2*>(po + j * 8 + qd * 2) = make_float2(o[t][j][hf * 2], o[t][j][hf * 2 + 1]);
@@ -338,30 +342,31 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
       d.rows = rows;
       d.last = block_of(U, Gr, g.u0 + (long long)(g.nch - 1) * g.w);
       d.slot = slot;
+      d.pass = x.pass();
     }
   }
   if (warp == 0) cp.drain(S, full);
   if (tid == 0) p.cuts[b] = d;
 }
 
-template <int HD, int MT>
-size_t fixed_smem(int n_seq) {
+template <int HD, int MT, typename E>
+size_t fixed_smem(int entries) {
   return 1024 + 16 * MT * HD * 2 + 2 * 16 * HD * 4 + 32 * 8 + 8 * 8 +
-         (size_t)n_seq * (sizeof(long long) + sizeof(Entry));
+         (size_t)entries * (sizeof(long long) + sizeof(E));
 }
 
-template <int HD, int MT>
+template <int HD, int MT, typename E>
 cudaError_t stream_as(const AttendParams& a, const AttendWork& w, cudaStream_t st) {
   size_t smem;
-  const StreamParams p = stream_params<2, HD>(a, w, 16 * MT, fixed_smem<HD, MT>(a.rows.n_seq), smem);
-  const cudaError_t e = launch_dependent(attend_stream_kernel<HD, MT>, dim3(2 * w.sms), kThreads, smem, st, p);
+  const StreamParams p = stream_params<2, HD>(a, w, 16 * MT, fixed_smem<HD, MT, E>(a.n_group + a.rows.n_seq), smem);
+  const cudaError_t e = launch_dependent(attend_stream_kernel<HD, MT, E>, dim3(2 * w.sms), kThreads, smem, st, p);
   if (e != cudaSuccess) return e;
-  return launch_join<2, HD>(a, w, 16 * MT, 2 * w.sms, st);
+  return launch_join<2, HD, E>(a, w, 16 * MT, 2 * w.sms, st);
 }
 
-template <int HD, int MT>
+template <int HD, int MT, typename E>
 cudaError_t raise_smem() {
-  return cudaFuncSetAttribute(attend_stream_kernel<HD, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemTwo);
+  return cudaFuncSetAttribute(attend_stream_kernel<HD, MT, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemTwo);
 }
 
 }  // namespace
@@ -376,17 +381,21 @@ size_t attend_part_rows(int el, int hd) { return 2 * (size_t)kAttendSms * (atten
 cudaError_t configure_attend() {
   cudaError_t e = configure_attend_umma();
   if (e == cudaSuccess) e = configure_attend_f32();
-  if (e == cudaSuccess) e = raise_smem<32, 1>();
-  if (e == cudaSuccess) e = raise_smem<32, 2>();
+  if (e == cudaSuccess) e = raise_smem<32, 1, Entry>();
+  if (e == cudaSuccess) e = raise_smem<32, 2, Entry>();
+  if (e == cudaSuccess) e = raise_smem<32, 1, PartEntry>();
+  if (e == cudaSuccess) e = raise_smem<32, 2, PartEntry>();
   return e;
 }
 
 cudaError_t launch_attend(const AttendParams& a, const AttendWork& w, cudaStream_t st) {
   if (a.c.el == 4) return launch_attend_f32(a, w, st);
   if (attend_on_umma(a.c.el, a.c.hd)) return launch_attend_umma(a, w, st);
-  // 32-row tiles once a call has entries of more than 16 rows per kv head
+  // 32-row tiles once a call has entries (groups) of more than 16 rows per kv head
+  if (a.n_group)
+    return (long long)a.rows.T * a.grp <= 16 ? stream_as<32, 1, PartEntry>(a, w, st) : stream_as<32, 2, PartEntry>(a, w, st);
   const long long rows = (long long)a.max_tree * a.grp;
-  return rows <= 16 ? stream_as<32, 1>(a, w, st) : stream_as<32, 2>(a, w, st);
+  return rows <= 16 ? stream_as<32, 1, Entry>(a, w, st) : stream_as<32, 2, Entry>(a, w, st);
 }
 
 }  // namespace dflash

@@ -68,7 +68,7 @@ constexpr int TR = 16;                       // rows of a tile
 constexpr int kAll = kThreads + 32;          // one warp more copies
 constexpr int kPerSm = 2;                    // blocks per SM
 
-template <int HD>
+template <int HD, typename E>
 __global__ void __launch_bounds__(kAll, kPerSm) attend_f32_kernel(const __grid_constant__ StreamParams p) {
   using G = Geo<4, HD>;
   constexpr int NS = G::WS / 2;                 // slots of a lane in the products with K (x 4 rows)
@@ -86,7 +86,8 @@ __global__ void __launch_bounds__(kAll, kPerSm) attend_f32_kernel(const __grid_c
   uint64_t* empty = full + S;
   long long* s_warp = reinterpret_cast<long long*>(empty + S);          // [16]
   long long* s_end = s_warp + 16;
-  Entry* s_e = reinterpret_cast<Entry*>(s_end + p.a.rows.n_seq);
+  const int entries = E::count(p.a);
+  E* s_e = reinterpret_cast<E*>(s_end + entries);
   float* s_o = reinterpret_cast<float*>(s_q);   // [TR][HD], once the tile's scores are done
   __shared__ volatile int s_abort;
 
@@ -104,18 +105,18 @@ __global__ void __launch_bounds__(kAll, kPerSm) attend_f32_kernel(const __grid_c
   pdl_wait();
   plan_entries(p.a, cutting<4>(TR), s_e, s_end, s_warp, kAll, blockIdx.x == 0);
   __syncthreads();
-  const long long U = s_end[p.a.rows.n_seq - 1];
+  const long long U = s_end[entries - 1];
   const int Gr = blocks_used(U, gridDim.x, kMinUnits), b = blockIdx.x;
-  Cut d = {0, 0, 0, 0, -1, 0};
+  Cut d = {0, 0, 0, 0, -1, 0, 0};
   if (b >= Gr || U == 0) {
     if (tid == 0) p.cuts[b] = d;
     return;
   }
   const long long ub0 = range_begin(U, Gr, b), ub1 = range_begin(U, Gr, b + 1);
-  const int s_first = find_entry(s_end, p.a.rows.n_seq, ub0);
+  const int s_first = find_entry(s_end, entries, ub0);
   const int grp = p.a.grp;
   if (warp == kConsumers) {
-    Copies<4, HD> cp;
+    Copies<4, HD, E> cp;
     cp.u = ub0;
     cp.s = s_first;
     cp.open(p, s_e, s_end, ub1, TR);
@@ -147,9 +148,9 @@ __global__ void __launch_bounds__(kAll, kPerSm) attend_f32_kernel(const __grid_c
   };
   Segment g;
   while (next_segment(p.a, cutting<4>(TR), s_e, s_end, u, ub1, s, g)) {
-    const Entry x = s_e[g.s];
-    const int rows = min(TR, x.n * grp - g.row0), end = x.len + x.n;
-    const int all = x.len + (p.a.mask ? 0 : g.row0 / grp + 1);   // slots that all rows see
+    const E x = s_e[g.s];
+    const int rows = min(TR, x.n * grp - g.row0), end = x.len + x.nodes(), slots0 = x.base();
+    const int all = x.len + (p.a.mask || !x.nodes() ? 0 : g.row0 / grp + 1);   // slots that all rows see
     sync_tile<kThreads>();   // the previous tile's sums have been read
     for (int i = tid; i < TR * (G::kRowB / 16); i += kThreads) {
       const int r = i / (G::kRowB / 16), pc = i - r * (G::kRowB / 16);
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kAll, kPerSm) attend_f32_kernel(const __grid_c
       for (int k = 0; k < NX; ++k) o[r][k][0] = o[r][k][1] = 0;
 
     for (int ch = g.c0; ch < g.c1; ++ch) {
-      const int slot0 = ch * G::CS + warp * G::WS;
+      const int slot0 = slots0 + ch * G::CS + warp * G::WS;
       // ---- scores
       bar_wait(&full[st], (uint32_t)ph, &s_abort, c.status);
       uint64_t acc[4][NS];
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kAll, kPerSm) attend_f32_kernel(const __grid_c
         const float2 y = s_ml[k * TR + pr + r];
         sum += ex2(y.x - use) * y.y;
       }
-      wt[r] = ex2(s_ml[warp * TR + pr + r].x - use) * (!whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f);
+      wt[r] = ex2(s_ml[warp * TR + pr + r].x - use) * (E::kParts || !whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f);
     }
 #pragma unroll 1
     for (int k0 = 0; k0 < kConsumers; ++k0) {
@@ -321,45 +322,55 @@ __global__ void __launch_bounds__(kAll, kPerSm) attend_f32_kernel(const __grid_c
       const int r = i / (HD / 4), pc = i - r * (HD / 4);
       const float4 y = *reinterpret_cast<const float4*>(s_o + r * HD + pc * 4);
       const int node = (g.row0 + r) / grp, h = g.kvh * grp + (g.row0 + r) - node * grp;
-      if (whole)
+      const size_t at = E::kParts && whole ? part_row(p.a, x.pass(), x.lo + node, h) : (size_t)slot * TR + r;
+      if (!E::kParts && whole)
         *reinterpret_cast<float4*>(p.a.out + (size_t)(x.lo + node) * p.a.out_ld + (size_t)h * G::kRowB + pc * 16) = y;
       else
-        *reinterpret_cast<float4*>(p.part_o + ((size_t)slot * TR + r) * HD + pc * 4) = y;
+        *reinterpret_cast<float4*>((E::kParts && whole ? p.a.row_o : p.part_o) + at * HD + pc * 4) = y;
       if (pc) continue;
       float top = -CUDART_INF_F, sum = 0.f;
       for (int k = 0; k < kConsumers; ++k) top = fmaxf(top, s_ml[k * TR + r].x);
       const float use = top == -CUDART_INF_F ? 0.f : top;
       for (int k = 0; k < kConsumers; ++k) sum += ex2(s_ml[k * TR + r].x - use) * s_ml[k * TR + r].y;
-      if (!whole)
-        p.part_ml[(size_t)slot * TR + r] = make_float2(top, sum);
+      if (E::kParts || !whole)
+        (E::kParts && whole ? p.a.row_ml : p.part_ml)[at] = make_float2(top, sum);
       else if (p.a.lse)
         p.a.lse[(size_t)(x.lo + node) * c.n_head + h] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -CUDART_INF_F;
     }
     // the block with a cut tile's first chunk describes it to the join
     if (tid == 0 && g.c0 == 0 && !whole)
-      d = {x.lo, g.row0, g.kvh, rows, block_of(U, Gr, g.u0 + (long long)(g.nch - 1) * g.w), slot};
+      d = {x.lo, g.row0, g.kvh, rows, block_of(U, Gr, g.u0 + (long long)(g.nch - 1) * g.w), slot,
+           x.pass()};
   }
   if (tid == 0) p.cuts[b] = d;
 }
 
-template <int HD>
-size_t fixed_smem(int n_seq) {
+template <int HD, typename E>
+size_t fixed_smem(int entries) {
   return 1024 + TR * HD * 4 + kConsumers * (Geo<4, HD>::WS * kPad + 16) * 4 + kConsumers * TR * 8 + 16 * 8 +
-         (size_t)n_seq * (sizeof(long long) + sizeof(Entry));
+         (size_t)entries * (sizeof(long long) + sizeof(E));
 }
 
-template <int HD>
+template <int HD, typename E>
 cudaError_t f32_as(const AttendParams& a, const AttendWork& w, cudaStream_t st) {
   size_t smem;
-  const StreamParams p = stream_params<4, HD>(a, w, TR, fixed_smem<HD>(a.rows.n_seq), smem);
-  const cudaError_t e = launch_dependent(attend_f32_kernel<HD>, dim3(kPerSm * w.sms), kAll, smem, st, p);
+  const StreamParams p = stream_params<4, HD>(a, w, TR, fixed_smem<HD, E>(a.n_group + a.rows.n_seq), smem);
+  const cudaError_t e = launch_dependent(attend_f32_kernel<HD, E>, dim3(kPerSm * w.sms), kAll, smem, st, p);
   if (e != cudaSuccess) return e;
-  return launch_join<4, HD>(a, w, TR, kPerSm * w.sms, st);
+  return launch_join<4, HD, E>(a, w, TR, kPerSm * w.sms, st);
 }
 
 template <int HD>
 cudaError_t raise_smem() {
-  return cudaFuncSetAttribute(attend_f32_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemTwo);
+  const cudaError_t e = cudaFuncSetAttribute(attend_f32_kernel<HD, Entry>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)kSmemTwo);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(attend_f32_kernel<HD, PartEntry>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemTwo);
+}
+
+template <typename E>
+cudaError_t f32_by_head(const AttendParams& a, const AttendWork& w, cudaStream_t st) {
+  return a.c.hd == 32 ? f32_as<32, E>(a, w, st) : a.c.hd == 64 ? f32_as<64, E>(a, w, st) : f32_as<128, E>(a, w, st);
 }
 
 }  // namespace
@@ -372,7 +383,7 @@ cudaError_t configure_attend_f32() {
 }
 
 cudaError_t launch_attend_f32(const AttendParams& a, const AttendWork& w, cudaStream_t st) {
-  return a.c.hd == 32 ? f32_as<32>(a, w, st) : a.c.hd == 64 ? f32_as<64>(a, w, st) : f32_as<128>(a, w, st);
+  return a.n_group ? f32_by_head<PartEntry>(a, w, st) : f32_by_head<Entry>(a, w, st);
 }
 
 }  // namespace dflash

@@ -202,10 +202,11 @@ struct UmmaParams {
 
 // Bit j: the row sees slot `slot` + j.  (Plain loads: a dependent launch may start
 // before the kernel that writes the mask has ended, which the read-only path excludes.)
-DF_DEVICE uint32_t visible(const AttendParams& p, const Entry& x, int node, int slot) {
+template <typename E>
+DF_DEVICE uint32_t visible(const AttendParams& p, const E& x, int node, int slot) {
   const int a = slot - x.len;                    // node index of bit 0
   if (a <= -32) return ~0u;
-  const int valid = x.n - a;                     // bits below it are slots of the entry
+  const int valid = x.nodes() - a;               // bits below it are slots of the entry
   uint32_t v;
   if (!p.mask) {
     const int c = node - a + 1;
@@ -225,7 +226,8 @@ DF_DEVICE uint32_t visible(const AttendParams& p, const Entry& x, int node, int 
 }
 
 // The mask words of the 128 slots from `slot` on, into L1 ahead of their use.
-DF_DEVICE void prefetch_mask(const AttendParams& p, const Entry& x, int node, int slot) {
+template <typename E>
+DF_DEVICE void prefetch_mask(const AttendParams& p, const E& x, int node, int slot) {
   const int k = max(slot - x.len, 0) >> 5;
   if (k >= p.words) return;
   const uint32_t* w = p.mask + (size_t)(x.lo + node) * p.words;
@@ -272,8 +274,8 @@ DF_DEVICE void hide(uint32_t (&v)[32], uint32_t see) {
 // the scores before the first exponential - is not on the path: it took prompts of
 // 2047 rows over 8192 slots from 348 to 326 us.  MASKED: the row may not see every
 // slot.  `later`: the accumulator holds something.
-template <int NB, int HD, bool MASKED, typename F>
-DF_DEVICE void softmax_step(const AttendParams& p, const Entry& x, int node, int slot0, int col0, uint32_t tS,
+template <int NB, int HD, bool MASKED, typename E, typename F>
+DF_DEVICE void softmax_step(const AttendParams& p, const E& x, int node, int slot0, int col0, uint32_t tS,
                             uint32_t tO, float scale, bool later, F settle, float& m, float& l) {
   uint32_t w[NB][16];
   float sum;
@@ -416,8 +418,9 @@ struct Int { static constexpr int value = N; };
 
 // A segment (a run of a tile's chunks), planned by one warp for all: the
 // arithmetic that finds it, and its instructions, are paid for once.
+template <typename E>
 struct SegDesc {
-  Entry x;
+  E x;
   int kvh, row0, left;   // kv head, first row, rows of the tile
   int node0, h0;         // node and query head of row 0
   int c0, nc;            // first chunk, chunks
@@ -442,7 +445,7 @@ DF_DEVICE bool seg_wait(int* planned, int* total, int seg, volatile int* abort, 
   }
 }
 
-template <int HD>
+template <int HD, typename E>
 __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_constant__ UmmaParams p) {
   using Lt = Lay<HD>;
   constexpr int kMat = Lt::kMat, kHalf = Lt::kHalf, kHalves = Lt::kHalves;
@@ -462,8 +465,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
   uint64_t* o_free = o_full + 1;     // the segment's O has been read
   long long* s_warp = reinterpret_cast<long long*>(o_free + 1);   // [12]
   long long* s_end = s_warp + 12;
-  Entry* s_e = reinterpret_cast<Entry*>(s_end + p.a.rows.n_seq);
-  __shared__ SegDesc s_seg[kSegs];
+  const int entries = E::count(p.a);
+  E* s_e = reinterpret_cast<E*>(s_end + entries);
+  __shared__ SegDesc<E> s_seg[kSegs];
   __shared__ uint32_t s_tmem;
   __shared__ int s_issued;           // copies issued so far
   __shared__ int s_planned, s_total; // segments planned so far; all of them, once known
@@ -511,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
   // Few entries: warp 11 plans alone, and the roles wait for the launch before this
   // one where their instructions are, which are then there when it ends (together
   // with less to divide: 16 nodes over 2048 slots 16.4 us instead of 17.6).
-  const bool few = p.a.rows.n_seq <= 32;
+  const bool few = entries <= 32;
   if (!few) {
     pdl_wait();
     plan_entries(p.a, cutting(), s_e, s_end, s_warp, kThreads, b == 0);
@@ -524,15 +528,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       const int none = c.n_pages * c.n_layer * 2 * c.n_head_kv;   // past the tensor: reads as zero
       int st = 0, ph = 1, n = 0, stop = 0;   // ring position, parity of its empty barrier, copies issued
       for (int seg = 0; !stop && seg_wait(&s_planned, &s_total, seg, &s_abort, c.status); ++seg) {
-        const SegDesc& d = s_seg[seg % kSegs];
-        const Entry x = d.x;
+        const SegDesc<E>& d = s_seg[seg % kSegs];
+        const E x = d.x;
+        const int off = x.base();
         const int32_t* table = c.table + (size_t)x.q * c.max_pages;
-        const int last = (x.len + x.n - 1) >> c.ps_log2, head = p.a.layer * 2 * c.n_head_kv + d.kvh;
+        const int last = (x.len + x.nodes() - 1) >> c.ps_log2, head = p.a.layer * 2 * c.n_head_kv + d.kvh;
         const int c0 = d.c0, c1 = c0 + d.nc;
         int base = -64, row = none;             // lane i holds the tensor row of page base + i
         for (int ch = c0; ch < c1 && !stop; ++ch) {
-          if (((ch * kChunk + kChunk - 1) >> c.ps_log2) > base + 31) {
-            base = (ch * kChunk) >> c.ps_log2;
+          if (((off + ch * kChunk + kChunk - 1) >> c.ps_log2) > base + 31) {
+            base = (off + ch * kChunk) >> c.ps_log2;
             row = none;
             if (base + lane <= last) {
               const int t = table[base + lane];
@@ -555,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
             if (stop) break;
             uint8_t* dst = ring + st * kMat;
             for (int i = 0; i < kChunk; i += p.box_rows) {
-              const int slot = ch * kChunk + i;
+              const int slot = off + ch * kChunk + i;
               const int r = __shfl_sync(0xffffffffu, row, ((slot >> c.ps_log2) - base) & 31);
               if (lane == 0)
 #pragma unroll
@@ -588,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         const uint64_t q0 = desc_k(su32(sm)), k0 = desc_k(su32(ring)), v0 = desc_mn(su32(ring), kHalf);
         const uint32_t dS = tmem + i * 128, dO = tmem + 256 + i * HD;
         for (int seg = 0; live && seg_wait(&s_planned, &s_total, seg, &s_abort, c.status); ++seg) {
-          const SegDesc& d = s_seg[seg % kSegs];
+          const SegDesc<E>& d = s_seg[seg % kSegs];
           const bool pair = d.left > 128;
           const int nc = d.nc, mine = pair ? nc : (nc + 1 - i) >> 1;
           const uint64_t qa = q0 + (uint64_t)((pair ? i : qb) * (kMat >> 4));
@@ -678,15 +683,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
     } else {
       // ----------------------------------------------------- segments, queries
       pdl_wait();
-      if (lane == 0) p.cuts[b] = {0, 0, 0, 0, -1, 0};
+      if (lane == 0) p.cuts[b] = {0, 0, 0, 0, -1, 0, 0};
       if (few) plan_few(p.a, cutting(), s_e, s_end, b == 0);
-      const long long U = s_end[p.a.rows.n_seq - 1];
+      const long long U = s_end[entries - 1];
       // fewer blocks than launched where their shares would get too small
       const int Gr = blocks_used(U, gridDim.x, kMinUnits), grp = p.a.grp;
       const long long ub0 = U > 0 && b < Gr ? range_begin(U, Gr, b) : 0;
       const long long ub1 = U > 0 && b < Gr ? range_begin(U, Gr, b + 1) : 0;
       long long u = ub0;
-      int s = ub1 > ub0 ? find_entry(s_end, p.a.rows.n_seq, ub0) : 0, planned = 0;
+      int s = ub1 > ub0 ? find_entry(s_end, entries, ub0) : 0, planned = 0;
       bool more = true, live = true;
       int free_par[2] = {1, 1}, qb = 0;
       for (int seg = 0; live; ++seg) {
@@ -699,8 +704,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
             if (lane == 0) publish(&s_total, planned);
             break;
           }
-          const Entry x = s_e[g.s];
-          SegDesc& d = s_seg[planned % kSegs];
+          const E x = s_e[g.s];
+          SegDesc<E>& d = s_seg[planned % kSegs];
           const int left = (int)min((long long)x.n * grp - g.row0, (long long)kTile);
           if (lane == 0) {
             d.x = x;
@@ -716,7 +721,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
             d.slot = 2 * b + (ub0 >= g.u0 ? 0 : 1);
             // the block with a cut tile's first chunk describes it to the join
             if (g.c0 == 0 && !d.whole)
-              p.cuts[b] = {x.lo, g.row0, g.kvh, left, block_of(U, Gr, g.u0 + (long long)(g.nch - 1) * g.w), d.slot};
+              p.cuts[b] = {x.lo, g.row0, g.kvh, left, block_of(U, Gr, g.u0 + (long long)(g.nch - 1) * g.w), d.slot,
+                           x.pass()};
             publish(&s_planned, planned + 1);
           }
           __syncwarp();
@@ -724,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         }
         if (seg >= planned) break;
         // Q: lane q of tile t is row 128 t + q of a pair, row q % per of a split tile
-        const SegDesc& d = s_seg[seg % kSegs];
+        const SegDesc<E>& d = s_seg[seg % kSegs];
         const int left = d.left;
         const bool pair = left > 128;
         const int per = left > 64 ? 128 : 64;
@@ -793,10 +799,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       int there = 0;
       if (lane == 0) there = seg_wait(&s_planned, &s_total, seg, &s_abort, c.status);
       if (!__shfl_sync(0xffffffffu, there, 0)) break;
-      const SegDesc& d = s_seg[seg % kSegs];
-      const int left = d.left, nc = d.nc, ch0 = d.c0, end = d.x.len + d.x.n;
+      const SegDesc<E>& d = s_seg[seg % kSegs];
+      const int left = d.left, nc = d.nc, ch0 = d.c0, end = d.x.len + d.x.nodes();
       // the slots that all rows see (of a chain those of its nodes up to the tile's first)
-      const int all = d.x.len + (p.a.mask ? 0 : d.node0 + 1);
+      const int all = d.x.len + (p.a.mask || !d.x.nodes() ? 0 : d.node0 + 1);
       const bool pair = left > 128;
       const int rep = left > 64 ? 1 : 2, per = 128 / rep;   // copies of a row, rows
       const int steps = pair ? 2 * nc : nc;
@@ -826,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
           softmax_step<NB, HD, false>(p.a, d.x, node, slot0, col0, tS + 64 * h, tO, scale, later, settle, m, l);
       };
       for (int k = i; k < steps; k += 2, ++n_s) {
-        const int j = pair ? k >> 1 : k, slot0 = (ch0 + j) * kChunk;
+        const int j = pair ? k >> 1 : k, slot0 = d.x.base() + (ch0 + j) * kChunk;
         const bool masked = slot0 + kChunk > all;
         if (masked && real && p.a.mask) prefetch_mask(p.a, d.x, node, slot0);
         if (slot0 + kChunk > end) {
@@ -895,18 +901,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         wb = ex2(ml[128 + pos].x - use);
         sync_rows();   // the area is the accumulators' from here on
       }
-      if (whole) {
+      const bool last_word = whole && !E::kParts;   // else fp32 sums, relative to the row's reference
+      if (last_word) {
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         wa *= inv;
         wb *= inv;
       }
-      char* dst = reinterpret_cast<char*>(p.part_o + ((size_t)slot * kTile + row) * HD);
+      // where row r's sums go
+      auto part_of = [&](int r) {
+        if (!E::kParts || !whole) return (size_t)slot * kTile + r;
+        const int y = d.h0 + r, nd = small_quotient(y, p.grp_magic);
+        return part_row(p.a, d.x.pass(), d.x.lo + d.node0 + nd, d.kvh * p.a.grp + y - nd * p.a.grp);
+      };
+      float* const sums_o = E::kParts && whole ? p.a.row_o : p.part_o;
+      float2* const sums_ml = E::kParts && whole ? p.a.row_ml : p.part_ml;
+      char* dst = reinterpret_cast<char*>(sums_o + part_of(real ? row : 0) * HD);
       if (real) {
         float* lse;
-        if (whole) out_row(row, dst, lse);
+        if (last_word) out_row(row, dst, lse);
         if (pair || (i == 0 && pos < per)) {
-          if (!whole)
-            p.part_ml[(size_t)slot * kTile + row] = make_float2(top, sum);
+          if (!last_word)
+            sums_ml[part_of(row)] = make_float2(top, sum);
           else if (lse)
             *lse = sum > 0.f ? (top + log2f(sum)) * kLn2 : -CUDART_INF_F;
         }
@@ -955,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
               x[e] = *reinterpret_cast<const float4*>(buf + r * 32 + ((q ^ (r & 7)) << 2));
               to[e] = __shfl_sync(0xffffffffu, (unsigned long long)dst, r);
             }
-            if (whole) {
+            if (last_word) {
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 if (4 * e + (lane >> 3) < last)
@@ -1005,14 +1020,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
             for (int k = 0; k < 4; ++k) {
               const int e = e0 + 256 * k, r = e >> ql, dim = p0 + 4 * (e - (r << ql));
               if (r >= left) continue;
-              if (whole) {
+              if (last_word) {
                 char* to;
                 float* lse;
                 out_row(r, to, lse);
                 *reinterpret_cast<uint2*>(to + dim * 2) =
                     make_uint2(pack_bf16x2(x[k].x, x[k].y), pack_bf16x2(x[k].z, x[k].w));
               } else {
-                *reinterpret_cast<float4*>(p.part_o + ((size_t)slot * kTile + r) * HD + dim) = x[k];
+                *reinterpret_cast<float4*>(sums_o + part_of(r) * HD + dim) = x[k];
               }
             }
           }
@@ -1038,19 +1053,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
   }
 }
 
-template <int HD>
-constexpr size_t fixed_smem(int n_seq) {   // without the ring
-  return 1024 + Lay<HD>::kOffScratch + 16 * 8 + 12 * 8 + (size_t)n_seq * (sizeof(long long) + sizeof(Entry));
+template <int HD, typename E>
+constexpr size_t fixed_smem(int entries) {   // without the ring
+  return 1024 + Lay<HD>::kOffScratch + 16 * 8 + 12 * 8 + (size_t)entries * (sizeof(long long) + sizeof(E));
 }
 constexpr size_t kSmemMost = 227 * 1024 - 512;   // static shared memory aside
 // stages of the ring (128 dims: 5, beside the scratch 4, there with 53 entries and more 3)
-template <int HD>
-constexpr int ring_stages(int n_seq, int scratch) {
-  const size_t n = (kSmemMost - fixed_smem<HD>(n_seq) - scratch) / (Lay<HD>::kMat + 16);
+template <int HD, typename E>
+constexpr int ring_stages(int entries, int scratch) {
+  const size_t n = (kSmemMost - fixed_smem<HD, E>(entries) - scratch) / (Lay<HD>::kMat + 16);
   return n > Lay<HD>::kStagesMost ? Lay<HD>::kStagesMost : (int)n;
 }
 // (a stream's chunk and the next one's keys)
-static_assert(ring_stages<128>(kCallSeq, kScratch) >= 3 && ring_stages<64>(kCallSeq, kScratch) >= 3, "ring too short");
+static_assert(ring_stages<128, Entry>(kCallSeq, kScratch) >= 3 && ring_stages<64, Entry>(kCallSeq, kScratch) >= 3 &&
+                  ring_stages<128, PartEntry>(kCallSeq, kScratch) >= 3 && ring_stages<64, PartEntry>(kCallSeq, kScratch) >= 3,
+              "ring too short");
 
 // The call's queries as a 3-D tensor (made per call: it names the caller's buffer).
 bool q_map(CUtensorMap* m, const AttendParams& a, uint32_t grp) {
@@ -1064,7 +1081,7 @@ bool q_map(CUtensorMap* m, const AttendParams& a, uint32_t grp) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int HD>
+template <int HD, typename E>
 cudaError_t umma_as(const AttendParams& a, const AttendWork& w, cudaStream_t st) {
   using Lt = Lay<HD>;
   UmmaParams p;
@@ -1080,27 +1097,35 @@ cudaError_t umma_as(const AttendParams& a, const AttendWork& w, cudaStream_t st)
   p.box_rows = a.c.ps < kChunk ? a.c.ps : kChunk;
   // pairs fill both Q areas; split tiles of 128 dims alternate between them and
   // are bound by memory, where the stage counts for more
-  const bool pairs = (long long)a.max_tree * a.grp > kWide;
+  const bool pairs = (long long)(E::kParts ? a.rows.T : a.max_tree) * a.grp > kWide;
   p.grp_magic = quotient_magic(grp);
   p.scratch = pairs || HD == 64 ? kScratch : 0;
-  p.stages = ring_stages<HD>(a.rows.n_seq, p.scratch);
-  const size_t smem = fixed_smem<HD>(a.rows.n_seq) + p.scratch + (size_t)p.stages * (Lt::kMat + 16);
-  const cudaError_t e = launch_dependent(attend_umma_kernel<HD>, dim3(w.sms), kThreads, smem, st, p);
+  const int entries = a.n_group + a.rows.n_seq;
+  p.stages = ring_stages<HD, E>(entries, p.scratch);
+  const size_t smem = fixed_smem<HD, E>(entries) + p.scratch + (size_t)p.stages * (Lt::kMat + 16);
+  const cudaError_t e = launch_dependent(attend_umma_kernel<HD, E>, dim3(w.sms), kThreads, smem, st, p);
   if (e != cudaSuccess) return e;
-  return launch_join<2, HD>(a, w, kTile, w.sms, st);
+  return launch_join<2, HD, E>(a, w, kTile, w.sms, st);
+}
+
+template <int HD, typename E>
+cudaError_t raise_smem() {
+  return cudaFuncSetAttribute(attend_umma_kernel<HD, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost);
 }
 
 }  // namespace
 
 cudaError_t configure_attend_umma() {
-  const cudaError_t e = cudaFuncSetAttribute(attend_umma_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)kSmemMost);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(attend_umma_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost);
+  cudaError_t e = raise_smem<64, Entry>();
+  if (e == cudaSuccess) e = raise_smem<128, Entry>();
+  if (e == cudaSuccess) e = raise_smem<64, PartEntry>();
+  if (e == cudaSuccess) e = raise_smem<128, PartEntry>();
+  return e;
 }
 
 cudaError_t launch_attend_umma(const AttendParams& a, const AttendWork& w, cudaStream_t st) {
-  return a.c.hd == 64 ? umma_as<64>(a, w, st) : umma_as<128>(a, w, st);
+  if (a.n_group) return a.c.hd == 64 ? umma_as<64, PartEntry>(a, w, st) : umma_as<128, PartEntry>(a, w, st);
+  return a.c.hd == 64 ? umma_as<64, Entry>(a, w, st) : umma_as<128, Entry>(a, w, st);
 }
 
 }  // namespace dflash

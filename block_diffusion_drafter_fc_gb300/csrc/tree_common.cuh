@@ -75,8 +75,31 @@ DF_DEVICE long long quotient(long long a, long long b) {
 // of one node) form tiles, its slots chunks; the work is the chunks of every
 // tile of every kv head.
 struct Entry {
+  static constexpr bool kParts = false;
   int lo, n, len, q;
+  DF_DEVICE int base() const { return 0; }      // the first slot
+  DF_DEVICE int nodes() const { return n; }     // slots behind the length: one per row node
+  DF_DEVICE int pass() const { return 0; }
+  DF_DEVICE static int count(const AttendParams& p) { return p.rows.n_seq; }
 };
+
+// With shared prefixes a call has two kinds: groups (all rows of the group's entries over
+// the slots that they share: no nodes behind them, q the first entry's sequence), then
+// entries, over their slots from `base0` on.  Every tile leaves its rows' parts.
+struct PartEntry {
+  static constexpr bool kParts = true;
+  int lo, n, len, q;
+  int base0, nodes0;
+  DF_DEVICE int base() const { return base0; }
+  DF_DEVICE int nodes() const { return nodes0; }
+  DF_DEVICE int pass() const { return nodes0 > 0; }
+  DF_DEVICE static int count(const AttendParams& p) { return p.n_group + p.rows.n_seq; }
+};
+
+// Row `t`, head `h`: its place among the parts of `pass`.
+DF_DEVICE size_t part_row(const AttendParams& p, int pass, int t, int h) {
+  return ((size_t)pass * p.rows.T + t) * p.c.n_head + h;
+}
 
 // How a kernel cuts a call's rows and slots, and what the pieces cost: a chunk
 // of a tile of more than `wide` rows `heavy` units, of others `light`, and every
@@ -104,14 +127,15 @@ struct Blocks {
   int last;                // units of a chunk of the last block (the others are full)
   long long first;         // slots of block 0, + chunk - 1
 
-  DF_DEVICE Blocks(const AttendParams& p, const Cutting& cut, const Entry& x) : c(cut), step(0), first(0) {
+  template <typename E>
+  DF_DEVICE Blocks(const AttendParams& p, const Cutting& cut, const E& x) : c(cut), step(0), first(0) {
     const long long rows = (long long)x.n * p.grp;
     count = (int)quotient(rows + c.tile - 1, c.tile);
-    nch = (int)quotient((long long)x.len + x.n + c.chunk - 1, c.chunk);
+    nch = (int)quotient((long long)x.len - x.base() + x.nodes() + c.chunk - 1, c.chunk);
     last = rows - (long long)(count - 1) * c.tile > c.wide ? c.heavy : c.light;
-    if (p.step && count > 1) {
+    if (p.step && count > 1 && x.nodes()) {
       step = p.step;
-      first = (long long)x.len + step + c.chunk - 1;
+      first = (long long)x.len - x.base() + step + c.chunk - 1;
     }
   }
   DF_DEVICE int units(int i) const { return i == count - 1 ? last : c.heavy; }   // of a chunk of block i
@@ -168,19 +192,60 @@ DF_DEVICE long long plan_entry(const AttendParams& p, const Cutting& cut, int s,
   return c.n_head_kv * b.before(b.count);
 }
 
+// The same with shared prefixes: group s, or entry s - n_group.  (The plan's slots end
+// pages, whatever it says; what does not fit the lengths as they are is refused.)
+DF_DEVICE long long plan_entry(const AttendParams& p, const Cutting& cut, int s, PartEntry& x, unsigned& bad) {
+  const CacheView& c = p.c;
+  int e0 = s - p.n_group, e1 = e0 + 1, shared;
+  const bool group = e0 < 0;
+  x = {0, 0, 0, 0, 0, 0};
+  bad = 0;
+  if (group) {
+    e0 = p.group_start[s];
+    e1 = p.group_start[s + 1];
+    shared = p.plan[p.rows.n_seq + s] & ~(c.ps - 1);
+    if (e0 < 0 || e0 > e1 || e1 > p.rows.n_seq) {
+      bad = DEV_BAD_ROWS;
+      return 0;
+    }
+    if (e0 == e1 || shared == 0) return 0;
+  } else {
+    shared = p.plan[e0] & ~(c.ps - 1);
+  }
+  const int lo = p.rows.row_start[e0], hi = p.rows.row_start[e1];
+  x.q = entry_sequence(p.rows, e0, c.max_seq);
+  const int len = x.q >= 0 ? c.length[x.q] : 0;
+  x.lo = lo;
+  x.n = hi - lo;
+  if (lo < 0 || lo > hi || hi > p.rows.T || (!group && x.n > p.max_tree))
+    bad = DEV_BAD_ROWS;
+  else if (x.n > 0 && x.q < 0)
+    bad = DEV_BAD_SEQ;
+  else if (x.n > 0 && (shared < 0 || len < shared || (long long)len + (group ? 0 : x.n) > (long long)c.max_pages * c.ps))
+    bad = DEV_BAD_ROWS;
+  if (bad) x.n = 0;
+  if (x.n <= 0) return 0;
+  x.len = group ? shared : len;
+  x.base0 = group ? 0 : shared;
+  x.nodes0 = group ? 0 : x.n;
+  const Blocks b(p, cut, x);
+  return c.n_head_kv * b.before(b.count);
+}
+
 // plan_entries by one warp, of at most 32 entries: the block's other warps need not wait.
-DF_DEVICE void plan_few(const AttendParams& p, const Cutting& cut, Entry* e, long long* end, bool report) {
-  const int s = threadIdx.x & 31;
-  Entry x;
+template <typename E>
+DF_DEVICE void plan_few(const AttendParams& p, const Cutting& cut, E* e, long long* end, bool report) {
+  const int s = threadIdx.x & 31, n = E::count(p);
+  E x;
   unsigned bad = 0;
-  long long v = s < p.rows.n_seq ? plan_entry(p, cut, s, x, bad) : 0;
+  long long v = s < n ? plan_entry(p, cut, s, x, bad) : 0;
   if (bad && report) set_status(p.c.status, bad);
 #pragma unroll 1
-  for (int o = 1; o < p.rows.n_seq; o <<= 1) {
+  for (int o = 1; o < n; o <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, v, o);
     if (s >= o) v += y;
   }
-  if (s < p.rows.n_seq) {
+  if (s < n) {
     e[s] = x;
     end[s] = v;
   }
@@ -191,15 +256,16 @@ DF_DEVICE void plan_few(const AttendParams& p, const Cutting& cut, Entry* e, lon
 // e[] and end[] (end[s]: units of entries 0..s; a skipped entry has none) with
 // all `threads` threads of the block (a multiple of 32).  One block reports
 // faults.  s_warp: a word per warp in shared memory.
-DF_DEVICE void plan_entries(const AttendParams& p, const Cutting& cut, Entry* e, long long* end,
+template <typename E>
+DF_DEVICE void plan_entries(const AttendParams& p, const Cutting& cut, E* e, long long* end,
                             long long* s_warp, int threads, bool report) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, count = E::count(p);
   long long before = 0;
-  for (int s0 = 0; s0 < p.rows.n_seq; s0 += threads) {
+  for (int s0 = 0; s0 < count; s0 += threads) {
     const int s = s0 + threadIdx.x;
     long long units = 0;
-    if (s < p.rows.n_seq) {
-      Entry x;
+    if (s < count) {
+      E x;
       unsigned bad;
       units = plan_entry(p, cut, s, x, bad);
       if (bad && report) set_status(p.c.status, bad);
@@ -218,7 +284,7 @@ DF_DEVICE void plan_entries(const AttendParams& p, const Cutting& cut, Entry* e,
       if (w < warp) base += s_warp[w];
       all += s_warp[w];
     }
-    if (s < p.rows.n_seq) end[s] = base + v;
+    if (s < count) end[s] = base + v;
     before += all;
     __syncthreads();
   }
@@ -243,7 +309,8 @@ struct Segment {
 };
 
 // The segments of units [u, u1): call repeatedly; s carries the entry.
-DF_DEVICE bool next_segment(const AttendParams& p, const Cutting& cut, const Entry* e,
+template <typename E>
+DF_DEVICE bool next_segment(const AttendParams& p, const Cutting& cut, const E* e,
                             const long long* end, long long& u, long long u1, int& s, Segment& g) {
   while (u < u1) {
     while (end[s] <= u) ++s;
@@ -303,7 +370,7 @@ DF_DEVICE int block_of(long long U, int G, long long u) { return (int)quotient((
 // 8 groups, 91.1 with 32, 93.0 with 64), a warp per row.  Part i of a tile that begins in block b0 is slot
 // 2 i of the partial rows (b0 itself: the slot its description names).  Weights
 // e^(m_i - max) are applied and summed in block order.
-template <int EL, int HD>
+template <int EL, int HD, bool PARTS>
 __global__ void __launch_bounds__(128) attend_join_kernel(AttendParams p, const Cut* cuts, const float* part_o,
                                                           const float2* part_ml, int tile) {
   constexpr int VL = HD / 32;
@@ -345,6 +412,12 @@ __global__ void __launch_bounds__(128) attend_join_kernel(AttendParams p, const 
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     const int grp = p.grp, node = (d.row0 + r) / grp;
     const int h = d.kvh * grp + (d.row0 + r) - node * grp;
+    if constexpr (PARTS) {
+      const size_t to = part_row(p, d.pass, d.lo + node, h);
+      *reinterpret_cast<V*>(p.row_o + to * HD + lane * VL) = *reinterpret_cast<const V*>(acc);
+      if (lane == 0) p.row_ml[to] = make_float2(m, sum);
+      continue;
+    }
     char* dst = p.out + (size_t)(d.lo + node) * p.out_ld + (size_t)(h * HD + lane * VL) * EL;
 #pragma unroll
     for (int v = 0; v < VL; ++v) acc[v] *= inv;
@@ -361,12 +434,66 @@ __global__ void __launch_bounds__(128) attend_join_kernel(AttendParams p, const 
   }
 }
 
+// Rows whose slots two parts hold: the group's and the entry's, joined and written.  Grid
+// (entries, up to 64 groups of four rows), a warp per row of a query head.  A part without
+// slots of the row has sum 0 and reference -inf.
 template <int EL, int HD>
+__global__ void __launch_bounds__(128) attend_combine_kernel(AttendParams p) {
+  constexpr int VL = HD / 32;
+  using V = typename DimVec<VL>::T;
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  PartEntry x;
+  unsigned bad;
+  plan_entry(p, Cutting{16, 32, 0, 1, 1, 0}, p.n_group + blockIdx.x, x, bad);
+  const int rows = x.n * p.c.n_head;
+  for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < rows; r += 4 * gridDim.y) {
+    const int t = x.lo + r / p.c.n_head, h = r % p.c.n_head;
+    const size_t at[2] = {part_row(p, 0, t, h), part_row(p, 1, t, h)};
+    float2 ml[2];
+    alignas(16) float f[2][VL];
+    ml[0] = make_float2(-CUDART_INF_F, 0.f);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (k || x.base0) {
+        ml[k] = p.row_ml[at[k]];
+        *reinterpret_cast<V*>(f[k]) = *reinterpret_cast<const V*>(p.row_o + at[k] * HD + lane * VL);
+      } else {
+#pragma unroll
+        for (int v = 0; v < VL; ++v) f[k][v] = 0.f;
+      }
+    const float m = fmaxf(ml[0].x, ml[1].x), use = m == -CUDART_INF_F ? 0.f : m;
+    const float w0 = ex2(ml[0].x - use), w1 = ex2(ml[1].x - use);
+    const float sum = w0 * ml[0].y + w1 * ml[1].y, inv = sum > 0.f ? 1.f / sum : 0.f;
+    alignas(16) float acc[VL];
+#pragma unroll
+    for (int v = 0; v < VL; ++v) acc[v] = (w0 * f[0][v] + w1 * f[1][v]) * inv;
+    char* dst = p.out + (size_t)t * p.out_ld + (size_t)(h * HD + lane * VL) * EL;
+    if constexpr (EL == 4) {
+      *reinterpret_cast<V*>(dst) = *reinterpret_cast<const V*>(acc);
+    } else if constexpr (VL == 1) {
+      *reinterpret_cast<uint16_t*>(dst) = f32_to_bf16_bits(acc[0]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < VL; v += 2) reinterpret_cast<uint32_t*>(dst)[v / 2] = pack_bf16x2(acc[v], acc[v + 1]);
+    }
+    if (p.lse && lane == 0)
+      p.lse[(size_t)t * p.c.n_head + h] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -CUDART_INF_F;
+  }
+}
+
+template <int EL, int HD, typename E>
 cudaError_t launch_join(const AttendParams& p, const AttendWork& w, int tile, int blocks, cudaStream_t st) {
-  const long long rows = (long long)p.max_tree * p.grp;
+  const long long rows = (long long)(E::kParts ? p.rows.T : p.max_tree) * p.grp;
   const int most = rows < tile ? (int)rows : tile;
-  return launch_dependent(attend_join_kernel<EL, HD>, dim3(blocks, most < 64 ? (most + 3) / 4 : 16), 128, 0, st, p,
-                          (const Cut*)w.cuts, (const float*)w.part_o, (const float2*)w.part_ml, tile);
+  const cudaError_t e =
+      launch_dependent(attend_join_kernel<EL, HD, E::kParts>, dim3(blocks, most < 64 ? (most + 3) / 4 : 16), 128, 0, st,
+                       p, (const Cut*)w.cuts, (const float*)w.part_o, (const float2*)w.part_ml, tile);
+  if (!E::kParts || e != cudaSuccess) return e;
+  const long long heads = (long long)p.max_tree * p.c.n_head;   // rows of an entry
+  return launch_dependent(attend_combine_kernel<EL, HD>, dim3(p.rows.n_seq, heads < 256 ? ((int)heads + 3) / 4 : 64), 128,
+                          0, st, p);
 }
 
 }  // namespace tree

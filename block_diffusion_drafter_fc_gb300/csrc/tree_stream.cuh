@@ -48,31 +48,33 @@ struct StreamParams {
 
 // The copies of a block's chunks, run ahead of their use by one warp: K, then V
 // of every chunk of every segment.
-template <int EL, int HD>
+template <int EL, int HD, typename E>
 struct Copies {
   using G = Geo<EL, HD>;
   long long u;
   int s, it = 0, ch = 0, kv = 0;
   int base = 0, row = 0;    // lane i holds the tensor row of page base + i
+  int off = 0;              // the entry's first slot
   bool more = false;
   Segment g;
 
-  DF_DEVICE void open(const StreamParams& p, const Entry* e, const long long* end, long long u1, int tile) {
+  DF_DEVICE void open(const StreamParams& p, const E* e, const long long* end, long long u1, int tile) {
     more = next_segment(p.a, cutting<EL>(tile), e, end, u, u1, s, g);
+    if (more) off = e[g.s].base();
     ch = g.c0;
     base = -64;
   }
-  DF_DEVICE void issue(const StreamParams& p, uint8_t* sm, uint64_t* full, uint64_t* empty, const Entry* e,
+  DF_DEVICE void issue(const StreamParams& p, uint8_t* sm, uint64_t* full, uint64_t* empty, const E* e,
                        const long long* end, long long u1, int tile, volatile int* abort) {
     if (!more) return;
     const CacheView& c = p.a.c;
     const int lane = threadIdx.x & 31, S = p.stages, st = it % S;
     const int none = c.n_pages * c.n_layer * 2 * c.n_head_kv;   // past the tensor: reads as zero
-    if (kv == 0 && ((ch * G::CS + G::CS - 1) >> c.ps_log2) > base + 31) {
-      const Entry x = e[g.s];
-      base = (ch * G::CS) >> c.ps_log2;
+    if (kv == 0 && ((off + ch * G::CS + G::CS - 1) >> c.ps_log2) > base + 31) {
+      const E x = e[g.s];
+      base = (off + ch * G::CS) >> c.ps_log2;
       row = none;
-      if (base + lane <= (x.len + x.n - 1) >> c.ps_log2) {
+      if (base + lane <= (x.len + x.nodes() - 1) >> c.ps_log2) {
         const int t = c.table[(size_t)x.q * c.max_pages + base + lane];
         if (t >= 0 && t < c.n_pages)
           row = (t * c.n_layer + p.a.layer) * 2 * c.n_head_kv + g.kvh;
@@ -92,7 +94,7 @@ struct Copies {
     }
     uint8_t* dst = sm + st * G::kHalf;
     for (int i = 0; i < G::CS; i += p.box_rows) {
-      const int slot = ch * G::CS + i;
+      const int slot = off + ch * G::CS + i;
       const int r = __shfl_sync(0xffffffffu, row, ((slot >> c.ps_log2) - base) & 31);
       if (lane == 0)
 #pragma unroll

@@ -115,6 +115,10 @@ def _load() -> C.CDLL:
         "dflash_tree_mask": (C.c_int, [vp, i32, vp, i32, vp, vp, i32, vp, vp]),
         "dflash_tree_attend": (C.c_int, [vp, i32, i32, vp, vp, i32, i32, vp, i32, vp, i64, vp, i64,
                                          vp, vp]),
+        "dflash_prefix_plan": (C.c_int, [vp, i32, vp, i32, vp, vp, vp]),
+        "dflash_prefix_workspace_size": (C.c_int, [vp, i32, szp]),
+        "dflash_prefix_attend": (C.c_int, [vp, i32, i32, vp, vp, i32, i32, vp, i32, i32, vp, vp, vp, vp, i64, vp, i64,
+                                           vp, vp]),
         "dflash_tree_accept": (C.c_int, [vp, i32, vp, i32, vp, vp, vp, vp, i32, vp, vp, vp]),
         "dflash_cache_commit": (C.c_int, [vp, i32, vp, vp, i32, vp, vp]),
         "dflash_cache_reserve": (C.c_int, [vp, i32, vp, vp, vp]),
@@ -622,28 +626,64 @@ class PagedCache:
             self.h, row_start.shape[0] - 1, i("tree_mask", row_start, 1), T, i("tree_mask", parents, T),
             i("tree_mask", mask, T), shape[1], i("tree_mask", depth, T), self._on(stream)), "tree_mask")
 
-    def dflash_tree_attend(self, layer: int, row_start, max_tree: int, q, out, mask=None, lse=None,
-                           seqs=None, stream=None):
-        hq, n = self.cfg.n_head, row_start.shape[0] - 1
-        T, qs = self._rows(q, "tree_attend", hq)
-        rows, os_ = self._rows(out, "tree_attend", hq)
+    def _attend_rows(self, what: str, q, out, mask, lse):
+        """(rows, q's and out's strides, mask words, lse's address) of an attention call."""
+        hq = self.cfg.n_head
+        T, qs = self._rows(q, what, hq)
+        rows, os_ = self._rows(out, what, hq)
         words = lp = 0
         if mask is not None:
             if mask.dim() != 2 or mask.shape[0] != T or T and not mask.shape[1]:   # (no words: a null address, a chain)
-                raise DFlashError("tree_attend: mask is int32 [T][words]")
+                raise DFlashError(f"{what}: mask is int32 [T][words]")
             words = mask.shape[1]
         if rows != T:
-            raise DFlashError("tree_attend: q and out have different rows")
+            raise DFlashError(f"{what}: q and out have different rows")
         if lse is not None:
             if (lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() != T * hq
                     or lse.get_device() != self.device_index):
-                raise DFlashError("tree_attend: lse is contiguous f32 [T][n_head] on the cache's device")
+                raise DFlashError(f"{what}: lse is contiguous f32 [T][n_head] on the cache's device")
             lp = lse.data_ptr()
-        i = self._int
+        return T, qs, os_, words, lp
+
+    def dflash_tree_attend(self, layer: int, row_start, max_tree: int, q, out, mask=None, lse=None,
+                           seqs=None, stream=None):
+        n, i = row_start.shape[0] - 1, self._int
+        T, qs, os_, words, lp = self._attend_rows("tree_attend", q, out, mask, lse)
         self._ok(LIB.dflash_tree_attend(
             self.h, layer, n, i("tree_attend", seqs, n), i("tree_attend", row_start, 1), T, max_tree,
             i("tree_attend", mask, 0), words, q.data_ptr(), qs, out.data_ptr(), os_, lp, self._on(stream)),
             "tree_attend")
+
+    def dflash_prefix_plan(self, group_start, plan, seqs=None, stream=None):
+        """plan int32 [n_seq + n_group], written."""
+        g, i = group_start.shape[0] - 1, self._int
+        n = plan.shape[0] - g
+        if n < 0:
+            raise DFlashError("prefix_plan: plan is int32 [n_seq + n_group]")
+        self._ok(LIB.dflash_prefix_plan(self.h, n, i("prefix_plan", seqs, n), g, i("prefix_plan", group_start, 1),
+                                        i("prefix_plan", plan, n + g), self._on(stream)), "prefix_plan")
+
+    def prefix_workspace(self, rows: int) -> int:
+        """Bytes of dflash_prefix_attend's work area."""
+        b = C.c_size_t()
+        self._ok(LIB.dflash_prefix_workspace_size(self.h, rows, C.byref(b)), "prefix_workspace")
+        return b.value
+
+    def dflash_prefix_attend(self, layer: int, row_start, max_tree: int, q, out, group_start, plan, work,
+                             mask=None, lse=None, seqs=None, stream=None):
+        """work: a tensor of prefix_workspace(rows) bytes."""
+        n, g, i = row_start.shape[0] - 1, group_start.shape[0] - 1, self._int
+        T, qs, os_, words, lp = self._attend_rows("prefix_attend", q, out, mask, lse)
+        if plan.shape[0] != n + g:
+            raise DFlashError("prefix_attend: plan is int32 [n_seq + n_group]")
+        if work.get_device() != self.device_index:
+            raise DFlashError(f"prefix_attend: work on {work.device}, not on the cache's device")
+        if not work.is_contiguous() or work.numel() * work.element_size() < self.prefix_workspace(T):
+            raise DFlashError(f"prefix_attend: work is contiguous, of prefix_workspace({T}) bytes")
+        self._ok(LIB.dflash_prefix_attend(
+            self.h, layer, n, i("prefix_attend", seqs, n), i("prefix_attend", row_start, 1), T, max_tree,
+            i("prefix_attend", mask, 0), words, g, i("prefix_attend", group_start, 1), i("prefix_attend", plan, n + g),
+            work.data_ptr(), q.data_ptr(), qs, out.data_ptr(), os_, lp, self._on(stream)), "prefix_attend")
 
     def dflash_tree_accept(self, row_start, parents, tokens, targets, path, n_path, id_last,
                            stream=None):

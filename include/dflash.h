@@ -711,6 +711,45 @@ DFLASH_API int dflash_tree_attend(dflash_cache* c, int32_t layer, int32_t n_seq,
                                   void* stream);
 
 /*
+ * Slots that groups of entries share: group g is entries group_start[g] ..
+ * group_start[g + 1] - 1 (device int32 [n_group + 1], ascending, within 0..n_seq), for
+ * instance the forks of one prompt.  What a group shares is found in the page table: the
+ * full pages below its members' least length that are the same for all of them (0 for a
+ * group of one).
+ *   plan: device int32 [n_seq + n_group], written: slots that entry s has in common with
+ *   its group (0: in none), then the slots that group g has in common.
+ * Made once a turn, after dflash_cache_reserve and for the same entries; it is out of date
+ * once a sequence is trimmed, forked or reserved for.  n_seq + n_group <=
+ * DFLASH_MAX_CALL_SEQ; ranges that are none make a plan that shares nothing (BAD_ROWS).
+ */
+DFLASH_API int dflash_prefix_plan(dflash_cache* c, int32_t n_seq, const int32_t* seqs, int32_t n_group,
+                                  const int32_t* group_start, int32_t* plan, void* stream);
+
+/* Bytes of dflash_prefix_attend's work area for T rows: two fp32 rows of every query head. */
+DFLASH_API int dflash_prefix_workspace_size(const dflash_cache* c, int32_t T, size_t* bytes);
+
+/*
+ * dflash_tree_attend where entries share prefixes: the same outputs, with the slots that a
+ * group shares read and multiplied once for the rows of all its members (their query heads
+ * fill common tiles); every entry's other slots follow as in dflash_tree_attend, and the
+ * two parts of a row are joined in fp32.
+ *   seqs, row_start, T, max_tree, mask, q, out, lse as there;
+ *   n_group, group_start, plan: as given to and written by dflash_prefix_plan for these
+ *   entries (the first member's pages are read for all of a group);
+ *   work: device, 256-byte aligned, dflash_prefix_workspace_size(T) bytes; one call at a
+ *   time uses it.
+ * An entry that is skipped (dflash_tree_attend), or whose length is below what the plan
+ * shares (BAD_ROWS), is not written; where a group is skipped, because its first member's
+ * sequence or its range of rows is bad, its members' outputs are unspecified.
+ */
+DFLASH_API int dflash_prefix_attend(dflash_cache* c, int32_t layer, int32_t n_seq, const int32_t* seqs,
+                                    const int32_t* row_start, int32_t T, int32_t max_tree,
+                                    const uint32_t* mask, int32_t mask_words, int32_t n_group,
+                                    const int32_t* group_start, const int32_t* plan, void* work,
+                                    const void* q, int64_t q_stride, void* out, int64_t out_stride,
+                                    float* lse, void* stream);
+
+/*
  * Greedy acceptance along trees (the tree form of dflash_accept): node 0 is the
  * anchor, always accepted; after an accepted node i follows its child of lowest
  * index whose token equals targets[row of i], until there is none or the path
