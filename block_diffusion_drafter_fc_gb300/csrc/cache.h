@@ -11,13 +11,15 @@ namespace dflash {
 
 // device status bits (include/dflash.h)
 enum : unsigned {
+  DEV_BAD_TOKEN = 0x1u,
   DEV_BAD_POSITION = 0x2u,
   DEV_TIMEOUT = 0x4u,
   DEV_BAD_ROWS = 0x8u,
   DEV_BAD_PAGE = 0x10u,
   DEV_BAD_TREE = 0x20u,
   DEV_BAD_SEQ = 0x40u,
-  DEV_NO_PAGES = 0x80u
+  DEV_NO_PAGES = 0x80u,
+  DEV_BAD_PROBS = 0x100u
 };
 
 constexpr int kCallSeq = 1024;   // most entries of one call

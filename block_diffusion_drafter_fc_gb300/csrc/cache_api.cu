@@ -4,6 +4,7 @@
 #include "../../include/dflash.h"
 #include "cache.h"
 #include "internal.h"
+#include "verify.h"
 
 #include <algorithm>
 #include <cmath>
@@ -12,11 +13,14 @@
 
 using namespace dflash;
 
-static_assert(DFLASH_MAX_TREE == kTreeMax && DFLASH_MAX_CALL_SEQ == kCallSeq, "limits of the header");
+static_assert(DFLASH_MAX_TREE == kTreeMax && DFLASH_MAX_CALL_SEQ == kCallSeq && DFLASH_MAX_VOCAB == kVocabMost &&
+                  DFLASH_MAX_VERIFY_ROWS == kVerifyRows,
+              "limits of the header");
 static_assert(DFLASH_DEV_BAD_POSITION == DEV_BAD_POSITION && DFLASH_DEV_TIMEOUT == DEV_TIMEOUT &&
                   DFLASH_DEV_BAD_ROWS == DEV_BAD_ROWS && DFLASH_DEV_BAD_PAGE == DEV_BAD_PAGE &&
                   DFLASH_DEV_BAD_TREE == DEV_BAD_TREE && DFLASH_DEV_BAD_SEQ == DEV_BAD_SEQ &&
-                  DFLASH_DEV_NO_PAGES == DEV_NO_PAGES,
+                  DFLASH_DEV_NO_PAGES == DEV_NO_PAGES && DFLASH_DEV_BAD_TOKEN == DEV_BAD_TOKEN &&
+                  DFLASH_DEV_BAD_PROBS == DEV_BAD_PROBS,
               "status bits of the header");
 
 namespace {
@@ -29,7 +33,7 @@ size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 struct Layout {
   size_t page_bytes;
   size_t table, length, refs, state_bytes;
-  size_t status, turns, tickets, free_list, copies, part_o, part_ml, cuts, norm_sums, scratch_bytes;
+  size_t status, turns, tickets, free_list, copies, part_o, part_ml, cuts, norm_sums, stats, scratch_bytes;
 };
 
 int el_of(const dflash_cache_config& c) { return c.dtype == DFLASH_DTYPE_BF16 ? 2 : 4; }
@@ -58,6 +62,7 @@ Layout layout(const dflash_cache_config& c) {
   L.part_ml = take(sizeof(float2) * parts);
   L.cuts = take(sizeof(Cut) * 2 * kAttendSms);
   L.norm_sums = take(sizeof(float) * kNormBlocks * 2 * c.head_dim);
+  L.stats = take(sizeof(RowStats) * kVerifyRows);
   L.scratch_bytes = off;
   return L;
 }
@@ -288,6 +293,7 @@ int dflash_cache_create(const dflash_cache_config* cfg, void* page_mem, void* st
       e = cudaMemcpy(c->S<void>(c->L.turns), turns, sizeof(turns), cudaMemcpyHostToDevice);
     if (e == cudaSuccess) e = configure_tree();
     if (e == cudaSuccess) e = configure_attend();
+    if (e == cudaSuccess) e = configure_verify();
     int sms = 0;
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c->device);
     if (e == cudaSuccess && !page_map(&c->tm, w, attend_chunk(w.el, w.hd))) e = cudaErrorNotSupported;
@@ -562,6 +568,78 @@ int dflash_tree_accept(dflash_cache* c, int32_t n_seq, const int32_t* row_start,
   OnDevice on(c->device);
   DC_CHECK(c, launch_tree_accept({n_seq, nullptr, row_start, T}, parents, tokens, targets, path, max_path,
                                  n_path, id_last, c->v.status, static_cast<cudaStream_t>(stream)));
+  return DFLASH_OK;
+}
+
+// Logits [rows][n_vocab] of a type: false when refused.
+static bool logits_of(const void* at, int64_t stride, int dtype, int n_vocab, int rows, const float* temperature, Logits& x) {
+  if (dtype != DFLASH_DTYPE_F32 && dtype != DFLASH_DTYPE_BF16) return false;
+  const int el = dtype == DFLASH_DTYPE_F32 ? 4 : 2;
+  x = {static_cast<const char*>(at), stride * el, rows, el, temperature};
+  return (at || rows == 0) && !(reinterpret_cast<uintptr_t>(at) & (el - 1)) && (stride >= n_vocab || rows < 2);
+}
+
+int dflash_tree_verify(dflash_cache* c, int32_t n_seq, const int32_t* row_start, int32_t T, const int32_t* parents,
+                       const int32_t* tokens, int32_t n_vocab, const void* target, int64_t target_stride,
+                       int32_t target_dtype, const float* temperature, const void* draft, int64_t draft_stride,
+                       int32_t draft_dtype, int32_t n_draft, const int32_t* draft_row, const float* draft_temperature,
+                       const float* uniform, const float* noise, int64_t noise_stride, int32_t* path, int32_t max_path,
+                       int32_t* n_path, int32_t* id_last, void* stream) {
+  const int rc = check_call(c, n_seq, row_start, T);
+  if (rc != DFLASH_OK) return rc;
+  if (n_vocab < 1 || max_path < 1 || n_draft < 0 || (!draft && (n_draft || draft_row || draft_temperature)))
+    return DFLASH_ERR_INVALID_ARG;
+  if (n_vocab > kVocabMost) return DFLASH_ERR_UNSUPPORTED;
+  VerifyParams p;
+  if (!logits_of(target, target_stride, target_dtype, n_vocab, T, temperature, p.target)) return DFLASH_ERR_INVALID_ARG;
+  if (!draft)
+    p.draft = {};
+  else if (!logits_of(draft, draft_stride, draft_dtype, n_vocab, n_draft, draft_temperature, p.draft))
+    return DFLASH_ERR_INVALID_ARG;
+  if ((int64_t)T + n_draft > kVerifyRows) return DFLASH_ERR_TOO_MANY_ROWS;
+  if (n_seq == 0) return DFLASH_OK;
+  if ((T > 0 && (!parents || !tokens || !uniform)) || !noise || (noise_stride < n_vocab && n_seq > 1) || !path || !n_path ||
+      !id_last)
+    return DFLASH_ERR_INVALID_ARG;
+  p.rows = {n_seq, nullptr, row_start, T};
+  p.V = n_vocab;
+  p.parents = parents;
+  p.tokens = tokens;
+  p.draft_row = draft_row;
+  p.uniform = uniform;
+  p.noise = noise;
+  p.noise_ld = noise_stride;
+  p.stats = c->S<RowStats>(c->L.stats);
+  p.path = path;
+  p.max_path = max_path;
+  p.n_path = n_path;
+  p.id_last = id_last;
+  p.status = c->v.status;
+  OnDevice on(c->device);
+  DC_CHECK(c, launch_verify(p, static_cast<cudaStream_t>(stream)));
+  return DFLASH_OK;
+}
+
+int dflash_sample(dflash_cache* c, int32_t T, int32_t n_vocab, const void* logits, int64_t logits_stride, int32_t dtype,
+                  int32_t n_rows, const int32_t* rows, const float* temperature, const float* noise, int64_t noise_stride,
+                  int32_t* tokens, void* stream) {
+  if (!c || T < 0 || n_vocab < 1 || n_rows < 0 || (!rows && n_rows < T)) return DFLASH_ERR_INVALID_ARG;
+  if (n_vocab > kVocabMost) return DFLASH_ERR_UNSUPPORTED;
+  SampleParams p;
+  if (!logits_of(logits, logits_stride, dtype, n_vocab, n_rows, temperature, p.logits)) return DFLASH_ERR_INVALID_ARG;
+  if (T == 0) return DFLASH_OK;
+  if (!noise || (noise_stride < n_vocab && T > 1) || !tokens) return DFLASH_ERR_INVALID_ARG;
+  if (T > (1 << 24)) return DFLASH_ERR_TOO_MANY_ROWS;
+  p.T = T;
+  p.V = n_vocab;
+  p.n_rows = n_rows;
+  p.rows = rows;
+  p.noise = reinterpret_cast<const char*>(noise);
+  p.noise_ld = noise_stride * 4;
+  p.tokens = tokens;
+  p.status = c->v.status;
+  OnDevice on(c->device);
+  DC_CHECK(c, launch_sample(p, static_cast<cudaStream_t>(stream)));
   return DFLASH_OK;
 }
 

@@ -120,6 +120,9 @@ def _load() -> C.CDLL:
         "dflash_prefix_attend": (C.c_int, [vp, i32, i32, vp, vp, i32, i32, vp, i32, i32, vp, vp, vp, vp, i64, vp, i64,
                                            vp, vp]),
         "dflash_tree_accept": (C.c_int, [vp, i32, vp, i32, vp, vp, vp, vp, i32, vp, vp, vp]),
+        "dflash_sample": (C.c_int, [vp, i32, i32, vp, i64, i32, i32, vp, vp, vp, i64, vp, vp]),
+        "dflash_tree_verify": (C.c_int, [vp, i32, vp, i32, vp, vp, i32, vp, i64, i32, vp, vp, i64, i32, i32, vp, vp, vp, vp,
+                                         i64, vp, i32, vp, vp, vp]),
         "dflash_cache_commit": (C.c_int, [vp, i32, vp, vp, i32, vp, vp]),
         "dflash_cache_reserve": (C.c_int, [vp, i32, vp, vp, vp]),
         "dflash_cache_fork": (C.c_int, [vp, i32, vp, vp, vp]),
@@ -361,6 +364,7 @@ class DeviceWeight:
 
 MAX_TREE = 1024       # most nodes of a tree with a mask
 _INT32, _raw_stream = torch.int32, getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_LOGITS = {torch.float32: DTYPE["f32"], torch.bfloat16: DTYPE["bf16"]}
 ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -694,6 +698,64 @@ class PagedCache:
             self.h, n, i("tree_accept", row_start, 1), T, i("tree_accept", parents, T),
             i("tree_accept", tokens, T), i("tree_accept", targets, T), i("tree_accept", path, 0), shape[1],
             i("tree_accept", n_path, n), i("tree_accept", id_last, n), self._on(stream)), "tree_accept")
+
+    def _logits(self, what: str, t):
+        """(address, row stride, dtype code, rows, tokens) of logits [rows][n_vocab]."""
+        code = _LOGITS.get(t.dtype)
+        if code is None or t.dim() != 2 or t.stride(1) != 1 and t.shape[1] > 1:
+            raise DFlashError(f"{what}: logits are f32 or bf16 [rows][n_vocab], a row's contiguous")
+        if t.get_device() != self.device_index:
+            raise DFlashError(f"{what}: logits on {t.device}, not on the cache's device")
+        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1], code, t.shape[0], t.shape[1]
+
+    def _floats(self, what: str, t, n: int) -> int:
+        """Address of a contiguous f32 tensor of at least n values (None: null)."""
+        if t is None:
+            return 0
+        if t.dtype is not torch.float32 or not t.is_contiguous() or t.numel() < n:
+            raise DFlashError(f"{what}: temperatures and uniform numbers are contiguous f32 of the call's size")
+        if t.get_device() != self.device_index:
+            raise DFlashError(f"{what}: a tensor on {t.device}, not on the cache's device")
+        return t.data_ptr()
+
+    def _noise(self, what: str, t, rows: int, vocab: int):
+        p, stride, code, n, v = self._logits(what, t)
+        if code != DTYPE["f32"] or n < rows or v != vocab:
+            raise DFlashError(f"{what}: noise is f32 [{rows}][{vocab}]")
+        return p, stride
+
+    def dflash_sample(self, logits, noise, tokens, rows=None, temperature=None, stream=None):
+        """tokens int32 [T]; rows int32 [T] or None: row t of logits for tokens[t]."""
+        T, i = tokens.shape[0], self._int
+        p, stride, code, n, vocab = self._logits("sample", logits)
+        e, es = self._noise("sample", noise, T, vocab)
+        self._ok(LIB.dflash_sample(self.h, T, vocab, p, stride, code, n, i("sample", rows, T),
+                                   self._floats("sample", temperature, T), e, es, i("sample", tokens, T), self._on(stream)),
+                 "sample")
+
+    def dflash_tree_verify(self, row_start, parents, tokens, target, uniform, noise, path, n_path, id_last,
+                           draft=None, draft_row=None, temperature=None, draft_temperature=None, stream=None):
+        n, T, shape, i, f = row_start.shape[0] - 1, parents.shape[0], path.shape, self._int, self._floats
+        if len(shape) != 2 or shape[0] != n:
+            raise DFlashError("tree_verify: path is int32 [n_seq][max_path]")
+        p, stride, code, rows, vocab = self._logits("tree_verify", target)
+        if rows != T:
+            raise DFlashError("tree_verify: target has a row of logits for every node")
+        e, es = self._noise("tree_verify", noise, n, vocab)
+        d, ds, dc, nd = 0, 0, 0, 0
+        if draft is not None:
+            d, ds, dc, nd, dv = self._logits("tree_verify", draft)
+            if dv != vocab or draft_row is None and nd < T:
+                raise DFlashError("tree_verify: draft is [n_draft][n_vocab], a row for every node without draft_row")
+        elif draft_row is not None or draft_temperature is not None:
+            raise DFlashError("tree_verify: draft_row and draft_temperature go with draft")
+        if uniform is None:
+            raise DFlashError("tree_verify: a uniform number for every node")
+        self._ok(LIB.dflash_tree_verify(
+            self.h, n, i("tree_verify", row_start, 1), T, i("tree_verify", parents, T), i("tree_verify", tokens, T), vocab,
+            p, stride, code, f("tree_verify", temperature, T), d, ds, dc, nd, i("tree_verify", draft_row, T),
+            f("tree_verify", draft_temperature, nd), f("tree_verify", uniform, T), e, es, i("tree_verify", path, 0), shape[1],
+            i("tree_verify", n_path, n), i("tree_verify", id_last, n), self._on(stream)), "tree_verify")
 
     def dflash_cache_commit(self, path, n_path, seqs=None, stream=None):
         """path int32 [n_seq][max_path], or None: the first n_path nodes stay in place."""

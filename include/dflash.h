@@ -90,6 +90,7 @@ typedef enum {
 #define DFLASH_DEV_BAD_TREE 0x20u     /* a parent that is not an earlier node, or a path that is not ascending */
 #define DFLASH_DEV_BAD_SEQ 0x40u      /* a sequence out of range, listed twice, or not empty where it has to be */
 #define DFLASH_DEV_NO_PAGES 0x80u     /* dflash_cache_reserve found too few pages: nothing was changed */
+#define DFLASH_DEV_BAD_PROBS 0x100u   /* a row of logits that is no distribution, or a bad temperature (BAD_TOKEN: a drafted token out of range, rejected) */
 
 /*
  * Drafter geometry and storage formats.
@@ -507,6 +508,9 @@ DFLASH_API const char* dflash_last_error(const dflash_handle* h);
 /* Most nodes of a tree that has a mask, and most entries of one call. */
 #define DFLASH_MAX_TREE 1024
 #define DFLASH_MAX_CALL_SEQ 1024
+/* Most tokens of a vocabulary, and most rows of logits of one dflash_tree_verify. */
+#define DFLASH_MAX_VOCAB 327680
+#define DFLASH_MAX_VERIFY_ROWS 65536
 
 typedef enum {
   DFLASH_ROPE_HALF = 0,         /* pair j: dims j and rotary_dim / 2 + j of a head */
@@ -766,6 +770,66 @@ DFLASH_API int dflash_tree_accept(dflash_cache* c, int32_t n_seq, const int32_t*
                                   const int32_t* parents, const int32_t* tokens, const int32_t* targets,
                                   int32_t* path, int32_t max_path, int32_t* n_path, int32_t* id_last,
                                   void* stream);
+
+/*
+ * Probabilities (dflash_sample, dflash_tree_verify).  A row x of n_vocab logits at
+ * temperature t means p_i = exp(x_i / t) / sum_j exp(x_j / t); -inf excludes a token (what a
+ * top-k or top-p filter leaves; log probabilities are logits too).  Temperature 0 (to 2^-20)
+ * means the largest logit, the lowest index of equal ones.  A row with a NaN or +inf, or
+ * without anything above -inf, or of a temperature that is negative, NaN or above 2^20, is no
+ * distribution (DFLASH_DEV_BAD_PROBS); scores x_i log2(e) / t of 2^30 and more in magnitude
+ * count as infinite.
+ *   logits: device f32 or bf16 (dtype) [rows][n_vocab], rows `stride` >= n_vocab elements
+ *   apart; any alignment of the type (16-byte aligned rows are read fastest);
+ *   temperature: device f32, one per row, or NULL: 1;
+ *   noise: device f32 [..][n_vocab] (stride as for logits): exponential variates e, for
+ *   instance -ln(u); the token of the largest p_i / e_i is drawn, the lowest index of equal
+ *   ones, which is token i with probability p_i.  A NaN excludes its token.
+ * Sums are fp64 and what decides is compared in fp64: results are those of the formulas up to
+ * comparisons closer than about 1e-6.
+ */
+
+/*
+ * Draw tokens[t] from row rows[t] of logits (device int32 [T], within 0..n_rows - 1; several
+ * draws of one row have their own noise; NULL: row t) at temperature[t], with noise row t.
+ *   tokens: device int32 [T], written; -1 for a row that is no distribution (BAD_PROBS) or
+ *   out of range (BAD_ROWS).
+ * With the drafter's logits of dflash_step it draws the drafts that dflash_tree_verify takes.
+ */
+DFLASH_API int dflash_sample(dflash_cache* c, int32_t T, int32_t n_vocab, const void* logits,
+                             int64_t logits_stride, int32_t dtype, int32_t n_rows, const int32_t* rows,
+                             const float* temperature, const float* noise, int64_t noise_stride,
+                             int32_t* tokens, void* stream);
+
+/*
+ * Sampled acceptance along trees (dflash_tree_accept is the greedy one): the accepted path
+ * and the token behind it are distributed as if the target had been sampled token by token.
+ * Node 0, the anchor, is accepted.  At an accepted node, r is the target's distribution of
+ * its row at first; its children are tried in the order of their indices: child c with token
+ * x, drawn from q, is accepted when uniform[row of c] * q(x) < r(x), and the walk goes on
+ * there; otherwise r becomes max(r - q, 0) divided by its sum.  When no child is accepted, or
+ * the path holds max_path nodes, the token behind it is drawn from r with the entry's noise.
+ *   parents, tokens: as for dflash_tree_accept (entries of up to DFLASH_MAX_TREE nodes);
+ *   target: logits of the target, row t of node t, temperature [T];
+ *   draft: logits that the drafts were drawn from: node t's token from row draft_row[t]
+ *   (device int32 [T]; NULL: row t) of n_draft, draft_temperature [n_draft]; siblings may
+ *   share a row.  NULL, or temperature 0: q is 1 at the token (argmaxes, looked-up tokens);
+ *   uniform: device f32 [T], in [0, 1); noise: device f32 [n_seq][n_vocab];
+ *   path, n_path, id_last: as for dflash_tree_accept.
+ * A target row of temperature 0 accepts its argmax alone: with all of them 0, the call is
+ * dflash_tree_accept.  A drafted token out of range is rejected (BAD_TOKEN).  An entry whose
+ * walk meets a row that is no distribution, or a draft_row out of range (BAD_PROBS), or of
+ * more nodes (BAD_ROWS), gets n_path 0 and keeps its id_last.  T + n_draft <=
+ * DFLASH_MAX_VERIFY_ROWS (TOO_MANY_ROWS).
+ */
+DFLASH_API int dflash_tree_verify(dflash_cache* c, int32_t n_seq, const int32_t* row_start, int32_t T,
+                                  const int32_t* parents, const int32_t* tokens, int32_t n_vocab,
+                                  const void* target, int64_t target_stride, int32_t target_dtype,
+                                  const float* temperature, const void* draft, int64_t draft_stride,
+                                  int32_t draft_dtype, int32_t n_draft, const int32_t* draft_row,
+                                  const float* draft_temperature, const float* uniform, const float* noise,
+                                  int64_t noise_stride, int32_t* path, int32_t max_path, int32_t* n_path,
+                                  int32_t* id_last, void* stream);
 
 /*
  * Keep an accepted path: in every layer the keys and values of slots n +
