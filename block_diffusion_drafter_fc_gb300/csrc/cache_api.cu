@@ -62,7 +62,7 @@ Layout layout(const dflash_cache_config& c) {
   L.part_ml = take(sizeof(float2) * parts);
   L.cuts = take(sizeof(Cut) * 2 * kAttendSms);
   L.norm_sums = take(sizeof(float) * kNormBlocks * 2 * c.head_dim);
-  L.stats = take(sizeof(RowStats) * kVerifyRows);
+  L.stats = take(sizeof(Piece) * kVerifyRows);
   L.scratch_bytes = off;
   return L;
 }
@@ -592,7 +592,8 @@ int dflash_tree_verify(dflash_cache* c, int32_t n_seq, const int32_t* row_start,
   if (n_vocab > kVocabMost) return DFLASH_ERR_UNSUPPORTED;
   VerifyParams p;
   if (!logits_of(target, target_stride, target_dtype, n_vocab, T, temperature, p.target)) return DFLASH_ERR_INVALID_ARG;
-  if (!draft)
+  if (draft && n_draft == 0 && T > 0) return DFLASH_ERR_INVALID_ARG;
+  if (!draft || n_draft == 0)
     p.draft = {};
   else if (!logits_of(draft, draft_stride, draft_dtype, n_vocab, n_draft, draft_temperature, p.draft))
     return DFLASH_ERR_INVALID_ARG;
@@ -609,7 +610,7 @@ int dflash_tree_verify(dflash_cache* c, int32_t n_seq, const int32_t* row_start,
   p.uniform = uniform;
   p.noise = noise;
   p.noise_ld = noise_stride;
-  p.stats = c->S<RowStats>(c->L.stats);
+  p.stats = c->S<Piece>(c->L.stats);
   p.path = path;
   p.max_path = max_path;
   p.n_path = n_path;

@@ -6,32 +6,42 @@
 //   draft distribution q is accepted when u_c q(x) < r(x); else r becomes max(r - q, 0)
 //   divided by its sum.  With none accepted, the next token is drawn from r.
 //
-// Three kernels, all over rows of n_vocab logits cut into tiles of 2048, a row's tiles going
-// round the blocks of a cluster (1 to 8; sums and maxima through distributed shared memory):
-//   row_stats   one pass over every row: sum of 2^(x s - m), s = log2(e) / T, m a whole number;
+// Three kernels, all over rows of n_vocab logits in tiles of 8 elements a thread:
+//   row_stats   one pass over every row, cut into pieces: sums of 2^(x s - m), s = log2(e) / T,
+//               m a whole number;
 //   verify      a cluster walks an entry's tree: the tests need single logits and the sums,
-//               so only a draw, and a rejection with more children to come, read a row;
+//               so only a draw, and a rejection with more children to come, read a row; its
+//               tiles go round the cluster's blocks;
 //   sample      a cluster draws a row's token: x s - log2(e), largest.
 //
 // Precision.  Which token wins and whether a test passes is decided by comparing numbers, so
-// what is compared is exact to far below the gaps: sums are fp64 of fp32 weights (m being a
-// whole number, moving it rescales exactly), tests are fp64, and in a race the candidates that
-// fp32 cannot tell apart (a block's within 2^-9) are compared again in fp64.
+// what is compared is exact to far below the gaps: sums are 64-bit whole numbers of fp32
+// weights (m being whole, moving it shifts them), a test's probabilities are 2^frac in fp32
+// times an exact power of two and the sum (2e-7); in a race the candidates that single fp32
+// operations cannot tell apart (a block's within 2^-9) are compared again as 64-bit whole
+// numbers of 2^-32.  All of it without fp64 units, of which an SM has two lanes here: with the
+// sums and the winners in fp64, 480 draws in blocks of two tiles took 69 us, without 45 (and in
+// one round of blocks 22).
 //
-// Bound: the logits' bytes at the copy rate; a small call by latency.
+// Bound: the logits' bytes at the copy rate; a small call by latency.  480 draws over 32768
+// tokens: 22 us (0.83 of the copy rate); 32 chains of 16 rows, f32, drafts drawn: 37 us, 24
+// of them the sums (0.83), then the walk and draw, some fifteen dependent steps.
 #include "verify.h"
 
 #include "cache.cuh"
 
 #include <math_constants.h>
 
+#include <algorithm>
+
 namespace dflash {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTile = 8 * kThreads;        // elements of a row that a block takes at once, 8 a thread
-constexpr double kLog2e = 1.4426950408889634;
+constexpr int kThreads = 256;              // of row_stats and sample
+constexpr int kWalkThreads = 512;          // of verify: few entries, whole rows
+constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596303e-8f;   // log2(e) in two parts
+constexpr float kUnit = 0x1p40f;           // of sums: a row's is below 2^21 (a batch of 16 is at most 64)
 constexpr float kCold = 0x1p-20f;          // temperatures below it (and not below 0) count as 0
 constexpr float kScoreMost = 0x1p30f;      // scores x log2(e) / T of this magnitude count as infinite
 
@@ -78,18 +88,18 @@ DF_DEVICE float lg2(float x) {
 // ------------------------------------------------------------------ rows
 
 // Element k of a thread's eight of the tile that begins at `tile0`.  VEC: eight neighbours
-// (vector loads: every row 16-byte aligned); else every 256th, so that a warp's loads of any
+// (vector loads: every row 16-byte aligned); else every NT-th (threads of the block), so that a warp's loads of any
 // alignment are whole lines.
-template <bool VEC>
+template <bool VEC, int NT>
 DF_DEVICE int element(int tile0, int k) {
-  return VEC ? tile0 + 8 * (int)threadIdx.x + k : tile0 + k * kThreads + (int)threadIdx.x;
+  return VEC ? tile0 + 8 * (int)threadIdx.x + k : tile0 + k * NT + (int)threadIdx.x;
 }
 
 // A thread's eight elements of a tile; `none` behind the row's end.
-template <int EL, bool VEC>
+template <int EL, bool VEC, int NT>
 DF_DEVICE void load8(const char* row, int tile0, int V, float none, float (&x)[8]) {
   if (VEC && tile0 + 8 * (int)threadIdx.x + 8 <= V) {
-    const char* at = row + (size_t)element<true>(tile0, 0) * EL;
+    const char* at = row + (size_t)element<true, NT>(tile0, 0) * EL;
     if constexpr (EL == 4) {
       const float4 a = *reinterpret_cast<const float4*>(at), b = *reinterpret_cast<const float4*>(at + 16);
       x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
@@ -106,7 +116,7 @@ DF_DEVICE void load8(const char* row, int tile0, int V, float none, float (&x)[8
   }
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const int i = element<VEC>(tile0, k);
+    const int i = element<VEC, NT>(tile0, k);
     if constexpr (EL == 4)
       x[k] = i < V ? reinterpret_cast<const float*>(row)[i] : none;
     else
@@ -124,51 +134,92 @@ DF_DEVICE Heat heat_of(float t) {
 }
 DF_DEVICE float heat_at(const float* temperature, int row) { return temperature ? temperature[row] : 1.f; }
 
+// log2(e) / t in two parts.
+struct Slope {
+  float hi, lo;
+};
+DF_DEVICE Slope slope_of(float t) {
+  Slope s;
+  s.hi = __fdiv_rn(kLog2e, t);
+  s.lo = __fdividef(fmaf(-s.hi, t, kLog2e) + kLog2eRest, t);
+  return s;
+}
+// 2^(x s - m) to 2e-7: the exponent with its rounding errors kept.
+DF_DEVICE float weight_of(float x, float s, int m) {
+  const float p = x * s, mf = (float)-m, a = p + mf, bb = a - p;
+  if (!(a > -200.f)) return a != a ? a : 0.f;
+  const float rest = fmaf(x, s, -p) + ((p - (a - bb)) + (mf - bb)), k = rintf(a);
+  return ldexpf(exp2f((a - k) + rest), (int)fminf(k, 200.f));
+}
+// Powers of two as whole numbers of 2^-32: x log2(e) / t, and log2 of a variate or a share
+// (to 4e-8).  Within 2^62 and 2^61, so that a difference fits.
+DF_DEVICE long long score_of(float x, Slope s) {
+  const float p = x * s.hi;
+  if (!(fabsf(p) < kScoreMost)) return p > 0.f ? 1ll << 62 : -(1ll << 62);
+  return __float2ll_rn(p * 0x1p32f) + __float2ll_rn((fmaf(x, s.hi, -p) + x * s.lo) * 0x1p32f);
+}
+DF_DEVICE long long log2_of(float e) {
+  if (!(e > 0.f)) return -(1ll << 61);
+  if (e == CUDART_INF_F) return 1ll << 61;
+  int k;
+  float f = frexpf(e, &k);   // [1/2, 1)
+  if (f < 0.7071f) {
+    f *= 2.f;
+    --k;
+  }
+  return (long long)k * (1ll << 32) + __float2ll_rn(log2f(f) * 0x1p32f);
+}
+
 // ------------------------------------------------------------------ reductions
 
-DF_DEVICE double warp_sum(double v) {
+DF_DEVICE long long warp_sum(long long v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// The larger key, the lower index of equal ones; NaN never wins.
-DF_DEVICE void best_of(double& v, int& i, double v2, int i2) {
+// The larger key, the lower index of equal ones (-1: none).
+DF_DEVICE void best_of(long long& v, int& i, long long v2, int i2) {
   if (i2 >= 0 && (i < 0 || v2 > v || (v2 == v && i2 < i))) {
     v = v2;
     i = i2;
   }
 }
-DF_DEVICE void warp_best(double& v, int& i) {
+DF_DEVICE void warp_best(long long& v, int& i) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const double v2 = __shfl_xor_sync(0xffffffffu, v, o);
+    const long long v2 = __shfl_xor_sync(0xffffffffu, v, o);
     const int i2 = __shfl_xor_sync(0xffffffffu, i, o);
     best_of(v, i, v2, i2);
   }
 }
+// A float's bits in its order (whole numbers).
+DF_DEVICE long long order_of(float x) {
+  const int b = __float_as_int(x == 0.f ? 0.f : x);
+  return b < 0 ? (long long)(b ^ 0x7fffffff) : (long long)b;
+}
 
 // What a block tells its cluster, twice: a block may write one while others read the other.
 struct Told {
-  double v[2];
+  long long v[2];
   int i[2], bad[2];
 };
+template <int NT>
 struct Shared {
   Told told;
-  double w_v[kThreads / 32];
-  int w_i[kThreads / 32];
-  float w_f[kThreads / 32];
+  long long w_v[NT / 32];
+  int w_i[NT / 32];
+  float w_f[NT / 32];
   int turn;      // which of the two is next (the same in all blocks)
 };
 
 // Sum of v over the cluster (all threads, the same everywhere).
-DF_DEVICE double cluster_total(double v, Shared& s, int S) {
+template <int NT>
+DF_DEVICE long long cluster_total(long long v, Shared<NT>& s, int S) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = s.turn;
   v = warp_sum(v);
   if (lane == 0) s.w_v[warp] = v;
   __syncthreads();
-  double sum = 0.0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) sum += s.w_v[w];
+  const long long sum = warp_sum(lane < NT / 32 ? s.w_v[lane] : 0ll);
   if (threadIdx.x == 0) {
     s.told.v[k] = sum;
     s.turn = k ^ 1;
@@ -178,41 +229,39 @@ DF_DEVICE double cluster_total(double v, Shared& s, int S) {
     return sum;
   }
   cluster_sync();
-  double all = 0.0;
+  long long all = 0;
   for (int r = 0; r < S; ++r) all += peer(&s.told.v[k], r);
   return all;
 }
 
 // The cluster's winner among the threads' candidates (float key in powers of two, index; -1:
-// none): those within 2^-9 and a rounding of the block's largest are compared by exact(i).
-// bad: any thread's flag.
-template <typename F>
-DF_DEVICE int cluster_winner(float key, int i, bool& bad, F exact, Shared& s, int S) {
+// none): those within 2^-9 and a rounding of the block's largest are compared by exact(), of
+// the thread's own.  bad: any thread's flag.
+template <int NT, typename F>
+DF_DEVICE int cluster_winner(float key, int i, bool& bad, F exact, Shared<NT>& s, int S) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = s.turn;
   const float mine = i >= 0 ? key : -CUDART_INF_F;
   const float w = warp_max(mine);
   if (lane == 0) s.w_f[warp] = w;
   const int any = __syncthreads_or(bad);
-  float top = s.w_f[0];
-#pragma unroll
-  for (int j = 1; j < kThreads / 32; ++j) top = fmaxf(top, s.w_f[j]);
+  const float top = warp_max(lane < NT / 32 ? s.w_f[lane] : -CUDART_INF_F);
   const float near = top - 0x1p-9f - fabsf(top) * 0x1p-20f;
-  double v = 0.0;
+  long long v = 0;
   if (i >= 0) {
     if (mine >= near || mine == top)
-      v = exact(i);
+      v = exact();
     else
       i = -1;
   }
-  warp_best(v, i);
+  if (__any_sync(0xffffffffu, i >= 0)) warp_best(v, i);
   if (lane == 0) {
     s.w_v[warp] = v;
     s.w_i[warp] = i;
   }
   __syncthreads();
   if (warp == 0) {
-    v = lane < kThreads / 32 ? s.w_v[lane] : 0.0;
-    i = lane < kThreads / 32 ? s.w_i[lane] : -1;
+    v = lane < NT / 32 ? s.w_v[lane] : 0;
+    i = lane < NT / 32 ? s.w_i[lane] : -1;
     warp_best(v, i);
     if (lane == 0) {
       s.told.v[k] = v;
@@ -225,59 +274,70 @@ DF_DEVICE int cluster_winner(float key, int i, bool& bad, F exact, Shared& s, in
     __syncthreads();
   else
     cluster_sync();
-  v = 0.0;
-  i = -1;
-  int b = 0;
-  for (int r = 0; r < S; ++r) {
-    best_of(v, i, peer(&s.told.v[k], r), peer(&s.told.i[k], r));
-    b |= peer(&s.told.bad[k], r);
-  }
-  bad = b != 0;
+  v = lane < S ? peer(&s.told.v[k], lane) : 0;
+  i = lane < S ? peer(&s.told.i[k], lane) : -1;
+  bad = __any_sync(0xffffffffu, lane < S && peer(&s.told.bad[k], lane));
+  warp_best(v, i);
   return i;
 }
 
 // ------------------------------------------------------------------ sums of rows
 
-// Rows 0 .. target_rows - 1 of the target's logits, then the drafter's.  A cluster per row.
-//
-// A thread adds up 2^(x s - m) for the first m that keeps a batch's sum below 2^40 (its first
-// batch's largest, rounded up); larger scores later make it move m and rescale, exactly.
+// Piece `g` of P of a row: the tiles g, g + P, ..  A thread adds up 2^(x s - m), m its first
+// batch's largest score, rounded up; a later batch of more than 64 makes it move m and shift
+// its sum.
 template <int EL, bool VEC>
-DF_DEVICE void row_stats(const char* row, int V, float temperature, bool draft, RowStats* out, Shared& s, int S) {
+DF_DEVICE void row_piece(const char* row, int V, float temperature, bool draft, int g, int P, Piece* out) {
+  constexpr int kTile = 8 * kThreads;
   constexpr int kTiles = EL == 2 ? 4 : 2;    // tiles of a batch: 64 bytes of a thread in flight
+  __shared__ long long w_v[kThreads / 32];
+  __shared__ float w_f[kThreads / 32];
+  __shared__ int w_i[kThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Heat heat = heat_of(temperature);
-  const int rank = cluster_rank();
   if (heat == kBadHeat || (draft && heat == kGreedy)) {   // (a greedy drafter's row is not needed)
-    if (rank == 0 && threadIdx.x == 0) *out = {heat == kBadHeat ? (double)CUDART_NAN_F : -1.0, 0, -1};
+    if (threadIdx.x == 0) *out = {heat == kBadHeat ? kNoPiece : kGreedyPiece, 0.f, -1};
     return;
   }
   if (heat == kGreedy) {
     float top = -CUDART_INF_F;
     int at = -1;
     bool bad = false;
-    for (int t0 = rank * kTile; t0 < V; t0 += S * kTile) {
+    for (int t0 = g * kTile; t0 < V; t0 += P * kTile) {
       float x[8];
-      load8<EL, VEC>(row, t0, V, -CUDART_INF_F, x);
+      load8<EL, VEC, kThreads>(row, t0, V, -CUDART_INF_F, x);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         bad |= !(x[k] < CUDART_INF_F);
         if (x[k] > top) {
           top = x[k];
-          at = element<VEC>(t0, k);
+          at = element<VEC, kThreads>(t0, k);
         }
       }
     }
-    const int arg = cluster_winner(top, at, bad, [&](int i) { return (double)logit(row, EL, i); }, s, S);
-    if (rank == 0 && threadIdx.x == 0) *out = {bad || arg < 0 ? (double)CUDART_NAN_F : -1.0, 0, arg};
+    long long v = order_of(top);
+    warp_best(v, at);
+    if (lane == 0) {
+      w_v[warp] = v;
+      w_i[warp] = at;
+    }
+    const int any = __syncthreads_or(bad);
+    if (warp == 0) {
+      v = lane < kThreads / 32 ? w_v[lane] : 0;
+      at = lane < kThreads / 32 ? w_i[lane] : -1;
+      warp_best(v, at);
+      if (lane == 0) *out = {any ? kNoPiece : kGreedyPiece, at >= 0 ? logit(row, EL, at) : 0.f, at};
+    }
     return;
   }
-  const float sc = (float)(kLog2e / temperature);
-  double sum = 0.0;
+  const float sc = slope_of(temperature).hi;
+  long long sum = 0;
+  bool bad = false;
   float m = -kScoreMost;                     // nothing seen
-  for (int t0 = rank * kTile; t0 < V; t0 += kTiles * S * kTile) {
+  for (int t0 = g * kTile; t0 < V; t0 += kTiles * P * kTile) {
     float x[kTiles][8];
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j) load8<EL, VEC>(row, t0 + j * S * kTile, V, -CUDART_INF_F, x[j]);
+    for (int j = 0; j < kTiles; ++j) load8<EL, VEC, kThreads>(row, t0 + j * P * kTile, V, -CUDART_INF_F, x[j]);
     for (bool again = false;; again = true) {
       float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -285,78 +345,113 @@ DF_DEVICE void row_stats(const char* row, int V, float temperature, bool draft, 
 #pragma unroll
         for (int k = 0; k < 8; ++k) part[k & 3] += ex2(fmaf(x[j][k], sc, -m));
       const float b = (part[0] + part[1]) + (part[2] + part[3]);
-      if (b < 0x1p40f || again) {
-        sum += (double)b;
+      if (b <= 64.f || again) {
+        bad |= !(b <= 64.f);                 // NaN or infinite
+        sum += __float2ll_rn(b * kUnit);
         break;
       }
-      float top = -CUDART_INF_F;             // (of a batch with NaN: of its numbers; its sum stays NaN)
+      float top = -CUDART_INF_F;
 #pragma unroll
       for (int j = 0; j < kTiles; ++j)
 #pragma unroll
         for (int k = 0; k < 8; ++k) top = fmaxf(top, x[j][k] * sc);
       const float to = top < kScoreMost ? ceilf(top) : m;
       if (to > m) {
-        sum = ldexp(sum, (int)fmaxf(m - to, -2000.f));
+        sum >>= (int)fminf(to - m, 63.f);
         m = to;
       }
     }
   }
   // one reference for all: the largest
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = s.turn;
   const float w = warp_max(m);
-  if (lane == 0) s.w_f[warp] = w;
+  if (lane == 0) w_f[warp] = w;
   __syncthreads();
-  float top = s.w_f[0];
+  const float top = warp_max(lane < kThreads / 32 ? w_f[lane] : -kScoreMost);
+  sum = warp_sum(sum >> (int)fminf(top - m, 63.f));
+  if (lane == 0) w_v[warp] = sum;
+  const int any = __syncthreads_or(bad);
+  if (threadIdx.x == 0) {
+    sum = w_v[0];
 #pragma unroll
-  for (int j = 1; j < kThreads / 32; ++j) top = fmaxf(top, s.w_f[j]);
-  if (S > 1) {
-    if (threadIdx.x == 0) {
-      s.told.v[k] = (double)top;
-      s.turn = k ^ 1;
-    }
-    cluster_sync();
-    for (int r = 0; r < S; ++r) top = fmaxf(top, (float)peer(&s.told.v[k], r));
+    for (int j = 1; j < kThreads / 32; ++j) sum += w_v[j];
+    *out = {any ? kNoPiece : sum, top, 0};
   }
-  // (a NaN or an infinite sum stays what it is)
-  const double z = cluster_total(sum == 0.0 ? 0.0 : ldexp(sum, (int)fmaxf(m - top, -2000.f)), s, S);
-  if (rank == 0 && threadIdx.x == 0)
-    *out = {z > 0.0 && z < CUDART_INF ? z : (double)CUDART_NAN_F, (int)top, -1};
 }
 
+// Grid: P pieces of every row of the target's logits, then the drafter's.
 template <int ELT, int ELD, bool VEC>
-__global__ void __launch_bounds__(kThreads) row_stats_kernel(const __grid_constant__ VerifyParams p, int target_rows,
-                                                             int S) {
-  __shared__ Shared s;
-  pdl_trigger();
+__global__ void __launch_bounds__(kThreads) row_stats_kernel(const __grid_constant__ VerifyParams p) {
   pdl_wait();
-  if (threadIdx.x == 0) s.turn = 0;
-  __syncthreads();
-  const int r = blockIdx.x / S, d = r - target_rows;
+  pdl_trigger();   // (behind the wait: the walk may then read what earlier launches wrote ahead of its own)
+  const int P = p.pieces, r = blockIdx.x / P, g = blockIdx.x - r * P, d = r - p.rows.T;
   if (d < 0)
-    row_stats<ELT, VEC>(p.target.at + (size_t)r * p.target.ld, p.V, heat_at(p.target.temperature, r), false, p.stats + r, s, S);
-  else
-    row_stats<ELD, VEC>(p.draft.at + (size_t)d * p.draft.ld, p.V, heat_at(p.draft.temperature, d), true, p.stats + r, s, S);
-  if (S > 1) cluster_sync();   // no block ends while another reads what it told
+    row_piece<ELT, VEC>(p.target.at + (size_t)r * p.target.ld, p.V, heat_at(p.target.temperature, r), false, g, P,
+                        p.stats + blockIdx.x);
+  else if (d < p.draft.rows)   // (a call without rows has blocks for one)
+    row_piece<ELD, VEC>(p.draft.at + (size_t)d * p.draft.ld, p.V, heat_at(p.draft.temperature, d), true, g, P,
+                        p.stats + blockIdx.x);
+}
+
+// A row's probabilities: p_i = 2^(x_i s - m) inv.  inv -1: all on token m (a target of
+// temperature 0) or not needed (a drafter's); NaN: not a distribution.
+struct RowStats {
+  float inv, s;
+  int m;
+};
+
+// Row `r` from its pieces, by `G` neighbouring lanes (a power of two, all of the warp's lanes
+// call; the result is theirs alike).
+DF_DEVICE RowStats row_of(const Piece* pieces, int P, int r, float temperature, int G) {
+  const int lane = threadIdx.x & (G - 1);
+  long long z = 0, v = 0;
+  float top = -kScoreMost;
+  int arg = -1, greedy = 0, bad = 0;
+  for (int g0 = 0; g0 < P; g0 += G) {
+    const Piece x = g0 + lane < P ? pieces[(size_t)r * P + g0 + lane] : Piece{0, -kScoreMost, -1};
+    bad |= x.z == kNoPiece;
+    if (x.z == kGreedyPiece) {
+      greedy = 1;
+      best_of(v, arg, order_of(x.m), x.arg);
+    } else if (x.z >= 0) {
+      const float to = fmaxf(top, x.m);
+      z = (z >> (int)fminf(to - top, 63.f)) + (x.z >> (int)fminf(to - x.m, 63.f));
+      top = to;
+    }
+  }
+  for (int o = G >> 1; o > 0; o >>= 1) {
+    const float to = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    z >>= (int)fminf(to - top, 63.f);
+    z += __shfl_xor_sync(0xffffffffu, z, o);
+    top = to;
+    const long long v2 = __shfl_xor_sync(0xffffffffu, v, o);
+    best_of(v, arg, v2, __shfl_xor_sync(0xffffffffu, arg, o));
+    greedy |= __shfl_xor_sync(0xffffffffu, greedy, o);
+    bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+  }
+  const float s = slope_of(temperature).hi;
+  if (bad || (!greedy && z <= 0)) return {CUDART_NAN_F, s, 0};
+  if (greedy) return {-1.f, s, arg};
+  return {__fdiv_rn(kUnit, __ll2float_rn(z)), s, (int)top};
 }
 
 // ------------------------------------------------------------------ draws
 
 // The winner of the race over a row's probabilities (bad: a NaN or +inf among the logits).
 // barred(i): tokens that have no share any more.
-template <int EL, bool VEC, typename F>
-DF_DEVICE int race(const char* row, const char* noise, int V, float temperature, bool& bad, F barred, Shared& s, int S) {
-  constexpr int kTiles = 2;
-  const double sd = kLog2e / temperature;
-  const float sc = (float)sd;
-  const float most = kScoreMost / sc;
-  float top = -kScoreMost;
+template <int EL, bool VEC, int NT, typename F>
+DF_DEVICE int race(const char* row, const char* noise, int V, float temperature, bool& bad, F barred, Shared<NT>& s,
+                   int S) {
+  constexpr int kTiles = 2, kTile = 8 * NT;
+  const Slope slope = slope_of(temperature);
+  const float sc = slope.hi, most = kScoreMost / sc;
+  float top = -kScoreMost, at_x = 0.f, at_e = 1.f;
   int at = -1;
   for (int t0 = cluster_rank() * kTile; t0 < V; t0 += kTiles * S * kTile) {
     float x[kTiles][8], e[kTiles][8];
 #pragma unroll
     for (int j = 0; j < kTiles; ++j) {
-      load8<EL, VEC>(row, t0 + j * S * kTile, V, -CUDART_INF_F, x[j]);
-      load8<4, VEC>(noise, t0 + j * S * kTile, V, 1.f, e[j]);
+      load8<EL, VEC, NT>(row, t0 + j * S * kTile, V, -CUDART_INF_F, x[j]);
+      load8<4, VEC, NT>(noise, t0 + j * S * kTile, V, 1.f, e[j]);
     }
 #pragma unroll
     for (int j = 0; j < kTiles; ++j)
@@ -364,20 +459,21 @@ DF_DEVICE int race(const char* row, const char* noise, int V, float temperature,
       for (int k = 0; k < 8; ++k) {
         bad |= !(x[j][k] < most);
         const float key = fmaf(x[j][k], sc, -lg2(e[j][k]));
-        if (key > top && !barred(element<VEC>(t0 + j * S * kTile, k))) {
+        if (key > top && !barred(element<VEC, NT>(t0 + j * S * kTile, k))) {
           top = key;
-          at = element<VEC>(t0 + j * S * kTile, k);
+          at = element<VEC, NT>(t0 + j * S * kTile, k);
+          at_x = x[j][k];
+          at_e = e[j][k];
         }
       }
   }
-  return cluster_winner(top, at, bad, [&](int i) {
-    return (double)logit(row, EL, i) * sd - log2((double)reinterpret_cast<const float*>(noise)[i]);
-  }, s, S);
+  return cluster_winner(top, at, bad, [&] { return score_of(at_x, slope) - log2_of(at_e); }, s, S);
 }
 
 template <int EL, bool VEC>
 __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ SampleParams p, int S) {
-  __shared__ Shared s;
+  constexpr int kTile = 8 * kThreads;
+  __shared__ Shared<kThreads> s;
   pdl_trigger();
   pdl_wait();
   if (threadIdx.x == 0) s.turn = 0;
@@ -401,17 +497,17 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     i = -1;
     for (int t0 = cluster_rank() * kTile; t0 < p.V; t0 += S * kTile) {
       float x[8];
-      load8<EL, VEC>(row, t0, p.V, -CUDART_INF_F, x);
+      load8<EL, VEC, kThreads>(row, t0, p.V, -CUDART_INF_F, x);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         bad |= !(x[k] < CUDART_INF_F);
         if (x[k] > top) {
           top = x[k];
-          i = element<VEC>(t0, k);
+          i = element<VEC, kThreads>(t0, k);
         }
       }
     }
-    i = cluster_winner(top, i, bad, [&](int j) { return (double)logit(row, EL, j); }, s, S);
+    i = cluster_winner(top, i, bad, [&] { return order_of(top); }, s, S);
   } else {
     i = race<EL, VEC>(row, p.noise + (size_t)t * p.noise_ld, p.V, temperature, bad, [](int) { return false; }, s, S);
   }
@@ -428,11 +524,14 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
 // ------------------------------------------------------------------ the walk
 
 struct Node {
-  double p, q;    // the target's and the drafter's probability of its token (q -1: drafted with certainty)
-  int parent, token;
+  float p, q;          // the target's and the drafter's probability of its token (before: its logits)
+  RowStats own, from;  // its row of the target; the row of the drafter that its token was drawn from
+  int token;
   float u;
-  int heat;       // of the target's row: 0, 1 (greedy) or 2 (no distribution)
+  short parent, first; // first child (0: none)
+  short is;            // bits of Is
 };
+enum Is { kNoRow = 1, kGreedyRow = 2, kNoToken = 4, kNoDraft = 8, kSure = 16, kTaken = 32 };   // (kTaken: as a first child)
 
 enum Act { kUpdate, kDraw, kDrawRest, kEnd, kBad };
 
@@ -440,56 +539,60 @@ enum Act { kUpdate, kDraw, kDrawRest, kEnd, kBad };
 // without the tokens of s_barred, until a rejection with other children behind it makes the
 // blocks write it down (s_r, each its tiles); `total` is its sum.
 template <int ELT, int ELD, bool VEC>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VerifyParams p, int S) {
-  extern __shared__ float s_r[];
-  __shared__ Shared s;
-  __shared__ Node s_node[kTreeMax];
-  __shared__ int s_path[kTreeMax], s_barred[kTreeMax];
-  __shared__ int s_act, s_child, s_cur, s_len, s_from, s_n_barred, s_written;
+__global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_constant__ VerifyParams p, int S, int most) {
+  constexpr int NT = kWalkThreads, kTile = 8 * NT;
+  extern __shared__ __align__(16) char smem[];
+  __shared__ Shared<NT> s;
+  __shared__ int s_act, s_child, s_cur, s_len, s_from, s_n_barred, s_written, s_seen;
   __shared__ double s_total;
+  // (`most`: nodes of an entry that there is room for)
+  Node* s_node = reinterpret_cast<Node*>(smem);
+  int* s_barred = reinterpret_cast<int*>(s_node + most);
+  float* s_r = reinterpret_cast<float*>(s_barred + (most + 3) / 4 * 4);
+  short* s_path = reinterpret_cast<short*>(s_r + (ELD ? p.rest : 0));
   pdl_trigger();
-  pdl_wait();
   const int e = blockIdx.x / S, rank = cluster_rank(), tid = threadIdx.x, lane = tid & 31, V = p.V;
   const bool lead = rank == 0 && tid == 0;
   int32_t* path = p.path + (size_t)e * p.max_path;
+  const char* noise = reinterpret_cast<const char*>(p.noise + (size_t)e * p.noise_ld);
   int lo, n;
-  const bool fits = entry_rows(p.rows, e, lo, n) && n <= kTreeMax;
+  const bool fits = entry_rows(p.rows, e, lo, n) && n <= most;
   if (!fits || n == 0) {   // (the whole cluster)
+    pdl_wait();
     if (!fits && lead) set_status(p.status, DEV_BAD_ROWS);
     if (rank == 0)
-      for (int j = tid; j < p.max_path; j += kThreads) path[j] = -1;
+      for (int j = tid; j < p.max_path; j += NT) path[j] = -1;
     if (lead) p.n_path[e] = 0;
     return;
   }
   auto target_row = [&](int node) { return p.target.at + (size_t)(lo + node) * p.target.ld; };
-  auto target_heat = [&](int node) { return heat_at(p.target.temperature, lo + node); };
   auto draft_of = [&](int node) { return p.draft_row ? p.draft_row[lo + node] : lo + node; };
-  // x's share of its row, in fp64
-  auto share = [](float x, float temperature, const RowStats& st) {
-    return exp2((double)x * (double)(float)(kLog2e / temperature) - st.m) / st.z;
-  };
-  // every node's test, should the walk come to it
-  for (int i = tid; i < n; i += kThreads) {
-    const RowStats own = p.stats[lo + i];
-    const int up = p.parents[lo + i], x = p.tokens[lo + i];
-    Node nd = {0.0, -1.0, i > 0 && up >= 0 && up < i ? up : -1, x, p.uniform[lo + i],
-               own.z != own.z ? 2 : own.z < 0.0 ? 1 : 0};
-    if (nd.parent >= 0 && x >= 0 && x < V) {
-      const RowStats st = p.stats[lo + up];
-      nd.p = st.z < 0.0 ? (x == st.arg ? 1.0 : 0.0) : share(logit(target_row(up), ELT, x), target_heat(up), st);
+  auto draft_row = [&](int d) { return p.draft.at + (size_t)d * p.draft.ld; };
+  auto draft_stats = [&](int d, int G) { return row_of(p.stats + (size_t)p.rows.T * p.pieces, p.pieces, d, heat_at(p.draft.temperature, d), G); };
+  // every node's test, should the walk come to it: first what the sums are not needed for
+  for (int i = tid; i < n; i += NT) {
+    const int up = p.parents[lo + i];
+    Node nd;
+    nd.parent = i > 0 && up >= 0 && up < i ? up : -1;
+    nd.token = p.tokens[lo + i];
+    nd.u = p.uniform[lo + i];
+    nd.p = nd.q = 0.f;
+    nd.first = 0;
+    nd.is = nd.token >= 0 && nd.token < V ? 0 : kNoToken;
+    if (nd.parent >= 0 && !nd.is) {
+      nd.p = logit(target_row(up), ELT, nd.token);
       if constexpr (ELD > 0) {
         const int d = draft_of(i);
-        if (d < 0 || d >= p.draft.rows) {
-          nd.q = CUDART_NAN;
-        } else {
-          const RowStats sd = p.stats[p.rows.T + d];
-          if (!(sd.z < 0.0))
-            nd.q = share(logit(p.draft.at + (size_t)d * p.draft.ld, ELD, x), heat_at(p.draft.temperature, d), sd);
-        }
+        if (d >= 0 && d < p.draft.rows)
+          nd.q = logit(draft_row(d), ELD, nd.token);
+        else
+          nd.is |= kNoDraft;
       }
     }
     s_node[i] = nd;
   }
+  for (int t0 = (rank * NT + tid) * 32; t0 < V; t0 += S * NT * 32)   // the draw's variates towards L2
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(noise + (size_t)t0 * 4));
   if (tid == 0) {
     s.turn = 0;
     s_cur = 0;
@@ -498,7 +601,52 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     s_from = 1;
     s_n_barred = 0;
     s_written = 0;
+    s_seen = 0;
     s_total = 1.0;
+  }
+  pdl_wait();
+  __syncthreads();
+  // G lanes a node: as many as a row has pieces
+  int G = 1;
+  while (G < p.pieces && G < 32) G *= 2;
+  for (int i0 = tid / 32 * (32 / G); i0 < n; i0 += NT / G) {
+    const int i = min(i0 + (tid & 31) / G, n - 1);
+    const bool mine = (tid & (G - 1)) == 0 && i0 + (tid & 31) / G < n;
+    const RowStats st = row_of(p.stats, p.pieces, lo + i, heat_at(p.target.temperature, lo + i), G);
+    if (mine) s_node[i].own = st;
+    if constexpr (ELD > 0) {
+      const int d = draft_of(i);
+      const RowStats sd = draft_stats(d >= 0 && d < p.draft.rows ? d : 0, G);
+      if (mine) s_node[i].from = sd;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += NT) {
+    Node& nd = s_node[i];
+    short is = nd.is;
+    is |= nd.own.inv != nd.own.inv ? kNoRow : nd.own.inv < 0.f ? kGreedyRow : 0;
+    float q = 1.f;
+    if constexpr (ELD > 0) {
+      if (nd.from.inv != nd.from.inv)
+        is |= kNoDraft;
+      else if (nd.from.inv < 0.f)
+        is |= kSure;
+      else
+        q = weight_of(nd.q, nd.from.s, nd.from.m) * nd.from.inv;
+    } else {
+      is |= kSure;
+    }
+    nd.q = q;
+    if (nd.parent >= 0) {
+      const RowStats st = s_node[nd.parent].own;
+      nd.p = st.inv < 0.f ? (nd.token == st.m ? 1.f : 0.f) : weight_of(nd.p, st.s, st.m) * st.inv;
+      if ((double)nd.u * (double)q < (double)nd.p) is |= kTaken;
+      // (the parent's first child: no node between is its child)
+      bool least = true;
+      for (int j = nd.parent + 1; j < i && least; ++j) least = s_node[j].parent != nd.parent;
+      if (least) s_node[nd.parent].first = i;
+    }
+    nd.is = is;
   }
   __syncthreads();
 
@@ -507,38 +655,48 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     if (tid < 32) {
       int cur = s_cur, len = s_len, from = s_from, barred = s_n_barred, written = s_written, child = -1, act = -1;
       double total = s_total;
+      bool fresh = from == 1 && len == 1;   // no child of cur has been tried
       while (act < 0) {
-        const int heat = s_node[cur].heat;
-        if (heat == 2) {
+        const int row = s_node[cur].is;
+        if (row & kNoRow) {
           act = kBad;
           break;
         }
         int next = -1;   // the first child of cur from `from` on
-        if (len < p.max_path)
-          for (int b = from; b < n && next < 0; b += 32) {
-            const unsigned is = __ballot_sync(0xffffffffu, b + lane < n && s_node[min(b + lane, n - 1)].parent == cur);
-            if (is) next = b + __ffs(is) - 1;
+        if (len < p.max_path) {
+          if (fresh) {
+            next = s_node[cur].first - 1;
+            if (next >= 0) ++next;
+          } else {
+            for (int b = from; b < n && next < 0; b += 32) {
+              const unsigned is = __ballot_sync(0xffffffffu, b + lane < n && s_node[min(b + lane, n - 1)].parent == cur);
+              if (is) next = b + __ffs(is) - 1;
+            }
           }
+        }
         if (next < 0) {
-          act = heat == 1 ? kEnd : child >= 0 ? kDrawRest : kDraw;
+          act = row & kGreedyRow ? kEnd : child >= 0 ? kDrawRest : kDraw;
           break;
         }
         if (child >= 0) {   // the rejected child's distribution has to be taken off first
           act = kUpdate;
           break;
         }
-        const Node nd = s_node[next];
+        const Node& nd = s_node[next];
+        const int is = nd.is;
         from = next + 1;
-        if (nd.token < 0 || nd.token >= V) {
+        if (is & kNoToken) {
           if (lead) set_status(p.status, DEV_BAD_TOKEN);
+          fresh = false;
           continue;
         }
-        if (nd.q != nd.q) {
+        if (is & kNoDraft) {
           act = kBad;
           break;
         }
+        bool taken = is & kTaken;
         double r = nd.p;
-        if (heat == 0) {
+        if (!(row & kGreedyRow) && (barred || written)) {
           int out = 0;
           for (int j = lane; j < barred; j += 32) out |= s_barred[j] == nd.token;
           const bool gone = __any_sync(0xffffffffu, out) || !(total > 0.0);
@@ -547,17 +705,22 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
             r = (double)peer(s_r + tile / S * kTile + (nd.token - tile * kTile), tile % S);
           }
           r = gone ? 0.0 : r / total;
+          taken = (double)nd.u * (double)nd.q < r;
         }
-        const bool sure = nd.q < 0.0;
-        if ((double)nd.u * (sure ? 1.0 : nd.q) < r) {
+        if (taken) {
           if (lane == 0) s_path[len] = next;
           ++len;
           cur = next;
           barred = written = 0;
           total = 1.0;
-        } else if (heat == 0 && !sure) {
+          fresh = true;
+          continue;
+        }
+        fresh = false;
+        if (row & kGreedyRow) continue;
+        if (!(is & kSure)) {
           child = next;
-        } else if (heat == 0 && r > 0.0) {
+        } else if (r > 0.0) {
           if (lane == 0) s_barred[barred] = nd.token;
           ++barred;
           total -= r * total;
@@ -575,43 +738,41 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
         s_total = total;
       }
     }
-    // (no block changes s_r while the walk of another may still look into it)
-    if (S > 1)
-      cluster_sync();
-    else
-      __syncthreads();
+    __syncthreads();
     if (s_act != kUpdate) break;
 
     // ---- r becomes max(r - q, 0), written down
     if constexpr (ELD > 0) {
-      const int cur = s_cur, d = draft_of(s_child), barred = s_n_barred, written = s_written;
-      const RowStats st = p.stats[lo + cur], sd = p.stats[p.rows.T + d];
-      const float sc = (float)(kLog2e / target_heat(cur)), scd = (float)(kLog2e / heat_at(p.draft.temperature, d));
-      const float inv = (float)(1.0 / ((written ? 1.0 : st.z) * s_total)), inv_d = (float)(1.0 / sd.z);
-      const char *row = target_row(cur), *row_d = p.draft.at + (size_t)d * p.draft.ld;
-      double sum = 0.0;
+      if (S > 1 && s_seen) cluster_sync();   // no block changes s_r while the walk of another looks into it
+      const int cur = s_cur, barred = s_n_barred, written = s_written;
+      const RowStats st = s_node[cur].own, sd = s_node[s_child].from;
+      const float inv = (written ? 1.f : st.inv) / (float)s_total, inv_d = sd.inv, m = (float)-st.m, md = (float)-sd.m;
+      const char *row = target_row(cur), *row_d = draft_row(draft_of(s_child));
+      long long units = 0;   // of 2^-50 (r adds up to at most 1)
+#pragma unroll 2
       for (int t0 = rank * kTile, at = 0; t0 < V; t0 += S * kTile, at += kTile) {
         float x[8], y[8];
-        load8<ELD, VEC>(row_d, t0, V, -CUDART_INF_F, y);
-        if (!written) load8<ELT, VEC>(row, t0, V, -CUDART_INF_F, x);
+        load8<ELD, VEC, NT>(row_d, t0, V, -CUDART_INF_F, y);
+        if (!written) load8<ELT, VEC, NT>(row, t0, V, -CUDART_INF_F, x);
         float part = 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int i = element<VEC>(t0, k);
-          float r = written ? s_r[at + i - t0] : ex2(fmaf(x[k], sc, (float)-st.m));
+          const int i = element<VEC, NT>(t0, k);
+          float r = written ? s_r[at + i - t0] : ex2(fmaf(x[k], st.s, m));
           for (int j = 0; j < barred; ++j)
             if (s_barred[j] == i) r = 0.f;
-          r = fmaxf(fmaf(r, inv, -ex2(fmaf(y[k], scd, (float)-sd.m)) * inv_d), 0.f);
+          r = fmaxf(fmaf(r, inv, -ex2(fmaf(y[k], sd.s, md)) * inv_d), 0.f);
           s_r[at + i - t0] = r;
           part += r;
         }
-        sum += (double)part;
+        units += __float2ll_rn(part * 0x1p50f);
       }
-      sum = cluster_total(sum, s, S);
+      const double sum = (double)cluster_total(units, s, S) * 0x1p-50;
       if (tid == 0) {   // (nothing left, by rounding alone: the target's own)
         s_written = sum > 0.0;
         s_total = sum > 0.0 ? sum : 1.0;
         s_n_barred = 0;
+        s_seen = 1;
       }
       __syncthreads();
     }
@@ -619,71 +780,68 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
 
   // ---- the token behind the path
   const int act = s_act, cur = s_cur, barred = s_n_barred, written = s_written;
-  const RowStats st = p.stats[lo + cur];
-  const char* noise = reinterpret_cast<const char*>(p.noise + (size_t)e * p.noise_ld);
-  const float* noise_f = reinterpret_cast<const float*>(noise);
+  const RowStats st = s_node[cur].own;
+  const float temperature = heat_at(p.target.temperature, lo + cur);
   auto is_barred = [&](int i) {
     for (int j = 0; j < barred; ++j)
       if (s_barred[j] == i) return true;
     return false;
   };
-  int token = act == kEnd ? st.arg : -1;
+  int token = act == kEnd ? st.m : -1;
   bool bad = false;
   if (act == kDrawRest || (act == kDraw && written)) {
     const bool less = ELD > 0 && act == kDrawRest;   // a last child's q comes off on the way
-    const int d = less ? draft_of(s_child) : 0;
-    RowStats sd = {1.0, 0, 0};
-    double sdd = 0.0;
+    RowStats sd = {1.f, 0.f, 0};
     const char* row_d = nullptr;
     if (less) {
-      sd = p.stats[p.rows.T + d];
-      sdd = (double)(float)(kLog2e / heat_at(p.draft.temperature, d));
-      row_d = p.draft.at + (size_t)d * p.draft.ld;
+      sd = s_node[s_child].from;
+      row_d = draft_row(draft_of(s_child));
     }
-    const double st_s = (double)(float)(kLog2e / target_heat(cur)), all = (written ? 1.0 : st.z) * s_total;
-    const float sc = (float)st_s, scd = (float)sdd, inv = (float)(1.0 / all), inv_d = (float)(1.0 / sd.z);
+    const float inv = (written ? 1.f : st.inv) / (float)s_total, inv_d = sd.inv, m = (float)-st.m, md = (float)-sd.m;
     const char* row = target_row(cur);
-    float top = -CUDART_INF_F;
+    float top = -CUDART_INF_F, at_x = 0.f, at_y = 0.f, at_e = 1.f;
     int win = -1;
+#pragma unroll 2
     for (int t0 = rank * kTile, at = 0; t0 < V; t0 += S * kTile, at += kTile) {
       float x[8], y[8], z[8];
-      load8<4, VEC>(noise, t0, V, 1.f, z);
+      load8<4, VEC, NT>(noise, t0, V, 1.f, z);
       if constexpr (ELD > 0) {
-        if (less) load8<ELD, VEC>(row_d, t0, V, -CUDART_INF_F, y);
+        if (less) load8<ELD, VEC, NT>(row_d, t0, V, -CUDART_INF_F, y);
       }
-      if (!written) load8<ELT, VEC>(row, t0, V, -CUDART_INF_F, x);
+      if (!written) load8<ELT, VEC, NT>(row, t0, V, -CUDART_INF_F, x);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int i = element<VEC>(t0, k);
-        float r = (written ? s_r[at + i - t0] : ex2(fmaf(x[k], sc, (float)-st.m))) * inv;
-        if (less) r = r - ex2(fmaf(y[k], scd, (float)-sd.m)) * inv_d;
+        const int i = element<VEC, NT>(t0, k);
+        if (written) x[k] = s_r[at + i - t0];
+        float r = (written ? x[k] : ex2(fmaf(x[k], st.s, m))) * inv;
+        if (less) r = r - ex2(fmaf(y[k], sd.s, md)) * inv_d;
         const float key = lg2(r) - lg2(z[k]);   // (NaN for what is not positive)
         if (i < V && r > 0.f && key > top && !is_barred(i)) {
           top = key;
           win = i;
+          at_x = x[k];
+          at_e = z[k];
+          if (less) at_y = y[k];
         }
       }
     }
-    token = cluster_winner(top, win, bad, [&](int i) {
-      const int tile = i / kTile;
-      double r = written ? (double)s_r[tile / S * kTile + (i - tile * kTile)] : exp2((double)logit(row, ELT, i) * st_s - st.m);
-      r /= all;
-      if constexpr (ELD > 0)
-        if (less) r -= exp2((double)logit(row_d, ELD, i) * sdd - sd.m) / sd.z;
-      return log2(fmax(r, 0.0)) - log2((double)noise_f[i]);
+    token = cluster_winner(top, win, bad, [&] {
+      float r = (written ? at_x : weight_of(at_x, st.s, st.m)) * inv;
+      if (less) r = fmaf(-weight_of(at_y, sd.s, sd.m), inv_d, r);
+      return log2_of(r) - log2_of(at_e);
     }, s, S);
   }
-  // (a rest that rounding left nothing of: the target's own)
+  // the target's own row: the usual draw, or because rounding left nothing of the rest
   if (token < 0 && (act == kDraw || act == kDrawRest)) {
     const bool rest = act == kDraw && !written;
-    token = race<ELT, VEC>(target_row(cur), noise, V, target_heat(cur), bad, [&](int i) { return rest && is_barred(i); }, s, S);
+    token = race<ELT, VEC>(target_row(cur), noise, V, temperature, bad, [&](int i) { return rest && is_barred(i); }, s, S);
     if (token < 0 && rest && barred > 0)
-      token = race<ELT, VEC>(target_row(cur), noise, V, target_heat(cur), bad, [](int) { return false; }, s, S);
+      token = race<ELT, VEC>(target_row(cur), noise, V, temperature, bad, [](int) { return false; }, s, S);
   }
   const bool none = token < 0 || bad;
   if (rank == 0) {
     const int len = none ? 0 : s_len;
-    for (int j = tid; j < p.max_path; j += kThreads) path[j] = j < len ? s_path[j] : -1;
+    for (int j = tid; j < p.max_path; j += NT) path[j] = j < len ? s_path[j] : -1;
     if (tid == 0) {
       p.n_path[e] = len;
       if (none)
@@ -702,20 +860,19 @@ bool vector_rows(const void* at, int64_t ld_bytes) {
 }
 bool vector_rows(const Logits& x) { return vector_rows(x.at, x.ld); }
 
-// Blocks of a cluster: as many as keep the GPU's blocks within `most`, at least `least`, no
+// Blocks of a cluster: as many as keep the launch within `most` blocks, at least `least`, no
 // more than a row has tiles.
-int cluster_of(int64_t rows, int V, int most, int least) {
+int cluster_of(int64_t rows, int tiles, int most, int least) {
   int S = 1;
-  const int tiles = (V + kTile - 1) / kTile;
   while (S < 8 && (S < least || (rows * 2 * S <= most && 2 * S <= tiles))) S *= 2;
   return S;
 }
 
 template <typename K, typename... A>
-cudaError_t launch_clusters(K* kernel, int64_t rows, int S, size_t smem, cudaStream_t st, A... args) {
+cudaError_t launch_clusters(K* kernel, int64_t rows, int S, int threads, size_t smem, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * S));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
@@ -724,35 +881,42 @@ cudaError_t launch_clusters(K* kernel, int64_t rows, int S, size_t smem, cudaStr
   at[1].id = cudaLaunchAttributeClusterDimension;
   at[1].val.clusterDim = {(unsigned)S, 1, 1};
   cfg.attrs = at;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = S > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-constexpr int kBlocks = 152 * 8;   // blocks that the GPU holds at once
-constexpr size_t kRestMost = sizeof(float) * kTile * (kVocabMost / 8 / kTile);
+constexpr int kSms = 152;
+constexpr size_t kRestMost = sizeof(float) * (kVocabMost / 8);   // a block's share of the largest vocabulary
+constexpr size_t kNodeBytes = sizeof(Node) + sizeof(int) + sizeof(short);
+constexpr size_t kSmemMost = kRestMost + kTreeMax * kNodeBytes + 16;
+static_assert(kVocabMost % (8 * 8 * kWalkThreads) == 0, "whole tiles");
+static_assert(kSmemMost <= 225 * 1024, "shared memory");
 
 template <int ELT, int ELD, bool VEC>
-cudaError_t verify_as(const VerifyParams& p, cudaStream_t st) {
-  const int rows = p.rows.T + (ELD ? p.draft.rows : 0);
-  const int S = cluster_of(rows, p.V, kBlocks, 1);
-  cudaError_t e = cudaSuccess;
-  if (rows > 0)
-    e = launch_clusters(row_stats_kernel<ELT, ELD ? ELD : 4, VEC>, rows, S, 0, st, p, p.rows.T, S);
+cudaError_t verify_as(VerifyParams& p, cudaStream_t st) {
+  const int rows = p.rows.T + (ELD ? p.draft.rows : 0), tiles = (p.V + 8 * kThreads - 1) / (8 * kThreads);
+  // pieces of a row: enough blocks for six rounds of the GPU's, each of two tiles at least
+  p.pieces = (int)std::min<int64_t>(std::max(rows > 0 ? kSms * 30 / rows : 1, 1), (tiles + 1) / 2);
+  // (without rows too: the walk may start ahead of this launch's end, not of what came before)
+  const cudaError_t e = launch_dependent(row_stats_kernel<ELT, ELD ? ELD : 4, VEC>, dim3(std::max(rows, 1) * p.pieces),
+                                         kThreads, 0, st, p);
   if (e != cudaSuccess) return e;
-  const int tiles = (p.V + kTile - 1) / kTile, most = (int)(kRestMost / sizeof(float) / kTile);
-  const int W = cluster_of(p.rows.n_seq, p.V, kBlocks / 4, (tiles + most - 1) / most);
-  const size_t smem = ELD ? sizeof(float) * kTile * ((tiles + W - 1) / W) : 0;
-  return launch_clusters(verify_kernel<ELT, ELD, VEC>, p.rows.n_seq, W, smem, st, p, W);
+  const int walk_tiles = (p.V + 8 * kWalkThreads - 1) / (8 * kWalkThreads), most = kVocabMost / (8 * 8 * kWalkThreads);
+  const int W = cluster_of(p.rows.n_seq, walk_tiles, kSms, (walk_tiles + most - 1) / most);
+  const int nodes = std::max(std::min(p.rows.T, kTreeMax), 1);
+  p.rest = ELD ? 8 * kWalkThreads * ((walk_tiles + W - 1) / W) : 0;
+  return launch_clusters(verify_kernel<ELT, ELD, VEC>, p.rows.n_seq, W, kWalkThreads,
+                         nodes * kNodeBytes + 16 + sizeof(float) * p.rest, st, p, W, nodes);
 }
 
 template <int ELT, int ELD>
-cudaError_t verify_by_rows(const VerifyParams& p, cudaStream_t st) {
+cudaError_t verify_by_rows(VerifyParams& p, cudaStream_t st) {
   const bool vec = vector_rows(p.target) && (!ELD || vector_rows(p.draft)) && vector_rows(p.noise, p.noise_ld * 4);
   return vec ? verify_as<ELT, ELD, true>(p, st) : verify_as<ELT, ELD, false>(p, st);
 }
 
 template <int ELT>
-cudaError_t verify_by_draft(const VerifyParams& p, cudaStream_t st) {
+cudaError_t verify_by_draft(VerifyParams& p, cudaStream_t st) {
   return !p.draft.at ? verify_by_rows<ELT, 0>(p, st) : p.draft.el == 4 ? verify_by_rows<ELT, 4>(p, st)
                                                                        : verify_by_rows<ELT, 2>(p, st);
 }
@@ -760,30 +924,32 @@ cudaError_t verify_by_draft(const VerifyParams& p, cudaStream_t st) {
 template <int ELT, int ELD>
 cudaError_t raise_smem() {
   const cudaError_t e = cudaFuncSetAttribute(verify_kernel<ELT, ELD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)kRestMost);
+                                             (int)kSmemMost);
   if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(verify_kernel<ELT, ELD, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRestMost);
+  return cudaFuncSetAttribute(verify_kernel<ELT, ELD, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost);
 }
 
 template <int EL>
 cudaError_t sample_as(const SampleParams& p, cudaStream_t st) {
-  const int S = cluster_of(p.T, p.V, kBlocks, 1);
+  const int S = cluster_of(p.T, (p.V + 8 * kThreads - 1) / (8 * kThreads), kSms * 4, 1);
   return vector_rows(p.logits) && vector_rows(p.noise, p.noise_ld)
-             ? launch_clusters(sample_kernel<EL, true>, p.T, S, 0, st, p, S)
-             : launch_clusters(sample_kernel<EL, false>, p.T, S, 0, st, p, S);
+             ? launch_clusters(sample_kernel<EL, true>, p.T, S, kThreads, 0, st, p, S)
+             : launch_clusters(sample_kernel<EL, false>, p.T, S, kThreads, 0, st, p, S);
 }
 
 }  // namespace
 
 cudaError_t configure_verify() {
-  cudaError_t e = raise_smem<2, 2>();
+  cudaError_t e = raise_smem<2, 0>();
+  if (e == cudaSuccess) e = raise_smem<4, 0>();
+  if (e == cudaSuccess) e = raise_smem<2, 2>();
   if (e == cudaSuccess) e = raise_smem<2, 4>();
   if (e == cudaSuccess) e = raise_smem<4, 2>();
   if (e == cudaSuccess) e = raise_smem<4, 4>();
   return e;
 }
 
-cudaError_t launch_verify(const VerifyParams& p, cudaStream_t st) {
+cudaError_t launch_verify(VerifyParams p, cudaStream_t st) {
   return p.target.el == 4 ? verify_by_draft<4>(p, st) : verify_by_draft<2>(p, st);
 }
 

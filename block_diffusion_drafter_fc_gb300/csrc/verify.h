@@ -5,8 +5,8 @@
 
 namespace dflash {
 
-constexpr int kVocabMost = 327680;     // a block of a cluster of 8 holds 20 tiles of a row
-constexpr int kVerifyRows = 65536;     // rows of logits of one call
+constexpr int kVocabMost = 327680;     // a block of a cluster of 8 holds an eighth of a row in fp32
+constexpr int kVerifyRows = 65536;     // rows of logits of one call, and pieces of them
 
 // Rows of logits, f32 or bf16.
 struct Logits {
@@ -16,11 +16,13 @@ struct Logits {
   const float* temperature;    // [rows], null: 1
 };
 
-// A row's probabilities: p_i = 2^(x_i s - m) / z.  z -1: all on `arg` (a target of temperature 0)
-// or not needed (a drafter's); NaN: not a distribution.
-struct RowStats {
-  double z;
-  int m, arg;
+// A piece of a row: z 2^-40 is the sum of 2^(x s - m).  kGreedyPiece: its largest logit m, at
+// `arg` (a target of temperature 0), or not needed (a drafter's); kNoPiece: no distribution.
+constexpr long long kGreedyPiece = -1, kNoPiece = -2;
+struct Piece {
+  long long z;
+  float m;
+  int arg;
 };
 
 struct VerifyParams {
@@ -30,13 +32,14 @@ struct VerifyParams {
   const int32_t *parents, *tokens, *draft_row;
   const float *uniform, *noise;
   int64_t noise_ld;            // elements
-  RowStats* stats;             // [T + draft rows]
+  Piece* stats;                // [T + draft rows][pieces]
+  int pieces, rest;            // (set by launch_verify: pieces of a row, a block's share of a rest)
   int32_t* path;
   int max_path;
   int32_t *n_path, *id_last;
   unsigned* status;
 };
-cudaError_t launch_verify(const VerifyParams& p, cudaStream_t st);
+cudaError_t launch_verify(VerifyParams p, cudaStream_t st);
 
 struct SampleParams {
   int T, V, n_rows;

@@ -743,9 +743,11 @@ class PagedCache:
             raise DFlashError("tree_verify: target has a row of logits for every node")
         e, es = self._noise("tree_verify", noise, n, vocab)
         d, ds, dc, nd = 0, 0, 0, 0
+        if draft is not None and not T:
+            draft = draft_row = draft_temperature = None
         if draft is not None:
             d, ds, dc, nd, dv = self._logits("tree_verify", draft)
-            if dv != vocab or draft_row is None and nd < T:
+            if dv != vocab or (nd < T if draft_row is None else T and not nd):
                 raise DFlashError("tree_verify: draft is [n_draft][n_vocab], a row for every node without draft_row")
         elif draft_row is not None or draft_temperature is not None:
             raise DFlashError("tree_verify: draft_row and draft_temperature go with draft")

@@ -785,8 +785,8 @@ DFLASH_API int dflash_tree_accept(dflash_cache* c, int32_t n_seq, const int32_t*
  *   noise: device f32 [..][n_vocab] (stride as for logits): exponential variates e, for
  *   instance -ln(u); the token of the largest p_i / e_i is drawn, the lowest index of equal
  *   ones, which is token i with probability p_i.  A NaN excludes its token.
- * Sums are fp64 and what decides is compared in fp64: results are those of the formulas up to
- * comparisons closer than about 1e-6.
+ * Results are those of the formulas up to comparisons that are closer than about 1e-6, and do
+ * not depend on the order of anything.
  */
 
 /*
