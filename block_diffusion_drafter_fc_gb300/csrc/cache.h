@@ -81,6 +81,7 @@ struct AppendParams {
   float per_dim, eps;
 };
 cudaError_t launch_append(const AppendParams& p, cudaStream_t st);
+cudaError_t launch_norm_append(const AppendParams& p, cudaStream_t st);
 
 // Norm and rotation of T rows' query heads (part 0) and key heads (part 1), or the
 // gradient.  A part without heads has none.
@@ -101,7 +102,7 @@ struct NormRopeParams {
   float* sums;              // gradient: [kNormBlocks][2][hd]
   unsigned* status;
 };
-constexpr int kNormBlocks = 608;   // most blocks of a gradient's launch: 4 on each of 152 SMs
+constexpr int kNormBlocks = 608;   // most blocks of a gradient's launch (rows of up to 608 x 256 items)
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t st);
 cudaError_t launch_norm_rope_grad(const NormRopeParams& p, cudaStream_t st);
 

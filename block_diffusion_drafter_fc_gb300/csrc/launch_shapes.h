@@ -100,4 +100,54 @@ inline Shape append_shape(int T, int items, int rd) {
 inline uint32_t append_magic(const Shape& s, int items) { return quotient_magic(s.rows > 1 ? items : 1 << 30); }
 
 }  // namespace rope
+
+// ------------------------------------------------------------------ norms of heads
+
+namespace norm {
+
+constexpr int kThreads = 256;   // most threads of a block
+constexpr int kMaxRows = 32;    // rows whose angles a block holds at once
+
+// A block's threads own items of a row (its columns), `side` rows side by side where rows are
+// short, and walk down rows: gx blocks of `rows` rows, gy of columns.
+struct Shape {
+  int cols, side, threads, rows, gx, gy;
+};
+inline Shape columns_of(int items) {
+  Shape s = {};
+  s.gy = (items + kThreads - 1) / kThreads;
+  s.cols = s.gy == 1 ? items : ((items + s.gy - 1) / s.gy + 31) / 32 * 32;
+  s.side = s.cols < 256 ? 256 / s.cols : 1;
+  if (s.side > kMaxRows) s.side = kMaxRows;
+  s.threads = (s.cols * s.side + 31) / 32 * 32;
+  return s;
+}
+constexpr int kSms = 152;
+// Blocks that the GPU holds at once, `threads` threads an SM.
+inline int wave_of(const Shape& s, int threads) { return kSms * (threads / s.threads > 1 ? threads / s.threads : 1); }
+// Whole rounds of blocks of up to kMaxRows rows.
+inline Shape shape_of(int T, int items, int threads) {
+  Shape s = columns_of(items);
+  const int wave = wave_of(s, threads);
+  const long long per = (long long)T * s.gy, round = (long long)wave * (kMaxRows / s.side * s.side);
+  const long long waves = (per + round - 1) / round;
+  long long rows = (per + wave * waves - 1) / (wave * waves);
+  rows = (rows + s.side - 1) / s.side * s.side;
+  s.rows = (int)(rows < kMaxRows / s.side * s.side ? rows : kMaxRows / s.side * s.side);
+  s.gx = (int)(((long long)T + s.rows - 1) / s.rows);
+  return s;
+}
+// One round of blocks of any number of rows, at most `limit`.
+inline Shape sum_shape_of(int T, int items, int threads, int limit) {
+  Shape s = columns_of(items);
+  const int most = wave_of(s, threads) < limit ? wave_of(s, threads) : limit;
+  const int least = (T + s.side - 1) / s.side, gx = most / s.gy > 1 ? most / s.gy : 1;
+  s.gx = gx < least ? gx : least;
+  s.rows = (T + s.gx - 1) / s.gx;
+  s.rows = (s.rows + s.side - 1) / s.side * s.side;
+  s.gx = (int)(((long long)T + s.rows - 1) / s.rows);
+  return s;
+}
+
+}  // namespace norm
 }  // namespace dflash

@@ -1,14 +1,22 @@
-// Norm of every query and key head and its rotation in one pass, and the gradient.
+// Norm of every query and key head and its rotation in one pass: of rows, fused with the
+// append of keys and values to the cache, and the gradient.
 //
 //   n = x / sqrt(mean(x^2) + eps) over a head's dims, y = R(p) (w * n), R the rotation of
 //   rope.cu (dims from rotary_dim on keep w * n).
 //   With g = R(p)^T dy:  dw = sum over rows and heads of g * n,  dn = g * w,
 //   dx = (dn - n mean(dn * n)) / sqrt(mean(x^2) + eps).
 //
-// A head lies with 2 to 16 neighbouring lanes (an item of two vectors each, rope.cuh), so
-// its sums are shuffles and every value is read and written once: bytes at the copy rate
-// are the floor.  All arithmetic is fp32; y and dx are rounded once, to their type.
+// Every value is read and written once: bytes at the copy rate are the floor.  All arithmetic
+// is fp32; y and dx are rounded once, to their type.
+//
+// A head lies with 2 to 16 neighbouring lanes (an item of two vectors each, rope.cuh), so its
+// sums are shuffles.  A thread owns an item of the row and walks down rows: its head, weights
+// and addresses' steps do not change, and the next rows' loads are under way.  (Walking along
+// a row's items instead, as the append of rope.cu does, took 370 instructions an item, 60% of
+// the issue slots, and 46 us for the append of 8192 rows, 56 for the gradient of 8191.)
 #include "rope.cuh"
+
+#include <algorithm>
 
 namespace dflash {
 
@@ -16,277 +24,419 @@ using namespace rope;
 
 namespace {
 
-// Row `t`'s item `it`: its part, head's bytes and place in the head.
-struct Where {
-  int part, i;
-  size_t head;   // bytes from the row's start
+constexpr int kMost = norm::kThreads, kRows = norm::kMaxRows;
+constexpr int kGradRows = 2 * kRows;   // a gradient's: an even number of rounds, whatever rows lie side by side
+
+// Queries, keys and (of the append) values.
+struct NormRows {
+  RopeView r;
+  int T, hd, heads[3];
+  const char* x[3];
+  const char* w[2];
+  char* out[2];
+  int64_t x_ld[3], out_ld[2];   // bytes
+  float per_dim, eps;
+  const int32_t* pos;
+  unsigned* status;
+  AppendParams a;               // of the append: rows, pages
 };
-DF_DEVICE Where where(const NormRopeParams& p, int it, int li, int hd_bytes) {
-  const int h = it >> li, k = h >= p.part[0].heads;
-  return {k, it - (h << li), (size_t)(h - (k ? p.part[0].heads : 0)) * hd_bytes};
+
+// A row's angles: two pairs' cosines and sines (16 bytes) of every item, then of their next
+// two, so that neighbouring lanes read neighbouring words.
+template <int E>
+DF_DEVICE void put_angle(float* row, const RopeView& r, int pos, int j, bool backward) {
+  const int i = j / E, e = j - i * E;
+  float* at = row + ((e >> 1) * (r.rd / (2 * E)) + i) * 4 + (e & 1);
+  const float2 cs = angle(r, pos, j, backward);
+  at[0] = cs.x;
+  at[2] = cs.y;
+}
+template <int E>
+DF_DEVICE void turn_item(float (&f)[2 * E], const float* row, int i, const RopeView& r) {
+  const float4* t4 = reinterpret_cast<const float4*>(row) + i;
+  const int step = r.rd / (2 * E);
+  auto pair = [](float& x, float& y, float c, float s) {
+    const float a = x, b = y;
+    x = a * c - b * s;
+    y = b * c + a * s;
+  };
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    const float4 t = t4[e / 2 * step];
+    if (r.interleaved) {
+      pair(f[2 * e], f[2 * e + 1], t.x, t.z);
+      pair(f[2 * e + 2], f[2 * e + 3], t.y, t.w);
+    } else {
+      pair(f[e], f[E + e], t.x, t.z);
+      pair(f[e + 1], f[E + e + 1], t.y, t.w);
+    }
+  }
 }
 
-template <int EL, int VB, int U>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p,
-                                                             int rows_per_block, int span, uint32_t width_magic) {
+// Two fp32 operations at a time.
+DF_DEVICE void mul2(float& x, float& y, float a, float b) {
+  asm("{\n .reg .b64 p, q;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n mul.rn.f32x2 p, p, q;\n"
+      " mov.b64 {%0, %1}, p;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+DF_DEVICE void fma2(float& x, float& y, float a0, float a1, float b0, float b1) {   // += a b
+  asm("{\n .reg .b64 p, q, d;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n mov.b64 d, {%0, %1};\n"
+      " fma.rn.f32x2 d, p, q, d;\n mov.b64 {%0, %1}, d;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// Sum over the 2, 4, 8 or 16 neighbouring lanes that hold a head (all lanes of the warp).
+DF_DEVICE float head_sum(float v, int lanes) {
+  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int E>
+DF_DEVICE float dot_item(const float (&a)[2 * E], const float (&b)[2 * E]) {
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+  for (int e = 0; e < 2 * E; e += 2) fma2(s0, s1, a[e], a[e + 1], b[e], b[e + 1]);
+  return s0 + s1;
+}
+// 1 / root mean square of the head.
+template <int E>
+DF_DEVICE float norm_of(const float (&f)[2 * E], int lanes, float per_dim, float eps) {
+  return rsqrtf(fmaf(head_sum(dot_item<E>(f, f), lanes), per_dim, eps));
+}
+
+// A thread's column: item `it` of the rows.
+template <int E>
+struct Column {
+  int part, h, place, o0, o1;   // part: 0 queries, 1 keys, 2 values
+  bool rot;
+  DF_DEVICE Column(const int (&heads)[3], const RopeView& r, int hd, int it) {
+    const int ipr = hd / (2 * E);
+    h = it / ipr;
+    place = it - h * ipr;
+    part = h < heads[0] ? 0 : h < heads[0] + heads[1] ? 1 : 2;
+    h -= part == 0 ? 0 : part == 1 ? heads[0] : heads[0] + heads[1];
+    rot = item_offsets<E>(r, place, o0, o1);
+  }
+};
+
+template <int EL, int VB, bool CACHE>
+__global__ void __launch_bounds__(kMost, 3) norm_rows_kernel(const __grid_constant__ NormRows p, norm::Shape s) {
   using V = typename Vec<VB>::T;
-  constexpr int E = VB / EL;
-  extern __shared__ float2 cs[];   // [rows][rd / 2]
-  __shared__ int s_pos[kMaxRows];
+  constexpr int E = VB / EL, kAhead = 2;   // rows on their way
+  extern __shared__ __align__(16) float cs[];   // [rows][rd]
+  __shared__ int s_pos[kRows];
+  __shared__ long long s_dst[kRows];
   pdl_trigger();
   pdl_wait();
-  const int ipr = p.hd / (2 * E), li = __ffs(ipr) - 1, half = p.r.rd / 2, hb = p.hd * EL;
-  const int items = (p.part[0].heads + p.part[1].heads) * ipr;
-  const Span sp = U == 1 ? block_span(p.T, rows_per_block, items, span, blockIdx.x, blockIdx.y)
-                         : block_span(p.T, rows_per_block, items, items, blockIdx.x, 0);
-  const int width = sp.it1 - sp.it0, total = sp.n_rows * width;
-  V v[2][U][2], w[2][2];
-  auto load = [&](int g0, V (&x)[U][2]) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int g = g0 + threadIdx.x + u * kThreads;
-      if (g >= total) continue;
-      const int r = small_quotient(g, width_magic);
-      const Where at = where(p, sp.it0 + g - r * width, li, hb);
-      int o0, o1;
-      item_offsets<E>(p.r, at.i, o0, o1);
-      const NormRopePart& q = p.part[at.part];
-      const char* src = q.x + (size_t)(sp.row0 + r) * q.x_ld + at.head;
-      x[u][0] = *reinterpret_cast<const V*>(src + o0 * EL);
-      x[u][1] = *reinterpret_cast<const V*>(src + o1 * EL);
+  const int ipr = p.hd / (2 * E), items = (p.heads[0] + p.heads[1] + p.heads[2]) * ipr, tid = threadIdx.x;
+  const int row0 = blockIdx.x * s.rows, n_rows = min(s.rows, p.T - row0), side = tid / s.cols;
+  const int it = blockIdx.y * s.cols + tid - side * s.cols;
+  const bool real = side < s.side && it < items;
+  const Column<E> c(p.heads, p.r, p.hd, real ? it : 0);
+  const char* src = p.x[c.part] + (size_t)(row0 + side) * p.x_ld[c.part] + (size_t)c.h * p.hd * EL;
+  const int64_t step = p.x_ld[c.part] * s.side;
+  V v[kAhead][2];
+  auto load = [&](int r, V (&x)[2]) {
+    if (real && r < n_rows) {
+      x[0] = *reinterpret_cast<const V*>(src + c.o0 * EL);
+      x[1] = *reinterpret_cast<const V*>(src + c.o1 * EL);
     }
+    src += step;
   };
-  load(0, v[0]);
-  {   // (a thread's items are all at the same place of their heads)
-    int o0, o1;
-    item_offsets<E>(p.r, (sp.it0 + (int)threadIdx.x) & (ipr - 1), o0, o1);
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (p.part[k].heads) {
-        w[k][0] = *reinterpret_cast<const V*>(p.part[k].w + o0 * EL);
-        w[k][1] = *reinterpret_cast<const V*>(p.part[k].w + o1 * EL);
+  for (int j = 0; j < kAhead; ++j) load(side + j * s.side, v[j]);
+  float w[2 * E];
+  if (c.part < 2) {
+    unpack<EL, VB>(*reinterpret_cast<const V*>(p.w[c.part] + c.o0 * EL), w);
+    unpack<EL, VB>(*reinterpret_cast<const V*>(p.w[c.part] + c.o1 * EL), w + E);
+  }
+  const bool first = blockIdx.y == 0;
+  if constexpr (CACHE) {
+    const int lane = tid & 31;
+    for (int r = tid >> 5; r < n_rows; r += blockDim.x >> 5) {
+      int pos;
+      long long dst;
+      append_row(p.a, row0 + r, lane, first && lane == 0, pos, dst);
+      if (lane == 0) {
+        s_pos[r] = pos;
+        s_dst[r] = dst;
       }
-  }
-  if (threadIdx.x < sp.n_rows) {
-    const int q = p.pos[sp.row0 + threadIdx.x];
-    s_pos[threadIdx.x] = q;
-    if (q < 0 && blockIdx.y == 0) set_status(p.status, DEV_BAD_POSITION);
+    }
+    if (blockIdx.x == 0 && first) report_ranges(p.a.rows, p.status);
+  } else if (tid < n_rows) {
+    const int q = p.pos[row0 + tid];
+    s_pos[tid] = q;
+    if (q < 0 && first) set_status(p.status, DEV_BAD_POSITION);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < sp.n_rows * half; e += kThreads) {
+  const int half = p.r.rd / 2;
+  for (int e = tid; e < n_rows * half; e += blockDim.x) {
     const int r = e / half;
-    cs[e] = angle(p.r, s_pos[r], e - r * half, false);
+    put_angle<E>(cs + r * p.r.rd, p.r, s_pos[r], e - r * half, false);
   }
   __syncthreads();
-  auto store = [&](int g0, V (&x)[U][2]) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int g = g0 + threadIdx.x + u * kThreads;
-      float f[2 * E], y[2 * E];
-      unpack<EL, VB>(x[u][0], f);
-      unpack<EL, VB>(x[u][1], f + E);
-      norm_head<E>(f, ipr, p.per_dim, p.eps);   // (all lanes)
-      if (g >= total) continue;
-      const int r = small_quotient(g, width_magic);
-      if (s_pos[r] < 0) continue;
-      const Where at = where(p, sp.it0 + g - r * width, li, hb);
-      unpack<EL, VB>(at.part ? w[1][0] : w[0][0], y);
-      unpack<EL, VB>(at.part ? w[1][1] : w[0][1], y + E);
-#pragma unroll
-      for (int e = 0; e < 2 * E; ++e) f[e] *= y[e];
-      int o0, o1;
-      if (item_offsets<E>(p.r, at.i, o0, o1)) turn<E>(f, cs + r * half + at.i * E, p.r.interleaved);
-      const NormRopePart& q = p.part[at.part];
-      char* dst = q.out + (size_t)(sp.row0 + r) * q.out_ld + at.head;
-      *reinterpret_cast<V*>(dst + o0 * EL) = pack<EL, VB>(f);
-      *reinterpret_cast<V*>(dst + o1 * EL) = pack<EL, VB>(f + E);
-    }
-  };
-  constexpr int kStep = U * kThreads;
-  for (int g0 = 0; g0 < total; g0 += 2 * kStep) {
-    if (g0 + kStep < total) load(g0 + kStep, v[1]);
-    store(g0, v[0]);
-    if (g0 + kStep >= total) break;
-    if (g0 + 2 * kStep < total) load(g0 + 2 * kStep, v[0]);
-    store(g0 + kStep, v[1]);
+  // where the column's results go: rows of out, or slots of the pages
+  const bool paged = CACHE && c.part > 0;
+  char* dst0;
+  int64_t out_step = 0;
+  if (paged) {
+    dst0 = p.a.c.pages + (size_t)(c.h + (c.part == 2 ? p.heads[1] : 0)) * p.a.c.ps * p.hd * EL;
+  } else {
+    out_step = p.out_ld[c.part & 1] * s.side;
+    dst0 = p.out[c.part & 1] + (size_t)(row0 + side) * p.out_ld[c.part & 1] + (size_t)c.h * p.hd * EL;
   }
-}
-
-// Rows [T b / G, T (b + 1) / G) of block b of G, `rows` at a time (the table of their angles
-// fills the dynamic shared memory).  The weights' gradients stay in registers: a thread's
-// items are all at the same place of their heads; at the end the block adds up its threads'
-// in order and leaves them for norm_rope_sums_kernel.
-template <int EL, int VB>
-__global__ void __launch_bounds__(kThreads) norm_rope_grad_kernel(const __grid_constant__ NormRopeParams p, int rows) {
-  using V = typename Vec<VB>::T;
-  constexpr int E = VB / EL;
-  extern __shared__ float2 cs[];   // [rows][rd / 2]
-  __shared__ int s_pos[kMaxRows];
-  __shared__ float s_dw[kThreads / 32][128];
-  pdl_trigger();
-  pdl_wait();
-  const int ipr = p.hd / (2 * E), li = __ffs(ipr) - 1, half = p.r.rd / 2, hb = p.hd * EL;
-  const int items = (p.part[0].heads + p.part[1].heads) * ipr, G = gridDim.x;
-  const int row1 = (int)((long long)p.T * (blockIdx.x + 1) / G);
-  const int place = threadIdx.x & (ipr - 1);
-  int o0, o1;
-  const bool rot = item_offsets<E>(p.r, place, o0, o1);
-  V w[2][2];
-  float dw[2][2 * E];
+  const bool warp_norms = __any_sync(0xffffffffu, c.part < 2);
+  const int steps = (n_rows + s.side - 1) / s.side;
+  for (int k0 = 0; k0 < steps; k0 += kAhead) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (p.part[k].heads) {
-      w[k][0] = *reinterpret_cast<const V*>(p.part[k].w + o0 * EL);
-      w[k][1] = *reinterpret_cast<const V*>(p.part[k].w + o1 * EL);
-    }
+    for (int j = 0; j < kAhead; ++j) {
+      if (k0 + j >= steps) break;
+      const int r = side + (k0 + j) * s.side;
+      V x[2] = {v[j][0], v[j][1]};
+      load(r + kAhead * s.side, v[j]);
+      const bool on = real && r < n_rows && s_pos[r] >= 0;
+      if (warp_norms) {
+        float f[2 * E];
+        unpack<EL, VB>(x[0], f);
+        unpack<EL, VB>(x[1], f + E);
+        const float inv = norm_of<E>(f, ipr, p.per_dim, p.eps);   // (all lanes)
+        if (on && c.part < 2) {
 #pragma unroll
-    for (int e = 0; e < 2 * E; ++e) dw[k][e] = 0.f;
-  }
-  V v[2][4];   // x and dy of the next item and of the one before it
-  for (int row0 = (int)((long long)p.T * blockIdx.x / G); row0 < row1; row0 += rows) {
-    const int n_rows = min(rows, row1 - row0), total = n_rows * items;
-    auto load = [&](int g, V (&x)[4]) {
-      if (g >= total) return;
-      const int r = g / items;
-      const Where at = where(p, g - r * items, li, hb);
-      const NormRopePart& q = p.part[at.part];
-      const char* src = q.x + (size_t)(row0 + r) * q.x_ld + at.head;
-      const char* dy = q.dy + (size_t)(row0 + r) * q.dy_ld + at.head;
-      x[0] = *reinterpret_cast<const V*>(src + o0 * EL);
-      x[1] = *reinterpret_cast<const V*>(src + o1 * EL);
-      x[2] = *reinterpret_cast<const V*>(dy + o0 * EL);
-      x[3] = *reinterpret_cast<const V*>(dy + o1 * EL);
-    };
-    load(threadIdx.x, v[0]);
-    __syncthreads();   // the last rows' angles have been read
-    if (threadIdx.x < n_rows) {
-      const int q = p.pos[row0 + threadIdx.x];
-      s_pos[threadIdx.x] = q;
-      if (q < 0) set_status(p.status, DEV_BAD_POSITION);
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < n_rows * half; e += kThreads) {
-      const int r = e / half;
-      cs[e] = angle(p.r, s_pos[r], e - r * half, true);
-    }
-    __syncthreads();
-    auto step = [&](int g, V (&x)[4]) {
-      const bool on = g < total;
-      const int r = on ? g / items : 0;
-      const Where at = where(p, on ? g - r * items : 0, li, hb);
-      float n[2 * E], d[2 * E], y[2 * E];
-      unpack<EL, VB>(x[0], n);
-      unpack<EL, VB>(x[1], n + E);
-      unpack<EL, VB>(x[2], d);
-      unpack<EL, VB>(x[3], d + E);
-      const float inv = norm_head<E>(n, ipr, p.per_dim, p.eps);
-      if (rot) turn<E>(d, cs + r * half + place * E, p.r.interleaved);
-      const bool used = on && s_pos[r] >= 0;
-      if (used) {
-        if (at.part) {
-#pragma unroll
-          for (int e = 0; e < 2 * E; ++e) dw[1][e] = fmaf(d[e], n[e], dw[1][e]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 2 * E; ++e) dw[0][e] = fmaf(d[e], n[e], dw[0][e]);
+          for (int e = 0; e < 2 * E; e += 2) {
+            mul2(f[e], f[e + 1], inv, inv);
+            mul2(f[e], f[e + 1], w[e], w[e + 1]);
+          }
+          if (c.rot) turn_item<E>(f, cs + r * p.r.rd, c.place, p.r);
+          x[0] = pack<EL, VB>(f);
+          x[1] = pack<EL, VB>(f + E);
         }
       }
-      unpack<EL, VB>(at.part ? w[1][0] : w[0][0], y);
-      unpack<EL, VB>(at.part ? w[1][1] : w[0][1], y + E);
-      float dot = 0.f;
-#pragma unroll
-      for (int e = 0; e < 2 * E; ++e) {
-        d[e] *= y[e];
-        dot = fmaf(d[e], n[e], dot);
+      char* dst = dst0;
+      if (paged) {
+        const long long at = r < n_rows ? s_dst[r] : -1;
+        if (!on || at < 0) continue;
+        dst += at;
+      } else {
+        dst0 += out_step;
+        if (!on) continue;
       }
-      dot = head_sum(dot, ipr) * p.per_dim;   // (all lanes)
-      if (!used) return;
-#pragma unroll
-      for (int e = 0; e < 2 * E; ++e) d[e] = inv * fmaf(-n[e], dot, d[e]);
-      const NormRopePart& q = p.part[at.part];
-      char* dst = q.out + (size_t)(row0 + r) * q.out_ld + at.head;
-      *reinterpret_cast<V*>(dst + o0 * EL) = pack<EL, VB>(d);
-      *reinterpret_cast<V*>(dst + o1 * EL) = pack<EL, VB>(d + E);
-    };
-    for (int g0 = 0; g0 < total; g0 += 2 * kThreads) {
-      load(g0 + kThreads + threadIdx.x, v[1]);
-      step(g0 + threadIdx.x, v[0]);
-      if (g0 + kThreads >= total) break;
-      load(g0 + 2 * kThreads + threadIdx.x, v[0]);
-      step(g0 + kThreads + threadIdx.x, v[1]);
-    }
-  }
-  // lanes at the same place of a head, then the warps in order
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (!p.part[k].heads) continue;
-#pragma unroll
-    for (int e = 0; e < 2 * E; ++e)
-      for (int o = ipr; o < 32; o <<= 1) dw[k][e] += __shfl_xor_sync(0xffffffffu, dw[k][e], o);
-    __syncthreads();
-    if ((threadIdx.x & 31) < ipr) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        s_dw[threadIdx.x >> 5][o0 + e] = dw[k][e];
-        s_dw[threadIdx.x >> 5][o1 + e] = dw[k][E + e];
-      }
-    }
-    __syncthreads();
-    if (threadIdx.x < p.hd) {
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i) sum += s_dw[i][threadIdx.x];
-      p.sums[((size_t)blockIdx.x * 2 + k) * p.hd + threadIdx.x] = sum;
+      *reinterpret_cast<V*>(dst + c.o0 * EL) = x[0];
+      *reinterpret_cast<V*>(dst + c.o1 * EL) = x[1];
     }
   }
 }
 
-// The blocks' sums of the weights' gradients, each thread every eighth block's of a dim,
-// the eight in order.  One block per part.
-__global__ void __launch_bounds__(1024) norm_rope_sums_kernel(const __grid_constant__ NormRopeParams p, int blocks) {
-  __shared__ float s[8][128];
+// The weights' gradients stay in registers (a thread's items are all at the same place of
+// their heads); at the end the block adds up its threads' in order and leaves them for
+// norm_sums_kernel.
+template <int EL, int VB>
+__global__ void __launch_bounds__(kMost, 2) norm_rope_grad_kernel(const __grid_constant__ NormRopeParams p, norm::Shape s) {
+  using V = typename Vec<VB>::T;
+  constexpr int E = VB / EL, kAhead = 2;
+  extern __shared__ __align__(16) float cs[];   // [rows][rd], then the threads' sums
+  __shared__ int s_pos[kGradRows];
   pdl_trigger();
   pdl_wait();
-  const int k = blockIdx.x, d = threadIdx.x & 127, i0 = threadIdx.x >> 7;
-  if (!p.part[k].heads) return;
-  float sum = 0.f;
-  if (d < p.hd)
-#pragma unroll 8
-    for (int i = i0; i < blocks; i += 8) sum += p.sums[((size_t)i * 2 + k) * p.hd + d];
-  s[i0][d] = sum;
-  __syncthreads();
-  if (i0 == 0 && d < p.hd) {
+  const int heads[3] = {p.part[0].heads, p.part[1].heads, 0};
+  const int ipr = p.hd / (2 * E), items = (heads[0] + heads[1]) * ipr, tid = threadIdx.x;
+  const int row0 = blockIdx.x * s.rows, n_rows = min(s.rows, p.T - row0), side = tid / s.cols;
+  const int it = blockIdx.y * s.cols + tid - side * s.cols;
+  const bool real = side < s.side && it < items;
+  const Column<E> c(heads, p.r, p.hd, real ? it : 0);
+  const NormRopePart& q = p.part[c.part];
+  const size_t head = (size_t)c.h * p.hd * EL;
+  const char* src = q.x + (size_t)(row0 + side) * q.x_ld + head;
+  const char* dys = q.dy + (size_t)(row0 + side) * q.dy_ld + head;
+  char* dst = q.out + (size_t)(row0 + side) * q.out_ld + head;
+  const int64_t step = q.x_ld * s.side, dy_step = q.dy_ld * s.side, out_step = q.out_ld * s.side;
+  V v[kAhead][4];
+  auto load = [&](int r, V (&x)[4]) {
+    if (real && r < n_rows) {
+      x[0] = *reinterpret_cast<const V*>(src + c.o0 * EL);
+      x[1] = *reinterpret_cast<const V*>(src + c.o1 * EL);
+      x[2] = *reinterpret_cast<const V*>(dys + c.o0 * EL);
+      x[3] = *reinterpret_cast<const V*>(dys + c.o1 * EL);
+    }
+    src += step;
+    dys += dy_step;
+  };
 #pragma unroll
-    for (int i = 1; i < 8; ++i) sum += s[i][d];
+  for (int j = 0; j < kAhead; ++j) load(side + j * s.side, v[j]);
+  float w[2 * E], dw[2 * E];
+  unpack<EL, VB>(*reinterpret_cast<const V*>(q.w + c.o0 * EL), w);
+  unpack<EL, VB>(*reinterpret_cast<const V*>(q.w + c.o1 * EL), w + E);
+#pragma unroll
+  for (int e = 0; e < 2 * E; ++e) dw[e] = 0.f;
+  const int half = p.r.rd / 2, batch = kGradRows / (kAhead * s.side) * kAhead * s.side;   // rows whose angles are there
+  for (int b0 = 0; b0 < n_rows; b0 += batch) {
+    const int nb = min(batch, n_rows - b0), steps = (nb + s.side - 1) / s.side;
+    __syncthreads();   // the last rows' angles have been read
+    if (tid < nb) {
+      const int t = p.pos[row0 + b0 + tid];
+      s_pos[tid] = t;
+      if (t < 0 && blockIdx.y == 0) set_status(p.status, DEV_BAD_POSITION);
+    }
+    __syncthreads();
+    for (int e = tid; e < nb * half; e += blockDim.x) {
+      const int r = e / half;
+      put_angle<E>(cs + r * p.r.rd, p.r, s_pos[r], e - r * half, true);
+    }
+    __syncthreads();
+    for (int k0 = 0; k0 < steps; k0 += kAhead) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (k0 + j >= steps) break;
+        const int r = side + (k0 + j) * s.side;   // within the batch
+        float n[2 * E], d[2 * E];
+        unpack<EL, VB>(v[j][0], n);
+        unpack<EL, VB>(v[j][1], n + E);
+        unpack<EL, VB>(v[j][2], d);
+        unpack<EL, VB>(v[j][3], d + E);
+        load(b0 + r + kAhead * s.side, v[j]);
+        const bool on = real && r < nb && s_pos[r] >= 0;
+        const float inv = norm_of<E>(n, ipr, p.per_dim, p.eps);
+#pragma unroll
+        for (int e = 0; e < 2 * E; e += 2) mul2(n[e], n[e + 1], inv, inv);
+        if (c.rot) turn_item<E>(d, cs + min(r, nb - 1) * p.r.rd, c.place, p.r);
+        if (on) {
+#pragma unroll
+          for (int e = 0; e < 2 * E; e += 2) fma2(dw[e], dw[e + 1], d[e], d[e + 1], n[e], n[e + 1]);
+        }
+#pragma unroll
+        for (int e = 0; e < 2 * E; e += 2) mul2(d[e], d[e + 1], w[e], w[e + 1]);
+        const float dot = -head_sum(dot_item<E>(d, n), ipr) * p.per_dim;   // (all lanes)
+        if (on) {
+#pragma unroll
+          for (int e = 0; e < 2 * E; e += 2) {
+            fma2(d[e], d[e + 1], n[e], n[e + 1], dot, dot);
+            mul2(d[e], d[e + 1], inv, inv);
+          }
+          *reinterpret_cast<V*>(dst + c.o0 * EL) = pack<EL, VB>(d);
+          *reinterpret_cast<V*>(dst + c.o1 * EL) = pack<EL, VB>(d + E);
+        }
+        dst += out_step;
+      }
+    }
+  }
+  // the block's sums by dim: all threads of the part at the dim's place, in order
+  __syncthreads();
+  float* sums = cs;   // [thread][2 E]
+#pragma unroll
+  for (int e = 0; e < 2 * E; ++e) sums[tid * 2 * E + e] = real ? dw[e] : 0.f;
+  __syncthreads();
+  const int it0 = blockIdx.y * s.cols, it1 = min(it0 + s.cols, items);
+  for (int e = tid; e < 2 * p.hd; e += blockDim.x) {
+    const int part = e >= p.hd, d = e - part * p.hd, h0 = part ? heads[0] : 0, h1 = h0 + heads[part];
+    // dim d's place and number among its item's
+    const int rd = p.r.rd;
+    int place, at;
+    if (d >= rd || p.r.interleaved) {
+      place = d / (2 * E);
+      at = d - place * 2 * E;
+    } else {
+      const int y = d >= rd / 2 ? d - rd / 2 : d;
+      place = y / E;
+      at = y - place * E + (d >= rd / 2 ? E : 0);
+    }
+    float sum = 0.f;
+    for (int k = 0; k < s.side; ++k)
+      for (int h = h0; h < h1; ++h) {
+        const int i = h * ipr + place;
+        if (i >= it0 && i < it1) sum += sums[(k * s.cols + i - it0) * 2 * E + at];
+      }
+    p.sums[((size_t)(blockIdx.y * gridDim.x + blockIdx.x) * 2) * p.hd + e] = sum;
+  }
+}
+
+// The blocks' sums of the weights' gradients: grid (parts, 32 dims each), a warp every 32nd
+// block's, the warps in order.
+__global__ void __launch_bounds__(1024) norm_sums_kernel(const __grid_constant__ NormRopeParams p, int blocks) {
+  __shared__ float s[32][32];
+  pdl_trigger();
+  pdl_wait();
+  const int k = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = blockIdx.y * 32 + lane;
+  if (!p.part[k].heads) return;
+  const float* from = p.sums + k * p.hd + d;
+  float sum = 0.f;
+#pragma unroll 16
+  for (int i = warp; i < blocks; i += 32) sum += from[(size_t)i * 2 * p.hd];
+  s[warp][lane] = sum;
+  __syncthreads();
+  if (warp == 0) {
+#pragma unroll
+    for (int i = 1; i < 32; ++i) sum += s[i][lane];
     p.part[k].dw[d] = sum;
   }
 }
 
-template <int EL, int VB>
-cudaError_t norm_rope_as(const NormRopeParams& p, cudaStream_t st) {
-  const int items = (p.part[0].heads + p.part[1].heads) * (p.hd / (2 * (VB / EL)));
-  const Shape s = append_shape(p.T, items, p.r.rd);
-  const dim3 grid(s.gx, s.gy);
-  const uint32_t magic = append_magic(s, items);
-  return s.u == 1 ? launch_dependent(norm_rope_kernel<EL, VB, 1>, grid, kThreads, s.smem, st, p, s.rows, s.span, magic)
-                  : launch_dependent(norm_rope_kernel<EL, VB, 2>, grid, kThreads, s.smem, st, p, s.rows, s.span, magic);
+template <int EL, int VB, bool CACHE>
+cudaError_t norm_rows_as(const NormRows& p, cudaStream_t st) {
+  const norm::Shape s = norm::shape_of(p.T, (p.heads[0] + p.heads[1] + p.heads[2]) * (p.hd / (2 * (VB / EL))), 65536 / 80);
+  return launch_dependent(norm_rows_kernel<EL, VB, CACHE>, dim3(s.gx, s.gy), s.threads, sizeof(float) * s.rows * p.r.rd,
+                          st, p, s);
+}
+
+template <bool CACHE>
+cudaError_t norm_rows(const NormRows& p, int el, cudaStream_t st) {
+  if (el == 4) return norm_rows_as<4, 16, CACHE>(p, st);
+  return p.r.rd % 16 == 0 ? norm_rows_as<2, 16, CACHE>(p, st) : norm_rows_as<2, 8, CACHE>(p, st);
 }
 
 template <int EL, int VB>
 cudaError_t norm_rope_grad_as(const NormRopeParams& p, cudaStream_t st) {
-  const int blocks = p.T < kNormBlocks ? p.T : kNormBlocks;
-  const int rows = (p.T + blocks - 1) / blocks < kAppendRows ? (p.T + blocks - 1) / blocks : kAppendRows;
-  const size_t smem = sizeof(float) * 2 * rows * (p.r.rd / 2);
-  const cudaError_t e = launch_dependent(norm_rope_grad_kernel<EL, VB>, dim3(blocks), kThreads, smem, st, p, rows);
+  constexpr int E = VB / EL;
+  const norm::Shape s = norm::sum_shape_of(p.T, (p.part[0].heads + p.part[1].heads) * (p.hd / (2 * E)), 65536 / 128, kNormBlocks);
+  const size_t smem = sizeof(float) * std::max(kGradRows * p.r.rd, s.threads * 2 * E);
+  const cudaError_t e = launch_dependent(norm_rope_grad_kernel<EL, VB>, dim3(s.gx, s.gy), s.threads, smem, st, p, s);
   if (e != cudaSuccess) return e;
-  return launch_dependent(norm_rope_sums_kernel, dim3(2), 1024, 0, st, p, blocks);
+  return launch_dependent(norm_sums_kernel, dim3(2, p.hd / 32), 1024, 0, st, p, s.gx * s.gy);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t st) {
-  if (p.el == 4) return norm_rope_as<4, 16>(p, st);
-  return p.r.rd % 16 == 0 ? norm_rope_as<2, 16>(p, st) : norm_rope_as<2, 8>(p, st);
+  NormRows n = {};
+  n.r = p.r;
+  n.T = p.T;
+  n.hd = p.hd;
+  for (int k = 0; k < 2; ++k) {
+    n.heads[k] = p.part[k].heads;
+    n.x[k] = p.part[k].x;
+    n.w[k] = p.part[k].w;
+    n.out[k] = p.part[k].out;
+    n.x_ld[k] = p.part[k].x_ld;
+    n.out_ld[k] = p.part[k].out_ld;
+  }
+  n.per_dim = p.per_dim;
+  n.eps = p.eps;
+  n.pos = p.pos;
+  n.status = p.status;
+  return norm_rows<false>(n, p.el, st);
+}
+
+cudaError_t launch_norm_append(const AppendParams& a, cudaStream_t st) {
+  NormRows n = {};
+  n.r = a.r;
+  n.T = a.rows.T;
+  n.hd = a.c.hd;
+  n.heads[0] = a.q ? a.c.n_head : 0;
+  n.heads[1] = n.heads[2] = a.c.n_head_kv;
+  n.x[0] = a.q;
+  n.x[1] = a.k;
+  n.x[2] = a.v;
+  n.w[0] = a.q_norm;
+  n.w[1] = a.k_norm;
+  n.out[0] = a.q_out;
+  n.x_ld[0] = a.q_ld;
+  n.x_ld[1] = a.k_ld;
+  n.x_ld[2] = a.v_ld;
+  n.out_ld[0] = a.q_out_ld;
+  n.per_dim = a.per_dim;
+  n.eps = a.eps;
+  n.status = a.c.status;
+  n.a = a;
+  return norm_rows<true>(n, a.c.el, st);
 }
 
 cudaError_t launch_norm_rope_grad(const NormRopeParams& p, cudaStream_t st) {

@@ -18,10 +18,17 @@ def weights(g, hd, dtype):
     return (1 + 0.3 * torch.randn(hd, generator=g)).to(DT[dtype])
 
 
-def adds(T, heads):
-    """Most additions a term of a weight's gradient goes through: its thread's items (at most the rows of
-    one of 608 blocks times the heads), 4 across lanes, 8 warps, 76 blocks of a thread, 8 threads."""
-    return min(T * heads, -(-T // 608) * heads + 4 + 8 + 76 + 8)
+def adds(T, heads, others, hd, lanes):
+    """Most additions a term of a weight's gradient goes through: the rows of its thread (of at least 152 blocks, shared
+    by blocks of up to 256 columns), a block's threads at its place (256 over a head's lanes), 19 of up to 608
+    blocks by each warp, 32 warps."""
+    ny = -(-(heads + others) * lanes // 256)
+    return min(T * heads, -(-T // max(1, 152 // ny)) + 256 // lanes + 19 + 32)
+
+
+def lanes(hd, dtype, rd):
+    """Lanes of a head: two vectors of 16 bytes each, of 8 where 16 do not hold whole pairs."""
+    return hd // (8 if dtype == "f32" or rd % 16 else 16)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -49,7 +56,7 @@ def test_norm_rope_and_gradient(dtype, hd, layout, rot, kw):
             args = (pos.numpy(), EPS, layout, rd, f, m, HALF[dtype])
             y, tol = N.forward(np64(x[i]), np64(w[i]), *args)
             check(np64(out[i]), y, tol, f"{T} rows, part {i}")
-            ex, tx, ew, tw = N.backward(np64(x[i]), np64(w[i]), np64(dy[i]), *args, adds(T, h))
+            ex, tx, ew, tw = N.backward(np64(x[i]), np64(w[i]), np64(dy[i]), *args, adds(T, h, hq + hkv - h, hd, lanes(hd, dtype, rd)))
             check(np64(dx[i]), ex, tx, f"{T} rows, part {i}: dx")
             check(np64(dw[i]), ew, tw, f"{T} rows, part {i}: dw")
         assert c.dflash_cache_read_status() == 0
@@ -80,7 +87,7 @@ def test_many_rows_strided_in_place(dtype, T):
     for i, (a, b, h) in enumerate(((0, hq, hq), (hq, hq + hkv, hkv))):
         y, tol = N.forward(np64(fused[:, a:b]), np64(w[i]), *args)
         check(np64(dev[:, a:b]), y, tol, f"part {i}")
-        ex, tx, ew, tw = N.backward(np64(fused[:, a:b]), np64(w[i]), np64(dy[:, a:b]), *args, adds(T, h))
+        ex, tx, ew, tw = N.backward(np64(fused[:, a:b]), np64(w[i]), np64(dy[:, a:b]), *args, adds(T, h, hq + hkv - h, hd, lanes(hd, dtype, rd)))
         check(np64(ddev[:, a:b]), ex, tx, f"part {i}: dx")
         check(np64(dw[i]), ew, tw, f"part {i}: dw")
         check(np64(dw[(3, 2)[i]]), ew, tw, f"part {i} alone: dw")
