@@ -153,14 +153,20 @@ __global__ void __launch_bounds__(kMost, 3) norm_rows_kernel(const __grid_consta
   }
   const bool first = blockIdx.y == 0;
   if constexpr (CACHE) {
+    // (few entries: a lane a row, all rows at once; rows of a warp one after another are five
+    // dependent loads each)
     const int lane = tid & 31;
-    for (int r = tid >> 5; r < n_rows; r += blockDim.x >> 5) {
-      int pos;
-      long long dst;
-      append_row(p.a, row0 + r, lane, first && lane == 0, pos, dst);
-      if (lane == 0) {
-        s_pos[r] = pos;
-        s_dst[r] = dst;
+    if (p.a.rows.n_seq <= 32) {
+      if (tid < n_rows) append_row_alone(p.a, row0 + tid, first, s_pos[tid], s_dst[tid]);
+    } else {
+      for (int r = tid >> 5; r < n_rows; r += blockDim.x >> 5) {
+        int pos;
+        long long dst;
+        append_row(p.a, row0 + r, lane, first && lane == 0, pos, dst);
+        if (lane == 0) {
+          s_pos[r] = pos;
+          s_dst[r] = dst;
+        }
       }
     }
     if (blockIdx.x == 0 && first) report_ranges(p.a.rows, p.status);

@@ -149,6 +149,34 @@ DF_DEVICE void append_row(const AppendParams& p, int t, int lane, bool first, in
     }
   }
 }
+// The same by one lane, of calls of few entries: a block's rows all at once.
+DF_DEVICE void append_row_alone(const AppendParams& p, int t, bool first, int& pos, long long& dst) {
+  const CacheView& c = p.c;
+  int s = -1;
+  for (int i = 0; i <= p.rows.n_seq; ++i) s += p.rows.row_start[i] <= t;
+  pos = -1;
+  dst = -1;
+  int lo = 0, n = 0;
+  if (s < 0 || s >= p.rows.n_seq || !entry_rows(p.rows, s, lo, n) || t < lo || t >= lo + n) return;
+  const int q = entry_sequence(p.rows, s, c.max_seq);
+  bool twice = false;
+  if (p.rows.seqs)
+    for (int i = 0; i < s; ++i) twice |= p.rows.seqs[i] == q;
+  const int len = q >= 0 ? c.length[q] : -1;
+  const long long at = (long long)len + (p.depth ? p.depth[t] : t - lo);
+  const unsigned bad = q < 0 || twice ? DEV_BAD_SEQ : len < 0 ? DEV_BAD_ROWS : at < 0 || at > 0x7fffffffLL ? DEV_BAD_POSITION : 0u;
+  if (bad) {
+    if (first) set_status(c.status, bad);
+    return;
+  }
+  pos = (int)at;
+  const long long slot = (long long)len + (t - lo), idx = slot >> c.ps_log2;
+  const int page = idx < c.max_pages ? c.table[(size_t)q * c.max_pages + idx] : -1;
+  if (page >= 0 && page < c.n_pages && c.refs[page] <= 1)
+    dst = (long long)page_row(c, page, p.layer, 0, 0, (int)(slot & (c.ps - 1)));
+  else if (first)
+    set_status(c.status, DEV_BAD_PAGE);
+}
 // Ranges that are no ranges, by one block.
 DF_DEVICE void report_ranges(const RowView& rows, unsigned* status) {
   for (int s = threadIdx.x; s < rows.n_seq; s += blockDim.x) {

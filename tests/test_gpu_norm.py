@@ -224,6 +224,42 @@ def test_norm_append(dtype, hd, ps, rot, kw, with_q):
         assert c.dflash_cache_read_status() == 0
 
 
+@pytest.mark.parametrize("n", [32, 33, 200])
+def test_norm_append_of_many_entries(n):
+    """Entries that a lane looks through and those that a warp does: the same rows as norm_rope's, faults reported."""
+    hq, hkv, hd, ps = 4, 2, 64, 16
+    rng = np.random.default_rng(n)
+    c = make(n_head=hq, n_head_kv=hkv, head_dim=hd, page_size=ps, n_pages=700, max_seq=256, max_pages=6)
+    counts, lens = rng.integers(0, 5, n), rng.integers(0, 40, n)
+    seqs = rng.permutation(256)[:n]
+    scattered(c, rng, seqs.tolist(), lens.tolist(), counts.tolist())
+    seqs[n // 2] = seqs[1]                       # listed twice: the later one does nothing
+    T = int(counts.sum()) + 3
+    g = torch.Generator().manual_seed(n)
+    x = normal(g, (T, hq + 2 * hkv, hd), "bf16").cuda()
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    wq, wk = weights(g, hd, "bf16").cuda(), weights(g, hd, "bf16").cuda()
+    pos = np.full(T, -1)
+    of = np.repeat(np.arange(n), counts)
+    for t, s in enumerate(of):
+        pos[t] = lens[s] + t - counts[:s].sum()
+    dead = (of == n // 2)
+    qa, qb, kb = torch.full_like(q, 3.0), torch.full_like(q, 3.0), torch.full_like(k, 3.0)
+    c.pages.zero_()
+    c.dflash_norm_append(0, starts(counts), k, v, wk, q=q, q_norm=wq, q_out=qa, seqs=ints(seqs))
+    assert c.dflash_cache_read_status() == (0x40 if dead.any() else 0)
+    pos[:len(of)][dead] = -1
+    c.dflash_norm_rope(ints(pos), q=q, q_norm=wq, q_out=qb, k=k, k_norm=wk, k_out=kb)
+    c.dflash_cache_read_status()
+    assert torch.equal(qa, qb)
+    table, want = c.table.cpu().numpy(), torch.zeros_like(c.pages)
+    for t, s in enumerate(of):
+        if not dead[t]:
+            page, at = int(table[seqs[s], pos[t] // ps]), pos[t] % ps
+            want[page, 0, 0, :, at], want[page, 0, 1, :, at] = kb[t], v[t]
+    assert torch.equal(c.pages, want)
+
+
 def test_norm_append_agrees_with_norm_rope_and_append():
     """The fused call's keys and queries are those of norm_rope, its faults those of the append."""
     hq, hkv, hd, ps = 8, 2, 128, 16
