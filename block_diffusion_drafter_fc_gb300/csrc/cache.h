@@ -143,7 +143,8 @@ struct AttendParams {
   int n_group;
   const int32_t *group_start, *plan;
   float* row_o;      // [2][T][n_head][hd]
-  float2* row_ml;    // [2][T][n_head]: reference in powers of two, sum
+  float2* row_ml;    // [2][T][n_head]: reference in powers of two, sum; or where the parts of a cut tile are
+  int4* table;       // [n_seq] first row, rows (0: skipped), first own slot
 };
 // What a handle keeps for attention: tensor maps of the pages, scratch for the
 // partial rows of tiles that several blocks share, and a description per block
@@ -151,7 +152,6 @@ struct AttendParams {
 struct Cut {
   int lo, row0, kvh, rows;   // first row of the entry; the tile's first row, kv head, rows
   int last, slot;            // its last block (below the block itself: no such tile), the first part's slot
-  int pass;                  // the part of its rows (shared prefixes): 0 a group's, 1 an entry's
 };
 constexpr int kAttendSms = 160;        // most SMs a launch uses: 1 (tcgen05) or 2 (streaming) blocks each
 struct AttendWork {
@@ -159,6 +159,7 @@ struct AttendWork {
   float* part_o;      // [attend_part_rows][hd]
   float2* part_ml;    // [attend_part_rows]
   Cut* cuts;          // [2 kAttendSms]
+  int4* table;        // [kCallSeq]
   int sms;
 };
 // plan: [n_seq + n_group] (AttendParams)

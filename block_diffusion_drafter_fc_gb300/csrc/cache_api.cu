@@ -33,7 +33,7 @@ size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 struct Layout {
   size_t page_bytes;
   size_t table, length, refs, state_bytes;
-  size_t status, turns, tickets, free_list, copies, part_o, part_ml, cuts, norm_sums, stats, scratch_bytes;
+  size_t status, turns, tickets, free_list, copies, part_o, part_ml, cuts, table_rows, norm_sums, stats, scratch_bytes;
 };
 
 int el_of(const dflash_cache_config& c) { return c.dtype == DFLASH_DTYPE_BF16 ? 2 : 4; }
@@ -61,6 +61,7 @@ Layout layout(const dflash_cache_config& c) {
   L.part_o = take(sizeof(float) * parts * c.head_dim);
   L.part_ml = take(sizeof(float2) * parts);
   L.cuts = take(sizeof(Cut) * 2 * kAttendSms);
+  L.table_rows = take(sizeof(int4) * kCallSeq);
   L.norm_sums = take(sizeof(float) * kNormBlocks * 2 * c.head_dim);
   L.stats = take(sizeof(Piece) * kVerifyRows);
   L.scratch_bytes = off;
@@ -298,7 +299,7 @@ int dflash_cache_create(const dflash_cache_config* cfg, void* page_mem, void* st
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c->device);
     if (e == cudaSuccess && !page_map(&c->tm, w, attend_chunk(w.el, w.hd))) e = cudaErrorNotSupported;
     c->work = {&c->tm, c->S<float>(c->L.part_o), c->S<float2>(c->L.part_ml),
-               c->S<Cut>(c->L.cuts), std::min(sms, kAttendSms)};
+               c->S<Cut>(c->L.cuts), c->S<int4>(c->L.table_rows), std::min(sms, kAttendSms)};
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
   }
   if (e != cudaSuccess) {
@@ -508,6 +509,7 @@ static int attend(dflash_cache* c, int32_t layer, int32_t n_seq, const int32_t* 
   p.group_start = group_start;
   p.plan = plan;
   p.row_o = static_cast<float*>(work);
+  p.table = c->work.table;
   p.row_ml = n_group ? reinterpret_cast<float2*>(static_cast<char*>(work) + prefix_ml(c, T)) : nullptr;
   p.scale = c->cfg.attn_scale != 0.f ? c->cfg.attn_scale : (float)(1.0 / std::sqrt((double)c->cfg.head_dim));
   DC_CHECK(c, launch_attend(p, c->work, static_cast<cudaStream_t>(stream)));

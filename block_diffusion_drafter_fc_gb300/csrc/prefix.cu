@@ -9,7 +9,7 @@ namespace dflash {
 
 namespace {
 
-constexpr int kPlanThreads = 256;
+constexpr int kPlanThreads = 1024;
 
 // A block per group.  The group shares the full pages, below the least length, in which no
 // member's row of the table differs from the first's.  Bound: latency, five dependent loads.
@@ -50,12 +50,23 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(CacheView c, 
   __syncthreads();
   if (pages > 0) {
     const int32_t* first = c.table + (size_t)entry_sequence(rows, e0, c.max_seq) * c.max_pages;
-    // (members of a warp's own: its lanes follow the member's row of the table)
+    // (a warp a member, eight pages a lane at a time: 32 members of 256 pages in one round of
+    // loads; page after page took 22 us)
     int same = pages;
     for (int i = 1 + (tid >> 5); i < members; i += kPlanThreads / 32) {
       const int32_t* mine = c.table + (size_t)entry_sequence(rows, e0 + i, c.max_seq) * c.max_pages;
-      for (int p = tid & 31; p < same; p += 32)
-        if (mine[p] != first[p]) same = p;
+      for (int p0 = tid & 31; p0 < same; p0 += 256) {
+        int a[8], b[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int p = min(p0 + 32 * k, pages - 1);
+          a[k] = mine[p];
+          b[k] = first[p];
+        }
+#pragma unroll
+        for (int k = 7; k >= 0; --k)
+          if (a[k] != b[k]) same = min(same, p0 + 32 * k);
+      }
     }
     if (same < pages) atomicMin(&s_pages, same);
     __syncthreads();

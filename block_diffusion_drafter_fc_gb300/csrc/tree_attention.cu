@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
   const long long U = s_end[entries - 1];
   // fewer blocks than launched where their shares would get too small
   const int Gr = blocks_used(U, gridDim.x, kMinUnits), b = blockIdx.x;
-  Cut d = {0, 0, 0, 0, -1, 0, 0};
+  Cut d = {0, 0, 0, 0, -1, 0};
   if (b >= Gr || U == 0) {
     if (tid == 0) p.cuts[b] = d;
     return;
@@ -328,6 +328,9 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
                                                  : (size_t)slot * TR + r;
             float* po = (E::kParts && whole ? p.a.row_o : p.part_o) + at * HD;
             if (qd == 0) (E::kParts && whole ? p.a.row_ml : p.part_ml)[at] = make_float2(m[t][hf], l[t][hf]);
+            if (E::kParts && !whole && g.c0 == 0 && qd == 0)   // the cut tile's first block tells where its parts are
+              p.a.row_ml[part_row(p.a, x.pass(), x.lo + node, g.kvh * grp + g.row0 + r - node * grp)] =
+                  parts_at(b, block_of(U, Gr, g.u0 + (long long)(g.nch - 1) * g.w), slot, r);
 #pragma unroll
             for (int j = 0; j < NV; ++j)
               *reinterpret_cast<float2*>(po + j * 8 + qd * 2) = make_float2(o[t][j][hf * 2], o[t][j][hf * 2 + 1]);
@@ -342,7 +345,6 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
       d.rows = rows;
       d.last = block_of(U, Gr, g.u0 + (long long)(g.nch - 1) * g.w);
       d.slot = slot;
-      d.pass = x.pass();
     }
   }
   if (warp == 0) cp.drain(S, full);

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kAll, kPerSm) attend_f32_kernel(const __grid_c
   __syncthreads();
   const long long U = s_end[entries - 1];
   const int Gr = blocks_used(U, gridDim.x, kMinUnits), b = blockIdx.x;
-  Cut d = {0, 0, 0, 0, -1, 0, 0};
+  Cut d = {0, 0, 0, 0, -1, 0};
   if (b >= Gr || U == 0) {
     if (tid == 0) p.cuts[b] = d;
     return;
@@ -328,6 +328,8 @@ __global__ void __launch_bounds__(kAll, kPerSm) attend_f32_kernel(const __grid_c
       else
         *reinterpret_cast<float4*>((E::kParts && whole ? p.a.row_o : p.part_o) + at * HD + pc * 4) = y;
       if (pc) continue;
+      if (E::kParts && !whole && g.c0 == 0)   // the cut tile's first block tells where its parts are
+        p.a.row_ml[part_row(p.a, x.pass(), x.lo + node, h)] = parts_at(b, block_of(U, Gr, g.u0 + (long long)(g.nch - 1) * g.w), slot, r);
       float top = -CUDART_INF_F, sum = 0.f;
       for (int k = 0; k < kConsumers; ++k) top = fmaxf(top, s_ml[k * TR + r].x);
       const float use = top == -CUDART_INF_F ? 0.f : top;
@@ -339,8 +341,7 @@ __global__ void __launch_bounds__(kAll, kPerSm) attend_f32_kernel(const __grid_c
     }
     // the block with a cut tile's first chunk describes it to the join
     if (tid == 0 && g.c0 == 0 && !whole)
-      d = {x.lo, g.row0, g.kvh, rows, block_of(U, Gr, g.u0 + (long long)(g.nch - 1) * g.w), slot,
-           x.pass()};
+      d = {x.lo, g.row0, g.kvh, rows, block_of(U, Gr, g.u0 + (long long)(g.nch - 1) * g.w), slot};
   }
   if (tid == 0) p.cuts[b] = d;
 }

@@ -424,7 +424,7 @@ struct SegDesc {
   int kvh, row0, left;   // kv head, first row, rows of the tile
   int node0, h0;         // node and query head of row 0
   int c0, nc;            // first chunk, chunks
-  int whole, slot;       // the whole tile; else the slot of its partial rows
+  int last, slot;        // -1: the whole tile; else its last block (told by its first), the slot of its partial rows
 };
 constexpr int kSegs = 8;
 
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
   // Few entries: warp 11 plans alone, and the roles wait for the launch before this
   // one where their instructions are, which are then there when it ends (together
   // with less to divide: 16 nodes over 2048 slots 16.4 us instead of 17.6).
-  const bool few = entries <= 32;
+  const bool few = entries <= (E::kParts ? 64 : 32);
   if (!few) {
     pdl_wait();
     plan_entries(p.a, cutting(), s_e, s_end, s_warp, kThreads, b == 0);
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
     } else {
       // ----------------------------------------------------- segments, queries
       pdl_wait();
-      if (lane == 0) p.cuts[b] = {0, 0, 0, 0, -1, 0, 0};
+      if (lane == 0) p.cuts[b] = {0, 0, 0, 0, -1, 0};
       if (few) plan_few(p.a, cutting(), s_e, s_end, b == 0);
       const long long U = s_end[entries - 1];
       // fewer blocks than launched where their shares would get too small
@@ -716,13 +716,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
             d.h0 = g.row0 - d.node0 * grp;
             d.c0 = g.c0;
             d.nc = g.c1 - g.c0;
-            d.whole = g.c0 == 0 && g.c1 == g.nch;
             // partial rows: slot 0 of the block if its range starts in the tile, else 1
             d.slot = 2 * b + (ub0 >= g.u0 ? 0 : 1);
             // the block with a cut tile's first chunk describes it to the join
-            if (g.c0 == 0 && !d.whole)
-              p.cuts[b] = {x.lo, g.row0, g.kvh, left, block_of(U, Gr, g.u0 + (long long)(g.nch - 1) * g.w), d.slot,
-                           x.pass()};
+            d.last = g.c0 == 0 ? -1 : 0;
+            if (g.c0 == 0 && g.c1 != g.nch) {
+              d.last = block_of(U, Gr, g.u0 + (long long)(g.nch - 1) * g.w);
+              p.cuts[b] = {x.lo, g.row0, g.kvh, left, d.last, d.slot};
+            }
             publish(&s_planned, planned + 1);
           }
           __syncwarp();
@@ -876,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
       live = live && bar_wait(o_full, seg & 1, &s_abort, c.status);
       fence_after();
       if (l == 0.f) m = -CUDART_INF_F;   // nothing attended: no reference to others
-      const bool whole = d.whole;
+      const bool whole = d.last < 0;
       const int slot = d.slot;
       auto out_row = [&](int r, char*& dst, float*& lse) {
         const int y = d.h0 + r, nd = small_quotient(y, p.grp_magic), h = d.kvh * p.a.grp + y - nd * p.a.grp;
@@ -908,22 +909,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         wb *= inv;
       }
       // where row r's sums go
-      auto part_of = [&](int r) {
-        if (!E::kParts || !whole) return (size_t)slot * kTile + r;
+      auto part_of = [&](int r, bool rows) {
+        if (!E::kParts || !rows) return (size_t)slot * kTile + r;
         const int y = d.h0 + r, nd = small_quotient(y, p.grp_magic);
         return part_row(p.a, d.x.pass(), d.x.lo + d.node0 + nd, d.kvh * p.a.grp + y - nd * p.a.grp);
       };
       float* const sums_o = E::kParts && whole ? p.a.row_o : p.part_o;
       float2* const sums_ml = E::kParts && whole ? p.a.row_ml : p.part_ml;
-      char* dst = reinterpret_cast<char*>(sums_o + part_of(real ? row : 0) * HD);
+      char* dst = reinterpret_cast<char*>(sums_o + part_of(real ? row : 0, whole) * HD);
       if (real) {
         float* lse;
         if (last_word) out_row(row, dst, lse);
         if (pair || (i == 0 && pos < per)) {
           if (!last_word)
-            sums_ml[part_of(row)] = make_float2(top, sum);
+            sums_ml[part_of(row, whole)] = make_float2(top, sum);
           else if (lse)
             *lse = sum > 0.f ? (top + log2f(sum)) * kLn2 : -CUDART_INF_F;
+          if (E::kParts && !whole && d.c0 == 0)   // the cut tile's first block tells where its parts are
+            p.a.row_ml[part_of(row, true)] = parts_at(b, d.last, slot, row);
         }
       }
       // 32 weighted columns of this thread's row: column d of stream 0's (a pair: of
@@ -1027,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
                 *reinterpret_cast<uint2*>(to + dim * 2) =
                     make_uint2(pack_bf16x2(x[k].x, x[k].y), pack_bf16x2(x[k].z, x[k].w));
               } else {
-                *reinterpret_cast<float4*>(sums_o + part_of(r) * HD + dim) = x[k];
+                *reinterpret_cast<float4*>(sums_o + part_of(r, whole) * HD + dim) = x[k];
               }
             }
           }

@@ -96,6 +96,12 @@ struct PartEntry {
   DF_DEVICE static int count(const AttendParams& p) { return p.n_group + p.rows.n_seq; }
 };
 
+// Where the parts of row r of a cut tile are, in the place of its reference and sum: the blocks
+// b0 .. last have one each, the first in its slot 0 or 1.
+DF_DEVICE float2 parts_at(int b0, int last, int slot, int r) {
+  return make_float2(__int_as_float(last << 16 | (slot & 1) << 15 | r), -1.f - (float)b0);
+}
+
 // Row `t`, head `h`: its place among the parts of `pass`.
 DF_DEVICE size_t part_row(const AttendParams& p, int pass, int t, int h) {
   return ((size_t)pass * p.rows.T + t) * p.c.n_head + h;
@@ -232,22 +238,35 @@ DF_DEVICE long long plan_entry(const AttendParams& p, const Cutting& cut, int s,
   return c.n_head_kv * b.before(b.count);
 }
 
-// plan_entries by one warp, of at most 32 entries: the block's other warps need not wait.
+// What the combination needs of entry s.
+DF_DEVICE void tell_entry(const AttendParams&, int, const Entry&) {}
+DF_DEVICE void tell_entry(const AttendParams& p, int s, const PartEntry& x) {
+  if (s >= p.n_group) p.table[s - p.n_group] = make_int4(x.lo, x.n, x.base0, 0);
+}
+
+// plan_entries by one warp, of few entries: the block's other warps need not wait.
 template <typename E>
 DF_DEVICE void plan_few(const AttendParams& p, const Cutting& cut, E* e, long long* end, bool report) {
-  const int s = threadIdx.x & 31, n = E::count(p);
-  E x;
-  unsigned bad = 0;
-  long long v = s < n ? plan_entry(p, cut, s, x, bad) : 0;
-  if (bad && report) set_status(p.c.status, bad);
+  const int lane = threadIdx.x & 31, n = E::count(p);
+  long long base = 0;
 #pragma unroll 1
-  for (int o = 1; o < n; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, v, o);
-    if (s >= o) v += y;
-  }
-  if (s < n) {
-    e[s] = x;
-    end[s] = v;
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    const int s = s0 + lane;
+    E x;
+    unsigned bad = 0;
+    long long v = s < n ? plan_entry(p, cut, s, x, bad) : 0;
+    if (bad && report) set_status(p.c.status, bad);
+#pragma unroll 1
+    for (int o = 1; o < min(n - s0, 32); o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    if (s < n) {
+      e[s] = x;
+      end[s] = base + v;
+      if (report) tell_entry(p, s, x);
+    }
+    base += __shfl_sync(0xffffffffu, v, min(n - s0, 32) - 1);
   }
   __syncwarp();
 }
@@ -269,6 +288,7 @@ DF_DEVICE void plan_entries(const AttendParams& p, const Cutting& cut, E* e, lon
       unsigned bad;
       units = plan_entry(p, cut, s, x, bad);
       if (bad && report) set_status(p.c.status, bad);
+      if (report) tell_entry(p, s, x);
       e[s] = x;
     }
     long long v = units;
@@ -365,12 +385,47 @@ DF_DEVICE int block_of(long long U, int G, long long u) { return (int)quotient((
 
 // ------------------------------------------------------------------ join
 
+// The parts of row r of the cut tile `d` that begins in block b0, added to what (m, sum, acc)
+// hold of it, by a warp.  Part i of the tile is slot 2 i of the partial rows (b0 itself: the
+// slot its description names).  Weights e^(m_i - max) are applied and summed in block order.
+template <int HD>
+DF_DEVICE void join_parts(const Cut& d, int b0, int r, const float* part_o, const float2* part_ml, int tile, float& m,
+                          float& sum, float (&acc)[HD / 32]) {
+  constexpr int VL = HD / 32;
+  using V = typename DimVec<VL>::T;
+  const int lane = threadIdx.x & 31;
+  for (int i0 = b0; i0 <= d.last; i0 += 32) {
+    const int n = min(32, d.last - i0 + 1), i = i0 + lane;
+    const int at = ((i == b0 ? d.slot : 2 * i) * tile + r);
+    const float2 ml = lane < n ? part_ml[at] : make_float2(-CUDART_INF_F, 0.f);
+    const float top = fmaxf(m, warp_max(ml.x)), use = top == -CUDART_INF_F ? 0.f : top;
+    const float w = ex2(ml.x - use), fade = ex2(m - use);
+    m = top;
+    sum = sum * fade + warp_sum(w * ml.y);
+#pragma unroll
+    for (int v = 0; v < VL; ++v) acc[v] *= fade;
+    for (int k = 0; k < n; k += 8) {
+      V x[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int a = __shfl_sync(0xffffffffu, at, min(k + q, n - 1));
+        x[q] = *reinterpret_cast<const V*>(part_o + (size_t)a * HD + lane * VL);
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float wk = k + q < n ? __shfl_sync(0xffffffffu, w, min(k + q, n - 1)) : 0.f;
+#pragma unroll
+        for (int v = 0; v < VL; ++v)
+          if (k + q < n) acc[v] += wk * reinterpret_cast<const float*>(&x[q])[v];
+      }
+    }
+  }
+}
+
 // Rows of tiles cut by ranges: grid (blocks of the attention launch, up to 16
 // groups of four rows: 32 trees of 17..64 nodes took 91.6 us in all (88 now), 93.8 with
-// 8 groups, 91.1 with 32, 93.0 with 64), a warp per row.  Part i of a tile that begins in block b0 is slot
-// 2 i of the partial rows (b0 itself: the slot its description names).  Weights
-// e^(m_i - max) are applied and summed in block order.
-template <int EL, int HD, bool PARTS>
+// 8 groups, 91.1 with 32, 93.0 with 64), a warp per row.
+template <int EL, int HD>
 __global__ void __launch_bounds__(128) attend_join_kernel(AttendParams p, const Cut* cuts, const float* part_o,
                                                           const float2* part_ml, int tile) {
   constexpr int VL = HD / 32;
@@ -383,41 +438,10 @@ __global__ void __launch_bounds__(128) attend_join_kernel(AttendParams p, const 
   for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < d.rows; r += 4 * gridDim.y) {
     float m = -CUDART_INF_F, sum = 0.f;
     alignas(16) float acc[VL] = {};
-    for (int i0 = b0; i0 <= d.last; i0 += 32) {
-      const int n = min(32, d.last - i0 + 1), i = i0 + lane;
-      const int at = ((i == b0 ? d.slot : 2 * i) * tile + r);
-      const float2 ml = lane < n ? part_ml[at] : make_float2(-CUDART_INF_F, 0.f);
-      const float top = fmaxf(m, warp_max(ml.x)), use = top == -CUDART_INF_F ? 0.f : top;
-      const float w = ex2(ml.x - use), fade = ex2(m - use);
-      m = top;
-      sum = sum * fade + warp_sum(w * ml.y);
-#pragma unroll
-      for (int v = 0; v < VL; ++v) acc[v] *= fade;
-      for (int k = 0; k < n; k += 8) {
-        V x[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int a = __shfl_sync(0xffffffffu, at, min(k + q, n - 1));
-          x[q] = *reinterpret_cast<const V*>(part_o + (size_t)a * HD + lane * VL);
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float wk = k + q < n ? __shfl_sync(0xffffffffu, w, min(k + q, n - 1)) : 0.f;
-#pragma unroll
-          for (int v = 0; v < VL; ++v)
-            if (k + q < n) acc[v] += wk * reinterpret_cast<const float*>(&x[q])[v];
-        }
-      }
-    }
+    join_parts<HD>(d, b0, r, part_o, part_ml, tile, m, sum, acc);
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     const int grp = p.grp, node = (d.row0 + r) / grp;
     const int h = d.kvh * grp + (d.row0 + r) - node * grp;
-    if constexpr (PARTS) {
-      const size_t to = part_row(p, d.pass, d.lo + node, h);
-      *reinterpret_cast<V*>(p.row_o + to * HD + lane * VL) = *reinterpret_cast<const V*>(acc);
-      if (lane == 0) p.row_ml[to] = make_float2(m, sum);
-      continue;
-    }
     char* dst = p.out + (size_t)(d.lo + node) * p.out_ld + (size_t)(h * HD + lane * VL) * EL;
 #pragma unroll
     for (int v = 0; v < VL; ++v) acc[v] *= inv;
@@ -434,41 +458,47 @@ __global__ void __launch_bounds__(128) attend_join_kernel(AttendParams p, const 
   }
 }
 
-// Rows whose slots two parts hold: the group's and the entry's, joined and written.  Grid
-// (entries, up to 64 groups of four rows), a warp per row of a query head.  A part without
-// slots of the row has sum 0 and reference -inf.
+// Rows whose slots two parts hold, the group's and the entry's, each whole or of a cut tile:
+// joined and written.  Grid (entries, up to 256 groups of four rows), a warp per row of a query
+// head; `most`: blocks that may have left parts.  A part without slots of the row has sum 0 and
+// reference -inf.
 template <int EL, int HD>
-__global__ void __launch_bounds__(128) attend_combine_kernel(AttendParams p) {
+__global__ void __launch_bounds__(128) attend_combine_kernel(AttendParams p, const float* part_o, const float2* part_ml,
+                                                             int tile, int most) {
   constexpr int VL = HD / 32;
   using V = typename DimVec<VL>::T;
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  PartEntry x;
-  unsigned bad;
-  plan_entry(p, Cutting{16, 32, 0, 1, 1, 0}, p.n_group + blockIdx.x, x, bad);
-  const int rows = x.n * p.c.n_head;
-  for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < rows; r += 4 * gridDim.y) {
-    const int t = x.lo + r / p.c.n_head, h = r % p.c.n_head;
+  const int4 x = p.table[blockIdx.x];   // (rows that exist: checked by the plan)
+  const int rows = x.y * p.c.n_head;
+  for (int i = blockIdx.y * 4 + (threadIdx.x >> 5); i < rows; i += 4 * gridDim.y) {
+    const int t = x.x + i / p.c.n_head, h = i % p.c.n_head;
+    float m = -CUDART_INF_F, sum = 0.f;
+    alignas(16) float acc[VL] = {};
     const size_t at[2] = {part_row(p, 0, t, h), part_row(p, 1, t, h)};
-    float2 ml[2];
-    alignas(16) float f[2][VL];
-    ml[0] = make_float2(-CUDART_INF_F, 0.f);
+    const float2 ml[2] = {x.z ? p.row_ml[at[0]] : make_float2(-CUDART_INF_F, 0.f), p.row_ml[at[1]]};
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (k || x.base0) {
-        ml[k] = p.row_ml[at[k]];
-        *reinterpret_cast<V*>(f[k]) = *reinterpret_cast<const V*>(p.row_o + at[k] * HD + lane * VL);
-      } else {
+    for (int k = 0; k < 2; ++k) {
+      if (ml[k].y < 0.f) {
+        // (what a group that was skipped left may be anything: within the partial rows)
+        const int w = __float_as_int(ml[k].x), b0 = (int)fminf(-ml[k].y, 2.f * kAttendSms) - 1;
+        const int last = min(w >> 16, most - 1), r = min(w & 0x7fff, tile - 1);
+        if (b0 < most) join_parts<HD>({0, 0, 0, 0, last, 2 * b0 + (w >> 15 & 1)}, b0, r, part_o, part_ml, tile, m, sum, acc);
+      } else if (k || x.z) {
+        alignas(16) float o[VL];
+        *reinterpret_cast<V*>(o) = *reinterpret_cast<const V*>(p.row_o + at[k] * HD + lane * VL);
+        const float top = fmaxf(m, ml[k].x), use = top == -CUDART_INF_F ? 0.f : top;
+        const float w = ex2(ml[k].x - use), fade = ex2(m - use);
+        m = top;
+        sum = sum * fade + w * ml[k].y;
 #pragma unroll
-        for (int v = 0; v < VL; ++v) f[k][v] = 0.f;
+        for (int v = 0; v < VL; ++v) acc[v] = acc[v] * fade + w * o[v];
       }
-    const float m = fmaxf(ml[0].x, ml[1].x), use = m == -CUDART_INF_F ? 0.f : m;
-    const float w0 = ex2(ml[0].x - use), w1 = ex2(ml[1].x - use);
-    const float sum = w0 * ml[0].y + w1 * ml[1].y, inv = sum > 0.f ? 1.f / sum : 0.f;
-    alignas(16) float acc[VL];
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-    for (int v = 0; v < VL; ++v) acc[v] = (w0 * f[0][v] + w1 * f[1][v]) * inv;
+    for (int v = 0; v < VL; ++v) acc[v] *= inv;
     char* dst = p.out + (size_t)t * p.out_ld + (size_t)(h * HD + lane * VL) * EL;
     if constexpr (EL == 4) {
       *reinterpret_cast<V*>(dst) = *reinterpret_cast<const V*>(acc);
@@ -485,15 +515,18 @@ __global__ void __launch_bounds__(128) attend_combine_kernel(AttendParams p) {
 
 template <int EL, int HD, typename E>
 cudaError_t launch_join(const AttendParams& p, const AttendWork& w, int tile, int blocks, cudaStream_t st) {
-  const long long rows = (long long)(E::kParts ? p.rows.T : p.max_tree) * p.grp;
-  const int most = rows < tile ? (int)rows : tile;
-  const cudaError_t e =
-      launch_dependent(attend_join_kernel<EL, HD, E::kParts>, dim3(blocks, most < 64 ? (most + 3) / 4 : 16), 128, 0, st,
-                       p, (const Cut*)w.cuts, (const float*)w.part_o, (const float2*)w.part_ml, tile);
-  if (!E::kParts || e != cudaSuccess) return e;
-  const long long heads = (long long)p.max_tree * p.c.n_head;   // rows of an entry
-  return launch_dependent(attend_combine_kernel<EL, HD>, dim3(p.rows.n_seq, heads < 256 ? ((int)heads + 3) / 4 : 64), 128,
-                          0, st, p);
+  const float* part_o = w.part_o;
+  const float2* part_ml = w.part_ml;
+  if constexpr (E::kParts) {
+    const long long heads = (long long)p.max_tree * p.c.n_head;   // rows of an entry
+    return launch_dependent(attend_combine_kernel<EL, HD>, dim3(p.rows.n_seq, heads < 1024 ? ((int)heads + 3) / 4 : 256),
+                            128, 0, st, p, part_o, part_ml, tile, blocks);
+  } else {
+    const long long rows = (long long)p.max_tree * p.grp;
+    const int most = rows < tile ? (int)rows : tile;
+    return launch_dependent(attend_join_kernel<EL, HD>, dim3(blocks, most < 64 ? (most + 3) / 4 : 16), 128, 0, st, p,
+                            (const Cut*)w.cuts, part_o, part_ml, tile);
+  }
 }
 
 }  // namespace tree

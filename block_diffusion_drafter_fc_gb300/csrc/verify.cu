@@ -229,9 +229,7 @@ DF_DEVICE long long cluster_total(long long v, Shared<NT>& s, int S) {
     return sum;
   }
   cluster_sync();
-  long long all = 0;
-  for (int r = 0; r < S; ++r) all += peer(&s.told.v[k], r);
-  return all;
+  return warp_sum(lane < S ? peer(&s.told.v[k], lane) : 0ll);
 }
 
 // The cluster's winner among the threads' candidates (float key in powers of two, index; -1:

@@ -551,11 +551,12 @@ class PagedCache:
 
     def _norm(self, what: str, w) -> int:
         """Address of a head's norm weights."""
+        if (w.dtype is self.dtype and w.get_device() == self.device_index and w.dim() == 1
+                and w.shape[0] == self.cfg.head_dim and w.is_contiguous()):
+            return w.data_ptr()
         if w.get_device() != self.device_index:
             raise DFlashError(f"{what}: norm weights on {w.device}, not on the cache's device")
-        if w.dtype is not self.dtype or w.shape != (self.cfg.head_dim,) or not w.is_contiguous():
-            raise DFlashError(f"{what}: norm weights are contiguous [{self.cfg.head_dim}] {self.dtype}")
-        return w.data_ptr()
+        raise DFlashError(f"{what}: norm weights are contiguous [{self.cfg.head_dim}] {self.dtype}")
 
     def dflash_norm_append(self, layer: int, row_start, k, v, k_norm, depth=None, q=None, q_out=None,
                            q_norm=None, eps: float = 1e-6, seqs=None, stream=None):
@@ -579,47 +580,55 @@ class PagedCache:
             eps, qp, qs, qn, qop, qos, k.data_ptr(), ks, self._norm("norm_append", k_norm), v.data_ptr(), vs,
             self._on(stream)), "norm_append")
 
-    def _parts(self, what: str, T: int, heads: int, tensors, w, dw=None):
-        """Addresses and strides of a part's row tensors, weights after the first; all None: absent."""
-        if all(t is None for t in (*tensors, w)) and dw is None:
-            return None
-        if any(t is None for t in (*tensors, w)):
+    def _pair(self, what: str, T: int, heads: int, x, w, out):
+        """(address, stride) of x, address of its weights, (address, stride) of out; all None: nulls."""
+        if x is None or w is None or out is None:
+            if x is None and w is None and out is None:
+                return 0, 0, 0, 0, 0
             raise DFlashError(f"{what}: a part's tensors go together")
-        got = []
-        for t in tensors:
-            rows, stride = self._rows(t, what, heads)
-            if rows != T:
-                raise DFlashError(f"{what}: operands have different rows")
-            got += [t.data_ptr(), stride]
-        return got[:2] + [self._norm(what, w)] + got[2:]
+        rows, xs = self._rows(x, what, heads)
+        rows_out, os_ = self._rows(out, what, heads)
+        if rows != T or rows_out != T:
+            raise DFlashError(f"{what}: operands have different rows")
+        return x.data_ptr(), xs, self._norm(what, w), out.data_ptr(), os_
 
     def dflash_norm_rope(self, pos, q=None, q_norm=None, q_out=None, k=None, k_norm=None, k_out=None,
                          eps: float = 1e-6, stream=None):
-        if q is None and k is None:
+        x = k if q is None else q
+        if x is None:
             raise DFlashError("norm_rope: neither q nor k")
-        T = (k if q is None else q).shape[0]
-        a = self._parts("norm_rope", T, self.cfg.n_head, (q, q_out), q_norm) or [0] * 5
-        b = self._parts("norm_rope", T, self.cfg.n_head_kv, (k, k_out), k_norm) or [0] * 5
-        self._ok(LIB.dflash_norm_rope(self.h, T, self._int("norm_rope", pos, T), eps, *a, *b, self._on(stream)),
-                 "norm_rope")
+        T = x.shape[0]
+        self._ok(LIB.dflash_norm_rope(
+            self.h, T, self._int("norm_rope", pos, T), eps, *self._pair("norm_rope", T, self.cfg.n_head, q, q_norm, q_out),
+            *self._pair("norm_rope", T, self.cfg.n_head_kv, k, k_norm, k_out), self._on(stream)), "norm_rope")
 
-    def _sum(self, what: str, t) -> int:
-        if (t is None or t.dtype is not torch.float32 or t.shape != (self.cfg.head_dim,) or not t.is_contiguous()
-                or t.get_device() != self.device_index):
-            raise DFlashError(f"{what}: gradients of norm weights are contiguous f32 [head_dim] on the cache's device")
-        return t.data_ptr()
+    def _grad(self, T: int, heads: int, x, w, dout, dx, dw):
+        """_pair's, with the gradients of the result and of the weights."""
+        if dout is None or dw is None:
+            if all(t is None for t in (x, w, dout, dx, dw)):
+                return 0, 0, 0, 0, 0, 0, 0, 0
+            raise DFlashError("norm_rope_grad: a part's tensors go together")
+        rows, ds = self._rows(dout, "norm_rope_grad", heads)
+        if rows != T:
+            raise DFlashError("norm_rope_grad: operands have different rows")
+        p, xs, wp, dp, dxs = self._pair("norm_rope_grad", T, heads, x, w, dx)
+        if not p and x is None:
+            raise DFlashError("norm_rope_grad: a part's tensors go together")
+        if (dw.dtype is not torch.float32 or dw.dim() != 1 or dw.shape[0] != self.cfg.head_dim or not dw.is_contiguous()
+                or dw.get_device() != self.device_index):
+            raise DFlashError("norm_rope_grad: gradients of norm weights are contiguous f32 [head_dim] on the cache's device")
+        return p, xs, wp, dout.data_ptr(), ds, dp, dxs, dw.data_ptr()
 
     def dflash_norm_rope_grad(self, pos, q=None, q_norm=None, dq_out=None, dq=None, dq_norm=None, k=None,
                               k_norm=None, dk_out=None, dk=None, dk_norm=None, eps: float = 1e-6, stream=None):
-        if q is None and k is None:
+        x = k if q is None else q
+        if x is None:
             raise DFlashError("norm_rope_grad: neither q nor k")
-        T = (k if q is None else q).shape[0]
-        a = self._parts("norm_rope_grad", T, self.cfg.n_head, (q, dq_out, dq), q_norm, dq_norm)
-        b = self._parts("norm_rope_grad", T, self.cfg.n_head_kv, (k, dk_out, dk), k_norm, dk_norm)
-        a = a + [self._sum("norm_rope_grad", dq_norm)] if a else [0] * 8
-        b = b + [self._sum("norm_rope_grad", dk_norm)] if b else [0] * 8
-        self._ok(LIB.dflash_norm_rope_grad(self.h, T, self._int("norm_rope_grad", pos, T), eps, *a, *b,
-                                           self._on(stream)), "norm_rope_grad")
+        T = x.shape[0]
+        self._ok(LIB.dflash_norm_rope_grad(
+            self.h, T, self._int("norm_rope_grad", pos, T), eps,
+            *self._grad(T, self.cfg.n_head, q, q_norm, dq_out, dq, dq_norm),
+            *self._grad(T, self.cfg.n_head_kv, k, k_norm, dk_out, dk, dk_norm), self._on(stream)), "norm_rope_grad")
 
     def dflash_tree_mask(self, row_start, parents, mask, depth=None, stream=None):
         T, shape = parents.shape[0], mask.shape
@@ -701,12 +710,13 @@ class PagedCache:
 
     def _logits(self, what: str, t):
         """(address, row stride, dtype code, rows, tokens) of logits [rows][n_vocab]."""
-        code = _LOGITS.get(t.dtype)
-        if code is None or t.dim() != 2 or t.stride(1) != 1 and t.shape[1] > 1:
+        code, shape = _LOGITS.get(t.dtype), t.shape
+        if code is None or len(shape) != 2 or (t.stride(1) != 1 and shape[1] > 1):
             raise DFlashError(f"{what}: logits are f32 or bf16 [rows][n_vocab], a row's contiguous")
         if t.get_device() != self.device_index:
             raise DFlashError(f"{what}: logits on {t.device}, not on the cache's device")
-        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1], code, t.shape[0], t.shape[1]
+        rows, vocab = shape
+        return t.data_ptr(), t.stride(0) if rows > 1 else vocab, code, rows, vocab
 
     def _floats(self, what: str, t, n: int) -> int:
         """Address of a contiguous f32 tensor of at least n values (None: null)."""
