@@ -18,8 +18,7 @@
 // what is compared is exact to far below the gaps: sums are 64-bit whole numbers of fp32
 // weights (m being whole, moving it shifts them), a test's probabilities are 2^frac in fp32
 // times an exact power of two and the sum (2e-7); in a race the candidates that single fp32
-// operations cannot tell apart (a block's within 2^-9) are compared again as 64-bit whole
-// numbers of 2^-32.  All of it without fp64 units, of which an SM has two lanes here: with the
+// operations cannot tell apart (within 2^-9) are compared again as 64-bit whole numbers of 2^-32.  All of it without fp64 units, of which an SM has two lanes here: with the
 // sums and the winners in fp64, 480 draws in blocks of two tiles took 69 us, without 45 (and in
 // one round of blocks 22).
 //
@@ -172,11 +171,6 @@ DF_DEVICE long long log2_of(float e) {
 
 // ------------------------------------------------------------------ reductions
 
-DF_DEVICE long long warp_sum(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
 // The larger key, the lower index of equal ones (-1: none).
 DF_DEVICE void best_of(long long& v, int& i, long long v2, int i2) {
   if (i2 >= 0 && (i < 0 || v2 > v || (v2 == v && i2 < i))) {
@@ -184,24 +178,36 @@ DF_DEVICE void best_of(long long& v, int& i, long long v2, int i2) {
     i = i2;
   }
 }
+// ... of the warp's lanes that have one: usually a single one.
 DF_DEVICE void warp_best(long long& v, int& i) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const long long v2 = __shfl_xor_sync(0xffffffffu, v, o);
-    const int i2 = __shfl_xor_sync(0xffffffffu, i, o);
-    best_of(v, i, v2, i2);
+  unsigned has = __ballot_sync(0xffffffffu, i >= 0);
+  if (!has) return;
+  const int at = __ffs(has) - 1;
+  long long bv = __shfl_sync(0xffffffffu, v, at);
+  int bi = __shfl_sync(0xffffffffu, i, at);
+  for (has &= has - 1; has; has &= has - 1) {
+    const int k = __ffs(has) - 1;
+    const long long v2 = __shfl_sync(0xffffffffu, v, k);
+    best_of(bv, bi, v2, __shfl_sync(0xffffffffu, i, k));
   }
+  v = bv;
+  i = bi;
 }
-// A float's bits in its order (whole numbers).
-DF_DEVICE long long order_of(float x) {
+// A float's bits in its order (a whole number), and back.
+DF_DEVICE int order_of(float x) {
   const int b = __float_as_int(x == 0.f ? 0.f : x);
-  return b < 0 ? (long long)(b ^ 0x7fffffff) : (long long)b;
+  return b < 0 ? b ^ 0x7fffffff : b;
+}
+DF_DEVICE float largest(float x) {   // of the warp
+  const int b = __reduce_max_sync(0xffffffffu, order_of(x));
+  return __int_as_float(b < 0 ? b ^ 0x7fffffff : b);
 }
 
 // What a block tells its cluster, twice: a block may write one while others read the other.
 struct Told {
   long long v[2];
-  int i[2], bad[2];
+  float key[2];
+  int i[2], n[2];   // n: candidates; -1: something is bad
 };
 template <int NT>
 struct Shared {
@@ -212,14 +218,21 @@ struct Shared {
   int turn;      // which of the two is next (the same in all blocks)
 };
 
+template <int N>
+DF_DEVICE long long lane_sum(long long v) {   // of lanes 0 .. N - 1 (a power of two), in all of them
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+
 // Sum of v over the cluster (all threads, the same everywhere).
 template <int NT>
 DF_DEVICE long long cluster_total(long long v, Shared<NT>& s, int S) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = s.turn;
-  v = warp_sum(v);
+  v = lane_sum<32>(v);
   if (lane == 0) s.w_v[warp] = v;
   __syncthreads();
-  const long long sum = warp_sum(lane < NT / 32 ? s.w_v[lane] : 0ll);
+  const long long sum = lane_sum<NT / 32>(lane < NT / 32 ? s.w_v[lane] : 0ll);
   if (threadIdx.x == 0) {
     s.told.v[k] = sum;
     s.turn = k ^ 1;
@@ -229,29 +242,53 @@ DF_DEVICE long long cluster_total(long long v, Shared<NT>& s, int S) {
     return sum;
   }
   cluster_sync();
-  return warp_sum(lane < S ? peer(&s.told.v[k], lane) : 0ll);
+  return lane_sum<8>(lane < S ? peer(&s.told.v[k], lane) : 0ll);
 }
 
 // The cluster's winner among the threads' candidates (float key in powers of two, index; -1:
-// none): those within 2^-9 and a rounding of the block's largest are compared by exact(), of
-// the thread's own.  bad: any thread's flag.
+// none).  Where others come within 2^-9 and a rounding of the largest, they are compared by
+// exact(), of the thread's own (a race in two hundred).  bad: any thread's flag.
 template <int NT, typename F>
 DF_DEVICE int cluster_winner(float key, int i, bool& bad, F exact, Shared<NT>& s, int S) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = s.turn;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int k = s.turn;
   const float mine = i >= 0 ? key : -CUDART_INF_F;
-  const float w = warp_max(mine);
+  const float w = largest(mine);
   if (lane == 0) s.w_f[warp] = w;
   const int any = __syncthreads_or(bad);
-  const float top = warp_max(lane < NT / 32 ? s.w_f[lane] : -CUDART_INF_F);
-  const float near = top - 0x1p-9f - fabsf(top) * 0x1p-20f;
-  long long v = 0;
-  if (i >= 0) {
-    if (mine >= near || mine == top)
-      v = exact();
-    else
-      i = -1;
+  float top = largest(lane < NT / 32 ? s.w_f[lane] : -CUDART_INF_F);
+  auto near = [](float key, float top) { return key == top || key >= top - 0x1p-9f - fabsf(top) * 0x1p-20f; };
+  bool in = i >= 0 && near(mine, top);
+  if (in) s.told.i[k] = i;   // (one of them: all that is needed of a single one)
+  const int n = __syncthreads_count(in);
+  if (threadIdx.x == 0) {
+    s.told.key[k] = top;
+    s.told.n[k] = any ? -1 : n;
+    s.turn = k ^ 1;
   }
-  if (__any_sync(0xffffffffu, i >= 0)) warp_best(v, i);
+  auto meet = [&] {
+    if (S == 1)
+      __syncthreads();
+    else
+      cluster_sync();
+  };
+  meet();
+  float their = lane < S ? peer(&s.told.key[k], lane) : -CUDART_INF_F;
+  int their_n = lane < S ? peer(&s.told.n[k], lane) : 0, their_i = lane < S ? peer(&s.told.i[k], lane) : -1;
+  bad = __any_sync(0xffffffffu, their_n < 0);
+  if (bad) return -1;
+  top = largest(their_n > 0 ? their : -CUDART_INF_F);
+  const bool close = their_n > 0 && near(their, top);
+  const unsigned who = __ballot_sync(0xffffffffu, close);
+  if (!who) return -1;
+  const int first = __ffs(who) - 1;
+  if ((who & (who - 1)) == 0 && __shfl_sync(0xffffffffu, their_n, first) == 1) return __shfl_sync(0xffffffffu, their_i, first);
+  // ---- too close
+  k ^= 1;
+  in = in && near(mine, top);
+  long long v = in ? exact() : 0;
+  i = in ? i : -1;
+  warp_best(v, i);
   if (lane == 0) {
     s.w_v[warp] = v;
     s.w_i[warp] = i;
@@ -264,17 +301,12 @@ DF_DEVICE int cluster_winner(float key, int i, bool& bad, F exact, Shared<NT>& s
     if (lane == 0) {
       s.told.v[k] = v;
       s.told.i[k] = i;
-      s.told.bad[k] = any;
       s.turn = k ^ 1;
     }
   }
-  if (S == 1)
-    __syncthreads();
-  else
-    cluster_sync();
+  meet();
   v = lane < S ? peer(&s.told.v[k], lane) : 0;
   i = lane < S ? peer(&s.told.i[k], lane) : -1;
-  bad = __any_sync(0xffffffffu, lane < S && peer(&s.told.bad[k], lane));
   warp_best(v, i);
   return i;
 }
@@ -361,11 +393,11 @@ DF_DEVICE void row_piece(const char* row, int V, float temperature, bool draft, 
     }
   }
   // one reference for all: the largest
-  const float w = warp_max(m);
+  const float w = largest(m);
   if (lane == 0) w_f[warp] = w;
   __syncthreads();
-  const float top = warp_max(lane < kThreads / 32 ? w_f[lane] : -kScoreMost);
-  sum = warp_sum(sum >> (int)fminf(top - m, 63.f));
+  const float top = largest(lane < kThreads / 32 ? w_f[lane] : -kScoreMost);
+  sum = lane_sum<32>(sum >> (int)fminf(top - m, 63.f));
   if (lane == 0) w_v[warp] = sum;
   const int any = __syncthreads_or(bad);
   if (threadIdx.x == 0) {
@@ -399,7 +431,7 @@ struct RowStats {
 
 // Row `r` from its pieces, by `G` neighbouring lanes (a power of two, all of the warp's lanes
 // call; the result is theirs alike).
-DF_DEVICE RowStats row_of(const Piece* pieces, int P, int r, float temperature, int G) {
+DF_DEVICE RowStats row_of(const Piece* pieces, int P, int r, float s, int G) {
   const int lane = threadIdx.x & (G - 1);
   long long z = 0, v = 0;
   float top = -kScoreMost;
@@ -409,7 +441,7 @@ DF_DEVICE RowStats row_of(const Piece* pieces, int P, int r, float temperature, 
     bad |= x.z == kNoPiece;
     if (x.z == kGreedyPiece) {
       greedy = 1;
-      best_of(v, arg, order_of(x.m), x.arg);
+      best_of(v, arg, (long long)order_of(x.m), x.arg);
     } else if (x.z >= 0) {
       const float to = fmaxf(top, x.m);
       z = (z >> (int)fminf(to - top, 63.f)) + (x.z >> (int)fminf(to - x.m, 63.f));
@@ -426,7 +458,6 @@ DF_DEVICE RowStats row_of(const Piece* pieces, int P, int r, float temperature, 
     greedy |= __shfl_xor_sync(0xffffffffu, greedy, o);
     bad |= __shfl_xor_sync(0xffffffffu, bad, o);
   }
-  const float s = slope_of(temperature).hi;
   if (bad || (!greedy && z <= 0)) return {CUDART_NAN_F, s, 0};
   if (greedy) return {-1.f, s, arg};
   return {__fdiv_rn(kUnit, __ll2float_rn(z)), s, (int)top};
@@ -505,7 +536,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         }
       }
     }
-    i = cluster_winner(top, i, bad, [&] { return order_of(top); }, s, S);
+    i = cluster_winner(top, i, bad, [&] { return (long long)order_of(top); }, s, S);
   } else {
     i = race<EL, VEC>(row, p.noise + (size_t)t * p.noise_ld, p.V, temperature, bad, [](int) { return false; }, s, S);
   }
@@ -524,7 +555,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
 struct Node {
   float p, q;          // the target's and the drafter's probability of its token (before: its logits)
   RowStats own, from;  // its row of the target; the row of the drafter that its token was drawn from
-  int token;
+  int token, row;      // row: of the drafter
   float u;
   short parent, first; // first child (0: none)
   short is;            // bits of Is
@@ -566,7 +597,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
   auto target_row = [&](int node) { return p.target.at + (size_t)(lo + node) * p.target.ld; };
   auto draft_of = [&](int node) { return p.draft_row ? p.draft_row[lo + node] : lo + node; };
   auto draft_row = [&](int d) { return p.draft.at + (size_t)d * p.draft.ld; };
-  auto draft_stats = [&](int d, int G) { return row_of(p.stats + (size_t)p.rows.T * p.pieces, p.pieces, d, heat_at(p.draft.temperature, d), G); };
   // every node's test, should the walk come to it: first what the sums are not needed for
   for (int i = tid; i < n; i += NT) {
     const int up = p.parents[lo + i];
@@ -575,16 +605,22 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
     nd.token = p.tokens[lo + i];
     nd.u = p.uniform[lo + i];
     nd.p = nd.q = 0.f;
+    nd.row = 0;
     nd.first = 0;
+    nd.own.s = slope_of(heat_at(p.target.temperature, lo + i)).hi;
+    nd.from.s = 0.f;
     nd.is = nd.token >= 0 && nd.token < V ? 0 : kNoToken;
     if (nd.parent >= 0 && !nd.is) {
       nd.p = logit(target_row(up), ELT, nd.token);
       if constexpr (ELD > 0) {
         const int d = draft_of(i);
-        if (d >= 0 && d < p.draft.rows)
+        if (d >= 0 && d < p.draft.rows) {
           nd.q = logit(draft_row(d), ELD, nd.token);
-        else
+          nd.from.s = slope_of(heat_at(p.draft.temperature, d)).hi;
+          nd.row = d;
+        } else {
           nd.is |= kNoDraft;
+        }
       }
     }
     s_node[i] = nd;
@@ -610,11 +646,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
   for (int i0 = tid / 32 * (32 / G); i0 < n; i0 += NT / G) {
     const int i = min(i0 + (tid & 31) / G, n - 1);
     const bool mine = (tid & (G - 1)) == 0 && i0 + (tid & 31) / G < n;
-    const RowStats st = row_of(p.stats, p.pieces, lo + i, heat_at(p.target.temperature, lo + i), G);
+    const RowStats st = row_of(p.stats, p.pieces, lo + i, s_node[i].own.s, G);
     if (mine) s_node[i].own = st;
     if constexpr (ELD > 0) {
-      const int d = draft_of(i);
-      const RowStats sd = draft_stats(d >= 0 && d < p.draft.rows ? d : 0, G);
+      const RowStats sd = row_of(p.stats, p.pieces, p.rows.T + s_node[i].row, s_node[i].from.s, G);
       if (mine) s_node[i].from = sd;
     }
   }
@@ -745,13 +780,14 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
       const int cur = s_cur, barred = s_n_barred, written = s_written;
       const RowStats st = s_node[cur].own, sd = s_node[s_child].from;
       const float inv = (written ? 1.f : st.inv) / (float)s_total, inv_d = sd.inv, m = (float)-st.m, md = (float)-sd.m;
-      const char *row = target_row(cur), *row_d = draft_row(draft_of(s_child));
+      const char *row = target_row(cur), *row_d = draft_row(s_node[s_child].row);
       long long units = 0;   // of 2^-50 (r adds up to at most 1)
-#pragma unroll 2
-      for (int t0 = rank * kTile, at = 0; t0 < V; t0 += S * kTile, at += kTile) {
-        float x[8], y[8];
+      float x[2][8], y[2][8];
+      auto fetch = [&](int t0, float(&x)[8], float(&y)[8]) {
         load8<ELD, VEC, NT>(row_d, t0, V, -CUDART_INF_F, y);
         if (!written) load8<ELT, VEC, NT>(row, t0, V, -CUDART_INF_F, x);
+      };
+      auto take = [&](int t0, int at, const float(&x)[8], const float(&y)[8]) {
         float part = 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -764,6 +800,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
           part += r;
         }
         units += __float2ll_rn(part * 0x1p50f);
+      };
+      const int hop = S * kTile;
+      int t0 = rank * kTile, at = 0;
+      fetch(t0, x[0], y[0]);
+      for (; t0 < V; t0 += 2 * hop, at += 2 * kTile) {   // (the next tile on its way under a tile's arithmetic)
+        fetch(t0 + hop, x[1], y[1]);
+        take(t0, at, x[0], y[0]);
+        if (t0 + hop >= V) break;
+        fetch(t0 + 2 * hop, x[0], y[0]);
+        take(t0 + hop, at + kTile, x[1], y[1]);
       }
       const double sum = (double)cluster_total(units, s, S) * 0x1p-50;
       if (tid == 0) {   // (nothing left, by rounding alone: the target's own)
@@ -793,36 +839,48 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
     const char* row_d = nullptr;
     if (less) {
       sd = s_node[s_child].from;
-      row_d = draft_row(draft_of(s_child));
+      row_d = draft_row(s_node[s_child].row);
     }
     const float inv = (written ? 1.f : st.inv) / (float)s_total, inv_d = sd.inv, m = (float)-st.m, md = (float)-sd.m;
     const char* row = target_row(cur);
-    float top = -CUDART_INF_F, at_x = 0.f, at_y = 0.f, at_e = 1.f;
+    float best = 0.f, at_x = 0.f, at_y = 0.f, at_e = 1.f;   // best / at_e is the largest so far
     int win = -1;
-#pragma unroll 2
-    for (int t0 = rank * kTile, at = 0; t0 < V; t0 += S * kTile, at += kTile) {
-      float x[8], y[8], z[8];
-      load8<4, VEC, NT>(noise, t0, V, 1.f, z);
+    float x[2][8], y[2][8], z[2][8];
+    auto fetch = [&](int t0, float(&x)[8], float(&y)[8], float(&z)[8]) {
+      load8<4, VEC, NT>(noise, t0, V, CUDART_NAN_F, z);
       if constexpr (ELD > 0) {
         if (less) load8<ELD, VEC, NT>(row_d, t0, V, -CUDART_INF_F, y);
       }
       if (!written) load8<ELT, VEC, NT>(row, t0, V, -CUDART_INF_F, x);
+    };
+    auto take = [&](int t0, int at, float(&x)[8], const float(&y)[8], const float(&z)[8]) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int i = element<VEC, NT>(t0, k);
         if (written) x[k] = s_r[at + i - t0];
         float r = (written ? x[k] : ex2(fmaf(x[k], st.s, m))) * inv;
         if (less) r = r - ex2(fmaf(y[k], sd.s, md)) * inv_d;
-        const float key = lg2(r) - lg2(z[k]);   // (NaN for what is not positive)
-        if (i < V && r > 0.f && key > top && !is_barred(i)) {
-          top = key;
+        // (r / z above the best, without a quotient)
+        if (r > 0.f && z[k] >= 0.f && r * at_e > best * z[k] && !is_barred(i)) {
+          best = r;
           win = i;
           at_x = x[k];
           at_e = z[k];
           if (less) at_y = y[k];
         }
       }
+    };
+    const int hop = S * kTile;
+    int t0 = rank * kTile, at = 0;
+    fetch(t0, x[0], y[0], z[0]);
+    for (; t0 < V; t0 += 2 * hop, at += 2 * kTile) {
+      fetch(t0 + hop, x[1], y[1], z[1]);
+      take(t0, at, x[0], y[0], z[0]);
+      if (t0 + hop >= V) break;
+      fetch(t0 + 2 * hop, x[0], y[0], z[0]);
+      take(t0 + hop, at + kTile, x[1], y[1], z[1]);
     }
+    const float top = lg2(best) - lg2(at_e);
     token = cluster_winner(top, win, bad, [&] {
       float r = (written ? at_x : weight_of(at_x, st.s, st.m)) * inv;
       if (less) r = fmaf(-weight_of(at_y, sd.s, sd.m), inv_d, r);
