@@ -125,15 +125,18 @@ inline Shape columns_of(int items) {
 constexpr int kSms = 152;
 // Blocks that the GPU holds at once, `threads` threads an SM.
 inline int wave_of(const Shape& s, int threads) { return kSms * (threads / s.threads > 1 ? threads / s.threads : 1); }
-// Whole rounds of blocks of up to kMaxRows rows.
+// Whole rounds of blocks of up to kRound rows (the append of 8192 rows of 48 heads: 39.4 us in
+// blocks of 9 rows, 40.5 of 14, 40.7 of 27: the next round's look-ups run under a round's copies).
+constexpr int kRound = 12;
 inline Shape shape_of(int T, int items, int threads) {
   Shape s = columns_of(items);
   const int wave = wave_of(s, threads);
-  const long long per = (long long)T * s.gy, round = (long long)wave * (kMaxRows / s.side * s.side);
+  const int most = kRound > s.side ? kRound / s.side * s.side : s.side;
+  const long long per = (long long)T * s.gy, round = (long long)wave * most;
   const long long waves = (per + round - 1) / round;
   long long rows = (per + wave * waves - 1) / (wave * waves);
   rows = (rows + s.side - 1) / s.side * s.side;
-  s.rows = (int)(rows < kMaxRows / s.side * s.side ? rows : kMaxRows / s.side * s.side);
+  s.rows = (int)(rows < most ? rows : most);
   s.gx = (int)(((long long)T + s.rows - 1) / s.rows);
   return s;
 }
@@ -141,10 +144,10 @@ inline Shape shape_of(int T, int items, int threads) {
 inline Shape sum_shape_of(int T, int items, int threads, int limit) {
   Shape s = columns_of(items);
   const int most = wave_of(s, threads) < limit ? wave_of(s, threads) : limit;
-  const int least = (T + s.side - 1) / s.side, gx = most / s.gy > 1 ? most / s.gy : 1;
-  s.gx = gx < least ? gx : least;
-  s.rows = (T + s.gx - 1) / s.gx;
-  s.rows = (s.rows + s.side - 1) / s.side * s.side;
+  const long long least = ((long long)T + s.side - 1) / s.side, gx = most / s.gy > 1 ? most / s.gy : 1;
+  s.gx = (int)(gx < least ? gx : least);
+  const long long rows = ((long long)T + s.gx - 1) / s.gx;
+  s.rows = (int)((rows + s.side - 1) / s.side * s.side);
   s.gx = (int)(((long long)T + s.rows - 1) / s.rows);
   return s;
 }

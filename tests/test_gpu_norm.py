@@ -280,3 +280,31 @@ def test_norm_append_agrees_with_norm_rope_and_append():
     assert torch.equal(q1, q2)
     assert torch.equal(c.pages[int(c.table[0, 0]), 0, 0, :, 10:16].transpose(0, 1), k1[:6])
     assert float(c.pages[int(c.table[1, 1])].abs().sum()) == 0
+
+
+def test_offsets_past_32_bits():
+    """Rows behind 4 GB: the last ones, forward and gradient, against 64 bits."""
+    hq, hkv, hd, T = 32, 8, 128, 420_001
+    c = make(n_head=hq, n_head_kv=hkv, head_dim=hd)
+    x = torch.zeros(T, hq + hkv, hd, dtype=torch.bfloat16, device="cuda")
+    assert x.numel() * 2 > 1 << 32
+    g = torch.Generator().manual_seed(0)
+    rows = [0, 1, T // 2, T - 2, T - 1]
+    part = normal(g, (len(rows), hq + hkv, hd), "bf16")
+    x[rows] = part.cuda()
+    w = weights(g, hd, "bf16")
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    rd, f, m = rope_setup(hd, "half", None, {})
+    args = (np.asarray(rows), EPS, "half", rd, f, m, HALF["bf16"])
+    dy = normal(g, (len(rows), hkv, hd), "bf16")
+    dys = torch.zeros(T, hkv, hd, dtype=torch.bfloat16, device="cuda")
+    dys[rows] = dy.cuda()
+    dw = torch.zeros(hd, device="cuda")
+    c.dflash_norm_rope_grad(pos, k=x[:, hq:], k_norm=w.cuda(), dk_out=dys, dk=dys, dk_norm=dw)
+    ex, tx, ew, tw = N.backward(np64(part[:, hq:]), np64(w), np64(dy), *args, 3000)
+    check(np64(dys[rows]), ex, tx, "dx")
+    check(np64(dw), ew, tw, "dw")
+    c.dflash_norm_rope(pos, q=x[:, :hq], q_norm=w.cuda(), q_out=x[:, :hq], k=x[:, hq:], k_norm=w.cuda(), k_out=x[:, hq:])
+    y, tol = N.forward(np64(part), np64(w), *args)
+    check(np64(x[rows]), y, tol, "rows")
+    assert c.dflash_cache_read_status() == 0
