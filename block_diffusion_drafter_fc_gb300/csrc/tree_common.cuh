@@ -459,68 +459,131 @@ __global__ void __launch_bounds__(128) attend_join_kernel(AttendParams p, const 
 }
 
 // Rows whose slots two parts hold, the group's and the entry's, each whole or of a cut tile:
-// joined and written.  Grid (entries, up to 256 groups of four rows), a warp per row of a query
-// head; `most`: blocks that may have left parts.  A part without slots of the row has sum 0 and
-// reference -inf.
-template <int EL, int HD>
+// joined and written.  Grid (entries, groups of rows); LANES lanes a row of a query head, which
+// look up LANES of its parts at a time and read 16 pieces of 16 bytes at once.  `most`: blocks
+// that may have left parts.  A part without slots of the row has sum 0 and reference -inf.
+template <int EL, int HD, int LANES>
 __global__ void __launch_bounds__(128) attend_combine_kernel(AttendParams p, const float* part_o, const float2* part_ml,
                                                              int tile, int most) {
-  constexpr int VL = HD / 32;
-  using V = typename DimVec<VL>::T;
+  constexpr int NC = HD / (4 * LANES), B = 16 / NC, R = 32 / LANES;   // pieces of a lane, parts at once, rows of a warp
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, sub = lane % LANES;
   const int4 x = p.table[blockIdx.x];   // (rows that exist: checked by the plan)
   const int rows = x.y * p.c.n_head;
-  for (int i = blockIdx.y * 4 + (threadIdx.x >> 5); i < rows; i += 4 * gridDim.y) {
-    const int t = x.x + i / p.c.n_head, h = i % p.c.n_head;
+  for (int i0 = (blockIdx.y * 4 + (threadIdx.x >> 5)) * R; i0 < rows; i0 += 4 * R * gridDim.y) {
+    const int i = i0 + lane / LANES;
+    const bool real = i < rows;
+    const int node = (real ? i : 0) / p.c.n_head, t = x.x + node, h = (real ? i : 0) - node * p.c.n_head;
+    const size_t at0 = part_row(p, 0, t, h), at1 = part_row(p, 1, t, h);
+    const float2 none = make_float2(-CUDART_INF_F, 0.f);
+    const float2 ml0 = real && x.z ? p.row_ml[at0] : none, ml1 = real ? p.row_ml[at1] : none;
+    // a cut tile's: first and last block (what a group that was skipped left may be anything:
+    // within the partial rows)
+    auto first_of = [&](const float2& ml) { return ml.y < 0.f ? min((int)fminf(-ml.y, 2.f * kAttendSms) - 1, most - 1) : -1; };
+    auto count_of = [&](const float2& ml, int b0) {
+      return b0 < 0 ? 1 : max(min(__float_as_int(ml.x) >> 16, most - 1) - b0 + 1, 0);
+    };
+    const int b0 = first_of(ml0), b1 = first_of(ml1);
+    const int n0 = real && x.z ? count_of(ml0, b0) : 0, n = n0 + (real ? count_of(ml1, b1) : 0);
+    const int n_warp = __reduce_max_sync(0xffffffffu, n);
     float m = -CUDART_INF_F, sum = 0.f;
-    alignas(16) float acc[VL] = {};
-    const size_t at[2] = {part_row(p, 0, t, h), part_row(p, 1, t, h)};
-    const float2 ml[2] = {x.z ? p.row_ml[at[0]] : make_float2(-CUDART_INF_F, 0.f), p.row_ml[at[1]]};
+    float4 acc[NC];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (ml[k].y < 0.f) {
-        // (what a group that was skipped left may be anything: within the partial rows)
-        const int w = __float_as_int(ml[k].x), b0 = (int)fminf(-ml[k].y, 2.f * kAttendSms) - 1;
-        const int last = min(w >> 16, most - 1), r = min(w & 0x7fff, tile - 1);
-        if (b0 < most) join_parts<HD>({0, 0, 0, 0, last, 2 * b0 + (w >> 15 & 1)}, b0, r, part_o, part_ml, tile, m, sum, acc);
-      } else if (k || x.z) {
-        alignas(16) float o[VL];
-        *reinterpret_cast<V*>(o) = *reinterpret_cast<const V*>(p.row_o + at[k] * HD + lane * VL);
-        const float top = fmaxf(m, ml[k].x), use = top == -CUDART_INF_F ? 0.f : top;
-        const float w = ex2(ml[k].x - use), fade = ex2(m - use);
-        m = top;
-        sum = sum * fade + w * ml[k].y;
+    for (int v = 0; v < NC; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < n_warp; j0 += LANES) {
+      const int j = j0 + sub;
+      float2 its = none;
+      const float* src = p.row_o;
+      if (j < n) {
+        const bool own = j >= n0;
+        const int b = own ? b1 : b0, k = own ? j - n0 : j, w = __float_as_int(own ? ml1.x : ml0.x);
+        if (b >= 0) {
+          const size_t at = (size_t)(k ? 2 * (b + k) : 2 * b + (w >> 15 & 1)) * tile + min(w & 0x7fff, tile - 1);
+          its = part_ml[at];
+          src = part_o + at * HD;
+        } else {
+          its = own ? ml1 : ml0;
+          src += (own ? at1 : at0) * HD;
+        }
+      }
+      float top = its.x;
 #pragma unroll
-        for (int v = 0; v < VL; ++v) acc[v] = acc[v] * fade + w * o[v];
+      for (int o = LANES / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      top = fmaxf(top, m);
+      const float use = top == -CUDART_INF_F ? 0.f : top, w = ex2(its.x - use), fade = ex2(m - use);
+      float s = w * its.y;
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      m = top;
+      sum = sum * fade + s;
+#pragma unroll
+      for (int v = 0; v < NC; ++v) {
+        acc[v].x *= fade;
+        acc[v].y *= fade;
+        acc[v].z *= fade;
+        acc[v].w *= fade;
+      }
+      const int count = n - j0;   // this row's parts left
+      for (int q0 = 0; q0 < min(LANES, n_warp - j0); q0 += B) {
+        float4 o[B][NC];
+#pragma unroll
+        for (int q = 0; q < B; ++q) {
+          const unsigned long long from = __shfl_sync(0xffffffffu, (unsigned long long)src, q0 + q, LANES);
+          if (q0 + q < LANES && q0 + q < count)
+#pragma unroll
+            for (int v = 0; v < NC; ++v)
+              o[q][v] = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(from) + v * 4 * LANES + sub * 4);
+        }
+#pragma unroll
+        for (int q = 0; q < B; ++q) {
+          const float wq = __shfl_sync(0xffffffffu, w, q0 + q, LANES);
+          if (q0 + q < LANES && q0 + q < count)
+#pragma unroll
+            for (int v = 0; v < NC; ++v) {
+              acc[v].x += wq * o[q][v].x;
+              acc[v].y += wq * o[q][v].y;
+              acc[v].z += wq * o[q][v].z;
+              acc[v].w += wq * o[q][v].w;
+            }
+        }
       }
     }
+    if (!real) continue;
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    char* dst = p.out + (size_t)t * p.out_ld + (size_t)h * HD * EL;
 #pragma unroll
-    for (int v = 0; v < VL; ++v) acc[v] *= inv;
-    char* dst = p.out + (size_t)t * p.out_ld + (size_t)(h * HD + lane * VL) * EL;
-    if constexpr (EL == 4) {
-      *reinterpret_cast<V*>(dst) = *reinterpret_cast<const V*>(acc);
-    } else if constexpr (VL == 1) {
-      *reinterpret_cast<uint16_t*>(dst) = f32_to_bf16_bits(acc[0]);
-    } else {
-#pragma unroll
-      for (int v = 0; v < VL; v += 2) reinterpret_cast<uint32_t*>(dst)[v / 2] = pack_bf16x2(acc[v], acc[v + 1]);
+    for (int v = 0; v < NC; ++v) {
+      const float4 y = make_float4(acc[v].x * inv, acc[v].y * inv, acc[v].z * inv, acc[v].w * inv);
+      char* to = dst + (v * 4 * LANES + sub * 4) * EL;
+      if constexpr (EL == 4)
+        *reinterpret_cast<float4*>(to) = y;
+      else
+        *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
     }
-    if (p.lse && lane == 0)
+    if (p.lse && sub == 0)
       p.lse[(size_t)t * p.c.n_head + h] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -CUDART_INF_F;
   }
 }
+
+constexpr int kManyRows = 8192;
 
 template <int EL, int HD, typename E>
 cudaError_t launch_join(const AttendParams& p, const AttendWork& w, int tile, int blocks, cudaStream_t st) {
   const float* part_o = w.part_o;
   const float2* part_ml = w.part_ml;
   if constexpr (E::kParts) {
+    // a lane a piece while rows are few (their parts are many, and each round of loads counts);
+    // eight lanes a row, so that more rows are under way at once, beyond COMBINEFIG
     const long long heads = (long long)p.max_tree * p.c.n_head;   // rows of an entry
-    return launch_dependent(attend_combine_kernel<EL, HD>, dim3(p.rows.n_seq, heads < 1024 ? ((int)heads + 3) / 4 : 256),
-                            128, 0, st, p, part_o, part_ml, tile, blocks);
+    auto grid = [&](int lanes) {
+      const int r = 4 * (32 / lanes);   // rows of a block
+      return dim3(p.rows.n_seq, heads < 256 * r ? ((int)heads + r - 1) / r : 256);
+    };
+    if ((long long)p.rows.T * p.c.n_head < kManyRows)
+      return launch_dependent(attend_combine_kernel<EL, HD, HD / 4>, grid(HD / 4), 128, 0, st, p, part_o, part_ml, tile,
+                              blocks);
+    return launch_dependent(attend_combine_kernel<EL, HD, 8>, grid(8), 128, 0, st, p, part_o, part_ml, tile, blocks);
   } else {
     const long long rows = (long long)p.max_tree * p.grp;
     const int most = rows < tile ? (int)rows : tile;
