@@ -11,6 +11,11 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 
+// Fewest slots that sharing has to save, over all members, to be worth the rows' second part
+// (us shared, and not): one row each, 4 samples of 960 slots 16.7, 18.6; 2 of 2048 15.4, 15.6;
+// 32 of 512 23, 30; 32 of 256 23, 24; but 32 trees of 16 nodes over 64 slots 33, 22.
+constexpr int kWorthSlots = 2048;
+
 // A block per group.  The group shares the full pages, below the least length, in which no
 // member's row of the table differs from the first's.  Bound: latency, five dependent loads.
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(CacheView c, RowView rows, int n_group,
@@ -72,7 +77,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(CacheView c, 
     __syncthreads();
     pages = s_pages;
   }
-  const int shared = pages << c.ps_log2;
+  const int slots = pages << c.ps_log2, shared = (long long)slots * (members - 1) < kWorthSlots ? 0 : slots;
   for (int i = tid; i < members; i += kPlanThreads) plan[e0 + i] = shared;
   if (tid == 0) plan[n + g] = shared;
 }

@@ -311,7 +311,12 @@ __global__ void __launch_bounds__(kThreads, 2) attend_stream_kernel(const __grid
         for (int hf = 0; hf < 2; ++hf) {
           const int r = t * 16 + hf * 8 + gr;
           if (r >= rows) continue;
-          if (!E::kParts && whole) {
+          const bool last_word = whole && x.alone();
+          if (E::kParts && last_word && qd == 0) {
+            const int node = (g.row0 + r) / grp;
+            p.a.row_ml[part_row(p.a, x.pass(), x.lo + node, g.kvh * grp + g.row0 + r - node * grp)] = make_float2(0.f, kDone);
+          }
+          if (last_word) {
             const float inv = l[t][hf] > 0.f ? 1.f / l[t][hf] : 0.f;
             char* dst;
             float* lse;

@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kAll, kPerSm) attend_f32_kernel(const __grid_c
     // ---- the four warps' parts of the tile, added up in warp order
     l += __shfl_xor_sync(0xffffffffu, l, 16);
     if (sg == 0) s_ml[warp * TR + rs] = make_float2(m, l);
-    const bool whole = g.c0 == 0 && g.c1 == g.nch;
+    const bool whole = g.c0 == 0 && g.c1 == g.nch, last_word = whole && x.alone();
     sync_tile<kThreads>();   // (and every warp is done with Q)
     float wt[PR];      // this warp's weight in its lanes' rows
 #pragma unroll
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kAll, kPerSm) attend_f32_kernel(const __grid_c
         const float2 y = s_ml[k * TR + pr + r];
         sum += ex2(y.x - use) * y.y;
       }
-      wt[r] = ex2(s_ml[warp * TR + pr + r].x - use) * (E::kParts || !whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f);
+      wt[r] = ex2(s_ml[warp * TR + pr + r].x - use) * (!last_word ? 1.f : sum > 0.f ? 1.f / sum : 0.f);
     }
 #pragma unroll 1
     for (int k0 = 0; k0 < kConsumers; ++k0) {
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kAll, kPerSm) attend_f32_kernel(const __grid_c
       const float4 y = *reinterpret_cast<const float4*>(s_o + r * HD + pc * 4);
       const int node = (g.row0 + r) / grp, h = g.kvh * grp + (g.row0 + r) - node * grp;
       const size_t at = E::kParts && whole ? part_row(p.a, x.pass(), x.lo + node, h) : (size_t)slot * TR + r;
-      if (!E::kParts && whole)
+      if (last_word)
         *reinterpret_cast<float4*>(p.a.out + (size_t)(x.lo + node) * p.a.out_ld + (size_t)h * G::kRowB + pc * 16) = y;
       else
         *reinterpret_cast<float4*>((E::kParts && whole ? p.a.row_o : p.part_o) + at * HD + pc * 4) = y;
@@ -334,7 +334,8 @@ __global__ void __launch_bounds__(kAll, kPerSm) attend_f32_kernel(const __grid_c
       for (int k = 0; k < kConsumers; ++k) top = fmaxf(top, s_ml[k * TR + r].x);
       const float use = top == -CUDART_INF_F ? 0.f : top;
       for (int k = 0; k < kConsumers; ++k) sum += ex2(s_ml[k * TR + r].x - use) * s_ml[k * TR + r].y;
-      if (E::kParts || !whole)
+      if (E::kParts && last_word) p.a.row_ml[at] = make_float2(0.f, kDone);
+      if (!last_word)
         (E::kParts && whole ? p.a.row_ml : p.part_ml)[at] = make_float2(top, sum);
       else if (p.a.lse)
         p.a.lse[(size_t)(x.lo + node) * c.n_head + h] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -CUDART_INF_F;

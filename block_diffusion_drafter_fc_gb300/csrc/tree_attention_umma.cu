@@ -902,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
         wb = ex2(ml[128 + pos].x - use);
         sync_rows();   // the area is the accumulators' from here on
       }
-      const bool last_word = whole && !E::kParts;   // else fp32 sums, relative to the row's reference
+      const bool last_word = whole && d.x.alone();   // else fp32 sums, relative to the row's reference
       if (last_word) {
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         wa *= inv;
@@ -925,6 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_umma_kernel(const __grid_c
             sums_ml[part_of(row, whole)] = make_float2(top, sum);
           else if (lse)
             *lse = sum > 0.f ? (top + log2f(sum)) * kLn2 : -CUDART_INF_F;
+          if (E::kParts && last_word) p.a.row_ml[part_of(row, true)] = make_float2(0.f, kDone);
           if (E::kParts && !whole && d.c0 == 0)   // the cut tile's first block tells where its parts are
             p.a.row_ml[part_of(row, true)] = parts_at(b, d.last, slot, row);
         }

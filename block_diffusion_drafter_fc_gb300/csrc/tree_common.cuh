@@ -80,12 +80,14 @@ struct Entry {
   DF_DEVICE int base() const { return 0; }      // the first slot
   DF_DEVICE int nodes() const { return n; }     // slots behind the length: one per row node
   DF_DEVICE int pass() const { return 0; }
+  DF_DEVICE bool alone() const { return true; }   // no other part of its rows
   DF_DEVICE static int count(const AttendParams& p) { return p.rows.n_seq; }
 };
 
 // With shared prefixes a call has two kinds: groups (all rows of the group's entries over
 // the slots that they share: no nodes behind them, q the first entry's sequence), then
-// entries, over their slots from `base0` on.  Every tile leaves its rows' parts.
+// entries, over their slots from `base0` on.  A tile leaves its rows' parts, unless it is all
+// that they have (kDone in the place of a part's sum).
 struct PartEntry {
   static constexpr bool kParts = true;
   int lo, n, len, q;
@@ -93,9 +95,11 @@ struct PartEntry {
   DF_DEVICE int base() const { return base0; }
   DF_DEVICE int nodes() const { return nodes0; }
   DF_DEVICE int pass() const { return nodes0 > 0; }
+  DF_DEVICE bool alone() const { return nodes0 > 0 && base0 == 0; }
   DF_DEVICE static int count(const AttendParams& p) { return p.n_group + p.rows.n_seq; }
 };
 
+constexpr float kDone = -0.5f;
 // Where the parts of row r of a cut tile are, in the place of its reference and sum: the blocks
 // b0 .. last have one each, the first in its slot 0 or 1.
 DF_DEVICE float2 parts_at(int b0, int last, int slot, int r) {
@@ -473,11 +477,12 @@ __global__ void __launch_bounds__(128) attend_combine_kernel(AttendParams p, con
   const int rows = x.y * p.c.n_head;
   for (int i0 = (blockIdx.y * 4 + (threadIdx.x >> 5)) * R; i0 < rows; i0 += 4 * R * gridDim.y) {
     const int i = i0 + lane / LANES;
-    const bool real = i < rows;
+    bool real = i < rows;
     const int node = (real ? i : 0) / p.c.n_head, t = x.x + node, h = (real ? i : 0) - node * p.c.n_head;
     const size_t at0 = part_row(p, 0, t, h), at1 = part_row(p, 1, t, h);
     const float2 none = make_float2(-CUDART_INF_F, 0.f);
     const float2 ml0 = real && x.z ? p.row_ml[at0] : none, ml1 = real ? p.row_ml[at1] : none;
+    real = real && ml1.y != kDone;
     // a cut tile's: first and last block (what a group that was skipped left may be anything:
     // within the partial rows)
     auto first_of = [&](const float2& ml) { return ml.y < 0.f ? min((int)fminf(-ml.y, 2.f * kAttendSms) - 1, most - 1) : -1; };
@@ -574,7 +579,8 @@ cudaError_t launch_join(const AttendParams& p, const AttendWork& w, int tile, in
   const float2* part_ml = w.part_ml;
   if constexpr (E::kParts) {
     // a lane a piece while rows are few (their parts are many, and each round of loads counts);
-    // eight lanes a row, so that more rows are under way at once, beyond COMBINEFIG
+    // eight lanes a row, so that more rows are under way at once, beyond (128 f32 rows of 32 parts
+    // 9 us with a lane a piece, 30 four rows a warp; 21504 rows of 2 to 4 parts 21 and 13)
     const long long heads = (long long)p.max_tree * p.c.n_head;   // rows of an entry
     auto grid = [&](int lanes) {
       const int r = 4 * (32 / lanes);   // rows of a block

@@ -718,10 +718,12 @@ DFLASH_API int dflash_tree_attend(dflash_cache* c, int32_t layer, int32_t n_seq,
  * Slots that groups of entries share: group g is entries group_start[g] ..
  * group_start[g + 1] - 1 (device int32 [n_group + 1], ascending, within 0..n_seq), for
  * instance the forks of one prompt.  What a group shares is found in the page table: the
- * full pages below its members' least length that are the same for all of them (0 for a
- * group of one).
+ * full pages below its members' least length that are the same for all of them; 0 where
+ * sharing would save fewer than 2048 slots over all members, which takes longer than not
+ * sharing.
  *   plan: device int32 [n_seq + n_group], written: slots that entry s has in common with
- *   its group (0: in none), then the slots that group g has in common.
+ *   its group (0: in none), then the slots that group g has in common.  A caller may change
+ *   them, for a group and its entries alike, to any number of common slots.
  * Made once a turn, after dflash_cache_reserve and for the same entries; it is out of date
  * once a sequence is trimmed, forked or reserved for.  n_seq + n_group <=
  * DFLASH_MAX_CALL_SEQ; ranges that are none make a plan that shares nothing (BAD_ROWS).

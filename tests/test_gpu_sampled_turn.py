@@ -30,7 +30,7 @@ def test_sampled_turns_of_forks_equal_a_plain_model(dtype):
     bounds = ints([0, 3, 6])
     history = {q: [] for q in range(6)}
 
-    def forward(seqs, tokens, trees, groups):
+    def forward(seqs, tokens, trees, groups, turn=0):
         """The layers' outputs of a tree per sequence, groups: bounds of those that share a prompt (None: plain attention)."""
         counts = [len(t) for t in tokens]
         start, flat = starts(counts), torch.as_tensor(np.concatenate(tokens)).cuda()
@@ -42,7 +42,8 @@ def test_sampled_turns_of_forks_equal_a_plain_model(dtype):
         if groups is not None:
             plan = torch.zeros(len(seqs) + groups.shape[0] - 1, dtype=torch.int32, device="cuda")
             c.dflash_prefix_plan(groups, plan, seqs=ints(seqs))
-            assert int(plan.min()) > 0
+            if turn % 2:      # (these prompts are too short to be worth it: shared all the same in every other turn)
+                plan.copy_(ints([32] * 3 + [48] * 3 + [32, 48]))
             work = torch.empty(c.prefix_workspace(T), dtype=torch.uint8, device="cuda")
         outs = []
         for layer in range(L):
@@ -113,7 +114,7 @@ def test_sampled_turns_of_forks_equal_a_plain_model(dtype):
             drawn[r] = last[q]              # the anchor: the token behind the last path
             tokens.append(drawn[r:r + n].tolist())
             r += n
-        outs, start = forward(seqs, tokens, trees, bounds)
+        outs, start = forward(seqs, tokens, trees, bounds, turn)
         compare(outs, seqs, tokens, trees)
         # (the target's logits: any function of the tokens does for the acceptance)
         target = (draft + 0.7 * torch.randn(T, vocab, generator=g)).to(DT[dtype])
