@@ -16,15 +16,16 @@
 //
 // Precision.  Which token wins and whether a test passes is decided by comparing numbers, so
 // what is compared is exact to far below the gaps: sums are 64-bit whole numbers of fp32
-// weights (m being whole, moving it shifts them), a test's probabilities are 2^frac in fp32
-// times an exact power of two and the sum (2e-7); in a race the candidates that single fp32
-// operations cannot tell apart (within 2^-9) are compared again as 64-bit whole numbers of 2^-32.  All of it without fp64 units, of which an SM has two lanes here: with the
-// sums and the winners in fp64, 480 draws in blocks of two tiles took 69 us, without 45 (and in
-// one round of blocks 22).
+// weights (m being whole, moving it shifts them); a test's probabilities are 2^frac in fp32
+// times an exact power of two and the sum (3e-7); in a race the candidates that single fp32
+// operations cannot tell apart (within 2^-9) are compared again as 64-bit whole numbers of
+// 2^-32.  Whole numbers, because an SM has two lanes for fp64 here: 480 draws in blocks of two
+// tiles took 69 us with fp64 sums and winners, 45 without.
 //
-// Bound: the logits' bytes at the copy rate; a small call by latency.  480 draws over 32768
-// tokens: 22 us (0.83 of the copy rate); 32 chains of 16 rows, f32, drafts drawn: 37 us, 24
-// of them the sums (0.83), then the walk and draw, some fifteen dependent steps.
+// Bound: the logits' bytes at the copy rate.  480 draws over 32768 tokens: 20.3 us, 0.92 of it.
+// 32 chains of 16 rows, f32, drafts drawn: 34.5 us, 24 of them the sums (0.83 of it), then the
+// walk and the draw, some fifteen dependent steps.  A small call is latency: 16 bf16 rows of
+// 8192 8.4 us.
 #include "verify.h"
 
 #include "cache.cuh"
@@ -87,8 +88,8 @@ DF_DEVICE float lg2(float x) {
 // ------------------------------------------------------------------ rows
 
 // Element k of a thread's eight of the tile that begins at `tile0`.  VEC: eight neighbours
-// (vector loads: every row 16-byte aligned); else every NT-th (threads of the block), so that a warp's loads of any
-// alignment are whole lines.
+// (vector loads: every row 16-byte aligned); else every NT-th (threads of the block), so that a
+// warp's loads of any alignment are whole lines.
 template <bool VEC, int NT>
 DF_DEVICE int element(int tile0, int k) {
   return VEC ? tile0 + 8 * (int)threadIdx.x + k : tile0 + k * NT + (int)threadIdx.x;
@@ -151,12 +152,14 @@ DF_DEVICE float weight_of(float x, float s, int m) {
   return ldexpf(exp2f((a - k) + rest), (int)fminf(k, 200.f));
 }
 // Powers of two as whole numbers of 2^-32: x log2(e) / t, and log2 of a variate or a share
-// (to 4e-8).  Within 2^62 and 2^61, so that a difference fits.
+// (to 4e-8), within 2^62 and 2^61, so that their difference fits.
 DF_DEVICE long long score_of(float x, Slope s) {
   const float p = x * s.hi;
   if (!(fabsf(p) < kScoreMost)) return p > 0.f ? 1ll << 62 : -(1ll << 62);
   return __float2ll_rn(p * 0x1p32f) + __float2ll_rn((fmaf(x, s.hi, -p) + x * s.lo) * 0x1p32f);
 }
+// What wins over them all, equal to itself: a variate of 0.
+constexpr long long kWins = 0x7fffffffffffffffll;
 DF_DEVICE long long log2_of(float e) {
   if (!(e > 0.f)) return -(1ll << 61);
   if (e == CUDART_INF_F) return 1ll << 61;
@@ -247,7 +250,7 @@ DF_DEVICE long long cluster_total(long long v, Shared<NT>& s, int S) {
 
 // The cluster's winner among the threads' candidates (float key in powers of two, index; -1:
 // none).  Where others come within 2^-9 and a rounding of the largest, they are compared by
-// exact(), of the thread's own (a race in two hundred).  bad: any thread's flag.
+// exact(), of the thread's own (a race in some hundreds).  bad: any thread's flag.
 template <int NT, typename F>
 DF_DEVICE int cluster_winner(float key, int i, bool& bad, F exact, Shared<NT>& s, int S) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -496,7 +499,7 @@ DF_DEVICE int race(const char* row, const char* noise, int V, float temperature,
         }
       }
   }
-  return cluster_winner(top, at, bad, [&] { return score_of(at_x, slope) - log2_of(at_e); }, s, S);
+  return cluster_winner(top, at, bad, [&] { return at_e > 0.f ? score_of(at_x, slope) - log2_of(at_e) : kWins; }, s, S);
 }
 
 template <int EL, bool VEC>
@@ -884,7 +887,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
     token = cluster_winner(top, win, bad, [&] {
       float r = (written ? at_x : weight_of(at_x, st.s, st.m)) * inv;
       if (less) r = fmaf(-weight_of(at_y, sd.s, sd.m), inv_d, r);
-      return log2_of(r) - log2_of(at_e);
+      return at_e > 0.f ? log2_of(r) - log2_of(at_e) : kWins;
     }, s, S);
   }
   // the target's own row: the usual draw, or because rounding left nothing of the rest

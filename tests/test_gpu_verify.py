@@ -96,6 +96,10 @@ def test_sample_rows_that_are_no_distribution(dtype, vocab):
         i, margin = V.race(V.distribution(np64(y)[r], 1.0), np64(e)[r])
         assert int(tokens[r]) == i or margin < CLOSE
     assert int(tokens[2]) == 11 and c.dflash_cache_read_status() == 0
+    e[2, 7] = e[2, 40] = 0                     # of several variates of 0 the first one wins, whatever the logits
+    y[2, 7] = -40.0
+    c.dflash_sample(y.cuda(), e.cuda(), tokens[:3])
+    assert int(tokens[2]) == 7
     tokens.fill_(5)
     c.dflash_sample(y.cuda(), e.cuda(), tokens[:3], rows=ints([0, 3, -1]))
     assert tokens.tolist()[1:3] == [-1, -1] and c.dflash_cache_read_status() == 0x8
