@@ -308,3 +308,35 @@ def test_offsets_past_32_bits():
     y, tol = N.forward(np64(part), np64(w), *args)
     check(np64(x[rows]), y, tol, "rows")
     assert c.dflash_cache_read_status() == 0
+
+
+def test_calls_that_the_library_refuses():
+    """Bad epsilons, alignments, strides and parts that are not whole return before anything is launched."""
+    D = _D()
+    c = make(n_head=2, n_head_kv=2, head_dim=64)
+    L, h, p = D.LIB, c.h, torch.zeros(4096, device="cuda").data_ptr()
+
+    def rope(T=1, pos=p, eps=1e-6, q=(p, 128, p, p, 128), k=(p, 128, p, p, 128)):
+        return L.dflash_norm_rope(h, T, pos, eps, *q, *k, None)
+
+    none = (None, 0, None, None, 0)
+    assert rope(T=-1) == rope(pos=None) == rope(eps=0.0) == rope(eps=-1.0) == rope(eps=float("nan")) == rope(eps=float("inf")) == -1
+    assert rope(q=none, k=none) == rope(q=(p, 127, p, p, 128)) == rope(q=(p + 2, 128, p, p, 128)) == rope(q=(p, 132, p, p, 128)) == -1
+    assert rope(q=(p, 128, None, p, 128)) == rope(q=(p, 128, p + 2, p, 128)) == rope(k=(None, 128, p, p, 128)) == -1
+    assert rope(k=(p, 128, p, None, 128)) == rope(k=(p, 128, p, p, 120)) == -1
+    assert rope(T=0, q=none, k=none) == 0
+
+    def grad(q=(p, 128, p, p, 128, p, 128, p), k=(None, 0, None, None, 0, None, 0, None), eps=1e-6):
+        return L.dflash_norm_rope_grad(h, 1, p, eps, *q, *k, None)
+
+    assert grad(eps=0.0) == grad(q=(p, 128, p, None, 128, p, 128, p)) == grad(q=(p, 128, p, p, 64, p, 128, p)) == -1
+    assert grad(q=(p, 128, p, p, 128, p, 128, None)) == grad(q=(p, 128, p, p, 128, p, 128, p + 2)) == -1
+    assert grad(q=(None, 0, None, None, 0, None, 0, None)) == -1
+
+    def app(layer=0, eps=1e-6, q=(p, 128, p, p, 128), k=(p, 128, p), n=1):
+        return L.dflash_norm_append(h, layer, n, None, p, 1, None, eps, *q, *k, p, 128, None)
+
+    assert app(layer=1) == app(layer=-1) == app(eps=0.0) == app(k=(p, 128, None)) == app(k=(p, 128, p + 4)) == -1
+    assert app(q=(p, 128, None, p, 128)) == app(q=(None, 0, p, None, 0)) == app(q=(p, 128, p, None, 0)) == -1
+    assert app(n=1025) == -4 and app(n=0) == 0
+    assert c.dflash_cache_read_status() == 0

@@ -305,3 +305,59 @@ def test_offsets_past_32_bits():
         tol, _ = R.attend_bounds(o, size, big, 600, 128, "bf16")
         check(np64(out[s:s + 1]), o, tol + 2.02 * size * (2.0 ** -21 + big[..., None] * 2.0 ** -23), f"sequence {s}")
     assert c.dflash_cache_read_status() == 0
+
+
+def test_calls_that_the_library_refuses():
+    """Bad counts, null pointers and work areas return before anything is launched."""
+    D = _D()
+    c = make(n_head=2, n_head_kv=1, head_dim=64)
+    L, h, p = D.LIB, c.h, torch.zeros(4096, device="cuda").data_ptr()
+    assert p % 256 == 0
+
+    def plan(n=1, g=1, start=p, out=p):
+        return L.dflash_prefix_plan(h, n, None, g, start, out, None)
+
+    assert plan(g=0) == plan(g=-1) == plan(start=None) == plan(out=None) == -1
+    assert plan(n=-1) == plan(n=1024) == plan(n=1, g=1024) == -4
+
+    def attend(layer=0, n=1, T=1, most=1, mask=None, words=0, g=1, start=p, pl=p, work=p, q=p, out=p + 8192, rs=p):
+        return L.dflash_prefix_attend(h, layer, n, None, rs, T, most, mask, words, g, start, pl, work, q, 128, out, 128, None, None)
+
+    assert attend(layer=1) == attend(most=0) == attend(T=-1) == attend(g=0) == attend(start=None) == attend(pl=None) == -1
+    assert attend(work=None) == attend(work=p + 16) == attend(q=None) == attend(out=p + 4) == attend(rs=None) == -1
+    assert attend(mask=p, words=0) == attend(mask=p, words=33) == attend(mask=p, words=1, most=33) == -1
+    assert attend(n=1023, g=2) == -4 and attend(n=0, work=None) == attend(T=0, work=None) == 0
+    assert L.dflash_prefix_workspace_size(h, -1, None) == -1
+    assert c.dflash_cache_read_status() == 0
+
+
+def test_two_handles_on_two_streams():
+    """Plans and attention of two handles at the same time equal those of each alone, bit for bit."""
+    rng = np.random.default_rng(7)
+    g = torch.Generator().manual_seed(7)
+    sides = []
+    for _ in range(2):
+        c = make(n_head=8, n_head_kv=2, head_dim=128, page_size=64, n_pages=120, max_seq=6, max_pages=64)
+        seqs, *_ = lay_out(c, rng, g, [(2000, [(int(t), 3) for t in rng.integers(0, 300, 6)])])
+        q = normal(g, (18, 8, 128), "bf16").cuda()
+        sides.append(dict(c=c, q=q, seqs=ints(seqs), s=torch.cuda.Stream(), plan=torch.zeros(7, dtype=torch.int32, device="cuda"),
+                          work=torch.zeros(c.prefix_workspace(18), dtype=torch.uint8, device="cuda")))
+    start, bounds = starts([3] * 6), ints([0, 6])
+
+    def turn(k, out, stream=None):
+        k["c"].dflash_prefix_plan(bounds, k["plan"], seqs=k["seqs"], stream=stream)
+        k["c"].dflash_prefix_attend(0, start, 3, k["q"], out, bounds, k["plan"], k["work"], seqs=k["seqs"], stream=stream)
+
+    alone = [torch.zeros_like(k["q"]) for k in sides]
+    for k, o in zip(sides, alone):
+        turn(k, o)
+    assert int(sides[0]["plan"].min()) > 0
+    outs = [[torch.zeros_like(k["q"]) for k in sides] for _ in range(10)]
+    torch.cuda.synchronize()
+    for pair in outs:
+        for k, o in zip(sides, pair):
+            turn(k, o, stream=k["s"])
+    torch.cuda.synchronize()
+    for pair in outs:
+        for o, want in zip(pair, alone):
+            assert torch.equal(o, want)

@@ -393,3 +393,72 @@ def test_offsets_past_32_bits():
     c.dflash_sample(x, noise, tokens, rows=ints([rows - 1, rows - 2, 5]))
     assert tokens.tolist() == [39999, 7, 123]
     assert c.dflash_cache_read_status() == 0
+
+
+def test_calls_that_the_library_refuses():
+    """Bad sizes, types, strides and null pointers return before anything is launched."""
+    D = _D()
+    c = make()
+    L, h, p = D.LIB, c.h, torch.zeros(64, device="cuda").data_ptr()
+
+    def sample(T=2, V=8, x=p, ld=8, dt=0, n=2, rows=None, t=None, e=p, els=8, out=p):
+        return L.dflash_sample(h, T, V, x, ld, dt, n, rows, t, e, els, out, None)
+
+    assert sample(T=-1) == sample(V=0) == sample(ld=7) == sample(dt=2) == sample(dt=-1) == sample(n=1) == sample(n=-1) == -1
+    assert sample(x=None) == sample(x=p + 2) == sample(x=p + 1, dt=1) == sample(e=None) == sample(els=7) == sample(out=None) == -1
+    assert sample(V=327681, ld=327681, els=327681) == -2 and sample(T=(1 << 24) + 1, n=1 << 25) == -3
+    assert sample(T=0, e=None, out=None) == 0
+
+    def verify(n=1, start=p, T=2, par=p, tok=p, V=8, x=p, ld=8, dt=0, t=None, d=None, dld=8, ddt=0, nd=0, dr=None, td=None, u=p, e=p,
+               els=8, path=p, mp=2, npth=p, last=p):
+        return L.dflash_tree_verify(h, n, start, T, par, tok, V, x, ld, dt, t, d, dld, ddt, nd, dr, td, u, e, els, path, mp, npth,
+                                    last, None)
+
+    assert verify(T=-1) == verify(V=0) == verify(mp=0) == verify(start=None) == verify(par=None) == verify(tok=None) == -1
+    assert verify(x=None) == verify(ld=7) == verify(dt=3) == verify(u=None) == verify(e=None) == verify(path=None) == -1
+    assert verify(npth=None) == verify(last=None) == verify(n=2, els=7) == -1
+    assert verify(nd=1) == verify(dr=p) == verify(td=p) == verify(d=p) == verify(d=p, nd=-1) == -1      # what goes with draft
+    assert verify(d=p, nd=2, dld=7) == verify(d=p, nd=2, ddt=2) == -1
+    assert verify(V=327681, ld=327681) == -2 and verify(n=1025) == verify(n=-1) == -4
+    assert verify(T=65536, d=p, nd=1) == -3
+    assert verify(n=0) == 0
+    assert c.dflash_cache_read_status() == 0
+
+
+def test_two_handles_on_two_streams():
+    """Draws and verifications of two handles at the same time equal those of each alone."""
+    g = torch.Generator().manual_seed(2)
+    rng = np.random.default_rng(2)
+    n, B, vocab = 7, 12, 5000
+    T = n * B
+    sides = []
+    for _ in range(2):
+        target = logits(g, T, vocab, "bf16")
+        draft = target.float() + 0.5 * torch.randn(T, vocab, generator=g)
+        sides.append(dict(c=make(), s=torch.cuda.Stream(), parents=ints(np.concatenate([random_parents(rng, B, "random") for _ in range(n)])),
+                          target=target.cuda(), draft=draft.cuda(), e=exponential(g, T, vocab).cuda(), e2=exponential(g, n, vocab).cuda(),
+                          u=torch.rand(T, generator=g).cuda()))
+    start = starts([B] * n)
+
+    def turn(k, stream=None):
+        o = [torch.zeros(T, dtype=torch.int32, device="cuda"), torch.zeros(n, B, dtype=torch.int32, device="cuda"),
+             torch.zeros(n, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")]
+        torch.cuda.synchronize()
+        return o, lambda: (k["c"].dflash_sample(k["draft"], k["e"], o[0], stream=stream),
+                           k["c"].dflash_tree_verify(start, k["parents"], o[0], k["target"], k["u"], k["e2"], *o[1:], draft=k["draft"],
+                                                     stream=stream))
+
+    alone = []
+    for k in sides:
+        o, call = turn(k)
+        call()
+        alone.append(o)
+    torch.cuda.synchronize()
+    both = [[turn(k, k["s"]) for k in sides] for _ in range(10)]
+    for pair in both:
+        for _, call in pair:
+            call()
+    torch.cuda.synchronize()
+    for pair in both:
+        for (o, _), want in zip(pair, alone):
+            assert all(torch.equal(a, b) for a, b in zip(o, want))
