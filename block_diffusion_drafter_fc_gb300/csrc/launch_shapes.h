@@ -109,7 +109,8 @@ constexpr int kThreads = 256;   // most threads of a block
 constexpr int kMaxRows = 32;    // rows whose angles a block holds at once
 
 // A block's threads own items of a row (its columns), `side` rows side by side where rows are
-// short, and walk down rows: gx blocks of `rows` rows, gy of columns.
+// short, and walk down rows: gx blocks of `rows` rows, gy of columns.  A head has two items or
+// more, so a block has 64 threads or more: one for each row whose angles it holds.
 struct Shape {
   int cols, side, threads, rows, gx, gy;
 };

@@ -7,7 +7,6 @@
 namespace dflash {
 namespace rope {
 
-
 template <int VB>
 struct Vec;
 template <>

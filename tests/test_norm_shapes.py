@@ -12,7 +12,7 @@ using namespace dflash;
 
 // 0: the blocks cover every item of every row once, within their limits; else what does not hold
 static int cover(const norm::Shape& s, int T, int items, int ipr, long long limit) {
-  if (s.threads < 32 || s.threads > norm::kThreads || s.threads % 32 || s.cols % ipr) return 1;
+  if (s.threads < 2 * norm::kMaxRows || s.threads > norm::kThreads || s.threads % 32 || s.cols % ipr) return 1;
   if (s.cols * s.side > s.threads || s.side < 1 || s.side > norm::kMaxRows) return 2;
   if (s.rows < 1 || s.rows % s.side || s.gx < 1 || s.gy < 1 || s.gy > 65535) return 3;
   if ((long long)s.cols * s.gy < items || (long long)s.cols * (s.gy - 1) >= items) return 4;
