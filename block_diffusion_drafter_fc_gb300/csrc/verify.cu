@@ -17,12 +17,12 @@
 // Precision.  Which token wins and whether a test passes is decided by comparing numbers, so
 // what is compared is exact to far below the gaps: sums are 64-bit whole numbers of fp32
 // weights (m being whole, moving it shifts them); a test's probabilities are 2^frac in fp32
-// times an exact power of two and the sum (3e-7); in a race the candidates that single fp32
-// operations cannot tell apart (within 2^-9) are compared again as 64-bit whole numbers of
-// 2^-32.  Whole numbers, because an SM has two lanes for fp64 here: 480 draws in blocks of two
+// times an exact power of two and the sum (3e-7); in a race a thread counts its keys from its
+// winner's, and of the threads' candidates those that single fp32 operations cannot tell apart
+// (within 2^-9) are compared again as 64-bit whole numbers of 2^-32.  Whole numbers, because an SM has two lanes for fp64 here: 480 draws in blocks of two
 // tiles took 69 us with fp64 sums and winners, 45 without.
 //
-// Bound: the logits' bytes at the copy rate.  480 draws over 32768 tokens: 20.3 us, 0.92 of it.
+// Bound: the logits' bytes at the copy rate.  480 draws over 32768 tokens: 20.5 us, 0.91 of it.
 // 32 chains of 16 rows, f32, drafts drawn: 34.5 us, 24 of them the sums (0.83 of it), then the
 // walk and the draw, some fifteen dependent steps.  A small call is latency: 16 bf16 rows of
 // 8192 8.4 us.
@@ -43,6 +43,7 @@ constexpr int kWalkThreads = 512;          // of verify: few entries, whole rows
 constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596303e-8f;   // log2(e) in two parts
 constexpr float kUnit = 0x1p40f;           // of sums: a row's is below 2^21 (a batch of 16 is at most 64)
 constexpr float kCold = 0x1p-20f;          // temperatures below it (and not below 0) count as 0
+constexpr float kLeastVariate = 0x1p-126f; // variates below it count as 0 (lg2 takes them so)
 constexpr float kScoreMost = 0x1p30f;      // scores x log2(e) / T of this magnitude count as infinite
 
 // ------------------------------------------------------------------ clusters
@@ -476,7 +477,9 @@ DF_DEVICE int race(const char* row, const char* noise, int V, float temperature,
   constexpr int kTiles = 2, kTile = 8 * NT;
   const Slope slope = slope_of(temperature);
   const float sc = slope.hi, most = kScoreMost / sc;
-  float top = -kScoreMost, at_x = 0.f, at_e = 1.f;
+  // keys are counted from the winner's: close ones are small then, whatever the scores (with a
+  // variate of 0 it is infinite, and no key comes after it)
+  float top = -kScoreMost, from = 0.f;
   int at = -1;
   for (int t0 = cluster_rank() * kTile; t0 < V; t0 += kTiles * S * kTile) {
     float x[kTiles][8], e[kTiles][8];
@@ -490,16 +493,18 @@ DF_DEVICE int race(const char* row, const char* noise, int V, float temperature,
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         bad |= !(x[j][k] < most);
-        const float key = fmaf(x[j][k], sc, -lg2(e[j][k]));
-        if (key > top && !barred(element<VEC, NT>(t0 + j * S * kTile, k))) {
-          top = key;
+        const float l = lg2(e[j][k]);
+        if (fmaf(x[j][k], sc, -from) - l > top && !barred(element<VEC, NT>(t0 + j * S * kTile, k))) {
+          from = fmaf(x[j][k], sc, -l);
+          top = fmaf(x[j][k], sc, -from) - l;
           at = element<VEC, NT>(t0 + j * S * kTile, k);
-          at_x = x[j][k];
-          at_e = e[j][k];
         }
       }
   }
-  return cluster_winner(top, at, bad, [&] { return at_e > 0.f ? score_of(at_x, slope) - log2_of(at_e) : kWins; }, s, S);
+  return cluster_winner(from == CUDART_INF_F ? from : top + from, at, bad, [&] {
+    const float e = reinterpret_cast<const float*>(noise)[at];
+    return e >= kLeastVariate ? score_of(logit(row, EL, at), slope) - log2_of(e) : kWins;
+  }, s, S);
 }
 
 template <int EL, bool VEC>
@@ -887,7 +892,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
     token = cluster_winner(top, win, bad, [&] {
       float r = (written ? at_x : weight_of(at_x, st.s, st.m)) * inv;
       if (less) r = fmaf(-weight_of(at_y, sd.s, sd.m), inv_d, r);
-      return at_e > 0.f ? log2_of(r) - log2_of(at_e) : kWins;
+      return at_e >= kLeastVariate ? log2_of(r) - log2_of(at_e) : kWins;
     }, s, S);
   }
   // the target's own row: the usual draw, or because rounding left nothing of the rest

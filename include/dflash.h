@@ -786,9 +786,10 @@ DFLASH_API int dflash_tree_accept(dflash_cache* c, int32_t n_seq, const int32_t*
  *   temperature: device f32, one per row, or NULL: 1;
  *   noise: device f32 [..][n_vocab] (stride as for logits): exponential variates e, for
  *   instance -ln(u); the token of the largest p_i / e_i is drawn, the lowest index of equal
- *   ones, which is token i with probability p_i.  A NaN excludes its token.
- * Results are those of the formulas up to comparisons that are closer than about 1e-6, and do
- * not depend on the order of anything.
+ *   ones, which is token i with probability p_i.  A NaN excludes its token, a variate below
+ *   2^-126 counts as 0.
+ * Results are those of the formulas up to comparisons that are closer than some 1e-6, whatever
+ * the scores, and do not depend on the order of anything.
  */
 
 /*

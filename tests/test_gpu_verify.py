@@ -8,8 +8,8 @@ from test_gpu_cache import DT, ints, make, np64, random_parents, starts, _D
 
 pytestmark = pytest.mark.gpu
 
-# Comparisons are made in fp64 from sums that fp32 weights put within 1e-7 of the formula's: a decision
-# closer than this may fall either way (and a winner is settled in fp64 among those within 2^-9)
+# Tests compare numbers that fp32 weights put within 3e-7 of the formula's; a race's keys are within 4e-6
+# (log2 of a variate of 2^-24 to 2^-22 of it): a decision closer than this may fall either way
 CLOSE = 1e-5
 
 
@@ -100,9 +100,49 @@ def test_sample_rows_that_are_no_distribution(dtype, vocab):
     y[2, 7] = -40.0
     c.dflash_sample(y.cuda(), e.cuda(), tokens[:3])
     assert int(tokens[2]) == 7
+    e[2, 7], e[2, 40] = 1e-40, 1.0             # one below the least normal number counts as 0
+    e[2, 11], y[2, 7] = 1.0, -400.0
+    c.dflash_sample(y.cuda(), e.cuda(), tokens[:3])
+    assert int(tokens[2]) == 7
     tokens.fill_(5)
     c.dflash_sample(y.cuda(), e.cuda(), tokens[:3], rows=ints([0, 3, -1]))
     assert tokens.tolist()[1:3] == [-1, -1] and c.dflash_cache_read_status() == 0x8
+
+
+@pytest.mark.parametrize("pad", [0, 1])
+def test_close_races_of_large_scores(pad):
+    """Two tokens whose p / e differ by 1e-4 or by 3e-5, wherever they lie, whatever the scores are.
+
+    A score's own ulp is up to 4 here; p / e is still decided by what tells the tokens apart."""
+    g = torch.Generator().manual_seed(1)
+    c = make()
+    heats = [(1000.0, 0.1), (-30000.0, 0.5), (5e7, 1.0), (60.0, 0.6), (0.0, 1.0), (-2000.0, 0.05), (0.001, 0.001)]
+    vocab, per = 40, 24
+    x, e, temp = [], [], []
+    for centre, t in heats:
+        for k in range(per):
+            row = centre + t * 4 * torch.rand(vocab, generator=g, dtype=torch.float64)
+            row = row.float()
+            t32 = torch.tensor(t)
+            far = 1 + 3 * torch.rand(vocab, generator=g, dtype=torch.float64)
+            a, b = torch.randperm(vocab if k % 2 else 8, generator=g)[:2].tolist()
+            far[a], far[b] = 1, 1 + (1e-4 if k % 4 < 2 else 3e-5)
+            x.append(row)
+            e.append((far * torch.exp((row.double() - row.double().max()) / t32.double())).float())
+            temp.append(t32)
+    x, e, temp = torch.stack(x), torch.stack(e), torch.stack(temp)
+    tokens = torch.zeros(len(x), dtype=torch.int32, device="cuda")
+    c.dflash_sample(padded(x, pad), padded(e, pad), tokens, temperature=temp.cuda())
+    want = [V.race(V.distribution(np64(x)[r], float(temp[r])), np64(e)[r]) for r in range(len(x))]
+    assert min(m for _, m in want) > CLOSE
+    assert tokens.tolist() == [i for i, _ in want]
+    # as the draw of a verification: single nodes
+    n = len(x)
+    path, n_path, last = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((n, 1), n, n))
+    c.dflash_tree_verify(starts([1] * n), ints([-1] * n), ints([0] * n), padded(x, pad), torch.zeros(n, device="cuda"),
+                         padded(e, pad), path, n_path, last, temperature=temp.cuda())
+    assert last.tolist() == [i for i, _ in want]
+    assert c.dflash_cache_read_status() == 0
 
 
 def test_samples_follow_the_probabilities():
