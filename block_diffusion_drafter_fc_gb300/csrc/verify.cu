@@ -8,7 +8,7 @@
 //
 // Three kernels, all over rows of n_vocab logits in tiles of 8 elements a thread:
 //   row_stats   one pass over every row, cut into pieces: sums of 2^(x s - m), s = log2(e) / T,
-//               m a whole number;
+//               m a whole number: the largest score's, of the unrounded product;
 //   verify      a cluster walks an entry's tree: the tests need single logits and the sums,
 //               so only a draw, and a rejection with more children to come, read a row; its
 //               tiles go round the cluster's blocks;
@@ -45,6 +45,7 @@ constexpr float kUnit = 0x1p40f;           // of sums: a row's is below 2^21 (a 
 constexpr float kCold = 0x1p-20f;          // temperatures below it (and not below 0) count as 0
 constexpr float kLeastVariate = 0x1p-126f; // variates below it count as 0 (lg2 takes them so)
 constexpr float kScoreMost = 0x1p30f;      // scores x log2(e) / T of this magnitude count as infinite
+constexpr int kLeast = -(1 << 30);         // the reference of a sum of nothing
 
 // ------------------------------------------------------------------ clusters
 
@@ -145,11 +146,21 @@ DF_DEVICE Slope slope_of(float t) {
   s.lo = __fdividef(fmaf(-s.hi, t, kLog2e) + kLog2eRest, t);
   return s;
 }
+// 2^(y - m) = 2^(y + at) by for the whole number m of a sum: fp32 does not hold all of them
+// beyond 2^24, and what it leaves (up to 64) is a power of two of its own.
+struct Reference {
+  float at, by;
+};
+DF_DEVICE Reference reference_of(int m) {
+  const float at = (float)-m;
+  return {at, __int_as_float((127 - m - (int)at) << 23)};
+}
 // 2^(x s - m) to 2e-7: the exponent with its rounding errors kept.
 DF_DEVICE float weight_of(float x, float s, int m) {
-  const float p = x * s, mf = (float)-m, a = p + mf, bb = a - p;
+  // (beyond 2^24 all of this is whole: `left` adds up exactly)
+  const float p = x * s, mf = (float)-m, left = (float)(-m - (int)mf), y = p + mf, bb = y - p, a = y + left;
   if (!(a > -200.f)) return a != a ? a : 0.f;
-  const float rest = fmaf(x, s, -p) + ((p - (a - bb)) + (mf - bb)), k = rintf(a);
+  const float rest = fmaf(x, s, -p) + ((p - (y - bb)) + (mf - bb)), k = rintf(a);
   return ldexpf(exp2f((a - k) + rest), (int)fminf(k, 200.f));
 }
 // Powers of two as whole numbers of 2^-32: x log2(e) / t, and log2 of a variate or a share
@@ -315,7 +326,12 @@ DF_DEVICE int cluster_winner(float key, int i, bool& bad, F exact, Shared<NT>& s
   return i;
 }
 
+DF_DEVICE int largest(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
 // ------------------------------------------------------------------ sums of rows
+
+// A sum whose reference moves up from m to `to`.
+DF_DEVICE long long shifted(long long z, int m, int to) { return z >> min((unsigned)to - (unsigned)m, 63u); }
 
 // Piece `g` of P of a row: the tiles g, g + P, ..  A thread adds up 2^(x s - m), m its first
 // batch's largest score, rounded up; a later batch of more than 64 makes it move m and shift
@@ -325,12 +341,11 @@ DF_DEVICE void row_piece(const char* row, int V, float temperature, bool draft, 
   constexpr int kTile = 8 * kThreads;
   constexpr int kTiles = EL == 2 ? 4 : 2;    // tiles of a batch: 64 bytes of a thread in flight
   __shared__ long long w_v[kThreads / 32];
-  __shared__ float w_f[kThreads / 32];
-  __shared__ int w_i[kThreads / 32];
+  __shared__ int w_m[kThreads / 32], w_i[kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Heat heat = heat_of(temperature);
   if (heat == kBadHeat || (draft && heat == kGreedy)) {   // (a greedy drafter's row is not needed)
-    if (threadIdx.x == 0) *out = {heat == kBadHeat ? kNoPiece : kGreedyPiece, 0.f, -1};
+    if (threadIdx.x == 0) *out = {heat == kBadHeat ? kNoPiece : kGreedyPiece, 0, -1};
     return;
   }
   if (heat == kGreedy) {
@@ -360,14 +375,15 @@ DF_DEVICE void row_piece(const char* row, int V, float temperature, bool draft, 
       v = lane < kThreads / 32 ? w_v[lane] : 0;
       at = lane < kThreads / 32 ? w_i[lane] : -1;
       warp_best(v, at);
-      if (lane == 0) *out = {any ? kNoPiece : kGreedyPiece, at >= 0 ? logit(row, EL, at) : 0.f, at};
+      if (lane == 0) *out = {any ? kNoPiece : kGreedyPiece, (int)v, at};
     }
     return;
   }
   const float sc = slope_of(temperature).hi;
   long long sum = 0;
   bool bad = false;
-  float m = -kScoreMost;                     // nothing seen
+  int m = kLeast;                            // nothing seen
+  Reference ref = reference_of(m);
   for (int t0 = g * kTile; t0 < V; t0 += kTiles * P * kTile) {
     float x[kTiles][8];
 #pragma unroll
@@ -377,31 +393,40 @@ DF_DEVICE void row_piece(const char* row, int V, float temperature, bool draft, 
 #pragma unroll
       for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) part[k & 3] += ex2(fmaf(x[j][k], sc, -m));
-      const float b = (part[0] + part[1]) + (part[2] + part[3]);
+        for (int k = 0; k < 8; ++k) part[k & 3] += ex2(fmaf(x[j][k], sc, ref.at));
+      const float b = ((part[0] + part[1]) + (part[2] + part[3])) * ref.by;
       if (b <= 64.f || again) {
         bad |= !(b <= 64.f);                 // NaN or infinite
         sum += __float2ll_rn(b * kUnit);
         break;
       }
-      float top = -CUDART_INF_F;
+      // the largest score, rounded (its own step is up to 64), and what the rounding left of it
+      float top = -CUDART_INF_F, left = -CUDART_INF_F;
 #pragma unroll
       for (int j = 0; j < kTiles; ++j)
 #pragma unroll
         for (int k = 0; k < 8; ++k) top = fmaxf(top, x[j][k] * sc);
-      const float to = top < kScoreMost ? ceilf(top) : m;
+      if (b == b && top <= -kScoreMost) break;   // (counts as -inf: nothing to add)
+      if (!(top > -kScoreMost && top < kScoreMost)) continue;
+      top = ceilf(top);
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) left = fmaxf(left, fmaf(x[j][k], sc, -top));
+      const int to = (int)top + (int)ceilf(left);
       if (to > m) {
-        sum >>= (int)fminf(to - m, 63.f);
+        sum = m > kLeast ? shifted(sum, m, to) : 0;
         m = to;
+        ref = reference_of(m);
       }
     }
   }
   // one reference for all: the largest
-  const float w = largest(m);
-  if (lane == 0) w_f[warp] = w;
+  const int w = largest(m);
+  if (lane == 0) w_m[warp] = w;
   __syncthreads();
-  const float top = largest(lane < kThreads / 32 ? w_f[lane] : -kScoreMost);
-  sum = lane_sum<32>(sum >> (int)fminf(top - m, 63.f));
+  const int top = largest(lane < kThreads / 32 ? w_m[lane] : kLeast);
+  sum = lane_sum<32>(m > kLeast ? shifted(sum, m, top) : 0ll);
   if (lane == 0) w_v[warp] = sum;
   const int any = __syncthreads_or(bad);
   if (threadIdx.x == 0) {
@@ -438,23 +463,22 @@ struct RowStats {
 DF_DEVICE RowStats row_of(const Piece* pieces, int P, int r, float s, int G) {
   const int lane = threadIdx.x & (G - 1);
   long long z = 0, v = 0;
-  float top = -kScoreMost;
-  int arg = -1, greedy = 0, bad = 0;
+  int top = kLeast, arg = -1, greedy = 0, bad = 0;
   for (int g0 = 0; g0 < P; g0 += G) {
-    const Piece x = g0 + lane < P ? pieces[(size_t)r * P + g0 + lane] : Piece{0, -kScoreMost, -1};
+    const Piece x = g0 + lane < P ? pieces[(size_t)r * P + g0 + lane] : Piece{0, kLeast, -1};
     bad |= x.z == kNoPiece;
     if (x.z == kGreedyPiece) {
       greedy = 1;
-      best_of(v, arg, (long long)order_of(x.m), x.arg);
+      best_of(v, arg, (long long)x.m, x.arg);
     } else if (x.z >= 0) {
-      const float to = fmaxf(top, x.m);
-      z = (z >> (int)fminf(to - top, 63.f)) + (x.z >> (int)fminf(to - x.m, 63.f));
+      const int to = max(top, x.m);
+      z = shifted(z, top, to) + shifted(x.z, x.m, to);
       top = to;
     }
   }
   for (int o = G >> 1; o > 0; o >>= 1) {
-    const float to = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    z >>= (int)fminf(to - top, 63.f);
+    const int to = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    z = shifted(z, top, to);
     z += __shfl_xor_sync(0xffffffffu, z, o);
     top = to;
     const long long v2 = __shfl_xor_sync(0xffffffffu, v, o);
@@ -464,7 +488,7 @@ DF_DEVICE RowStats row_of(const Piece* pieces, int P, int r, float s, int G) {
   }
   if (bad || (!greedy && z <= 0)) return {CUDART_NAN_F, s, 0};
   if (greedy) return {-1.f, s, arg};
-  return {__fdiv_rn(kUnit, __ll2float_rn(z)), s, (int)top};
+  return {__fdiv_rn(kUnit, __ll2float_rn(z)), s, top};
 }
 
 // ------------------------------------------------------------------ draws
@@ -787,7 +811,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
       if (S > 1 && s_seen) cluster_sync();   // no block changes s_r while the walk of another looks into it
       const int cur = s_cur, barred = s_n_barred, written = s_written;
       const RowStats st = s_node[cur].own, sd = s_node[s_child].from;
-      const float inv = (written ? 1.f : st.inv) / (float)s_total, inv_d = sd.inv, m = (float)-st.m, md = (float)-sd.m;
+      const Reference ref = reference_of(st.m), ref_d = reference_of(sd.m);
+      const float inv = (written ? 1.f : st.inv * ref.by) / (float)s_total, inv_d = sd.inv * ref_d.by;
       const char *row = target_row(cur), *row_d = draft_row(s_node[s_child].row);
       long long units = 0;   // of 2^-50 (r adds up to at most 1)
       float x[2][8], y[2][8];
@@ -800,10 +825,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int i = element<VEC, NT>(t0, k);
-          float r = written ? s_r[at + i - t0] : ex2(fmaf(x[k], st.s, m));
+          float r = written ? s_r[at + i - t0] : ex2(fmaf(x[k], st.s, ref.at));
           for (int j = 0; j < barred; ++j)
             if (s_barred[j] == i) r = 0.f;
-          r = fmaxf(fmaf(r, inv, -ex2(fmaf(y[k], sd.s, md)) * inv_d), 0.f);
+          r = fmaxf(fmaf(r, inv, -ex2(fmaf(y[k], sd.s, ref_d.at)) * inv_d), 0.f);
           s_r[at + i - t0] = r;
           part += r;
         }
@@ -849,7 +874,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
       sd = s_node[s_child].from;
       row_d = draft_row(s_node[s_child].row);
     }
-    const float inv = (written ? 1.f : st.inv) / (float)s_total, inv_d = sd.inv, m = (float)-st.m, md = (float)-sd.m;
+    const Reference ref = reference_of(st.m), ref_d = reference_of(sd.m);
+    const float inv0 = (written ? 1.f : st.inv) / (float)s_total, inv = written ? inv0 : inv0 * ref.by, inv_d = sd.inv * ref_d.by;
     const char* row = target_row(cur);
     float best = 0.f, at_x = 0.f, at_y = 0.f, at_e = 1.f;   // best / at_e is the largest so far
     int win = -1;
@@ -866,8 +892,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
       for (int k = 0; k < 8; ++k) {
         const int i = element<VEC, NT>(t0, k);
         if (written) x[k] = s_r[at + i - t0];
-        float r = (written ? x[k] : ex2(fmaf(x[k], st.s, m))) * inv;
-        if (less) r = r - ex2(fmaf(y[k], sd.s, md)) * inv_d;
+        float r = (written ? x[k] : ex2(fmaf(x[k], st.s, ref.at))) * inv;
+        if (less) r = r - ex2(fmaf(y[k], sd.s, ref_d.at)) * inv_d;
         // (r / z above the best, without a quotient)
         if (r > 0.f && z[k] >= 0.f && r * at_e > best * z[k] && !is_barred(i)) {
           best = r;
@@ -890,8 +916,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
     }
     const float top = lg2(best) - lg2(at_e);
     token = cluster_winner(top, win, bad, [&] {
-      float r = (written ? at_x : weight_of(at_x, st.s, st.m)) * inv;
-      if (less) r = fmaf(-weight_of(at_y, sd.s, sd.m), inv_d, r);
+      float r = (written ? at_x : weight_of(at_x, st.s, st.m)) * inv0;
+      if (less) r = fmaf(-weight_of(at_y, sd.s, sd.m), sd.inv, r);
       return at_e >= kLeastVariate ? log2_of(r) - log2_of(at_e) : kWins;
     }, s, S);
   }

@@ -16,13 +16,13 @@ struct Logits {
   const float* temperature;    // [rows], null: 1
 };
 
-// A piece of a row: z 2^-40 is the sum of 2^(x s - m).  kGreedyPiece: its largest logit m, at
-// `arg` (a target of temperature 0), or not needed (a drafter's); kNoPiece: no distribution.
+// A piece of a row: z 2^-40 is the sum of 2^(x s - m).  kGreedyPiece: its largest logit is at
+// `arg`, m its bits in their order (a target of temperature 0), or not needed (a drafter's);
+// kNoPiece: no distribution.
 constexpr long long kGreedyPiece = -1, kNoPiece = -2;
 struct Piece {
   long long z;
-  float m;
-  int arg;
+  int m, arg;
 };
 
 struct VerifyParams {
