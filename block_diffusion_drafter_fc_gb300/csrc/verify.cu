@@ -19,8 +19,10 @@
 // weights (m being whole, moving it shifts them); a test's probabilities are 2^frac in fp32
 // times an exact power of two and the sum (3e-7); in a race a thread counts its keys from its
 // winner's, and of the threads' candidates those that single fp32 operations cannot tell apart
-// (within 2^-9) are compared again as 64-bit whole numbers of 2^-32.  Whole numbers, because an SM has two lanes for fp64 here: 480 draws in blocks of two
-// tiles took 69 us with fp64 sums and winners, 45 without.
+// (within 2^-9) are compared again as 64-bit whole numbers of 2^-32.  Whole numbers, because an SM
+// has two lanes for fp64 here: 480 draws in blocks of two tiles took 69 us with fp64 sums and
+// winners, 45 without.  What rejections leave is a difference of probabilities and keeps their
+// absolute error; where it is small the entry is walked again with two floats a weight (kLittle).
 //
 // Bound: the logits' bytes at the copy rate.  480 draws over 32768 tokens: 20.5 us, 0.91 of it.
 // 32 chains of 16 rows, f32, drafts drawn: 34.5 us, 24 of them the sums (0.83 of it), then the
@@ -218,11 +220,14 @@ DF_DEVICE float largest(float x) {   // of the warp
   return __int_as_float(b < 0 ? b ^ 0x7fffffff : b);
 }
 
+DF_DEVICE int largest(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
 // What a block tells its cluster, twice: a block may write one while others read the other.
 struct Told {
   long long v[2];
   float key[2];
   int i[2], n[2];   // n: candidates; -1: something is bad
+  unsigned part[2];
 };
 template <int NT>
 struct Shared {
@@ -230,6 +235,7 @@ struct Shared {
   long long w_v[NT / 32];
   int w_i[NT / 32];
   float w_f[NT / 32];
+  unsigned w_part[NT / 32];
   int turn;      // which of the two is next (the same in all blocks)
 };
 
@@ -260,22 +266,51 @@ DF_DEVICE long long cluster_total(long long v, Shared<NT>& s, int S) {
   return lane_sum<8>(lane < S ? peer(&s.told.v[k], lane) : 0ll);
 }
 
+// The largest of the cluster.
+template <int NT>
+DF_DEVICE int cluster_largest(int v, Shared<NT>& s, int S) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = s.turn;
+  v = largest(v);
+  if (lane == 0) s.w_i[warp] = v;
+  __syncthreads();
+  v = largest(lane < NT / 32 ? s.w_i[lane] : v);
+  if (threadIdx.x == 0) {
+    s.told.i[k] = v;
+    s.turn = k ^ 1;
+  }
+  if (S == 1) {
+    __syncthreads();
+    return v;
+  }
+  cluster_sync();
+  return largest(lane < S ? peer(&s.told.i[k], lane) : v);
+}
+
 // The cluster's winner among the threads' candidates (float key in powers of two, index; -1:
 // none).  Where others come within 2^-9 and a rounding of the largest, they are compared by
-// exact(), of the thread's own (a race in some hundreds).  bad: any thread's flag.
-template <int NT, typename F>
-DF_DEVICE int cluster_winner(float key, int i, bool& bad, F exact, Shared<NT>& s, int S) {
+// exact(), of the thread's own (a race in some hundreds).  bad: any thread's flag.  PART: and the
+// sum of the threads' parts.
+template <bool PART, int NT, typename F>
+DF_DEVICE int cluster_winner(float key, int i, bool& bad, F exact, Shared<NT>& s, int S, unsigned* part = nullptr) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int k = s.turn;
   const float mine = i >= 0 ? key : -CUDART_INF_F;
   const float w = largest(mine);
   if (lane == 0) s.w_f[warp] = w;
+  if constexpr (PART) {
+    const unsigned u = __reduce_add_sync(0xffffffffu, *part);
+    if (lane == 0) s.w_part[warp] = u;
+  }
   const int any = __syncthreads_or(bad);
   float top = largest(lane < NT / 32 ? s.w_f[lane] : -CUDART_INF_F);
   auto near = [](float key, float top) { return key == top || key >= top - 0x1p-9f - fabsf(top) * 0x1p-20f; };
   bool in = i >= 0 && near(mine, top);
   if (in) s.told.i[k] = i;   // (one of them: all that is needed of a single one)
   const int n = __syncthreads_count(in);
+  if constexpr (PART) {
+    const unsigned u = __reduce_add_sync(0xffffffffu, lane < NT / 32 ? s.w_part[lane] : 0u);
+    if (threadIdx.x == 0) s.told.part[k] = u;
+  }
   if (threadIdx.x == 0) {
     s.told.key[k] = top;
     s.told.n[k] = any ? -1 : n;
@@ -290,6 +325,7 @@ DF_DEVICE int cluster_winner(float key, int i, bool& bad, F exact, Shared<NT>& s
   meet();
   float their = lane < S ? peer(&s.told.key[k], lane) : -CUDART_INF_F;
   int their_n = lane < S ? peer(&s.told.n[k], lane) : 0, their_i = lane < S ? peer(&s.told.i[k], lane) : -1;
+  if constexpr (PART) *part = __reduce_add_sync(0xffffffffu, lane < S ? peer(&s.told.part[k], lane) : 0u);
   bad = __any_sync(0xffffffffu, their_n < 0);
   if (bad) return -1;
   top = largest(their_n > 0 ? their : -CUDART_INF_F);
@@ -325,8 +361,6 @@ DF_DEVICE int cluster_winner(float key, int i, bool& bad, F exact, Shared<NT>& s
   warp_best(v, i);
   return i;
 }
-
-DF_DEVICE int largest(int x) { return __reduce_max_sync(0xffffffffu, x); }
 
 // ------------------------------------------------------------------ sums of rows
 
@@ -525,7 +559,7 @@ DF_DEVICE int race(const char* row, const char* noise, int V, float temperature,
         }
       }
   }
-  return cluster_winner(from == CUDART_INF_F ? from : top + from, at, bad, [&] {
+  return cluster_winner<false>(from == CUDART_INF_F ? from : top + from, at, bad, [&] {
     const float e = reinterpret_cast<const float*>(noise)[at];
     return e >= kLeastVariate ? score_of(logit(row, EL, at), slope) - log2_of(e) : kWins;
   }, s, S);
@@ -568,7 +602,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         }
       }
     }
-    i = cluster_winner(top, i, bad, [&] { return (long long)order_of(top); }, s, S);
+    i = cluster_winner<false>(top, i, bad, [&] { return (long long)order_of(top); }, s, S);
   } else {
     i = race<EL, VEC>(row, p.noise + (size_t)t * p.noise_ld, p.V, temperature, bad, [](int) { return false; }, s, S);
   }
@@ -594,7 +628,320 @@ struct Node {
 };
 enum Is { kNoRow = 1, kGreedyRow = 2, kNoToken = 4, kNoDraft = 8, kSure = 16, kTaken = 32 };   // (kTaken: as a first child)
 
-enum Act { kUpdate, kDraw, kDrawRest, kEnd, kBad };
+enum Act { kUpdate, kDraw, kDrawRest, kEnd, kBad, kCareful };
+
+// Less than this part of the target's mass left at a node: the entry is walked again, carefully.  p
+// and q are known to some 5e-7 of themselves here, so that a part m left as their difference is
+// known to 5e-7 / m: to 1e-5 at least.  A rejection that leaves m has the probability m, so the
+// second walk is as rare as it is slow: of one rejected draft over 32768 tokens 35 us instead of 9,
+// of two argmax siblings 20 instead of 8.
+constexpr float kLittle = 0x1p-4f;
+
+// Which of a thread's elements of a tile are among `n` barred tokens.
+template <bool VEC, int NT>
+DF_DEVICE unsigned barred_of(const int* barred, int n, int tile0) {
+  unsigned mask = 0;
+  for (int j = 0; j < n; ++j) {
+    const unsigned off = (unsigned)(barred[j] - tile0);
+    if (off < 8u * NT && (VEC ? off >> 3 : off % NT) == threadIdx.x) mask |= 1u << (VEC ? off & 7 : off / NT);
+  }
+  return mask;
+}
+
+// ---- careful passes: weights as two floats, to 2^-38
+
+struct Two {
+  float hi, lo;
+};
+// 2^(j / 64) for j = -32 .. 32
+constexpr int kPowers = 65;
+DF_DEVICE void make_powers(Two* power) {
+  if (threadIdx.x < kPowers) {
+    const double w = exp2(((int)threadIdx.x - 32) / 64.0);
+    power[threadIdx.x] = {(float)w, (float)(w - (float)w)};
+  }
+}
+// 2^(x s - m), at most about 1: the exponent as two floats (product and sums with what their
+// roundings left), k + j / 64 + g, |g| < 1 / 100, and a polynomial in g.  (__fmul_rn: products
+// whose rounding is taken off again are not to be fused into a sum.)
+DF_DEVICE Two two_of(float x, Slope s, int m, const Two* power) {
+  const float p = __fmul_rn(x, s.hi), mf = (float)-m, left = (float)(-m - (int)mf), y = p + mf, bb = y - p, a = y + left;
+  if (!(a > -160.f)) return {0.f, 0.f};
+  const float l = ((p - (y - bb)) + (mf - bb)) + (fmaf(x, s.hi, -p) + x * s.lo);
+  const float t = a + l, cc = t - a, rest = (a - (t - cc)) + (l - cc);
+  const float k = rintf(t), j = rintf((t - k) * 64.f), g = fmaf(j, -0x1p-6f, t - k);
+  constexpr float kLn2 = 0.693147182f, kLn2Rest = -1.90465430e-9f;   // ln 2 in two parts; ln^n 2 / n!
+  const float h = __fmul_rn(g, kLn2), q = g * g * fmaf(g, fmaf(g, 0.00961812911f, 0.0555041087f), 0.240226507f);
+  const float v = fmaf(g, kLn2, -h) + (g * kLn2Rest + q), e = h + v, e2 = (h - e) + v + rest * kLn2 * (1.f + e);
+  const Two c = power[(int)j + 32];
+  const float w = __fmul_rn(c.hi, e), hi = c.hi + w, lo = ((c.hi - hi) + w) + (fmaf(c.hi, e, -w) + (c.lo + fmaf(c.hi, e2, c.lo * e)));
+  const float by = __int_as_float((127 + (int)fminf(fmaxf(k, -126.f), 100.f)) << 23);
+  return {hi * by, lo * by};
+}
+constexpr float kFine = 0x1p56f;   // units of a thread's sums of weights (a thread has 80 elements at most)
+constexpr int kCoarse = 14;        // ... and of a row's, 2^-42
+DF_DEVICE long long fine_of(Two w) { return __float2ll_rn(w.hi * kFine) + __float2ll_rn(w.lo * kFine); }
+
+// r at node `cur` of a careful walk: the target's p, or (`written`) s_r, without the tokens of
+// s_barred; `total` is its sum: of p relative to `sum`, which is p's without those that were
+// barred when it was last added up.
+struct Rest {
+  int m, written, n_barred;
+  double total, exact;   // exact: `total` when it was last added up
+  float ratio, ratio_rest, inv;
+};
+
+// All blocks of a cluster: r is added up, and with a drafter's row becomes max(r - q, 0), written.
+// What would leave nothing (by rounding, or u beyond its range) leaves r as it was.
+template <int ELT, int ELD, bool VEC, int NT>
+__device__ void take_off(const char* row, Slope s, const char* row_d, Slope s_d, int V, int S, Rest& w, Shared<NT>& sh,
+                         const int* s_barred, float* s_r, const Two* power) {
+  constexpr int kTile = 8 * NT;
+  const int tid = threadIdx.x, rank = cluster_rank(), hop = S * kTile;
+  const bool written = w.written;
+  auto barred = [&](int t0) { return barred_of<VEC, NT>(s_barred, w.n_barred, t0); };
+  auto top_of = [](float x, const Slope& s, int top) {
+    const float p = x * s.hi;
+    return p > -kScoreMost ? max(top, (int)ceilf(p) + (int)ceilf(fmaf(x, s.hi, -p))) : top;
+  };
+  int m = 0, m_d = 0;
+  long long z = 0, z_d = 0;
+  float scale = 1.f;   // of s_r, so that its sum is near 1
+  if (written) {
+    int k;
+    frexpf((float)w.exact, &k);
+    scale = ldexpf(1.f, -k);
+  }
+  while (true) {
+    if (!written) {
+      int top = kLeast;
+      for (int t0 = rank * kTile; t0 < V; t0 += hop) {
+        float x[8];
+        load8<ELT, VEC, NT>(row, t0, V, -CUDART_INF_F, x);
+        const unsigned out = barred(t0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (!(out >> k & 1)) top = top_of(x[k], s, top);
+      }
+      m = cluster_largest(top, sh, S);
+    }
+    z = 0;
+    int at = 0;
+    for (int t0 = rank * kTile; t0 < V; t0 += hop, at += kTile) {
+      float x[8];
+      if (!written) load8<ELT, VEC, NT>(row, t0, V, -CUDART_INF_F, x);
+      const unsigned out = barred(t0);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const Two v = written ? Two{s_r[at + element<VEC, NT>(t0, k) - t0] * scale, 0.f} : two_of(x[k], s, m, power);
+        if (!(out >> k & 1)) z += fine_of(v);
+      }
+    }
+    z = cluster_total((z + (1ll << (kCoarse - 1))) >> kCoarse, sh, S);
+    if (!written && m == kLeast) z = 0;
+    if (written && z > 0 && z < 1ll << 34) {   // (below 2^-8: with a larger scale again)
+      scale *= 0x1p8f;
+      continue;
+    }
+    if (z > 0 || w.n_barred == 0) break;
+    __syncthreads();
+    if (tid == 0) --w.n_barred;
+    __syncthreads();
+  }
+  __syncthreads();   // (all have read n_barred)
+  if (tid == 0) {
+    w.m = m;
+    if (z > 0) w.total = w.exact = (double)z * 0x1p-42 / scale;
+  }
+  if constexpr (ELD > 0) {
+    if (row_d) {
+      int top = kLeast;
+      for (int t0 = rank * kTile; t0 < V; t0 += hop) {
+        float y[8];
+        load8<ELD, VEC, NT>(row_d, t0, V, -CUDART_INF_F, y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = top_of(y[k], s_d, top);
+      }
+      m_d = cluster_largest(top, sh, S);
+      for (int t0 = rank * kTile; t0 < V; t0 += hop) {
+        float y[8];
+        load8<ELD, VEC, NT>(row_d, t0, V, -CUDART_INF_F, y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) z_d += fine_of(two_of(y[k], s_d, m_d, power));
+      }
+      z_d = cluster_total((z_d + (1ll << (kCoarse - 1))) >> kCoarse, sh, S);
+      if (tid == 0) {
+        const double c = w.total / ((double)z_d * 0x1p-42);
+        w.ratio = (float)c;
+        w.ratio_rest = (float)(c - (float)c);
+        w.inv = (float)(1.0 / w.total);
+      }
+      __syncthreads();
+      const float c = w.ratio, c2 = w.ratio_rest, inv = w.inv;
+      for (int write = 0; write < 2; ++write) {   // (added up first: nothing left leaves s_r as it is)
+        long long units = 0;   // of 2^-60
+        int at = 0;
+        for (int t0 = rank * kTile; t0 < V; t0 += hop, at += kTile) {
+          float x[8], y[8];
+          load8<ELD, VEC, NT>(row_d, t0, V, -CUDART_INF_F, y);
+          if (!written) load8<ELT, VEC, NT>(row, t0, V, -CUDART_INF_F, x);
+          const unsigned out = barred(t0);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float* const to = s_r + (at + element<VEC, NT>(t0, k) - t0);
+            const Two a = written ? Two{*to, 0.f} : two_of(x[k], s, m, power), b = two_of(y[k], s_d, m_d, power);
+            const float v = __fmul_rn(b.hi, c), v2 = fmaf(b.hi, c, -v) + fmaf(b.hi, c2, b.lo * c);
+            const float r = out >> k & 1 ? 0.f : fmaxf(((a.hi - v) + (a.lo - v2)) * inv, 0.f);
+            if (write)
+              *to = r;
+            else
+              units += __float2ll_rn(r * 0x1p60f);
+          }
+        }
+        if (write) break;
+        const double left = (double)cluster_total(units, sh, S) * 0x1p-60;
+        if (!(left > 0x1p-34)) return;   // (known to some 2^-37)
+        if (tid == 0) w.total = w.exact = left;
+      }
+      __syncthreads();
+      if (tid == 0) {
+        w.written = 1;
+        w.n_barred = 0;
+      }
+    }
+  }
+  if (S > 1) cluster_sync();   // (s_r is there for all blocks)
+  __syncthreads();
+}
+
+// An entry walked again from its anchor: every small difference from numbers with bits to spare.
+// All threads walk.  Returns the token behind the path (-1: none).
+template <int ELT, int ELD, bool VEC, int NT>
+__device__ __noinline__ int walk_carefully(const VerifyParams& p, int lo, int n, int S, const char* noise, const Node* s_node,
+                                           int* s_barred, float* s_r, short* s_path, int* s_len, Shared<NT>& sh) {
+  constexpr int kTile = 8 * NT;
+  __shared__ Rest w;
+  __shared__ Two s_power[kPowers];
+  const int tid = threadIdx.x, rank = cluster_rank(), V = p.V;
+  make_powers(s_power);
+  bool bad = false;
+  int cur = 0, len = 1;
+  while (true) {
+    const int is_row = s_node[cur].is;
+    if (is_row & kNoRow) return -1;
+    const char* row = p.target.at + (size_t)(lo + cur) * p.target.ld;
+    const float temperature = heat_at(p.target.temperature, lo + cur);
+    const Slope s = slope_of(temperature);
+    __syncthreads();
+    if (tid == 0) {
+      w.written = w.n_barred = 0;
+      w.total = w.exact = 0.0;   // (not added up: the first child's test is settled)
+    }
+    __syncthreads();
+    auto take = [&](int child) {
+      const char* row_d = nullptr;
+      Slope s_d = {0.f, 0.f};
+      if constexpr (ELD > 0) {
+        if (child >= 0) {
+          const int d = s_node[child].row;
+          row_d = p.draft.at + (size_t)d * p.draft.ld;
+          s_d = slope_of(heat_at(p.draft.temperature, d));
+        }
+      }
+      take_off<ELT, ELD, VEC, NT>(row, s, row_d, s_d, V, S, w, sh, s_barred, s_r, s_power);
+    };
+    int next = -1;
+    bool first = true;
+    for (int j = cur + 1; j < n && next < 0 && len < p.max_path; ++j) {
+      if (s_node[j].parent != cur) continue;
+      const int is = s_node[j].is, token = s_node[j].token;
+      if (is & kNoToken) {
+        if (rank == 0 && tid == 0) set_status(p.status, DEV_BAD_TOKEN);
+        continue;
+      }
+      if (is & kNoDraft) return -1;
+      double r = s_node[j].p;
+      bool taken = is & kTaken;
+      if (!first && !(is_row & kGreedyRow)) {
+        bool out = false;
+        for (int k = 0; k < w.n_barred; ++k) out |= s_barred[k] == token;
+        if ((!out && w.total < kLittle * w.exact) || w.exact == 0.0) take(-1);
+        for (int k = 0; k < w.n_barred; ++k) out |= s_barred[k] == token;
+        r = 0.0;
+        if (!out && w.written) {
+          const int tile = token / kTile;
+          r = (double)peer(s_r + tile / S * kTile + (token - tile * kTile), tile % S) / w.total;
+        } else if (!out) {
+          const Two t = two_of(logit(row, ELT, token), s, w.m, s_power);
+          r = ((double)t.hi + t.lo) / w.total;
+        }
+        taken = (double)s_node[j].u * (double)s_node[j].q < r;
+      }
+      if (taken) {
+        next = j;
+      } else if (!(is_row & kGreedyRow)) {
+        if (!(is & kSure)) {
+          take(j);
+        } else if (r > 0.0) {
+          __syncthreads();   // (all have read s_barred and the sums)
+          if (tid == 0) {
+            s_barred[w.n_barred++] = token;
+            w.total -= r * w.total;
+          }
+          __syncthreads();
+        }
+      }
+      first = false;
+    }
+    if (next >= 0) {
+      cur = next;
+      if (tid == 0) s_path[len] = (short)cur;
+      ++len;
+      continue;
+    }
+    if (tid == 0) *s_len = len;
+    if (is_row & kGreedyRow) return s_node[cur].own.m;
+    // ---- the token behind the path: from what is left, or (only barred tokens: u beyond its range)
+    // from what was before the last ones were
+    for (bool again = false;; again = true) {
+      if (again) {
+        __syncthreads();
+        take(-1);
+      }
+      const int n_barred = w.n_barred;
+      int token;
+      if (!w.written) {
+        token = race<ELT, VEC>(row, noise, V, temperature, bad, [&](int i) {
+          for (int j = 0; j < n_barred; ++j)
+            if (s_barred[j] == i) return true;
+          return false;
+        }, sh, S);
+      } else {
+        float best = 0.f, at_e = 1.f;   // best / at_e is the largest so far
+        int win = -1, at = 0;
+        const float inv = (float)(1.0 / w.total);
+        for (int t0 = rank * kTile; t0 < V; t0 += S * kTile, at += kTile) {
+          float z[8];
+          load8<4, VEC, NT>(noise, t0, V, CUDART_NAN_F, z);
+          const unsigned out = barred_of<VEC, NT>(s_barred, n_barred, t0);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int i = element<VEC, NT>(t0, k);
+            const float r = s_r[at + i - t0] * inv;
+            if (r > 0.f && z[k] >= 0.f && r * at_e > best * z[k] && !(out >> k & 1)) {
+              best = r;
+              win = i;
+              at_e = z[k];
+            }
+          }
+        }
+        token = cluster_winner<false>(lg2(best) - lg2(at_e), win, bad,
+                                      [&] { return at_e >= kLeastVariate ? log2_of(best) - log2_of(at_e) : kWins; }, sh, S);
+      }
+      if (token >= 0 || n_barred == 0 || again) return token;
+    }
+  }
+}
 
 // A cluster per entry; its blocks walk alike, from the same numbers.  r is the target's p
 // without the tokens of s_barred, until a rejection with other children behind it makes the
@@ -605,6 +952,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
   extern __shared__ __align__(16) char smem[];
   __shared__ Shared<NT> s;
   __shared__ int s_act, s_child, s_cur, s_len, s_from, s_n_barred, s_written, s_seen;
+  __shared__ float s_mass;   // of the target's at the node, what rejections have left
   __shared__ double s_total;
   // (`most`: nodes of an entry that there is room for)
   Node* s_node = reinterpret_cast<Node*>(smem);
@@ -669,6 +1017,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
     s_written = 0;
     s_seen = 0;
     s_total = 1.0;
+    s_mass = 1.f;
   }
   pdl_wait();
   __syncthreads();
@@ -720,6 +1069,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
     if (tid < 32) {
       int cur = s_cur, len = s_len, from = s_from, barred = s_n_barred, written = s_written, child = -1, act = -1;
       double total = s_total;
+      float mass = s_mass;
       bool fresh = from == 1 && len == 1;   // no child of cur has been tried
       while (act < 0) {
         const int row = s_node[cur].is;
@@ -747,6 +1097,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
           act = kUpdate;
           break;
         }
+        if (mass < kLittle) {   // (its test needs what is left)
+          act = kCareful;
+          break;
+        }
         const Node& nd = s_node[next];
         const int is = nd.is;
         from = next + 1;
@@ -764,7 +1118,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
         if (!(row & kGreedyRow) && (barred || written)) {
           int out = 0;
           for (int j = lane; j < barred; j += 32) out |= s_barred[j] == nd.token;
-          const bool gone = __any_sync(0xffffffffu, out) || !(total > 0.0);
+          const bool gone = __any_sync(0xffffffffu, out);
           if (written && !gone) {
             const int tile = nd.token / kTile;
             r = (double)peer(s_r + tile / S * kTile + (nd.token - tile * kTile), tile % S);
@@ -778,6 +1132,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
           cur = next;
           barred = written = 0;
           total = 1.0;
+          mass = 1.f;
           fresh = true;
           continue;
         }
@@ -789,6 +1144,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
           if (lane == 0) s_barred[barred] = nd.token;
           ++barred;
           total -= r * total;
+          mass *= (float)(1.0 - r);
           __syncwarp();
         }
       }
@@ -801,10 +1157,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
         s_n_barred = barred;
         s_written = written;
         s_total = total;
+        s_mass = mass;
       }
     }
     __syncthreads();
-    if (s_act != kUpdate) break;
+    if (s_act != kUpdate || s_mass < kLittle) break;
 
     // ---- r becomes max(r - q, 0), written down
     if constexpr (ELD > 0) {
@@ -845,9 +1202,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
         take(t0 + hop, at + kTile, x[1], y[1]);
       }
       const double sum = (double)cluster_total(units, s, S) * 0x1p-50;
-      if (tid == 0) {   // (nothing left, by rounding alone: the target's own)
-        s_written = sum > 0.0;
-        s_total = sum > 0.0 ? sum : 1.0;
+      if (tid == 0) {
+        s_written = 1;
+        s_total = sum;
+        s_mass *= (float)sum;
         s_n_barred = 0;
         s_seen = 1;
       }
@@ -856,7 +1214,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
   }
 
   // ---- the token behind the path
-  const int act = s_act, cur = s_cur, barred = s_n_barred, written = s_written;
+  int act = s_act;
+  const int cur = s_cur, barred = s_n_barred, written = s_written;
+  // (tokens barred beside a drafter's distribution: what is left is not added up here)
+  if (act == kUpdate || (act == kDrawRest && (barred || s_mass < kLittle)) || (act == kDraw && written && s_mass < kLittle))
+    act = kCareful;
   const RowStats st = s_node[cur].own;
   const float temperature = heat_at(p.target.temperature, lo + cur);
   auto is_barred = [&](int i) {
@@ -879,6 +1241,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
     const char* row = target_row(cur);
     float best = 0.f, at_x = 0.f, at_y = 0.f, at_e = 1.f;   // best / at_e is the largest so far
     int win = -1;
+    float part = 0.f;   // of what is left
     float x[2][8], y[2][8], z[2][8];
     auto fetch = [&](int t0, float(&x)[8], float(&y)[8], float(&z)[8]) {
       load8<4, VEC, NT>(noise, t0, V, CUDART_NAN_F, z);
@@ -893,7 +1256,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
         const int i = element<VEC, NT>(t0, k);
         if (written) x[k] = s_r[at + i - t0];
         float r = (written ? x[k] : ex2(fmaf(x[k], st.s, ref.at))) * inv;
-        if (less) r = r - ex2(fmaf(y[k], sd.s, ref_d.at)) * inv_d;
+        if (less) {
+          r = r - ex2(fmaf(y[k], sd.s, ref_d.at)) * inv_d;
+          part += fmaxf(r, 0.f);
+        }
         // (r / z above the best, without a quotient)
         if (r > 0.f && z[k] >= 0.f && r * at_e > best * z[k] && !is_barred(i)) {
           best = r;
@@ -915,18 +1281,20 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
       take(t0 + hop, at + kTile, x[1], y[1], z[1]);
     }
     const float top = lg2(best) - lg2(at_e);
-    token = cluster_winner(top, win, bad, [&] {
+    unsigned parts = (unsigned)__float2int_rn(part * 0x1p30f);
+    token = cluster_winner<ELD != 0>(top, win, bad, [&] {
       float r = (written ? at_x : weight_of(at_x, st.s, st.m)) * inv0;
       if (less) r = fmaf(-weight_of(at_y, sd.s, sd.m), sd.inv, r);
       return at_e >= kLeastVariate ? log2_of(r) - log2_of(at_e) : kWins;
-    }, s, S);
+    }, s, S, &parts);
+    if (less && s_mass * ((float)parts * 0x1p-30f) < kLittle) act = kCareful;
   }
-  // the target's own row: the usual draw, or because rounding left nothing of the rest
-  if (token < 0 && (act == kDraw || act == kDrawRest)) {
-    const bool rest = act == kDraw && !written;
-    token = race<ELT, VEC>(target_row(cur), noise, V, temperature, bad, [&](int i) { return rest && is_barred(i); }, s, S);
-    if (token < 0 && rest && barred > 0)
-      token = race<ELT, VEC>(target_row(cur), noise, V, temperature, bad, [](int) { return false; }, s, S);
+  if (act == kDraw && !written)
+    token = race<ELT, VEC>(target_row(cur), noise, V, temperature, bad, is_barred, s, S);
+  // (and where tokens are barred and nothing else is to be drawn)
+  if (act == kCareful || (act == kDraw && token < 0 && barred > 0 && !bad)) {
+    token = walk_carefully<ELT, ELD, VEC, NT>(p, lo, n, S, noise, s_node, s_barred, s_r, s_path, &s_len, s);
+    __syncthreads();
   }
   const bool none = token < 0 || bad;
   if (rank == 0) {

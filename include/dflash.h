@@ -789,7 +789,10 @@ DFLASH_API int dflash_tree_accept(dflash_cache* c, int32_t n_seq, const int32_t*
  *   ones, which is token i with probability p_i.  A NaN excludes its token, a variate below
  *   2^-126 counts as 0.
  * Results are those of the formulas up to comparisons that are closer than some 1e-6, whatever
- * the scores, and do not depend on the order of anything.
+ * the scores, and do not depend on the order of anything.  What rejected drafts leave of a row,
+ * max(p - q, 0), is a difference, known to some 1e-6 of p before it is divided by its sum; where
+ * less than 1/16 of p is left, to 2^-37 of p (every further drawn sibling adds 2^-24 of what was
+ * left before it).  Less than 2^-34 counts as nothing: then the rejection leaves r as it was.
  */
 
 /*
@@ -821,8 +824,8 @@ DFLASH_API int dflash_sample(dflash_cache* c, int32_t T, int32_t n_vocab, const 
  *   path, n_path, id_last: as for dflash_tree_accept.
  * A target row of temperature 0 accepts its argmax alone: with all of them 0, the call is
  * dflash_tree_accept.  A drafted token out of range is rejected (BAD_TOKEN).  An entry whose
- * walk meets a row that is no distribution, or a draft_row out of range (BAD_PROBS), or of
- * more nodes (BAD_ROWS), gets n_path 0 and keeps its id_last.  T + n_draft <=
+ * walk meets a row that is no distribution, a draft_row out of range, or a draw whose tokens all
+ * have a NaN variate (BAD_PROBS), or of more nodes (BAD_ROWS), gets n_path 0 and keeps its id_last.  T + n_draft <=
  * DFLASH_MAX_VERIFY_ROWS (TOO_MANY_ROWS).
  */
 DFLASH_API int dflash_tree_verify(dflash_cache* c, int32_t n_seq, const int32_t* row_start, int32_t T,
