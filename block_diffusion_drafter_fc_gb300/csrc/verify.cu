@@ -43,7 +43,7 @@ namespace {
 constexpr int kThreads = 256;              // of row_stats and sample
 constexpr int kWalkThreads = 512;          // of verify: few entries, whole rows
 constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596303e-8f;   // log2(e) in two parts
-constexpr float kUnit = 0x1p40f;           // of sums: a row's is below 2^21 (a batch of 16 is at most 64)
+constexpr float kUnit = 0x1p40f;           // of sums
 constexpr float kCold = 0x1p-20f;          // temperatures below it (and not below 0) count as 0
 constexpr float kLeastVariate = 0x1p-126f; // variates below it count as 0 (lg2 takes them so)
 constexpr float kScoreMost = 0x1p30f;      // scores x log2(e) / T of this magnitude count as infinite
@@ -367,13 +367,23 @@ DF_DEVICE int cluster_winner(float key, int i, bool& bad, F exact, Shared<NT>& s
 // A sum whose reference moves up from m to `to`.
 DF_DEVICE long long shifted(long long z, int m, int to) { return z >> min((unsigned)to - (unsigned)m, 63u); }
 
+// Tiles of a batch: 64 bytes of a thread in flight.
+template <int EL>
+constexpr int kBatch = EL == 2 ? 4 : 2;
+// A batch adds 64 at most (kBatchMost), and every thread of every piece (of two tiles or more) may have
+// one that is not full: a row's sum stays within 63 bits.
+constexpr float kBatchMost = 64.f;
+constexpr int pieces_most(int V) { return ((V + 8 * kThreads - 1) / (8 * kThreads) + 1) / 2; }
+static_assert((kVocabMost / (8 * kBatch<4>) + kThreads * pieces_most(kVocabMost)) * (double)kBatchMost * kUnit < 0x1p62,
+              "a row's sum overflows");
+
 // Piece `g` of P of a row: the tiles g, g + P, ..  A thread adds up 2^(x s - m), m its first
 // batch's largest score, rounded up; a later batch of more than 64 makes it move m and shift
 // its sum.
 template <int EL, bool VEC>
 DF_DEVICE void row_piece(const char* row, int V, float temperature, bool draft, int g, int P, Piece* out) {
   constexpr int kTile = 8 * kThreads;
-  constexpr int kTiles = EL == 2 ? 4 : 2;    // tiles of a batch: 64 bytes of a thread in flight
+  constexpr int kTiles = kBatch<EL>;
   __shared__ long long w_v[kThreads / 32];
   __shared__ int w_m[kThreads / 32], w_i[kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -429,8 +439,8 @@ DF_DEVICE void row_piece(const char* row, int V, float temperature, bool draft, 
 #pragma unroll
         for (int k = 0; k < 8; ++k) part[k & 3] += ex2(fmaf(x[j][k], sc, ref.at));
       const float b = ((part[0] + part[1]) + (part[2] + part[3])) * ref.by;
-      if (b <= 64.f || again) {
-        bad |= !(b <= 64.f);                 // NaN or infinite
+      if (b <= kBatchMost || again) {
+        bad |= !(b <= kBatchMost);           // NaN or infinite
         sum += __float2ll_rn(b * kUnit);
         break;
       }
@@ -1352,9 +1362,9 @@ static_assert(kSmemMost <= 225 * 1024, "shared memory");
 
 template <int ELT, int ELD, bool VEC>
 cudaError_t verify_as(VerifyParams& p, cudaStream_t st) {
-  const int rows = p.rows.T + (ELD ? p.draft.rows : 0), tiles = (p.V + 8 * kThreads - 1) / (8 * kThreads);
+  const int rows = p.rows.T + (ELD ? p.draft.rows : 0);
   // pieces of a row: enough blocks for six rounds of the GPU's, each of two tiles at least
-  p.pieces = (int)std::min<int64_t>(std::max(rows > 0 ? kSms * 30 / rows : 1, 1), (tiles + 1) / 2);
+  p.pieces = std::min(std::max(rows > 0 ? kSms * 30 / rows : 1, 1), pieces_most(p.V));
   // (without rows too: the walk may start ahead of this launch's end, not of what came before)
   const cudaError_t e = launch_dependent(row_stats_kernel<ELT, ELD ? ELD : 4, VEC>, dim3(std::max(rows, 1) * p.pieces),
                                          kThreads, 0, st, p);
