@@ -43,7 +43,10 @@ DF_DEVICE int small_quotient(int y, uint32_t magic) { return magic ? (int)__umul
 // A launch that may start while the kernel before it ends: every kernel here lets
 // the next one be scheduled at once and waits for the one before it with
 // griddepcontrol.wait before it touches global memory (a turn's small calls then
-// cost no launch gaps).
+// cost no launch gaps).  One exception: verify_kernel reads its call's inputs ahead
+// of its wait; row_stats_kernel, launched just before it, lets it start only behind
+// its own wait, when everything that came earlier is done.  No launch may come
+// between the two.
 template <typename K, typename... A>
 cudaError_t launch_dependent(K* kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};

@@ -11,9 +11,11 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 
-// Fewest slots that sharing has to save, over all members, to be worth the rows' second part
-// (us shared, and not): one row each, 4 samples of 960 slots 16.7, 18.6; 2 of 2048 15.4, 15.6;
-// 32 of 512 23, 30; 32 of 256 23, 24; but 32 trees of 16 nodes over 64 slots 33, 22.
+// Fewest slots that sharing has to save, over all members, to be worth the rows' second part,
+// for entries of one row (us of the attention shared, and with a plan of zeros): 4 members over
+// 1024 slots 13.1, 14.8, over 512 12.9, 13.2; 32 members over 256 19.7, 25.6, over 64 20.6, 20.4.
+// The rule does not know the rows.  32 members of 16: over 512 slots 35, 33, 1024 40.6, 40.6, 4096 62,
+// 82; of 32: 4096 104, 93, 16384 260, 277; of 64 (x 4 heads: a tile of their own): 4096 182, 134.
 constexpr int kWorthSlots = 2048;
 
 // A block per group.  The group shares the full pages, below the least length, in which no

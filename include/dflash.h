@@ -661,7 +661,8 @@ DFLASH_API int dflash_norm_rope(dflash_cache* c, int32_t T, const int32_t* pos, 
  *   dq, dk: as q_out, k_out there (each may be its own input or dout);
  *   dq_norm, dk_norm: device f32 [head_dim].
  * A row of a negative position (DFLASH_DEV_BAD_POSITION) is not written and not counted.
- * Sums are taken in an order that depends on T alone.
+ * Sums are taken in an order that depends on T, on the handle's geometry and on which of q and k are
+ * given (dq_norm of a call with q alone may differ in its last bits from that of a call with both).
  */
 DFLASH_API int dflash_norm_rope_grad(dflash_cache* c, int32_t T, const int32_t* pos, float eps, const void* q,
                                      int64_t q_stride, const void* q_norm, const void* dq_out,
@@ -719,8 +720,11 @@ DFLASH_API int dflash_tree_attend(dflash_cache* c, int32_t layer, int32_t n_seq,
  * group_start[g + 1] - 1 (device int32 [n_group + 1], ascending, within 0..n_seq), for
  * instance the forks of one prompt.  What a group shares is found in the page table: the
  * full pages below its members' least length that are the same for all of them; 0 where
- * sharing would save fewer than 2048 slots over all members, which takes longer than not
- * sharing.
+ * sharing would save fewer than 2048 slots over all members, which is about what entries of
+ * one row need to gain from it.  The plan does not know the rows, and every row gets a second
+ * part: entries of 16 rows (of 4 query heads a kv head) gain from some 2000 to 4000 common
+ * slots on, of 32 from some 16000; entries of 64 fill a tile by themselves and lose: they are
+ * better served by dflash_tree_attend, or by a plan of zeros.
  *   plan: device int32 [n_seq + n_group], written: slots that entry s has in common with
  *   its group (0: in none), then the slots that group g has in common.  A caller may change
  *   them, for a group and its entries alike, to any number of common slots.
@@ -738,7 +742,8 @@ DFLASH_API int dflash_prefix_workspace_size(const dflash_cache* c, int32_t T, si
  * dflash_tree_attend where entries share prefixes: the same outputs, with the slots that a
  * group shares read and multiplied once for the rows of all its members (their query heads
  * fill common tiles); every entry's other slots follow as in dflash_tree_attend, and the
- * two parts of a row are joined in fp32.
+ * two parts of a row are joined in fp32.  Weights are rounded for the product with V as there
+ * (bf16 heads of 64 and 128: to bf16).
  *   seqs, row_start, T, max_tree, mask, q, out, lse as there;
  *   n_group, group_start, plan: as given to and written by dflash_prefix_plan for these
  *   entries (the first member's pages are read for all of a group);
