@@ -444,20 +444,16 @@ DF_DEVICE void row_piece(const char* row, int V, float temperature, bool draft, 
         sum += __float2ll_rn(b * kUnit);
         break;
       }
-      // the largest score, rounded (its own step is up to 64), and what the rounding left of it
-      float top = -CUDART_INF_F, left = -CUDART_INF_F;
+      float top = -CUDART_INF_F;
 #pragma unroll
       for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) top = fmaxf(top, x[j][k] * sc);
-      if (b == b && top <= -kScoreMost) break;   // (counts as -inf: nothing to add)
-      if (!(top > -kScoreMost && top < kScoreMost)) continue;
-      top = ceilf(top);
-#pragma unroll
-      for (int j = 0; j < kTiles; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) left = fmaxf(left, fmaf(x[j][k], sc, -top));
-      const int to = (int)top + (int)ceilf(left);
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, x[j][k]);
+      // its score, rounded (a step of it is up to 64), and what the rounding left
+      const float score = ceilf(top * sc);
+      if (b == b && score <= -kScoreMost) break;   // (counts as -inf: nothing to add)
+      if (!(score > -kScoreMost && score < kScoreMost)) continue;
+      const int to = (int)score + (int)ceilf(fmaf(top, sc, -score));
       if (to > m) {
         sum = m > kLeast ? shifted(sum, m, to) : 0;
         m = to;
