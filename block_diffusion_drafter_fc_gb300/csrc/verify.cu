@@ -639,8 +639,8 @@ enum Act { kUpdate, kDraw, kDrawRest, kEnd, kBad, kCareful };
 // Less than this part of the target's mass left at a node: the entry is walked again, carefully.  p
 // and q are known to some 5e-7 of themselves here, so that a part m left as their difference is
 // known to 5e-7 / m: to 1e-5 at least.  A rejection that leaves m has the probability m, so the
-// second walk is as rare as it is slow: of one rejected draft over 32768 tokens 35 us instead of 9,
-// of two argmax siblings 20 instead of 8.
+// second walk is as rare as it is slow: of one rejected draft over 32768 tokens 29 us instead of 9 (over
+// 151936 68, 14), of two argmax siblings 18 instead of 8.
 constexpr float kLittle = 0x1p-4f;
 
 // Which of a thread's elements of a tile are among `n` barred tokens.
@@ -684,113 +684,122 @@ DF_DEVICE Two two_of(float x, Slope s, int m, const Two* power) {
   const float by = __int_as_float((127 + (int)fminf(fmaxf(k, -126.f), 100.f)) << 23);
   return {hi * by, lo * by};
 }
-constexpr float kFine = 0x1p56f;   // units of a thread's sums of weights (a thread has 80 elements at most)
-constexpr int kCoarse = 14;        // ... and of a row's, 2^-42
+// Units of a careful sum, 2^-60: references are such that sums are at most 1.
+constexpr float kFine = 0x1p60f;
 DF_DEVICE long long fine_of(Two w) { return __float2ll_rn(w.hi * kFine) + __float2ll_rn(w.lo * kFine); }
+// A reference as high as a row's sum.
+DF_DEVICE int above_sum(RowStats st) {
+  int k;
+  frexpf(__fdiv_rn(1.f, st.inv), &k);
+  return st.m + k;
+}
 
-// r at node `cur` of a careful walk: the target's p, or (`written`) s_r, without the tokens of
-// s_barred; `total` is its sum: of p relative to `sum`, which is p's without those that were
-// barred when it was last added up.
+// r at node `cur` of a careful walk: the target's p (by 2^(x s - m)), or (`written`) s_r, without
+// the tokens of s_barred; `total` is its sum, `exact` what it was when it was last added up.
 struct Rest {
   int m, written, n_barred;
-  double total, exact;   // exact: `total` when it was last added up
+  double total, exact;
   float ratio, ratio_rest, inv;
 };
+// A row, its slope, and its sum as the first pass left it.
+struct Row {
+  const char* at;
+  Slope s;
+  RowStats sum;
+};
 
-// All blocks of a cluster: r is added up, and with a drafter's row becomes max(r - q, 0), written.
-// What would leave nothing (by rounding, or u beyond its range) leaves r as it was.
+// All blocks of a cluster: r is added up, and with a drafter's row (at: not null) becomes
+// max(r - q, 0), written.  What would leave nothing (by rounding, or u beyond its range) leaves r
+// as it was.
 template <int ELT, int ELD, bool VEC, int NT>
-__device__ void take_off(const char* row, Slope s, const char* row_d, Slope s_d, int V, int S, Rest& w, Shared<NT>& sh,
-                         const int* s_barred, float* s_r, const Two* power) {
+__device__ void take_off(const Row& row, const Row& draft, int V, int S, Rest& w, Shared<NT>& sh, const int* s_barred,
+                         float* s_r, const Two* power) {
   constexpr int kTile = 8 * NT;
   const int tid = threadIdx.x, rank = cluster_rank(), hop = S * kTile;
   const bool written = w.written;
+  const Slope s = row.s, s_d = draft.s;
   auto barred = [&](int t0) { return barred_of<VEC, NT>(s_barred, w.n_barred, t0); };
-  auto top_of = [](float x, const Slope& s, int top) {
-    const float p = x * s.hi;
-    return p > -kScoreMost ? max(top, (int)ceilf(p) + (int)ceilf(fmaf(x, s.hi, -p))) : top;
-  };
-  int m = 0, m_d = 0;
-  long long z = 0, z_d = 0;
-  float scale = 1.f;   // of s_r, so that its sum is near 1
+  int m = above_sum(row.sum), m_d = 0;
+  float scale = 1.f;   // of s_r: so that its sum is at most 1
   if (written) {
     int k;
     frexpf((float)w.exact, &k);
     scale = ldexpf(1.f, -k);
   }
+  if (ELD && draft.at) m_d = above_sum(draft.sum);
+  long long z = 0, z_d = 0;
   while (true) {
-    if (!written) {
-      int top = kLeast;
-      for (int t0 = rank * kTile; t0 < V; t0 += hop) {
-        float x[8];
-        load8<ELT, VEC, NT>(row, t0, V, -CUDART_INF_F, x);
-        const unsigned out = barred(t0);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (!(out >> k & 1)) top = top_of(x[k], s, top);
-      }
-      m = cluster_largest(top, sh, S);
-    }
     z = 0;
+    const bool both = ELD && draft.at && z_d == 0;
     int at = 0;
     for (int t0 = rank * kTile; t0 < V; t0 += hop, at += kTile) {
-      float x[8];
-      if (!written) load8<ELT, VEC, NT>(row, t0, V, -CUDART_INF_F, x);
+      float x[8], y[8];
+      if (!written) load8<ELT, VEC, NT>(row.at, t0, V, -CUDART_INF_F, x);
+      if (ELD && both) load8<ELD ? ELD : 4, VEC, NT>(draft.at, t0, V, -CUDART_INF_F, y);
       const unsigned out = barred(t0);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const Two v = written ? Two{s_r[at + element<VEC, NT>(t0, k) - t0] * scale, 0.f} : two_of(x[k], s, m, power);
         if (!(out >> k & 1)) z += fine_of(v);
+        if (ELD && both) z_d += fine_of(two_of(y[k], s_d, m_d, power));
       }
     }
-    z = cluster_total((z + (1ll << (kCoarse - 1))) >> kCoarse, sh, S);
-    if (!written && m == kLeast) z = 0;
-    if (written && z > 0 && z < 1ll << 34) {   // (below 2^-8: with a larger scale again)
-      scale *= 0x1p8f;
+    z = cluster_total(z, sh, S);
+    if (both) z_d = cluster_total(z_d, sh, S);
+    if (z >= 1ll << 46) break;
+    // without the barred tokens it is small: a lower reference (a token may have lost half a unit)
+    if (z > 0) {
+      const int k = __clzll(z + V) - 4;
+      if (written)
+        scale = ldexpf(scale, k);
+      else
+        m -= k;
       continue;
     }
-    if (z > 0 || w.n_barred == 0) break;
+    int top = kLeast;   // the largest score
+    for (int t0 = rank * kTile; t0 < V && !written; t0 += hop) {
+      float x[8];
+      load8<ELT, VEC, NT>(row.at, t0, V, -CUDART_INF_F, x);
+      const unsigned out = barred(t0);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float v = __fmul_rn(x[k], s.hi);
+        if (!(out >> k & 1) && v > -kScoreMost) top = max(top, (int)ceilf(v) + (int)ceilf(fmaf(x[k], s.hi, -v)));
+      }
+    }
+    top = cluster_largest(top, sh, S);
+    if (top > kLeast) {
+      m = top + 19;
+      continue;
+    }
+    if (w.n_barred == 0) break;   // (nothing is left: r as it was before the last one)
     __syncthreads();
     if (tid == 0) --w.n_barred;
+    m = above_sum(row.sum);
     __syncthreads();
   }
-  __syncthreads();   // (all have read n_barred)
+  __syncthreads();   // (all have read the sums)
   if (tid == 0) {
     w.m = m;
-    if (z > 0) w.total = w.exact = (double)z * 0x1p-42 / scale;
+    w.total = w.exact = (double)z * 0x1p-60 / scale;
   }
   if constexpr (ELD > 0) {
-    if (row_d) {
-      int top = kLeast;
-      for (int t0 = rank * kTile; t0 < V; t0 += hop) {
-        float y[8];
-        load8<ELD, VEC, NT>(row_d, t0, V, -CUDART_INF_F, y);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = top_of(y[k], s_d, top);
-      }
-      m_d = cluster_largest(top, sh, S);
-      for (int t0 = rank * kTile; t0 < V; t0 += hop) {
-        float y[8];
-        load8<ELD, VEC, NT>(row_d, t0, V, -CUDART_INF_F, y);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) z_d += fine_of(two_of(y[k], s_d, m_d, power));
-      }
-      z_d = cluster_total((z_d + (1ll << (kCoarse - 1))) >> kCoarse, sh, S);
+    if (draft.at) {
       if (tid == 0) {
-        const double c = w.total / ((double)z_d * 0x1p-42);
+        const double c = w.total / ((double)z_d * 0x1p-60);
         w.ratio = (float)c;
         w.ratio_rest = (float)(c - (float)c);
         w.inv = (float)(1.0 / w.total);
       }
       __syncthreads();
       const float c = w.ratio, c2 = w.ratio_rest, inv = w.inv;
-      for (int write = 0; write < 2; ++write) {   // (added up first: nothing left leaves s_r as it is)
-        long long units = 0;   // of 2^-60
+      for (int pass = written ? 0 : 1; pass < 2; ++pass) {   // (nothing left leaves s_r as it is: added up first)
+        long long units = 0;
         int at = 0;
         for (int t0 = rank * kTile; t0 < V; t0 += hop, at += kTile) {
           float x[8], y[8];
-          load8<ELD, VEC, NT>(row_d, t0, V, -CUDART_INF_F, y);
-          if (!written) load8<ELT, VEC, NT>(row, t0, V, -CUDART_INF_F, x);
+          load8<ELD, VEC, NT>(draft.at, t0, V, -CUDART_INF_F, y);
+          if (!written) load8<ELT, VEC, NT>(row.at, t0, V, -CUDART_INF_F, x);
           const unsigned out = barred(t0);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -798,18 +807,14 @@ __device__ void take_off(const char* row, Slope s, const char* row_d, Slope s_d,
             const Two a = written ? Two{*to, 0.f} : two_of(x[k], s, m, power), b = two_of(y[k], s_d, m_d, power);
             const float v = __fmul_rn(b.hi, c), v2 = fmaf(b.hi, c, -v) + fmaf(b.hi, c2, b.lo * c);
             const float r = out >> k & 1 ? 0.f : fmaxf(((a.hi - v) + (a.lo - v2)) * inv, 0.f);
-            if (write)
-              *to = r;
-            else
-              units += __float2ll_rn(r * 0x1p60f);
+            units += __float2ll_rn(r * kFine);
+            if (pass == 1) *to = r;
           }
         }
-        if (write) break;
         const double left = (double)cluster_total(units, sh, S) * 0x1p-60;
         if (!(left > 0x1p-34)) return;   // (known to some 2^-37)
-        if (tid == 0) w.total = w.exact = left;
+        if (tid == 0 && pass == 1) w.total = w.exact = left;
       }
-      __syncthreads();
       if (tid == 0) {
         w.written = 1;
         w.n_barred = 0;
@@ -820,24 +825,23 @@ __device__ void take_off(const char* row, Slope s, const char* row_d, Slope s_d,
   __syncthreads();
 }
 
-// An entry walked again from its anchor: every small difference from numbers with bits to spare.
-// All threads walk.  Returns the token behind the path (-1: none).
+// The walk from node `cur` on, the path's last: every difference from numbers with bits to spare.  All
+// threads walk.  Returns the token behind the path (-1: none).
 template <int ELT, int ELD, bool VEC, int NT>
 __device__ __noinline__ int walk_carefully(const VerifyParams& p, int lo, int n, int S, const char* noise, const Node* s_node,
-                                           int* s_barred, float* s_r, short* s_path, int* s_len, Shared<NT>& sh) {
+                                           int* s_barred, float* s_r, short* s_path, int* s_len, int cur, Shared<NT>& sh) {
   constexpr int kTile = 8 * NT;
   __shared__ Rest w;
   __shared__ Two s_power[kPowers];
   const int tid = threadIdx.x, rank = cluster_rank(), V = p.V;
   make_powers(s_power);
   bool bad = false;
-  int cur = 0, len = 1;
+  int len = *s_len;
   while (true) {
     const int is_row = s_node[cur].is;
     if (is_row & kNoRow) return -1;
-    const char* row = p.target.at + (size_t)(lo + cur) * p.target.ld;
     const float temperature = heat_at(p.target.temperature, lo + cur);
-    const Slope s = slope_of(temperature);
+    const Row row = {p.target.at + (size_t)(lo + cur) * p.target.ld, slope_of(temperature), s_node[cur].own};
     __syncthreads();
     if (tid == 0) {
       w.written = w.n_barred = 0;
@@ -845,16 +849,12 @@ __device__ __noinline__ int walk_carefully(const VerifyParams& p, int lo, int n,
     }
     __syncthreads();
     auto take = [&](int child) {
-      const char* row_d = nullptr;
-      Slope s_d = {0.f, 0.f};
-      if constexpr (ELD > 0) {
-        if (child >= 0) {
-          const int d = s_node[child].row;
-          row_d = p.draft.at + (size_t)d * p.draft.ld;
-          s_d = slope_of(heat_at(p.draft.temperature, d));
-        }
+      Row draft = {nullptr, {0.f, 0.f}, {1.f, 0.f, 0}};
+      if (ELD && child >= 0) {
+        const int d = s_node[child].row;
+        draft = {p.draft.at + (size_t)d * p.draft.ld, slope_of(heat_at(p.draft.temperature, d)), s_node[child].from};
       }
-      take_off<ELT, ELD, VEC, NT>(row, s, row_d, s_d, V, S, w, sh, s_barred, s_r, s_power);
+      take_off<ELT, ELD, VEC, NT>(row, draft, V, S, w, sh, s_barred, s_r, s_power);
     };
     int next = -1;
     bool first = true;
@@ -878,7 +878,7 @@ __device__ __noinline__ int walk_carefully(const VerifyParams& p, int lo, int n,
           const int tile = token / kTile;
           r = (double)peer(s_r + tile / S * kTile + (token - tile * kTile), tile % S) / w.total;
         } else if (!out) {
-          const Two t = two_of(logit(row, ELT, token), s, w.m, s_power);
+          const Two t = two_of(logit(row.at, ELT, token), row.s, w.m, s_power);
           r = ((double)t.hi + t.lo) / w.total;
         }
         taken = (double)s_node[j].u * (double)s_node[j].q < r;
@@ -917,7 +917,7 @@ __device__ __noinline__ int walk_carefully(const VerifyParams& p, int lo, int n,
       const int n_barred = w.n_barred;
       int token;
       if (!w.written) {
-        token = race<ELT, VEC>(row, noise, V, temperature, bad, [&](int i) {
+        token = race<ELT, VEC>(row.at, noise, V, temperature, bad, [&](int i) {
           for (int j = 0; j < n_barred; ++j)
             if (s_barred[j] == i) return true;
           return false;
@@ -1299,7 +1299,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) verify_kernel(const __grid_co
     token = race<ELT, VEC>(target_row(cur), noise, V, temperature, bad, is_barred, s, S);
   // (and where tokens are barred and nothing else is to be drawn)
   if (act == kCareful || (act == kDraw && token < 0 && barred > 0 && !bad)) {
-    token = walk_carefully<ELT, ELD, VEC, NT>(p, lo, n, S, noise, s_node, s_barred, s_r, s_path, &s_len, s);
+    token = walk_carefully<ELT, ELD, VEC, NT>(p, lo, n, S, noise, s_node, s_barred, s_r, s_path, &s_len, cur, s);
     __syncthreads();
   }
   const bool none = token < 0 || bad;
