@@ -160,7 +160,8 @@ DF_DEVICE Reference reference_of(int m) {
 // 2^(x s - m) to 2e-7: the exponent with its rounding errors kept.
 DF_DEVICE float weight_of(float x, float s, int m) {
   // (beyond 2^24 all of this is whole: `left` adds up exactly)
-  const float p = x * s, mf = (float)-m, left = (float)(-m - (int)mf), y = p + mf, bb = y - p, a = y + left;
+  // (__fmul_rn: a product whose rounding is taken off again is not to be fused into a sum)
+  const float p = __fmul_rn(x, s), mf = (float)-m, left = (float)(-m - (int)mf), y = p + mf, bb = y - p, a = y + left;
   if (!(a > -200.f)) return a != a ? a : 0.f;
   const float rest = fmaf(x, s, -p) + ((p - (y - bb)) + (mf - bb)), k = rintf(a);
   return ldexpf(exp2f((a - k) + rest), (int)fminf(k, 200.f));
@@ -869,9 +870,8 @@ __device__ __noinline__ int walk_carefully(const VerifyParams& p, int lo, int n,
       double r = s_node[j].p;
       bool taken = is & kTaken;
       if (!first && !(is_row & kGreedyRow)) {
+        if (w.total < kLittle * w.exact || w.exact == 0.0) take(-1);
         bool out = false;
-        for (int k = 0; k < w.n_barred; ++k) out |= s_barred[k] == token;
-        if ((!out && w.total < kLittle * w.exact) || w.exact == 0.0) take(-1);
         for (int k = 0; k < w.n_barred; ++k) out |= s_barred[k] == token;
         r = 0.0;
         if (!out && w.written) {
